@@ -15,6 +15,15 @@ Entry points (same names as the C ABI in include/forge.h):
   linear_backward(dY, X, W, m, v, qscales, dX, opt, hp, step, seed, stream=None)
   opt_step(dW, W, m, v, qscales, opt, hp, step, seed, stream=None)
   sync_status(stream=None), set_wait_limit_ns(ns), launch_count()
+The operators around the fused layers (operators.py):
+  layer_norm(x, weight, bias, y, mean, rstd, eps, kind, stream=None)
+  layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, add, kind, stream=None)
+  gated_mlp(X, Wg, Wu, Wd, Y, G, U, residual, act, stream=None)
+  gated_mlp_backward(dY, X, G, U, Wg, Wu, Wd, dX, dWg, dWu, dWd, act, stream=None)
+  gated_mlp_backward_step(dY, X, G, U, gate, up, down, dX, act, opt, hp, step, stream=None)
+  linear_cross_entropy(X, W, target, loss, lse, ignore_index, stream=None)
+  linear_cross_entropy_backward(X, W, target, lse, dloss, dX, dW, ignore_index, stream=None)
+  linear_cross_entropy_step(X, W, target, lse, dloss, dX, m, v, qscales, ignore_index, opt, hp, step, seed, stream=None)
 """
 from __future__ import annotations
 
@@ -26,6 +35,8 @@ __all__ = [
     "OPT_KINDS", "STATE_FP32", "STATE_INT8_B64", "STATE_BF16", "ForgeError", "ForgeUnavailable", "lib", "library_path",
     "fused_dw_step", "fused_dw_step_layers", "dw_gemm", "dx_gemm", "linear_backward", "opt_step", "fused_dw_step_e4m3", "dw_gemm_e4m3", "sync_status", "set_wait_limit_ns", "launch_count", "build",
     "ForgeShape", "ForgeHparams", "hparams_struct",
+    "layer_norm", "layer_norm_backward", "gated_mlp", "gated_mlp_backward", "gated_mlp_backward_step",
+    "linear_cross_entropy", "linear_cross_entropy_backward", "linear_cross_entropy_step",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -134,6 +145,7 @@ def lib() -> ctypes.CDLL:
     L.forge_launch_count.restype = u64
     L.forge_status_string.argtypes = [ctypes.c_int]
     L.forge_status_string.restype = ctypes.c_char_p
+    operators.declare(L)
     _lib = L
     return L
 
@@ -421,3 +433,9 @@ def dx_launch_shape(T: int, d_out: int, d_in: int) -> dict:
 def debug_withhold_next_stage() -> None:
     """Test switch: the next tile-kernel launch withholds one pipeline stage so a bounded wait runs out."""
     lib().forge_debug_withhold_next_stage()
+
+
+from . import operators  # noqa: E402  (it uses the checks above)
+from .operators import (gated_mlp, gated_mlp_backward, gated_mlp_backward_step, layer_norm,  # noqa: E402
+                        layer_norm_backward, linear_cross_entropy, linear_cross_entropy_backward,
+                        linear_cross_entropy_step)

@@ -1,0 +1,892 @@
+// block_api.cu -- the C ABI of the operators around the fused layers that are made of matrix products
+// (include/forge.h): the gated feed-forward block and the cross entropy of a linear head.  Argument
+// checks, the cutting of the products into units, workspace layout and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include "block_kernel.cuh"
+#include "block_launch.h"
+#include "forge.h"
+#include "host.h"
+
+namespace {
+
+using forge::BlockGroup;
+using forge::BlockProblem;
+using forge::kMaxProducts;
+namespace host = forge::host;
+
+constexpr int64_t kMaxDim = 1ll << 30;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+forge_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA; }
+
+struct Machine {
+    host::Device dev;
+    int pairs;  // CTA pairs resident at once
+};
+
+forge_status machine(Machine* m) {
+    forge_status st = host::device(&m->dev);
+    if (st != FORGE_OK) return st;
+    static std::atomic<int> pairs[64];
+    int d = 0;
+    if (cudaGetDevice(&d) != cudaSuccess) return FORGE_ERR_CUDA;
+    d &= 63;
+    int n = pairs[d].load();
+    if (n == 0) {
+        if (forge::block_pairs(m->dev.num_sms, &n) != cudaSuccess || n < 1) return FORGE_ERR_CUDA;
+        pairs[d].store(n);
+    }
+    m->pairs = n;
+    return FORGE_OK;
+}
+
+// ---------------------------------------------------------------- cutting products into units
+
+// One product as the plan sees it: the output's rows and columns, columns per 256-wide tile (128 for
+// the gated forward, whose tile holds gate and up), and its reduction slices.
+struct Cut {
+    int64_t rows, cols;
+    int kb;
+    int parts;        // units per split tile
+    int split_from;   // tiles before this one are whole
+    int tiles_m, tiles_n;
+    int64_t part_base;
+    int count_base;
+    int units() const { return split_from + (tiles_m * tiles_n - split_from) * parts; }
+};
+
+struct Plan {
+    bool pair;
+    int width;  // pairs or CTAs
+    int n;
+    Cut cut[kMaxProducts];
+    int64_t part_floats;
+    int counts;
+};
+
+// A unit shorter than this many slices costs more in its fill, its partial sums and their join than
+// it saves.
+constexpr int kMinSlices = 8;
+constexpr int kMaxParts = 16;
+// the epilogue of a tile, in slices of the mainloop: only to weigh units against one another
+constexpr int kEpiSlices = 8;
+
+void plan_products(Plan& p, const Machine& mc, bool gated) {
+    // Pairs on 256 x 256 tiles move half the operand bytes per product of single CTAs on 128 x 128
+    // tiles, so they are taken unless they would leave half of the SMs idle, or every tile's second
+    // 128 rows empty.
+    auto tiles_of = [&](const Cut& c, bool pair) {
+        const int64_t tm = pair ? 256 : 128, tn = (pair ? 256 : 128) / (gated ? 2 : 1);
+        return ceil_div(c.rows, tm) * ceil_div(c.cols, tn);
+    };
+    int64_t pair_tiles = 0;
+    bool tall = false;
+    for (int i = 0; i < p.n; ++i) {
+        pair_tiles += tiles_of(p.cut[i], true);
+        tall = tall || p.cut[i].rows > 128;
+    }
+    p.pair = tall && 2 * pair_tiles > mc.pairs;
+    p.width = p.pair ? mc.pairs : mc.dev.num_sms;
+    const int64_t tm = p.pair ? 256 : 128, tn = (p.pair ? 256 : 128) / (gated ? 2 : 1);
+    int64_t tiles = 0;
+    double work = 0;
+    for (int i = 0; i < p.n; ++i) {
+        Cut& c = p.cut[i];
+        c.tiles_m = static_cast<int>(ceil_div(c.rows, tm));
+        c.tiles_n = static_cast<int>(ceil_div(c.cols, tn));
+        c.parts = 1;
+        c.split_from = c.tiles_m * c.tiles_n;
+        tiles += c.split_from;
+        work += static_cast<double>(c.split_from) * (c.kb + kEpiSlices);
+    }
+    if (tiles < p.width) {
+        // fewer tiles than pairs: the longest units are cut further while all still run at once
+        int64_t units = tiles;
+        for (;;) {
+            int best = -1;
+            for (int i = 0; i < p.n; ++i) {
+                const Cut& c = p.cut[i];
+                if (c.parts < kMaxParts && c.kb >= kMinSlices * (c.parts + 1) &&
+                    (best < 0 || static_cast<int64_t>(c.kb) * p.cut[best].parts >
+                                     static_cast<int64_t>(p.cut[best].kb) * c.parts))
+                    best = i;
+            }
+            if (best < 0) break;
+            const int more = p.cut[best].tiles_m * p.cut[best].tiles_n;
+            if (units + more > p.width) break;
+            units += more;
+            ++p.cut[best].parts;
+        }
+        for (int i = 0; i < p.n; ++i)
+            if (p.cut[i].parts > 1) p.cut[i].split_from = 0;
+    } else if (p.n == 1) {
+        // a last wave that would leave half of the pairs idle or more is cut so that it fills them
+        Cut& c = p.cut[0];
+        const int t = c.tiles_m * c.tiles_n, rest = t % p.width;
+        if (rest > 0 && 2 * rest <= p.width) {
+            const int parts = std::min({p.width / rest, 4, c.kb / kMinSlices});
+            if (parts > 1) {
+                c.parts = parts;
+                c.split_from = t - rest;
+            }
+        }
+    } else {
+        // a product whose units are a sizeable part of a pair's whole work is cut
+        const double each = work / p.width;
+        for (int i = 0; i < p.n; ++i) {
+            Cut& c = p.cut[i];
+            if (4.0 * c.kb <= each) continue;
+            const int parts = std::min({static_cast<int>(4.0 * c.kb / each) + 1, kMaxParts, c.kb / kMinSlices});
+            if (parts > 1) {
+                c.parts = parts;
+                c.split_from = 0;
+            }
+        }
+    }
+    p.part_floats = 0;
+    p.counts = 0;
+    const int cg = p.pair ? 2 : 1;
+    for (int i = 0; i < p.n; ++i) {
+        Cut& c = p.cut[i];
+        const int split = c.parts > 1 ? c.tiles_m * c.tiles_n - c.split_from : 0;
+        c.part_base = p.part_floats;
+        c.count_base = p.counts;
+        p.part_floats += static_cast<int64_t>(split) * c.parts * (cg == 2 ? 256 * 256 : 128 * 128);
+        p.counts += split * cg * 8;
+    }
+}
+
+Plan plan_one(const Machine& mc, int64_t rows, int64_t cols, int kb, bool gated = false) {
+    Plan p{};
+    p.n = 1;
+    p.cut[0].rows = rows;
+    p.cut[0].cols = cols;
+    p.cut[0].kb = kb;
+    plan_products(p, mc, gated);
+    return p;
+}
+
+int slices(int64_t k) { return static_cast<int>(ceil_div(k, forge::kBK)); }
+
+// Workspace: regions one after another, each 256-byte aligned.
+struct Arena {
+    int64_t used = 0;
+    int64_t take(int64_t bytes) {
+        const int64_t at = used;
+        used += round_up(bytes, 256);
+        return at;
+    }
+};
+
+// The split tiles' regions of one launch: FP32 parts, and counters that have to be zero before it.
+struct SplitSpace {
+    int64_t parts, counts, count_bytes;
+};
+
+SplitSpace take_split(Arena& a, const Plan& p) {
+    return SplitSpace{a.take(p.part_floats * 4), a.take(p.counts * 4ll), p.counts * 4ll};
+}
+
+struct Operand {
+    const void* base;
+    int64_t cols, rows, ld;  // as it lies in memory
+};
+
+// The schedule and everything of a launch that does not depend on the epilogue.  The products come
+// longest first.
+template <int NP>
+forge_status fill_group(BlockGroup<NP>& g, const Plan& p, const Machine& mc, char* ws, const SplitSpace& sp) {
+    g.n = p.n;
+    int u = 0, kb_max = 0;
+    int longest = 0;
+    for (int i = 0; i < p.n; ++i) {
+        BlockProblem& b = g.prob[i];
+        const Cut& c = p.cut[i];
+        b.rows = static_cast<int>(c.rows);
+        b.cols = static_cast<int>(c.cols);
+        const int group = c.tiles_m < 8 ? c.tiles_m : 8;
+        b.order = forge::TileOrder{c.tiles_m, c.tiles_n, group, 0};
+        b.unit_start = u;
+        b.split_from = c.split_from;
+        b.parts = c.parts;
+        b.part_base = c.part_base;
+        b.count_base = c.count_base;
+        u += c.units();
+        kb_max = std::max(kb_max, c.kb);
+        longest = std::max(longest, c.split_from > 0 ? c.kb : c.kb / c.parts);
+    }
+    // units at the front that take at least three quarters of the longest one's time are the long ones
+    int n_long = 0, short_kb = 0;
+    bool front = true;
+    for (int i = 0; i < p.n; ++i) {
+        const Cut& c = p.cut[i];
+        const int whole = c.split_from, rest = c.units() - c.split_from;
+        const int kb_part = c.kb / c.parts;
+        if (whole > 0) {
+            if (front && 4 * c.kb >= 3 * longest) n_long += whole;
+            else { front = false; short_kb = std::max(short_kb, c.kb); }
+        }
+        if (rest > 0) {
+            if (front && 4 * kb_part >= 3 * longest) n_long += rest;
+            else { front = false; short_kb = std::max(short_kb, kb_part); }
+        }
+    }
+    g.units = forge::plan_units(u, n_long, std::min(p.width, u), longest + kEpiSlices, short_kb + kEpiSlices);
+    g.parts = reinterpret_cast<float*>(ws + sp.parts);
+    g.counts = reinterpret_cast<uint32_t*>(ws + sp.counts);
+    g.status = mc.dev.status;
+    g.wait_limit_ns = host::wait_limit_ns();
+    g.acc_wait_limit_ns = host::acc_wait_limit_ns(kb_max);
+    g.withhold_first_stage = host::take_withhold();
+    return FORGE_OK;
+}
+
+template <int NP>
+forge_status set_map(BlockGroup<NP>& g, int i, const Operand& o) {
+    return host::operand_map(&g.maps[i], o.base, o.cols, o.rows, o.ld);
+}
+
+template <int EPI, int NP>
+forge_status launch(const BlockGroup<NP>& g, const Plan& p, cudaStream_t stream) {
+    host::count_launch();
+    return cuda_status(forge::launch_block<EPI>(&g, p.pair, std::min(p.width, g.units.n_units), stream));
+}
+
+#define FORGE_TRY(expr)                      \
+    do {                                     \
+        const forge_status st_ = (expr);     \
+        if (st_ != FORGE_OK) return st_;     \
+    } while (0)
+
+// One product of a kBlockStore launch.
+struct Product {
+    int64_t rows, cols;
+    Operand a[2], b[2];
+    int64_t k[2];
+    int a_mn, b_mn;
+    uint16_t* out;
+    const uint16_t* add;
+    float* sum;
+    int sum_in, sum_out;
+    const float* unit;
+};
+
+Plan plan_store(const Machine& mc, Product* pr, int n) {
+    std::stable_sort(pr, pr + n, [](const Product& x, const Product& y) {
+        return slices(x.k[0]) + slices(x.k[1]) > slices(y.k[0]) + slices(y.k[1]);
+    });
+    Plan p{};
+    p.n = n;
+    for (int i = 0; i < n; ++i) {
+        p.cut[i].rows = pr[i].rows;
+        p.cut[i].cols = pr[i].cols;
+        p.cut[i].kb = slices(pr[i].k[0]) + slices(pr[i].k[1]);
+    }
+    plan_products(p, mc, false);
+    return p;
+}
+
+// pr: in the order that plan_store left them in
+forge_status run_store(const Machine& mc, const Plan& p, const Product* pr, char* ws, const SplitSpace& sp,
+                       cudaStream_t stream) {
+    BlockGroup<kMaxProducts> g;
+    std::memset(&g, 0, sizeof(g));
+    FORGE_TRY(fill_group(g, p, mc, ws, sp));
+    for (int i = 0; i < p.n; ++i) {
+        BlockProblem& b = g.prob[i];
+        for (int s = 0; s < 2; ++s) {
+            b.kb[s] = slices(pr[i].k[s]);
+            if (b.kb[s] == 0) continue;
+            FORGE_TRY(set_map(g, 4 * i + 2 * s, pr[i].a[s]));
+            FORGE_TRY(set_map(g, 4 * i + 2 * s + 1, pr[i].b[s]));
+        }
+        b.a_mn = pr[i].a_mn;
+        b.b_mn = pr[i].b_mn;
+        b.out = pr[i].out;
+        b.add = pr[i].add;
+        b.sum = pr[i].sum;
+        b.sum_in = pr[i].sum_in;
+        b.sum_out = pr[i].sum_out;
+        b.unit = pr[i].unit;
+        b.ld = pr[i].cols;
+    }
+    return launch<forge::kBlockStore>(g, p, stream);
+}
+
+forge_status zero_counts(char* ws, const SplitSpace& sp, cudaStream_t stream) {
+    return sp.count_bytes == 0 ? FORGE_OK : cuda_status(cudaMemsetAsync(ws + sp.counts, 0, sp.count_bytes, stream));
+}
+
+// y [rows, n] = a [rows, k] w [n, k]^T (+ add)
+Product product_nt(const void* a, const void* w, int64_t rows, int64_t n, int64_t k, void* y, const void* add) {
+    Product p{};
+    p.rows = rows;
+    p.cols = n;
+    p.a[0] = Operand{a, k, rows, k};
+    p.b[0] = Operand{w, k, n, k};
+    p.k[0] = k;
+    p.out = static_cast<uint16_t*>(y);
+    p.add = static_cast<const uint16_t*>(add);
+    return p;
+}
+
+// dX [T, d_in] = dY [T, d_out] W [d_out, d_in]; dY's rows ld apart
+Product product_dx(const void* dY, int64_t ld, const void* W, int64_t T, int64_t d_out, int64_t d_in, void* dX) {
+    Product p{};
+    p.rows = T;
+    p.cols = d_in;
+    p.a[0] = Operand{dY, d_out, T, ld};
+    p.b[0] = Operand{W, d_in, d_out, d_in};
+    p.k[0] = d_out;
+    p.b_mn = 1;
+    p.out = static_cast<uint16_t*>(dX);
+    return p;
+}
+
+// dW [d_out, d_in] = dY [T, d_out]^T X [T, d_in]; dY's rows ld apart
+Product product_dw(const void* dY, int64_t ld, const void* X, int64_t T, int64_t d_out, int64_t d_in, void* dW) {
+    Product p{};
+    p.rows = d_out;
+    p.cols = d_in;
+    p.a[0] = Operand{dY, d_out, T, ld};
+    p.b[0] = Operand{X, d_in, T, d_in};
+    p.k[0] = T;
+    p.a_mn = p.b_mn = 1;
+    p.out = static_cast<uint16_t*>(dW);
+    return p;
+}
+
+// ---------------------------------------------------------------- gated feed-forward block
+
+forge_status check_gated(const forge_gated_shape* s) {
+    if (s == nullptr || s->reserved != 0) return FORGE_ERR_INVALID_ARGUMENT;
+    if (s->T < 0 || s->T > kMaxDim || s->d_model < 8 || s->d_ff < 8 || s->d_model > kMaxDim || s->d_ff > kMaxDim)
+        return FORGE_ERR_INVALID_ARGUMENT;
+    if (s->d_model % 8 != 0 || s->d_ff % 8 != 0) return FORGE_ERR_INVALID_ARGUMENT;
+    // tiles are counted in int
+    if ((s->T / 128 + 1) * (std::max(s->d_model, s->d_ff) / 64 + 1) > kMaxDim ||
+        (s->d_ff / 128 + 1) * (s->d_model / 128 + 1) > kMaxDim)
+        return FORGE_ERR_INVALID_ARGUMENT;
+    if (s->act != FORGE_ACT_SILU && s->act != FORGE_ACT_GELU_TANH && s->act != FORGE_ACT_RELU)
+        return FORGE_ERR_INVALID_ARGUMENT;
+    return FORGE_OK;
+}
+
+// Non-null and 32-byte aligned.
+forge_status check_all(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (p == nullptr) return FORGE_ERR_INVALID_ARGUMENT;
+    for (const void* p : ps)
+        if (!aligned(p, 32)) return FORGE_ERR_MISALIGNED;
+    return FORGE_OK;
+}
+
+forge_status check_workspace(const void* ws, int64_t have, int64_t need) {
+    if (need == 0) return FORGE_OK;
+    if (ws == nullptr || have < need) return FORGE_ERR_INVALID_ARGUMENT;
+    return aligned(ws, 256) ? FORGE_OK : FORGE_ERR_MISALIGNED;
+}
+
+struct GatedForward {
+    Plan up, down;
+    Product y;
+    int64_t h, bytes;
+    SplitSpace up_split, down_split;
+};
+
+GatedForward layout_gated_forward(const Machine& mc, const forge_gated_shape& s) {
+    GatedForward l;
+    Arena a;
+    l.up = plan_one(mc, s.T, s.d_ff, slices(s.d_model), true);
+    l.y = product_nt(nullptr, nullptr, s.T, s.d_model, s.d_ff, nullptr, nullptr);
+    l.down = plan_store(mc, &l.y, 1);
+    // both launches' counters first, so that one memset clears them
+    const int64_t counts = a.take((l.up.counts + l.down.counts) * 4ll);
+    l.up_split = SplitSpace{a.take(l.up.part_floats * 4), counts, (l.up.counts + l.down.counts) * 4ll};
+    l.down_split = SplitSpace{a.take(l.down.part_floats * 4), counts + l.up.counts * 4ll, 0};
+    l.h = a.take(s.T * s.d_ff * 2);
+    l.bytes = a.used;
+    return l;
+}
+
+struct GatedBackward {
+    Plan dh, grads;
+    Product pr[4];
+    int n;
+    int64_t dg, du, h, bytes;
+    SplitSpace dh_split, grads_split;
+};
+
+// dw: the weights' gradients are wanted (else the fused step makes them its own way)
+GatedBackward layout_gated_backward(const Machine& mc, const forge_gated_shape& s, const void* dY, const void* X,
+                                    const void* Wg, const void* Wu, void* dX, void* dWg, void* dWu, void* dWd, bool dw,
+                                    bool dx, char* ws) {
+    GatedBackward l;
+    Arena a;
+    l.dg = a.take(s.T * s.d_ff * 2);
+    l.du = a.take(s.T * s.d_ff * 2);
+    l.h = a.take(s.T * s.d_ff * 2);
+    l.dh = plan_one(mc, s.T, s.d_ff, slices(s.d_model));
+    l.n = 0;
+    if (dx) {
+        Product p = product_dx(ws + l.dg, s.d_ff, Wg, s.T, s.d_ff, s.d_model, dX);
+        p.a[1] = Operand{ws + l.du, s.d_ff, s.T, s.d_ff};
+        p.b[1] = Operand{Wu, s.d_model, s.d_ff, s.d_model};
+        p.k[1] = s.d_ff;
+        l.pr[l.n++] = p;
+    }
+    if (dw) {
+        l.pr[l.n++] = product_dw(ws + l.dg, s.d_ff, X, s.T, s.d_ff, s.d_model, dWg);
+        l.pr[l.n++] = product_dw(ws + l.du, s.d_ff, X, s.T, s.d_ff, s.d_model, dWu);
+        l.pr[l.n++] = product_dw(dY, s.d_model, ws + l.h, s.T, s.d_model, s.d_ff, dWd);
+    }
+    l.grads = Plan{};
+    if (l.n > 0) l.grads = plan_store(mc, l.pr, l.n);
+    const int64_t counts = a.take((l.dh.counts + l.grads.counts) * 4ll);
+    l.dh_split = SplitSpace{a.take(l.dh.part_floats * 4), counts, (l.dh.counts + l.grads.counts) * 4ll};
+    l.grads_split = SplitSpace{a.take(l.grads.part_floats * 4), counts + l.dh.counts * 4ll, 0};
+    l.bytes = a.used;
+    return l;
+}
+
+forge_status run_gated_dh(const Machine& mc, const GatedBackward& l, const void* dY, const void* Wd, const void* G,
+                          const void* U, char* ws, const forge_gated_shape& s, cudaStream_t stream) {
+    FORGE_TRY(zero_counts(ws, l.dh_split, stream));
+    BlockGroup<1> g;
+    std::memset(&g, 0, sizeof(g));
+    FORGE_TRY(fill_group(g, l.dh, mc, ws, l.dh_split));
+    BlockProblem& b = g.prob[0];
+    b.kb[0] = slices(s.d_model);
+    b.ld = s.d_ff;
+    b.g_in = static_cast<const uint16_t*>(G);
+    b.u_in = static_cast<const uint16_t*>(U);
+    b.g_out = reinterpret_cast<uint16_t*>(ws + l.dg);
+    b.u_out = reinterpret_cast<uint16_t*>(ws + l.du);
+    b.h_out = reinterpret_cast<uint16_t*>(ws + l.h);
+    b.act = s.act;
+    FORGE_TRY(set_map(g, 0, Operand{dY, s.d_model, s.T, s.d_model}));
+    FORGE_TRY(set_map(g, 1, Operand{Wd, s.d_ff, s.d_model, s.d_ff}));
+    return launch<forge::kBlockGatedBwd>(g, l.dh, stream);
+}
+
+// ---------------------------------------------------------------- cross entropy of a linear head
+
+forge_status check_loss(const forge_loss_shape* s) {
+    if (s == nullptr || s->reserved != 0) return FORGE_ERR_INVALID_ARGUMENT;
+    if (s->T < 0 || s->T > kMaxDim || s->vocab < 1 || s->vocab > kMaxDim || s->d_model < 8 || s->d_model > kMaxDim ||
+        s->d_model % 8 != 0)
+        return FORGE_ERR_INVALID_ARGUMENT;
+    if ((s->T / 128 + 1) * (std::max(s->vocab, s->d_model) / 128 + 1) > kMaxDim ||
+        (s->vocab / 128 + 1) * (s->d_model / 128 + 1) > kMaxDim)
+        return FORGE_ERR_INVALID_ARGUMENT;
+    return FORGE_OK;
+}
+
+struct LossForward {
+    Plan plan;
+    int64_t stats, bytes;
+    int stat_parts;
+    SplitSpace split;
+};
+
+LossForward layout_loss_forward(const Machine& mc, const forge_loss_shape& s) {
+    LossForward l;
+    Arena a;
+    l.plan = plan_one(mc, s.T, s.vocab, slices(s.d_model));
+    l.split = take_split(a, l.plan);
+    l.stat_parts = 2 * l.plan.cut[0].tiles_n;
+    l.stats = a.take(static_cast<int64_t>(l.stat_parts) * s.T * 8);
+    l.bytes = a.used;
+    return l;
+}
+
+// Vocabulary entries per piece of the backward pass: g of one piece is [T, piece] bfloat16, at most
+// 256 MiB unless T alone asks for more than 2048 entries' worth.
+int64_t loss_piece(const forge_loss_shape& s) {
+    const int64_t fit = (256ll << 20) / (2 * std::max<int64_t>(s.T, 1)) / 256 * 256;
+    return std::min(round_up(s.vocab, 8), std::max<int64_t>(fit, 2048));
+}
+
+struct LossBackward {
+    int64_t piece, pieces;
+    int64_t g, sum, unit, bytes;
+    bool scaled;       // g is kept relative to the largest dloss
+    SplitSpace split;  // the largest that any piece's launch takes
+};
+
+struct LossPiece {
+    int64_t v0, n, ld;
+    Plan grad, out;
+    Product pr[2];
+    int np;
+};
+
+LossPiece loss_piece_of(const Machine& mc, const forge_loss_shape& s, const LossBackward& l, int64_t i, const void* X,
+                        const void* W, void* dX, void* dW, bool dx, bool dw, char* ws) {
+    LossPiece p{};
+    p.v0 = i * l.piece;
+    p.n = std::min(l.piece, s.vocab - p.v0);
+    p.ld = round_up(p.n, 8);
+    p.grad = plan_one(mc, s.T, p.n, slices(s.d_model));
+    const size_t row = static_cast<size_t>(p.v0) * s.d_model * 2;
+    if (dx) {
+        Product x = product_dx(ws + l.g, p.ld, static_cast<const char*>(W) + row, s.T, p.n, s.d_model, dX);
+        x.sum = reinterpret_cast<float*>(ws + l.sum);
+        x.sum_in = i > 0;
+        x.sum_out = i + 1 < l.pieces;
+        p.pr[p.np++] = x;
+    }
+    if (dw) p.pr[p.np++] = product_dw(ws + l.g, p.ld, X, s.T, p.n, s.d_model, static_cast<char*>(dW) + row);
+    if (l.scaled)
+        for (int j = 0; j < p.np; ++j) p.pr[j].unit = reinterpret_cast<const float*>(ws + l.unit);
+    if (p.np > 0) p.out = plan_store(mc, p.pr, p.np);
+    return p;
+}
+
+// step: the fused step takes g (it has no factor of its own for the gradient, so g is not scaled)
+LossBackward layout_loss_backward(const Machine& mc, const forge_loss_shape& s, bool dx, bool dw, bool step) {
+    LossBackward l{};
+    Arena a;
+    l.scaled = !step;
+    l.unit = a.take(4);
+    l.piece = loss_piece(s);
+    l.pieces = ceil_div(s.vocab, l.piece);
+    l.g = a.take(s.T * round_up(std::min(l.piece, s.vocab), 8) * 2);
+    l.sum = a.take(dx && l.pieces > 1 ? s.T * s.d_model * 4 : 0);
+    // pieces are alike but for the last one
+    int64_t floats = 0, counts = 0;
+    for (int64_t i : {int64_t{0}, l.pieces - 1}) {
+        const LossPiece p = loss_piece_of(mc, s, l, i, nullptr, nullptr, nullptr, nullptr, dx, dw, nullptr);
+        floats = std::max({floats, p.grad.part_floats, p.out.part_floats});
+        counts = std::max<int64_t>(counts, p.grad.counts + p.out.counts);
+    }
+    l.split = SplitSpace{a.take(floats * 4), a.take(counts * 4), 0};
+    l.bytes = a.used;
+    return l;
+}
+
+// g of one piece of the vocabulary
+forge_status run_loss_grad(const Machine& mc, const LossBackward& l, const LossPiece& p, const forge_loss_shape& s,
+                           const void* X, const void* W, const int64_t* target, const float* lse, const float* dloss,
+                           char* ws, cudaStream_t stream) {
+    SplitSpace sp = l.split;
+    sp.count_bytes = (p.grad.counts + p.out.counts) * 4ll;
+    FORGE_TRY(zero_counts(ws, sp, stream));
+    BlockGroup<1> g;
+    std::memset(&g, 0, sizeof(g));
+    FORGE_TRY(fill_group(g, p.grad, mc, ws, sp));
+    BlockProblem& b = g.prob[0];
+    b.kb[0] = slices(s.d_model);
+    b.out = reinterpret_cast<uint16_t*>(ws + l.g);
+    b.ld = p.ld;
+    b.target = target;
+    b.v0 = p.v0;
+    b.vocab = s.vocab;
+    b.ignore = s.ignore_index;
+    b.lse = lse;
+    b.dloss = dloss;
+    b.unit = l.scaled ? reinterpret_cast<const float*>(ws + l.unit) : nullptr;
+    FORGE_TRY(set_map(g, 0, Operand{X, s.d_model, s.T, s.d_model}));
+    FORGE_TRY(set_map(g, 1, Operand{static_cast<const char*>(W) + static_cast<size_t>(p.v0) * s.d_model * 2, s.d_model,
+                                    p.n, s.d_model}));
+    return launch<forge::kBlockLossGrad>(g, p.grad, stream);
+}
+
+forge_status run_loss_products(const Machine& mc, const LossBackward& l, const LossPiece& p, char* ws,
+                               cudaStream_t stream) {
+    if (p.np == 0) return FORGE_OK;
+    SplitSpace sp = l.split;
+    sp.counts += p.grad.counts * 4ll;
+    return run_store(mc, p.out, p.pr, ws, sp, stream);
+}
+
+// Joins the tiles' maxima and sums of one row: lse, and the loss of the target's logit that one tile's
+// epilogue left in `loss`.  A block takes 32 rows; its warps share the parts.
+constexpr int kFinishWarps = 16;
+__global__ void __launch_bounds__(32 * kFinishWarps)
+    loss_finish_kernel(const float2* stats, int parts, int rows, const int64_t* target, int64_t vocab, int64_t ignore,
+                       float* loss, float* lse) {
+    __shared__ float2 part[kFinishWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x * 32 + lane;
+    float m = -INFINITY, s = 0.0f;
+    if (row < rows) {
+#pragma unroll 8
+        for (int i = warp; i < parts; i += kFinishWarps) {
+            const float2 v = stats[static_cast<size_t>(i) * rows + row];
+            const float mn = fmaxf(m, v.x), base = mn == -INFINITY ? 0.0f : mn;
+            s = s * forge::exp2_fast(m - base) + v.y * forge::exp2_fast(v.x - base);
+            m = mn;
+        }
+    }
+    part[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    if (warp != 0 || row >= rows) return;
+    for (int w = 1; w < kFinishWarps; ++w) {
+        const float2 v = part[w][lane];
+        const float mn = fmaxf(m, v.x), base = mn == -INFINITY ? 0.0f : mn;
+        s = s * forge::exp2_fast(m - base) + v.y * forge::exp2_fast(v.x - base);
+        m = mn;
+    }
+    const float l = m == -INFINITY && s == 0.0f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(s));
+    lse[row] = l;
+    const int64_t t = target[row];
+    loss[row] = t == ignore ? 0.0f : t >= 0 && t < vocab ? l - loss[row] : NAN;
+}
+
+// The largest |dloss| of the tokens that count, or 1 where there is none above 0: one block.
+__global__ void __launch_bounds__(1024)
+    loss_unit_kernel(const float* dloss, const int64_t* target, int64_t ignore, int rows, float* unit) {
+    __shared__ float part[32];
+    float m = 0.0f;
+    for (int i = threadIdx.x; i < rows; i += 1024) m = fmaxf(m, target[i] == ignore ? 0.0f : fabsf(dloss[i]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    m = part[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if (threadIdx.x == 0) *unit = m > 0.0f ? m : 1.0f;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t forge_gated_mlp_workspace(const forge_gated_shape* shape, int32_t backward) {
+    if (check_gated(shape) != FORGE_OK) return -1;
+    Machine mc;
+    if (shape->T == 0) return 0;
+    if (machine(&mc) != FORGE_OK) return -1;
+    if (!backward) return layout_gated_forward(mc, *shape).bytes;
+    // with and without the weights' gradients and dX
+    int64_t most = 0;
+    for (int i = 0; i < 4; ++i)
+        most = std::max(most, layout_gated_backward(mc, *shape, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                                                    nullptr, nullptr, i & 1, i >> 1, nullptr).bytes);
+    return most;
+}
+
+forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, const void* Wd, const void* residual,
+                             void* Y, void* G, void* U, void* workspace, int64_t workspace_bytes,
+                             const forge_gated_shape* shape, struct CUstream_st* stream) {
+    FORGE_TRY(check_gated(shape));
+    if (shape->T == 0) return FORGE_OK;
+    FORGE_TRY(check_all({X, Wg, Wu, Wd, Y}));
+    if ((G == nullptr) != (U == nullptr)) return FORGE_ERR_INVALID_ARGUMENT;
+    if (!aligned(G, 32) || !aligned(U, 32) || !aligned(residual, 32)) return FORGE_ERR_MISALIGNED;
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    const forge_gated_shape& s = *shape;
+    GatedForward l = layout_gated_forward(mc, s);
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
+    char* ws = static_cast<char*>(workspace);
+    FORGE_TRY(zero_counts(ws, l.up_split, stream));
+    BlockGroup<1> g;
+    std::memset(&g, 0, sizeof(g));
+    FORGE_TRY(fill_group(g, l.up, mc, ws, l.up_split));
+    BlockProblem& b = g.prob[0];
+    b.kb[0] = slices(s.d_model);
+    b.ld = s.d_ff;
+    b.g_out = static_cast<uint16_t*>(G);
+    b.u_out = static_cast<uint16_t*>(U);
+    b.h_out = reinterpret_cast<uint16_t*>(ws + l.h);
+    b.act = s.act;
+    FORGE_TRY(set_map(g, 0, Operand{X, s.d_model, s.T, s.d_model}));
+    FORGE_TRY(set_map(g, 1, Operand{Wg, s.d_model, s.d_ff, s.d_model}));
+    FORGE_TRY(set_map(g, 3, Operand{Wu, s.d_model, s.d_ff, s.d_model}));
+    FORGE_TRY(launch<forge::kBlockGatedFwd>(g, l.up, stream));
+    const Product y = product_nt(ws + l.h, Wd, s.T, s.d_model, s.d_ff, Y, residual);
+    return run_store(mc, l.down, &y, ws, l.down_split, stream);
+}
+
+forge_status forge_gated_mlp_backward(const void* dY, const void* X, const void* G, const void* U, const void* Wg,
+                                      const void* Wu, const void* Wd, void* dX, void* dWg, void* dWu, void* dWd,
+                                      void* workspace, int64_t workspace_bytes, const forge_gated_shape* shape,
+                                      struct CUstream_st* stream) {
+    FORGE_TRY(check_gated(shape));
+    const forge_gated_shape& s = *shape;
+    FORGE_TRY(check_all({dWg, dWu, dWd}));
+    if (s.T > 0) FORGE_TRY(check_all({dY, X, G, U, Wg, Wu, Wd}));
+    if (!aligned(dX, 32)) return FORGE_ERR_MISALIGNED;
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    if (s.T == 0) {  // no tokens: the gradients are zero
+        for (void* p : {dWg, dWu, dWd})
+            if (cudaMemsetAsync(p, 0, static_cast<size_t>(s.d_ff) * s.d_model * 2, stream) != cudaSuccess)
+                return FORGE_ERR_CUDA;
+        return FORGE_OK;
+    }
+    char* ws = static_cast<char*>(workspace);
+    const GatedBackward l = layout_gated_backward(mc, s, dY, X, Wg, Wu, dX, dWg, dWu, dWd, true, dX != nullptr, ws);
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
+    FORGE_TRY(run_gated_dh(mc, l, dY, Wd, G, U, ws, s, stream));
+    return run_store(mc, l.grads, l.pr, ws, l.grads_split, stream);
+}
+
+forge_status forge_gated_mlp_backward_step(const void* dY, const void* X, const void* G, const void* U,
+                                           const forge_layer* gate, const forge_layer* up, const forge_layer* down,
+                                           void* dX, void* workspace, int64_t workspace_bytes, int32_t state,
+                                           forge_opt_kind opt_kind, const forge_hparams* hp,
+                                           const forge_gated_shape* shape, int64_t step, struct CUstream_st* stream) {
+    FORGE_TRY(check_gated(shape));
+    const forge_gated_shape& s = *shape;
+    if (gate == nullptr || up == nullptr || down == nullptr) return FORGE_ERR_INVALID_ARGUMENT;
+    for (const forge_layer* w : {gate, up})
+        FORGE_TRY(host::check_step(w->W, w->m, w->v, w->qscales, opt_kind, hp, s.d_ff, s.d_model, state, step));
+    FORGE_TRY(host::check_step(down->W, down->m, down->v, down->qscales, opt_kind, hp, s.d_model, s.d_ff, state, step));
+    if (s.T > 0) FORGE_TRY(check_all({dY, X, G, U}));
+    if (!aligned(dX, 32)) return FORGE_ERR_MISALIGNED;
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    char* ws = static_cast<char*>(workspace);
+    forge_layer layers[3] = {*gate, *up, *down};
+    for (forge_layer& w : layers) {
+        w.T = s.T;
+        w.X = X;
+        w.d_out = s.d_ff;
+        w.d_in = s.d_model;
+    }
+    layers[2].d_out = s.d_model;
+    layers[2].d_in = s.d_ff;
+    if (s.T > 0) {
+        const GatedBackward l = layout_gated_backward(mc, s, dY, X, gate->W, up->W, dX, nullptr, nullptr, nullptr, false,
+                                                      dX != nullptr, ws);
+        FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
+        // the input gradients read the weights before the fused step replaces them: same stream, this order
+        FORGE_TRY(run_gated_dh(mc, l, dY, down->W, G, U, ws, s, stream));
+        if (dX != nullptr) FORGE_TRY(run_store(mc, l.grads, l.pr, ws, l.grads_split, stream));
+        layers[0].dY = ws + l.dg;
+        layers[1].dY = ws + l.du;
+        layers[2].dY = dY;
+        layers[2].X = ws + l.h;
+    }
+    return forge_fused_dw_step_layers(layers, 3, state, opt_kind, hp, step, stream);
+}
+
+int64_t forge_linear_cross_entropy_workspace(const forge_loss_shape* shape, int32_t backward) {
+    if (check_loss(shape) != FORGE_OK) return -1;
+    Machine mc;
+    if (shape->T == 0) return 0;
+    if (machine(&mc) != FORGE_OK) return -1;
+    if (!backward) return layout_loss_forward(mc, *shape).bytes;
+    int64_t most = 0;
+    for (int i = 0; i < 8; ++i)
+        most = std::max(most, layout_loss_backward(mc, *shape, i & 1, (i >> 1) & 1, i >> 2).bytes);
+    return most;
+}
+
+forge_status forge_linear_cross_entropy(const void* X, const void* W, const int64_t* target, float* loss, float* lse,
+                                        void* workspace, int64_t workspace_bytes, const forge_loss_shape* shape,
+                                        struct CUstream_st* stream) {
+    FORGE_TRY(check_loss(shape));
+    const forge_loss_shape& s = *shape;
+    if (s.T == 0) return FORGE_OK;
+    FORGE_TRY(check_all({X, W}));
+    if (target == nullptr || loss == nullptr || lse == nullptr) return FORGE_ERR_INVALID_ARGUMENT;
+    if (!aligned(target, 8) || !aligned(loss, 4) || !aligned(lse, 4)) return FORGE_ERR_MISALIGNED;
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    const LossForward l = layout_loss_forward(mc, s);
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
+    char* ws = static_cast<char*>(workspace);
+    FORGE_TRY(zero_counts(ws, l.split, stream));
+    BlockGroup<1> g;
+    std::memset(&g, 0, sizeof(g));
+    FORGE_TRY(fill_group(g, l.plan, mc, ws, l.split));
+    BlockProblem& b = g.prob[0];
+    b.kb[0] = slices(s.d_model);
+    b.target = target;
+    b.vocab = s.vocab;
+    b.ignore = s.ignore_index;
+    b.stats = reinterpret_cast<float2*>(ws + l.stats);
+    b.target_logit = loss;
+    FORGE_TRY(set_map(g, 0, Operand{X, s.d_model, s.T, s.d_model}));
+    FORGE_TRY(set_map(g, 1, Operand{W, s.d_model, s.vocab, s.d_model}));
+    FORGE_TRY(launch<forge::kBlockLossStats>(g, l.plan, stream));
+    loss_finish_kernel<<<static_cast<unsigned>(ceil_div(s.T, 32)), 32 * kFinishWarps, 0, stream>>>(
+        b.stats, l.stat_parts, static_cast<int>(s.T), target, s.vocab, s.ignore_index, loss, lse);
+    host::count_launch();
+    return cuda_status(cudaGetLastError());
+}
+
+forge_status forge_linear_cross_entropy_backward(const void* X, const void* W, const int64_t* target, const float* lse,
+                                                 const float* dloss, void* dX, void* dW, void* workspace,
+                                                 int64_t workspace_bytes, const forge_loss_shape* shape,
+                                                 struct CUstream_st* stream) {
+    FORGE_TRY(check_loss(shape));
+    const forge_loss_shape& s = *shape;
+    if (dX == nullptr && dW == nullptr) return FORGE_ERR_INVALID_ARGUMENT;
+    if (!aligned(dX, 32) || !aligned(dW, 32)) return FORGE_ERR_MISALIGNED;
+    if (s.T > 0) {
+        FORGE_TRY(check_all({X, W}));
+        if (target == nullptr || lse == nullptr || dloss == nullptr) return FORGE_ERR_INVALID_ARGUMENT;
+        if (!aligned(target, 8) || !aligned(lse, 4) || !aligned(dloss, 4)) return FORGE_ERR_MISALIGNED;
+    }
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    if (s.T == 0)
+        return dW == nullptr ? FORGE_OK
+                             : cuda_status(cudaMemsetAsync(dW, 0, static_cast<size_t>(s.vocab) * s.d_model * 2, stream));
+    const bool dx = dX != nullptr, dw = dW != nullptr;
+    const LossBackward l = layout_loss_backward(mc, s, dx, dw, false);
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
+    char* ws = static_cast<char*>(workspace);
+    loss_unit_kernel<<<1, 1024, 0, stream>>>(dloss, target, s.ignore_index, static_cast<int>(s.T),
+                                             reinterpret_cast<float*>(ws + l.unit));
+    host::count_launch();
+    for (int64_t i = 0; i < l.pieces; ++i) {
+        const LossPiece p = loss_piece_of(mc, s, l, i, X, W, dX, dW, dx, dw, ws);
+        FORGE_TRY(run_loss_grad(mc, l, p, s, X, W, target, lse, dloss, ws, stream));
+        FORGE_TRY(run_loss_products(mc, l, p, ws, stream));
+    }
+    return FORGE_OK;
+}
+
+forge_status forge_linear_cross_entropy_step(const void* X, void* W, const int64_t* target, const float* lse,
+                                             const float* dloss, void* dX, void* m, void* v, float* qscales,
+                                             void* workspace, int64_t workspace_bytes, int32_t state,
+                                             forge_opt_kind opt_kind, const forge_hparams* hp,
+                                             const forge_loss_shape* shape, int64_t step, uint64_t seed,
+                                             struct CUstream_st* stream) {
+    FORGE_TRY(check_loss(shape));
+    const forge_loss_shape& s = *shape;
+    FORGE_TRY(host::check_step(W, m, v, qscales, opt_kind, hp, s.vocab, s.d_model, state, step));
+    if (!aligned(dX, 32)) return FORGE_ERR_MISALIGNED;
+    if (s.T > 0) {
+        FORGE_TRY(check_all({X, W}));
+        if (target == nullptr || lse == nullptr || dloss == nullptr) return FORGE_ERR_INVALID_ARGUMENT;
+        if (!aligned(target, 8) || !aligned(lse, 4) || !aligned(dloss, 4)) return FORGE_ERR_MISALIGNED;
+    }
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    if (s.T == 0)
+        return host::fused_rows(nullptr, 0, X, 0, 0, s.vocab, W, m, v, qscales, opt_kind, hp, s.vocab, s.d_model, state,
+                                step, seed, stream);
+    const bool dx = dX != nullptr;
+    const LossBackward l = layout_loss_backward(mc, s, dx, false, true);
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
+    char* ws = static_cast<char*>(workspace);
+    for (int64_t i = 0; i < l.pieces; ++i) {
+        const LossPiece p = loss_piece_of(mc, s, l, i, X, W, dX, nullptr, dx, false, ws);
+        // logits and dX read the piece's rows before the fused step replaces them
+        FORGE_TRY(run_loss_grad(mc, l, p, s, X, W, target, lse, dloss, ws, stream));
+        FORGE_TRY(run_loss_products(mc, l, p, ws, stream));
+        // each piece numbers its elements from 0: a seed of its own keeps its random bits its own
+        FORGE_TRY(host::fused_rows(ws + l.g, p.ld, X, s.T, p.v0, p.n, W, m, v, qscales, opt_kind, hp, s.vocab, s.d_model,
+                                   state, step, seed ^ (static_cast<uint64_t>(i) << 40), stream));
+    }
+    return FORGE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,53 @@
+// block_instantiate.cuh -- defines the launchers of block_launch.h for one epilogue.
+#pragma once
+
+#include <atomic>
+
+#include "block_kernel.cuh"
+#include "block_launch.h"
+
+namespace forge {
+
+template <int BN, int CG, int EPI, int NP>
+cudaError_t block_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int units, cudaStream_t stream) {
+    using C = BlockCfg<BN, CG>;
+    static std::atomic<uint64_t> configured{0};  // one bit per device ordinal
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(configured.load() & bit)) {
+        err = cudaFuncSetAttribute(forge_block_kernel<BN, CG, EPI, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   C::kSmemBytes);
+        if (err != cudaSuccess) return err;
+        configured.fetch_or(bit);
+    }
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = CG;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(units * CG, 1, 1);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = CG > 1 ? &attr : nullptr;
+    cfg.numAttrs = CG > 1 ? 1 : 0;
+    return cudaSuccess;
+}
+
+template <int BN, int CG, int EPI>
+cudaError_t launch_block_as(const void* group, int units, cudaStream_t stream) {
+    constexpr int NP = EPI == kBlockStore ? kMaxProducts : 1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    cudaError_t err = block_config<BN, CG, EPI, NP>(cfg, attr, units, stream);
+    if (err != cudaSuccess) return err;
+    return cudaLaunchKernelEx(&cfg, forge_block_kernel<BN, CG, EPI, NP>, *static_cast<const BlockGroup<NP>*>(group));
+}
+
+template <int EPI>
+cudaError_t launch_block(const void* group, bool pair, int units, cudaStream_t stream) {
+    return pair ? launch_block_as<256, 2, EPI>(group, units, stream) : launch_block_as<128, 1, EPI>(group, units, stream);
+}
+
+}  // namespace forge

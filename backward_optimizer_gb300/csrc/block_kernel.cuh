@@ -1,0 +1,724 @@
+// block_kernel.cuh -- the persistent matrix-product kernel of the operators around the fused layers:
+// the gated feed-forward block and the softmax cross entropy of a linear head, forward and backward.
+//
+// Every product of these operators is C = A B over a long reduction, followed by arithmetic on the
+// finished tile of C.  One pipeline serves them all (the roles of tile_kernel.cuh):
+//   warp 0      TMA producer: 64-deep slices of A and B into a shared-memory ring, 128-byte swizzle
+//   warp 1      MMA issuer: tcgen05.mma kind::f16, bf16 x bf16 -> f32, accumulating in TMEM; two
+//               accumulators, so the next tile's mainloop overlaps this tile's epilogue
+//   warps 2-9   epilogue: thread = output row; tcgen05.ld gives it 32 columns at a time
+// What is computed per finished tile is the EPI parameter:
+//   kBlockGatedFwd   A = X, B = the gate's and the up projection's rows side by side: the tile holds
+//                    G and U of the same columns, and H = act(G) U leaves the chip with them (or
+//                    without them, where no backward pass follows)
+//   kBlockGatedBwd   the tile is dH = dY Wd, which is never written: with G and U it becomes dG, dU, H
+//   kBlockLossStats  the tile is a piece of the logits, which are never written: each row leaves its
+//                    maximum and its sum of exponentials over the tile's columns
+//   kBlockLossGrad   the logits again; g = dloss (exp(l - lse) - [target]) is written for one piece of
+//                    the vocabulary
+//   kBlockStore      the tile itself, rounded to bfloat16, with a residual added or with the FP32 sum
+//                    of earlier pieces carried in memory; up to NP products in one launch
+//
+// Layouts.  An operand is K-major when the reduction index runs along memory (X and W of y = X W^T),
+// MN-major when it does not; kBlockStore takes either for each operand of each product, the other
+// epilogues have theirs fixed.  A product may have two pairs of operands whose products are summed in
+// one accumulator (dX = dG Wg + dU Wu).
+//
+// Units of work.  A unit is one tile over its whole reduction, or one of `parts` pieces of it.  A
+// split tile has no CTA that waits for another: each epilogue warp leaves its FP32 values in memory,
+// counts itself in, and the warp that arrives last adds the parts up in their order and runs the
+// epilogue.  The order of the sum is fixed, so results do not depend on which one is last.
+//
+// Waits are bounded as in tile_kernel.cuh, and an aborted launch drains its copies the same way.
+#pragma once
+
+#include <cstdint>
+
+#include "tile_kernel.cuh"
+
+namespace forge {
+
+enum BlockEpi : int { kBlockStore = 0, kBlockGatedFwd = 1, kBlockGatedBwd = 2, kBlockLossStats = 3, kBlockLossGrad = 4 };
+enum BlockAct : int { kActSilu = 0, kActGeluTanh = 1, kActRelu = 2 };
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int BN, int CG>
+struct BlockCfg {
+    static_assert((BN == 256 && CG == 2) || (BN == 128 && CG == 1), "tile shapes");
+    static constexpr int kBLoad = BN / CG;  // B rows (or columns) staged by this CTA
+    static constexpr int kABytes = kBM * kBK * 2;
+    static constexpr int kBBytes = kBLoad * kBK * 2;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kTmemCols = 2 * BN;
+    static constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, half the columns each
+    static constexpr int kThreads = 64 + 32 * kEpiWarps;
+    static constexpr int kStages = 7;
+    static constexpr int kSmemBytes = kStages * kStageBytes + 256 + 1024;  // barriers, alignment slack
+    static_assert(kSmemBytes <= 232448, "shared memory");
+};
+
+struct BlockProblem {
+    int rows, cols;       // of the output (gated forward: cols = d_ff, a tile spans BN / 2 of them)
+    TileOrder order;
+    int unit_start;       // number of its first unit
+    int split_from;       // tiles from here on are cut into `parts` units along the reduction
+    int parts;
+    int kb[2];            // 64-deep reduction slices of the two operand pairs (the second may have none)
+    int a_mn, b_mn;       // operand orders (kBlockStore): 1 = MN-major
+    int64_t part_base;    // where its split tiles' FP32 values start (floats)
+    int count_base;       // and their counters
+    // kBlockStore: out [rows, ld] bf16; add: residual [rows, ld] or null; sum: FP32 [rows, cols] of
+    // earlier pieces, read if sum_in, written instead of out if sum_out
+    uint16_t* out;
+    const uint16_t* add;
+    float* sum;
+    int sum_in, sum_out;
+    int64_t ld;
+    // gated: G, U, H / dG, dU [rows, cols] bf16
+    const uint16_t* g_in;
+    const uint16_t* u_in;
+    uint16_t* g_out;
+    uint16_t* u_out;
+    uint16_t* h_out;
+    int act;
+    // loss: columns are vocabulary entries v0 .. v0 + cols - 1
+    const int64_t* target;
+    int64_t v0, vocab, ignore;
+    float2* stats;        // [2 * tile columns][rows]: (max, sum of exponentials), base 2
+    float* target_logit;  // [rows]
+    const float* lse;     // [rows]
+    const float* dloss;   // [rows]
+    // kBlockLossGrad writes g / *unit, and kBlockStore multiplies its finished sums by *unit (null: 1)
+    const float* unit;
+};
+
+// Up to NP products, the one with the longest units first.
+template <int NP>
+struct BlockGroup {
+    int n;
+    UnitPlan units;
+    BlockProblem prob[NP];
+    CUtensorMap maps[4 * NP];  // per product: A, B of the first pair, A, B of the second
+    float* parts;
+    uint32_t* counts;
+    int* status;
+    uint64_t wait_limit_ns, acc_wait_limit_ns;
+    int withhold_first_stage;  // test switch, as TileArgs::withhold_first_stage
+};
+
+struct Unit {
+    int prob, mb, nb, part, split;  // split: which split tile of the product, or -1
+    int k_first, k_end;             // slices of the concatenated operand pairs
+};
+
+template <int NP>
+__device__ __forceinline__ Unit unit_of(const BlockGroup<NP>& g, int u, int l) {
+    if constexpr (NP > 1) {
+        while (l + 1 < g.n && u >= g.prob[l + 1].unit_start) ++l;
+    } else {
+        l = 0;
+    }
+    const BlockProblem& b = g.prob[l];
+    int t = u - b.unit_start;
+    Unit r{l, 0, 0, 0, -1, 0, b.kb[0] + b.kb[1]};
+    if (t >= b.split_from) {
+        const int s = t - b.split_from, kb = r.k_end;
+        r.split = s / b.parts;
+        r.part = s - r.split * b.parts;
+        r.k_first = static_cast<int>(static_cast<int64_t>(kb) * r.part / b.parts);
+        r.k_end = static_cast<int>(static_cast<int64_t>(kb) * (r.part + 1) / b.parts);
+        t = b.split_from + r.split;
+    }
+    tile_coords(t, b.order, r.mb, r.nb);
+    return r;
+}
+
+// ---------------------------------------------------------------- arithmetic
+
+__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+// act(g), and for the backward pass its derivative.  gelu with the tanh form is
+// g (1 + tanh y) / 2 = g sigmoid(2 y), y = sqrt(2 / pi) (g + 0.044715 g^3).
+constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+
+__device__ __forceinline__ float act_value(float g, int act) {
+    if (act == kActRelu) return g > 0.0f ? g : (g != g ? g : 0.0f);
+    const float a = act == kActSilu ? g : kGelu2 * (g + 0.044715f * g * g * g);
+    return __fdividef(g, 1.0f + __expf(-a));
+}
+
+__device__ __forceinline__ void act_both(float g, int act, float& value, float& slope) {
+    if (act == kActRelu) {
+        value = g > 0.0f ? g : (g != g ? g : 0.0f);
+        slope = g > 0.0f ? 1.0f : 0.0f;
+    } else if (act == kActSilu) {
+        const float p = sigmoid_fast(g);
+        value = g * p;
+        slope = p * (1.0f + g * (1.0f - p));
+    } else {
+        const float p = sigmoid_fast(kGelu2 * (g + 0.044715f * g * g * g));
+        value = g * p;
+        slope = p + g * p * (1.0f - p) * (kGelu2 * (1.0f + 3.0f * 0.044715f * g * g));
+    }
+}
+
+// 2^x by the hardware approximation (2 ulp)
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---------------------------------------------------------------- rows of bfloat16 in memory
+
+// 32 columns of one row, packed in pairs; `left`: columns from here to the end of the row (stored or
+// loaded in runs of 8); wide: the row's address is a multiple of 32 bytes at every 16th column
+__device__ __forceinline__ void store_run(uint16_t* p, const uint32_t (&v)[16], int left, bool wide) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (wide && left >= 16 * h + 16) {
+            const uint32_t r[8] = {v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3],
+                                   v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]};
+            st_v8(p + 16 * h, r);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (left >= 16 * h + 8 * q + 8) {
+                    const uint32_t r[4] = {v[8 * h + 4 * q], v[8 * h + 4 * q + 1], v[8 * h + 4 * q + 2],
+                                           v[8 * h + 4 * q + 3]};
+                    st_v4(p + 16 * h + 8 * q, r);
+                }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void load_run(const uint16_t* p, uint32_t (&v)[16], int left, bool wide) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (wide && left >= 16 * h + 16) {
+            uint32_t r[8];
+            ld_v8(p + 16 * h, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * h + i] = r[i];
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t r[4] = {0u, 0u, 0u, 0u};
+                if (left >= 16 * h + 8 * q + 8) ld_v4(p + 16 * h + 8 * q, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[8 * h + 4 * q + i] = r[i];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- the accumulator a warp reads
+// Column `c` of the tile, 32 at a time, for this thread's row: from TMEM, or the sum of a split
+// tile's parts.
+
+struct AccTmem {
+    uint32_t taddr;
+    __device__ __forceinline__ void load(int c, uint32_t (&g)[32]) const {
+        __syncwarp();  // tcgen05.ld is a warp's: lanes that skipped a row's stores rejoin here
+        tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(c), g);
+        tmem_ld_wait(g);
+    }
+};
+
+struct AccParts {
+    const float* p;  // this thread's row of part 0; columns are 32 floats apart
+    size_t step;     // floats from part to part
+    int parts;
+    bool valid;      // rows past the output's last left nothing in memory
+    __device__ __forceinline__ void load(int c, uint32_t (&g)[32]) const {
+        float s[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s[j] = valid ? __ldcg(p + static_cast<size_t>(c + j) * 32) : 0.0f;
+        for (int k = 1; k < parts; ++k) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                s[j] = __fadd_rn(s[j], valid ? __ldcg(p + k * step + static_cast<size_t>(c + j) * 32) : 0.0f);
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) g[j] = __float_as_uint(s[j]);
+    }
+};
+
+// ---------------------------------------------------------------- epilogues
+// `row`: this thread's output row; h: the half of the tile's columns that the warp owns.
+
+template <int BN, class Acc>
+__device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
+    const bool wide = (b.ld & 15) == 0;
+#pragma unroll 1
+    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
+        const int col = nb * BN + c, left = b.cols - col;
+        if (left <= 0) break;  // the same for the whole warp
+        const bool mine = row < b.rows;
+        uint32_t add[16];
+        if (b.add != nullptr && mine) load_run(b.add + static_cast<size_t>(row) * b.ld + col, add, left, wide);
+        uint32_t g[32];
+        acc.load(c, g);
+        if (!mine) continue;
+        if (b.sum_in) {
+            const float* s = b.sum + static_cast<size_t>(row) * b.cols + col;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t r[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                if (left >= 8 * q + 8) ld_v8(s + 8 * q, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    g[8 * q + i] = __float_as_uint(__fadd_rn(__uint_as_float(r[i]), __uint_as_float(g[8 * q + i])));
+            }
+        }
+        if (b.sum_out) {
+            float* s = b.sum + static_cast<size_t>(row) * b.cols + col;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t r[8] = {g[8 * q], g[8 * q + 1], g[8 * q + 2], g[8 * q + 3],
+                                       g[8 * q + 4], g[8 * q + 5], g[8 * q + 6], g[8 * q + 7]};
+                if (left >= 8 * q + 8) st_v8(s + 8 * q, r);
+            }
+            continue;
+        }
+        if (b.unit != nullptr) {
+            const float unit = __ldg(b.unit);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) g[j] = __float_as_uint(__fmul_rn(__uint_as_float(g[j]), unit));
+        }
+        if (b.add != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                g[2 * j] = __float_as_uint(__fadd_rn(__uint_as_float(g[2 * j]), bf16_lo(add[j])));
+                g[2 * j + 1] = __float_as_uint(__fadd_rn(__uint_as_float(g[2 * j + 1]), bf16_hi(add[j])));
+            }
+        }
+        uint32_t o[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2_rn(g[2 * j], g[2 * j + 1]);
+        store_run(b.out + static_cast<size_t>(row) * b.ld + col, o, left, wide);
+    }
+}
+
+template <int BN, class Acc>
+__device__ __forceinline__ void epi_gated_fwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
+    const bool wide = (b.cols & 15) == 0;
+#pragma unroll 1
+    for (int c = h * (BN / 4); c < (h + 1) * (BN / 4); c += 32) {
+        const int col = nb * (BN / 2) + c, left = b.cols - col;
+        if (left <= 0) break;
+        uint32_t g[32], u[32];
+        acc.load(c, g);
+        acc.load(BN / 2 + c, u);
+        if (row >= b.rows) continue;
+        const size_t at = static_cast<size_t>(row) * b.cols + col;
+        uint32_t o[16];
+        if (b.g_out != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2_rn(g[2 * j], g[2 * j + 1]);
+            store_run(b.g_out + at, o, left, wide);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2_rn(u[2 * j], u[2 * j + 1]);
+            store_run(b.u_out + at, o, left, wide);
+        }
+        // H is rounded to bfloat16, the type of the next product's operand
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float a0 = act_value(__uint_as_float(g[2 * j]), b.act) * __uint_as_float(u[2 * j]);
+            const float a1 = act_value(__uint_as_float(g[2 * j + 1]), b.act) * __uint_as_float(u[2 * j + 1]);
+            o[j] = pack_bf16x2_rn(__float_as_uint(a0), __float_as_uint(a1));
+        }
+        store_run(b.h_out + at, o, left, wide);
+    }
+}
+
+// G and U are read, and dG, dU and H written, by the thread that owns the element: dG and dU may lie
+// where G and U do.
+template <int BN, class Acc>
+__device__ __forceinline__ void epi_gated_bwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
+    const bool wide = (b.cols & 15) == 0;
+#pragma unroll 1
+    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
+        const int col = nb * BN + c, left = b.cols - col;
+        if (left <= 0) break;
+        const bool mine = row < b.rows;
+        const size_t at = static_cast<size_t>(row) * b.cols + col;
+        uint32_t g[16], u[16];
+        if (mine) {
+            load_run(b.g_in + at, g, left, wide);
+            load_run(b.u_in + at, u, left, wide);
+        }
+        uint32_t d[32];
+        acc.load(c, d);
+        if (!mine) continue;
+        uint32_t o[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float a0, s0, a1, s1;
+            act_both(bf16_lo(g[j]), b.act, a0, s0);
+            act_both(bf16_hi(g[j]), b.act, a1, s1);
+            const float u0 = bf16_lo(u[j]), u1 = bf16_hi(u[j]);
+            const float d0 = __uint_as_float(d[2 * j]), d1 = __uint_as_float(d[2 * j + 1]);
+            g[j] = pack_bf16x2_rn(__float_as_uint(d0 * u0 * s0), __float_as_uint(d1 * u1 * s1));
+            u[j] = pack_bf16x2_rn(__float_as_uint(d0 * a0), __float_as_uint(d1 * a1));
+            o[j] = pack_bf16x2_rn(__float_as_uint(a0 * u0), __float_as_uint(a1 * u1));
+        }
+        store_run(b.g_out + at, g, left, wide);
+        store_run(b.u_out + at, u, left, wide);
+        store_run(b.h_out + at, o, left, wide);
+    }
+}
+
+// One pass over the warp's columns with the running maximum and sum, in base 2.  A row whose logits
+// so far are all -inf keeps sum 0.
+template <int BN, class Acc>
+__device__ __forceinline__ void epi_loss_stats(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
+    const bool mine = row < b.rows;
+    const int64_t t = mine ? b.target[row] : -1;
+    const int64_t first = b.v0 + static_cast<int64_t>(nb) * BN;  // vocabulary entry of the tile's column 0
+    float m = -INFINITY, s = 0.0f;
+#pragma unroll 1
+    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
+        const int left = b.cols - (nb * BN + c);
+        if (left <= 0) break;
+        uint32_t g[32];
+        acc.load(c, g);
+        const int64_t at = t - (first + c);
+        if (at >= 0 && at < 32 && t < b.vocab) {
+            float lt = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) lt = at == j ? __uint_as_float(g[j]) : lt;
+            b.target_logit[row] = lt;
+        }
+        if (left < 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) g[j] = j < left ? g[j] : __float_as_uint(-INFINITY);
+        }
+        float top = __uint_as_float(g[0]);
+#pragma unroll
+        for (int j = 1; j < 32; ++j) top = fmaxf(top, __uint_as_float(g[j]));
+        const float mn = fmaxf(m, top * kLog2e);
+        const float base = mn == -INFINITY ? 0.0f : mn;
+        float e = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) e += exp2_fast(__fmaf_rn(__uint_as_float(g[j]), kLog2e, -base));
+        s = __fmaf_rn(s, exp2_fast(m - base), e);
+        m = mn;
+    }
+    if (mine) b.stats[static_cast<size_t>(2 * nb + h) * b.rows + row] = make_float2(m, s);
+}
+
+template <int BN, class Acc>
+__device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
+    const bool mine = row < b.rows, wide = (b.ld & 15) == 0;
+    const int64_t t = mine ? b.target[row] : -1;
+    const bool counts = t != b.ignore;
+    const float shift = mine ? -b.lse[row] * kLog2e : 0.0f;
+    // a target outside the vocabulary that is not the ignored one shows as NaN
+    const float given = !mine || !counts ? 0.0f : (t >= 0 && t < b.vocab ? b.dloss[row] : NAN);
+    // Under the usual mean over tokens every dloss is the same number, and so is, nearly, every
+    // target's entry -dloss (1 - p): rounded to bfloat16 as it is, that number's one rounding error (up
+    // to 2^-8) would stand in all of dX and dW.  Relative to the largest dloss the entry is -(1 - p).
+    const float scale = b.unit != nullptr ? given / __ldg(b.unit) : given;
+    const int64_t first = b.v0 + static_cast<int64_t>(nb) * BN;
+#pragma unroll 1
+    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
+        const int left = static_cast<int>(b.ld) - (nb * BN + c);
+        if (left <= 0) break;
+        uint32_t g[32];
+        acc.load(c, g);
+        if (!mine) continue;
+        const int64_t off = t - (first + c);
+        const int at = off >= 0 && off < 32 ? static_cast<int>(off) : -1;
+        uint32_t o[16];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float p = exp2_fast(__fmaf_rn(__uint_as_float(g[j]), kLog2e, shift));
+            const float v = (at == j ? p - 1.0f : p) * scale;
+            g[j] = counts ? __float_as_uint(v) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2_rn(g[2 * j], g[2 * j + 1]);
+        store_run(b.out + static_cast<size_t>(row) * b.ld + nb * BN + c, o, left, wide);
+    }
+}
+
+template <int BN, int EPI, class Acc>
+__device__ __forceinline__ void block_epilogue(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
+    if constexpr (EPI == kBlockStore) epi_store<BN>(b, acc, row, nb, h);
+    else if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, acc, row, nb, h);
+    else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, acc, row, nb, h);
+    else if constexpr (EPI == kBlockLossStats) epi_loss_stats<BN>(b, acc, row, nb, h);
+    else epi_loss_grad<BN>(b, acc, row, nb, h);
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int BN, int CG, int EPI, int NP>
+__global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
+    forge_block_kernel(const __grid_constant__ BlockGroup<NP> grp) {
+    using C = BlockCfg<BN, CG>;
+    constexpr bool kGated = EPI == kBlockGatedFwd;
+    constexpr int kColsPerTile = kGated ? BN / 2 : BN;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + C::kStages * C::kABytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
+    uint64_t* empty = full + C::kStages;
+    uint64_t* acc_full = empty + C::kStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drain = acc_empty + 2;
+    uint64_t* peer_done = drain + 1;
+    uint64_t* peer_count = peer_done + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(peer_count + 1);
+    int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = CG > 1 ? cluster_ctarank() : 0u;
+    const int pair = static_cast<int>(blockIdx.x) / CG;
+    const int pairs = static_cast<int>(gridDim.x) / CG;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], C::kEpiWarps * CG);
+        }
+        mbar_init(drain, 1);
+        mbar_init(peer_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        for (int l = 0; l < grp.n; ++l) {
+            tma_prefetch_desc(&grp.maps[4 * l]);
+            tma_prefetch_desc(&grp.maps[4 * l + 1]);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(tmem_slot, C::kTmemCols);
+        tmem_relinquish<CG>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG > 1) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const AbortCtx ab{abort_flag, grp.status, grp.wait_limit_ns};
+    uint64_t n_issued = 0;
+    int64_t withheld = -1;
+
+    // operand orders: fixed by what the epilogue's product is, or the product's own (kBlockStore)
+    auto a_mn = [&](const BlockProblem& b) { return EPI == kBlockStore ? b.a_mn != 0 : false; };
+    auto b_mn = [&](const BlockProblem& b) { return EPI == kBlockStore ? b.b_mn != 0 : EPI == kBlockGatedBwd; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const uint64_t keep = policy_evict_last();
+            UnitCursor cur;
+            int l = 0;
+            for (int u = cur.next(grp.units, pair, pairs); ok && u >= 0; u = cur.next(grp.units, pair, pairs)) {
+                const Unit w = unit_of(grp, u, l);
+                l = w.prob;
+                const BlockProblem& b = grp.prob[l];
+                const bool amn = a_mn(b), bmn = b_mn(b);
+                const int row_a = w.mb * kBM * CG + static_cast<int>(rank) * kBM;
+                // gated forward: the even CTA (or the first half of the columns) holds the gate's
+                // rows, the other the up projection's, of the same d_ff columns
+                const int col_b = kGated ? w.nb * kColsPerTile : w.nb * BN + static_cast<int>(rank) * C::kBLoad;
+                for (int kb = w.k_first; kb < w.k_end; ++kb) {
+                    if (!wait_bounded(&empty[stage], phase ^ 1u, ab)) { ok = false; break; }
+                    uint32_t bar = smem_addr(&full[stage]);
+                    if constexpr (CG == 2) bar = map_to_rank(bar, 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * C::kStageBytes);
+                    if (grp.withhold_first_stage && rank == 0 && n_issued == 0) {
+                        withheld = static_cast<int64_t>(n_issued);
+                    } else {
+                        const int second = kb >= b.kb[0] ? 1 : 0;
+                        const int k0 = (kb - (second ? b.kb[0] : 0)) * kBK;
+                        const CUtensorMap* ma = &grp.maps[4 * l + 2 * second];
+                        const CUtensorMap* mb = ma + 1;
+                        uint8_t* a_dst = sA + stage * C::kABytes;
+                        uint8_t* b_dst = sB + stage * C::kBBytes;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int r = row_a + 64 * j;
+                            tma_load_2d_cg<CG>(a_dst + j * kBK * 128, ma, bar, amn ? r : k0, amn ? k0 : r, keep);
+                        }
+                        if constexpr (kGated) {
+                            // maps: A = X, B = Wg; the second pair's B is Wu
+                            const CUtensorMap* mu = &grp.maps[4 * l + 3];
+#pragma unroll
+                            for (int j = 0; j < C::kBLoad / 64; ++j) {
+                                const bool up = CG == 2 ? rank == 1 : j >= C::kBLoad / 128;
+                                const int r = col_b + 64 * (CG == 2 ? j : j % (C::kBLoad / 128));
+                                tma_load_2d_cg<CG>(b_dst + j * kBK * 128, up ? mu : mb, bar, k0, r, keep);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < C::kBLoad / 64; ++j) {
+                                const int r = col_b + 64 * j;
+                                tma_load_2d_cg<CG>(b_dst + j * kBK * 128, mb, bar, bmn ? r : k0, bmn ? k0 : r, keep);
+                            }
+                        }
+                    }
+                    ++n_issued;
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if constexpr (CG == 2) {
+                if (rank == 1) {
+                    st_shared_cluster_u64(map_to_rank(smem_addr(peer_count), 0), n_issued);
+                    mbar_arrive_remote(map_to_rank(smem_addr(peer_done), 0));
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true, issued_any = false;
+            UnitCursor cur;
+            int l = 0;
+            for (int u = cur.next(grp.units, pair, pairs); ok && u >= 0; u = cur.next(grp.units, pair, pairs)) {
+                const Unit w = unit_of(grp, u, l);
+                l = w.prob;
+                const BlockProblem& b = grp.prob[l];
+                const bool amn = a_mn(b), bmn = b_mn(b);
+                const uint32_t idesc = idesc_bf16_f32(kBM * CG, BN, amn, bmn);
+                // MN-major: 16 reduction steps are 16 rows of 128 bytes, 64-element blocks 8 KiB apart;
+                // K-major: 32 bytes within each 128-byte row, 8-row groups 1024 bytes apart
+                const uint32_t a_step = amn ? 2048u : 32u, b_step = bmn ? 2048u : 32u;
+                const uint32_t a_lbo = amn ? kBK * 128u : 16u, b_lbo = bmn ? kBK * 128u : 16u;
+                if (!wait_bounded(&acc_empty[acc], acc_phase ^ 1u, ab)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                for (int kb = w.k_first; kb < w.k_end; ++kb) {
+                    if (!wait_bounded(&full[stage], phase, ab)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t a_base = smem_addr(sA + stage * C::kABytes);
+                    const uint32_t b_base = smem_addr(sB + stage * C::kBBytes);
+#pragma unroll
+                    for (int kk = 0; kk < kBK / kUmmaK; ++kk) {
+                        const uint64_t ad = smem_desc_sw128(a_base + kk * a_step, a_lbo, 1024);
+                        const uint64_t bd = smem_desc_sw128(b_base + kk * b_step, b_lbo, 1024);
+                        tc_mma_bf16<CG>(d_tmem, ad, bd, idesc, (kb != w.k_first || kk != 0) ? 1u : 0u);
+                    }
+                    issued_any = true;
+                    tc_commit_mask<CG>(&empty[stage], 0x3u);
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                tc_commit_mask<CG>(&acc_full[acc], 0x3u);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (!ok && issued_any) {
+                tc_commit_local<CG>(drain);
+                drain_bounded(drain, 0, grp.wait_limit_ns);
+            }
+        }
+    } else {
+        const int e = warp - 2;
+        const int quarter = warp & 3;  // a warp may only touch TMEM lanes 32 (warp mod 4) .. +31
+        const int half = e >> 2;
+        const AbortCtx ab_acc{abort_flag, grp.status, grp.acc_wait_limit_ns};
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        UnitCursor cur;
+        int l = 0;
+        for (int u = cur.next(grp.units, pair, pairs); u >= 0; u = cur.next(grp.units, pair, pairs)) {
+            const Unit w = unit_of(grp, u, l);
+            l = w.prob;
+            const BlockProblem& b = grp.prob[l];
+            const int row = w.mb * kBM * CG + static_cast<int>(rank) * kBM + quarter * 32 + lane;
+            int ok = 1;
+            if (lane == 0) ok = wait_bounded(&acc_full[acc], acc_phase, ab_acc) ? 1 : 0;
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
+            tc_fence_after();
+            const AccTmem tm{tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN)};
+            if (w.split < 0) block_epilogue<BN, EPI>(b, tm, row, w.nb, half);
+            // [split tile][part][CTA][lane quarter][column][lane]
+            const size_t step = static_cast<size_t>(CG) * 4 * BN * 32;
+            const size_t own = (static_cast<size_t>(rank) * 4 + quarter) * BN * 32 + lane;
+            if (w.split >= 0) {
+                float* p = grp.parts + b.part_base +
+                           (static_cast<size_t>(w.split) * b.parts + w.part) * step + own;
+                // the columns whose epilogue this warp runs: gate and up columns come from both halves
+                constexpr int kRuns = kGated ? 2 : 1, kRun = BN / 2 / kRuns;
+#pragma unroll 1
+                for (int r = 0; r < kRuns; ++r) {
+#pragma unroll 1
+                    for (int c = 0; c < kRun; c += 32) {
+                        const int at = r * (BN / 2) + half * kRun + c;
+                        uint32_t g[32];
+                        tm.load(at, g);
+                        if (row < b.rows) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                __stcg(p + static_cast<size_t>(at + j) * 32, __uint_as_float(g[j]));
+                        }
+                    }
+                }
+            }
+            // the accumulator's reads are done: it may be overwritten
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(map_to_rank(smem_addr(&acc_empty[acc]), 0));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+            if (w.split >= 0) {
+                // every lane's values are visible device-wide before the warp counts itself in; the
+                // last one to arrive sees the other parts' values
+                __threadfence();
+                __syncwarp();
+                uint32_t before = 0;
+                if (lane == 0)
+                    before = atomicAdd(grp.counts + b.count_base + (w.split * CG + static_cast<int>(rank)) * C::kEpiWarps + e, 1u);
+                before = __shfl_sync(0xFFFFFFFFu, before, 0);
+                if (before + 1 == static_cast<uint32_t>(b.parts)) {
+                    __threadfence();
+                    const AccParts sum{grp.parts + b.part_base + static_cast<size_t>(w.split) * b.parts * step + own,
+                                       step, b.parts, row < b.rows};
+                    block_epilogue<BN, EPI>(b, sum, row, w.nb, half);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && lane == 0 && rank == 0 && *abort_flag) {
+        uint64_t n_peer = n_issued;
+        bool counted = true;
+        if constexpr (CG == 2) {
+            counted = false;
+            const uint64_t t0 = global_timer_ns();
+            while (!counted && global_timer_ns() - t0 <= 4 * grp.wait_limit_ns) counted = mbar_try_wait_cluster(peer_done, 0);
+            if (counted) n_peer = ld_shared_volatile_u64(peer_count);
+        }
+        if (counted) {
+            drain_copies<C::kStages, CG>(full, n_issued, n_peer, withheld, C::kStageBytes, grp.wait_limit_ns);
+        } else {
+            drain_copies<C::kStages, 1>(full, n_issued, n_issued, withheld, C::kStageBytes, grp.wait_limit_ns);
+        }
+    }
+    if constexpr (CG > 1) cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc<CG>(tmem_base, C::kTmemCols);
+    }
+}
+
+}  // namespace forge

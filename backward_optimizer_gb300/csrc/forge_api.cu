@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "forge.h"
+#include "host.h"
 #include "launch.h"
 #include "opt_step_kernel.cuh"
 #include "tile_kernel.cuh"
@@ -160,12 +161,12 @@ OptScalars derive_scalars(forge_opt_kind k, const forge_hparams& hp, int64_t ste
     return s;
 }
 
-forge_status encode_operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, bool e4m3) {
-    // A [rows, cols] row-major operand, bf16 or E4M3, read in boxes of 64 rows whose rows are
-    // exactly one 128-byte swizzle span (64 bf16 or 128 E4M3 columns).
+forge_status encode_operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, bool e4m3, int64_t ld) {
+    // A [rows, cols] row-major operand, bf16 or E4M3, its rows ld elements apart, read in boxes of 64
+    // rows whose rows are exactly one 128-byte swizzle span (64 bf16 or 128 E4M3 columns).
     const int64_t esize = e4m3 ? 1 : 2;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * esize)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * esize)};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esize), 64};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = g_encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
@@ -177,15 +178,15 @@ forge_status encode_operand_map(CUtensorMap* map, const void* base, int64_t cols
 
 // Encoded tensor maps of recent calls, per host thread.  A training loop passes the same buffers
 // with the same shapes every step, and encoding a map costs host time comparable to a small layer's
-// whole kernel.  A map is plain host data determined by (base, cols, rows, element type), handed to
+// whole kernel.  A map is plain host data determined by (base, cols, rows, ld, element type), handed to
 // the kernel by value, so a cached one is exactly the one a new encoding would give, whatever
 // happened to the buffer in between.
 struct MapKey {
     const void* base;
-    int64_t cols, rows;
+    int64_t cols, rows, ld;
     bool e4m3;
     bool operator==(const MapKey& o) const {
-        return base == o.base && cols == o.cols && rows == o.rows && e4m3 == o.e4m3;
+        return base == o.base && cols == o.cols && rows == o.rows && ld == o.ld && e4m3 == o.e4m3;
     }
 };
 struct MapSlot {
@@ -196,17 +197,21 @@ struct MapSlot {
 constexpr int kMapSlots = 64;
 thread_local MapSlot t_maps[kMapSlots];
 
-forge_status make_operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, bool e4m3 = false) {
-    const MapKey key{base, cols, rows, e4m3};
+// ld: elements from row to row (0: the rows are contiguous)
+forge_status make_operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, bool e4m3 = false,
+                              int64_t ld = 0) {
+    if (ld == 0) ld = cols;
+    const MapKey key{base, cols, rows, ld, e4m3};
     uint64_t h = reinterpret_cast<uintptr_t>(base) * 0x9E3779B97F4A7C15ull;
     h ^= static_cast<uint64_t>(cols) * 0xC2B2AE3D27D4EB4Full ^ static_cast<uint64_t>(rows) * 0x165667B19E3779F9ull;
     h ^= e4m3 ? 0x27D4EB2F165667C5ull : 0;
+    h ^= static_cast<uint64_t>(ld - cols) * 0x85EBCA77C2B2AE63ull;
     MapSlot& slot = t_maps[(h >> 32) % kMapSlots];
     if (slot.used && slot.key == key) {
         *map = slot.map;
         return FORGE_OK;
     }
-    forge_status st = encode_operand_map(map, base, cols, rows, e4m3);
+    forge_status st = encode_operand_map(map, base, cols, rows, e4m3, ld);
     if (st == FORGE_OK) {
         slot.key = key;
         slot.map = *map;
@@ -419,11 +424,13 @@ forge_status run_opt(const float* dW, void* W, void* m, void* v, float* qscales,
 
 // One layer's kernel arguments and tensor maps for tile shape ts.  e4m3: dY and X are E4M3 codes and
 // the gradient tile is scaled by g_scale = s_dY * s_X (or per channel by row_scales x col_scales).
+// dy_ld: elements between dY's rows where they are not contiguous; v_scales: where the INT8 scales of v
+// are not right behind those of m (both for a run of rows of a larger layer).
 forge_status prepare_layer(forge::TileArgs& a, CUtensorMap* maps, const void* dY, const void* X, float* dW, void* W,
                            void* m, void* v, float* qscales, forge_opt_kind k, const forge_hparams* hp,
                            const forge_shape* shape, int64_t step, uint64_t seed, const DeviceInfo& dev, TileShape ts,
                            bool e4m3, float g_scale, const float* row_scales, const float* col_scales,
-                           int withhold) {
+                           int withhold, int64_t dy_ld = 0, float* v_scales = nullptr) {
     const bool int8 = shape->state == FORGE_STATE_INT8_B64;
     const uint64_t n = static_cast<uint64_t>(shape->d_out) * static_cast<uint64_t>(shape->d_in);
     std::memset(&a, 0, sizeof(a));
@@ -443,7 +450,7 @@ forge_status prepare_layer(forge::TileArgs& a, CUtensorMap* maps, const void* dY
     a.m = m;
     a.v = v;
     a.m_scales = int8 ? qscales : nullptr;
-    a.v_scales = int8 ? qscales + n / 64 : nullptr;
+    a.v_scales = !int8 ? nullptr : v_scales != nullptr ? v_scales : qscales + n / 64;
     if (hp != nullptr) a.s = derive_scalars(k, *hp, step);
     a.seed = seed;
     a.step = static_cast<uint64_t>(step);
@@ -451,7 +458,7 @@ forge_status prepare_layer(forge::TileArgs& a, CUtensorMap* maps, const void* dY
     a.wait_limit_ns = g_wait_limit_ns.load();
     a.acc_wait_limit_ns = acc_wait_limit(a.wait_limit_ns, a.k_blocks);
     a.withhold_first_stage = withhold;
-    forge_status st = make_operand_map(&maps[0], dY, shape->d_out, shape->T, e4m3);
+    forge_status st = make_operand_map(&maps[0], dY, shape->d_out, shape->T, e4m3, dy_ld);
     if (st != FORGE_OK) return st;
     return make_operand_map(&maps[1], X, shape->d_in, shape->T, e4m3);
 }
@@ -459,14 +466,15 @@ forge_status prepare_layer(forge::TileArgs& a, CUtensorMap* maps, const void* dY
 forge_status run_tile(const void* dY, const void* X, float* dW, void* W, void* m, void* v, float* qscales,
                       forge_opt_kind k, int epi, const forge_hparams* hp, const forge_shape* shape, int64_t step,
                       uint64_t seed, cudaStream_t stream, const DeviceInfo& dev, bool e4m3 = false,
-                      float g_scale = 1.0f, const float* row_scales = nullptr, const float* col_scales = nullptr) {
+                      float g_scale = 1.0f, const float* row_scales = nullptr, const float* col_scales = nullptr,
+                      int64_t dy_ld = 0, float* v_scales = nullptr) {
     // 128 x 64 tiles need bf16 operands and an epilogue on 32-column runs (not INT8 states)
     const bool narrow_ok = !e4m3 && (epi == forge::kEpiStoreGrad || shape->state != FORGE_STATE_INT8_B64);
     const TileShape ts = pick_shape(shape->d_out, shape->d_in, shape->T, dev.num_sms, narrow_ok);
     forge::TileGroup<1> g;
     g.n = 1;
     forge_status st = prepare_layer(g.layer[0], g.maps, dY, X, dW, W, m, v, qscales, k, hp, shape, step, seed, dev,
-                                    ts, e4m3, g_scale, row_scales, col_scales, g_withhold_next.exchange(0));
+                                    ts, e4m3, g_scale, row_scales, col_scales, g_withhold_next.exchange(0), dy_ld, v_scales);
     if (st != FORGE_OK) return st;
     g.tile_start[0] = 0;
     g.tile_start[1] = g.layer[0].num_tiles;
@@ -577,6 +585,56 @@ forge_status launch_dx(const void* dY, const void* W, void* dX, const forge_shap
 }
 
 }  // namespace
+
+namespace forge {
+namespace host {
+
+forge_status device(Device* out) {
+    DeviceInfo* d = nullptr;
+    forge_status st = device_info(&d);
+    if (st == FORGE_OK) *out = Device{d->num_sms, d->status};
+    return st;
+}
+
+forge_status operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld) {
+    return make_operand_map(map, base, cols, rows, false, ld);
+}
+
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
+uint64_t acc_wait_limit_ns(int64_t k_blocks) { return acc_wait_limit(g_wait_limit_ns.load(), k_blocks); }
+int take_withhold() { return g_withhold_next.exchange(0); }
+void count_launch() { g_launches.fetch_add(1); }
+
+forge_status check_step(const void* W, const void* m, const void* v, const float* qscales, forge_opt_kind k,
+                        const forge_hparams* hp, int64_t d_out, int64_t d_in, int32_t state, int64_t step) {
+    const forge_shape shape{0, d_out, d_in, state, 0};
+    if (state != FORGE_STATE_FP32 && state != FORGE_STATE_INT8_B64 && state != FORGE_STATE_BF16)
+        return FORGE_ERR_INVALID_ARGUMENT;
+    return check_opt_args(W, m, v, qscales, k, hp, &shape, step);
+}
+
+forge_status fused_rows(const void* dY, int64_t dy_ld, const void* X, int64_t T, int64_t row0, int64_t rows, void* W,
+                        void* m, void* v, float* qscales, forge_opt_kind k, const forge_hparams* hp, int64_t d_out,
+                        int64_t d_in, int32_t state, int64_t step, uint64_t seed, cudaStream_t stream) {
+    DeviceInfo* dev = nullptr;
+    forge_status st = device_info(&dev);
+    if (st != FORGE_OK) return st;
+    if (T == 0 && rows == d_out) {  // no tokens: the gradient is exactly zero
+        const forge_shape whole{0, d_out, d_in, state, 0};
+        return run_opt(nullptr, W, m, v, qscales, k, hp, &whole, step, seed, stream, *dev);
+    }
+    const int64_t first = row0 * d_in, n = d_out * d_in;
+    const int64_t state_bytes = state == FORGE_STATE_INT8_B64 ? 1 : state == FORGE_STATE_BF16 ? 2 : 4;
+    auto at = [&](void* p, int64_t bytes) -> void* { return p == nullptr ? nullptr : static_cast<char*>(p) + first * bytes; };
+    float* ms = qscales == nullptr ? nullptr : qscales + first / 64;
+    float* vs = qscales == nullptr ? nullptr : qscales + n / 64 + first / 64;
+    const forge_shape shape{T, rows, d_in, state, 0};
+    return run_tile(dY, X, nullptr, at(W, 2), at(m, state_bytes), at(v, state_bytes), ms, k, kEpiOptFP32, hp, &shape,
+                    step, seed, stream, *dev, false, 1.0f, nullptr, nullptr, dy_ld, vs);
+}
+
+}  // namespace host
+}  // namespace forge
 
 extern "C" {
 

@@ -1,0 +1,43 @@
+// host.h -- host-side services of forge_api.cu for the library's other translation units (internal;
+// not part of the C ABI).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "forge.h"
+
+namespace forge {
+namespace host {
+
+struct Device {
+    int num_sms;
+    int* status;  // device status word
+};
+
+// The current device, checked to be sm_103a.
+forge_status device(Device* out);
+
+// Tensor map of a row-major bfloat16 operand [rows, cols] whose rows start `ld` elements apart, read
+// in boxes of 64 x 64 with the 128-byte swizzle.
+forge_status operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld);
+
+uint64_t wait_limit_ns();
+uint64_t acc_wait_limit_ns(int64_t k_blocks);
+int take_withhold();  // the test switch, consumed by the launch that takes it
+void count_launch();
+
+// The fused step's argument checks for a layer.
+forge_status check_step(const void* W, const void* m, const void* v, const float* qscales, forge_opt_kind k,
+                        const forge_hparams* hp, int64_t d_out, int64_t d_in, int32_t state, int64_t step);
+
+// The fused step on rows row0 .. row0 + rows - 1 of a layer's weights [d_out, d_in]: dY [T, rows] with
+// rows `dy_ld` elements apart (a multiple of 8), X [T, d_in]; W, m, v and qscales are the whole layer's.
+forge_status fused_rows(const void* dY, int64_t dy_ld, const void* X, int64_t T, int64_t row0, int64_t rows, void* W,
+                        void* m, void* v, float* qscales, forge_opt_kind k, const forge_hparams* hp, int64_t d_out,
+                        int64_t d_in, int32_t state, int64_t step, uint64_t seed, cudaStream_t stream);
+
+}  // namespace host
+}  // namespace forge

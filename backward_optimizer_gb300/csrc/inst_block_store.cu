@@ -1,0 +1,13 @@
+// The matrix-product kernel with the epilogue kBlockStore.
+#include "block_instantiate.cuh"
+
+template cudaError_t forge::launch_block<forge::kBlockStore>(const void*, bool, int, cudaStream_t);
+
+cudaError_t forge::block_pairs(int num_sms, int* pairs) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    cudaError_t err = block_config<256, 2, kBlockStore, kMaxProducts>(cfg, attr, num_sms, nullptr);
+    if (err != cudaSuccess) return err;
+    // every epilogue has the same shared memory and one CTA per SM, so one count serves all
+    return cudaOccupancyMaxActiveClusters(pairs, forge_block_kernel<256, 2, kBlockStore, kMaxProducts>, &cfg);
+}

@@ -60,4 +60,46 @@ FORGE_HD int tail_tile(int t, int split_from, int& part) {
     return split_from + ((t - split_from) >> 1);
 }
 
+// The units of work of a matrix-product launch (block_kernel.cuh), numbered longest first.  Units
+// 0 .. n_long-1 take about the same time, longer than the rest.  They go round the pairs; the pairs
+// left with one long unit less than the others take `fill` short units each first, and the remaining
+// short units go round all of them, beginning with those pairs.
+struct UnitPlan {
+    int n_units, n_long, fill;
+};
+
+// `longest` and `shortest`: the two kinds' times, in any unit.
+FORGE_HD UnitPlan plan_units(int n_units, int n_long, int pairs, int longest, int shortest) {
+    UnitPlan u{n_units, n_long, 0};
+    const int rest = n_long % pairs, n_short = n_units - n_long;
+    if (rest > 0 && n_short > 0) {
+        const int ratio = longest / (shortest > 0 ? shortest : 1), each = n_short / (pairs - rest);
+        u.fill = ratio < each ? ratio : each;
+    }
+    return u;
+}
+
+// The units of pair p, in increasing order; -1 after the last.
+struct UnitCursor {
+    int phase, i;
+    FORGE_HD UnitCursor() : phase(0), i(0) {}
+    FORGE_HD int next(const UnitPlan& g, int p, int pairs) {
+        const int rest = g.n_long % pairs;
+        if (phase == 0) {
+            const int u = p + pairs * i++;
+            if (u < g.n_long) return u;
+            phase = 1;
+            i = 0;
+        }
+        if (phase == 1) {
+            if (rest > 0 && p >= rest && i < g.fill) return g.n_long + (p - rest) + (pairs - rest) * i++;
+            phase = 2;
+            i = 0;
+        }
+        const int at = p >= rest ? p - rest : p - rest + pairs;
+        const int u = g.n_long + (rest > 0 ? g.fill * (pairs - rest) : 0) + at + pairs * i++;
+        return u < g.n_units ? u : -1;
+    }
+};
+
 }  // namespace forge

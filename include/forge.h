@@ -279,6 +279,136 @@ FORGE_API forge_status forge_linear_backward(const void *dY, const void *X, void
                                              const forge_hparams *hp, const forge_shape *shape, int64_t step,
                                              uint64_t seed, struct CUstream_st *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Operators around the fused layers
+ * ---------------------------------------------------------------------------------------------
+ * The norm in front of a block, the gated feed-forward block, and the cross entropy of a linear
+ * head, each with its backward pass.  The conventions above hold: row-major contiguous device
+ * memory owned by the caller, bfloat16 unless said otherwise, results in place of the buffers passed
+ * for them, everything queued on `stream`, argument errors returned before any launch.  The library
+ * allocates nothing: what an operator keeps between its kernels lies in `workspace`, at least as many
+ * bytes as the operator's workspace function answers (which needs a device, and answers -1 for
+ * arguments the operator refuses or without a device), 256-byte aligned, free for other use once the
+ * call's work on the stream is done.  Matrices are 32-byte aligned.  Sums are FP32; a value is rounded
+ * to bfloat16 where it is stored as an operand of the next product, and nowhere else.  Results do not
+ * depend on timing: the same call on the same inputs gives the same bits.
+ */
+
+typedef enum forge_norm_kind { FORGE_NORM_LAYER = 0, FORGE_NORM_RMS = 1 } forge_norm_kind;
+typedef enum forge_type { FORGE_TYPE_BF16 = 0, FORGE_TYPE_FP32 = 1 } forge_type;
+typedef enum forge_act { FORGE_ACT_SILU = 0, FORGE_ACT_GELU_TANH = 1, FORGE_ACT_RELU = 2 } forge_act;
+
+typedef struct forge_norm_shape {
+    int64_t T;       /* rows (tokens), >= 0 */
+    int64_t D;       /* columns, 1 .. 2^24 */
+    int32_t kind;    /* forge_norm_kind */
+    int32_t x_type;  /* forge_type of x, y, dy, dx, add */
+    int32_t w_type;  /* forge_type of weight and bias */
+    int32_t reserved;
+} forge_norm_shape;
+
+/* y = (x - mu) r * weight (+ bias), r = 1 / sqrt(mean((x - mu)^2) + eps), per row of x [T, D]; mu is the
+ * row's mean (FORGE_NORM_LAYER) or 0 (FORGE_NORM_RMS).  mean and rstd: FP32 [T], what the backward
+ * pass needs; either may be null.  bias may be null; it and mean must be null for FORGE_NORM_RMS.
+ * Pointers need only their elements' alignment; 16-byte aligned ones with rows of a multiple of 16
+ * bytes are faster.  y may be x. */
+FORGE_API forge_status forge_layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean,
+                                        float *rstd, float eps, const forge_norm_shape *shape,
+                                        struct CUstream_st *stream);
+
+/* From dy [T, D], x, weight and the forward pass's mean and rstd:
+ *   dx = r (w dy - mean(w dy) - xh mean(w dy xh)) (+ add), xh = (x - mu) r   (RMS: no mean(w dy), mean null)
+ *   dweight [D] = sum_t dy xh, dbias [D] = sum_t dy   (both FP32; dbias null exactly for FORGE_NORM_RMS)
+ * add [T, D] may be null: the gradient that reaches x past the norm, along a residual branch.  dx may
+ * be dy or add.  T = 0 sets dweight and dbias to zero. */
+FORGE_API forge_status forge_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean,
+                                                 const float *rstd, const void *add, void *dx, float *dweight,
+                                                 float *dbias, void *workspace, int64_t workspace_bytes,
+                                                 const forge_norm_shape *shape, struct CUstream_st *stream);
+FORGE_API int64_t forge_layer_norm_backward_workspace(const forge_norm_shape *shape);
+
+typedef struct forge_gated_shape {
+    int64_t T;        /* tokens, >= 0 */
+    int64_t d_model;  /* >= 8, a multiple of 8 */
+    int64_t d_ff;     /* >= 8, a multiple of 8 */
+    int32_t act;      /* forge_act */
+    int32_t reserved;
+} forge_gated_shape;
+
+/* Y [T, d_model] = H Wd^T (+ residual [T, d_model]), H = act(X Wg^T) * (X Wu^T), with X [T, d_model],
+ * Wg and Wu [d_ff, d_model], Wd [d_model, d_ff].  G and U [T, d_ff], both or neither null: X Wg^T and
+ * X Wu^T rounded to bfloat16, which the backward pass needs.  residual may be null.  Gate, up projection,
+ * activation and their product are one kernel.  Y must not overlap X; it may be residual. */
+FORGE_API forge_status forge_gated_mlp(const void *X, const void *Wg, const void *Wu, const void *Wd,
+                                       const void *residual, void *Y, void *G, void *U, void *workspace,
+                                       int64_t workspace_bytes, const forge_gated_shape *shape,
+                                       struct CUstream_st *stream);
+
+/* The block's gradients from dY [T, d_model] and the forward pass's X, G and U:
+ *   dH = dY Wd, dU = dH act(G), dG = dH U act'(G), dX = dG Wg + dU Wu,
+ *   dWg = dG^T X, dWu = dU^T X, dWd = dY^T (act(G) U)                    (all bfloat16)
+ * dX may be null: it is not computed.  T = 0 sets the weights' gradients to zero.  (The gradient of
+ * the residual is dY itself.) */
+FORGE_API forge_status forge_gated_mlp_backward(const void *dY, const void *X, const void *G, const void *U,
+                                                const void *Wg, const void *Wu, const void *Wd, void *dX, void *dWg,
+                                                void *dWu, void *dWd, void *workspace, int64_t workspace_bytes,
+                                                const forge_gated_shape *shape, struct CUstream_st *stream);
+
+/* The same backward pass with the fused step in place of the weights' gradients: dX from the weights as
+ * they are (null: not computed), then one forge_fused_dw_step_layers call that updates the gate's, the
+ * up projection's and the down projection's W, m, v in place.  Of each forge_layer only W, m, v, qscales
+ * and seed are read.  The gradients of the weights never exist. */
+FORGE_API forge_status forge_gated_mlp_backward_step(const void *dY, const void *X, const void *G, const void *U,
+                                                     const forge_layer *gate, const forge_layer *up,
+                                                     const forge_layer *down, void *dX, void *workspace,
+                                                     int64_t workspace_bytes, int32_t state, forge_opt_kind opt_kind,
+                                                     const forge_hparams *hp, const forge_gated_shape *shape,
+                                                     int64_t step, struct CUstream_st *stream);
+
+/* backward: 0 for forge_gated_mlp, 1 for either backward call. */
+FORGE_API int64_t forge_gated_mlp_workspace(const forge_gated_shape *shape, int32_t backward);
+
+typedef struct forge_loss_shape {
+    int64_t T;             /* tokens, >= 0 */
+    int64_t vocab;         /* >= 1, any */
+    int64_t d_model;       /* >= 8, a multiple of 8 */
+    int64_t ignore_index;  /* target of a token without loss */
+    int64_t reserved;
+} forge_loss_shape;
+
+/* Softmax cross entropy of the logits X W^T, X [T, d_model], W [vocab, d_model], without the logits in
+ * memory: lse[t] = log sum_v exp(x_t . w_v), loss[t] = lse[t] - x_t . w_target[t]; loss and lse FP32 [T],
+ * target int64 [T].  A token whose target is ignore_index has loss 0 (and its lse).  Any other target
+ * outside 0 .. vocab-1 has loss NaN. */
+FORGE_API forge_status forge_linear_cross_entropy(const void *X, const void *W, const int64_t *target, float *loss,
+                                                  float *lse, void *workspace, int64_t workspace_bytes,
+                                                  const forge_loss_shape *shape, struct CUstream_st *stream);
+
+/* Its gradients, given dloss [T] (FP32, the gradient of each token's loss) and the forward pass's lse:
+ *   g[t, v] = dloss[t] (exp(x_t . w_v - lse[t]) - [v = target[t]]), 0 where target[t] = ignore_index
+ *   dX [T, d_model] = g W, dW [vocab, d_model] = g^T X                     (bfloat16)
+ * g is made one piece of the vocabulary at a time, rounded to bfloat16, in the workspace.  Either of dX
+ * and dW may be null: it is not computed.  A target outside the vocabulary that is not ignore_index
+ * makes the gradients NaN.  T = 0 sets dW to zero. */
+FORGE_API forge_status forge_linear_cross_entropy_backward(const void *X, const void *W, const int64_t *target,
+                                                           const float *lse, const float *dloss, void *dX, void *dW,
+                                                           void *workspace, int64_t workspace_bytes,
+                                                           const forge_loss_shape *shape, struct CUstream_st *stream);
+
+/* The same backward pass with the fused step in place of dW: piece by piece, g, its part of dX (null: not
+ * computed) from the weights as they were, then the fused step on the piece's rows of W, m, v (qscales as
+ * for the whole layer [vocab, d_model]).  Piece i's stochastic rounding runs under the key
+ * seed ^ (i << 40). */
+FORGE_API forge_status forge_linear_cross_entropy_step(const void *X, void *W, const int64_t *target, const float *lse,
+                                                       const float *dloss, void *dX, void *m, void *v, float *qscales,
+                                                       void *workspace, int64_t workspace_bytes, int32_t state,
+                                                       forge_opt_kind opt_kind, const forge_hparams *hp,
+                                                       const forge_loss_shape *shape, int64_t step, uint64_t seed,
+                                                       struct CUstream_st *stream);
+
+/* backward: 0 for forge_linear_cross_entropy, 1 for either backward call. */
+FORGE_API int64_t forge_linear_cross_entropy_workspace(const forge_loss_shape *shape, int32_t backward);
+
 /* Waits for `stream`, then reads and clears the device status word of the current
  * device: FORGE_ERR_TIMEOUT if a bounded wait ran out in a kernel (on any stream of
  * this device) since the last read, FORGE_ERR_CUDA if the stream reported an error,
