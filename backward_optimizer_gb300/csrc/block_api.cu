@@ -615,6 +615,8 @@ __global__ void __launch_bounds__(32 * kFinishWarps)
     loss_finish_kernel(const float2* stats, int parts, int rows, const int64_t* target, int64_t vocab, int64_t ignore,
                        float* loss, float* lse) {
     __shared__ float2 part[kFinishWarps][32];
+    forge::stream_release();
+    forge::stream_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * 32 + lane;
     float m = -INFINITY, s = 0.0f;
@@ -646,6 +648,8 @@ __global__ void __launch_bounds__(32 * kFinishWarps)
 __global__ void __launch_bounds__(1024)
     loss_unit_kernel(const float* dloss, const int64_t* target, int64_t ignore, int rows, float* unit) {
     __shared__ float part[32];
+    forge::stream_release();
+    forge::stream_wait();
     float m = 0.0f;
     for (int i = threadIdx.x; i < rows; i += 1024) m = fmaxf(m, target[i] == ignore ? 0.0f : fabsf(dloss[i]));
 #pragma unroll
@@ -814,10 +818,9 @@ forge_status forge_linear_cross_entropy(const void* X, const void* W, const int6
     FORGE_TRY(set_map(g, 0, Operand{X, s.d_model, s.T, s.d_model}));
     FORGE_TRY(set_map(g, 1, Operand{W, s.d_model, s.vocab, s.d_model}));
     FORGE_TRY(launch<forge::kBlockLossStats>(g, l.plan, stream));
-    loss_finish_kernel<<<static_cast<unsigned>(ceil_div(s.T, 32)), 32 * kFinishWarps, 0, stream>>>(
-        b.stats, l.stat_parts, static_cast<int>(s.T), target, s.vocab, s.ignore_index, loss, lse);
-    host::count_launch();
-    return cuda_status(cudaGetLastError());
+    return cuda_status(host::launch_early(loss_finish_kernel, dim3(static_cast<unsigned>(ceil_div(s.T, 32))),
+                                          dim3(32 * kFinishWarps), 0, stream, b.stats, l.stat_parts,
+                                          static_cast<int>(s.T), target, s.vocab, s.ignore_index, loss, lse));
 }
 
 forge_status forge_linear_cross_entropy_backward(const void* X, const void* W, const int64_t* target, const float* lse,
@@ -842,9 +845,9 @@ forge_status forge_linear_cross_entropy_backward(const void* X, const void* W, c
     const LossBackward l = layout_loss_backward(mc, s, dx, dw, false);
     FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     char* ws = static_cast<char*>(workspace);
-    loss_unit_kernel<<<1, 1024, 0, stream>>>(dloss, target, s.ignore_index, static_cast<int>(s.T),
-                                             reinterpret_cast<float*>(ws + l.unit));
-    host::count_launch();
+    FORGE_TRY(cuda_status(host::launch_early(loss_unit_kernel, dim3(1), dim3(1024), 0, stream, dloss, target,
+                                             s.ignore_index, static_cast<int>(s.T),
+                                             reinterpret_cast<float*>(ws + l.unit))));
     for (int64_t i = 0; i < l.pieces; ++i) {
         const LossPiece p = loss_piece_of(mc, s, l, i, X, W, dX, dW, dx, dw, ws);
         FORGE_TRY(run_loss_grad(mc, l, p, s, X, W, target, lse, dloss, ws, stream));

@@ -9,7 +9,7 @@
 namespace forge {
 
 template <int BN, int CG, int EPI, int NP>
-cudaError_t block_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int units, cudaStream_t stream) {
+cudaError_t block_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int units, cudaStream_t stream) {
     using C = BlockCfg<BN, CG>;
     static std::atomic<uint64_t> configured{0};  // one bit per device ordinal
     int dev = 0;
@@ -22,16 +22,18 @@ cudaError_t block_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int
         if (err != cudaSuccess) return err;
         configured.fetch_or(bit);
     }
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = CG;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(units * CG, 1, 1);
     cfg.blockDim = dim3(C::kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = stream;
-    cfg.attrs = CG > 1 ? &attr : nullptr;
-    cfg.numAttrs = CG > 1 ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG > 1 ? 2 : 1;
     return cudaSuccess;
 }
 
@@ -39,7 +41,7 @@ template <int BN, int CG, int EPI>
 cudaError_t launch_block_as(const void* group, int units, cudaStream_t stream) {
     constexpr int NP = EPI == kBlockStore ? kMaxProducts : 1;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
+    cudaLaunchAttribute attr[2];
     cudaError_t err = block_config<BN, CG, EPI, NP>(cfg, attr, units, stream);
     if (err != cudaSuccess) return err;
     return cudaLaunchKernelEx(&cfg, forge_block_kernel<BN, CG, EPI, NP>, *static_cast<const BlockGroup<NP>*>(group));

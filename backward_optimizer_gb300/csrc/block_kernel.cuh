@@ -509,6 +509,9 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
     __syncthreads();
     if constexpr (CG > 1) cluster_sync();
     tc_fence_after();
+    // the set-up above touches no memory of the stream's other work
+    stream_release();
+    stream_wait();
     const uint32_t tmem_base = *tmem_slot;
     const AbortCtx ab{abort_flag, grp.status, grp.wait_limit_ns};
     uint64_t n_issued = 0;

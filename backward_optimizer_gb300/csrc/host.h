@@ -29,6 +29,24 @@ uint64_t acc_wait_limit_ns(int64_t k_blocks);
 int take_withhold();  // the test switch, consumed by the launch that takes it
 void count_launch();
 
+// Launches `kernel` so that it may start while the kernel before it on the stream is still running: for
+// kernels that call stream_wait() (ptx.cuh) before they touch memory.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // The fused step's argument checks for a layer.
 forge_status check_step(const void* W, const void* m, const void* v, const float* qscales, forge_opt_kind k,
                         const forge_hparams* hp, int64_t d_out, int64_t d_in, int32_t state, int64_t step);

@@ -5,7 +5,7 @@ template cudaError_t forge::launch_block<forge::kBlockStore>(const void*, bool, 
 
 cudaError_t forge::block_pairs(int num_sms, int* pairs) {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
+    cudaLaunchAttribute attr[2];
     cudaError_t err = block_config<256, 2, kBlockStore, kMaxProducts>(cfg, attr, num_sms, nullptr);
     if (err != cudaSuccess) return err;
     // every epilogue has the same shared memory and one CTA per SM, so one count serves all

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "forge.h"
 #include "host.h"
@@ -32,41 +33,89 @@ struct NormShape {
     int vec, nv, threads, groups;
 };
 
-NormShape norm_shape(const forge_norm_shape& s, bool vectors, int most) {
+NormShape norm_shape(const forge_norm_shape& s, bool vectors, bool backward) {
     NormShape n;
     n.vec = vectors ? (s.x_type == FORGE_TYPE_BF16 ? 8 : 4) : 1;
-    // scalars take few registers: eight runs of one element cost less than one of eight
-    const int nv_most = vectors ? most : 8;
     const int64_t runs = ceil_div(s.D, n.vec);
-    n.threads = 32;
-    while (n.threads < kNormThreads && runs > 2 * n.threads) n.threads *= 2;
-    const int64_t nv = ceil_div(runs, n.threads);
-    n.nv = nv > nv_most ? 0 : nv > 4 ? 8 : nv > 2 ? 4 : static_cast<int>(nv);
-    n.groups = n.nv == 0 ? 1 : kNormThreads / n.threads;
+    // Four 16-byte runs a thread, eight scalars: longer runs mean fewer threads in a row's sums.  The
+    // layer norm's backward pass holds a weight and two column sums per element, and four runs of them
+    // spill at 512 threads: it takes two or three, whichever keeps more of the block's threads at work
+    // (bf16, 4096 tokens: width 4096 28.7 us with two, 35.3 with four; width 5120 37.5 us with three, 40.6
+    // with two; the RMS norm 24.9 us with four, 30.1 with two).
+    auto shape = [&](int most) {
+        n.threads = static_cast<int>(std::min<int64_t>(ceil_div(runs, 32 * most) * 32, kNormThreads));
+        const int64_t nv = ceil_div(runs, n.threads);
+        n.nv = nv > (vectors ? 4 : 8) ? 0 : nv > 4 ? 8 : static_cast<int>(nv);
+        n.groups = n.nv == 0 ? 1 : kNormThreads / n.threads;
+    };
+    shape(vectors ? 4 : 8);
+    if (vectors && backward && s.kind == FORGE_NORM_LAYER && n.nv > 2) {
+        const NormShape four = n;
+        shape(3);
+        const NormShape three = n;
+        shape(2);
+        // runs at work at once, per run of a thread; rows too long for three runs a thread keep four
+        auto busy = [&](const NormShape& m) { return m.groups * runs * (m.nv == 2 ? 3 : 2); };
+        if (three.nv != 3 && n.nv != 2) n = four;
+        else if (n.nv != 2 || (three.nv == 3 && busy(three) > busy(n))) n = three;
+    }
     return n;
 }
 
+// Shared memory of the rings; the rest is the block's own few KB of static memory.
+constexpr int64_t kRingBytes = 200 * 1024;
+
+// Slots of each group's ring: what the groups' shares hold (0: the row is not made of 16-byte runs, or
+// too long for registers; those that fit there always leave two slots).
+int ring_slots(const forge_norm_shape& s, const NormShape& n, int tensors) {
+    if (n.vec == 1 || n.nv == 0) return 0;
+    const int64_t slot = s.D * (s.x_type == FORGE_TYPE_BF16 ? 2 : 4) * tensors;
+    return static_cast<int>(std::min<int64_t>(kRingBytes / n.groups / slot, forge::kNormMaxSlots));
+}
+
+// slots: of the rings, or 0 for the kernels without them
 template <class TX, int VEC, bool CENTER, bool BWD>
-forge_status run_norm_as(const NormArgs& a, const NormShape& n, int blocks, size_t smem, cudaStream_t stream) {
+forge_status run_norm_as(const NormArgs& a, const NormShape& n, int blocks, size_t smem, int slots,
+                         cudaStream_t stream) {
     auto go = [&](auto kernel) {
-        kernel<<<blocks, dim3(n.threads, n.groups), smem, stream>>>(a);
-        host::count_launch();
-        return cudaGetLastError() == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+        return host::launch_early(kernel, dim3(blocks), dim3(n.threads, n.groups), smem, stream, a) == cudaSuccess
+                   ? FORGE_OK
+                   : FORGE_ERR_CUDA;
     };
-#define FORGE_NORM_CASE(NV)                                                                   \
+    if constexpr (VEC > 1) {
+        auto ring = [&](auto kernel) {
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
+                return FORGE_ERR_CUDA;
+            return host::launch_early(kernel, dim3(blocks), dim3(n.threads, n.groups), smem, stream, a, slots) ==
+                           cudaSuccess
+                       ? FORGE_OK
+                       : FORGE_ERR_CUDA;
+        };
+        auto pick = [&](auto nv) {
+            if constexpr (BWD) return ring(forge::forge_norm_bwd_ring_kernel<TX, nv.value, CENTER>);
+            else return ring(forge::forge_norm_ring_kernel<TX, nv.value, CENTER>);
+        };
+        switch (slots > 0 ? n.nv : 0) {
+            case 1: return pick(std::integral_constant<int, 1>{});
+            case 2: return pick(std::integral_constant<int, 2>{});
+            case 3: return pick(std::integral_constant<int, 3>{});
+            case 4: return pick(std::integral_constant<int, 4>{});
+        }
+    }
+#define FORGE_NORM_CASE(NV, REACHED)                                                          \
     case NV:                                                                                  \
-        if constexpr (BWD) return go(forge::forge_norm_bwd_kernel<TX, VEC, NV, CENTER>);      \
-        else return go(forge::forge_norm_kernel<TX, VEC, NV, CENTER>);
+        if constexpr (REACHED) {                                                              \
+            if constexpr (BWD) return go(forge::forge_norm_bwd_kernel<TX, VEC, NV, CENTER>);  \
+            else return go(forge::forge_norm_kernel<TX, VEC, NV, CENTER>);                    \
+        }                                                                                     \
+        break;
     switch (n.nv) {
-        FORGE_NORM_CASE(1)
-        FORGE_NORM_CASE(2)
-        FORGE_NORM_CASE(4)
-        FORGE_NORM_CASE(0)
-        case 8:
-            if constexpr (VEC == 1) {
-                if constexpr (BWD) return go(forge::forge_norm_bwd_kernel<TX, 1, 8, CENTER>);
-                else return go(forge::forge_norm_kernel<TX, 1, 8, CENTER>);
-            }
+        FORGE_NORM_CASE(1, VEC == 1)
+        FORGE_NORM_CASE(2, VEC == 1)
+        FORGE_NORM_CASE(3, VEC == 1)
+        FORGE_NORM_CASE(4, VEC == 1)
+        FORGE_NORM_CASE(8, VEC == 1)
+        FORGE_NORM_CASE(0, true)
     }
 #undef FORGE_NORM_CASE
     return FORGE_ERR_UNSUPPORTED;
@@ -74,20 +123,20 @@ forge_status run_norm_as(const NormArgs& a, const NormShape& n, int blocks, size
 
 template <bool BWD>
 forge_status run_norm(const NormArgs& a, const forge_norm_shape& s, const NormShape& n, int blocks, size_t smem,
-                      cudaStream_t stream) {
+                      int slots, cudaStream_t stream) {
     const bool center = s.kind == FORGE_NORM_LAYER;
     if (s.x_type == FORGE_TYPE_BF16) {
         if (n.vec == 8)
-            return center ? run_norm_as<__nv_bfloat16, 8, true, BWD>(a, n, blocks, smem, stream)
-                          : run_norm_as<__nv_bfloat16, 8, false, BWD>(a, n, blocks, smem, stream);
-        return center ? run_norm_as<__nv_bfloat16, 1, true, BWD>(a, n, blocks, smem, stream)
-                      : run_norm_as<__nv_bfloat16, 1, false, BWD>(a, n, blocks, smem, stream);
+            return center ? run_norm_as<__nv_bfloat16, 8, true, BWD>(a, n, blocks, smem, slots, stream)
+                          : run_norm_as<__nv_bfloat16, 8, false, BWD>(a, n, blocks, smem, slots, stream);
+        return center ? run_norm_as<__nv_bfloat16, 1, true, BWD>(a, n, blocks, smem, slots, stream)
+                      : run_norm_as<__nv_bfloat16, 1, false, BWD>(a, n, blocks, smem, slots, stream);
     }
     if (n.vec == 4)
-        return center ? run_norm_as<float, 4, true, BWD>(a, n, blocks, smem, stream)
-                      : run_norm_as<float, 4, false, BWD>(a, n, blocks, smem, stream);
-    return center ? run_norm_as<float, 1, true, BWD>(a, n, blocks, smem, stream)
-                  : run_norm_as<float, 1, false, BWD>(a, n, blocks, smem, stream);
+        return center ? run_norm_as<float, 4, true, BWD>(a, n, blocks, smem, slots, stream)
+                      : run_norm_as<float, 4, false, BWD>(a, n, blocks, smem, slots, stream);
+    return center ? run_norm_as<float, 1, true, BWD>(a, n, blocks, smem, slots, stream)
+                  : run_norm_as<float, 1, false, BWD>(a, n, blocks, smem, slots, stream);
 }
 
 // 16-byte runs need the row length and every pointer to allow them
@@ -110,8 +159,11 @@ bool elements_fit(const forge_norm_shape& s, std::initializer_list<const void*> 
     return true;
 }
 
-int backward_blocks(const forge_norm_shape& s, const NormShape& n, int num_sms) {
-    return static_cast<int>(std::min<int64_t>(ceil_div(s.T, n.groups), num_sms));
+// Blocks that walk rows: one per SM, and no more groups than there are rows for.
+int norm_blocks(const forge_norm_shape& s, NormShape& n, int num_sms) {
+    const int blocks = static_cast<int>(std::min<int64_t>(s.T, num_sms));
+    n.groups = static_cast<int>(std::min<int64_t>(n.groups, ceil_div(s.T, blocks)));
+    return blocks;
 }
 
 }  // namespace
@@ -142,10 +194,18 @@ forge_status forge_layer_norm(const void* x, const void* weight, const void* bia
     a.D = static_cast<int>(s.D);
     a.eps = eps;
     a.y = y;
-    NormShape n = norm_shape(s, vectors_fit(s, {x, weight, bias, y}), 4);
+    a.status = dev.status;
+    a.wait_limit_ns = host::wait_limit_ns();
+    NormShape n = norm_shape(s, vectors_fit(s, {x, weight, bias, y}), false);
+    const int slots = ring_slots(s, n, 1);
+    if (slots > 0) {
+        const int blocks = norm_blocks(s, n, dev.num_sms);
+        const int64_t smem = n.groups * slots * s.D * (s.x_type == FORGE_TYPE_BF16 ? 2 : 4);
+        return run_norm<false>(a, s, n, blocks, static_cast<size_t>(smem), slots, stream);
+    }
     if (n.nv > 0) n.groups = std::max(1, 128 / n.threads);
     const int blocks = static_cast<int>(std::min<int64_t>(ceil_div(s.T, n.groups), 1 << 20));
-    return run_norm<false>(a, s, n, blocks, 0, stream);
+    return run_norm<false>(a, s, n, blocks, 0, 0, stream);
 }
 
 int64_t forge_layer_norm_backward_workspace(const forge_norm_shape* shape) {
@@ -153,13 +213,8 @@ int64_t forge_layer_norm_backward_workspace(const forge_norm_shape* shape) {
     if (shape->T == 0) return 0;
     host::Device dev;
     if (host::device(&dev) != FORGE_OK) return -1;
-    int64_t most = 0;
-    for (bool vectors : {false, true}) {
-        const NormShape n = norm_shape(*shape, vectors, 4);
-        const int64_t blocks = backward_blocks(*shape, n, dev.num_sms);
-        most = std::max(most, blocks > 1 ? blocks * 2 * shape->D * 4 : 0);
-    }
-    return most;
+    const int64_t blocks = std::min<int64_t>(shape->T, dev.num_sms);
+    return blocks > 1 ? blocks * 2 * shape->D * 4 : 0;
 }
 
 forge_status forge_layer_norm_backward(const void* dy, const void* x, const void* weight, const float* mean,
@@ -184,8 +239,8 @@ forge_status forge_layer_norm_backward(const void* dy, const void* x, const void
             return FORGE_ERR_CUDA;
         return FORGE_OK;
     }
-    NormShape n = norm_shape(s, vectors_fit(s, {dy, x, add, weight, dx}), 4);
-    const int blocks = backward_blocks(s, n, dev.num_sms);
+    NormShape n = norm_shape(s, vectors_fit(s, {dy, x, add, weight, dx}), true);
+    const int blocks = norm_blocks(s, n, dev.num_sms);
     const int64_t width = (layer ? 2 : 1) * s.D;
     if (blocks > 1 && (workspace == nullptr || workspace_bytes < blocks * width * 4)) return FORGE_ERR_INVALID_ARGUMENT;
     if (blocks > 1 && !aligned(workspace, 16)) return FORGE_ERR_MISALIGNED;
@@ -203,13 +258,19 @@ forge_status forge_layer_norm_backward(const void* dy, const void* x, const void
     a.part = blocks > 1 ? static_cast<float*>(workspace) : dweight;
     a.part_b = blocks > 1 ? a.part + s.D : dbias;
     a.part_step = width;
-    const size_t smem = n.groups > 1 ? static_cast<size_t>(width) * 4 : 0;
-    st = run_norm<true>(a, s, n, blocks, smem, stream);
+    a.status = dev.status;
+    a.wait_limit_ns = host::wait_limit_ns();
+    const int slots = ring_slots(s, n, add != nullptr ? 3 : 2);
+    // the rings, and after them the groups' columns
+    const int64_t slot_bytes = s.D * (s.x_type == FORGE_TYPE_BF16 ? 2 : 4) * (add != nullptr ? 3 : 2);
+    const int64_t smem = n.nv == 0 ? 0 : std::max(n.groups * slots * slot_bytes, n.groups * width * 4);
+    st = run_norm<true>(a, s, n, blocks, static_cast<size_t>(smem), slots, stream);
     if (st != FORGE_OK || blocks == 1) return st;
-    forge::forge_norm_columns_kernel<<<static_cast<unsigned>(ceil_div(width, 32)), 256, 0, stream>>>(
-        a.part, width, blocks, static_cast<int>(width), dweight, dbias, a.D);
-    host::count_launch();
-    return cudaGetLastError() == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+    return host::launch_early(forge::forge_norm_columns_kernel, dim3(static_cast<unsigned>(ceil_div(width, 32))),
+                              dim3(32 * forge::kColumnWarps), 0, stream, a.part, width, blocks,
+                              static_cast<int>(width), dweight, dbias, a.D) == cudaSuccess
+               ? FORGE_OK
+               : FORGE_ERR_CUDA;
 }
 
 }  // extern "C"

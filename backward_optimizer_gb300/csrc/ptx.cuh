@@ -114,6 +114,15 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// ---------------------------------------------------------------- dependent launches
+// A kernel launched with programmatic stream serialization may start while the kernel before it on
+// the stream is still running.  It calls stream_wait() before it touches any memory that the stream's
+// earlier work reads or writes (every thread, so that nothing is ordered by luck), and lets the next
+// kernel start early with stream_release().
+
+__device__ __forceinline__ void stream_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void stream_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
@@ -139,6 +148,15 @@ __device__ __forceinline__ void tma_load_2d_cg(void* dst, const CUtensorMap* map
             "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
             : "memory");
     }
+}
+
+// Untiled copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) into this CTA's shared
+// memory, counted in bytes on one of its mbarriers.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_addr(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
 }
 
 __device__ __forceinline__ uint64_t policy_evict_last() {

@@ -18,7 +18,7 @@ import backward_optimizer_gb300 as _fg
 NORM_KINDS = {"layer": 0, "rms": 1}
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1, "relu": 2}
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
-_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+_BF16, _F32 = torch.bfloat16, torch.float32
 
 
 class NormShape(ctypes.Structure):
@@ -62,141 +62,166 @@ def declare(L: ctypes.CDLL) -> None:
         f.argtypes, f.restype = args, i64
 
 
-_bytes: dict = {}  # workspace sizes by device, function and shape: the same for the same sizes
+# The C structure of a shape, ready to pass, and the workspace that the shape needs, by sizes: a training
+# loop makes the same calls over and over, and building them costs as much host time as a small kernel.
+_shapes: dict = {}
 
 
-def _workspace(x, stream, name: str, shape, sizes: tuple, *more):
-    """A workspace of the size that `name` answers for `shape`, from the memory pool of the stream."""
-    key = (x.device.index, name, sizes)
-    n = _bytes.get(key)
+class _Shape:
+    __slots__ = ("arg", "bytes")
+
+    def __init__(self, struct):
+        self.arg, self.bytes = ctypes.byref(struct), {}  # workspace bytes by function, direction and device
+
+
+def _shape(cls, *values) -> _Shape:
+    key = (cls, values)
+    s = _shapes.get(key)
+    if s is None:
+        if len(_shapes) >= 4096:
+            _shapes.clear()
+        s = _shapes[key] = _Shape(cls(*values))
+    return s
+
+
+def _workspace(shape: _Shape, name: str, dev: int, stream, *more):
+    """Pointer and size of a workspace as large as `name` answers for the shape, and the tensor that holds it,
+    from the memory pool of the stream that the call runs on."""
+    n = shape.bytes.get((name, dev, more))
     if n is None:
-        n = getattr(_fg.lib(), name)(ctypes.byref(shape), *more)
-        if n < 0:  # the call itself says what is wrong
-            return None, 0
-        if len(_bytes) >= 4096:
-            _bytes.clear()
-        _bytes[key] = n
-    if n == 0:
-        return None, 0
+        n = getattr(_fg.lib(), name)(shape.arg, *more)
+        if n >= 0:  # else the call itself says what is wrong
+            shape.bytes[(name, dev, more)] = n
+    if n <= 0:
+        return None, 0, None
     if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=x.device), n
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_fg._stream(stream))
-    with torch.cuda.stream(s):
-        return torch.empty(n, dtype=torch.uint8, device=x.device), n
+        t = torch.empty(n, dtype=torch.uint8, device=dev)
+    else:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_fg._stream(stream))
+        with torch.cuda.stream(s):
+            t = torch.empty(n, dtype=torch.uint8, device=dev)
+    return t.data_ptr(), n, t
 
 
-def _here(x, name: str) -> None:
+def _device(x) -> int:
+    """The current device's number; x is checked to be there."""
     if not x.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {x.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    dev = x.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on {x.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _same_device(*ts) -> None:
-    if len({t.device for t in ts if t is not None}) > 1:
-        raise ValueError("tensors must live on one device")
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _fg._stream(stream)
+
+
+def _take(t, dtype, shape: tuple, dev: int, name: str):
+    """The address of an argument, checked: its type, shape, device and layout.  None stays None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous (row-major)")
+    return t.data_ptr()
 
 
 def _one_of(table: dict, key: str, name: str) -> int:
-    if key not in table:
+    v = table.get(key)
+    if v is None:
         raise ValueError(f"{name}: {key!r}, expected one of {list(table)}")
-    return table[key]
+    return v
 
 
-def _matrix(t, name: str):
+def _type(t, name: str) -> int:
+    v = _TYPES.get(t.dtype)
+    if v is None:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected one of {[str(d) for d in _TYPES]}")
+    return v
+
+
+def _matrix(t, name: str) -> tuple:
     if t.dim() != 2:
         raise ValueError(f"{name}: {t.dim()} dimensions, expected 2")
-    return t.shape
+    return tuple(t.shape)
+
+
+def _states(dev: int, W, m, v, qscales) -> None:
+    _fg._state_args(W, m, v, qscales)
+    for t, name in ((m, "m"), (v, "v"), (qscales, "qscales")):
+        if t is not None:
+            _take(t, t.dtype, tuple(t.shape), dev, name)
 
 
 # ------------------------------------------------------------------ norm
-
-
-def _norm_shape(x, weight, kind: str) -> NormShape:
-    T, D = _matrix(x, "x")
-    for t, name in ((x, "x"), (weight, "weight")):
-        if t.dtype not in _TYPES:
-            raise TypeError(f"{name}: dtype {t.dtype}, expected one of {[str(d) for d in _TYPES]}")
-    return NormShape(T, D, _one_of(NORM_KINDS, kind, "kind"), _TYPES[x.dtype], _TYPES[weight.dtype], 0)
 
 
 def layer_norm(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5, kind: str = "layer", stream=None) -> None:
     """y [T, D] = norm(x) * weight (+ bias) row by row: the layer norm, or with kind="rms" the RMS norm
     (no mean, no bias).  x and y bf16 or FP32, weight and bias [D] bf16 or FP32.  mean and rstd, FP32 [T],
     are what layer_norm_backward needs."""
-    shape = _norm_shape(x, weight, kind)
-    T, D = x.shape
-    _here(x, "x")
-    _same_device(x, weight, bias, y, mean, rstd)
-    _fg._expect(weight, (weight.dtype,), (D,), "weight")
-    _fg._expect(bias, (weight.dtype,), (D,), "bias")
-    _fg._expect(y, (x.dtype,), (T, D), "y")
-    _fg._expect(mean, _F32, (T,), "mean")
-    _fg._expect(rstd, _F32, (T,), "rstd")
-    p = _fg._ptr
-    _fg._check(_fg.lib().forge_layer_norm(p(x), p(weight), p(bias), p(y), p(mean), p(rstd), eps, ctypes.byref(shape),
-                                          _fg._stream(stream)), "forge_layer_norm")
+    dev = _device(x)
+    T, D = rows = _matrix(x, "x")
+    dt, wt = x.dtype, weight.dtype
+    shape = _shape(NormShape, T, D, _one_of(NORM_KINDS, kind, "kind"), _type(x, "x"), _type(weight, "weight"), 0)
+    st = _fg.lib().forge_layer_norm(
+        _take(x, dt, rows, dev, "x"), _take(weight, wt, (D,), dev, "weight"), _take(bias, wt, (D,), dev, "bias"),
+        _take(y, dt, rows, dev, "y"), _take(mean, _F32, (T,), dev, "mean"), _take(rstd, _F32, (T,), dev, "rstd"), eps,
+        shape.arg, _raw_stream(stream, dev))
+    _fg._check(st, "forge_layer_norm")
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias=None, add=None, kind: str = "layer",
                         stream=None) -> None:
     """dx [T, D], dweight and dbias (FP32 [D]) of layer_norm from its x and its mean and rstd (RMS norm:
     mean and dbias None).  add [T, D], the gradient along a residual branch past the norm, is added to dx."""
-    shape = _norm_shape(x, weight, kind)
-    T, D = x.shape
-    _here(x, "x")
-    _same_device(x, dy, weight, mean, rstd, dx, dweight, dbias, add)
-    _fg._expect(weight, (weight.dtype,), (D,), "weight")
-    for t, name in ((dy, "dy"), (dx, "dx"), (add, "add")):
-        _fg._expect(t, (x.dtype,), (T, D), name)
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _fg._expect(t, _F32, (T,), name)
-    for t, name in ((dweight, "dweight"), (dbias, "dbias")):
-        _fg._expect(t, _F32, (D,), name)
-    p = _fg._ptr
-    ws, n = _workspace(x, stream, "forge_layer_norm_backward_workspace", shape,
-                       (T, D, shape.kind, shape.x_type, shape.w_type))
-    _fg._check(_fg.lib().forge_layer_norm_backward(p(dy), p(x), p(weight), p(mean), p(rstd), p(add), p(dx), p(dweight),
-                                                   p(dbias), p(ws), n, ctypes.byref(shape), _fg._stream(stream)),
-               "forge_layer_norm_backward")
+    dev = _device(x)
+    T, D = rows = _matrix(x, "x")
+    dt = x.dtype
+    shape = _shape(NormShape, T, D, _one_of(NORM_KINDS, kind, "kind"), _type(x, "x"), _type(weight, "weight"), 0)
+    ws, n, _hold = _workspace(shape, "forge_layer_norm_backward_workspace", dev, stream)
+    st = _fg.lib().forge_layer_norm_backward(
+        _take(dy, dt, rows, dev, "dy"), _take(x, dt, rows, dev, "x"),
+        _take(weight, weight.dtype, (D,), dev, "weight"), _take(mean, _F32, (T,), dev, "mean"),
+        _take(rstd, _F32, (T,), dev, "rstd"), _take(add, dt, rows, dev, "add"), _take(dx, dt, rows, dev, "dx"),
+        _take(dweight, _F32, (D,), dev, "dweight"), _take(dbias, _F32, (D,), dev, "dbias"), ws, n, shape.arg,
+        _raw_stream(stream, dev))
+    _fg._check(st, "forge_layer_norm_backward")
 
 
 # ------------------------------------------------------------------ gated feed-forward block
 
 
-def _gated(X, Wg, Wu, Wd, act: str):
-    T, D = _matrix(X, "X")
-    F = _matrix(Wg, "Wg")[0]
-    _here(X, "X")
-    for t, name, shp in ((X, "X", (T, D)), (Wg, "Wg", (F, D)), (Wu, "Wu", (F, D)), (Wd, "Wd", (D, F))):
-        _fg._expect(t, _BF16, shp, name)
-    return T, D, F, GatedShape(T, D, F, _one_of(ACTIVATIONS, act, "act"), 0)
-
-
 def gated_mlp(X, Wg, Wu, Wd, Y, G=None, U=None, residual=None, act: str = "silu", stream=None) -> None:
     """Y [T, D] = (act(X Wg^T) * (X Wu^T)) Wd^T (+ residual), everything bf16: X [T, D], Wg and Wu [F, D],
     Wd [D, F].  G and U [T, F], both or neither: X Wg^T and X Wu^T, which the backward pass needs."""
-    T, D, F, shape = _gated(X, Wg, Wu, Wd, act)
-    for t, name, shp in ((Y, "Y", (T, D)), (residual, "residual", (T, D)), (G, "G", (T, F)), (U, "U", (T, F))):
-        _fg._expect(t, _BF16, shp, name)
-    _same_device(X, Wg, Wu, Wd, Y, G, U, residual)
-    p = _fg._ptr
-    ws, n = _workspace(X, stream, "forge_gated_mlp_workspace", shape, (T, D, F, 0), 0)
-    _fg._check(_fg.lib().forge_gated_mlp(p(X), p(Wg), p(Wu), p(Wd), p(residual), p(Y), p(G), p(U), p(ws), n,
-                                         ctypes.byref(shape), _fg._stream(stream)), "forge_gated_mlp")
+    dev = _device(X)
+    (T, D), F = _matrix(X, "X"), _matrix(Wg, "Wg")[0]
+    shape = _shape(GatedShape, T, D, F, _one_of(ACTIVATIONS, act, "act"), 0)
+    x, wg, wu = _take(X, _BF16, (T, D), dev, "X"), _take(Wg, _BF16, (F, D), dev, "Wg"), _take(Wu, _BF16, (F, D), dev, "Wu")
+    wd, y, r = _take(Wd, _BF16, (D, F), dev, "Wd"), _take(Y, _BF16, (T, D), dev, "Y"), _take(residual, _BF16, (T, D), dev, "residual")
+    g, u = _take(G, _BF16, (T, F), dev, "G"), _take(U, _BF16, (T, F), dev, "U")
+    ws, n, _hold = _workspace(shape, "forge_gated_mlp_workspace", dev, stream, 0)
+    _fg._check(_fg.lib().forge_gated_mlp(x, wg, wu, wd, r, y, g, u, ws, n, shape.arg, _raw_stream(stream, dev)),
+               "forge_gated_mlp")
 
 
 def gated_mlp_backward(dY, X, G, U, Wg, Wu, Wd, dX, dWg, dWu, dWd, act: str = "silu", stream=None) -> None:
     """The block's gradients, bf16, from dY [T, D] and the forward pass's X, G and U.  dX may be None."""
-    T, D, F, shape = _gated(X, Wg, Wu, Wd, act)
-    for t, name, shp in ((dY, "dY", (T, D)), (G, "G", (T, F)), (U, "U", (T, F)), (dX, "dX", (T, D)),
-                         (dWg, "dWg", (F, D)), (dWu, "dWu", (F, D)), (dWd, "dWd", (D, F))):
-        _fg._expect(t, _BF16, shp, name)
-    _same_device(X, dY, G, U, Wg, Wu, Wd, dX, dWg, dWu, dWd)
-    p = _fg._ptr
-    ws, n = _workspace(X, stream, "forge_gated_mlp_workspace", shape, (T, D, F, 1), 1)
-    _fg._check(_fg.lib().forge_gated_mlp_backward(p(dY), p(X), p(G), p(U), p(Wg), p(Wu), p(Wd), p(dX), p(dWg), p(dWu),
-                                                  p(dWd), p(ws), n, ctypes.byref(shape), _fg._stream(stream)),
+    dev = _device(X)
+    (T, D), F = _matrix(X, "X"), _matrix(Wg, "Wg")[0]
+    shape = _shape(GatedShape, T, D, F, _one_of(ACTIVATIONS, act, "act"), 0)
+    args = [_take(t, _BF16, s, dev, name) for t, s, name in (
+        (dY, (T, D), "dY"), (X, (T, D), "X"), (G, (T, F), "G"), (U, (T, F), "U"), (Wg, (F, D), "Wg"), (Wu, (F, D), "Wu"),
+        (Wd, (D, F), "Wd"), (dX, (T, D), "dX"), (dWg, (F, D), "dWg"), (dWu, (F, D), "dWu"), (dWd, (D, F), "dWd"))]
+    ws, n, _hold = _workspace(shape, "forge_gated_mlp_workspace", dev, stream, 1)
+    _fg._check(_fg.lib().forge_gated_mlp_backward(*args, ws, n, shape.arg, _raw_stream(stream, dev)),
                "forge_gated_mlp_backward")
 
 
@@ -205,82 +230,70 @@ def gated_mlp_backward_step(dY, X, G, U, gate, up, down, dX=None, act: str = "si
     """The block's backward pass with the fused step: dX (None: not computed) from the weights as they are,
     then W, m, v of the three layers updated in place.  gate, up and down are (W, m, v, qscales, seed), as
     fused_dw_step takes them, all with the same state format."""
-    Wg, Wu, Wd = gate[0], up[0], down[0]
-    T, D, F, shape = _gated(X, Wg, Wu, Wd, act)
-    for t, name, shp in ((dY, "dY", (T, D)), (G, "G", (T, F)), (U, "U", (T, F)), (dX, "dX", (T, D))):
-        _fg._expect(t, _BF16, shp, name)
-    _same_device(X, dY, G, U, dX, *gate[:4], *up[:4], *down[:4])
-    p = _fg._ptr
-    arg, states = [], set()
-    for W, m, v, q, seed in (gate, up, down):
-        _fg._state_args(W, m, v, q)
+    dev = _device(X)
+    (T, D), F = _matrix(X, "X"), _matrix(gate[0], "gate's W")[0]
+    shape = _shape(GatedShape, T, D, F, _one_of(ACTIVATIONS, act, "act"), 0)
+    args = [_take(t, _BF16, s, dev, name) for t, s, name in (
+        (dY, (T, D), "dY"), (X, (T, D), "X"), (G, (T, F), "G"), (U, (T, F), "U"))]
+    layers, states, p = [], set(), _fg._ptr
+    for (W, m, v, q, seed), s, name in ((gate, (F, D), "gate"), (up, (F, D), "up"), (down, (D, F), "down")):
+        w = _take(W, _BF16, s, dev, f"{name}'s W")
+        _states(dev, W, m, v, q)
         states.add(_fg._state_of(m, v))
-        arg.append(_fg.ForgeLayer(None, None, p(W), p(m), p(v), p(q), 0, 0, 0, int(seed) & (2**64 - 1)))
+        layers.append(_fg.ForgeLayer(None, None, w, p(m), p(v), p(q), 0, 0, 0, int(seed) & (2**64 - 1)))
     if len(states) > 1:
         raise TypeError("the three layers must use the same state format")
-    ws, n = _workspace(X, stream, "forge_gated_mlp_workspace", shape, (T, D, F, 1), 1)
-    _fg._check(_fg.lib().forge_gated_mlp_backward_step(
-        p(dY), p(X), p(G), p(U), *(ctypes.byref(a) for a in arg), p(dX), p(ws), n, states.pop(), _fg.OPT_KINDS[opt],
-        _fg._hp_arg(hp), ctypes.byref(shape), int(step), _fg._stream(stream)), "forge_gated_mlp_backward_step")
+    ws, n, _hold = _workspace(shape, "forge_gated_mlp_workspace", dev, stream, 1)
+    st = _fg.lib().forge_gated_mlp_backward_step(
+        *args, *(ctypes.byref(a) for a in layers), _take(dX, _BF16, (T, D), dev, "dX"), ws, n, states.pop(),
+        _fg.OPT_KINDS[opt], _fg._hp_arg(hp), shape.arg, int(step), _raw_stream(stream, dev))
+    _fg._check(st, "forge_gated_mlp_backward_step")
 
 
 # ------------------------------------------------------------------ cross entropy of a linear head
-
-
-def _loss(X, W, target, ignore_index: int):
-    T, D = _matrix(X, "X")
-    V = _matrix(W, "W")[0]
-    _here(X, "X")
-    _fg._expect(X, _BF16, (T, D), "X")
-    _fg._expect(W, _BF16, (V, D), "W")
-    _fg._expect(target, (torch.int64,), (T,), "target")
-    return T, V, D, LossShape(T, V, D, int(ignore_index), 0)
 
 
 def linear_cross_entropy(X, W, target, loss, lse, ignore_index: int = -100, stream=None) -> None:
     """loss [T] = lse - logit of the target, lse [T] = log sum exp of the logits X W^T (both FP32), without
     the logits in memory: X [T, D] and W [V, D] bf16, target [T] int64.  The loss is 0 where the target is
     ignore_index, NaN at any other target outside 0 .. V-1."""
-    T, V, D, shape = _loss(X, W, target, ignore_index)
-    _fg._expect(loss, _F32, (T,), "loss")
-    _fg._expect(lse, _F32, (T,), "lse")
-    _same_device(X, W, target, loss, lse)
-    p = _fg._ptr
-    ws, n = _workspace(X, stream, "forge_linear_cross_entropy_workspace", shape, (T, V, D, 0), 0)
-    _fg._check(_fg.lib().forge_linear_cross_entropy(p(X), p(W), p(target), p(loss), p(lse), p(ws), n,
-                                                    ctypes.byref(shape), _fg._stream(stream)),
+    dev = _device(X)
+    (T, D), V = _matrix(X, "X"), _matrix(W, "W")[0]
+    shape = _shape(LossShape, T, V, D, int(ignore_index), 0)
+    x, w, t = _take(X, _BF16, (T, D), dev, "X"), _take(W, _BF16, (V, D), dev, "W"), _take(target, torch.int64, (T,), dev, "target")
+    out, l = _take(loss, _F32, (T,), dev, "loss"), _take(lse, _F32, (T,), dev, "lse")
+    ws, n, _hold = _workspace(shape, "forge_linear_cross_entropy_workspace", dev, stream, 0)
+    _fg._check(_fg.lib().forge_linear_cross_entropy(x, w, t, out, l, ws, n, shape.arg, _raw_stream(stream, dev)),
                "forge_linear_cross_entropy")
+
+
+def _loss_gradient_args(X, W, target, lse, dloss, ignore_index: int):
+    dev = _device(X)
+    (T, D), V = _matrix(X, "X"), _matrix(W, "W")[0]
+    return dev, T, D, V, _shape(LossShape, T, V, D, int(ignore_index), 0), [
+        _take(X, _BF16, (T, D), dev, "X"), _take(W, _BF16, (V, D), dev, "W"), _take(target, torch.int64, (T,), dev, "target"),
+        _take(lse, _F32, (T,), dev, "lse"), _take(dloss, _F32, (T,), dev, "dloss")]
 
 
 def linear_cross_entropy_backward(X, W, target, lse, dloss, dX, dW, ignore_index: int = -100, stream=None) -> None:
     """dX [T, D] and dW [V, D] (bf16, either may be None) given dloss [T], the gradient of each token's loss,
     and the forward pass's lse."""
-    T, V, D, shape = _loss(X, W, target, ignore_index)
-    for t, name in ((lse, "lse"), (dloss, "dloss")):
-        _fg._expect(t, _F32, (T,), name)
-    _fg._expect(dX, _BF16, (T, D), "dX")
-    _fg._expect(dW, _BF16, (V, D), "dW")
-    _same_device(X, W, target, lse, dloss, dX, dW)
-    p = _fg._ptr
-    ws, n = _workspace(X, stream, "forge_linear_cross_entropy_workspace", shape, (T, V, D, 1), 1)
-    _fg._check(_fg.lib().forge_linear_cross_entropy_backward(p(X), p(W), p(target), p(lse), p(dloss), p(dX), p(dW),
-                                                             p(ws), n, ctypes.byref(shape), _fg._stream(stream)),
-               "forge_linear_cross_entropy_backward")
+    dev, T, D, V, shape, args = _loss_gradient_args(X, W, target, lse, dloss, ignore_index)
+    dx, dw = _take(dX, _BF16, (T, D), dev, "dX"), _take(dW, _BF16, (V, D), dev, "dW")
+    ws, n, _hold = _workspace(shape, "forge_linear_cross_entropy_workspace", dev, stream, 1)
+    st = _fg.lib().forge_linear_cross_entropy_backward(*args, dx, dw, ws, n, shape.arg, _raw_stream(stream, dev))
+    _fg._check(st, "forge_linear_cross_entropy_backward")
 
 
 def linear_cross_entropy_step(X, W, target, lse, dloss, dX=None, m=None, v=None, qscales=None, ignore_index: int = -100,
                               opt: str = "adamw", hp: Any = None, step: int = 1, seed: int = 0, stream=None) -> None:
     """The same backward pass with the fused step in place of dW: dX (None: not computed) from the weights as
     they are, and W, m, v updated in place, as fused_dw_step takes them."""
-    T, V, D, shape = _loss(X, W, target, ignore_index)
-    for t, name in ((lse, "lse"), (dloss, "dloss")):
-        _fg._expect(t, _F32, (T,), name)
-    _fg._expect(dX, _BF16, (T, D), "dX")
-    _fg._state_args(W, m, v, qscales)
-    _same_device(X, W, target, lse, dloss, dX, m, v, qscales)
-    p = _fg._ptr
-    ws, n = _workspace(X, stream, "forge_linear_cross_entropy_workspace", shape, (T, V, D, 1), 1)
-    _fg._check(_fg.lib().forge_linear_cross_entropy_step(
-        p(X), p(W), p(target), p(lse), p(dloss), p(dX), p(m), p(v), p(qscales), p(ws), n, _fg._state_of(m, v),
-        _fg.OPT_KINDS[opt], _fg._hp_arg(hp), ctypes.byref(shape), int(step), int(seed) & (2**64 - 1),
-        _fg._stream(stream)), "forge_linear_cross_entropy_step")
+    dev, T, D, V, shape, args = _loss_gradient_args(X, W, target, lse, dloss, ignore_index)
+    dx, p = _take(dX, _BF16, (T, D), dev, "dX"), _fg._ptr
+    _states(dev, W, m, v, qscales)
+    ws, n, _hold = _workspace(shape, "forge_linear_cross_entropy_workspace", dev, stream, 1)
+    st = _fg.lib().forge_linear_cross_entropy_step(
+        *args, dx, p(m), p(v), p(qscales), ws, n, _fg._state_of(m, v), _fg.OPT_KINDS[opt], _fg._hp_arg(hp), shape.arg,
+        int(step), int(seed) & (2**64 - 1), _raw_stream(stream, dev))
+    _fg._check(st, "forge_linear_cross_entropy_step")
