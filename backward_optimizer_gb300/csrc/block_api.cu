@@ -65,7 +65,8 @@ struct Cut {
 
 struct Plan {
     bool pair;
-    int width;  // pairs or CTAs
+    int width;   // pairs or CTAs
+    int a_rows;  // rows of A per stage (BlockGroup::a_rows)
     int n;
     Cut cut[kMaxProducts];
     int64_t part_floats;
@@ -79,7 +80,7 @@ constexpr int kMaxParts = 16;
 // the epilogue of a tile, in slices of the mainloop: only to weigh units against one another
 constexpr int kEpiSlices = 8;
 
-void plan_products(Plan& p, const Machine& mc, bool gated) {
+void plan_products(Plan& p, const Machine& mc, bool gated, bool a_k_major) {
     // Pairs on 256 x 256 tiles move half the operand bytes per product of single CTAs on 128 x 128
     // tiles, so they are taken unless they would leave half of the SMs idle, or every tile's second
     // 128 rows empty.
@@ -95,6 +96,8 @@ void plan_products(Plan& p, const Machine& mc, bool gated) {
     }
     p.pair = tall && 2 * pair_tiles > mc.pairs;
     p.width = p.pair ? mc.pairs : mc.dev.num_sms;
+    p.a_rows = 128;
+    if (p.n == 1 && !p.pair && a_k_major && p.cut[0].rows <= 64) p.a_rows = static_cast<int>(round_up(p.cut[0].rows, 8));
     const int64_t tm = p.pair ? 256 : 128, tn = (p.pair ? 256 : 128) / (gated ? 2 : 1);
     int64_t tiles = 0;
     double work = 0;
@@ -170,7 +173,7 @@ Plan plan_one(const Machine& mc, int64_t rows, int64_t cols, int kb, bool gated 
     p.cut[0].rows = rows;
     p.cut[0].cols = cols;
     p.cut[0].kb = kb;
-    plan_products(p, mc, gated);
+    plan_products(p, mc, gated, true);
     return p;
 }
 
@@ -205,6 +208,7 @@ struct Operand {
 template <int NP>
 forge_status fill_group(BlockGroup<NP>& g, const Plan& p, const Machine& mc, char* ws, const SplitSpace& sp) {
     g.n = p.n;
+    g.a_rows = p.a_rows;
     int u = 0, kb_max = 0;
     int longest = 0;
     for (int i = 0; i < p.n; ++i) {
@@ -251,7 +255,8 @@ forge_status fill_group(BlockGroup<NP>& g, const Plan& p, const Machine& mc, cha
 
 template <int NP>
 forge_status set_map(BlockGroup<NP>& g, int i, const Operand& o) {
-    return host::operand_map(&g.maps[i], o.base, o.cols, o.rows, o.ld);
+    const bool is_a = i % 2 == 0;
+    return host::operand_map(&g.maps[i], o.base, o.cols, o.rows, o.ld, is_a ? std::min(g.a_rows, 64) : 64);
 }
 
 template <int EPI, int NP>
@@ -290,7 +295,7 @@ Plan plan_store(const Machine& mc, Product* pr, int n) {
         p.cut[i].cols = pr[i].cols;
         p.cut[i].kb = slices(pr[i].k[0]) + slices(pr[i].k[1]);
     }
-    plan_products(p, mc, false);
+    plan_products(p, mc, false, pr[0].a_mn == 0);
     return p;
 }
 
@@ -609,35 +614,49 @@ forge_status run_loss_products(const Machine& mc, const LossBackward& l, const L
 }
 
 // Joins the tiles' maxima and sums of one row: lse, and the loss of the target's logit that one tile's
-// epilogue left in `loss`.  A block takes 32 rows; its warps share the parts.
-constexpr int kFinishWarps = 16;
-__global__ void __launch_bounds__(32 * kFinishWarps)
+// epilogue left in `loss`.  A block takes kRows rows (32 with many rows, so that loads of a part are
+// whole lines; 1 with few, so that all threads share the row's parts); its other threads share the parts.
+constexpr int kFinishThreads = 512;
+
+__device__ __forceinline__ void join(float& m, float& s, float vm, float vs) {
+    const float mn = fmaxf(m, vm), base = mn == -INFINITY ? 0.0f : mn;
+    s = s * forge::exp2_fast(m - base) + vs * forge::exp2_fast(vm - base);
+    m = mn;
+}
+
+template <int kRows>
+__global__ void __launch_bounds__(kFinishThreads)
     loss_finish_kernel(const float2* stats, int parts, int rows, const int64_t* target, int64_t vocab, int64_t ignore,
                        float* loss, float* lse) {
-    __shared__ float2 part[kFinishWarps][32];
+    constexpr int kShares = kFinishThreads / kRows;
+    __shared__ float2 part[kShares][kRows];
     forge::stream_release();
     forge::stream_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.x * 32 + lane;
+    const int r = threadIdx.x % kRows, share = threadIdx.x / kRows;
+    const int row = blockIdx.x * kRows + r;
     float m = -INFINITY, s = 0.0f;
     if (row < rows) {
-#pragma unroll 8
-        for (int i = warp; i < parts; i += kFinishWarps) {
-            const float2 v = stats[static_cast<size_t>(i) * rows + row];
-            const float mn = fmaxf(m, v.x), base = mn == -INFINITY ? 0.0f : mn;
-            s = s * forge::exp2_fast(m - base) + v.y * forge::exp2_fast(v.x - base);
-            m = mn;
+        for (int first = share; first < parts; first += 8 * kShares) {
+            float2 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int at = first + i * kShares;
+                v[i] = at < parts ? __ldcg(stats + static_cast<size_t>(at) * rows + row) : make_float2(-INFINITY, 0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) join(m, s, v[i].x, v[i].y);
         }
     }
-    part[warp][lane] = make_float2(m, s);
-    __syncthreads();
-    if (warp != 0 || row >= rows) return;
-    for (int w = 1; w < kFinishWarps; ++w) {
-        const float2 v = part[w][lane];
-        const float mn = fmaxf(m, v.x), base = mn == -INFINITY ? 0.0f : mn;
-        s = s * forge::exp2_fast(m - base) + v.y * forge::exp2_fast(v.x - base);
-        m = mn;
+    part[share][r] = make_float2(m, s);
+    for (int n = kShares / 2; n > 0; n /= 2) {
+        __syncthreads();
+        if (share < n) {
+            const float2 v = part[share + n][r];
+            join(m, s, v.x, v.y);
+            part[share][r] = make_float2(m, s);
+        }
     }
+    if (share != 0 || row >= rows) return;
     const float l = m == -INFINITY && s == 0.0f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(s));
     lse[row] = l;
     const int64_t t = target[row];
@@ -818,9 +837,12 @@ forge_status forge_linear_cross_entropy(const void* X, const void* W, const int6
     FORGE_TRY(set_map(g, 0, Operand{X, s.d_model, s.T, s.d_model}));
     FORGE_TRY(set_map(g, 1, Operand{W, s.d_model, s.vocab, s.d_model}));
     FORGE_TRY(launch<forge::kBlockLossStats>(g, l.plan, stream));
-    return cuda_status(host::launch_early(loss_finish_kernel, dim3(static_cast<unsigned>(ceil_div(s.T, 32))),
-                                          dim3(32 * kFinishWarps), 0, stream, b.stats, l.stat_parts,
-                                          static_cast<int>(s.T), target, s.vocab, s.ignore_index, loss, lse));
+    // 32 rows a block once those fill the GPU with blocks
+    const bool many = s.T >= 32 * mc.dev.num_sms / 4;
+    return cuda_status(host::launch_early(many ? loss_finish_kernel<32> : loss_finish_kernel<1>,
+                                          dim3(static_cast<unsigned>(many ? ceil_div(s.T, 32) : s.T)),
+                                          dim3(kFinishThreads), 0, stream, b.stats, l.stat_parts, static_cast<int>(s.T),
+                                          target, s.vocab, s.ignore_index, loss, lse));
 }
 
 forge_status forge_linear_cross_entropy_backward(const void* X, const void* W, const int64_t* target, const float* lse,

@@ -54,8 +54,15 @@ struct BlockCfg {
     static constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, half the columns each
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
     static constexpr int kStages = 7;
-    static constexpr int kSmemBytes = kStages * kStageBytes + 256 + 1024;  // barriers, alignment slack
+    static constexpr int kRingBytes = kStages * kStageBytes;
+    // where A has few rows (BlockGroup::a_rows) its slices are smaller and the ring holds more stages
+    static constexpr int kMaxStages = CG == 1 ? 13 : kStages;
+    static constexpr int kSmemBytes = kRingBytes + 512 + 1024;  // barriers, alignment slack
     static_assert(kSmemBytes <= 232448, "shared memory");
+    static constexpr int stages(int a_rows) {
+        const int fit = kRingBytes / (a_rows * 128 + kBBytes);
+        return fit < kMaxStages ? fit : kMaxStages;
+    }
 };
 
 struct BlockProblem {
@@ -98,6 +105,12 @@ template <int NP>
 struct BlockGroup {
     int n;
     UnitPlan units;
+    // Rows of A that a stage holds: 128, or on single CTAs with one row of tiles the rows there are, rounded
+    // up to a multiple of 8 (A's tensor maps have boxes of that many rows then).  The MMA reads 128 rows
+    // whatever lies in the rest of the stage: an accumulator row depends on its own row of A alone, and rows
+    // past the output's last are not used.  One token's X or H would otherwise be copied as 64 rows of zero
+    // fill, as many bytes as the weights beside it.
+    int a_rows;
     BlockProblem prob[NP];
     CUtensorMap maps[4 * NP];  // per product: A, B of the first pair, A, B of the second
     float* parts;
@@ -456,6 +469,24 @@ __device__ __forceinline__ void block_epilogue(const BlockProblem& b, const Acc&
 
 // ---------------------------------------------------------------- the kernel
 
+// drain_copies (tile_kernel.cuh) for a ring of `stages` stages.
+template <int CG>
+__device__ __forceinline__ void drain_ring(uint64_t* full, int stages, uint64_t n_own, uint64_t n_peer, int64_t withheld,
+                                           uint32_t stage_bytes, uint64_t limit_ns) {
+    auto last_of = [&](uint64_t n, int s) -> int64_t {
+        return n > static_cast<uint64_t>(s) ? s + stages * static_cast<int64_t>((n - 1 - s) / stages) : -1;
+    };
+    for (int s = 0; s < stages; ++s) {
+        const int64_t lo = last_of(n_own, s), lp = CG == 1 ? lo : last_of(n_peer, s);
+        const int64_t last = lo > lp ? lo : lp;
+        if (last < 0) continue;
+        if (CG == 2 && lo < last) mbar_arrive_expect_tx(&full[s], stage_bytes);
+        if (CG == 2 && lp < last) mbar_complete_tx(&full[s], stage_bytes);
+        if (last == withheld) mbar_complete_tx(&full[s], stage_bytes);
+        drain_bounded(&full[s], static_cast<uint32_t>((last / stages) & 1), limit_ns);
+    }
+}
+
 template <int BN, int CG, int EPI, int NP>
 __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
     forge_block_kernel(const __grid_constant__ BlockGroup<NP> grp) {
@@ -465,11 +496,14 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const int a_rows = CG == 1 ? grp.a_rows : kBM;
+    const int n_stages = CG == 1 ? C::stages(a_rows) : C::kStages;
+    const uint32_t stage_bytes = static_cast<uint32_t>(a_rows) * 128u + C::kBBytes;
     uint8_t* sA = smem;
-    uint8_t* sB = smem + C::kStages * C::kABytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
-    uint64_t* empty = full + C::kStages;
-    uint64_t* acc_full = empty + C::kStages;
+    uint8_t* sB = smem + n_stages * a_rows * 128;  // behind A: the MMA's reads past A's rows stay inside the ring
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRingBytes);
+    uint64_t* empty = full + C::kMaxStages;
+    uint64_t* acc_full = empty + C::kMaxStages;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
     uint64_t* peer_done = drain + 1;
@@ -484,7 +518,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
     const int pairs = static_cast<int>(gridDim.x) / CG;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
+        for (int i = 0; i < n_stages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
@@ -527,6 +561,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
             uint32_t phase = 0;
             bool ok = true;
             const uint64_t keep = policy_evict_last();
+            const uint64_t once = policy_evict_first();
             UnitCursor cur;
             int l = 0;
             for (int u = cur.next(grp.units, pair, pairs); ok && u >= 0; u = cur.next(grp.units, pair, pairs)) {
@@ -535,6 +570,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
                 const BlockProblem& b = grp.prob[l];
                 const bool amn = a_mn(b), bmn = b_mn(b);
                 const int row_a = w.mb * kBM * CG + static_cast<int>(rank) * kBM;
+                // with one row of tiles B passes through once
+                const uint64_t pol_b = b.order.tiles_m == 1 ? once : keep;
                 // gated forward: the even CTA (or the first half of the columns) holds the gate's
                 // rows, the other the up projection's, of the same d_ff columns
                 const int col_b = kGated ? w.nb * kColsPerTile : w.nb * BN + static_cast<int>(rank) * C::kBLoad;
@@ -542,7 +579,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
                     if (!wait_bounded(&empty[stage], phase ^ 1u, ab)) { ok = false; break; }
                     uint32_t bar = smem_addr(&full[stage]);
                     if constexpr (CG == 2) bar = map_to_rank(bar, 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * C::kStageBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * stage_bytes);
                     if (grp.withhold_first_stage && rank == 0 && n_issued == 0) {
                         withheld = static_cast<int64_t>(n_issued);
                     } else {
@@ -550,12 +587,13 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
                         const int k0 = (kb - (second ? b.kb[0] : 0)) * kBK;
                         const CUtensorMap* ma = &grp.maps[4 * l + 2 * second];
                         const CUtensorMap* mb = ma + 1;
-                        uint8_t* a_dst = sA + stage * C::kABytes;
+                        uint8_t* a_dst = sA + stage * (a_rows * 128);
                         uint8_t* b_dst = sB + stage * C::kBBytes;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const int r = row_a + 64 * j;
-                            tma_load_2d_cg<CG>(a_dst + j * kBK * 128, ma, bar, amn ? r : k0, amn ? k0 : r, keep);
+                            if (64 * j < a_rows)
+                                tma_load_2d_cg<CG>(a_dst + j * kBK * 128, ma, bar, amn ? r : k0, amn ? k0 : r, keep);
                         }
                         if constexpr (kGated) {
                             // maps: A = X, B = Wg; the second pair's B is Wu
@@ -564,18 +602,18 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
                             for (int j = 0; j < C::kBLoad / 64; ++j) {
                                 const bool up = CG == 2 ? rank == 1 : j >= C::kBLoad / 128;
                                 const int r = col_b + 64 * (CG == 2 ? j : j % (C::kBLoad / 128));
-                                tma_load_2d_cg<CG>(b_dst + j * kBK * 128, up ? mu : mb, bar, k0, r, keep);
+                                tma_load_2d_cg<CG>(b_dst + j * kBK * 128, up ? mu : mb, bar, k0, r, pol_b);
                             }
                         } else {
 #pragma unroll
                             for (int j = 0; j < C::kBLoad / 64; ++j) {
                                 const int r = col_b + 64 * j;
-                                tma_load_2d_cg<CG>(b_dst + j * kBK * 128, mb, bar, bmn ? r : k0, bmn ? k0 : r, keep);
+                                tma_load_2d_cg<CG>(b_dst + j * kBK * 128, mb, bar, bmn ? r : k0, bmn ? k0 : r, pol_b);
                             }
                         }
                     }
                     ++n_issued;
-                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                    if (++stage == n_stages) { stage = 0; phase ^= 1u; }
                 }
             }
             if constexpr (CG == 2) {
@@ -608,7 +646,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
                 for (int kb = w.k_first; kb < w.k_end; ++kb) {
                     if (!wait_bounded(&full[stage], phase, ab)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a_base = smem_addr(sA + stage * C::kABytes);
+                    const uint32_t a_base = smem_addr(sA + stage * (a_rows * 128));
                     const uint32_t b_base = smem_addr(sB + stage * C::kBBytes);
 #pragma unroll
                     for (int kk = 0; kk < kBK / kUmmaK; ++kk) {
@@ -618,7 +656,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
                     }
                     issued_any = true;
                     tc_commit_mask<CG>(&empty[stage], 0x3u);
-                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                    if (++stage == n_stages) { stage = 0; phase ^= 1u; }
                 }
                 if (!ok) break;
                 tc_commit_mask<CG>(&acc_full[acc], 0x3u);
@@ -710,11 +748,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
             while (!counted && global_timer_ns() - t0 <= 4 * grp.wait_limit_ns) counted = mbar_try_wait_cluster(peer_done, 0);
             if (counted) n_peer = ld_shared_volatile_u64(peer_count);
         }
-        if (counted) {
-            drain_copies<C::kStages, CG>(full, n_issued, n_peer, withheld, C::kStageBytes, grp.wait_limit_ns);
-        } else {
-            drain_copies<C::kStages, 1>(full, n_issued, n_issued, withheld, C::kStageBytes, grp.wait_limit_ns);
-        }
+        if (counted) drain_ring<CG>(full, n_stages, n_issued, n_peer, withheld, stage_bytes, grp.wait_limit_ns);
+        else drain_ring<1>(full, n_stages, n_issued, n_issued, withheld, stage_bytes, grp.wait_limit_ns);
     }
     if constexpr (CG > 1) cluster_sync();
     if (warp == 1) {

@@ -21,8 +21,8 @@ struct Device {
 forge_status device(Device* out);
 
 // Tensor map of a row-major bfloat16 operand [rows, cols] whose rows start `ld` elements apart, read
-// in boxes of 64 x 64 with the 128-byte swizzle.
-forge_status operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld);
+// in boxes of 64 columns x `box_rows` rows with the 128-byte swizzle.
+forge_status operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
 
 uint64_t wait_limit_ns();
 uint64_t acc_wait_limit_ns(int64_t k_blocks);
