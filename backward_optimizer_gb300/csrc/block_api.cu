@@ -64,7 +64,7 @@ struct Cut {
 };
 
 struct Plan {
-    bool pair;
+    int bn;      // tile columns: 256 on CTA pairs, 128 or 64 on single CTAs
     int width;   // pairs or CTAs
     int a_rows;  // rows of A per stage (BlockGroup::a_rows)
     int n;
@@ -80,25 +80,31 @@ constexpr int kMaxParts = 16;
 // the epilogue of a tile, in slices of the mainloop: only to weigh units against one another
 constexpr int kEpiSlices = 8;
 
-void plan_products(Plan& p, const Machine& mc, bool gated, bool a_k_major) {
-    // Pairs on 256 x 256 tiles move half the operand bytes per product of single CTAs on 128 x 128
-    // tiles, so they are taken unless they would leave half of the SMs idle, or every tile's second
-    // 128 rows empty.
-    auto tiles_of = [&](const Cut& c, bool pair) {
-        const int64_t tm = pair ? 256 : 128, tn = (pair ? 256 : 128) / (gated ? 2 : 1);
-        return ceil_div(c.rows, tm) * ceil_div(c.cols, tn);
+// Tile shape.  Pairs on 256 x 256 tiles move half the operand bytes per product of single CTAs on
+// 128 x 128 tiles, so they are taken unless they would leave half of the SMs idle, or every tile's second
+// 128 rows empty.  Single CTAs take 128 x 64 tiles where 128 x 128 would leave half of the SMs idle, but
+// not where all rows fit one tile: there the time is the weights' way from memory, and the smaller copies
+// keep less of it in flight (one token, 4096/14336: 102 us on 128 x 64 tiles against 78).
+int pick_width(const Plan& p, const Machine& mc, bool gated) {
+    auto tiles_of = [&](int bn) {
+        const int64_t tm = bn == 256 ? 256 : 128, tn = bn / (gated ? 2 : 1);
+        int64_t n = 0;
+        for (int i = 0; i < p.n; ++i) n += ceil_div(p.cut[i].rows, tm) * ceil_div(p.cut[i].cols, tn);
+        return n;
     };
-    int64_t pair_tiles = 0;
     bool tall = false;
-    for (int i = 0; i < p.n; ++i) {
-        pair_tiles += tiles_of(p.cut[i], true);
-        tall = tall || p.cut[i].rows > 128;
-    }
-    p.pair = tall && 2 * pair_tiles > mc.pairs;
-    p.width = p.pair ? mc.pairs : mc.dev.num_sms;
+    for (int i = 0; i < p.n; ++i) tall = tall || p.cut[i].rows > 128;
+    if (tall && 2 * tiles_of(256) > mc.pairs) return 256;
+    return tall && 2 * tiles_of(128) <= mc.dev.num_sms ? 64 : 128;
+}
+
+void plan_products(Plan& p, const Machine& mc, bool gated, bool a_k_major) {
+    p.bn = pick_width(p, mc, gated);
+    const bool pair = p.bn == 256;
+    p.width = pair ? mc.pairs : mc.dev.num_sms;
     p.a_rows = 128;
-    if (p.n == 1 && !p.pair && a_k_major && p.cut[0].rows <= 64) p.a_rows = static_cast<int>(round_up(p.cut[0].rows, 8));
-    const int64_t tm = p.pair ? 256 : 128, tn = (p.pair ? 256 : 128) / (gated ? 2 : 1);
+    if (p.n == 1 && !pair && a_k_major && p.cut[0].rows <= 64) p.a_rows = static_cast<int>(round_up(p.cut[0].rows, 8));
+    const int64_t tm = pair ? 256 : 128, tn = p.bn / (gated ? 2 : 1);
     int64_t tiles = 0;
     double work = 0;
     for (int i = 0; i < p.n; ++i) {
@@ -110,8 +116,20 @@ void plan_products(Plan& p, const Machine& mc, bool gated, bool a_k_major) {
         tiles += c.split_from;
         work += static_cast<double>(c.split_from) * (c.kb + kEpiSlices);
     }
-    if (tiles < p.width) {
-        // fewer tiles than pairs: the longest units are cut further while all still run at once
+    if (p.n == 1 && tiles < p.width) {
+        // fewer tiles than pairs: cut each so that the units' waves are shortest
+        Cut& c = p.cut[0];
+        int64_t best = c.kb + kEpiSlices;
+        for (int parts = 2; parts <= kMaxParts && c.kb >= kMinSlices * parts; ++parts) {
+            const int64_t t = ceil_div(tiles * parts, p.width) * (ceil_div(c.kb, parts) + kEpiSlices);
+            if (t < best) {
+                best = t;
+                c.parts = parts;
+                c.split_from = 0;
+            }
+        }
+    } else if (tiles < p.width) {
+        // the longest units are cut further while all still run at once
         int64_t units = tiles;
         for (;;) {
             int best = -1;
@@ -156,13 +174,13 @@ void plan_products(Plan& p, const Machine& mc, bool gated, bool a_k_major) {
     }
     p.part_floats = 0;
     p.counts = 0;
-    const int cg = p.pair ? 2 : 1;
+    const int cg = pair ? 2 : 1;
     for (int i = 0; i < p.n; ++i) {
         Cut& c = p.cut[i];
         const int split = c.parts > 1 ? c.tiles_m * c.tiles_n - c.split_from : 0;
         c.part_base = p.part_floats;
         c.count_base = p.counts;
-        p.part_floats += static_cast<int64_t>(split) * c.parts * (cg == 2 ? 256 * 256 : 128 * 128);
+        p.part_floats += static_cast<int64_t>(split) * c.parts * tm * p.bn;
         p.counts += split * cg * 8;
     }
 }
@@ -189,13 +207,21 @@ struct Arena {
     }
 };
 
-// The split tiles' regions of one launch: FP32 parts, and counters that have to be zero before it.
+// The split tiles' regions that the launches of a call share, each big enough for any of them: FP32
+// parts, and arrival counters, which are zero between launches once the call has cleared them.
 struct SplitSpace {
-    int64_t parts, counts, count_bytes;
+    int64_t parts, counts;
+    int n_counts;
 };
 
-SplitSpace take_split(Arena& a, const Plan& p) {
-    return SplitSpace{a.take(p.part_floats * 4), a.take(p.counts * 4ll), p.counts * 4ll};
+SplitSpace take_split(Arena& a, std::initializer_list<const Plan*> plans) {
+    int64_t floats = 0;
+    int counts = 0;
+    for (const Plan* p : plans) {
+        floats = std::max(floats, p->part_floats);
+        counts = std::max(counts, p->counts);
+    }
+    return SplitSpace{a.take(floats * 4), a.take(counts * 4ll), counts};
 }
 
 struct Operand {
@@ -253,16 +279,60 @@ forge_status fill_group(BlockGroup<NP>& g, const Plan& p, const Machine& mc, cha
     return FORGE_OK;
 }
 
+// Encoded tensor maps of recent calls, per host thread, as forge_api.cu keeps them for the weight-gradient
+// kernels: a map is plain host data determined by its key.
+struct MapKey {
+    const void* base;
+    int64_t cols, rows, ld;
+    int mn, extent;
+    bool operator==(const MapKey& o) const {
+        return base == o.base && cols == o.cols && rows == o.rows && ld == o.ld && mn == o.mn && extent == o.extent;
+    }
+};
+struct MapSlot {
+    MapKey key;
+    CUtensorMap map;
+    bool used;
+};
+constexpr int kMapSlots = 128;
+thread_local MapSlot t_maps[kMapSlots];
+
+// The map of an operand of which a CTA stages `extent` rows (K-major) or columns (MN-major) per slice, one
+// box a slice; or two boxes of 64 columns where the operand's width is no multiple of 64 (flat).
+forge_status operand_map(CUtensorMap* map, const Operand& o, bool mn, int extent) {
+    const MapKey key{o.base, o.cols, o.rows, o.ld, mn, extent};
+    uint64_t h = reinterpret_cast<uintptr_t>(o.base) * 0x9E3779B97F4A7C15ull;
+    h ^= static_cast<uint64_t>(o.cols) * 0xC2B2AE3D27D4EB4Full ^ static_cast<uint64_t>(o.rows) * 0x165667B19E3779F9ull;
+    h ^= static_cast<uint64_t>(o.ld * 1024 + extent * 2 + mn) * 0x85EBCA77C2B2AE63ull;
+    MapSlot& slot = t_maps[(h >> 32) % kMapSlots];
+    if (slot.used && slot.key == key) {
+        *map = slot.map;
+        return FORGE_OK;
+    }
+    const uint64_t cols = static_cast<uint64_t>(o.cols), rows = static_cast<uint64_t>(o.rows);
+    const uint64_t pitch = static_cast<uint64_t>(o.ld) * 2;
+    forge_status st;
+    if (mn && o.cols % 64 == 0)
+        st = host::encode_map(map, o.base, {64, rows, cols / 64}, {pitch, 128}, {64, 64, static_cast<uint32_t>(extent / 64)});
+    else
+        st = host::encode_map(map, o.base, {cols, rows, 1}, {pitch, pitch}, {64, mn ? 64u : static_cast<uint32_t>(extent), 1});
+    if (st == FORGE_OK) slot = MapSlot{key, *map, true};
+    return st;
+}
+
+// Map i of product l of a group (BlockGroup::maps).
 template <int NP>
-forge_status set_map(BlockGroup<NP>& g, int i, const Operand& o) {
-    const bool is_a = i % 2 == 0;
-    return host::operand_map(&g.maps[i], o.base, o.cols, o.rows, o.ld, is_a ? std::min(g.a_rows, 64) : 64);
+forge_status set_map(BlockGroup<NP>& g, const Plan& p, int l, int i, const Operand& o, bool mn, bool gated = false) {
+    const int extent = i % 2 == 0 ? p.a_rows : p.bn == 256 ? 128 : gated ? p.bn / 2 : p.bn;
+    int& flat = i % 2 == 0 ? g.prob[l].a_flat : g.prob[l].b_flat;
+    flat = flat || (mn && o.cols % 64 != 0);
+    return operand_map(&g.maps[4 * l + i], o, mn, extent);
 }
 
 template <int EPI, int NP>
 forge_status launch(const BlockGroup<NP>& g, const Plan& p, cudaStream_t stream) {
     host::count_launch();
-    return cuda_status(forge::launch_block<EPI>(&g, p.pair, std::min(p.width, g.units.n_units), stream));
+    return cuda_status(forge::launch_block<EPI>(&g, p.bn, std::min(p.width, g.units.n_units), stream));
 }
 
 #define FORGE_TRY(expr)                      \
@@ -310,8 +380,8 @@ forge_status run_store(const Machine& mc, const Plan& p, const Product* pr, char
         for (int s = 0; s < 2; ++s) {
             b.kb[s] = slices(pr[i].k[s]);
             if (b.kb[s] == 0) continue;
-            FORGE_TRY(set_map(g, 4 * i + 2 * s, pr[i].a[s]));
-            FORGE_TRY(set_map(g, 4 * i + 2 * s + 1, pr[i].b[s]));
+            FORGE_TRY(set_map(g, p, i, 2 * s, pr[i].a[s], pr[i].a_mn != 0));
+            FORGE_TRY(set_map(g, p, i, 2 * s + 1, pr[i].b[s], pr[i].b_mn != 0));
         }
         b.a_mn = pr[i].a_mn;
         b.b_mn = pr[i].b_mn;
@@ -326,8 +396,23 @@ forge_status run_store(const Machine& mc, const Plan& p, const Product* pr, char
     return launch<forge::kBlockStore>(g, p, stream);
 }
 
-forge_status zero_counts(char* ws, const SplitSpace& sp, cudaStream_t stream) {
-    return sp.count_bytes == 0 ? FORGE_OK : cuda_status(cudaMemsetAsync(ws + sp.counts, 0, sp.count_bytes, stream));
+__global__ void __launch_bounds__(256) zero_counts_kernel(uint32_t* counts, int n) {
+    forge::stream_release();
+    forge::stream_wait();
+    for (int i = threadIdx.x; i < n; i += 256) counts[i] = 0u;
+}
+
+// Clears the call's counters: the first launch does it for those behind it unless it needs them itself.
+template <int NP>
+forge_status clear_counts(BlockGroup<NP>& first, const Plan& p, char* ws, const SplitSpace& sp, cudaStream_t stream) {
+    if (sp.n_counts == 0) return FORGE_OK;
+    uint32_t* at = reinterpret_cast<uint32_t*>(ws + sp.counts);
+    if (p.counts == 0) {
+        first.zero_at = at;
+        first.zero_n = sp.n_counts;
+        return FORGE_OK;
+    }
+    return cuda_status(host::launch_early(zero_counts_kernel, dim3(1), dim3(256), 0, stream, at, sp.n_counts));
 }
 
 // y [rows, n] = a [rows, k] w [n, k]^T (+ add)
@@ -404,7 +489,7 @@ struct GatedForward {
     Plan up, down;
     Product y;
     int64_t h, bytes;
-    SplitSpace up_split, down_split;
+    SplitSpace split;
 };
 
 GatedForward layout_gated_forward(const Machine& mc, const forge_gated_shape& s) {
@@ -413,10 +498,7 @@ GatedForward layout_gated_forward(const Machine& mc, const forge_gated_shape& s)
     l.up = plan_one(mc, s.T, s.d_ff, slices(s.d_model), true);
     l.y = product_nt(nullptr, nullptr, s.T, s.d_model, s.d_ff, nullptr, nullptr);
     l.down = plan_store(mc, &l.y, 1);
-    // both launches' counters first, so that one memset clears them
-    const int64_t counts = a.take((l.up.counts + l.down.counts) * 4ll);
-    l.up_split = SplitSpace{a.take(l.up.part_floats * 4), counts, (l.up.counts + l.down.counts) * 4ll};
-    l.down_split = SplitSpace{a.take(l.down.part_floats * 4), counts + l.up.counts * 4ll, 0};
+    l.split = take_split(a, {&l.up, &l.down});
     l.h = a.take(s.T * s.d_ff * 2);
     l.bytes = a.used;
     return l;
@@ -427,7 +509,7 @@ struct GatedBackward {
     Product pr[4];
     int n;
     int64_t dg, du, h, bytes;
-    SplitSpace dh_split, grads_split;
+    SplitSpace split;
 };
 
 // dw: the weights' gradients are wanted (else the fused step makes them its own way)
@@ -455,19 +537,17 @@ GatedBackward layout_gated_backward(const Machine& mc, const forge_gated_shape& 
     }
     l.grads = Plan{};
     if (l.n > 0) l.grads = plan_store(mc, l.pr, l.n);
-    const int64_t counts = a.take((l.dh.counts + l.grads.counts) * 4ll);
-    l.dh_split = SplitSpace{a.take(l.dh.part_floats * 4), counts, (l.dh.counts + l.grads.counts) * 4ll};
-    l.grads_split = SplitSpace{a.take(l.grads.part_floats * 4), counts + l.dh.counts * 4ll, 0};
+    l.split = take_split(a, {&l.dh, &l.grads});
     l.bytes = a.used;
     return l;
 }
 
 forge_status run_gated_dh(const Machine& mc, const GatedBackward& l, const void* dY, const void* Wd, const void* G,
                           const void* U, char* ws, const forge_gated_shape& s, cudaStream_t stream) {
-    FORGE_TRY(zero_counts(ws, l.dh_split, stream));
     BlockGroup<1> g;
     std::memset(&g, 0, sizeof(g));
-    FORGE_TRY(fill_group(g, l.dh, mc, ws, l.dh_split));
+    FORGE_TRY(fill_group(g, l.dh, mc, ws, l.split));
+    FORGE_TRY(clear_counts(g, l.dh, ws, l.split, stream));
     BlockProblem& b = g.prob[0];
     b.kb[0] = slices(s.d_model);
     b.ld = s.d_ff;
@@ -477,8 +557,8 @@ forge_status run_gated_dh(const Machine& mc, const GatedBackward& l, const void*
     b.u_out = reinterpret_cast<uint16_t*>(ws + l.du);
     b.h_out = reinterpret_cast<uint16_t*>(ws + l.h);
     b.act = s.act;
-    FORGE_TRY(set_map(g, 0, Operand{dY, s.d_model, s.T, s.d_model}));
-    FORGE_TRY(set_map(g, 1, Operand{Wd, s.d_ff, s.d_model, s.d_ff}));
+    FORGE_TRY(set_map(g, l.dh, 0, 0, Operand{dY, s.d_model, s.T, s.d_model}, false));
+    FORGE_TRY(set_map(g, l.dh, 0, 1, Operand{Wd, s.d_ff, s.d_model, s.d_ff}, true));
     return launch<forge::kBlockGatedBwd>(g, l.dh, stream);
 }
 
@@ -506,7 +586,7 @@ LossForward layout_loss_forward(const Machine& mc, const forge_loss_shape& s) {
     LossForward l;
     Arena a;
     l.plan = plan_one(mc, s.T, s.vocab, slices(s.d_model));
-    l.split = take_split(a, l.plan);
+    l.split = take_split(a, {&l.plan});
     l.stat_parts = 2 * l.plan.cut[0].tiles_n;
     l.stats = a.take(static_cast<int64_t>(l.stat_parts) * s.T * 8);
     l.bytes = a.used;
@@ -517,14 +597,14 @@ LossForward layout_loss_forward(const Machine& mc, const forge_loss_shape& s) {
 // 256 MiB unless T alone asks for more than 2048 entries' worth.
 int64_t loss_piece(const forge_loss_shape& s) {
     const int64_t fit = (256ll << 20) / (2 * std::max<int64_t>(s.T, 1)) / 256 * 256;
-    return std::min(round_up(s.vocab, 8), std::max<int64_t>(fit, 2048));
+    return std::min(round_up(s.vocab, 64), std::max<int64_t>(fit, 2048));
 }
 
 struct LossBackward {
     int64_t piece, pieces;
     int64_t g, sum, unit, bytes;
     bool scaled;       // g is kept relative to the largest dloss
-    SplitSpace split;  // the largest that any piece's launch takes
+    SplitSpace split;
 };
 
 struct LossPiece {
@@ -539,7 +619,7 @@ LossPiece loss_piece_of(const Machine& mc, const forge_loss_shape& s, const Loss
     LossPiece p{};
     p.v0 = i * l.piece;
     p.n = std::min(l.piece, s.vocab - p.v0);
-    p.ld = round_up(p.n, 8);
+    p.ld = round_up(p.n, 64);  // whole blocks of 64 columns for the copies of dW's operand
     p.grad = plan_one(mc, s.T, p.n, slices(s.d_model));
     const size_t row = static_cast<size_t>(p.v0) * s.d_model * 2;
     if (dx) {
@@ -549,7 +629,11 @@ LossPiece loss_piece_of(const Machine& mc, const forge_loss_shape& s, const Loss
         x.sum_out = i + 1 < l.pieces;
         p.pr[p.np++] = x;
     }
-    if (dw) p.pr[p.np++] = product_dw(ws + l.g, p.ld, X, s.T, p.n, s.d_model, static_cast<char*>(dW) + row);
+    if (dw) {
+        Product w = product_dw(ws + l.g, p.ld, X, s.T, p.n, s.d_model, static_cast<char*>(dW) + row);
+        w.a[0].cols = p.ld;  // g's padding is finite and ends in rows of dW that are not stored
+        p.pr[p.np++] = w;
+    }
     if (l.scaled)
         for (int j = 0; j < p.np; ++j) p.pr[j].unit = reinterpret_cast<const float*>(ws + l.unit);
     if (p.np > 0) p.out = plan_store(mc, p.pr, p.np);
@@ -564,16 +648,12 @@ LossBackward layout_loss_backward(const Machine& mc, const forge_loss_shape& s, 
     l.unit = a.take(4);
     l.piece = loss_piece(s);
     l.pieces = ceil_div(s.vocab, l.piece);
-    l.g = a.take(s.T * round_up(std::min(l.piece, s.vocab), 8) * 2);
+    l.g = a.take(s.T * l.piece * 2);
     l.sum = a.take(dx && l.pieces > 1 ? s.T * s.d_model * 4 : 0);
     // pieces are alike but for the last one
-    int64_t floats = 0, counts = 0;
-    for (int64_t i : {int64_t{0}, l.pieces - 1}) {
-        const LossPiece p = loss_piece_of(mc, s, l, i, nullptr, nullptr, nullptr, nullptr, dx, dw, nullptr);
-        floats = std::max({floats, p.grad.part_floats, p.out.part_floats});
-        counts = std::max<int64_t>(counts, p.grad.counts + p.out.counts);
-    }
-    l.split = SplitSpace{a.take(floats * 4), a.take(counts * 4), 0};
+    const LossPiece p = loss_piece_of(mc, s, l, 0, nullptr, nullptr, nullptr, nullptr, dx, dw, nullptr);
+    const LossPiece q = loss_piece_of(mc, s, l, l.pieces - 1, nullptr, nullptr, nullptr, nullptr, dx, dw, nullptr);
+    l.split = take_split(a, {&p.grad, &p.out, &q.grad, &q.out});
     l.bytes = a.used;
     return l;
 }
@@ -582,12 +662,9 @@ LossBackward layout_loss_backward(const Machine& mc, const forge_loss_shape& s, 
 forge_status run_loss_grad(const Machine& mc, const LossBackward& l, const LossPiece& p, const forge_loss_shape& s,
                            const void* X, const void* W, const int64_t* target, const float* lse, const float* dloss,
                            char* ws, cudaStream_t stream) {
-    SplitSpace sp = l.split;
-    sp.count_bytes = (p.grad.counts + p.out.counts) * 4ll;
-    FORGE_TRY(zero_counts(ws, sp, stream));
     BlockGroup<1> g;
     std::memset(&g, 0, sizeof(g));
-    FORGE_TRY(fill_group(g, p.grad, mc, ws, sp));
+    FORGE_TRY(fill_group(g, p.grad, mc, ws, l.split));
     BlockProblem& b = g.prob[0];
     b.kb[0] = slices(s.d_model);
     b.out = reinterpret_cast<uint16_t*>(ws + l.g);
@@ -599,23 +676,21 @@ forge_status run_loss_grad(const Machine& mc, const LossBackward& l, const LossP
     b.lse = lse;
     b.dloss = dloss;
     b.unit = l.scaled ? reinterpret_cast<const float*>(ws + l.unit) : nullptr;
-    FORGE_TRY(set_map(g, 0, Operand{X, s.d_model, s.T, s.d_model}));
-    FORGE_TRY(set_map(g, 1, Operand{static_cast<const char*>(W) + static_cast<size_t>(p.v0) * s.d_model * 2, s.d_model,
-                                    p.n, s.d_model}));
+    FORGE_TRY(set_map(g, p.grad, 0, 0, Operand{X, s.d_model, s.T, s.d_model}, false));
+    FORGE_TRY(set_map(g, p.grad, 0, 1, Operand{static_cast<const char*>(W) + static_cast<size_t>(p.v0) * s.d_model * 2,
+                                            s.d_model, p.n, s.d_model}, false));
     return launch<forge::kBlockLossGrad>(g, p.grad, stream);
 }
 
 forge_status run_loss_products(const Machine& mc, const LossBackward& l, const LossPiece& p, char* ws,
                                cudaStream_t stream) {
     if (p.np == 0) return FORGE_OK;
-    SplitSpace sp = l.split;
-    sp.counts += p.grad.counts * 4ll;
-    return run_store(mc, p.out, p.pr, ws, sp, stream);
+    return run_store(mc, p.out, p.pr, ws, l.split, stream);
 }
 
 // Joins the tiles' maxima and sums of one row: lse, and the loss of the target's logit that one tile's
 // epilogue left in `loss`.  A block takes kRows rows (32 with many rows, so that loads of a part are
-// whole lines; 1 with few, so that all threads share the row's parts); its other threads share the parts.
+// whole lines; fewer with few rows, so that more blocks and threads share the parts).
 constexpr int kFinishThreads = 512;
 
 __device__ __forceinline__ void join(float& m, float& s, float vm, float vs) {
@@ -663,12 +738,15 @@ __global__ void __launch_bounds__(kFinishThreads)
     loss[row] = t == ignore ? 0.0f : t >= 0 && t < vocab ? l - loss[row] : NAN;
 }
 
-// The largest |dloss| of the tokens that count, or 1 where there is none above 0: one block.
+// The largest |dloss| of the tokens that count, or 1 where there is none above 0; and the counters of the
+// call's split tiles cleared: one block.
 __global__ void __launch_bounds__(1024)
-    loss_unit_kernel(const float* dloss, const int64_t* target, int64_t ignore, int rows, float* unit) {
+    loss_begin_kernel(const float* dloss, const int64_t* target, int64_t ignore, int rows, float* unit, uint32_t* counts,
+                      int n_counts) {
     __shared__ float part[32];
     forge::stream_release();
     forge::stream_wait();
+    for (int i = threadIdx.x; i < n_counts; i += 1024) counts[i] = 0u;
     float m = 0.0f;
     for (int i = threadIdx.x; i < rows; i += 1024) m = fmaxf(m, target[i] == ignore ? 0.0f : fabsf(dloss[i]));
 #pragma unroll
@@ -680,6 +758,13 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     if (threadIdx.x == 0) *unit = m > 0.0f ? m : 1.0f;
+}
+
+forge_status run_loss_begin(const LossBackward& l, const forge_loss_shape& s, const int64_t* target, const float* dloss,
+                            char* ws, cudaStream_t stream) {
+    return cuda_status(host::launch_early(loss_begin_kernel, dim3(1), dim3(1024), 0, stream, dloss, target,
+                                          s.ignore_index, static_cast<int>(s.T), reinterpret_cast<float*>(ws + l.unit),
+                                          reinterpret_cast<uint32_t*>(ws + l.split.counts), l.split.n_counts));
 }
 
 }  // namespace
@@ -714,10 +799,10 @@ forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, cons
     GatedForward l = layout_gated_forward(mc, s);
     FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     char* ws = static_cast<char*>(workspace);
-    FORGE_TRY(zero_counts(ws, l.up_split, stream));
     BlockGroup<1> g;
     std::memset(&g, 0, sizeof(g));
-    FORGE_TRY(fill_group(g, l.up, mc, ws, l.up_split));
+    FORGE_TRY(fill_group(g, l.up, mc, ws, l.split));
+    FORGE_TRY(clear_counts(g, l.up, ws, l.split, stream));
     BlockProblem& b = g.prob[0];
     b.kb[0] = slices(s.d_model);
     b.ld = s.d_ff;
@@ -725,12 +810,12 @@ forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, cons
     b.u_out = static_cast<uint16_t*>(U);
     b.h_out = reinterpret_cast<uint16_t*>(ws + l.h);
     b.act = s.act;
-    FORGE_TRY(set_map(g, 0, Operand{X, s.d_model, s.T, s.d_model}));
-    FORGE_TRY(set_map(g, 1, Operand{Wg, s.d_model, s.d_ff, s.d_model}));
-    FORGE_TRY(set_map(g, 3, Operand{Wu, s.d_model, s.d_ff, s.d_model}));
+    FORGE_TRY(set_map(g, l.up, 0, 0, Operand{X, s.d_model, s.T, s.d_model}, false));
+    FORGE_TRY(set_map(g, l.up, 0, 1, Operand{Wg, s.d_model, s.d_ff, s.d_model}, false, true));
+    FORGE_TRY(set_map(g, l.up, 0, 3, Operand{Wu, s.d_model, s.d_ff, s.d_model}, false, true));
     FORGE_TRY(launch<forge::kBlockGatedFwd>(g, l.up, stream));
     const Product y = product_nt(ws + l.h, Wd, s.T, s.d_model, s.d_ff, Y, residual);
-    return run_store(mc, l.down, &y, ws, l.down_split, stream);
+    return run_store(mc, l.down, &y, ws, l.split, stream);
 }
 
 forge_status forge_gated_mlp_backward(const void* dY, const void* X, const void* G, const void* U, const void* Wg,
@@ -754,7 +839,7 @@ forge_status forge_gated_mlp_backward(const void* dY, const void* X, const void*
     const GatedBackward l = layout_gated_backward(mc, s, dY, X, Wg, Wu, dX, dWg, dWu, dWd, true, dX != nullptr, ws);
     FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     FORGE_TRY(run_gated_dh(mc, l, dY, Wd, G, U, ws, s, stream));
-    return run_store(mc, l.grads, l.pr, ws, l.grads_split, stream);
+    return run_store(mc, l.grads, l.pr, ws, l.split, stream);
 }
 
 forge_status forge_gated_mlp_backward_step(const void* dY, const void* X, const void* G, const void* U,
@@ -788,7 +873,7 @@ forge_status forge_gated_mlp_backward_step(const void* dY, const void* X, const 
         FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
         // the input gradients read the weights before the fused step replaces them: same stream, this order
         FORGE_TRY(run_gated_dh(mc, l, dY, down->W, G, U, ws, s, stream));
-        if (dX != nullptr) FORGE_TRY(run_store(mc, l.grads, l.pr, ws, l.grads_split, stream));
+        if (dX != nullptr) FORGE_TRY(run_store(mc, l.grads, l.pr, ws, l.split, stream));
         layers[0].dY = ws + l.dg;
         layers[1].dY = ws + l.du;
         layers[2].dY = dY;
@@ -823,10 +908,10 @@ forge_status forge_linear_cross_entropy(const void* X, const void* W, const int6
     const LossForward l = layout_loss_forward(mc, s);
     FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     char* ws = static_cast<char*>(workspace);
-    FORGE_TRY(zero_counts(ws, l.split, stream));
     BlockGroup<1> g;
     std::memset(&g, 0, sizeof(g));
     FORGE_TRY(fill_group(g, l.plan, mc, ws, l.split));
+    FORGE_TRY(clear_counts(g, l.plan, ws, l.split, stream));
     BlockProblem& b = g.prob[0];
     b.kb[0] = slices(s.d_model);
     b.target = target;
@@ -834,13 +919,15 @@ forge_status forge_linear_cross_entropy(const void* X, const void* W, const int6
     b.ignore = s.ignore_index;
     b.stats = reinterpret_cast<float2*>(ws + l.stats);
     b.target_logit = loss;
-    FORGE_TRY(set_map(g, 0, Operand{X, s.d_model, s.T, s.d_model}));
-    FORGE_TRY(set_map(g, 1, Operand{W, s.d_model, s.vocab, s.d_model}));
+    FORGE_TRY(set_map(g, l.plan, 0, 0, Operand{X, s.d_model, s.T, s.d_model}, false));
+    FORGE_TRY(set_map(g, l.plan, 0, 1, Operand{W, s.d_model, s.vocab, s.d_model}, false));
     FORGE_TRY(launch<forge::kBlockLossStats>(g, l.plan, stream));
-    // 32 rows a block once those fill the GPU with blocks
-    const bool many = s.T >= 32 * mc.dev.num_sms / 4;
-    return cuda_status(host::launch_early(many ? loss_finish_kernel<32> : loss_finish_kernel<1>,
-                                          dim3(static_cast<unsigned>(many ? ceil_div(s.T, 32) : s.T)),
+    // as many rows a block as still give half of the SMs a block
+    const int rows = s.T >= 16 * mc.dev.num_sms ? 32 : s.T >= 4 * mc.dev.num_sms ? 8 : 1;
+    return cuda_status(host::launch_early(rows == 32  ? loss_finish_kernel<32>
+                                          : rows == 8 ? loss_finish_kernel<8>
+                                                      : loss_finish_kernel<1>,
+                                          dim3(static_cast<unsigned>(ceil_div(s.T, rows))),
                                           dim3(kFinishThreads), 0, stream, b.stats, l.stat_parts, static_cast<int>(s.T),
                                           target, s.vocab, s.ignore_index, loss, lse));
 }
@@ -867,9 +954,7 @@ forge_status forge_linear_cross_entropy_backward(const void* X, const void* W, c
     const LossBackward l = layout_loss_backward(mc, s, dx, dw, false);
     FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     char* ws = static_cast<char*>(workspace);
-    FORGE_TRY(cuda_status(host::launch_early(loss_unit_kernel, dim3(1), dim3(1024), 0, stream, dloss, target,
-                                             s.ignore_index, static_cast<int>(s.T),
-                                             reinterpret_cast<float*>(ws + l.unit))));
+    FORGE_TRY(run_loss_begin(l, s, target, dloss, ws, stream));
     for (int64_t i = 0; i < l.pieces; ++i) {
         const LossPiece p = loss_piece_of(mc, s, l, i, X, W, dX, dW, dx, dw, ws);
         FORGE_TRY(run_loss_grad(mc, l, p, s, X, W, target, lse, dloss, ws, stream));
@@ -902,6 +987,7 @@ forge_status forge_linear_cross_entropy_step(const void* X, void* W, const int64
     const LossBackward l = layout_loss_backward(mc, s, dx, false, true);
     FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     char* ws = static_cast<char*>(workspace);
+    FORGE_TRY(run_loss_begin(l, s, target, dloss, ws, stream));
     for (int64_t i = 0; i < l.pieces; ++i) {
         const LossPiece p = loss_piece_of(mc, s, l, i, X, W, dX, nullptr, dx, false, ws);
         // logits and dX read the piece's rows before the fused step replaces them

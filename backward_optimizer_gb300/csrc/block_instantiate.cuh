@@ -48,8 +48,9 @@ cudaError_t launch_block_as(const void* group, int units, cudaStream_t stream) {
 }
 
 template <int EPI>
-cudaError_t launch_block(const void* group, bool pair, int units, cudaStream_t stream) {
-    return pair ? launch_block_as<256, 2, EPI>(group, units, stream) : launch_block_as<128, 1, EPI>(group, units, stream);
+cudaError_t launch_block(const void* group, int bn, int units, cudaStream_t stream) {
+    if (bn == 256) return launch_block_as<256, 2, EPI>(group, units, stream);
+    return bn == 128 ? launch_block_as<128, 1, EPI>(group, units, stream) : launch_block_as<64, 1, EPI>(group, units, stream);
 }
 
 }  // namespace forge

@@ -24,6 +24,13 @@
 // epilogues have theirs fixed.  A product may have two pairs of operands whose products are summed in
 // one accumulator (dX = dG Wg + dU Wu).
 //
+// One copy per operand and slice.  A slice of either order is one box of a 3-D tensor map: K-major
+// (64 of the reduction, rows, -), MN-major (64 columns, the slice's 64 rows, blocks of 64 columns).  The
+// thread that issues copies sets the pace of the mainloop: with two copies of half the rows for each
+// operand, and their addresses worked out per slice, 4096 tokens against 65536 vocabulary entries of 4096
+// ran at 1.42-1.6 PFLOP/s, with one each at 1.73.  An MN-major operand whose width is no multiple of 64
+// takes two copies: its last block of 64 columns would reach past its rows.
+//
 // Units of work.  A unit is one tile over its whole reduction, or one of `parts` pieces of it.  A
 // split tile has no CTA that waits for another: each epilogue warp leaves its FP32 values in memory,
 // counts itself in, and the warp that arrives last adds the parts up in their order and runs the
@@ -34,6 +41,7 @@
 
 #include <cstdint>
 
+#include "pairs.cuh"
 #include "tile_kernel.cuh"
 
 namespace forge {
@@ -45,7 +53,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 template <int BN, int CG>
 struct BlockCfg {
-    static_assert((BN == 256 && CG == 2) || (BN == 128 && CG == 1), "tile shapes");
+    static_assert((BN == 256 && CG == 2) || ((BN == 128 || BN == 64) && CG == 1), "tile shapes");
     static constexpr int kBLoad = BN / CG;  // B rows (or columns) staged by this CTA
     static constexpr int kABytes = kBM * kBK * 2;
     static constexpr int kBBytes = kBLoad * kBK * 2;
@@ -53,10 +61,10 @@ struct BlockCfg {
     static constexpr int kTmemCols = 2 * BN;
     static constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, half the columns each
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
-    static constexpr int kStages = 7;
+    static constexpr int kStages = BN == 64 ? 9 : 7;
     static constexpr int kRingBytes = kStages * kStageBytes;
     // where A has few rows (BlockGroup::a_rows) its slices are smaller and the ring holds more stages
-    static constexpr int kMaxStages = CG == 1 ? 13 : kStages;
+    static constexpr int kMaxStages = BN == 64 ? 24 : CG == 1 ? 13 : kStages;
     static constexpr int kSmemBytes = kRingBytes + 512 + 1024;  // barriers, alignment slack
     static_assert(kSmemBytes <= 232448, "shared memory");
     static constexpr int stages(int a_rows) {
@@ -73,6 +81,7 @@ struct BlockProblem {
     int parts;
     int kb[2];            // 64-deep reduction slices of the two operand pairs (the second may have none)
     int a_mn, b_mn;       // operand orders (kBlockStore): 1 = MN-major
+    int a_flat, b_flat;   // MN-major and no multiple of 64 wide: (column, row, -) maps, a copy for each 64 columns
     int64_t part_base;    // where its split tiles' FP32 values start (floats)
     int count_base;       // and their counters
     // kBlockStore: out [rows, ld] bf16; add: residual [rows, ld] or null; sum: FP32 [rows, cols] of
@@ -114,7 +123,11 @@ struct BlockGroup {
     BlockProblem prob[NP];
     CUtensorMap maps[4 * NP];  // per product: A, B of the first pair, A, B of the second
     float* parts;
+    // Arrival counters of split tiles: zero before the launch, and zero again after it (the last arrival
+    // resets its own).  zero_n: counters, from zero_at, that this launch clears for the stream's next ones.
     uint32_t* counts;
+    uint32_t* zero_at;
+    int zero_n;
     int* status;
     uint64_t wait_limit_ns, acc_wait_limit_ns;
     int withhold_first_stage;  // test switch, as TileArgs::withhold_first_stage
@@ -318,8 +331,10 @@ __device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc,
 template <int BN, class Acc>
 __device__ __forceinline__ void epi_gated_fwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
     const bool wide = (b.cols & 15) == 0;
+    // 64-wide tiles: one warp of a lane quarter takes all 32 columns
+    constexpr int kCols = BN == 64 ? 32 : BN / 4;
 #pragma unroll 1
-    for (int c = h * (BN / 4); c < (h + 1) * (BN / 4); c += 32) {
+    for (int c = h * kCols; c < (h + 1) * kCols && c < BN / 2; c += 32) {
         const int col = nb * (BN / 2) + c, left = b.cols - col;
         if (left <= 0) break;
         uint32_t g[32], u[32];
@@ -385,7 +400,9 @@ __device__ __forceinline__ void epi_gated_bwd(const BlockProblem& b, const Acc& 
 }
 
 // One pass over the warp's columns with the running maximum and sum, in base 2.  A row whose logits
-// so far are all -inf keeps sum 0.
+// so far are all -inf keeps sum 0.  Maxima and sums run in four chains each, the sums in pairs of
+// binary32: a single chain of dependent operations over 128 columns took longer than the products of a
+// 1024-long reduction, and set the tile's pace.
 template <int BN, class Acc>
 __device__ __forceinline__ void epi_loss_stats(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
     const bool mine = row < b.rows;
@@ -409,15 +426,23 @@ __device__ __forceinline__ void epi_loss_stats(const BlockProblem& b, const Acc&
 #pragma unroll
             for (int j = 0; j < 32; ++j) g[j] = j < left ? g[j] : __float_as_uint(-INFINITY);
         }
-        float top = __uint_as_float(g[0]);
+        float top[4];
 #pragma unroll
-        for (int j = 1; j < 32; ++j) top = fmaxf(top, __uint_as_float(g[j]));
-        const float mn = fmaxf(m, top * kLog2e);
+        for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(g[k]);
+#pragma unroll
+        for (int j = 4; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(g[j]));
+        const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e);
         const float base = mn == -INFINITY ? 0.0f : mn;
-        float e = 0.0f;
+        const F2 scale = F2::all(kLog2e), less = F2::all(-base);
+        F2 e[4];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) e += exp2_fast(__fmaf_rn(__uint_as_float(g[j]), kLog2e, -base));
-        s = __fmaf_rn(s, exp2_fast(m - base), e);
+        for (int j = 0; j < 16; ++j) {
+            const F2 x = fma2(F2::of(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1])), scale, less);
+            const F2 y = F2::of(exp2_fast(x.lo()), exp2_fast(x.hi()));
+            e[j & 3] = j < 4 ? y : add2(e[j & 3], y);
+        }
+        const F2 sum = add2(add2(e[0], e[1]), add2(e[2], e[3]));
+        s = __fmaf_rn(s, exp2_fast(m - base), sum.lo() + sum.hi());
         m = mn;
     }
     if (mine) b.stats[static_cast<size_t>(2 * nb + h) * b.rows + row] = make_float2(m, s);
@@ -447,13 +472,12 @@ __device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& 
         const int at = off >= 0 && off < 32 ? static_cast<int>(off) : -1;
         uint32_t o[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float p = exp2_fast(__fmaf_rn(__uint_as_float(g[j]), kLog2e, shift));
-            const float v = (at == j ? p - 1.0f : p) * scale;
-            g[j] = counts ? __float_as_uint(v) : 0u;
+        for (int j = 0; j < 16; ++j) {
+            const F2 x = fma2(F2::of(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1])), F2::all(kLog2e), F2::all(shift));
+            const float p0 = exp2_fast(x.lo()), p1 = exp2_fast(x.hi());
+            const F2 v = mul2(F2::of(at == 2 * j ? p0 - 1.0f : p0, at == 2 * j + 1 ? p1 - 1.0f : p1), F2::all(scale));
+            o[j] = counts ? pack_bf16x2_rn(__float_as_uint(v.lo()), __float_as_uint(v.hi())) : 0u;
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2_rn(g[2 * j], g[2 * j + 1]);
         store_run(b.out + static_cast<size_t>(row) * b.ld + nb * BN + c, o, left, wide);
     }
 }
@@ -546,6 +570,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
     // the set-up above touches no memory of the stream's other work
     stream_release();
     stream_wait();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < grp.zero_n; i += C::kThreads) grp.zero_at[i] = 0u;
     const uint32_t tmem_base = *tmem_slot;
     const AbortCtx ab{abort_flag, grp.status, grp.wait_limit_ns};
     uint64_t n_issued = 0;
@@ -564,56 +590,62 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
             const uint64_t once = policy_evict_first();
             UnitCursor cur;
             int l = 0;
+            const bool leader = rank == 0;
+            const bool withhold = grp.withhold_first_stage && leader;
+            const uint32_t bars = CG == 2 ? map_to_rank(smem_addr(full), 0) : smem_addr(full);
+            const uint32_t a_bytes = static_cast<uint32_t>(a_rows) * 128u;
+            const uint32_t a_ring = smem_addr(sA), b_ring = smem_addr(sB);
             for (int u = cur.next(grp.units, pair, pairs); ok && u >= 0; u = cur.next(grp.units, pair, pairs)) {
                 const Unit w = unit_of(grp, u, l);
                 l = w.prob;
                 const BlockProblem& b = grp.prob[l];
-                const bool amn = a_mn(b), bmn = b_mn(b);
+                const bool amn = a_mn(b), bmn = b_mn(b), a_flat = b.a_flat != 0, b_flat = b.b_flat != 0;
                 const int row_a = w.mb * kBM * CG + static_cast<int>(rank) * kBM;
                 // with one row of tiles B passes through once
                 const uint64_t pol_b = b.order.tiles_m == 1 ? once : keep;
                 // gated forward: the even CTA (or the first half of the columns) holds the gate's
                 // rows, the other the up projection's, of the same d_ff columns
                 const int col_b = kGated ? w.nb * kColsPerTile : w.nb * BN + static_cast<int>(rank) * C::kBLoad;
-                for (int kb = w.k_first; kb < w.k_end; ++kb) {
-                    if (!wait_bounded(&empty[stage], phase ^ 1u, ab)) { ok = false; break; }
-                    uint32_t bar = smem_addr(&full[stage]);
-                    if constexpr (CG == 2) bar = map_to_rank(bar, 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * stage_bytes);
-                    if (grp.withhold_first_stage && rank == 0 && n_issued == 0) {
-                        withheld = static_cast<int64_t>(n_issued);
-                    } else {
-                        const int second = kb >= b.kb[0] ? 1 : 0;
-                        const int k0 = (kb - (second ? b.kb[0] : 0)) * kBK;
-                        const CUtensorMap* ma = &grp.maps[4 * l + 2 * second];
-                        const CUtensorMap* mb = ma + 1;
-                        uint8_t* a_dst = sA + stage * (a_rows * 128);
-                        uint8_t* b_dst = sB + stage * C::kBBytes;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int r = row_a + 64 * j;
-                            if (64 * j < a_rows)
-                                tma_load_2d_cg<CG>(a_dst + j * kBK * 128, ma, bar, amn ? r : k0, amn ? k0 : r, keep);
-                        }
-                        if constexpr (kGated) {
-                            // maps: A = X, B = Wg; the second pair's B is Wu
-                            const CUtensorMap* mu = &grp.maps[4 * l + 3];
-#pragma unroll
-                            for (int j = 0; j < C::kBLoad / 64; ++j) {
-                                const bool up = CG == 2 ? rank == 1 : j >= C::kBLoad / 128;
-                                const int r = col_b + 64 * (CG == 2 ? j : j % (C::kBLoad / 128));
-                                tma_load_2d_cg<CG>(b_dst + j * kBK * 128, up ? mu : mb, bar, k0, r, pol_b);
-                            }
+#pragma unroll 1
+                for (int seg = 0; seg < 2 && ok; ++seg) {
+                    // the unit's slices of this operand pair
+                    const int from = seg == 0 ? w.k_first : (w.k_first > b.kb[0] ? w.k_first : b.kb[0]);
+                    const int to = seg == 0 && w.k_end > b.kb[0] ? b.kb[0] : w.k_end;
+                    if (from >= to) continue;
+                    const int k0 = (from - (seg == 0 ? 0 : b.kb[0])) * kBK;
+                    const CUtensorMap* ma = &grp.maps[4 * l + 2 * seg];
+                    const CUtensorMap* mb = kGated && CG == 2 && rank == 1 ? &grp.maps[4 * l + 3] : ma + 1;
+                    const CUtensorMap* mu = &grp.maps[4 * l + 3];  // gated forward, one CTA: the up projection's
+                    // coordinates of the first slice and their steps: one of them moves along the reduction
+                    int a0 = amn ? (a_flat ? row_a : 0) : k0, a1 = amn ? k0 : row_a, a2 = amn && !a_flat ? row_a / 64 : 0;
+                    int b0 = bmn ? (b_flat ? col_b : 0) : k0, b1 = bmn ? k0 : col_b, b2 = bmn && !b_flat ? col_b / 64 : 0;
+                    const int da0 = amn ? 0 : kBK, da1 = amn ? kBK : 0, db0 = bmn ? 0 : kBK, db1 = bmn ? kBK : 0;
+#pragma unroll 1
+                    for (int n = to - from; n > 0; --n) {
+                        if (!wait_bounded(&empty[stage], phase ^ 1u, ab)) { ok = false; break; }
+                        const uint32_t bar = bars + 8u * static_cast<uint32_t>(stage);
+                        if (leader) mbar_arrive_expect_tx(&full[stage], CG * stage_bytes);
+                        if (withhold && n_issued == 0) {
+                            // test switch: arm this stage but never copy into it
+                            withheld = 0;
                         } else {
-#pragma unroll
-                            for (int j = 0; j < C::kBLoad / 64; ++j) {
-                                const int r = col_b + 64 * j;
-                                tma_load_2d_cg<CG>(b_dst + j * kBK * 128, mb, bar, bmn ? r : k0, bmn ? k0 : r, pol_b);
-                            }
+                            const uint32_t a_dst = a_ring + static_cast<uint32_t>(stage) * a_bytes;
+                            const uint32_t b_dst = b_ring + static_cast<uint32_t>(stage) * C::kBBytes;
+                            tma_load_3d_cg<CG>(a_dst, ma, bar, a0, a1, a2, keep);
+                            tma_load_3d_cg<CG>(b_dst, mb, bar, b0, b1, b2, pol_b);
+                            if (EPI == kBlockStore && a_flat) tma_load_3d_cg<CG>(a_dst + kBK * 128, ma, bar, a0 + 64, a1, 0, keep);
+                            if (kGated && CG == 1) tma_load_3d_cg<CG>(b_dst + BN / 2 * 128, mu, bar, b0, b1, 0, pol_b);
+                            if (C::kBLoad == 128 && (EPI == kBlockStore || EPI == kBlockGatedBwd) && b_flat)
+                                tma_load_3d_cg<CG>(b_dst + kBK * 128, mb, bar, b0 + 64, b1, 0, pol_b);
                         }
+                        a0 += da0;
+                        a1 += da1;
+                        b0 += db0;
+                        b1 += db1;
+                        ++n_issued;
+                        if (++stage == n_stages) { stage = 0; phase ^= 1u; }
                     }
-                    ++n_issued;
-                    if (++stage == n_stages) { stage = 0; phase ^= 1u; }
+                    if (kGated) break;  // its fourth map is the up projection's, not a second pair's
                 }
             }
             if constexpr (CG == 2) {
@@ -637,23 +669,24 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
                 const bool amn = a_mn(b), bmn = b_mn(b);
                 const uint32_t idesc = idesc_bf16_f32(kBM * CG, BN, amn, bmn);
                 // MN-major: 16 reduction steps are 16 rows of 128 bytes, 64-element blocks 8 KiB apart;
-                // K-major: 32 bytes within each 128-byte row, 8-row groups 1024 bytes apart
-                const uint32_t a_step = amn ? 2048u : 32u, b_step = bmn ? 2048u : 32u;
-                const uint32_t a_lbo = amn ? kBK * 128u : 16u, b_lbo = bmn ? kBK * 128u : 16u;
+                // K-major: 32 bytes within each 128-byte row, 8-row groups 1024 bytes apart.  A
+                // descriptor's address field counts 16 bytes, and no sum below leaves it
+                const uint32_t a_step = (amn ? 2048u : 32u) >> 4, b_step = (bmn ? 2048u : 32u) >> 4;
+                const uint64_t a_desc = smem_desc_sw128(smem_addr(sA), amn ? kBK * 128u : 16u, 1024);
+                const uint64_t b_desc = smem_desc_sw128(smem_addr(sB), bmn ? kBK * 128u : 16u, 1024);
                 if (!wait_bounded(&acc_empty[acc], acc_phase ^ 1u, ab)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+#pragma unroll 1
                 for (int kb = w.k_first; kb < w.k_end; ++kb) {
                     if (!wait_bounded(&full[stage], phase, ab)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a_base = smem_addr(sA + stage * (a_rows * 128));
-                    const uint32_t b_base = smem_addr(sB + stage * C::kBBytes);
+                    const uint64_t ad = a_desc + static_cast<uint32_t>(stage) * (static_cast<uint32_t>(a_rows) * 128u >> 4);
+                    const uint64_t bd = b_desc + static_cast<uint32_t>(stage) * (C::kBBytes >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kBK / kUmmaK; ++kk) {
-                        const uint64_t ad = smem_desc_sw128(a_base + kk * a_step, a_lbo, 1024);
-                        const uint64_t bd = smem_desc_sw128(b_base + kk * b_step, b_lbo, 1024);
-                        tc_mma_bf16<CG>(d_tmem, ad, bd, idesc, (kb != w.k_first || kk != 0) ? 1u : 0u);
-                    }
+                    for (int kk = 0; kk < kBK / kUmmaK; ++kk)
+                        tc_mma_bf16<CG>(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc,
+                                        (kb != w.k_first || kk != 0) ? 1u : 0u);
                     issued_any = true;
                     tc_commit_mask<CG>(&empty[stage], 0x3u);
                     if (++stage == n_stages) { stage = 0; phase ^= 1u; }
@@ -696,11 +729,11 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
                 float* p = grp.parts + b.part_base +
                            (static_cast<size_t>(w.split) * b.parts + w.part) * step + own;
                 // the columns whose epilogue this warp runs: gate and up columns come from both halves
-                constexpr int kRuns = kGated ? 2 : 1, kRun = BN / 2 / kRuns;
+                constexpr int kRuns = kGated ? 2 : 1, kRun = kGated && BN == 64 ? 32 : BN / 2 / kRuns;
 #pragma unroll 1
                 for (int r = 0; r < kRuns; ++r) {
 #pragma unroll 1
-                    for (int c = 0; c < kRun; c += 32) {
+                    for (int c = 0; c < kRun && half * kRun + c < BN / kRuns; c += 32) {
                         const int at = r * (BN / 2) + half * kRun + c;
                         uint32_t g[32];
                         tm.load(at, g);
@@ -724,11 +757,12 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
                 __threadfence();
                 __syncwarp();
                 uint32_t before = 0;
-                if (lane == 0)
-                    before = atomicAdd(grp.counts + b.count_base + (w.split * CG + static_cast<int>(rank)) * C::kEpiWarps + e, 1u);
+                uint32_t* count = grp.counts + b.count_base + (w.split * CG + static_cast<int>(rank)) * C::kEpiWarps + e;
+                if (lane == 0) before = atomicAdd(count, 1u);
                 before = __shfl_sync(0xFFFFFFFFu, before, 0);
                 if (before + 1 == static_cast<uint32_t>(b.parts)) {
                     __threadfence();
+                    if (lane == 0) *count = 0u;
                     const AccParts sum{grp.parts + b.part_base + static_cast<size_t>(w.split) * b.parts * step + own,
                                        step, b.parts, row < b.rows};
                     block_epilogue<BN, EPI>(b, sum, row, w.nb, half);

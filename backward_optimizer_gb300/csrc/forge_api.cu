@@ -161,13 +161,13 @@ OptScalars derive_scalars(forge_opt_kind k, const forge_hparams& hp, int64_t ste
     return s;
 }
 
-forge_status encode_operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, bool e4m3, int64_t ld, int box_rows) {
-    // A [rows, cols] row-major operand, bf16 or E4M3, its rows ld elements apart, read in boxes of box_rows
+forge_status encode_operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, bool e4m3, int64_t ld) {
+    // A [rows, cols] row-major operand, bf16 or E4M3, its rows ld elements apart, read in boxes of 64
     // rows whose rows are exactly one 128-byte swizzle span (64 bf16 or 128 E4M3 columns).
     const int64_t esize = e4m3 ? 1 : 2;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * esize)};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esize), static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esize), 64};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = g_encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                           const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -178,17 +178,15 @@ forge_status encode_operand_map(CUtensorMap* map, const void* base, int64_t cols
 
 // Encoded tensor maps of recent calls, per host thread.  A training loop passes the same buffers
 // with the same shapes every step, and encoding a map costs host time comparable to a small layer's
-// whole kernel.  A map is plain host data determined by (base, sizes, element type), handed to
+// whole kernel.  A map is plain host data determined by (base, cols, rows, ld, element type), handed to
 // the kernel by value, so a cached one is exactly the one a new encoding would give, whatever
 // happened to the buffer in between.
 struct MapKey {
     const void* base;
     int64_t cols, rows, ld;
-    int box_rows;
     bool e4m3;
     bool operator==(const MapKey& o) const {
-        return base == o.base && cols == o.cols && rows == o.rows && ld == o.ld && box_rows == o.box_rows &&
-               e4m3 == o.e4m3;
+        return base == o.base && cols == o.cols && rows == o.rows && ld == o.ld && e4m3 == o.e4m3;
     }
 };
 struct MapSlot {
@@ -201,19 +199,19 @@ thread_local MapSlot t_maps[kMapSlots];
 
 // ld: elements from row to row (0: the rows are contiguous)
 forge_status make_operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, bool e4m3 = false,
-                              int64_t ld = 0, int box_rows = 64) {
+                              int64_t ld = 0) {
     if (ld == 0) ld = cols;
-    const MapKey key{base, cols, rows, ld, box_rows, e4m3};
+    const MapKey key{base, cols, rows, ld, e4m3};
     uint64_t h = reinterpret_cast<uintptr_t>(base) * 0x9E3779B97F4A7C15ull;
     h ^= static_cast<uint64_t>(cols) * 0xC2B2AE3D27D4EB4Full ^ static_cast<uint64_t>(rows) * 0x165667B19E3779F9ull;
     h ^= e4m3 ? 0x27D4EB2F165667C5ull : 0;
-    h ^= static_cast<uint64_t>(ld - cols + 64 - box_rows) * 0x85EBCA77C2B2AE63ull;
+    h ^= static_cast<uint64_t>(ld - cols) * 0x85EBCA77C2B2AE63ull;
     MapSlot& slot = t_maps[(h >> 32) % kMapSlots];
     if (slot.used && slot.key == key) {
         *map = slot.map;
         return FORGE_OK;
     }
-    forge_status st = encode_operand_map(map, base, cols, rows, e4m3, ld, box_rows);
+    forge_status st = encode_operand_map(map, base, cols, rows, e4m3, ld);
     if (st == FORGE_OK) {
         slot.key = key;
         slot.map = *map;
@@ -598,8 +596,15 @@ forge_status device(Device* out) {
     return st;
 }
 
-forge_status operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
-    return make_operand_map(map, base, cols, rows, false, ld, box_rows);
+forge_status encode_map(CUtensorMap* map, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+                        const uint32_t (&box)[3]) {
+    const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, st[2] = {strides[0], strides[1]};
+    const cuuint32_t bx[3] = {box[0], box[1], box[2]}, one[3] = {1, 1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), d, st, bx, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? FORGE_OK
+               : FORGE_ERR_CUDA;
 }
 
 uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }

@@ -20,9 +20,10 @@ struct Device {
 // The current device, checked to be sm_103a.
 forge_status device(Device* out);
 
-// Tensor map of a row-major bfloat16 operand [rows, cols] whose rows start `ld` elements apart, read
-// in boxes of 64 columns x `box_rows` rows with the 128-byte swizzle.
-forge_status operand_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
+// Tensor map of a bfloat16 array of three dimensions (strides in bytes, of the second and third), read in
+// boxes with the 128-byte swizzle: the box's innermost extent is 64 elements.
+forge_status encode_map(CUtensorMap* map, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+                        const uint32_t (&box)[3]);
 
 uint64_t wait_limit_ns();
 uint64_t acc_wait_limit_ns(int64_t k_blocks);

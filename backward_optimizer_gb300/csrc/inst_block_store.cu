@@ -1,7 +1,7 @@
 // The matrix-product kernel with the epilogue kBlockStore.
 #include "block_instantiate.cuh"
 
-template cudaError_t forge::launch_block<forge::kBlockStore>(const void*, bool, int, cudaStream_t);
+template cudaError_t forge::launch_block<forge::kBlockStore>(const void*, int, int, cudaStream_t);
 
 cudaError_t forge::block_pairs(int num_sms, int* pairs) {
     cudaLaunchConfig_t cfg = {};

@@ -26,6 +26,7 @@
 
 #include <cstdint>
 
+#include "pairs.cuh"
 #include "ptx.cuh"
 #include "tile_kernel.cuh"
 
@@ -127,34 +128,6 @@ __device__ __forceinline__ void norm_weights(const void* w, int bf16, int c, flo
             f[0] = *p;
         }
     }
-}
-
-// Two binary32 values in one 64-bit register pair: the f32x2 forms round each as the scalar forms do.
-struct F2 {
-    uint64_t v;
-    __device__ __forceinline__ static F2 of(float a, float b) {
-        F2 r;
-        asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-        return r;
-    }
-    __device__ __forceinline__ static F2 all(float a) { return of(a, a); }
-    __device__ __forceinline__ float lo() const { return __uint_as_float(static_cast<uint32_t>(v)); }
-    __device__ __forceinline__ float hi() const { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-};
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
 }
 
 // A 16-byte run of a row in shared memory as pairs, and a run of results to device memory.
