@@ -106,7 +106,6 @@ void plan_products(Plan& p, const Machine& mc, bool gated, bool a_k_major) {
     if (p.n == 1 && !pair && a_k_major && p.cut[0].rows <= 64) p.a_rows = static_cast<int>(round_up(p.cut[0].rows, 8));
     const int64_t tm = pair ? 256 : 128, tn = p.bn / (gated ? 2 : 1);
     int64_t tiles = 0;
-    double work = 0;
     for (int i = 0; i < p.n; ++i) {
         Cut& c = p.cut[i];
         c.tiles_m = static_cast<int>(ceil_div(c.rows, tm));
@@ -114,40 +113,20 @@ void plan_products(Plan& p, const Machine& mc, bool gated, bool a_k_major) {
         c.parts = 1;
         c.split_from = c.tiles_m * c.tiles_n;
         tiles += c.split_from;
-        work += static_cast<double>(c.split_from) * (c.kb + kEpiSlices);
     }
     if (p.n == 1 && tiles < p.width) {
         // fewer tiles than pairs: cut each so that the units' waves are shortest
         Cut& c = p.cut[0];
         int64_t best = c.kb + kEpiSlices;
         for (int parts = 2; parts <= kMaxParts && c.kb >= kMinSlices * parts; ++parts) {
-            const int64_t t = ceil_div(tiles * parts, p.width) * (ceil_div(c.kb, parts) + kEpiSlices);
+            // each further part adds to the join
+            const int64_t t = ceil_div(tiles * parts, p.width) * (ceil_div(c.kb, parts) + kEpiSlices) + parts;
             if (t < best) {
                 best = t;
                 c.parts = parts;
                 c.split_from = 0;
             }
         }
-    } else if (tiles < p.width) {
-        // the longest units are cut further while all still run at once
-        int64_t units = tiles;
-        for (;;) {
-            int best = -1;
-            for (int i = 0; i < p.n; ++i) {
-                const Cut& c = p.cut[i];
-                if (c.parts < kMaxParts && c.kb >= kMinSlices * (c.parts + 1) &&
-                    (best < 0 || static_cast<int64_t>(c.kb) * p.cut[best].parts >
-                                     static_cast<int64_t>(p.cut[best].kb) * c.parts))
-                    best = i;
-            }
-            if (best < 0) break;
-            const int more = p.cut[best].tiles_m * p.cut[best].tiles_n;
-            if (units + more > p.width) break;
-            units += more;
-            ++p.cut[best].parts;
-        }
-        for (int i = 0; i < p.n; ++i)
-            if (p.cut[i].parts > 1) p.cut[i].split_from = 0;
     } else if (p.n == 1) {
         // a last wave that would leave half of the pairs idle or more is cut so that it fills them
         Cut& c = p.cut[0];
@@ -160,16 +139,36 @@ void plan_products(Plan& p, const Machine& mc, bool gated, bool a_k_major) {
             }
         }
     } else {
-        // a product whose units are a sizeable part of a pair's whole work is cut
-        const double each = work / p.width;
+        // The call lasts about as long as its longest unit, or as an even share of all work: units are cut
+        // to the length at which the larger of the two is smallest.  A unit's time: its slices, or its
+        // epilogue where that is longer; a part's sums cost it a little more.
+        auto parts_for = [&](const Cut& c, int length) {
+            return std::max(1, std::min({static_cast<int>(ceil_div(c.kb, length)), kMaxParts, c.kb / kMinSlices}));
+        };
+        int kb_max = 0;
+        for (int i = 0; i < p.n; ++i) kb_max = std::max(kb_max, p.cut[i].kb);
+        double best = 0;
+        int best_length = kb_max;
+        for (int cuts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            const int length = static_cast<int>(ceil_div(kb_max, cuts));
+            double longest = 0, work = 0;
+            for (int i = 0; i < p.n; ++i) {
+                const Cut& c = p.cut[i];
+                const int parts = parts_for(c, length);
+                const double unit = std::max<double>(static_cast<double>(c.kb) / parts, kEpiSlices) + (parts > 1 ? 3 : 1);
+                longest = std::max(longest, unit);
+                work += unit * parts * c.tiles_m * c.tiles_n;
+            }
+            const double t = std::max(longest, work / p.width);
+            if (cuts == 1 || t < 0.97 * best) {
+                best = t;
+                best_length = length;
+            }
+        }
         for (int i = 0; i < p.n; ++i) {
             Cut& c = p.cut[i];
-            if (4.0 * c.kb <= each) continue;
-            const int parts = std::min({static_cast<int>(4.0 * c.kb / each) + 1, kMaxParts, c.kb / kMinSlices});
-            if (parts > 1) {
-                c.parts = parts;
-                c.split_from = 0;
-            }
+            c.parts = parts_for(c, best_length);
+            if (c.parts > 1) c.split_from = 0;
         }
     }
     p.part_floats = 0;

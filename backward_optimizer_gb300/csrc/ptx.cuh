@@ -159,7 +159,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
-// The same for a 3-D tensor map.
+// tma_load_2d_cg for a 3-D tensor map.
 template <int CG>
 __device__ __forceinline__ void tma_load_3d_cg(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
                                                int32_t c2, uint64_t policy) {
