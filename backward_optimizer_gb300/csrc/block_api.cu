@@ -12,6 +12,7 @@
 #include "block_launch.h"
 #include "forge.h"
 #include "host.h"
+#include "rows_kernel.cuh"
 
 namespace {
 
@@ -485,6 +486,7 @@ forge_status check_workspace(const void* ws, int64_t have, int64_t need) {
 }
 
 struct GatedForward {
+    bool one;  // a single token: rows_kernel.cuh
     Plan up, down;
     Product y;
     int64_t h, bytes;
@@ -492,8 +494,14 @@ struct GatedForward {
 };
 
 GatedForward layout_gated_forward(const Machine& mc, const forge_gated_shape& s) {
-    GatedForward l;
+    GatedForward l{};
     Arena a;
+    l.one = forge::rows_fit(s.T, s.d_model, true) && forge::rows_fit(s.T, s.d_ff, false);
+    if (l.one) {
+        l.h = a.take(s.T * s.d_ff * 2);
+        l.bytes = a.used;
+        return l;
+    }
     l.up = plan_one(mc, s.T, s.d_ff, slices(s.d_model), true);
     l.y = product_nt(nullptr, nullptr, s.T, s.d_model, s.d_ff, nullptr, nullptr);
     l.down = plan_store(mc, &l.y, 1);
@@ -798,6 +806,31 @@ forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, cons
     GatedForward l = layout_gated_forward(mc, s);
     FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     char* ws = static_cast<char*>(workspace);
+    if (l.one) {
+        forge::RowsArgs r{};
+        r.x = static_cast<const uint16_t*>(X);
+        r.w = static_cast<const uint16_t*>(Wg);
+        r.w2 = static_cast<const uint16_t*>(Wu);
+        r.y = reinterpret_cast<uint16_t*>(ws + l.h);
+        r.g_out = static_cast<uint16_t*>(G);
+        r.u_out = static_cast<uint16_t*>(U);
+        r.N = static_cast<int>(s.d_ff);
+        r.K = static_cast<int>(s.d_model);
+        r.act = s.act;
+        r.status = mc.dev.status;
+        r.wait_limit_ns = host::wait_limit_ns();
+        FORGE_TRY(cuda_status(forge::launch_rows(r, true, mc.dev.num_sms, stream)));
+        forge::RowsArgs d = r;
+        d.x = r.y;
+        d.w = static_cast<const uint16_t*>(Wd);
+        d.w2 = nullptr;
+        d.add = static_cast<const uint16_t*>(residual);
+        d.y = static_cast<uint16_t*>(Y);
+        d.N = static_cast<int>(s.d_model);
+        d.K = static_cast<int>(s.d_ff);
+        d.weights_ready = 1;
+        return cuda_status(forge::launch_rows(d, false, mc.dev.num_sms, stream));
+    }
     BlockGroup<1> g;
     std::memset(&g, 0, sizeof(g));
     FORGE_TRY(fill_group(g, l.up, mc, ws, l.split));
