@@ -486,7 +486,7 @@ forge_status check_workspace(const void* ws, int64_t have, int64_t need) {
 }
 
 struct GatedForward {
-    bool one;  // a single token: rows_kernel.cuh
+    bool few;  // one to four tokens: rows_kernel.cuh
     Plan up, down;
     Product y;
     int64_t h, bytes;
@@ -496,8 +496,8 @@ struct GatedForward {
 GatedForward layout_gated_forward(const Machine& mc, const forge_gated_shape& s) {
     GatedForward l{};
     Arena a;
-    l.one = forge::rows_fit(s.T, s.d_model, true) && forge::rows_fit(s.T, s.d_ff, false);
-    if (l.one) {
+    l.few = forge::rows_fit(s.T, s.d_model, true) && forge::rows_fit(s.T, s.d_ff, false);
+    if (l.few) {
         l.h = a.take(s.T * s.d_ff * 2);
         l.bytes = a.used;
         return l;
@@ -806,7 +806,7 @@ forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, cons
     GatedForward l = layout_gated_forward(mc, s);
     FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     char* ws = static_cast<char*>(workspace);
-    if (l.one) {
+    if (l.few) {
         forge::RowsArgs r{};
         r.x = static_cast<const uint16_t*>(X);
         r.w = static_cast<const uint16_t*>(Wg);
@@ -814,6 +814,7 @@ forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, cons
         r.y = reinterpret_cast<uint16_t*>(ws + l.h);
         r.g_out = static_cast<uint16_t*>(G);
         r.u_out = static_cast<uint16_t*>(U);
+        r.T = static_cast<int>(s.T);
         r.N = static_cast<int>(s.d_ff);
         r.K = static_cast<int>(s.d_model);
         r.act = s.act;

@@ -19,7 +19,7 @@ template <int EPI> cudaError_t launch_block(const void* group, int bn, int units
 // CTA pairs that the current device runs at once.
 cudaError_t block_pairs(int num_sms, int* pairs);
 
-// Whether the single-token kernel (rows_kernel.cuh) takes T tokens and rows of K weights.
+// Whether the few-token kernel (rows_kernel.cuh) takes T tokens and rows of K weights.
 bool rows_fit(int64_t T, int64_t K, bool gated);
 cudaError_t launch_rows(RowsArgs a, bool gated, int num_sms, cudaStream_t stream);
 

@@ -1,15 +1,19 @@
-// rows_kernel.cuh -- the product of one token with a weight matrix: y[n] = sum_k x[k] W[n, k].
+// rows_kernel.cuh -- products of one to four tokens with a weight matrix: y[t, n] = sum_k x[t, k] W[n, k].
 //
-// Every weight is read once and used once, so the time is the weights' way from memory.  The tensor core's
+// Every weight is read once and used a few times, so the time is the weights' way from memory.  The tensor core's
 // 128-row tiles would be almost empty, and the splitting and joining along k that few tiles need costs
 // more than the products.  Here a block stays on its SM and walks groups of weight rows through a ring of
 // bulk copies (whole rows, contiguous in memory, up to 200 KB in flight per SM).  16 warps share each row
-// along k and keep their parts of x in registers; a warp leaves its sum of a group in shared memory and
+// along k and keep their parts of x in registers; a warp leaves its sums of a group in shared memory and
 // goes on to the next group.  The groups' sums are joined eight groups at a time, one output a warp: a
-// join behind every group, with all warps waiting for it, took as long as the copies of the next one.
+// join behind every group, with all warps waiting for it, took as long as the copies of the next one (one
+// token, 4096/14336: 58.9 us against 54.2).
 //
 // GATED: a group holds the same rows of the gate and of the up projection, and its result is
 // act(g) u (with g and u themselves where they are wanted); else y (+ add).
+//
+// Measured, both products of a gated block: 4096/14336 one token 54.2 us, 6.5 TB/s of weights (0.96 of the
+// copy rate), two 55.4; 2048/5632 one token 19 us, of which half is the two launches.
 #pragma once
 
 #include <cstdint>
@@ -27,14 +31,14 @@ constexpr int kRowsMaxVecs = 5;  // 16-byte pieces of x a thread holds: k up to 
 constexpr int kRowsBatch = 8;    // groups between joins
 
 struct RowsArgs {
-    const uint16_t* x;      // [K]
+    const uint16_t* x;      // [T, K]
     const uint16_t* w;      // [N, K]: gate, or W
     const uint16_t* w2;     // GATED: up [N, K]
-    const uint16_t* add;    // not GATED: residual [N] or null
-    uint16_t* y;            // [N]
-    uint16_t* g_out;        // GATED: [N], or null
+    const uint16_t* add;    // not GATED: residual [T, N] or null
+    uint16_t* y;            // [T, N]
+    uint16_t* g_out;        // GATED: [T, N], or null
     uint16_t* u_out;
-    int N, K, act;
+    int T, N, K, act;
     int slots;
     // The launch before this one on the stream does not write W, and was itself launched so that all work
     // before it is done once this one starts: the ring may fill before stream_wait().
@@ -43,11 +47,32 @@ struct RowsArgs {
     uint64_t wait_limit_ns;
 };
 
-// ROWS: weight rows per group (GATED: half of them the gate's); VECS: ceil(K / 8 / 512)
-template <int ROWS, int VECS, bool GATED>
+// Sums each of V values (a power of two) over a warp: every exchange halves the values a lane still holds,
+// V - 1 of them and then log2(32 / V) more, instead of 5 V.  Afterwards a lane holds the sum of value `at`.
+template <int V>
+__device__ __forceinline__ float warp_sums(float (&v)[V], int lane, int& at) {
+    at = 0;
+    int o = 16;
+#pragma unroll
+    for (int n = V / 2; n > 0; n /= 2, o /= 2) {
+        const bool high = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float keep = high ? v[i + n] : v[i], give = high ? v[i] : v[i + n];
+            v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+        }
+        if (high) at += n;
+    }
+#pragma unroll
+    for (; o > 0; o /= 2) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+    return v[0];
+}
+
+// T: tokens, at most (three run as four); ROWS: weight rows per group (GATED: half of them the gate's); VECS: ceil(K / 8 / 512)
+template <int T, int ROWS, int VECS, bool GATED>
 __global__ void __launch_bounds__(kRowsThreads, 1) forge_rows_kernel(const RowsArgs a) {
     extern __shared__ __align__(128) uint8_t rows_ring[];
-    __shared__ float part[2][kRowsBatch][ROWS][kRowsWarps];
+    __shared__ float part[2][kRowsBatch][ROWS * T][kRowsWarps];
     __shared__ uint64_t full[kRowsMaxSlots], empty[kRowsMaxSlots];
     __shared__ int abort_flag;
     constexpr int kN = GATED ? ROWS / 2 : ROWS;  // outputs per group
@@ -100,32 +125,36 @@ __global__ void __launch_bounds__(kRowsThreads, 1) forge_rows_kernel(const RowsA
                 drain_bounded(&full[i], static_cast<uint32_t>(((issued - 1 - i) / a.slots) & 1), a.wait_limit_ns);
         return;
     }
-    uint32_t x[VECS][4];
+    uint32_t x[T][VECS][4];
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-        const int k = 8 * (tid + i * kRowsLanes);
+    for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = 0u;
-        if (k < a.K) ld_v4(a.x + k, x[i]);
-    }
+        for (int i = 0; i < VECS; ++i) {
+            const int k = 8 * (tid + i * kRowsLanes);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[t][i][j] = 0u;
+            if (k < a.K && t < a.T) ld_v4(a.x + static_cast<size_t>(t) * a.K + k, x[t][i]);
+        }
     auto pair = [](uint32_t w) { return F2::of(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); };
     // the outputs of groups first .. first + n - 1 of this block
     auto join = [&](int first, int n) {
         const int buf = (first / kRowsBatch) & 1, half = lane >> 4;
-        // a half warp sums one row's 16 parts: gated, the two halves take an output's gate and up rows
-        for (int o = GATED ? warp : 2 * warp + half; o < n * kN + (GATED ? 0 : half); o += GATED ? kRowsWarps : 2 * kRowsWarps) {
-            const bool real = o < n * kN;
-            const int g = real ? o / kN : 0, c = real ? o - g * kN : 0;
-            float v = part[buf][g][GATED ? c + half * kN : c][lane & 15];
+        // output o = (group, column, token); a half warp sums one row's 16 parts: gated, the two halves take
+        // an output's gate and up rows
+        const int outputs = n * kN * T;
+        for (int o = GATED ? warp : 2 * warp + half; o < outputs + (GATED ? 0 : half); o += GATED ? kRowsWarps : 2 * kRowsWarps) {
+            const bool real = o < outputs;
+            const int g = real ? o / (kN * T) : 0, c = real ? o / T - g * kN : 0, t = o % T;
+            float v = part[buf][g][(GATED ? c + half * kN : c) * T + t][lane & 15];
 #pragma unroll
             for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-            const int at = (static_cast<int>(blockIdx.x) + (first + g) * stride) * kN + c;
+            const size_t at = static_cast<size_t>(t) * a.N + (static_cast<int>(blockIdx.x) + (first + g) * stride) * kN + c;
             auto put = [&](uint16_t* p, float f) {
                 p[at] = static_cast<uint16_t>(pack_bf16x2_rn(__float_as_uint(f), 0u) & 0xFFFFu);
             };
             if constexpr (GATED) {
                 const float u = __shfl_sync(0xFFFFFFFFu, v, 16);
-                if (lane == 0) {
+                if (lane == 0 && t < a.T) {
                     if (a.g_out != nullptr) {
                         put(a.g_out, v);
                         put(a.u_out, u);
@@ -133,7 +162,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) forge_rows_kernel(const RowsA
                     put(a.y, act_value(v, a.act) * u);
                 }
             } else {
-                if ((lane & 15) == 0 && real)
+                if ((lane & 15) == 0 && real && t < a.T)
                     put(a.y, a.add == nullptr ? v : v + __uint_as_float(static_cast<uint32_t>(a.add[at]) << 16));
             }
         }
@@ -143,9 +172,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1) forge_rows_kernel(const RowsA
     for (int k = 0; k < mine; ++k) {
         wait_bounded(&full[slot], phase, ab);
         const uint32_t src = smem_addr(rows_ring) + static_cast<uint32_t>(slot) * slot_bytes + 16u * tid;
-        F2 sum[ROWS][2];
+        // two chains of sums per output where there are few outputs
+        constexpr int kChains = T == 1 ? 2 : 1;
+        F2 sum[ROWS][T][kChains];
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) sum[r][0] = sum[r][1] = F2::all(0.0f);
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int h = 0; h < kChains; ++h) sum[r][t][h] = F2::all(0.0f);
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
             if (8 * (tid + i * kRowsLanes) < a.K) {
@@ -154,23 +189,35 @@ __global__ void __launch_bounds__(kRowsThreads, 1) forge_rows_kernel(const RowsA
                 for (int r = 0; r < ROWS; ++r) ld_shared_v4(src + r * row_bytes + i * (16u * kRowsLanes), w[r]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const F2 xp = pair(x[i][j]);
+                    F2 xp[T];
 #pragma unroll
-                    for (int r = 0; r < ROWS; ++r) sum[r][j & 1] = fma2(pair(w[r][j]), xp, sum[r][j & 1]);
+                    for (int t = 0; t < T; ++t) xp[t] = pair(x[t][i][j]);
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) {
+                        const F2 wp = pair(w[r][j]);
+#pragma unroll
+                        for (int t = 0; t < T; ++t) {
+                            F2& to = sum[r][t][j & (kChains - 1)];
+                            to = fma2(wp, xp[t], to);
+                        }
+                    }
                 }
             }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);  // this warp has read the slot
-        float(&out)[ROWS][kRowsWarps] = part[(k / kRowsBatch) & 1][k % kRowsBatch];
+        float v[ROWS * T];
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            const F2 both = add2(sum[r][0], sum[r][1]);
-            float v = both.lo() + both.hi();
+        for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            if (lane == 0) out[r][warp] = v;
-        }
+            for (int t = 0; t < T; ++t) {
+                const F2 s = kChains == 2 ? add2(sum[r][t][0], sum[r][t][kChains - 1]) : sum[r][t][0];
+                v[r * T + t] = s.lo() + s.hi();
+            }
+        int at;
+        const float total = warp_sums(v, lane, at);
+        // the lanes that hold the same value differ in the bits past its exchanges
+        if ((lane & (32 / (ROWS * T) - 1)) == 0) part[(k / kRowsBatch) & 1][k % kRowsBatch][at][warp] = total;
         if (k % kRowsBatch == kRowsBatch - 1 || k + 1 == mine) {
             // the other buffer is written before the next such barrier, which no warp passes before it is
             // done with this join
