@@ -400,8 +400,8 @@ forge_status run_store(const Machine& mc, const Plan& p, const Product* pr, char
 }
 
 __global__ void __launch_bounds__(256) zero_counts_kernel(uint32_t* counts, int n) {
-    forge::stream_release();
     forge::stream_wait();
+    forge::stream_release();
     for (int i = threadIdx.x; i < n; i += 256) counts[i] = 0u;
 }
 
@@ -715,8 +715,8 @@ __global__ void __launch_bounds__(kFinishThreads)
                        float* loss, float* lse) {
     constexpr int kShares = kFinishThreads / kRows;
     __shared__ float2 part[kShares][kRows];
-    forge::stream_release();
     forge::stream_wait();
+    forge::stream_release();
     const int r = threadIdx.x % kRows, share = threadIdx.x / kRows;
     const int row = blockIdx.x * kRows + r;
     float m = -INFINITY, s = 0.0f;
@@ -754,8 +754,8 @@ __global__ void __launch_bounds__(1024)
     loss_begin_kernel(const float* dloss, const int64_t* target, int64_t ignore, int rows, float* unit, uint32_t* counts,
                       int n_counts) {
     __shared__ float part[32];
-    forge::stream_release();
     forge::stream_wait();
+    forge::stream_release();
     for (int i = threadIdx.x; i < n_counts; i += 1024) counts[i] = 0u;
     float m = 0.0f;
     for (int i = threadIdx.x; i < rows; i += 1024) m = fmaxf(m, target[i] == ignore ? 0.0f : fabsf(dloss[i]));

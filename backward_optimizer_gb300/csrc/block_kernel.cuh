@@ -568,8 +568,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
     if constexpr (CG > 1) cluster_sync();
     tc_fence_after();
     // the set-up above touches no memory of the stream's other work
-    stream_release();
     stream_wait();
+    stream_release();
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < grp.zero_n; i += C::kThreads) grp.zero_at[i] = 0u;
     const uint32_t tmem_base = *tmem_slot;

@@ -195,8 +195,8 @@ struct GroupSum {
 template <class TX, int VEC, int NV, bool CENTER>
 __global__ void __launch_bounds__(kNormThreads) forge_norm_kernel(const NormArgs a) {
     __shared__ float2 buf[2][kNormThreads / 32];
-    stream_release();
     stream_wait();
+    stream_release();
     GroupSum sum{buf, 0};
     const float inv = 1.0f / static_cast<float>(a.D);
     const int step = blockDim.x * VEC;
@@ -293,8 +293,8 @@ template <class TX, int VEC, int NV, bool CENTER>
 __global__ void __launch_bounds__(kNormThreads) forge_norm_bwd_kernel(const NormArgs a) {
     __shared__ float2 buf[2][kNormThreads / 32];
     extern __shared__ float cols[];  // [groups][dw, db]
-    stream_release();
     stream_wait();
+    stream_release();
     GroupSum sum{buf, 0};
     const float inv = 1.0f / static_cast<float>(a.D);
     const int step = blockDim.x * VEC;
@@ -492,8 +492,8 @@ __device__ __forceinline__ NormRing<TX, TENSORS> norm_ring(const NormArgs& a, co
         if (threadIdx.y == 0) *abort_flag = 0;
         fence_mbar_init();
     }
-    stream_release();
     stream_wait();
+    stream_release();
     if (threadIdx.x == 0) r.start();  // its own barriers; the others wait on them past the block's barrier
     __syncthreads();
     return r;
@@ -707,8 +707,8 @@ __global__ void __launch_bounds__(32 * kColumnWarps)
     __shared__ float s[kColumnWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;  // column of the n = D (dw) or 2 D (dw, db) values of a row
-    stream_release();
     stream_wait();
+    stream_release();
     float v = 0.0f;
     if (c < n) {
         for (int first = warp; first < blocks; first += kColumnWarps * kColumnRows) {

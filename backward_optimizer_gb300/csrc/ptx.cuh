@@ -117,8 +117,9 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
 // ---------------------------------------------------------------- dependent launches
 // A kernel launched with programmatic stream serialization may start while the kernel before it on
 // the stream is still running.  It calls stream_wait() before it touches any memory that the stream's
-// earlier work reads or writes (every thread, so that nothing is ordered by luck), and lets the next
-// kernel start early with stream_release().
+// earlier work reads or writes (every thread, so that nothing is ordered by luck), and then lets the next
+// kernel start early with stream_release(), always in this order: when a launch starts, everything
+// on the stream but the one launch before it is done.
 
 __device__ __forceinline__ void stream_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void stream_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

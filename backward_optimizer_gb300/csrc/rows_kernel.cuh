@@ -40,8 +40,8 @@ struct RowsArgs {
     uint16_t* u_out;
     int T, N, K, act;
     int slots;
-    // The launch before this one on the stream does not write W, and was itself launched so that all work
-    // before it is done once this one starts: the ring may fill before stream_wait().
+    // The launch before this one on the stream does not write W, and all work before that one is done once
+    // this one starts (ptx.cuh): the ring may fill before stream_wait().
     int weights_ready;
     int* status;
     uint64_t wait_limit_ns;
@@ -100,7 +100,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1) forge_rows_kernel(const RowsA
             for (int k = 0; k < a.slots && k < mine; ++k) issue(k, k);
     }
     stream_wait();
-    // not before: what starts after this launch may rely on the work before it being done
     stream_release();
     __syncthreads();
     if (warp == kRowsWarps) {
