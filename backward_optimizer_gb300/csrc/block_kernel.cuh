@@ -715,16 +715,6 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
             l = w.prob;
             const BlockProblem& b = grp.prob[l];
             const int row = w.mb * kBM * CG + static_cast<int>(rank) * kBM + quarter * 32 + lane;
-            if constexpr (EPI == kBlockGatedBwd) {
-                // G and U of this tile come into L2 while its products run
-                if (w.split < 0 && row < b.rows) {
-                    for (int c = half * (BN / 2); c < (half + 1) * (BN / 2) && w.nb * BN + c < b.cols; c += 64) {
-                        const size_t at = static_cast<size_t>(row) * b.cols + w.nb * BN + c;
-                        prefetch_l2(b.g_in + at);
-                        prefetch_l2(b.u_in + at);
-                    }
-                }
-            }
             int ok = 1;
             if (lane == 0) ok = wait_bounded(&acc_full[acc], acc_phase, ab_acc) ? 1 : 0;
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
