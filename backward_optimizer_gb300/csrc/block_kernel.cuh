@@ -31,6 +31,18 @@
 // ran at 1.42-1.6 PFLOP/s, with one each at 1.73.  An MN-major operand whose width is no multiple of 64
 // takes two copies: its last block of 64 columns would reach past its rows.
 //
+// What bounds it, measured on one GB300.  Large products: the tensor core under the chip's power limit.  In
+// bursts below the limit, 4096 tokens: block forward 4096/14336 811 us (1.78 PFLOP/s, 0.93 of the measured
+// burst peak), block backward 1681 us (1.72), loss forward over 32768 x 4096 577 us (1.91), loss backward
+// 1800 us (1.83); run on end, at the limit, 1.79, 1.53, 1.78 and 1.64.  Products with MN-major operands
+// (dX, dW, dH) reach less there than K-major ones.  The tile with dH also shares the memory system with G,
+// U, dG, dU and H: 165 us at 2048 tokens (1.45 PFLOP/s), the same with 16 epilogue warps, with G and U
+// prefetched into L2, or loaded first to be evicted.  With one row of tiles: memory, 6.4 TB/s of weights for
+// the loss of one token over 155648 x 4096.
+//
+// Why these tiles.  A pair's 256 x 256 tile moves 32 KB into each SM's shared memory per 512 cycles of its
+// tensor core; single CTAs on 128 x 128 move twice as much per product and serve small calls.
+//
 // Units of work.  A unit is one tile over its whole reduction, or one of `parts` pieces of it.  A
 // split tile has no CTA that waits for another: each epilogue warp leaves its FP32 values in memory,
 // counts itself in, and the warp that arrives last adds the parts up in their order and runs the

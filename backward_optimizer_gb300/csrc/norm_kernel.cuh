@@ -16,6 +16,13 @@
 // Either way the variance is taken about the mean in a second pass over data on the SM, not as a
 // difference of large sums.
 //
+// Measured on one GB300 (copy rate 6.78 TB/s), bf16: RMS norm forward 8192 x 5120 27.5-29.3 us (5.7-6.1 TB/s),
+// 32768 x 5120 102 us (6.5 TB/s); layer norm forward 32768 x 4096 95 us (5.6); layer norm backward
+// 4096 x 4096 26.3 us (3.8), 32768 x 4096 142 us (5.7), RMS norm backward 32768 x 5120 153 us (6.6).  A
+// backward call has some 10 us of its own: two launches, the rings' first and last rows, the columns' join.
+// The layer norm's backward arithmetic issues at 0.53 of the schedulers' rate with the 16 warps that its
+// registers leave; 32 warps of one run each took longer (32.5 us: more of a row's time in its sums).
+//
 // dw and db are sums over all tokens of a column.  A thread owns the same columns in every row of its
 // group, so they gather in its registers; the groups of a block add up in shared memory, a block
 // leaves one row of partial sums, and a second kernel adds the blocks' rows up in their order: no
