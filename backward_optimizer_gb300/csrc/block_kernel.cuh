@@ -150,6 +150,15 @@ struct Unit {
     int k_first, k_end;             // slices of the concatenated operand pairs
 };
 
+// stream_wait() with a role's first unit in hand: the compiler may not move its computation past the wait.
+__device__ __forceinline__ void stream_wait_with(int& u, Unit& w) {
+    asm volatile("griddepcontrol.wait;"
+                 : "+r"(u), "+r"(w.prob), "+r"(w.mb), "+r"(w.nb), "+r"(w.part), "+r"(w.split), "+r"(w.k_first), "+r"(w.k_end)
+                 :
+                 : "memory");
+    stream_release();
+}
+
 template <int NP>
 __device__ __forceinline__ Unit unit_of(const BlockGroup<NP>& g, int u, int l) {
     if constexpr (NP > 1) {
@@ -210,11 +219,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // ---------------------------------------------------------------- rows of bfloat16 in memory
 
-// 32 columns of one row, packed in pairs; `left`: columns from here to the end of the row (stored or
+// 2 W columns of one row, packed in pairs; `left`: columns from here to the end of the row (stored or
 // loaded in runs of 8); wide: the row's address is a multiple of 32 bytes at every 16th column
-__device__ __forceinline__ void store_run(uint16_t* p, const uint32_t (&v)[16], int left, bool wide) {
+template <int W>
+__device__ __forceinline__ void store_run(uint16_t* p, const uint32_t (&v)[W], int left, bool wide) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < W / 8; ++h) {
         if (wide && left >= 16 * h + 16) {
             const uint32_t r[8] = {v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3],
                                    v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]};
@@ -232,9 +242,10 @@ __device__ __forceinline__ void store_run(uint16_t* p, const uint32_t (&v)[16], 
     }
 }
 
-__device__ __forceinline__ void load_run(const uint16_t* p, uint32_t (&v)[16], int left, bool wide) {
+template <int W>
+__device__ __forceinline__ void load_run(const uint16_t* p, uint32_t (&v)[W], int left, bool wide) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < W / 8; ++h) {
         if (wide && left >= 16 * h + 16) {
             uint32_t r[8];
             ld_v8(p + 16 * h, r);
@@ -263,6 +274,10 @@ struct AccTmem {
         tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(c), g);
         tmem_ld_wait(g);
     }
+    __device__ __forceinline__ void load(int c, uint32_t (&g)[16]) const {
+        __syncwarp();
+        tmem_ld_16(taddr + static_cast<uint32_t>(c), g);
+    }
 };
 
 struct AccParts {
@@ -270,17 +285,18 @@ struct AccParts {
     size_t step;     // floats from part to part
     int parts;
     bool valid;      // rows past the output's last left nothing in memory
-    __device__ __forceinline__ void load(int c, uint32_t (&g)[32]) const {
-        float s[32];
+    template <int N>
+    __device__ __forceinline__ void load(int c, uint32_t (&g)[N]) const {
+        float s[N];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[j] = valid ? __ldcg(p + static_cast<size_t>(c + j) * 32) : 0.0f;
+        for (int j = 0; j < N; ++j) s[j] = valid ? __ldcg(p + static_cast<size_t>(c + j) * 32) : 0.0f;
         for (int k = 1; k < parts; ++k) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < N; ++j)
                 s[j] = __fadd_rn(s[j], valid ? __ldcg(p + k * step + static_cast<size_t>(c + j) * 32) : 0.0f);
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) g[j] = __float_as_uint(s[j]);
+        for (int j = 0; j < N; ++j) g[j] = __float_as_uint(s[j]);
     }
 };
 
@@ -379,23 +395,26 @@ __device__ __forceinline__ void epi_gated_fwd(const BlockProblem& b, const Acc& 
 template <int BN, class Acc>
 __device__ __forceinline__ void epi_gated_bwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
     const bool wide = (b.cols & 15) == 0;
+    // Columns at a time: on single CTAs, which serve small calls, half as many: a launch's first pass through
+    // the arithmetic waits for its instructions
+    constexpr int kStep = BN == 256 ? 32 : 16;
 #pragma unroll 1
-    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
+    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += kStep) {
         const int col = nb * BN + c, left = b.cols - col;
         if (left <= 0) break;
         const bool mine = row < b.rows;
         const size_t at = static_cast<size_t>(row) * b.cols + col;
-        uint32_t g[16], u[16];
+        uint32_t g[kStep / 2], u[kStep / 2];
         if (mine) {
             load_run(b.g_in + at, g, left, wide);
             load_run(b.u_in + at, u, left, wide);
         }
-        uint32_t d[32];
+        uint32_t d[kStep];
         acc.load(c, d);
         if (!mine) continue;
-        uint32_t o[16];
+        uint32_t o[kStep / 2];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < kStep / 2; ++j) {
             float a0, s0, a1, s1;
             act_both(bf16_lo(g[j]), b.act, a0, s0);
             act_both(bf16_hi(g[j]), b.act, a1, s1);
@@ -579,11 +598,9 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
     __syncthreads();
     if constexpr (CG > 1) cluster_sync();
     tc_fence_after();
-    // the set-up above touches no memory of the stream's other work
-    stream_wait();
-    stream_release();
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < grp.zero_n; i += C::kThreads) grp.zero_at[i] = 0u;
+    // None of this touches memory of the stream's other work, and neither does finding a role's first
+    // unit: its divisions and the first reads of the launch's parameters take some 2000 cycles, which pass
+    // while the launch before this one ends.
     const uint32_t tmem_base = *tmem_slot;
     const AbortCtx ab{abort_flag, grp.status, grp.wait_limit_ns};
     uint64_t n_issued = 0;
@@ -594,22 +611,27 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
     auto b_mn = [&](const BlockProblem& b) { return EPI == kBlockStore ? b.b_mn != 0 : EPI == kBlockGatedBwd; };
 
     if (warp == 0) {
+        UnitCursor cur;
+        int u = cur.next(grp.units, pair, pairs);
+        Unit w = unit_of(grp, u < 0 ? 0 : u, 0);
+        stream_wait_with(u, w);
+        auto advance = [&]() {
+            u = cur.next(grp.units, pair, pairs);
+            if (u >= 0) w = unit_of(grp, u, w.prob);
+        };
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             const uint64_t keep = policy_evict_last();
             const uint64_t once = policy_evict_first();
-            UnitCursor cur;
-            int l = 0;
             const bool leader = rank == 0;
             const bool withhold = grp.withhold_first_stage && leader;
             const uint32_t bars = CG == 2 ? map_to_rank(smem_addr(full), 0) : smem_addr(full);
             const uint32_t a_bytes = static_cast<uint32_t>(a_rows) * 128u;
             const uint32_t a_ring = smem_addr(sA), b_ring = smem_addr(sB);
-            for (int u = cur.next(grp.units, pair, pairs); ok && u >= 0; u = cur.next(grp.units, pair, pairs)) {
-                const Unit w = unit_of(grp, u, l);
-                l = w.prob;
+            for (; ok && u >= 0; advance()) {
+                const int l = w.prob;
                 const BlockProblem& b = grp.prob[l];
                 const bool amn = a_mn(b), bmn = b_mn(b), a_flat = b.a_flat != 0, b_flat = b.b_flat != 0;
                 const int row_a = w.mb * kBM * CG + static_cast<int>(rank) * kBM;
@@ -668,16 +690,20 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
             }
         }
     } else if (warp == 1) {
+        UnitCursor cur;
+        int u = cur.next(grp.units, pair, pairs);
+        Unit w = unit_of(grp, u < 0 ? 0 : u, 0);
+        stream_wait_with(u, w);
+        auto advance = [&]() {
+            u = cur.next(grp.units, pair, pairs);
+            if (u >= 0) w = unit_of(grp, u, w.prob);
+        };
         if (lane == 0 && rank == 0) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, issued_any = false;
-            UnitCursor cur;
-            int l = 0;
-            for (int u = cur.next(grp.units, pair, pairs); ok && u >= 0; u = cur.next(grp.units, pair, pairs)) {
-                const Unit w = unit_of(grp, u, l);
-                l = w.prob;
-                const BlockProblem& b = grp.prob[l];
+            for (; ok && u >= 0; advance()) {
+                const BlockProblem& b = grp.prob[w.prob];
                 const bool amn = a_mn(b), bmn = b_mn(b);
                 const uint32_t idesc = idesc_bf16_f32(kBM * CG, BN, amn, bmn);
                 // MN-major: 16 reduction steps are 16 rows of 128 bytes, 64-element blocks 8 KiB apart;
@@ -722,6 +748,10 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
         uint32_t acc_phase = 0;
         UnitCursor cur;
         int l = 0;
+        stream_wait();
+        stream_release();
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x - 64; i < grp.zero_n; i += C::kThreads - 64) grp.zero_at[i] = 0u;
         for (int u = cur.next(grp.units, pair, pairs); u >= 0; u = cur.next(grp.units, pair, pairs)) {
             const Unit w = unit_of(grp, u, l);
             l = w.prob;

@@ -3,12 +3,13 @@ entropy of a linear head, each with its backward pass.
 
 Like the rest of the binding this module checks and marshals arguments; the computation is the
 library's.  Results are written to the tensors passed for them.  Tensors are contiguous and on the
-current device.  Workspace comes from PyTorch's allocator, on the stream that the call runs on.
+current device.  Workspace comes from PyTorch's allocator, for the stream that the call runs on.
 `include/forge.h` documents every operator's formulas, types and special cases.
 """
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import Any
 
 import torch
@@ -71,7 +72,7 @@ class _Shape:
     __slots__ = ("arg", "bytes")
 
     def __init__(self, struct):
-        self.arg, self.bytes = ctypes.byref(struct), {}  # workspace bytes by function, direction and device
+        self.arg, self.bytes = ctypes.byref(struct), {}  # workspace bytes by device and direction
 
 
 def _shape(cls, *values) -> _Shape:
@@ -84,23 +85,44 @@ def _shape(cls, *values) -> _Shape:
     return s
 
 
-def _workspace(shape: _Shape, name: str, dev: int, stream, *more):
-    """Pointer and size of a workspace as large as `name` answers for the shape, and the tensor that holds it,
-    from the memory pool of the stream that the call runs on."""
-    n = shape.bytes.get((name, dev, more))
+# Small workspaces are kept, one per host thread and stream: calls of one thread on one stream use them one
+# after another, and asking PyTorch's allocator costs as much host time as a small call's kernels take.
+# Captured calls take theirs from the graph's own pool, since a graph runs on streams of its own choosing.
+_KEEP = 16 << 20
+_kept = threading.local()
+
+
+def _workspace(shape: _Shape, name: str, dev: int, stream, raw: int, *more):
+    """Pointer and size of a workspace at least as large as `name` answers for the shape, and the tensor
+    that holds it."""
+    n = shape.bytes.get((dev, more))
     if n is None:
         n = getattr(_fg.lib(), name)(shape.arg, *more)
         if n >= 0:  # else the call itself says what is wrong
-            shape.bytes[(name, dev, more)] = n
+            shape.bytes[(dev, more)] = n
     if n <= 0:
-        return None, 0, None
+        return _NONE
     if stream is None:
-        t = torch.empty(n, dtype=torch.uint8, device=dev)
-    else:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_fg._stream(stream))
-        with torch.cuda.stream(s):
+        if n > _KEEP or torch._C._cuda_isCurrentStreamCapturing():
             t = torch.empty(n, dtype=torch.uint8, device=dev)
+            return t.data_ptr(), n, t
+        try:
+            kept = _kept.by_stream
+        except AttributeError:
+            kept = _kept.by_stream = {}
+        w = kept.get((dev, raw))
+        if w is None or w[1] < n:
+            size = min(_KEEP, max(2 * n, 1 << 20))
+            t = torch.empty(size, dtype=torch.uint8, device=dev)
+            w = kept[(dev, raw)] = (t.data_ptr(), size, t)
+        return w
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw)
+    with torch.cuda.stream(s):
+        t = torch.empty(n, dtype=torch.uint8, device=dev)
     return t.data_ptr(), n, t
+
+
+_NONE = (None, 0, None)
 
 
 def _device(x) -> int:
@@ -108,7 +130,7 @@ def _device(x) -> int:
     if not x.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
     dev = x.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on {x.device}, but the current device is cuda:{torch.cuda.current_device()}")
     return dev
 
@@ -185,13 +207,14 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias=None, add=
     T, D = rows = _matrix(x, "x")
     dt = x.dtype
     shape = _shape(NormShape, T, D, _one_of(NORM_KINDS, kind, "kind"), _type(x, "x"), _type(weight, "weight"), 0)
-    ws, n, _hold = _workspace(shape, "forge_layer_norm_backward_workspace", dev, stream)
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_layer_norm_backward_workspace", dev, stream, raw)
     st = _fg.lib().forge_layer_norm_backward(
         _take(dy, dt, rows, dev, "dy"), _take(x, dt, rows, dev, "x"),
         _take(weight, weight.dtype, (D,), dev, "weight"), _take(mean, _F32, (T,), dev, "mean"),
         _take(rstd, _F32, (T,), dev, "rstd"), _take(add, dt, rows, dev, "add"), _take(dx, dt, rows, dev, "dx"),
         _take(dweight, _F32, (D,), dev, "dweight"), _take(dbias, _F32, (D,), dev, "dbias"), ws, n, shape.arg,
-        _raw_stream(stream, dev))
+        raw)
     _fg._check(st, "forge_layer_norm_backward")
 
 
@@ -207,8 +230,9 @@ def gated_mlp(X, Wg, Wu, Wd, Y, G=None, U=None, residual=None, act: str = "silu"
     x, wg, wu = _take(X, _BF16, (T, D), dev, "X"), _take(Wg, _BF16, (F, D), dev, "Wg"), _take(Wu, _BF16, (F, D), dev, "Wu")
     wd, y, r = _take(Wd, _BF16, (D, F), dev, "Wd"), _take(Y, _BF16, (T, D), dev, "Y"), _take(residual, _BF16, (T, D), dev, "residual")
     g, u = _take(G, _BF16, (T, F), dev, "G"), _take(U, _BF16, (T, F), dev, "U")
-    ws, n, _hold = _workspace(shape, "forge_gated_mlp_workspace", dev, stream, 0)
-    _fg._check(_fg.lib().forge_gated_mlp(x, wg, wu, wd, r, y, g, u, ws, n, shape.arg, _raw_stream(stream, dev)),
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_gated_mlp_workspace", dev, stream, raw, 0)
+    _fg._check(_fg.lib().forge_gated_mlp(x, wg, wu, wd, r, y, g, u, ws, n, shape.arg, raw),
                "forge_gated_mlp")
 
 
@@ -220,8 +244,9 @@ def gated_mlp_backward(dY, X, G, U, Wg, Wu, Wd, dX, dWg, dWu, dWd, act: str = "s
     args = [_take(t, _BF16, s, dev, name) for t, s, name in (
         (dY, (T, D), "dY"), (X, (T, D), "X"), (G, (T, F), "G"), (U, (T, F), "U"), (Wg, (F, D), "Wg"), (Wu, (F, D), "Wu"),
         (Wd, (D, F), "Wd"), (dX, (T, D), "dX"), (dWg, (F, D), "dWg"), (dWu, (F, D), "dWu"), (dWd, (D, F), "dWd"))]
-    ws, n, _hold = _workspace(shape, "forge_gated_mlp_workspace", dev, stream, 1)
-    _fg._check(_fg.lib().forge_gated_mlp_backward(*args, ws, n, shape.arg, _raw_stream(stream, dev)),
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_gated_mlp_workspace", dev, stream, raw, 1)
+    _fg._check(_fg.lib().forge_gated_mlp_backward(*args, ws, n, shape.arg, raw),
                "forge_gated_mlp_backward")
 
 
@@ -243,10 +268,11 @@ def gated_mlp_backward_step(dY, X, G, U, gate, up, down, dX=None, act: str = "si
         layers.append(_fg.ForgeLayer(None, None, w, p(m), p(v), p(q), 0, 0, 0, int(seed) & (2**64 - 1)))
     if len(states) > 1:
         raise TypeError("the three layers must use the same state format")
-    ws, n, _hold = _workspace(shape, "forge_gated_mlp_workspace", dev, stream, 1)
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_gated_mlp_workspace", dev, stream, raw, 1)
     st = _fg.lib().forge_gated_mlp_backward_step(
         *args, *(ctypes.byref(a) for a in layers), _take(dX, _BF16, (T, D), dev, "dX"), ws, n, states.pop(),
-        _fg.OPT_KINDS[opt], _fg._hp_arg(hp), shape.arg, int(step), _raw_stream(stream, dev))
+        _fg.OPT_KINDS[opt], _fg._hp_arg(hp), shape.arg, int(step), raw)
     _fg._check(st, "forge_gated_mlp_backward_step")
 
 
@@ -262,8 +288,9 @@ def linear_cross_entropy(X, W, target, loss, lse, ignore_index: int = -100, stre
     shape = _shape(LossShape, T, V, D, int(ignore_index), 0)
     x, w, t = _take(X, _BF16, (T, D), dev, "X"), _take(W, _BF16, (V, D), dev, "W"), _take(target, torch.int64, (T,), dev, "target")
     out, l = _take(loss, _F32, (T,), dev, "loss"), _take(lse, _F32, (T,), dev, "lse")
-    ws, n, _hold = _workspace(shape, "forge_linear_cross_entropy_workspace", dev, stream, 0)
-    _fg._check(_fg.lib().forge_linear_cross_entropy(x, w, t, out, l, ws, n, shape.arg, _raw_stream(stream, dev)),
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_linear_cross_entropy_workspace", dev, stream, raw, 0)
+    _fg._check(_fg.lib().forge_linear_cross_entropy(x, w, t, out, l, ws, n, shape.arg, raw),
                "forge_linear_cross_entropy")
 
 
@@ -280,8 +307,9 @@ def linear_cross_entropy_backward(X, W, target, lse, dloss, dX, dW, ignore_index
     and the forward pass's lse."""
     dev, T, D, V, shape, args = _loss_gradient_args(X, W, target, lse, dloss, ignore_index)
     dx, dw = _take(dX, _BF16, (T, D), dev, "dX"), _take(dW, _BF16, (V, D), dev, "dW")
-    ws, n, _hold = _workspace(shape, "forge_linear_cross_entropy_workspace", dev, stream, 1)
-    st = _fg.lib().forge_linear_cross_entropy_backward(*args, dx, dw, ws, n, shape.arg, _raw_stream(stream, dev))
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_linear_cross_entropy_workspace", dev, stream, raw, 1)
+    st = _fg.lib().forge_linear_cross_entropy_backward(*args, dx, dw, ws, n, shape.arg, raw)
     _fg._check(st, "forge_linear_cross_entropy_backward")
 
 
@@ -292,8 +320,9 @@ def linear_cross_entropy_step(X, W, target, lse, dloss, dX=None, m=None, v=None,
     dev, T, D, V, shape, args = _loss_gradient_args(X, W, target, lse, dloss, ignore_index)
     dx, p = _take(dX, _BF16, (T, D), dev, "dX"), _fg._ptr
     _states(dev, W, m, v, qscales)
-    ws, n, _hold = _workspace(shape, "forge_linear_cross_entropy_workspace", dev, stream, 1)
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_linear_cross_entropy_workspace", dev, stream, raw, 1)
     st = _fg.lib().forge_linear_cross_entropy_step(
         *args, dx, p(m), p(v), p(qscales), ws, n, _fg._state_of(m, v), _fg.OPT_KINDS[opt], _fg._hp_arg(hp), shape.arg,
-        int(step), int(seed) & (2**64 - 1), _raw_stream(stream, dev))
+        int(step), int(seed) & (2**64 - 1), raw)
     _fg._check(st, "forge_linear_cross_entropy_step")
