@@ -389,7 +389,7 @@ forge_status run_store(const Machine& mc, const Plan& p, const Product* pr, char
         }
         b.a_mn = pr[i].a_mn;
         b.b_mn = pr[i].b_mn;
-        b.out = pr[i].out;
+        if (!pr[i].sum_out) FORGE_TRY(host::encode_result_map(&g.outs[i], pr[i].out, pr[i].cols, pr[i].rows, pr[i].cols));
         b.add = pr[i].add;
         b.sum = pr[i].sum;
         b.sum_in = pr[i].sum_in;
@@ -564,9 +564,8 @@ forge_status run_gated_dh(const Machine& mc, const GatedBackward& l, const void*
     b.ld = s.d_ff;
     b.g_in = static_cast<const uint16_t*>(G);
     b.u_in = static_cast<const uint16_t*>(U);
-    b.g_out = reinterpret_cast<uint16_t*>(ws + l.dg);
-    b.u_out = reinterpret_cast<uint16_t*>(ws + l.du);
-    b.h_out = reinterpret_cast<uint16_t*>(ws + l.h);
+    const int64_t outs[3] = {l.dg, l.du, l.h};
+    for (int i = 0; i < 3; ++i) FORGE_TRY(host::encode_result_map(&g.outs[i], ws + outs[i], s.d_ff, s.T, s.d_ff));
     b.act = s.act;
     FORGE_TRY(set_map(g, l.dh, 0, 0, Operand{dY, s.d_model, s.T, s.d_model}, false));
     FORGE_TRY(set_map(g, l.dh, 0, 1, Operand{Wd, s.d_ff, s.d_model, s.d_ff}, true));
@@ -678,7 +677,7 @@ forge_status run_loss_grad(const Machine& mc, const LossBackward& l, const LossP
     FORGE_TRY(fill_group(g, p.grad, mc, ws, l.split));
     BlockProblem& b = g.prob[0];
     b.kb[0] = slices(s.d_model);
-    b.out = reinterpret_cast<uint16_t*>(ws + l.g);
+    FORGE_TRY(host::encode_result_map(&g.outs[0], ws + l.g, p.ld, s.T, p.ld));
     b.ld = p.ld;
     b.target = target;
     b.v0 = p.v0;
@@ -843,9 +842,12 @@ forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, cons
     BlockProblem& b = g.prob[0];
     b.kb[0] = slices(s.d_model);
     b.ld = s.d_ff;
-    b.g_out = static_cast<uint16_t*>(G);
-    b.u_out = static_cast<uint16_t*>(U);
-    b.h_out = reinterpret_cast<uint16_t*>(ws + l.h);
+    b.keep = G != nullptr;
+    if (b.keep) {
+        FORGE_TRY(host::encode_result_map(&g.outs[0], G, s.d_ff, s.T, s.d_ff));
+        FORGE_TRY(host::encode_result_map(&g.outs[1], U, s.d_ff, s.T, s.d_ff));
+    }
+    FORGE_TRY(host::encode_result_map(&g.outs[2], ws + l.h, s.d_ff, s.T, s.d_ff));
     b.act = s.act;
     FORGE_TRY(set_map(g, l.up, 0, 0, Operand{X, s.d_model, s.T, s.d_model}, false));
     FORGE_TRY(set_map(g, l.up, 0, 1, Operand{Wg, s.d_model, s.d_ff, s.d_model}, false, true));

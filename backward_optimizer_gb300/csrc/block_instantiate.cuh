@@ -10,7 +10,7 @@ namespace forge {
 
 template <int BN, int CG, int EPI, int NP>
 cudaError_t block_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int units, cudaStream_t stream) {
-    using C = BlockCfg<BN, CG>;
+    using C = BlockCfg<BN, CG, EPI>;
     static std::atomic<uint64_t> configured{0};  // one bit per device ordinal
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);

@@ -63,7 +63,7 @@ enum BlockAct : int { kActSilu = 0, kActGeluTanh = 1, kActRelu = 2 };
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int BN, int CG>
+template <int BN, int CG, int EPI>
 struct BlockCfg {
     static_assert((BN == 256 && CG == 2) || ((BN == 128 || BN == 64) && CG == 1), "tile shapes");
     static constexpr int kBLoad = BN / CG;  // B rows (or columns) staged by this CTA
@@ -73,11 +73,14 @@ struct BlockCfg {
     static constexpr int kTmemCols = 2 * BN;
     static constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, half the columns each
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
-    static constexpr int kStages = BN == 64 ? 9 : 7;
+    // Two 2 KiB buffers per epilogue warp, 32 rows x 32 columns of bfloat16 each, on their way to memory.  The
+    // loss's statistics need none, and keep one stage more.
+    static constexpr int kStaging = EPI == kBlockLossStats ? 0 : kEpiWarps * 4096;
+    static constexpr int kStages = (7 * 32768 - kStaging) / kStageBytes;
     static constexpr int kRingBytes = kStages * kStageBytes;
     // where A has few rows (BlockGroup::a_rows) its slices are smaller and the ring holds more stages
     static constexpr int kMaxStages = BN == 64 ? 24 : CG == 1 ? 13 : kStages;
-    static constexpr int kSmemBytes = kRingBytes + 512 + 1024;  // barriers, alignment slack
+    static constexpr int kSmemBytes = kRingBytes + kStaging + 512 + 1024;  // barriers, alignment slack
     static_assert(kSmemBytes <= 232448, "shared memory");
     static constexpr int stages(int a_rows) {
         const int fit = kRingBytes / (a_rows * 128 + kBBytes);
@@ -96,19 +99,16 @@ struct BlockProblem {
     int a_flat, b_flat;   // MN-major and no multiple of 64 wide: (column, row, -) maps, a copy for each 64 columns
     int64_t part_base;    // where its split tiles' FP32 values start (floats)
     int count_base;       // and their counters
-    // kBlockStore: out [rows, ld] bf16; add: residual [rows, ld] or null; sum: FP32 [rows, cols] of
-    // earlier pieces, read if sum_in, written instead of out if sum_out
-    uint16_t* out;
+    // kBlockStore: add: residual [rows, ld] or null; sum: FP32 [rows, cols] of earlier pieces, read if
+    // sum_in, written instead of the result if sum_out
     const uint16_t* add;
     float* sum;
     int sum_in, sum_out;
     int64_t ld;
-    // gated: G, U, H / dG, dU [rows, cols] bf16
+    // gated backward: G, U [rows, cols] bf16; gated forward: whether G and U are wanted
     const uint16_t* g_in;
     const uint16_t* u_in;
-    uint16_t* g_out;
-    uint16_t* u_out;
-    uint16_t* h_out;
+    int keep;
     int act;
     // loss: columns are vocabulary entries v0 .. v0 + cols - 1
     const int64_t* target;
@@ -134,6 +134,8 @@ struct BlockGroup {
     int a_rows;
     BlockProblem prob[NP];
     CUtensorMap maps[4 * NP];  // per product: A, B of the first pair, A, B of the second
+    // results: kBlockStore's out of each product; G, U, H; dG, dU, H; kBlockLossGrad's g
+    CUtensorMap outs[NP > 3 ? NP : 3];
     float* parts;
     // Arrival counters of split tiles: zero before the launch, and zero again after it (the last arrival
     // resets its own).  zero_n: counters, from zero_at, that this launch clears for the stream's next ones.
@@ -219,33 +221,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // ---------------------------------------------------------------- rows of bfloat16 in memory
 
-// 2 W columns of one row, packed in pairs; `left`: columns from here to the end of the row (stored or
-// loaded in runs of 8); wide: the row's address is a multiple of 32 bytes at every 16th column
-template <int W>
-__device__ __forceinline__ void store_run(uint16_t* p, const uint32_t (&v)[W], int left, bool wide) {
+// 32 columns of one row, packed in pairs; `left`: columns from here to the end of the row (loaded in runs
+// of 8); wide: the row's address is a multiple of 32 bytes at every 16th column
+__device__ __forceinline__ void load_run(const uint16_t* p, uint32_t (&v)[16], int left, bool wide) {
 #pragma unroll
-    for (int h = 0; h < W / 8; ++h) {
-        if (wide && left >= 16 * h + 16) {
-            const uint32_t r[8] = {v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3],
-                                   v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]};
-            st_v8(p + 16 * h, r);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (left >= 16 * h + 8 * q + 8) {
-                    const uint32_t r[4] = {v[8 * h + 4 * q], v[8 * h + 4 * q + 1], v[8 * h + 4 * q + 2],
-                                           v[8 * h + 4 * q + 3]};
-                    st_v4(p + 16 * h + 8 * q, r);
-                }
-            }
-        }
-    }
-}
-
-template <int W>
-__device__ __forceinline__ void load_run(const uint16_t* p, uint32_t (&v)[W], int left, bool wide) {
-#pragma unroll
-    for (int h = 0; h < W / 8; ++h) {
+    for (int h = 0; h < 2; ++h) {
         if (wide && left >= 16 * h + 16) {
             uint32_t r[8];
             ld_v8(p + 16 * h, r);
@@ -263,6 +243,33 @@ __device__ __forceinline__ void load_run(const uint16_t* p, uint32_t (&v)[W], in
     }
 }
 
+// A warp's results on their way to memory: 32 rows x 32 columns of bfloat16 at a time, each lane its row,
+// through shared memory and a tiled store that writes whole row pieces and leaves out what lies past the
+// last row or column.  Stores by the lanes themselves, one row each, take 32 passes through the L1 for 32
+// rows and set the pace of tiles with short reductions (4637 tokens, 80 wide, through d_ff = 7224: 138 us).
+struct WarpOut {
+    uint32_t buf;  // two buffers, 1024-byte aligned
+    int turn;
+    __device__ __forceinline__ void put(const CUtensorMap* map, const uint32_t (&v)[16], int col, int row0) {
+        const uint32_t lane = threadIdx.x & 31u;
+        if (lane == 0) bulk_wait_read<1>();  // the buffer's last store has read it
+        __syncwarp();
+        const uint32_t at = buf + (static_cast<uint32_t>(turn) << 11);
+        turn ^= 1;
+        // the 64-byte swizzle: 16-byte piece j of row r lies at piece j ^ ((r / 2) mod 4)
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j)
+            st_shared_v4(at + lane * 64u + ((j ^ ((lane >> 1) & 3u)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2],
+                         v[4 * j + 3]);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(map, at, col, row0);
+            bulk_commit();
+        }
+    }
+};
+
 // ---------------------------------------------------------------- the accumulator a warp reads
 // Column `c` of the tile, 32 at a time, for this thread's row: from TMEM, or the sum of a split
 // tile's parts.
@@ -274,10 +281,6 @@ struct AccTmem {
         tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(c), g);
         tmem_ld_wait(g);
     }
-    __device__ __forceinline__ void load(int c, uint32_t (&g)[16]) const {
-        __syncwarp();
-        tmem_ld_16(taddr + static_cast<uint32_t>(c), g);
-    }
 };
 
 struct AccParts {
@@ -285,38 +288,40 @@ struct AccParts {
     size_t step;     // floats from part to part
     int parts;
     bool valid;      // rows past the output's last left nothing in memory
-    template <int N>
-    __device__ __forceinline__ void load(int c, uint32_t (&g)[N]) const {
-        float s[N];
+    __device__ __forceinline__ void load(int c, uint32_t (&g)[32]) const {
+        float s[32];
 #pragma unroll
-        for (int j = 0; j < N; ++j) s[j] = valid ? __ldcg(p + static_cast<size_t>(c + j) * 32) : 0.0f;
+        for (int j = 0; j < 32; ++j) s[j] = valid ? __ldcg(p + static_cast<size_t>(c + j) * 32) : 0.0f;
         for (int k = 1; k < parts; ++k) {
 #pragma unroll
-            for (int j = 0; j < N; ++j)
+            for (int j = 0; j < 32; ++j)
                 s[j] = __fadd_rn(s[j], valid ? __ldcg(p + k * step + static_cast<size_t>(c + j) * 32) : 0.0f);
         }
 #pragma unroll
-        for (int j = 0; j < N; ++j) g[j] = __float_as_uint(s[j]);
+        for (int j = 0; j < 32; ++j) g[j] = __float_as_uint(s[j]);
     }
 };
 
 // ---------------------------------------------------------------- epilogues
-// `row`: this thread's output row; h: the half of the tile's columns that the warp owns.
+// `row`: this thread's output row; h: the half of the tile's columns that the warp owns; out: its way to
+// memory; maps: the results'.  A warp whose first row is past the output's last does nothing.
+
+__device__ __forceinline__ int warp_row0(int row) { return row - static_cast<int>(threadIdx.x & 31u); }
 
 template <int BN, class Acc>
-__device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
-    const bool wide = (b.ld & 15) == 0;
+__device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc, int row, int nb, int h, WarpOut& out,
+                                          const CUtensorMap* map) {
+    if (warp_row0(row) >= b.rows) return;
+    const bool wide = (b.ld & 15) == 0, mine = row < b.rows;
 #pragma unroll 1
     for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
         const int col = nb * BN + c, left = b.cols - col;
         if (left <= 0) break;  // the same for the whole warp
-        const bool mine = row < b.rows;
         uint32_t add[16];
         if (b.add != nullptr && mine) load_run(b.add + static_cast<size_t>(row) * b.ld + col, add, left, wide);
         uint32_t g[32];
         acc.load(c, g);
-        if (!mine) continue;
-        if (b.sum_in) {
+        if (b.sum_in && mine) {
             const float* s = b.sum + static_cast<size_t>(row) * b.cols + col;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -328,12 +333,14 @@ __device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc,
             }
         }
         if (b.sum_out) {
-            float* s = b.sum + static_cast<size_t>(row) * b.cols + col;
+            if (mine) {
+                float* s = b.sum + static_cast<size_t>(row) * b.cols + col;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t r[8] = {g[8 * q], g[8 * q + 1], g[8 * q + 2], g[8 * q + 3],
-                                       g[8 * q + 4], g[8 * q + 5], g[8 * q + 6], g[8 * q + 7]};
-                if (left >= 8 * q + 8) st_v8(s + 8 * q, r);
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t r[8] = {g[8 * q], g[8 * q + 1], g[8 * q + 2], g[8 * q + 3],
+                                           g[8 * q + 4], g[8 * q + 5], g[8 * q + 6], g[8 * q + 7]};
+                    if (left >= 8 * q + 8) st_v8(s + 8 * q, r);
+                }
             }
             continue;
         }
@@ -342,7 +349,7 @@ __device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc,
 #pragma unroll
             for (int j = 0; j < 32; ++j) g[j] = __float_as_uint(__fmul_rn(__uint_as_float(g[j]), unit));
         }
-        if (b.add != nullptr) {
+        if (b.add != nullptr && mine) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 g[2 * j] = __float_as_uint(__fadd_rn(__uint_as_float(g[2 * j]), bf16_lo(add[j])));
@@ -352,32 +359,31 @@ __device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc,
         uint32_t o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2_rn(g[2 * j], g[2 * j + 1]);
-        store_run(b.out + static_cast<size_t>(row) * b.ld + col, o, left, wide);
+        out.put(map, o, col, warp_row0(row));
     }
 }
 
 template <int BN, class Acc>
-__device__ __forceinline__ void epi_gated_fwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
-    const bool wide = (b.cols & 15) == 0;
+__device__ __forceinline__ void epi_gated_fwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h, WarpOut& out,
+                                              const CUtensorMap* maps) {
+    if (warp_row0(row) >= b.rows) return;
     // 64-wide tiles: one warp of a lane quarter takes all 32 columns
     constexpr int kCols = BN == 64 ? 32 : BN / 4;
 #pragma unroll 1
     for (int c = h * kCols; c < (h + 1) * kCols && c < BN / 2; c += 32) {
-        const int col = nb * (BN / 2) + c, left = b.cols - col;
-        if (left <= 0) break;
+        const int col = nb * (BN / 2) + c;
+        if (b.cols - col <= 0) break;
         uint32_t g[32], u[32];
         acc.load(c, g);
         acc.load(BN / 2 + c, u);
-        if (row >= b.rows) continue;
-        const size_t at = static_cast<size_t>(row) * b.cols + col;
         uint32_t o[16];
-        if (b.g_out != nullptr) {
+        if (b.keep) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2_rn(g[2 * j], g[2 * j + 1]);
-            store_run(b.g_out + at, o, left, wide);
+            out.put(&maps[0], o, col, warp_row0(row));
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2_rn(u[2 * j], u[2 * j + 1]);
-            store_run(b.u_out + at, o, left, wide);
+            out.put(&maps[1], o, col, warp_row0(row));
         }
         // H is rounded to bfloat16, the type of the next product's operand
 #pragma unroll
@@ -386,35 +392,32 @@ __device__ __forceinline__ void epi_gated_fwd(const BlockProblem& b, const Acc& 
             const float a1 = act_value(__uint_as_float(g[2 * j + 1]), b.act) * __uint_as_float(u[2 * j + 1]);
             o[j] = pack_bf16x2_rn(__float_as_uint(a0), __float_as_uint(a1));
         }
-        store_run(b.h_out + at, o, left, wide);
+        out.put(&maps[2], o, col, warp_row0(row));
     }
 }
 
-// G and U are read, and dG, dU and H written, by the thread that owns the element: dG and dU may lie
-// where G and U do.
 template <int BN, class Acc>
-__device__ __forceinline__ void epi_gated_bwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
-    const bool wide = (b.cols & 15) == 0;
-    // Columns at a time: on single CTAs, which serve small calls, half as many: a launch's first pass through
-    // the arithmetic waits for its instructions
-    constexpr int kStep = BN == 256 ? 32 : 16;
+__device__ __forceinline__ void epi_gated_bwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h, WarpOut& out,
+                                              const CUtensorMap* maps) {
+    if (warp_row0(row) >= b.rows) return;
+    const bool wide = (b.cols & 15) == 0, mine = row < b.rows;
 #pragma unroll 1
-    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += kStep) {
+    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
         const int col = nb * BN + c, left = b.cols - col;
         if (left <= 0) break;
-        const bool mine = row < b.rows;
         const size_t at = static_cast<size_t>(row) * b.cols + col;
-        uint32_t g[kStep / 2], u[kStep / 2];
+        uint32_t g[16], u[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) g[j] = u[j] = 0u;
         if (mine) {
             load_run(b.g_in + at, g, left, wide);
             load_run(b.u_in + at, u, left, wide);
         }
-        uint32_t d[kStep];
+        uint32_t d[32];
         acc.load(c, d);
-        if (!mine) continue;
-        uint32_t o[kStep / 2];
+        uint32_t o[16];
 #pragma unroll
-        for (int j = 0; j < kStep / 2; ++j) {
+        for (int j = 0; j < 16; ++j) {
             float a0, s0, a1, s1;
             act_both(bf16_lo(g[j]), b.act, a0, s0);
             act_both(bf16_hi(g[j]), b.act, a1, s1);
@@ -424,9 +427,9 @@ __device__ __forceinline__ void epi_gated_bwd(const BlockProblem& b, const Acc& 
             u[j] = pack_bf16x2_rn(__float_as_uint(d0 * a0), __float_as_uint(d1 * a1));
             o[j] = pack_bf16x2_rn(__float_as_uint(a0 * u0), __float_as_uint(a1 * u1));
         }
-        store_run(b.g_out + at, g, left, wide);
-        store_run(b.u_out + at, u, left, wide);
-        store_run(b.h_out + at, o, left, wide);
+        out.put(&maps[0], g, col, warp_row0(row));
+        out.put(&maps[1], u, col, warp_row0(row));
+        out.put(&maps[2], o, col, warp_row0(row));
     }
 }
 
@@ -480,8 +483,10 @@ __device__ __forceinline__ void epi_loss_stats(const BlockProblem& b, const Acc&
 }
 
 template <int BN, class Acc>
-__device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
-    const bool mine = row < b.rows, wide = (b.ld & 15) == 0;
+__device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& acc, int row, int nb, int h, WarpOut& out,
+                                              const CUtensorMap* maps) {
+    if (warp_row0(row) >= b.rows) return;
+    const bool mine = row < b.rows;
     const int64_t t = mine ? b.target[row] : -1;
     const bool counts = t != b.ignore;
     const float shift = mine ? -b.lse[row] * kLog2e : 0.0f;
@@ -498,7 +503,6 @@ __device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& 
         if (left <= 0) break;
         uint32_t g[32];
         acc.load(c, g);
-        if (!mine) continue;
         const int64_t off = t - (first + c);
         const int at = off >= 0 && off < 32 ? static_cast<int>(off) : -1;
         uint32_t o[16];
@@ -509,17 +513,18 @@ __device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& 
             const F2 v = mul2(F2::of(at == 2 * j ? p0 - 1.0f : p0, at == 2 * j + 1 ? p1 - 1.0f : p1), F2::all(scale));
             o[j] = counts ? pack_bf16x2_rn(__float_as_uint(v.lo()), __float_as_uint(v.hi())) : 0u;
         }
-        store_run(b.out + static_cast<size_t>(row) * b.ld + nb * BN + c, o, left, wide);
+        out.put(&maps[0], o, nb * BN + c, warp_row0(row));
     }
 }
 
 template <int BN, int EPI, class Acc>
-__device__ __forceinline__ void block_epilogue(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
-    if constexpr (EPI == kBlockStore) epi_store<BN>(b, acc, row, nb, h);
-    else if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, acc, row, nb, h);
-    else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, acc, row, nb, h);
+__device__ __forceinline__ void block_epilogue(const BlockProblem& b, const Acc& acc, int row, int nb, int h, WarpOut& out,
+                                               const CUtensorMap* maps) {
+    if constexpr (EPI == kBlockStore) epi_store<BN>(b, acc, row, nb, h, out, maps);
+    else if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, acc, row, nb, h, out, maps);
+    else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, acc, row, nb, h, out, maps);
     else if constexpr (EPI == kBlockLossStats) epi_loss_stats<BN>(b, acc, row, nb, h);
-    else epi_loss_grad<BN>(b, acc, row, nb, h);
+    else epi_loss_grad<BN>(b, acc, row, nb, h, out, maps);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -543,9 +548,9 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int stages, uint64_t 
 }
 
 template <int BN, int CG, int EPI, int NP>
-__global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
+__global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
     forge_block_kernel(const __grid_constant__ BlockGroup<NP> grp) {
-    using C = BlockCfg<BN, CG>;
+    using C = BlockCfg<BN, CG, EPI>;
     constexpr bool kGated = EPI == kBlockGatedFwd;
     constexpr int kColsPerTile = kGated ? BN / 2 : BN;
     extern __shared__ uint8_t smem_raw[];
@@ -556,7 +561,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
     const uint32_t stage_bytes = static_cast<uint32_t>(a_rows) * 128u + C::kBBytes;
     uint8_t* sA = smem;
     uint8_t* sB = smem + n_stages * a_rows * 128;  // behind A: the MMA's reads past A's rows stay inside the ring
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRingBytes);
+    uint8_t* staging = smem + C::kRingBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + C::kStaging);
     uint64_t* empty = full + C::kMaxStages;
     uint64_t* acc_full = empty + C::kMaxStages;
     uint64_t* acc_empty = acc_full + 2;
@@ -746,6 +752,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
         const AbortCtx ab_acc{abort_flag, grp.status, grp.acc_wait_limit_ns};
         int acc = 0;
         uint32_t acc_phase = 0;
+        WarpOut out{smem_addr(staging) + static_cast<uint32_t>(e) * 4096u, 0};
         UnitCursor cur;
         int l = 0;
         stream_wait();
@@ -763,7 +770,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const AccTmem tm{tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN)};
-            if (w.split < 0) block_epilogue<BN, EPI>(b, tm, row, w.nb, half);
+            const CUtensorMap* maps = EPI == kBlockStore ? &grp.outs[l] : grp.outs;
+            if (w.split < 0) block_epilogue<BN, EPI>(b, tm, row, w.nb, half, out, maps);
             // [split tile][part][CTA][lane quarter][column][lane]
             const size_t step = static_cast<size_t>(CG) * 4 * BN * 32;
             const size_t own = (static_cast<size_t>(rank) * 4 + quarter) * BN * 32 + lane;
@@ -807,10 +815,11 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG>::kThreads, 1)
                     if (lane == 0) *count = 0u;
                     const AccParts sum{grp.parts + b.part_base + static_cast<size_t>(w.split) * b.parts * step + own,
                                        step, b.parts, row < b.rows};
-                    block_epilogue<BN, EPI>(b, sum, row, w.nb, half);
+                    block_epilogue<BN, EPI>(b, sum, row, w.nb, half, out, maps);
                 }
             }
         }
+        if (lane == 0 && C::kStaging > 0) bulk_wait_read<0>();  // shared memory stays until the last stores have read it
     }
 
     tc_fence_before();

@@ -8,6 +8,6 @@ cudaError_t forge::block_pairs(int num_sms, int* pairs) {
     cudaLaunchAttribute attr[2];
     cudaError_t err = block_config<256, 2, kBlockStore, kMaxProducts>(cfg, attr, num_sms, nullptr);
     if (err != cudaSuccess) return err;
-    // every epilogue has the same shared memory and one CTA per SM, so one count serves all
+    // every epilogue has one CTA per SM, so one count serves all
     return cudaOccupancyMaxActiveClusters(pairs, forge_block_kernel<256, 2, kBlockStore, kMaxProducts>, &cfg);
 }
