@@ -18,6 +18,7 @@ namespace {
 
 using forge::BlockGroup;
 using forge::BlockProblem;
+using forge::PairGroup;
 using forge::kMaxProducts;
 namespace host = forge::host;
 
@@ -78,103 +79,134 @@ struct Plan {
 // it saves.
 constexpr int kMinSlices = 8;
 constexpr int kMaxParts = 16;
-constexpr int kTailSlices = 32;
 // the epilogue of a tile, in slices of the mainloop: only to weigh units against one another
 constexpr int kEpiSlices = 8;
 
-// Tile shape.  Pairs on 256 x 256 tiles move half the operand bytes per product of single CTAs on
-// 128 x 128 tiles, so they are taken unless they would leave half of the SMs idle, or every tile's second
-// 128 rows empty.  Single CTAs take 128 x 64 tiles where 128 x 128 would leave half of the SMs idle, but
-// not where all rows fit one tile: there the time is the weights' way from memory, and the smaller copies
-// keep less of it in flight (one token, 4096/14336: 102 us on 128 x 64 tiles against 78).
-int pick_width(const Plan& p, const Machine& mc, bool gated) {
-    auto tiles_of = [&](int bn) {
-        const int64_t tm = bn == 256 ? 256 : 128, tn = bn / (gated ? 2 : 1);
-        int64_t n = 0;
-        for (int i = 0; i < p.n; ++i) n += ceil_div(p.cut[i].rows, tm) * ceil_div(p.cut[i].cols, tn);
-        return n;
-    };
-    bool tall = false;
-    for (int i = 0; i < p.n; ++i) tall = tall || p.cut[i].rows > 128;
-    if (tall && 2 * tiles_of(256) > mc.pairs) return 256;
-    return tall && 2 * tiles_of(128) <= mc.dev.num_sms ? 64 : 128;
+// Tile shapes and what they cost, in slices (some 0.27 us whatever the tile: the copies set the pace):
+// `epi`: a tile's epilogue and change of accumulator, which run beside the next tile's slices and are its
+// least time; `last`: the last tile's epilogue, beyond the narrowest tile's; a split tile's join: `join` and
+// `per_part` for each part.  Wide tiles need fewer slices for the same product, narrow ones fill the GPU with
+// less and end sooner.  The numbers are a fit to 1200 timings of products from 5 to 5366 rows, each with
+// every shape and several cuts; the plan below then comes within 1 % of the best shape and cut on average.
+// 256 tokens, 4096/14336, down product: 89 us on 256, 99 on 128, 123 on 64 columns.  256 tokens,
+// 1024/2816, dX and the weight gradients: 41.5 / 35.1 / 41.  256 tokens, 256/512: 24.5 / 20 / 18.
+struct TileCost {
+    int bn, epi, last, join, per_part;
+};
+constexpr TileCost kTiles[] = {{256, 8, 13, 8, 12}, {128, 8, 3, 6, 5}, {64, 6, 1, 10, 2}};
+
+int64_t tiles_of(const Cut& c, int bn, bool gated) {
+    return ceil_div(c.rows, bn == 256 ? 256 : 128) * ceil_div(c.cols, bn / (gated ? 2 : 1));
+}
+
+struct Choice {
+    double t;
+    int bn, parts, length;
+    void offer(double time, int width, int n_parts, int part_length) {
+        // equal times: the wider tile and fewer parts, which come first, read less
+        if (bn == 0 || time < 0.98 * t) *this = Choice{time, width, n_parts, part_length};
+    }
+};
+
+// One product: its full waves, then the last one's tiles, whole or cut into parts that fill the GPU.
+Choice choose_one(const Cut& c, const Machine& mc, bool gated) {
+    Choice best{};
+    for (const TileCost& k : kTiles) {
+        const int64_t width = k.bn == 256 ? mc.pairs : mc.dev.num_sms;
+        const int64_t tiles = tiles_of(c, k.bn, gated), full = tiles / width, rest = tiles % width;
+        const int64_t wave = std::max(c.kb, k.epi);
+        best.offer(static_cast<double>((ceil_div(tiles, width) - 1) * wave + c.kb + k.last), k.bn, 1, c.kb);
+        for (int parts = 2; rest > 0 && parts <= kMaxParts && c.kb >= kMinSlices * parts && rest * parts <= width; ++parts)
+            best.offer(static_cast<double>(full * wave + ceil_div(c.kb, parts) + k.last + k.join + k.per_part * parts),
+                       k.bn, parts, c.kb);
+    }
+    return best;
+}
+
+int parts_of(const Cut& c, int length) {
+    return std::max(1, std::min({static_cast<int>(ceil_div(c.kb, length)), kMaxParts, c.kb / kMinSlices}));
+}
+
+// Several products: the call lasts as long as its longest unit, or as an even share of all work.  For each
+// tile shape, units are cut to the length at which the larger of the two is smallest; a unit's time: its slices,
+// or its epilogue where that is longer; a part's sums cost it a little more.
+Choice choose_many(const Cut* cut, int n, const Machine& mc) {
+    Choice best{};
+    int kb_max = 0;
+    for (int i = 0; i < n; ++i) kb_max = std::max(kb_max, cut[i].kb);
+    for (const TileCost& k : kTiles) {
+        const int width = k.bn == 256 ? mc.pairs : mc.dev.num_sms;
+        double least = 0, time = 0;
+        int cut_to = kb_max;
+        for (int cuts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            const int length = static_cast<int>(ceil_div(kb_max, cuts));
+            double longest = 0, work = 0;
+            int most = 1;
+            for (int i = 0; i < n; ++i) {
+                const int parts = parts_of(cut[i], length);
+                const double unit = std::max<double>(static_cast<double>(cut[i].kb) / parts, kEpiSlices) + (parts > 1 ? 3 : 1);
+                longest = std::max(longest, unit);
+                work += unit * parts * tiles_of(cut[i], k.bn, false);
+                most = std::max(most, parts);
+            }
+            const double t = std::max(longest, work / width);
+            if (cuts == 1 || t < 0.97 * least) {
+                // joins run beside other units' slices, but not all the way
+                const double join = most > 1 ? k.join + k.per_part * most : 0;
+                least = t;
+                time = std::max(longest + join / 2, work / width) + k.last;
+                cut_to = length;
+            }
+        }
+        best.offer(time, k.bn, 0, cut_to);
+    }
+    return best;
+}
+
+// Choices of recent sizes, per host thread: working one out takes as much host time as a small kernel, and
+// the sizes alone determine it.
+struct ChoiceSlot {
+    int64_t key[3 * kMaxProducts + 3];
+    Choice choice;
+    bool used;
+};
+constexpr int kChoiceSlots = 64;
+thread_local ChoiceSlot t_choices[kChoiceSlots];
+
+Choice choose(const Plan& p, const Machine& mc, bool gated) {
+    int64_t key[3 * kMaxProducts + 3] = {p.n * 2 + gated, mc.pairs, mc.dev.num_sms};
+    uint64_t h = static_cast<uint64_t>(key[0]);
+    for (int i = 0; i < p.n; ++i) {
+        const int64_t size[3] = {p.cut[i].rows, p.cut[i].cols, p.cut[i].kb};
+        for (int j = 0; j < 3; ++j) {
+            key[3 + 3 * i + j] = size[j];
+            h = (h ^ static_cast<uint64_t>(size[j])) * 0x9E3779B97F4A7C15ull;
+        }
+    }
+    ChoiceSlot& slot = t_choices[(h >> 32) % kChoiceSlots];
+    if (!slot.used || std::memcmp(slot.key, key, sizeof key) != 0) {
+        slot.choice = p.n == 1 ? choose_one(p.cut[0], mc, gated) : choose_many(p.cut, p.n, mc);
+        std::memcpy(slot.key, key, sizeof key);
+        slot.used = true;
+    }
+    return slot.choice;
 }
 
 void plan_products(Plan& p, const Machine& mc, bool gated, bool a_k_major) {
-    p.bn = pick_width(p, mc, gated);
+    const Choice choice = choose(p, mc, gated);
+    p.bn = choice.bn;
     const bool pair = p.bn == 256;
     p.width = pair ? mc.pairs : mc.dev.num_sms;
     p.a_rows = 128;
     if (p.n == 1 && !pair && a_k_major && p.cut[0].rows <= 64) p.a_rows = static_cast<int>(round_up(p.cut[0].rows, 8));
     const int64_t tm = pair ? 256 : 128, tn = p.bn / (gated ? 2 : 1);
-    int64_t tiles = 0;
     for (int i = 0; i < p.n; ++i) {
         Cut& c = p.cut[i];
         c.tiles_m = static_cast<int>(ceil_div(c.rows, tm));
         c.tiles_n = static_cast<int>(ceil_div(c.cols, tn));
-        c.parts = 1;
-        c.split_from = c.tiles_m * c.tiles_n;
-        tiles += c.split_from;
-    }
-    if (p.n == 1 && tiles < p.width) {
-        // fewer tiles than pairs: cut each so that the units' waves are shortest
-        Cut& c = p.cut[0];
-        int64_t best = c.kb + kEpiSlices;
-        for (int parts = 2; parts <= kMaxParts && c.kb >= kMinSlices * parts; ++parts) {
-            // each further part adds a trip to memory to the join, some slices' time (8 tokens through
-            // 1024/2816 23.2 us with this term at 4 a part, 25.5 with 1)
-            const int64_t t = ceil_div(tiles * parts, p.width) * (ceil_div(c.kb, parts) + kEpiSlices) + 4 * parts;
-            if (t < best) {
-                best = t;
-                c.parts = parts;
-                c.split_from = 0;
-            }
-        }
-    } else if (p.n == 1) {
-        // a last wave that would leave half of the pairs idle or more is cut so that it fills them, where
-        // that shortens the call by more slices than the join of the parts takes (2048 tokens backward
-        // through 2048/5632 208 us without a cut that saves 16 slices, 224 with it)
-        Cut& c = p.cut[0];
-        const int t = c.tiles_m * c.tiles_n, rest = t % p.width;
-        if (rest > 0 && 2 * rest <= p.width) {
-            const int parts = std::min({p.width / rest, 4, c.kb / kMinSlices});
-            if (parts > 1 && c.kb - c.kb / parts >= kTailSlices) {
-                c.parts = parts;
-                c.split_from = t - rest;
-            }
-        }
-    } else {
-        // The call lasts about as long as its longest unit, or as an even share of all work: units are cut
-        // to the length at which the larger of the two is smallest.  A unit's time: its slices, or its
-        // epilogue where that is longer; a part's sums cost it a little more.
-        auto parts_for = [&](const Cut& c, int length) {
-            return std::max(1, std::min({static_cast<int>(ceil_div(c.kb, length)), kMaxParts, c.kb / kMinSlices}));
-        };
-        int kb_max = 0;
-        for (int i = 0; i < p.n; ++i) kb_max = std::max(kb_max, p.cut[i].kb);
-        double best = 0;
-        int best_length = kb_max;
-        for (int cuts : {1, 2, 3, 4, 6, 8, 12, 16}) {
-            const int length = static_cast<int>(ceil_div(kb_max, cuts));
-            double longest = 0, work = 0;
-            for (int i = 0; i < p.n; ++i) {
-                const Cut& c = p.cut[i];
-                const int parts = parts_for(c, length);
-                const double unit = std::max<double>(static_cast<double>(c.kb) / parts, kEpiSlices) + (parts > 1 ? 3 : 1);
-                longest = std::max(longest, unit);
-                work += unit * parts * c.tiles_m * c.tiles_n;
-            }
-            const double t = std::max(longest, work / p.width);
-            if (cuts == 1 || t < 0.97 * best) {
-                best = t;
-                best_length = length;
-            }
-        }
-        for (int i = 0; i < p.n; ++i) {
-            Cut& c = p.cut[i];
-            c.parts = parts_for(c, best_length);
-            if (c.parts > 1) c.split_from = 0;
-        }
+        c.parts = p.n == 1 ? choice.parts : parts_of(c, choice.length);
+        const int tiles = c.tiles_m * c.tiles_n;
+        c.split_from = c.parts == 1 ? tiles : p.n == 1 ? tiles - tiles % p.width : 0;
     }
     p.part_floats = 0;
     p.counts = 0;
@@ -301,27 +333,32 @@ struct MapSlot {
 constexpr int kMapSlots = 128;
 thread_local MapSlot t_maps[kMapSlots];
 
-// The map of an operand of which a CTA stages `extent` rows (K-major) or columns (MN-major) per slice, one
-// box a slice; or two boxes of 64 columns where the operand's width is no multiple of 64 (flat).
-forge_status operand_map(CUtensorMap* map, const Operand& o, bool mn, int extent) {
-    const MapKey key{o.base, o.cols, o.rows, o.ld, mn, extent};
-    uint64_t h = reinterpret_cast<uintptr_t>(o.base) * 0x9E3779B97F4A7C15ull;
-    h ^= static_cast<uint64_t>(o.cols) * 0xC2B2AE3D27D4EB4Full ^ static_cast<uint64_t>(o.rows) * 0x165667B19E3779F9ull;
-    h ^= static_cast<uint64_t>(o.ld * 1024 + extent * 2 + mn) * 0x85EBCA77C2B2AE63ull;
+template <class Encode>
+forge_status kept_map(CUtensorMap* map, const MapKey& key, Encode&& encode) {
+    uint64_t h = reinterpret_cast<uintptr_t>(key.base) * 0x9E3779B97F4A7C15ull;
+    h ^= static_cast<uint64_t>(key.cols) * 0xC2B2AE3D27D4EB4Full ^ static_cast<uint64_t>(key.rows) * 0x165667B19E3779F9ull;
+    h ^= static_cast<uint64_t>(key.ld * 1024 + key.extent * 2 + key.mn) * 0x85EBCA77C2B2AE63ull;
     MapSlot& slot = t_maps[(h >> 32) % kMapSlots];
     if (slot.used && slot.key == key) {
         *map = slot.map;
         return FORGE_OK;
     }
-    const uint64_t cols = static_cast<uint64_t>(o.cols), rows = static_cast<uint64_t>(o.rows);
-    const uint64_t pitch = static_cast<uint64_t>(o.ld) * 2;
-    forge_status st;
-    if (mn && o.cols % 64 == 0)
-        st = host::encode_map(map, o.base, {64, rows, cols / 64}, {pitch, 128}, {64, 64, static_cast<uint32_t>(extent / 64)});
-    else
-        st = host::encode_map(map, o.base, {cols, rows, 1}, {pitch, pitch}, {64, mn ? 64u : static_cast<uint32_t>(extent), 1});
+    const forge_status st = encode();
     if (st == FORGE_OK) slot = MapSlot{key, *map, true};
     return st;
+}
+
+// The map of an operand of which a CTA stages `extent` rows (K-major) or columns (MN-major) per slice, one
+// box a slice; or two boxes of 64 columns where the operand's width is no multiple of 64 (flat).
+forge_status operand_map(CUtensorMap* map, const Operand& o, bool mn, int extent) {
+    const MapKey key{o.base, o.cols, o.rows, o.ld, mn, extent};
+    return kept_map(map, key, [&] {
+        const uint64_t cols = static_cast<uint64_t>(o.cols), rows = static_cast<uint64_t>(o.rows);
+        const uint64_t pitch = static_cast<uint64_t>(o.ld) * 2;
+        if (mn && o.cols % 64 == 0)
+            return host::encode_map(map, o.base, {64, rows, cols / 64}, {pitch, 128}, {64, 64, static_cast<uint32_t>(extent / 64)});
+        return host::encode_map(map, o.base, {cols, rows, 1}, {pitch, pitch}, {64, mn ? 64u : static_cast<uint32_t>(extent), 1});
+    });
 }
 
 // Map i of product l of a group (BlockGroup::maps).
@@ -333,8 +370,17 @@ forge_status set_map(BlockGroup<NP>& g, const Plan& p, int l, int i, const Opera
     return operand_map(&g.maps[4 * l + i], o, mn, extent);
 }
 
-template <int EPI, int NP>
-forge_status launch(const BlockGroup<NP>& g, const Plan& p, cudaStream_t stream) {
+// Result i of a group, [rows, cols] in one piece (PairGroup::outs; an operand's extent is never 0).
+template <int EPI>
+forge_status set_result(PairGroup<EPI>& g, const Plan& p, int i, void* base, int64_t cols, int64_t rows) {
+    g.to[i] = static_cast<uint16_t*>(base);
+    if (!forge::staged(EPI) || p.bn != 256) return FORGE_OK;
+    return kept_map(&g.outs[i], MapKey{base, cols, rows, cols, 0, 0},
+                    [&] { return host::encode_result_map(&g.outs[i], base, cols, rows); });
+}
+
+template <int EPI>
+forge_status launch(const PairGroup<EPI>& g, const Plan& p, cudaStream_t stream) {
     host::count_launch();
     return cuda_status(forge::launch_block<EPI>(&g, p.bn, std::min(p.width, g.units.n_units), stream));
 }
@@ -376,7 +422,7 @@ Plan plan_store(const Machine& mc, Product* pr, int n) {
 // pr: in the order that plan_store left them in
 forge_status run_store(const Machine& mc, const Plan& p, const Product* pr, char* ws, const SplitSpace& sp,
                        cudaStream_t stream) {
-    BlockGroup<kMaxProducts> g;
+    PairGroup<forge::kBlockStore> g;
     std::memset(&g, 0, sizeof(g));
     FORGE_TRY(fill_group(g, p, mc, ws, sp));
     for (int i = 0; i < p.n; ++i) {
@@ -389,7 +435,7 @@ forge_status run_store(const Machine& mc, const Plan& p, const Product* pr, char
         }
         b.a_mn = pr[i].a_mn;
         b.b_mn = pr[i].b_mn;
-        if (!pr[i].sum_out) FORGE_TRY(host::encode_result_map(&g.outs[i], pr[i].out, pr[i].cols, pr[i].rows, pr[i].cols));
+        if (!pr[i].sum_out) FORGE_TRY(set_result(g, p, i, pr[i].out, pr[i].cols, pr[i].rows));
         b.add = pr[i].add;
         b.sum = pr[i].sum;
         b.sum_in = pr[i].sum_in;
@@ -555,7 +601,7 @@ GatedBackward layout_gated_backward(const Machine& mc, const forge_gated_shape& 
 
 forge_status run_gated_dh(const Machine& mc, const GatedBackward& l, const void* dY, const void* Wd, const void* G,
                           const void* U, char* ws, const forge_gated_shape& s, cudaStream_t stream) {
-    BlockGroup<1> g;
+    PairGroup<forge::kBlockGatedBwd> g;
     std::memset(&g, 0, sizeof(g));
     FORGE_TRY(fill_group(g, l.dh, mc, ws, l.split));
     FORGE_TRY(clear_counts(g, l.dh, ws, l.split, stream));
@@ -565,7 +611,7 @@ forge_status run_gated_dh(const Machine& mc, const GatedBackward& l, const void*
     b.g_in = static_cast<const uint16_t*>(G);
     b.u_in = static_cast<const uint16_t*>(U);
     const int64_t outs[3] = {l.dg, l.du, l.h};
-    for (int i = 0; i < 3; ++i) FORGE_TRY(host::encode_result_map(&g.outs[i], ws + outs[i], s.d_ff, s.T, s.d_ff));
+    for (int i = 0; i < 3; ++i) FORGE_TRY(set_result(g, l.dh, i, ws + outs[i], s.d_ff, s.T));
     b.act = s.act;
     FORGE_TRY(set_map(g, l.dh, 0, 0, Operand{dY, s.d_model, s.T, s.d_model}, false));
     FORGE_TRY(set_map(g, l.dh, 0, 1, Operand{Wd, s.d_ff, s.d_model, s.d_ff}, true));
@@ -672,12 +718,12 @@ LossBackward layout_loss_backward(const Machine& mc, const forge_loss_shape& s, 
 forge_status run_loss_grad(const Machine& mc, const LossBackward& l, const LossPiece& p, const forge_loss_shape& s,
                            const void* X, const void* W, const int64_t* target, const float* lse, const float* dloss,
                            char* ws, cudaStream_t stream) {
-    BlockGroup<1> g;
+    PairGroup<forge::kBlockLossGrad> g;
     std::memset(&g, 0, sizeof(g));
     FORGE_TRY(fill_group(g, p.grad, mc, ws, l.split));
     BlockProblem& b = g.prob[0];
     b.kb[0] = slices(s.d_model);
-    FORGE_TRY(host::encode_result_map(&g.outs[0], ws + l.g, p.ld, s.T, p.ld));
+    FORGE_TRY(set_result(g, p.grad, 0, ws + l.g, p.ld, s.T));
     b.ld = p.ld;
     b.target = target;
     b.v0 = p.v0;
@@ -835,7 +881,7 @@ forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, cons
         d.weights_ready = 1;
         return cuda_status(forge::launch_rows(d, false, mc.dev.num_sms, stream));
     }
-    BlockGroup<1> g;
+    PairGroup<forge::kBlockGatedFwd> g;
     std::memset(&g, 0, sizeof(g));
     FORGE_TRY(fill_group(g, l.up, mc, ws, l.split));
     FORGE_TRY(clear_counts(g, l.up, ws, l.split, stream));
@@ -844,10 +890,10 @@ forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, cons
     b.ld = s.d_ff;
     b.keep = G != nullptr;
     if (b.keep) {
-        FORGE_TRY(host::encode_result_map(&g.outs[0], G, s.d_ff, s.T, s.d_ff));
-        FORGE_TRY(host::encode_result_map(&g.outs[1], U, s.d_ff, s.T, s.d_ff));
+        FORGE_TRY(set_result(g, l.up, 0, G, s.d_ff, s.T));
+        FORGE_TRY(set_result(g, l.up, 1, U, s.d_ff, s.T));
     }
-    FORGE_TRY(host::encode_result_map(&g.outs[2], ws + l.h, s.d_ff, s.T, s.d_ff));
+    FORGE_TRY(set_result(g, l.up, 2, ws + l.h, s.d_ff, s.T));
     b.act = s.act;
     FORGE_TRY(set_map(g, l.up, 0, 0, Operand{X, s.d_model, s.T, s.d_model}, false));
     FORGE_TRY(set_map(g, l.up, 0, 1, Operand{Wg, s.d_model, s.d_ff, s.d_model}, false, true));
@@ -947,7 +993,7 @@ forge_status forge_linear_cross_entropy(const void* X, const void* W, const int6
     const LossForward l = layout_loss_forward(mc, s);
     FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     char* ws = static_cast<char*>(workspace);
-    BlockGroup<1> g;
+    PairGroup<forge::kBlockLossStats> g;
     std::memset(&g, 0, sizeof(g));
     FORGE_TRY(fill_group(g, l.plan, mc, ws, l.split));
     FORGE_TRY(clear_counts(g, l.plan, ws, l.split, stream));

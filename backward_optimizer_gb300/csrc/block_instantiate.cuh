@@ -8,7 +8,7 @@
 
 namespace forge {
 
-template <int BN, int CG, int EPI, int NP>
+template <int BN, int CG, int EPI>
 cudaError_t block_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int units, cudaStream_t stream) {
     using C = BlockCfg<BN, CG, EPI>;
     static std::atomic<uint64_t> configured{0};  // one bit per device ordinal
@@ -17,7 +17,7 @@ cudaError_t block_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2]
     if (err != cudaSuccess) return err;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
-        err = cudaFuncSetAttribute(forge_block_kernel<BN, CG, EPI, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        err = cudaFuncSetAttribute(forge_block_kernel<BN, CG, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    C::kSmemBytes);
         if (err != cudaSuccess) return err;
         configured.fetch_or(bit);
@@ -39,12 +39,11 @@ cudaError_t block_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2]
 
 template <int BN, int CG, int EPI>
 cudaError_t launch_block_as(const void* group, int units, cudaStream_t stream) {
-    constexpr int NP = EPI == kBlockStore ? kMaxProducts : 1;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cudaError_t err = block_config<BN, CG, EPI, NP>(cfg, attr, units, stream);
+    cudaError_t err = block_config<BN, CG, EPI>(cfg, attr, units, stream);
     if (err != cudaSuccess) return err;
-    return cudaLaunchKernelEx(&cfg, forge_block_kernel<BN, CG, EPI, NP>, *static_cast<const BlockGroup<NP>*>(group));
+    return cudaLaunchKernelEx(&cfg, forge_block_kernel<BN, CG, EPI>, static_cast<const GroupOf<CG, EPI>&>(*static_cast<const PairGroup<EPI>*>(group)));
 }
 
 template <int EPI>

@@ -52,7 +52,9 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
+#include "block_launch.h"
 #include "pairs.cuh"
 #include "tile_kernel.cuh"
 
@@ -62,6 +64,9 @@ enum BlockEpi : int { kBlockStore = 0, kBlockGatedFwd = 1, kBlockGatedBwd = 2, k
 enum BlockAct : int { kActSilu = 0, kActGeluTanh = 1, kActRelu = 2 };
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// Whether an epilogue's results go to memory through shared memory, on pairs (WarpOut).
+constexpr bool staged(int epi) { return epi == kBlockGatedFwd || epi == kBlockLossGrad; }
 
 template <int BN, int CG, int EPI>
 struct BlockCfg {
@@ -73,9 +78,8 @@ struct BlockCfg {
     static constexpr int kTmemCols = 2 * BN;
     static constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, half the columns each
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
-    // Two 2 KiB buffers per epilogue warp, 32 rows x 32 columns of bfloat16 each, on their way to memory.  The
-    // loss's statistics need none, and keep one stage more.
-    static constexpr int kStaging = EPI == kBlockLossStats ? 0 : kEpiWarps * 4096;
+    // two 2 KiB buffers per epilogue warp, 32 rows x 32 columns of bfloat16 each, on their way to memory
+    static constexpr int kStaging = CG == 2 && staged(EPI) ? kEpiWarps * 4096 : 0;
     static constexpr int kStages = (7 * 32768 - kStaging) / kStageBytes;
     static constexpr int kRingBytes = kStages * kStageBytes;
     // where A has few rows (BlockGroup::a_rows) its slices are smaller and the ring holds more stages
@@ -121,31 +125,42 @@ struct BlockProblem {
     const float* unit;
 };
 
-// Up to NP products, the one with the longest units first.
+// Up to NP products, the one with the longest units first.  What every role reads at its start comes first.
 template <int NP>
 struct BlockGroup {
     int n;
-    UnitPlan units;
     // Rows of A that a stage holds: 128, or on single CTAs with one row of tiles the rows there are, rounded
     // up to a multiple of 8 (A's tensor maps have boxes of that many rows then).  The MMA reads 128 rows
     // whatever lies in the rest of the stage: an accumulator row depends on its own row of A alone, and rows
     // past the output's last are not used.  One token's X or H would otherwise be copied as 64 rows of zero
     // fill, as many bytes as the weights beside it.
     int a_rows;
-    BlockProblem prob[NP];
-    CUtensorMap maps[4 * NP];  // per product: A, B of the first pair, A, B of the second
-    // results: kBlockStore's out of each product; G, U, H; dG, dU, H; kBlockLossGrad's g
-    CUtensorMap outs[NP > 3 ? NP : 3];
+    UnitPlan units;
+    int zero_n;
+    int* status;
+    uint64_t wait_limit_ns, acc_wait_limit_ns;
     float* parts;
     // Arrival counters of split tiles: zero before the launch, and zero again after it (the last arrival
     // resets its own).  zero_n: counters, from zero_at, that this launch clears for the stream's next ones.
     uint32_t* counts;
     uint32_t* zero_at;
-    int zero_n;
-    int* status;
-    uint64_t wait_limit_ns, acc_wait_limit_ns;
     int withhold_first_stage;  // test switch, as TileArgs::withhold_first_stage
+    // results: kBlockStore's out of each product; G, U, H; dG, dU, H; kBlockLossGrad's g
+    uint16_t* to[NP > 3 ? NP : 3];
+    BlockProblem prob[NP];
+    CUtensorMap maps[4 * NP];  // per product: A, B of the first pair, A, B of the second
 };
+
+constexpr int products_of(int epi) { return epi == kBlockStore ? kMaxProducts : 1; }
+
+// The results' maps besides, for pairs whose epilogue is staged.  Other launches go without: a small call's
+// time shows every parameter (256 tokens through 256/512: 13.0 us with them, 12.75 without).
+template <int EPI>
+struct PairGroup : BlockGroup<products_of(EPI)> {
+    CUtensorMap outs[EPI == kBlockGatedFwd ? 3 : 1];
+};
+template <int CG, int EPI>
+using GroupOf = std::conditional_t<CG == 2 && staged(EPI), PairGroup<EPI>, BlockGroup<products_of(EPI)>>;
 
 struct Unit {
     int prob, mb, nb, part, split;  // split: which split tile of the product, or -1
@@ -221,11 +236,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // ---------------------------------------------------------------- rows of bfloat16 in memory
 
-// 32 columns of one row, packed in pairs; `left`: columns from here to the end of the row (loaded in runs
+// 2 W columns of one row, packed in pairs; `left`: columns from here to the end of the row (loaded in runs
 // of 8); wide: the row's address is a multiple of 32 bytes at every 16th column
-__device__ __forceinline__ void load_run(const uint16_t* p, uint32_t (&v)[16], int left, bool wide) {
+template <int W>
+__device__ __forceinline__ void load_run(const uint16_t* p, uint32_t (&v)[W], int left, bool wide) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < W / 8; ++h) {
         if (wide && left >= 16 * h + 16) {
             uint32_t r[8];
             ld_v8(p + 16 * h, r);
@@ -243,29 +259,68 @@ __device__ __forceinline__ void load_run(const uint16_t* p, uint32_t (&v)[16], i
     }
 }
 
-// A warp's results on their way to memory: 32 rows x 32 columns of bfloat16 at a time, each lane its row,
-// through shared memory and a tiled store that writes whole row pieces and leaves out what lies past the
-// last row or column.  Stores by the lanes themselves, one row each, take 32 passes through the L1 for 32
-// rows and set the pace of tiles with short reductions (4637 tokens, 80 wide, through d_ff = 7224: 138 us).
+// A warp's results on their way to memory: 32 rows x 32 columns of bfloat16 at a time, each lane its row.
+// Staged, they go through shared memory and a tiled store, which writes whole row pieces and leaves out what
+// lies past the last row or column: stores by the lanes themselves, one row each, take 32 passes through the
+// L1 for 32 rows and set the pace of tiles with short reductions and much to write (forward, 4637 tokens, 80
+// wide, through d_ff = 7224: 138 us with them, 119 so; 8192 tokens through 5120/17408: 2760 and 2715; the
+// loss's gradient, 4096 x 32768, 128 wide: 174 and 170).  It costs a stage of the ring, which launches
+// where operands from memory set the pace (gradients of 256 and 512 tokens through 4096/14336: 202 and 292 us
+// so, 195.5 and 285 by the lanes), and single CTAs, which small calls have, some 0.5 us.
+template <bool kStaged>
 struct WarpOut {
-    uint32_t buf;  // two buffers, 1024-byte aligned
+    const CUtensorMap* maps;
+    uint16_t* const* to;
+    int64_t ld;  // the results' width
+    int rows;
+    uint32_t buf;  // staged: two buffers, 1024-byte aligned
     int turn;
-    __device__ __forceinline__ void put(const CUtensorMap* map, const uint32_t (&v)[16], int col, int row0) {
+    // result i, its columns from col on
+    template <int W>
+    __device__ __forceinline__ void put(int i, const uint32_t (&v)[W], int col, int row0) {
         const uint32_t lane = threadIdx.x & 31u;
-        if (lane == 0) bulk_wait_read<1>();  // the buffer's last store has read it
-        __syncwarp();
-        const uint32_t at = buf + (static_cast<uint32_t>(turn) << 11);
-        turn ^= 1;
-        // the 64-byte swizzle: 16-byte piece j of row r lies at piece j ^ ((r / 2) mod 4)
+        if constexpr (kStaged) {
+            static_assert(W == 16);
+            if (lane == 0) bulk_wait_read<1>();  // the buffer's last store has read it
+            __syncwarp();
+            const uint32_t at = buf + (static_cast<uint32_t>(turn) << 11);
+            turn ^= 1;
+            // the 64-byte swizzle: 16-byte piece j of row r lies at piece j ^ ((r / 2) mod 4)
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j)
-            st_shared_v4(at + lane * 64u + ((j ^ ((lane >> 1) & 3u)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2],
-                         v[4 * j + 3]);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(map, at, col, row0);
-            bulk_commit();
+            for (uint32_t j = 0; j < 4; ++j)
+                st_shared_v4(at + lane * 64u + ((j ^ ((lane >> 1) & 3u)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2],
+                             v[4 * j + 3]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(&maps[i], at, col, row0);
+                bulk_commit();
+            }
+        } else if (row0 + static_cast<int>(lane) < rows) {
+            uint16_t* p = to[i] + (static_cast<size_t>(row0) + lane) * ld + col;
+            const int left = static_cast<int>(ld) - col;
+            const bool wide = (ld & 15) == 0;
+#pragma unroll
+            for (int h = 0; h < W / 8; ++h) {
+                if (wide && left >= 16 * h + 16) {
+                    const uint32_t r[8] = {v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3],
+                                           v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]};
+                    st_v8(p + 16 * h, r);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t r[4] = {v[8 * h + 4 * q], v[8 * h + 4 * q + 1], v[8 * h + 4 * q + 2],
+                                               v[8 * h + 4 * q + 3]};
+                        if (left >= 16 * h + 8 * q + 8) st_v4(p + 16 * h + 8 * q, r);
+                    }
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void end() {
+        // shared memory stays until the last stores have read it
+        if constexpr (kStaged) {
+            if ((threadIdx.x & 31u) == 0) bulk_wait_read<0>();
         }
     }
 };
@@ -281,6 +336,10 @@ struct AccTmem {
         tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(c), g);
         tmem_ld_wait(g);
     }
+    __device__ __forceinline__ void load(int c, uint32_t (&g)[16]) const {
+        __syncwarp();
+        tmem_ld_16(taddr + static_cast<uint32_t>(c), g);
+    }
 };
 
 struct AccParts {
@@ -288,29 +347,45 @@ struct AccParts {
     size_t step;     // floats from part to part
     int parts;
     bool valid;      // rows past the output's last left nothing in memory
-    __device__ __forceinline__ void load(int c, uint32_t (&g)[32]) const {
-        float s[32];
+    template <int N>
+    __device__ __forceinline__ void load(int c, uint32_t (&g)[N]) const {
+        // two parts' loads are in flight at once: a trip to the L2 takes longer than all of a part's adds
+        float s[N], n[N];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[j] = valid ? __ldcg(p + static_cast<size_t>(c + j) * 32) : 0.0f;
-        for (int k = 1; k < parts; ++k) {
+        for (int j = 0; j < N; ++j) s[j] = valid ? __ldcg(p + static_cast<size_t>(c + j) * 32) : 0.0f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                s[j] = __fadd_rn(s[j], valid ? __ldcg(p + k * step + static_cast<size_t>(c + j) * 32) : 0.0f);
+        for (int j = 0; j < N; ++j) n[j] = valid ? __ldcg(p + step + static_cast<size_t>(c + j) * 32) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) s[j] = __fadd_rn(s[j], n[j]);
+        for (int k = 2; k < parts; k += 2) {
+            const bool both = valid && k + 1 < parts;
+            float m[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) n[j] = valid ? __ldcg(p + k * step + static_cast<size_t>(c + j) * 32) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < N; ++j) m[j] = both ? __ldcg(p + (k + 1) * step + static_cast<size_t>(c + j) * 32) : -0.0f;
+#pragma unroll
+            for (int j = 0; j < N; ++j) s[j] = __fadd_rn(__fadd_rn(s[j], n[j]), m[j]);
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) g[j] = __float_as_uint(s[j]);
+        for (int j = 0; j < N; ++j) g[j] = __float_as_uint(s[j]);
     }
 };
 
 // ---------------------------------------------------------------- epilogues
 // `row`: this thread's output row; h: the half of the tile's columns that the warp owns; out: its way to
-// memory; maps: the results'.  A warp whose first row is past the output's last does nothing.
+// memory.  A warp whose first row is past the output's last does nothing.
+
+// Columns at a time where the arithmetic is long: on single CTAs, which serve small calls, half as many, since
+// a launch's first pass through it waits for its instructions (256 tokens through 256/512: 12.75 us with 32
+// columns, 11.8 with 16; its gradients 18.6 and 17.5; a loss of 130 x 4099: 9.6 and 9.2).
+template <int BN>
+constexpr int kEpiStep = BN == 256 ? 32 : 16;
 
 __device__ __forceinline__ int warp_row0(int row) { return row - static_cast<int>(threadIdx.x & 31u); }
 
-template <int BN, class Acc>
-__device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc, int row, int nb, int h, WarpOut& out,
-                                          const CUtensorMap* map) {
+template <int BN, class Acc, class Out>
+__device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc, int row, int nb, int h, Out& out) {
     if (warp_row0(row) >= b.rows) return;
     const bool wide = (b.ld & 15) == 0, mine = row < b.rows;
 #pragma unroll 1
@@ -359,65 +434,63 @@ __device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc,
         uint32_t o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2_rn(g[2 * j], g[2 * j + 1]);
-        out.put(map, o, col, warp_row0(row));
+        out.put(0, o, col, warp_row0(row));
     }
 }
 
-template <int BN, class Acc>
-__device__ __forceinline__ void epi_gated_fwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h, WarpOut& out,
-                                              const CUtensorMap* maps) {
+template <int BN, class Acc, class Out>
+__device__ __forceinline__ void epi_gated_fwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h, Out& out) {
     if (warp_row0(row) >= b.rows) return;
-    // 64-wide tiles: one warp of a lane quarter takes all 32 columns
-    constexpr int kCols = BN == 64 ? 32 : BN / 4;
+    constexpr int kCols = BN / 4, kStep = kEpiStep<BN>;
 #pragma unroll 1
-    for (int c = h * kCols; c < (h + 1) * kCols && c < BN / 2; c += 32) {
+    for (int c = h * kCols; c < (h + 1) * kCols; c += kStep) {
         const int col = nb * (BN / 2) + c;
         if (b.cols - col <= 0) break;
-        uint32_t g[32], u[32];
+        uint32_t g[kStep], u[kStep];
         acc.load(c, g);
         acc.load(BN / 2 + c, u);
-        uint32_t o[16];
+        uint32_t o[kStep / 2];
         if (b.keep) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2_rn(g[2 * j], g[2 * j + 1]);
-            out.put(&maps[0], o, col, warp_row0(row));
+            for (int j = 0; j < kStep / 2; ++j) o[j] = pack_bf16x2_rn(g[2 * j], g[2 * j + 1]);
+            out.put(0, o, col, warp_row0(row));
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2_rn(u[2 * j], u[2 * j + 1]);
-            out.put(&maps[1], o, col, warp_row0(row));
+            for (int j = 0; j < kStep / 2; ++j) o[j] = pack_bf16x2_rn(u[2 * j], u[2 * j + 1]);
+            out.put(1, o, col, warp_row0(row));
         }
         // H is rounded to bfloat16, the type of the next product's operand
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < kStep / 2; ++j) {
             const float a0 = act_value(__uint_as_float(g[2 * j]), b.act) * __uint_as_float(u[2 * j]);
             const float a1 = act_value(__uint_as_float(g[2 * j + 1]), b.act) * __uint_as_float(u[2 * j + 1]);
             o[j] = pack_bf16x2_rn(__float_as_uint(a0), __float_as_uint(a1));
         }
-        out.put(&maps[2], o, col, warp_row0(row));
+        out.put(2, o, col, warp_row0(row));
     }
 }
 
-template <int BN, class Acc>
-__device__ __forceinline__ void epi_gated_bwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h, WarpOut& out,
-                                              const CUtensorMap* maps) {
+template <int BN, class Acc, class Out>
+__device__ __forceinline__ void epi_gated_bwd(const BlockProblem& b, const Acc& acc, int row, int nb, int h, Out& out) {
     if (warp_row0(row) >= b.rows) return;
     const bool wide = (b.cols & 15) == 0, mine = row < b.rows;
+    constexpr int kStep = kEpiStep<BN>;
 #pragma unroll 1
-    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
+    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += kStep) {
         const int col = nb * BN + c, left = b.cols - col;
         if (left <= 0) break;
         const size_t at = static_cast<size_t>(row) * b.cols + col;
-        uint32_t g[16], u[16];
+        uint32_t g[kStep / 2], u[kStep / 2];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) g[j] = u[j] = 0u;
+        for (int j = 0; j < kStep / 2; ++j) g[j] = u[j] = 0u;
         if (mine) {
             load_run(b.g_in + at, g, left, wide);
             load_run(b.u_in + at, u, left, wide);
         }
-        uint32_t d[32];
+        uint32_t d[kStep];
         acc.load(c, d);
-        uint32_t o[16];
+        uint32_t o[kStep / 2];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < kStep / 2; ++j) {
             float a0, s0, a1, s1;
             act_both(bf16_lo(g[j]), b.act, a0, s0);
             act_both(bf16_hi(g[j]), b.act, a1, s1);
@@ -427,9 +500,9 @@ __device__ __forceinline__ void epi_gated_bwd(const BlockProblem& b, const Acc& 
             u[j] = pack_bf16x2_rn(__float_as_uint(d0 * a0), __float_as_uint(d1 * a1));
             o[j] = pack_bf16x2_rn(__float_as_uint(a0 * u0), __float_as_uint(a1 * u1));
         }
-        out.put(&maps[0], g, col, warp_row0(row));
-        out.put(&maps[1], u, col, warp_row0(row));
-        out.put(&maps[2], o, col, warp_row0(row));
+        out.put(0, g, col, warp_row0(row));
+        out.put(1, u, col, warp_row0(row));
+        out.put(2, o, col, warp_row0(row));
     }
 }
 
@@ -443,34 +516,35 @@ __device__ __forceinline__ void epi_loss_stats(const BlockProblem& b, const Acc&
     const int64_t t = mine ? b.target[row] : -1;
     const int64_t first = b.v0 + static_cast<int64_t>(nb) * BN;  // vocabulary entry of the tile's column 0
     float m = -INFINITY, s = 0.0f;
+    constexpr int kStep = kEpiStep<BN>;
 #pragma unroll 1
-    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
+    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += kStep) {
         const int left = b.cols - (nb * BN + c);
         if (left <= 0) break;
-        uint32_t g[32];
+        uint32_t g[kStep];
         acc.load(c, g);
         const int64_t at = t - (first + c);
-        if (at >= 0 && at < 32 && t < b.vocab) {
+        if (at >= 0 && at < kStep && t < b.vocab) {
             float lt = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) lt = at == j ? __uint_as_float(g[j]) : lt;
+            for (int j = 0; j < kStep; ++j) lt = at == j ? __uint_as_float(g[j]) : lt;
             b.target_logit[row] = lt;
         }
-        if (left < 32) {
+        if (left < kStep) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) g[j] = j < left ? g[j] : __float_as_uint(-INFINITY);
+            for (int j = 0; j < kStep; ++j) g[j] = j < left ? g[j] : __float_as_uint(-INFINITY);
         }
         float top[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(g[k]);
 #pragma unroll
-        for (int j = 4; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(g[j]));
+        for (int j = 4; j < kStep; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(g[j]));
         const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e);
         const float base = mn == -INFINITY ? 0.0f : mn;
         const F2 scale = F2::all(kLog2e), less = F2::all(-base);
         F2 e[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < kStep / 2; ++j) {
             const F2 x = fma2(F2::of(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1])), scale, less);
             const F2 y = F2::of(exp2_fast(x.lo()), exp2_fast(x.hi()));
             e[j & 3] = j < 4 ? y : add2(e[j & 3], y);
@@ -482,9 +556,8 @@ __device__ __forceinline__ void epi_loss_stats(const BlockProblem& b, const Acc&
     if (mine) b.stats[static_cast<size_t>(2 * nb + h) * b.rows + row] = make_float2(m, s);
 }
 
-template <int BN, class Acc>
-__device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& acc, int row, int nb, int h, WarpOut& out,
-                                              const CUtensorMap* maps) {
+template <int BN, class Acc, class Out>
+__device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& acc, int row, int nb, int h, Out& out) {
     if (warp_row0(row) >= b.rows) return;
     const bool mine = row < b.rows;
     const int64_t t = mine ? b.target[row] : -1;
@@ -513,18 +586,17 @@ __device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& 
             const F2 v = mul2(F2::of(at == 2 * j ? p0 - 1.0f : p0, at == 2 * j + 1 ? p1 - 1.0f : p1), F2::all(scale));
             o[j] = counts ? pack_bf16x2_rn(__float_as_uint(v.lo()), __float_as_uint(v.hi())) : 0u;
         }
-        out.put(&maps[0], o, nb * BN + c, warp_row0(row));
+        out.put(0, o, nb * BN + c, warp_row0(row));
     }
 }
 
-template <int BN, int EPI, class Acc>
-__device__ __forceinline__ void block_epilogue(const BlockProblem& b, const Acc& acc, int row, int nb, int h, WarpOut& out,
-                                               const CUtensorMap* maps) {
-    if constexpr (EPI == kBlockStore) epi_store<BN>(b, acc, row, nb, h, out, maps);
-    else if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, acc, row, nb, h, out, maps);
-    else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, acc, row, nb, h, out, maps);
+template <int BN, int EPI, class Acc, class Out>
+__device__ __forceinline__ void block_epilogue(const BlockProblem& b, const Acc& acc, int row, int nb, int h, Out& out) {
+    if constexpr (EPI == kBlockStore) epi_store<BN>(b, acc, row, nb, h, out);
+    else if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, acc, row, nb, h, out);
+    else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, acc, row, nb, h, out);
     else if constexpr (EPI == kBlockLossStats) epi_loss_stats<BN>(b, acc, row, nb, h);
-    else epi_loss_grad<BN>(b, acc, row, nb, h, out, maps);
+    else epi_loss_grad<BN>(b, acc, row, nb, h, out);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -547,9 +619,9 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int stages, uint64_t 
     }
 }
 
-template <int BN, int CG, int EPI, int NP>
+template <int BN, int CG, int EPI>
 __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
-    forge_block_kernel(const __grid_constant__ BlockGroup<NP> grp) {
+    forge_block_kernel(const __grid_constant__ GroupOf<CG, EPI> grp) {
     using C = BlockCfg<BN, CG, EPI>;
     constexpr bool kGated = EPI == kBlockGatedFwd;
     constexpr int kColsPerTile = kGated ? BN / 2 : BN;
@@ -752,7 +824,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
         const AbortCtx ab_acc{abort_flag, grp.status, grp.acc_wait_limit_ns};
         int acc = 0;
         uint32_t acc_phase = 0;
-        WarpOut out{smem_addr(staging) + static_cast<uint32_t>(e) * 4096u, 0};
+        WarpOut<(C::kStaging > 0)> out{nullptr, grp.to, 0, 0, smem_addr(staging) + static_cast<uint32_t>(e) * 4096u, 0};
+        if constexpr (C::kStaging > 0) out.maps = grp.outs;
         UnitCursor cur;
         int l = 0;
         stream_wait();
@@ -770,8 +843,12 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const AccTmem tm{tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN)};
-            const CUtensorMap* maps = EPI == kBlockStore ? &grp.outs[l] : grp.outs;
-            if (w.split < 0) block_epilogue<BN, EPI>(b, tm, row, w.nb, half, out, maps);
+            if constexpr (EPI == kBlockStore) {
+                out.to = &grp.to[l];
+            }
+            out.ld = b.ld;
+            out.rows = b.rows;
+            if (w.split < 0) block_epilogue<BN, EPI>(b, tm, row, w.nb, half, out);
             // [split tile][part][CTA][lane quarter][column][lane]
             const size_t step = static_cast<size_t>(CG) * 4 * BN * 32;
             const size_t own = (static_cast<size_t>(rank) * 4 + quarter) * BN * 32 + lane;
@@ -779,17 +856,17 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                 float* p = grp.parts + b.part_base +
                            (static_cast<size_t>(w.split) * b.parts + w.part) * step + own;
                 // the columns whose epilogue this warp runs: gate and up columns come from both halves
-                constexpr int kRuns = kGated ? 2 : 1, kRun = kGated && BN == 64 ? 32 : BN / 2 / kRuns;
+                constexpr int kRuns = kGated ? 2 : 1, kRun = BN / 2 / kRuns, kStep = kRun < 32 ? kRun : 32;
 #pragma unroll 1
                 for (int r = 0; r < kRuns; ++r) {
 #pragma unroll 1
-                    for (int c = 0; c < kRun && half * kRun + c < BN / kRuns; c += 32) {
+                    for (int c = 0; c < kRun; c += kStep) {
                         const int at = r * (BN / 2) + half * kRun + c;
-                        uint32_t g[32];
+                        uint32_t g[kStep];
                         tm.load(at, g);
                         if (row < b.rows) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
+                            for (int j = 0; j < kStep; ++j)
                                 __stcg(p + static_cast<size_t>(at + j) * 32, __uint_as_float(g[j]));
                         }
                     }
@@ -815,11 +892,11 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                     if (lane == 0) *count = 0u;
                     const AccParts sum{grp.parts + b.part_base + static_cast<size_t>(w.split) * b.parts * step + own,
                                        step, b.parts, row < b.rows};
-                    block_epilogue<BN, EPI>(b, sum, row, w.nb, half, out, maps);
+                    block_epilogue<BN, EPI>(b, sum, row, w.nb, half, out);
                 }
             }
         }
-        if (lane == 0 && C::kStaging > 0) bulk_wait_read<0>();  // shared memory stays until the last stores have read it
+        out.end();
     }
 
     tc_fence_before();

@@ -7,13 +7,12 @@
 
 namespace forge {
 
-template <int NP> struct BlockGroup;
 struct RowsArgs;
 
 constexpr int kMaxProducts = 4;  // products of one kBlockStore launch
 
 // One launch of EPI on CTA pairs with 256 x 256 tiles (bn = 256) or single CTAs with 128 x bn tiles (128,
-// 64); group: a BlockGroup<kMaxProducts> for kBlockStore, a BlockGroup<1> for the others; units: pairs or CTAs.
+// 64); group: a PairGroup<EPI>; units: pairs or CTAs.
 template <int EPI> cudaError_t launch_block(const void* group, int bn, int units, cudaStream_t stream);
 
 // CTA pairs that the current device runs at once.

@@ -607,9 +607,9 @@ forge_status encode_map(CUtensorMap* map, const void* base, const uint64_t (&dim
                : FORGE_ERR_CUDA;
 }
 
-forge_status encode_result_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t ld) {
+forge_status encode_result_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows) {
     const cuuint64_t d[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t st[1] = {static_cast<cuuint64_t>(ld * 2)};
+    const cuuint64_t st[1] = {static_cast<cuuint64_t>(cols * 2)};
     const cuuint32_t bx[2] = {32, 32}, one[2] = {1, 1};
     return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d, st, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,

@@ -25,9 +25,9 @@ forge_status device(Device* out);
 forge_status encode_map(CUtensorMap* map, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
                         const uint32_t (&box)[3]);
 
-// Tensor map of a row-major bfloat16 result [rows, cols], rows `ld` elements apart, written in boxes of 32 x 32
-// with the 64-byte swizzle.
-forge_status encode_result_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t ld);
+// Tensor map of a row-major bfloat16 result [rows, cols] in one piece, written in boxes of 32 x 32 with the
+// 64-byte swizzle.
+forge_status encode_result_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows);
 
 uint64_t wait_limit_ns();
 uint64_t acc_wait_limit_ns(int64_t k_blocks);

@@ -126,6 +126,27 @@ def test_backward(T, D, F, act):
         assert_close(g, w, (1 + U8) * t + U8 * w.abs(), name)
 
 
+# sizes whose products take each tile shape, whole and cut into parts: pairs cut (256 x 4096/14336 down), single
+# CTAs on 128 columns with a cut last wave (128 tokens up) and cut (down), on 64 columns cut many times
+@pytest.mark.parametrize("T, D, F", [(256, 4096, 14336), (128, 4096, 14336), (19, 184, 6440), (300, 1000, 4000)])
+def test_forward_in_every_tile_shape(T, D, F):
+    i = _inputs(T, D, F, seed=11)
+    Y, G, U = _forward(i, "silu")
+    assert fg.sync_status() == 0
+    _check_forward(i, "silu", Y, G, U, True)
+
+
+# pairs whole and cut (1024/2816 and 240 wide), 128 columns cut, 64 columns cut
+@pytest.mark.parametrize("T, D, F", [(1024, 1024, 2816), (2683, 2552, 240), (64, 1024, 2816), (128, 512, 1024),
+                                     (5, 2256, 1096)])
+def test_backward_in_every_tile_shape(T, D, F):
+    i = _inputs(T, D, F, seed=12)
+    got = _backward(i, "gelu_tanh")
+    assert fg.sync_status() == 0
+    for g, w, t, name in zip(got, *_gradients(i, "gelu_tanh"), ("dX", "dWg", "dWu", "dWd")):
+        assert_close(g, w, (1 + U8) * t + U8 * w.abs(), name)
+
+
 def test_backward_without_dx_and_twice_the_same_bits():
     i = _inputs(300, 24, 4104, seed=2)  # dX's long reduction is split over several CTAs
     a, b, c = _backward(i, "silu"), _backward(i, "silu"), _backward(i, "silu", dx=False)
