@@ -6,7 +6,7 @@
 //   warp 0      TMA producer: 64-deep slices of A and B into a shared-memory ring, 128-byte swizzle
 //   warp 1      MMA issuer: tcgen05.mma kind::f16, bf16 x bf16 -> f32, accumulating in TMEM; two
 //               accumulators, so the next tile's mainloop overlaps this tile's epilogue
-//   warps 2-9   epilogue: thread = output row; tcgen05.ld gives it 32 columns at a time
+//   warps 2-9   epilogue: thread = output row; tcgen05.ld gives it 32 columns at a time, or 16
 // What is computed per finished tile is the EPI parameter:
 //   kBlockGatedFwd   A = X, B = the gate's and the up projection's rows side by side: the tile holds
 //                    G and U of the same columns, and H = act(G) U leaves the chip with them (or
@@ -32,16 +32,17 @@
 // takes two copies: its last block of 64 columns would reach past its rows.
 //
 // What bounds it, measured on one GB300.  Large products: the tensor core under the chip's power limit.  In
-// bursts below the limit, 4096 tokens: block forward 4096/14336 811 us (1.78 PFLOP/s, 0.93 of the measured
-// burst peak), block backward 1681 us (1.72), loss forward over 32768 x 4096 577 us (1.91), loss backward
-// 1800 us (1.83); run on end, at the limit, 1.79, 1.53, 1.78 and 1.64.  Products with MN-major operands
+// bursts below the limit, 4096 tokens: block forward 4096/14336 795 us (1.81 PFLOP/s, 0.95 of the measured
+// burst peak), block backward 1613 us (1.79), loss forward over 32768 x 4096 570 us (1.93), loss backward
+// 1766 us (1.87); run on end, at the limit, 1.82, 1.62, 1.78 and 1.68.  Products with MN-major operands
 // (dX, dW, dH) reach less there than K-major ones.  The tile with dH also shares the memory system with G,
 // U, dG, dU and H: 165 us at 2048 tokens (1.45 PFLOP/s), the same with 16 epilogue warps, with G and U
 // prefetched into L2, or loaded first to be evicted.  With one row of tiles: memory, 6.4 TB/s of weights for
 // the loss of one token over 155648 x 4096.
 //
 // Why these tiles.  A pair's 256 x 256 tile moves 32 KB into each SM's shared memory per 512 cycles of its
-// tensor core; single CTAs on 128 x 128 move twice as much per product and serve small calls.
+// tensor core; single CTAs on 128 x 128 or 128 x 64 move more per product, fill the GPU with less and serve small
+// calls.  The host picks one by what it costs (kTiles in block_api.cu).
 //
 // Units of work.  A unit is one tile over its whole reduction, or one of `parts` pieces of it.  A
 // split tile has no CTA that waits for another: each epilogue warp leaves its FP32 values in memory,
