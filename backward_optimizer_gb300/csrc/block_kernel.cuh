@@ -124,6 +124,8 @@ struct BlockProblem {
     const float* dloss;   // [rows]
     // kBlockLossGrad writes g / *unit, and kBlockStore multiplies its finished sums by *unit (null: 1)
     const float* unit;
+    // kBlockLossGrad: where this launch leaves the unit that it finds itself, or null
+    float* own_unit;
 };
 
 // Up to NP products, the one with the longest units first.  What every role reads at its start comes first.
@@ -557,8 +559,29 @@ __device__ __forceinline__ void epi_loss_stats(const BlockProblem& b, const Acc&
     if (mine) b.stats[static_cast<size_t>(2 * nb + h) * b.rows + row] = make_float2(m, s);
 }
 
+// What a token adds to the largest |dloss|.
+__device__ __forceinline__ float loss_weight(float dloss, int64_t target, int64_t ignore) {
+    return target == ignore ? 0.0f : fabsf(dloss);
+}
+
+// The number that g is kept relative to: the largest |dloss| of the tokens that count, or 1 where there is none
+// above 0.  With few tokens every warp finds it itself while the first tile's slices come in, and one of them
+// leaves it for the products that follow.
+__device__ __forceinline__ float loss_unit(const BlockProblem& b, bool leave) {
+    if (b.own_unit == nullptr) return b.unit != nullptr ? __ldg(b.unit) : 1.0f;
+    const int lane = static_cast<int>(threadIdx.x & 31u);
+    float m = 0.0f;
+    for (int i = lane; i < b.rows; i += 32) m = fmaxf(m, loss_weight(b.dloss[i], b.target[i], b.ignore));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    m = m > 0.0f ? m : 1.0f;
+    if (leave && lane == 0) *b.own_unit = m;
+    return m;
+}
+
 template <int BN, class Acc, class Out>
-__device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& acc, int row, int nb, int h, Out& out) {
+__device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& acc, int row, int nb, int h, Out& out,
+                                              float unit) {
     if (warp_row0(row) >= b.rows) return;
     const bool mine = row < b.rows;
     const int64_t t = mine ? b.target[row] : -1;
@@ -569,7 +592,7 @@ __device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& 
     // Under the usual mean over tokens every dloss is the same number, and so is, nearly, every
     // target's entry -dloss (1 - p): rounded to bfloat16 as it is, that number's one rounding error (up
     // to 2^-8) would stand in all of dX and dW.  Relative to the largest dloss the entry is -(1 - p).
-    const float scale = b.unit != nullptr ? given / __ldg(b.unit) : given;
+    const float scale = given / unit;
     const int64_t first = b.v0 + static_cast<int64_t>(nb) * BN;
 #pragma unroll 1
     for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
@@ -592,12 +615,13 @@ __device__ __forceinline__ void epi_loss_grad(const BlockProblem& b, const Acc& 
 }
 
 template <int BN, int EPI, class Acc, class Out>
-__device__ __forceinline__ void block_epilogue(const BlockProblem& b, const Acc& acc, int row, int nb, int h, Out& out) {
+__device__ __forceinline__ void block_epilogue(const BlockProblem& b, const Acc& acc, int row, int nb, int h, Out& out,
+                                               float unit) {
     if constexpr (EPI == kBlockStore) epi_store<BN>(b, acc, row, nb, h, out);
     else if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, acc, row, nb, h, out);
     else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, acc, row, nb, h, out);
     else if constexpr (EPI == kBlockLossStats) epi_loss_stats<BN>(b, acc, row, nb, h);
-    else epi_loss_grad<BN>(b, acc, row, nb, h, out);
+    else epi_loss_grad<BN>(b, acc, row, nb, h, out, unit);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -831,6 +855,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
         int l = 0;
         stream_wait();
         stream_release();
+        float unit = 1.0f;
+        if constexpr (EPI == kBlockLossGrad) unit = loss_unit(grp.prob[0], blockIdx.x == 0 && e == 0);
         if (blockIdx.x == 0)
             for (int i = threadIdx.x - 64; i < grp.zero_n; i += C::kThreads - 64) grp.zero_at[i] = 0u;
         for (int u = cur.next(grp.units, pair, pairs); u >= 0; u = cur.next(grp.units, pair, pairs)) {
@@ -849,7 +875,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             }
             out.ld = b.ld;
             out.rows = b.rows;
-            if (w.split < 0) block_epilogue<BN, EPI>(b, tm, row, w.nb, half, out);
+            if (w.split < 0) block_epilogue<BN, EPI>(b, tm, row, w.nb, half, out, unit);
             // [split tile][part][CTA][lane quarter][column][lane]
             const size_t step = static_cast<size_t>(CG) * 4 * BN * 32;
             const size_t own = (static_cast<size_t>(rank) * 4 + quarter) * BN * 32 + lane;
@@ -893,7 +919,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                     if (lane == 0) *count = 0u;
                     const AccParts sum{grp.parts + b.part_base + static_cast<size_t>(w.split) * b.parts * step + own,
                                        step, b.parts, row < b.rows};
-                    block_epilogue<BN, EPI>(b, sum, row, w.nb, half, out);
+                    block_epilogue<BN, EPI>(b, sum, row, w.nb, half, out, unit);
                 }
             }
         }
