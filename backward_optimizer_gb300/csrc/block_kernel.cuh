@@ -391,6 +391,8 @@ template <int BN, class Acc, class Out>
 __device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc, int row, int nb, int h, Out& out) {
     if (warp_row0(row) >= b.rows) return;
     const bool wide = (b.ld & 15) == 0, mine = row < b.rows;
+    // from the L2, not by __ldg: a launch that may still run when this one starts writes it
+    const float unit = b.unit != nullptr ? __ldcg(b.unit) : 1.0f;
 #pragma unroll 1
     for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 32) {
         const int col = nb * BN + c, left = b.cols - col;
@@ -423,7 +425,6 @@ __device__ __forceinline__ void epi_store(const BlockProblem& b, const Acc& acc,
             continue;
         }
         if (b.unit != nullptr) {
-            const float unit = __ldg(b.unit);
 #pragma unroll
             for (int j = 0; j < 32; ++j) g[j] = __float_as_uint(__fmul_rn(__uint_as_float(g[j]), unit));
         }
@@ -568,7 +569,7 @@ __device__ __forceinline__ float loss_weight(float dloss, int64_t target, int64_
 // above 0.  With few tokens every warp finds it itself while the first tile's slices come in, and one of them
 // leaves it for the products that follow.
 __device__ __forceinline__ float loss_unit(const BlockProblem& b, bool leave) {
-    if (b.own_unit == nullptr) return b.unit != nullptr ? __ldg(b.unit) : 1.0f;
+    if (b.own_unit == nullptr) return b.unit != nullptr ? __ldcg(b.unit) : 1.0f;
     const int lane = static_cast<int>(threadIdx.x & 31u);
     float m = 0.0f;
     for (int i = lane; i < b.rows; i += 32) m = fmaxf(m, loss_weight(b.dloss[i], b.target[i], b.ignore));
