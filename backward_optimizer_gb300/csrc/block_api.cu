@@ -448,7 +448,6 @@ forge_status run_store(const Machine& mc, const Plan& p, const Product* pr, char
 
 __global__ void __launch_bounds__(256) zero_counts_kernel(uint32_t* counts, int n) {
     forge::stream_wait();
-    forge::stream_release();
     for (int i = threadIdx.x; i < n; i += 256) counts[i] = 0u;
 }
 
@@ -777,7 +776,6 @@ __global__ void __launch_bounds__(kFinishThreads)
     constexpr int kShares = kFinishThreads / kRows;
     __shared__ float2 part[kShares][kRows];
     forge::stream_wait();
-    forge::stream_release();
     const int r = threadIdx.x % kRows, share = threadIdx.x / kRows;
     const int row = blockIdx.x * kRows + r;
     float m = -INFINITY, s = 0.0f;
@@ -816,7 +814,6 @@ __global__ void __launch_bounds__(1024)
                       int n_counts) {
     __shared__ float part[32];
     forge::stream_wait();
-    forge::stream_release();
     for (int i = threadIdx.x; i < n_counts; i += 1024) counts[i] = 0u;
     float m = 0.0f;
     for (int i = threadIdx.x; i < rows; i += 1024) m = fmaxf(m, forge::loss_weight(dloss[i], target[i], ignore));

@@ -172,11 +172,10 @@ struct Unit {
 
 // stream_wait() with a role's first unit in hand: the compiler may not move its computation past the wait.
 __device__ __forceinline__ void stream_wait_with(int& u, Unit& w) {
-    asm volatile("griddepcontrol.wait;"
+    asm volatile(FORGE_STREAM_WAIT
                  : "+r"(u), "+r"(w.prob), "+r"(w.mb), "+r"(w.nb), "+r"(w.part), "+r"(w.split), "+r"(w.k_first), "+r"(w.k_end)
                  :
                  : "memory");
-    stream_release();
 }
 
 template <int NP>
@@ -855,7 +854,6 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
         UnitCursor cur;
         int l = 0;
         stream_wait();
-        stream_release();
         float unit = 1.0f;
         if constexpr (EPI == kBlockLossGrad) unit = loss_unit(grp.prob[0], blockIdx.x == 0 && e == 0);
         if (blockIdx.x == 0)

@@ -203,7 +203,6 @@ template <class TX, int VEC, int NV, bool CENTER>
 __global__ void __launch_bounds__(kNormThreads) forge_norm_kernel(const NormArgs a) {
     __shared__ float2 buf[2][kNormThreads / 32];
     stream_wait();
-    stream_release();
     GroupSum sum{buf, 0};
     const float inv = 1.0f / static_cast<float>(a.D);
     const int step = blockDim.x * VEC;
@@ -301,7 +300,6 @@ __global__ void __launch_bounds__(kNormThreads) forge_norm_bwd_kernel(const Norm
     __shared__ float2 buf[2][kNormThreads / 32];
     extern __shared__ float cols[];  // [groups][dw, db]
     stream_wait();
-    stream_release();
     GroupSum sum{buf, 0};
     const float inv = 1.0f / static_cast<float>(a.D);
     const int step = blockDim.x * VEC;
@@ -500,7 +498,6 @@ __device__ __forceinline__ NormRing<TX, TENSORS> norm_ring(const NormArgs& a, co
         fence_mbar_init();
     }
     stream_wait();
-    stream_release();
     if (threadIdx.x == 0) r.start();  // its own barriers; the others wait on them past the block's barrier
     __syncthreads();
     return r;
@@ -715,7 +712,6 @@ __global__ void __launch_bounds__(32 * kColumnWarps)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;  // column of the n = D (dw) or 2 D (dw, db) values of a row
     stream_wait();
-    stream_release();
     float v = 0.0f;
     if (c < n) {
         for (int first = warp; first < blocks; first += kColumnWarps * kColumnRows) {

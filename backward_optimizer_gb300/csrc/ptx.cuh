@@ -116,13 +116,14 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
 
 // ---------------------------------------------------------------- dependent launches
 // A kernel launched with programmatic stream serialization may start while the kernel before it on
-// the stream is still running.  It calls stream_wait() before it touches any memory that the stream's
-// earlier work reads or writes (every thread, so that nothing is ordered by luck), and then lets the next
-// kernel start early with stream_release(), always in this order: when a launch starts, everything
-// on the stream but the one launch before it is done.
+// the stream is still running.  Every thread calls stream_wait() before it touches any memory that the
+// stream's earlier work reads or writes.  It waits for that work and only then lets the next kernel start
+// early: when a launch starts, everything on the stream but the one launch before it is done.  The early
+// read of weights (rows_kernel.cuh, weights_ready) rests on this order, so the two instructions are
+// never apart.
+#define FORGE_STREAM_WAIT "griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;"
 
-__device__ __forceinline__ void stream_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void stream_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void stream_wait() { asm volatile(FORGE_STREAM_WAIT ::: "memory"); }
 
 // ---------------------------------------------------------------- TMA
 

@@ -100,7 +100,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1) forge_rows_kernel(const RowsA
             for (int k = 0; k < a.slots && k < mine; ++k) issue(k, k);
     }
     stream_wait();
-    stream_release();
     __syncthreads();
     if (warp == kRowsWarps) {
         if (!producer) return;

@@ -20,3 +20,10 @@ def test_nothing_is_read_as_constant():
     early runs while the launch in front still writes, and the compiler may move such a load before the wait."""
     found = [f for f, text in _sources() if re.search(r"__ldg\s*\(|global\.nc|__restrict__", text)]
     assert found == []
+
+
+def test_the_next_launch_is_let_go_only_behind_the_wait():
+    """An early read (the weights of a few-token product) relies on it: all but one launch in front are done."""
+    for f, text in _sources():
+        for at in (m.start() for m in re.finditer("griddepcontrol.launch_dependents", text)):
+            assert text[:at].endswith('griddepcontrol.wait;\\n\\t'), f
