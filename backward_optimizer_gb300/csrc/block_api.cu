@@ -879,6 +879,7 @@ forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, cons
         r.N = static_cast<int>(s.d_ff);
         r.K = static_cast<int>(s.d_model);
         r.act = s.act;
+        r.withhold = host::take_withhold();
         r.status = mc.dev.status;
         r.wait_limit_ns = host::wait_limit_ns();
         FORGE_TRY(cuda_status(forge::launch_rows(r, true, mc.dev.num_sms, stream)));
@@ -891,6 +892,7 @@ forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, cons
         d.N = static_cast<int>(s.d_model);
         d.K = static_cast<int>(s.d_ff);
         d.weights_ready = 1;
+        d.withhold = 0;
         return cuda_status(forge::launch_rows(d, false, mc.dev.num_sms, stream));
     }
     PairGroup<forge::kBlockGatedFwd> g;

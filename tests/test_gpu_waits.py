@@ -57,3 +57,13 @@ def test_norm(T, D, kind, dtype):
     dx, dw, db = torch.empty_like(x), torch.empty(D, device="cuda"), torch.empty(D, device="cuda") if layer else None
     _check(lambda: fg.layer_norm_backward(dy, x, w, mean, rstd, dx, dw, db, add, kind=kind),
            [dx, dw] + ([db] if layer else []))
+
+
+# more groups of weight rows than slots, fewer than slots; a down projection whose ring fills before the wait
+@pytest.mark.parametrize("T", [1, 2, 3, 4])
+@pytest.mark.parametrize("D, F", [(1024, 8192), (64, 520), (4096, 4096)])
+def test_few_token_products(T, D, F):
+    X, R = _rand(0, T, D), _rand(1, T, D)
+    Wg, Wu, Wd = (_rand(i, *s) * s[1] ** -0.5 for i, s in ((2, (F, D)), (3, (F, D)), (4, (D, F))))
+    Y, G, U = torch.empty_like(X), *(torch.empty(T, F, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    _check(lambda: fg.gated_mlp(X, Wg, Wu, Wd, Y, G, U, residual=R), [Y, G, U])
