@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     loss[row] = t == ignore ? 0.0f : t >= 0 && t < vocab ? l - loss[row] : NAN;
 }
 
-// The largest |dloss| of the tokens that count, or 1 where there is none above 0; and the counters of the
+// The largest finite |dloss| of the tokens that count, or 1 where there is none above 0; and the counters of the
 // call's split tiles cleared: one block.
 __global__ void __launch_bounds__(1024)
     loss_begin_kernel(const float* dloss, const int64_t* target, int64_t ignore, int rows, float* unit, uint32_t* counts,

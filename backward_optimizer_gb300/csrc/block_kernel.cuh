@@ -559,13 +559,14 @@ __device__ __forceinline__ void epi_loss_stats(const BlockProblem& b, const Acc&
     if (mine) b.stats[static_cast<size_t>(2 * nb + h) * b.rows + row] = make_float2(m, s);
 }
 
-// What a token adds to the largest |dloss|.
+// What a token adds to the largest |dloss|.  An infinite one adds nothing: relative to it every other token's g
+// would be 0, and 0 times it NaN.
 __device__ __forceinline__ float loss_weight(float dloss, int64_t target, int64_t ignore) {
-    return target == ignore ? 0.0f : fabsf(dloss);
+    return target == ignore || fabsf(dloss) == INFINITY ? 0.0f : fabsf(dloss);
 }
 
-// The number that g is kept relative to: the largest |dloss| of the tokens that count, or 1 where there is none
-// above 0.  With few tokens every warp finds it itself while the first tile's slices come in, and one of them
+// The number that g is kept relative to: the largest finite |dloss| of the tokens that count, or 1 where there is
+// none above 0.  With few tokens every warp finds it itself while the first tile's slices come in, and one of them
 // leaves it for the products that follow.
 __device__ __forceinline__ float loss_unit(const BlockProblem& b, bool leave) {
     if (b.own_unit == nullptr) return b.unit != nullptr ? __ldcg(b.unit) : 1.0f;
