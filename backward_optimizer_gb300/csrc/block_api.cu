@@ -658,7 +658,6 @@ int64_t loss_piece(const forge_loss_shape& s) {
 struct LossBackward {
     int64_t piece, pieces;
     int64_t g, sum, unit, bytes;
-    bool scaled;       // g is kept relative to the largest dloss
     SplitSpace split;
 };
 
@@ -689,17 +688,14 @@ LossPiece loss_piece_of(const Machine& mc, const forge_loss_shape& s, const Loss
         w.a[0].cols = p.ld;  // g's padding is finite and ends in rows of dW that are not stored
         p.pr[p.np++] = w;
     }
-    if (l.scaled)
-        for (int j = 0; j < p.np; ++j) p.pr[j].unit = reinterpret_cast<const float*>(ws + l.unit);
+    for (int j = 0; j < p.np; ++j) p.pr[j].unit = reinterpret_cast<const float*>(ws + l.unit);
     if (p.np > 0) p.out = plan_store(mc, p.pr, p.np);
     return p;
 }
 
-// step: the fused step takes g (it has no factor of its own for the gradient, so g is not scaled)
-LossBackward layout_loss_backward(const Machine& mc, const forge_loss_shape& s, bool dx, bool dw, bool step) {
+LossBackward layout_loss_backward(const Machine& mc, const forge_loss_shape& s, bool dx, bool dw) {
     LossBackward l{};
     Arena a;
-    l.scaled = !step;
     l.unit = a.take(4);
     l.piece = loss_piece(s);
     l.pieces = ceil_div(s.vocab, l.piece);
@@ -719,15 +715,13 @@ LossBackward layout_loss_backward(const Machine& mc, const forge_loss_shape& s, 
 // and 26.3; 2048: 38.8 and 39.7.
 constexpr int64_t kOwnUnitRows = 1024;
 
-bool loss_begins(const LossBackward& l, const LossPiece& p, const forge_loss_shape& s) {
-    return p.grad.counts > 0 || (l.scaled && s.T > kOwnUnitRows);
-}
+bool loss_begins(const LossPiece& p, const forge_loss_shape& s) { return p.grad.counts > 0 || s.T > kOwnUnitRows; }
 
 // g of one piece of the vocabulary
 forge_status run_loss_grad(const Machine& mc, const LossBackward& l, const LossPiece& p, const forge_loss_shape& s,
                            const void* X, const void* W, const int64_t* target, const float* lse, const float* dloss,
                            char* ws, cudaStream_t stream) {
-    const bool first = p.v0 == 0 && !loss_begins(l, p, s);
+    const bool first = p.v0 == 0 && !loss_begins(p, s);
     PairGroup<forge::kBlockLossGrad> g;
     std::memset(&g, 0, sizeof(g));
     FORGE_TRY(fill_group(g, p.grad, mc, ws, l.split));
@@ -741,9 +735,9 @@ forge_status run_loss_grad(const Machine& mc, const LossBackward& l, const LossP
     b.ignore = s.ignore_index;
     b.lse = lse;
     b.dloss = dloss;
-    b.unit = l.scaled ? reinterpret_cast<const float*>(ws + l.unit) : nullptr;
+    b.unit = reinterpret_cast<const float*>(ws + l.unit);
     if (first) {
-        b.own_unit = l.scaled ? reinterpret_cast<float*>(ws + l.unit) : nullptr;
+        b.own_unit = reinterpret_cast<float*>(ws + l.unit);
         FORGE_TRY(clear_counts(g, p.grad, ws, l.split, stream));
     }
     FORGE_TRY(set_map(g, p.grad, 0, 0, Operand{X, s.d_model, s.T, s.d_model}, false));
@@ -988,8 +982,7 @@ int64_t forge_linear_cross_entropy_workspace(const forge_loss_shape* shape, int3
     if (machine(&mc) != FORGE_OK) return -1;
     if (!backward) return layout_loss_forward(mc, *shape).bytes;
     int64_t most = 0;
-    for (int i = 0; i < 8; ++i)
-        most = std::max(most, layout_loss_backward(mc, *shape, i & 1, (i >> 1) & 1, i >> 2).bytes);
+    for (int i = 0; i < 4; ++i) most = std::max(most, layout_loss_backward(mc, *shape, i & 1, i >> 1).bytes);
     return most;
 }
 
@@ -1050,12 +1043,12 @@ forge_status forge_linear_cross_entropy_backward(const void* X, const void* W, c
         return dW == nullptr ? FORGE_OK
                              : cuda_status(cudaMemsetAsync(dW, 0, static_cast<size_t>(s.vocab) * s.d_model * 2, stream));
     const bool dx = dX != nullptr, dw = dW != nullptr;
-    const LossBackward l = layout_loss_backward(mc, s, dx, dw, false);
+    const LossBackward l = layout_loss_backward(mc, s, dx, dw);
     FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     char* ws = static_cast<char*>(workspace);
     for (int64_t i = 0; i < l.pieces; ++i) {
         const LossPiece p = loss_piece_of(mc, s, l, i, X, W, dX, dW, dx, dw, ws);
-        if (i == 0 && loss_begins(l, p, s)) FORGE_TRY(run_loss_begin(l, s, target, dloss, ws, stream));
+        if (i == 0 && loss_begins(p, s)) FORGE_TRY(run_loss_begin(l, s, target, dloss, ws, stream));
         FORGE_TRY(run_loss_grad(mc, l, p, s, X, W, target, lse, dloss, ws, stream));
         FORGE_TRY(run_loss_products(mc, l, p, ws, stream));
     }
@@ -1081,20 +1074,21 @@ forge_status forge_linear_cross_entropy_step(const void* X, void* W, const int64
     FORGE_TRY(machine(&mc));
     if (s.T == 0)
         return host::fused_rows(nullptr, 0, X, 0, 0, s.vocab, W, m, v, qscales, opt_kind, hp, s.vocab, s.d_model, state,
-                                step, seed, stream);
+                                step, seed, nullptr, stream);
     const bool dx = dX != nullptr;
-    const LossBackward l = layout_loss_backward(mc, s, dx, false, true);
+    const LossBackward l = layout_loss_backward(mc, s, dx, false);
     FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     char* ws = static_cast<char*>(workspace);
     for (int64_t i = 0; i < l.pieces; ++i) {
         const LossPiece p = loss_piece_of(mc, s, l, i, X, W, dX, nullptr, dx, false, ws);
-        if (i == 0 && loss_begins(l, p, s)) FORGE_TRY(run_loss_begin(l, s, target, dloss, ws, stream));
+        if (i == 0 && loss_begins(p, s)) FORGE_TRY(run_loss_begin(l, s, target, dloss, ws, stream));
         // logits and dX read the piece's rows before the fused step replaces them
         FORGE_TRY(run_loss_grad(mc, l, p, s, X, W, target, lse, dloss, ws, stream));
         FORGE_TRY(run_loss_products(mc, l, p, ws, stream));
         // each piece numbers its elements from 0: a seed of its own keeps its random bits its own
         FORGE_TRY(host::fused_rows(ws + l.g, p.ld, X, s.T, p.v0, p.n, W, m, v, qscales, opt_kind, hp, s.vocab, s.d_model,
-                                   state, step, seed ^ (static_cast<uint64_t>(i) << 40), stream));
+                                   state, step, seed ^ (static_cast<uint64_t>(i) << 40),
+                                   reinterpret_cast<const float*>(ws + l.unit), stream));
     }
     return FORGE_OK;
 }

@@ -122,7 +122,7 @@ struct BlockProblem {
     float* target_logit;  // [rows]
     const float* lse;     // [rows]
     const float* dloss;   // [rows]
-    // kBlockLossGrad writes g / *unit, and kBlockStore multiplies its finished sums by *unit (null: 1)
+    // kBlockLossGrad writes g / *unit, and kBlockStore multiplies its finished sums by *unit (there, null: 1)
     const float* unit;
     // kBlockLossGrad: where this launch leaves the unit that it finds itself, or null
     float* own_unit;
@@ -569,7 +569,7 @@ __device__ __forceinline__ float loss_weight(float dloss, int64_t target, int64_
 // none above 0.  With few tokens every warp finds it itself while the first tile's slices come in, and one of them
 // leaves it for the products that follow.
 __device__ __forceinline__ float loss_unit(const BlockProblem& b, bool leave) {
-    if (b.own_unit == nullptr) return b.unit != nullptr ? __ldcg(b.unit) : 1.0f;
+    if (b.own_unit == nullptr) return __ldcg(b.unit);
     const int lane = static_cast<int>(threadIdx.x & 31u);
     float m = 0.0f;
     for (int i = lane; i < b.rows; i += 32) m = fmaxf(m, loss_weight(b.dloss[i], b.target[i], b.ignore));

@@ -355,22 +355,25 @@ TileFn tile_fn_ops(forge_opt_kind k, int state, int epi, TileShape t) {
         return t.bn == 256 ? launch_tile<0, kEpiDX, 256, 1, kOpsBF16, 1> : launch_tile<0, kEpiDX, 128, 1, kOpsBF16, 1>;
     }
     if (epi == kEpiStoreGrad) {
-        if (t.cg == 2) return launch_tile<0, kEpiStoreGrad, 256, 2, OPS, 1>;
+        constexpr int kOps = OPS == kOpsBF16Scaled ? kOpsBF16 : OPS;
+        if (OPS == kOpsBF16Scaled) return nullptr;  // no gradient to memory is scaled
+        if (t.cg == 2) return launch_tile<0, kEpiStoreGrad, 256, 2, kOps, 1>;
         if (t.bn == 64) {
             if constexpr (OPS != kOpsBF16) return nullptr;
             else return launch_tile<0, kEpiStoreGrad, 64, 1, kOpsBF16, 1>;
         }
-        return t.bn == 256 ? launch_tile<0, kEpiStoreGrad, 256, 1, OPS, 1> : launch_tile<0, kEpiStoreGrad, 128, 1, OPS, 1>;
+        return t.bn == 256 ? launch_tile<0, kEpiStoreGrad, 256, 1, kOps, 1> : launch_tile<0, kEpiStoreGrad, 128, 1, kOps, 1>;
     }
     if (t.cg == 2) return tile_fn_v<256, 2, OPS>(k, state);
     if (t.bn == 64) {
-        if constexpr (OPS != kOpsBF16) return nullptr;
+        if constexpr (OPS == kOpsE4M3) return nullptr;
         else return state == FORGE_STATE_INT8_B64 ? nullptr : tile_fn_v<64, 1, OPS>(k, state);
     }
     return t.bn == 256 ? tile_fn_v<256, 1, OPS>(k, state) : tile_fn_v<128, 1, OPS>(k, state);
 }
 
-TileFn tile_fn(forge_opt_kind k, int state, int epi, TileShape t, bool e4m3) {
+TileFn tile_fn(forge_opt_kind k, int state, int epi, TileShape t, bool e4m3, bool scaled = false) {
+    if (scaled) return tile_fn_ops<forge::kOpsBF16Scaled>(k, state, epi, t);
     return e4m3 ? tile_fn_ops<forge::kOpsE4M3>(k, state, epi, t) : tile_fn_ops<forge::kOpsBF16>(k, state, epi, t);
 }
 
@@ -467,7 +470,7 @@ forge_status run_tile(const void* dY, const void* X, float* dW, void* W, void* m
                       forge_opt_kind k, int epi, const forge_hparams* hp, const forge_shape* shape, int64_t step,
                       uint64_t seed, cudaStream_t stream, const DeviceInfo& dev, bool e4m3 = false,
                       float g_scale = 1.0f, const float* row_scales = nullptr, const float* col_scales = nullptr,
-                      int64_t dy_ld = 0, float* v_scales = nullptr) {
+                      int64_t dy_ld = 0, float* v_scales = nullptr, const float* g_unit = nullptr) {
     // 128 x 64 tiles need bf16 operands and an epilogue on 32-column runs (not INT8 states)
     const bool narrow_ok = !e4m3 && (epi == forge::kEpiStoreGrad || shape->state != FORGE_STATE_INT8_B64);
     const TileShape ts = pick_shape(shape->d_out, shape->d_in, shape->T, dev.num_sms, narrow_ok);
@@ -476,11 +479,12 @@ forge_status run_tile(const void* dY, const void* X, float* dW, void* W, void* m
     forge_status st = prepare_layer(g.layer[0], g.maps, dY, X, dW, W, m, v, qscales, k, hp, shape, step, seed, dev,
                                     ts, e4m3, g_scale, row_scales, col_scales, g_withhold_next.exchange(0), dy_ld, v_scales);
     if (st != FORGE_OK) return st;
+    if (g_unit != nullptr) g.layer[0].row_scales = g_unit;
     g.tile_start[0] = 0;
     g.tile_start[1] = g.layer[0].num_tiles;
     forge::TileLaunch l{&g, g.tile_start[1], dev.num_sms, stream};
     // epi is kEpiStoreGrad (dW to memory) or kEpiOptFP32 (the fused step, whose epilogue follows the state dtype)
-    TileFn fn = tile_fn(k, shape->state, epi, ts, e4m3);
+    TileFn fn = tile_fn(k, shape->state, epi, ts, e4m3, g_unit != nullptr);
     if (fn == nullptr) return FORGE_ERR_UNSUPPORTED;
     g_launches.fetch_add(1);
     return cuda_status(fn(l));
@@ -633,7 +637,8 @@ forge_status check_step(const void* W, const void* m, const void* v, const float
 
 forge_status fused_rows(const void* dY, int64_t dy_ld, const void* X, int64_t T, int64_t row0, int64_t rows, void* W,
                         void* m, void* v, float* qscales, forge_opt_kind k, const forge_hparams* hp, int64_t d_out,
-                        int64_t d_in, int32_t state, int64_t step, uint64_t seed, cudaStream_t stream) {
+                        int64_t d_in, int32_t state, int64_t step, uint64_t seed, const float* unit,
+                        cudaStream_t stream) {
     DeviceInfo* dev = nullptr;
     forge_status st = device_info(&dev);
     if (st != FORGE_OK) return st;
@@ -648,7 +653,7 @@ forge_status fused_rows(const void* dY, int64_t dy_ld, const void* X, int64_t T,
     float* vs = qscales == nullptr ? nullptr : qscales + n / 64 + first / 64;
     const forge_shape shape{T, rows, d_in, state, 0};
     return run_tile(dY, X, nullptr, at(W, 2), at(m, state_bytes), at(v, state_bytes), ms, k, kEpiOptFP32, hp, &shape,
-                    step, seed, stream, *dev, false, 1.0f, nullptr, nullptr, dy_ld, vs);
+                    step, seed, stream, *dev, false, 1.0f, nullptr, nullptr, dy_ld, vs, unit);
 }
 
 }  // namespace host

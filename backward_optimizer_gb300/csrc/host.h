@@ -57,10 +57,12 @@ forge_status check_step(const void* W, const void* m, const void* v, const float
                         const forge_hparams* hp, int64_t d_out, int64_t d_in, int32_t state, int64_t step);
 
 // The fused step on rows row0 .. row0 + rows - 1 of a layer's weights [d_out, d_in]: dY [T, rows] with
-// rows `dy_ld` elements apart (a multiple of 8), X [T, d_in]; W, m, v and qscales are the whole layer's.
+// rows `dy_ld` elements apart (a multiple of 8), X [T, d_in]; W, m, v and qscales are the whole layer's.  unit (device
+// memory, or null): dY is the gradient divided by it.
 forge_status fused_rows(const void* dY, int64_t dy_ld, const void* X, int64_t T, int64_t row0, int64_t rows, void* W,
                         void* m, void* v, float* qscales, forge_opt_kind k, const forge_hparams* hp, int64_t d_out,
-                        int64_t d_in, int32_t state, int64_t step, uint64_t seed, cudaStream_t stream);
+                        int64_t d_in, int32_t state, int64_t step, uint64_t seed, const float* unit,
+                        cudaStream_t stream);
 
 }  // namespace host
 }  // namespace forge

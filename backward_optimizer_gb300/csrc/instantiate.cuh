@@ -50,7 +50,7 @@ cudaError_t launch_tile(const TileLaunch& l) {
     // persistent grid: one CTA per SM (or one cluster per CL SMs), never more units than tiles.
     // Pair kernels with bf16 operands split a short last wave into half tiles (schedule.h).
     const int cap = CL == 1 ? l.num_sms : max_clusters[dev].load();
-    constexpr bool kSplitTail = CG == 2 && BN == 256 && OPS == kOpsBF16;
+    constexpr bool kSplitTail = CG == 2 && BN == 256 && OPS != kOpsE4M3;
     const int split_from = kSplitTail ? split_tail_from(l.num_tiles, cap) : l.num_tiles;
     const int launch_tiles = l.num_tiles + (l.num_tiles - split_from);
     const int units = launch_tiles < cap ? launch_tiles : cap;
@@ -114,6 +114,16 @@ cudaError_t launch_opt(const OptArgs& a, int grid, cudaStream_t stream) {
     FORGE_INSTANTIATE_TILES_OPS(OPT, forge::kEpiOptFP32, forge::kOpsE4M3) \
     FORGE_INSTANTIATE_TILES_OPS(OPT, forge::kEpiOptINT8, forge::kOpsE4M3) \
     FORGE_INSTANTIATE_TILES_OPS(OPT, forge::kEpiOptBF16, forge::kOpsE4M3)
+
+// bf16 operands with a scaled dY, every state format.
+#define FORGE_INSTANTIATE_SCALED(OPT, EPI)                            \
+    FORGE_INSTANTIATE_TILES_OPS(OPT, EPI, forge::kOpsBF16Scaled)       \
+    template cudaError_t forge::launch_tile<OPT, EPI, 64, 1, forge::kOpsBF16Scaled, 1>(const forge::TileLaunch&);
+
+#define FORGE_INSTANTIATE_OPT_SCALED(OPT)              \
+    FORGE_INSTANTIATE_SCALED(OPT, forge::kEpiOptFP32)  \
+    FORGE_INSTANTIATE_SCALED(OPT, forge::kEpiOptBF16)  \
+    FORGE_INSTANTIATE_TILES_OPS(OPT, forge::kEpiOptINT8, forge::kOpsBF16Scaled)
 
 #define FORGE_INSTANTIATE_OPT(OPT)                    \
     FORGE_INSTANTIATE_TILES(OPT, forge::kEpiOptFP32) \

@@ -29,7 +29,8 @@ struct TileLaunch {
 // with bfloat16 states.
 // BN: tile columns (128, or 256 = two 128 x 128 tiles side by side).
 // CL: CTAs per cluster (1: a 128 x BN tile per CTA; 2: a 256 x BN tile per CTA pair).
-// OPS: operand format of dY and X, 0 = bf16, 1 = E4M3 (the gradient tile is scaled by s_dY * s_X).
+// OPS: operand format of dY and X, 0 = bf16, 1 = E4M3 (the gradient tile is scaled by s_dY * s_X), 2 = bf16 with a dY
+// that is the gradient divided by one number in device memory.
 // G: the group size the kernel is built for (1, or kMaxGroup).
 template <int OPT, int EPI, int BN, int CL, int OPS, int G> cudaError_t launch_tile(const TileLaunch& l);
 

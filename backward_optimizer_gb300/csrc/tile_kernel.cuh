@@ -47,8 +47,11 @@ enum EpiKind : int { kEpiStoreGrad = 0, kEpiOptFP32 = 1, kEpiOptINT8 = 2, kEpiDX
 
 // Operand formats.  Either way a stage row is 128 bytes (the swizzle span) and a stage of one
 // operand is 16 KiB per 128 MN rows: 64 tokens of bf16, or 128 tokens of E4M3, whose products the
-// tensor core takes 32 tokens at a time (kind::f8f6f4) instead of 16.
-enum OperandKind : int { kOpsBF16 = 0, kOpsE4M3 = 1 };
+// tensor core takes 32 tokens at a time (kind::f8f6f4) instead of 16.  kOpsBF16Scaled: bf16, and dY is the
+// gradient divided by a number in device memory; instantiations of their own, so that the unscaled ones stay
+// as they are (a test of a pointer in their epilogue, and the pointer among their parameters, cost 1 %:
+// Llama-8B MLP with INT8 states 1.034 ms per step against 1.023).
+enum OperandKind : int { kOpsBF16 = 0, kOpsE4M3 = 1, kOpsBF16Scaled = 2 };
 
 template <int OPS>
 struct OperandTraits {
@@ -62,7 +65,7 @@ template <int BN, int CG, int EPI, int OPS = kOpsBF16>
 struct TileCfg {
     // 64-column tiles (one X box per stage, N = 64 MMAs) serve small layers with bf16 operands and
     // epilogues that work on 32-column runs; E4M3 rows hold 128 elements, INT8 blocks 64 per warp
-    static_assert(BN == 128 || BN == 256 || (BN == 64 && CG == 1 && OPS == kOpsBF16 && EPI != kEpiOptINT8),
+    static_assert(BN == 128 || BN == 256 || (BN == 64 && CG == 1 && OPS != kOpsE4M3 && EPI != kEpiOptINT8),
                   "tile width");
     static_assert(CG == 1 || CG == 2, "CTA group");
     static constexpr int kBLoad = BN / CG;         // X columns staged by this CTA
@@ -103,7 +106,8 @@ struct TileArgs {
     int k_blocks;                 // reduction slices per tile: T / 64 (dW; T / 128 for E4M3), d_out / 64 (dX)
     float g_scale;                // E4M3 operands: s_dY * s_X, applied to the FP32 gradient tile
     const float* row_scales;      // or per channel (both set): s_dY [d_out] and s_X [d_in], each
-    const float* col_scales;      //   element's tile value times RN(s_dY[o] * s_X[i])
+    const float* col_scales;      //   element's tile value times RN(s_dY[o] * s_X[i]); kOpsBF16Scaled: row_scales
+                                  //   is one number, applied to the tile
     float* dW;                    // kEpiStoreGrad: [d_out, d_in] FP32
     uint16_t* dX;                 // kEpiDX: [T, d_in] bf16; token rows >= T are not stored
     uint16_t* W;                  // bf16 [d_out, d_in]
@@ -184,6 +188,13 @@ __device__ __forceinline__ void st_v8_f32(float* p, const uint32_t (&r)[8]) {
                  : "memory");
 }
 
+// The one factor of a whole gradient (SCALE: the operand format), read once per tile.
+template <int SCALE>
+__device__ __forceinline__ float tensor_scale(const TileArgs& a) {
+    if constexpr (SCALE == kOpsBF16Scaled) return *a.row_scales;
+    else return a.g_scale;
+}
+
 // Moves a 32-row x 32-column FP32 strip of the accumulator from TMEM, where thread i holds row i,
 // to the ownership used for device-memory accesses: lane l receives columns 8(l mod 4) .. +7 of
 // rows (l div 4) + 8k, k = 0..3, in out[k][0..7].  Four consecutive lanes then cover one row's
@@ -194,12 +205,12 @@ __device__ __forceinline__ void st_v8_f32(float* p, const uint32_t (&r)[8]) {
 // col .. col+31: by the per-tensor product, or by each element's channel-scale product.  Column
 // scales are the same for every lane (broadcast loads); d_in is a multiple of 16 with E4M3
 // operands, so each 4-column group is wholly inside or outside the layer.
-template <bool SCALE>
-__device__ __forceinline__ void scale_strip(uint32_t (&g)[32], const TileArgs& a, int row, int col) {
+template <int SCALE>
+__device__ __forceinline__ void scale_strip(uint32_t (&g)[32], const TileArgs& a, int row, int col, float scale) {
     if constexpr (SCALE) {
-        if (a.row_scales == nullptr) {
+        if (SCALE == kOpsBF16Scaled || a.row_scales == nullptr) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) g[i] = __float_as_uint(__fmul_rn(__uint_as_float(g[i]), a.g_scale));
+            for (int i = 0; i < 32; ++i) g[i] = __float_as_uint(__fmul_rn(__uint_as_float(g[i]), scale));
         } else {
             const float rs = row < a.d_out ? a.row_scales[row] : 0.0f;
 #pragma unroll
@@ -216,14 +227,14 @@ __device__ __forceinline__ void scale_strip(uint32_t (&g)[32], const TileArgs& a
     }
 }
 
-template <bool SCALE = false>
+template <int SCALE = 0>
 __device__ __forceinline__ void strip_transpose(uint32_t taddr, uint8_t* strip, uint32_t (&out)[4][8],
-                                                const TileArgs& a, int row, int col) {
+                                                const TileArgs& a, int row, int col, float scale) {
     const uint32_t lane = threadIdx.x & 31u;
     uint32_t g[32];
     tmem_ld_32x32b_x32(taddr, g);
     tmem_ld_wait(g);
-    scale_strip<SCALE>(g, a, row, col);
+    scale_strip<SCALE>(g, a, row, col, scale);
     const uint32_t base = smem_addr(strip);
 #pragma unroll
     for (uint32_t j = 0; j < 8; ++j)
@@ -245,13 +256,14 @@ __device__ __forceinline__ void strip_transpose(uint32_t taddr, uint8_t* strip, 
 
 // The two halves of strip_transpose, for callers that consume one row group at a time: the strip
 // is written once, then lane l reads the 8 columns it owns of row (l div 4) + 8k.
-template <bool SCALE = false>
-__device__ __forceinline__ void strip_store(uint32_t taddr, uint8_t* strip, const TileArgs& a, int row, int col) {
+template <int SCALE = 0>
+__device__ __forceinline__ void strip_store(uint32_t taddr, uint8_t* strip, const TileArgs& a, int row, int col,
+                                            float scale) {
     const uint32_t lane = threadIdx.x & 31u;
     uint32_t g[32];
     tmem_ld_32x32b_x32(taddr, g);
     tmem_ld_wait(g);
-    scale_strip<SCALE>(g, a, row, col);
+    scale_strip<SCALE>(g, a, row, col, scale);
     const uint32_t base = smem_addr(strip);
     __syncwarp();  // earlier reads of the strip are complete
 #pragma unroll
@@ -272,7 +284,7 @@ __device__ __forceinline__ void strip_load_row(const uint8_t* strip, int k, uint
 }
 
 // width: columns of this warp's part (WIDTH, or half of it on a split tail tile)
-template <int WIDTH, bool SCALE>
+template <int WIDTH, int SCALE>
 __device__ __forceinline__ void epi_store_grad(const TileArgs& a, int row0, int col0, uint32_t taddr, int width,
                                                uint8_t* strip) {
     const int lane = threadIdx.x & 31;
@@ -281,7 +293,7 @@ __device__ __forceinline__ void epi_store_grad(const TileArgs& a, int row0, int 
 #pragma unroll 1
     for (int c = 0; c < width; c += 32) {
         uint32_t t[4][8];
-        strip_transpose<SCALE>(taddr + c, strip, t, a, row0 + lane, col0 + c);
+        strip_transpose<SCALE>(taddr + c, strip, t, a, row0 + lane, col0 + c, tensor_scale<SCALE>(a));
         if (col + c < a.d_in) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -292,7 +304,7 @@ __device__ __forceinline__ void epi_store_grad(const TileArgs& a, int row0, int 
 
 // Dense states: binary32 (BF16S = false) or bfloat16 rounded stochastically with their own Philox
 // streams (BF16S = true).  The update always runs on binary32 moments; only their storage differs.
-template <int OPT, int WIDTH, bool BF16S, bool SCALE, int R>
+template <int OPT, int WIDTH, bool BF16S, int SCALE, int R>
 __device__ __forceinline__ void epi_opt_dense(const TileArgs& a, const OptScalars& s, int row0, int col0,
                                               uint32_t taddr, int width, uint8_t* strip, int row0n = -1,
                                               int col0n = 0) {
@@ -303,6 +315,7 @@ __device__ __forceinline__ void epi_opt_dense(const TileArgs& a, const OptScalar
     // first element of this lane's 8-column run in row (row0 + lane/4); rows k = 1..3 follow at +8 rows
     const size_t lane_base = static_cast<size_t>(row) * a.d_in + col;
     const size_t row_step = static_cast<size_t>(8) * a.d_in;
+    const float scale = tensor_scale<SCALE>(a);
 #pragma unroll 1
     for (int c = 0; c < width; c += 32) {
         // R of the four row groups hold their W/m/v in registers at once: all four with two
@@ -349,7 +362,7 @@ __device__ __forceinline__ void epi_opt_dense(const TileArgs& a, const OptScalar
                 }
             }
             // the gradient strip goes to shared memory once; each row group then reads its 8 values
-            if (kk == 0) strip_store<SCALE>(taddr + c, strip, a, row0 + lane, col0 + c);
+            if (kk == 0) strip_store<SCALE>(taddr + c, strip, a, row0 + lane, col0 + c, scale);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int k = kk + r;
@@ -495,7 +508,7 @@ __device__ __forceinline__ void int8_row_load(const TileArgs& a, size_t e, bool 
 // position c ^ (r mod 8).  Half the rows at a time keep the strip at 4 KiB a warp, so 16 epilogue
 // warps leave shared memory for 5 operand stages.  The TMEM reads are warp-wide; only the lanes of
 // rows 16 hh .. 16 hh + 15 store (16 lanes x 16 bytes: two wavefronts, no bank conflict).
-template <bool SCALE>
+template <int SCALE>
 __device__ __forceinline__ void int8_strip_store(uint32_t taddr, uint8_t* strip, const TileArgs& a, int row0,
                                                  int col0, int hh) {
     const uint32_t lane = threadIdx.x & 31u;
@@ -512,8 +525,8 @@ __device__ __forceinline__ void int8_strip_store(uint32_t taddr, uint8_t* strip,
         tmem_ld_wait(g);
         // per-channel scales here; a per-tensor scale multiplies each lane's 8 values as it reads
         // them (int8_scale_run), once per element rather than once per half
-        if (SCALE && a.row_scales != nullptr)
-            scale_strip<SCALE>(g, a, row0 + static_cast<int>(lane), col0 + 32 * static_cast<int>(h));
+        if (SCALE == kOpsE4M3 && a.row_scales != nullptr)
+            scale_strip<SCALE>(g, a, row0 + static_cast<int>(lane), col0 + 32 * static_cast<int>(h), 1.0f);
         if (mine) {
 #pragma unroll
             for (uint32_t j = 0; j < 8; ++j)
@@ -524,13 +537,13 @@ __device__ __forceinline__ void int8_strip_store(uint32_t taddr, uint8_t* strip,
     __syncwarp();
 }
 
-// A per-tensor gradient scale (E4M3 operands), applied to the values a lane reads from the strip.
-template <bool SCALE>
-__device__ __forceinline__ void int8_scale_run(const TileArgs& a, uint32_t (&g)[8]) {
+// A per-tensor gradient scale, applied to the values a lane reads from the strip.
+template <int SCALE>
+__device__ __forceinline__ void int8_scale_run(const TileArgs& a, uint32_t (&g)[8], float scale) {
     if constexpr (SCALE) {
-        if (a.row_scales == nullptr) {
+        if (SCALE == kOpsBF16Scaled || a.row_scales == nullptr) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] = __float_as_uint(__fmul_rn(__uint_as_float(g[j]), a.g_scale));
+            for (int j = 0; j < 8; ++j) g[j] = __float_as_uint(__fmul_rn(__uint_as_float(g[j]), scale));
         }
     }
 }
@@ -612,13 +625,14 @@ __device__ __forceinline__ void int8_row_update(const TileArgs& a, const OptScal
 // rsub + 4k) this warp updates, first | (end << 4): all eight, or on a split tail tile, where the
 // 16-warp epilogue (no PREFETCH) gives each 64-column block to two warps, k < 4 or k >= 4.  Rows
 // are staged in two halves (int8_strip_store): iterations 0..3, then 4..7.
-template <int OPT, int WIDTH, bool SCALE, bool PREFETCH>
+template <int OPT, int WIDTH, int SCALE, bool PREFETCH>
 __device__ __forceinline__ void epi_opt_int8(const TileArgs& a, const OptScalars& s, int row0, int col0,
                                              uint32_t taddr, int width, uint8_t* strip, int krange) {
     static_assert(WIDTH % 64 == 0, "whole quantisation blocks");
     const uint32_t lane = threadIdx.x & 31u;
     const uint32_t q = lane & 7u, rsub = lane >> 3;  // column run (8 columns) and first row of this lane
     const int row = row0 + static_cast<int>(rsub);
+    const float scale = tensor_scale<SCALE>(a);
 #pragma unroll 1
     for (int c = 0; c < width; c += 64) {
         // d_in is a multiple of 64, so a 64-column block lies wholly inside or outside the layer:
@@ -640,7 +654,7 @@ __device__ __forceinline__ void epi_opt_int8(const TileArgs& a, const OptScalars
                         int8_row_load<OPT>(a, e0 + (k + 1) * row_step, row + 4 * (k + 1) < a.d_out, in[(k + 1) & 1]);
                     uint32_t g[8];
                     int8_strip_load_run(strip, rsub + 4u * kk, q, g);
-                    int8_scale_run<SCALE>(a, g);
+                    int8_scale_run<SCALE>(a, g, scale);
                     int8_row_update<OPT>(a, s, e0 + k * row_step, row + 4 * k < a.d_out, g, in[k & 1]);
                 }
             }
@@ -660,7 +674,7 @@ __device__ __forceinline__ void epi_opt_int8(const TileArgs& a, const OptScalars
                     int8_row_load<OPT>(a, e, ok, in);
                     uint32_t g[8];
                     int8_strip_load_run(strip, rsub + 4u * kk, q, g);
-                    int8_scale_run<SCALE>(a, g);
+                    int8_scale_run<SCALE>(a, g, scale);
                     int8_row_update<OPT>(a, s, e, ok, g, in);
                 }
             }
@@ -711,7 +725,7 @@ __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
     static_assert(CL == 1 || CL == 2, "cluster size");
     static_assert(OPS == kOpsBF16 || EPI != kEpiDX, "the input gradient takes bf16 operands");
     using O = OperandTraits<OPS>;
-    constexpr bool kScale = OPS == kOpsE4M3;
+    constexpr int kScale = OPS;
     constexpr int CG = CL;                    // CTAs per MMA (cta_group)
     using C = TileCfg<BN, CG, EPI, OPS>;
     constexpr bool kAKMajor = EPI == kEpiDX;  // A = dY with d_out (= K) along memory
@@ -770,7 +784,7 @@ __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
     const AbortCtx ab{abort_flag, a0.status, a0.wait_limit_ns};
     // pair kernels with bf16 operands run the tiles from split_from on as two 256 x 128 halves
     // (schedule.h, split_tail_from); the others take split_from = the tile count
-    constexpr bool kSplitTail = CG == 2 && BN == 256 && OPS == kOpsBF16;
+    constexpr bool kSplitTail = CG == 2 && BN == 256 && OPS != kOpsE4M3;
     const int layer_tiles = grp.tile_start[grp.n];
     const int num_tiles = kSplitTail ? layer_tiles + (layer_tiles - split_from) : layer_tiles;
     uint64_t n_issued = 0;   // producer: stages passed (armed and copied, but for the withheld one)
