@@ -758,7 +758,7 @@ forge_status run_loss_products(const Machine& mc, const LossBackward& l, const L
 constexpr int kFinishThreads = 512;
 
 __device__ __forceinline__ void join(float& m, float& s, float vm, float vs) {
-    const float mn = fmaxf(m, vm), base = mn == -INFINITY ? 0.0f : mn;
+    const float mn = fmaxf(m, vm), base = forge::stats_base(mn);
     s = s * forge::exp2_fast(m - base) + vs * forge::exp2_fast(vm - base);
     m = mn;
 }

@@ -509,10 +509,13 @@ __device__ __forceinline__ void epi_gated_bwd(const BlockProblem& b, const Acc& 
     }
 }
 
-// One pass over the warp's columns with the running maximum and sum, in base 2.  A row whose logits
-// so far are all -inf keeps sum 0.  Maxima and sums run in four chains each, the sums in pairs of
-// binary32: a single chain of dependent operations over 128 columns took longer than the products of a
-// 1024-long reduction, and set the tile's pace.
+// What a row's exponentials are taken relative to, given its maximum so far: an infinite one takes nothing out, so
+// that a row of -inf keeps sum 0 and a row with +inf has sum +inf.
+__device__ __forceinline__ float stats_base(float top) { return fabsf(top) == INFINITY ? 0.0f : top; }
+
+// One pass over the warp's columns with the running maximum and sum, in base 2.  Maxima and sums run in
+// four chains each, the sums in pairs of binary32: a single chain of dependent operations over 128 columns
+// took longer than the products of a 1024-long reduction, and set the tile's pace.
 template <int BN, class Acc>
 __device__ __forceinline__ void epi_loss_stats(const BlockProblem& b, const Acc& acc, int row, int nb, int h) {
     const bool mine = row < b.rows;
@@ -543,7 +546,7 @@ __device__ __forceinline__ void epi_loss_stats(const BlockProblem& b, const Acc&
 #pragma unroll
         for (int j = 4; j < kStep; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(g[j]));
         const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e);
-        const float base = mn == -INFINITY ? 0.0f : mn;
+        const float base = stats_base(mn);
         const F2 scale = F2::all(kLog2e), less = F2::all(-base);
         F2 e[4];
 #pragma unroll

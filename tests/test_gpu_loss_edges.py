@@ -51,3 +51,23 @@ def test_a_dloss_that_is_not_finite_stays_in_its_row(T, V, D, bad):
     d = g @ W
     tol = (1 + U8) * (rounded(g, W) + acc(d, V) + eg @ W.abs()) + U8 * d.abs() + 1e-30
     assert_close(dX[rest], d[rest], tol[rest], "dX of the other tokens")
+
+
+@pytest.mark.parametrize("T, V, D", [(40, 300, 64), (3, 5001, 64)])
+def test_an_infinite_logit(T, V, D):
+    """log sum exp with one term +inf is +inf, and so is the loss of every other target; a row whose logits are
+    all -inf has -inf."""
+    x, w, t, _ = _inputs(T, V, D, 2)
+    w[:, 0] = w[:, 0].abs() + 2 ** -10
+    w[5, 0] = -1.0
+    x[1, 0] = float("inf")     # +inf everywhere but at entry 5, which is -inf
+    x[2, 0] = float("-inf")    # +inf at entry 5 alone, -inf elsewhere
+    t[1], t[2] = 5, 7
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    fg.linear_cross_entropy(x, w, t, loss, lse)
+    assert fg.sync_status() == 0
+    want = torch.logsumexp(x.to(F64) @ w.to(F64).T, 1)
+    inf = float("inf")
+    assert [float(v) for v in want[1:3]] == [inf, inf]
+    assert [float(v) for v in lse[1:3]] == [inf, inf] and [float(v) for v in loss[1:3]] == [inf, inf]
+    assert torch.isfinite(lse[0]) and torch.isfinite(lse[3:]).all()
