@@ -225,7 +225,8 @@ __device__ __forceinline__ void act_both(float g, int act, float& value, float& 
     } else {
         const float p = sigmoid_fast(kGelu2 * (g + 0.044715f * g * g * g));
         value = g * p;
-        slope = p + g * p * (1.0f - p) * (kGelu2 * (1.0f + 3.0f * 0.044715f * g * g));
+        // p (1 - p) is 0 long before g^2 is 1e30, and times infinity it would be NaN
+        slope = p + g * p * (1.0f - p) * (kGelu2 * (1.0f + 3.0f * 0.044715f * fminf(g * g, 1e30f)));
     }
 }
 
