@@ -69,7 +69,7 @@ class ForgeLinear(torch.nn.Module):
         if state not in _STATE_DTYPES:
             raise ValueError("state: 'fp32', 'bf16' or 'int8'")
         dev = torch.device("cuda") if device is None else torch.device(device)
-        w = torch.randn(out_features, in_features, device=dev) * init_std
+        w = torch.randn(out_features, in_features, dtype=torch.float32, device=dev) * init_std
         # the backward itself updates the weight: autograd gives it no gradient
         self.weight = torch.nn.Parameter(w.to(torch.bfloat16), requires_grad=False)
         use_m, use_v = _MOMENTS[opt]
@@ -79,7 +79,8 @@ class ForgeLinear(torch.nn.Module):
         self.register_buffer("v", torch.zeros(shape, dtype=sdt, device=dev) if use_v else None)
         q = state == "int8" and (use_m or use_v)
         # all-zero codes decode to zero whatever their scale
-        self.register_buffer("qscales", torch.zeros(2 * out_features * in_features // 64, device=dev) if q else None)
+        self.register_buffer("qscales", torch.zeros(2 * out_features * in_features // 64, dtype=torch.float32, device=dev)
+                             if q else None)
         self.opt, self.hp, self.seed = opt, hp, int(seed)
         self.step = 1
         self._pending: Optional[int] = None

@@ -29,13 +29,18 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
     return t.reshape(-1, t.shape[-1]).contiguous()
 
 
+def _f32(n: int, device) -> torch.Tensor:
+    """FP32 whatever PyTorch's default type is."""
+    return torch.empty(n, dtype=torch.float32, device=device)
+
+
 class _NormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, kind, eps):
         X = _rows(x.detach())
         y = torch.empty_like(X)
-        mean = torch.empty(X.shape[0], device=X.device) if kind == "layer" else None
-        rstd = torch.empty(X.shape[0], device=X.device)
+        mean = _f32(X.shape[0], X.device) if kind == "layer" else None
+        rstd = _f32(X.shape[0], X.device)
         ops.layer_norm(X, weight, bias, y, mean, rstd, eps=eps, kind=kind)
         ctx.save_for_backward(X, weight, mean, rstd)
         ctx.kind, ctx.has_bias = kind, bias is not None
@@ -45,7 +50,7 @@ class _NormFn(torch.autograd.Function):
     def backward(ctx, grad_out):
         X, weight, mean, rstd = ctx.saved_tensors
         dy = _rows(grad_out).to(X.dtype)
-        dx, dw = torch.empty_like(X), torch.empty(X.shape[1], device=X.device)
+        dx, dw = torch.empty_like(X), _f32(X.shape[1], X.device)
         db = torch.empty_like(dw) if ctx.kind == "layer" else None
         ops.layer_norm_backward(dy, X, weight, mean, rstd, dx, dw, db, kind=ctx.kind)
         return (dx.view(grad_out.shape), dw.to(weight.dtype), db.to(weight.dtype) if ctx.has_bias else None, None, None)
@@ -60,8 +65,9 @@ class ForgeNorm(torch.nn.Module):
         if kind not in ops.NORM_KINDS:
             raise ValueError(f"kind: {kind!r}, expected one of {list(ops.NORM_KINDS)}")
         dev = torch.device("cuda") if device is None else torch.device(device)
-        self.weight = torch.nn.Parameter(torch.ones(width, device=dev))
-        self.bias = torch.nn.Parameter(torch.zeros(width, device=dev)) if kind == "layer" and bias else None
+        self.weight = torch.nn.Parameter(torch.ones(width, dtype=torch.float32, device=dev))
+        self.bias = (torch.nn.Parameter(torch.zeros(width, dtype=torch.float32, device=dev)) if kind == "layer" and bias
+                     else None)
         self.kind, self.eps = kind, float(eps)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
@@ -84,14 +90,14 @@ class _Trained(torch.nn.Module):
         use_m, use_v = _MOMENTS[opt]
         sdt = _STATE_DTYPES[state]
         for name, shape in shapes.items():
-            w = (torch.randn(shape, device=dev) * init_std).to(torch.bfloat16)
+            w = (torch.randn(shape, dtype=torch.float32, device=dev) * init_std).to(torch.bfloat16)
             # the backward itself updates the weight: autograd gives it no gradient
             self.register_parameter(name, torch.nn.Parameter(w, requires_grad=False))
             self.register_buffer(f"{name}_m", torch.zeros(shape, dtype=sdt, device=dev) if use_m else None)
             self.register_buffer(f"{name}_v", torch.zeros(shape, dtype=sdt, device=dev) if use_v else None)
             q = state == "int8" and (use_m or use_v)
             # all-zero codes decode to zero whatever their scale
-            self.register_buffer(f"{name}_q", torch.zeros(2 * w.numel() // 64, device=dev) if q else None)
+            self.register_buffer(f"{name}_q", torch.zeros(2 * w.numel() // 64, dtype=torch.float32, device=dev) if q else None)
         self.opt, self.hp, self.seed = opt, hp, int(seed)
         self.step = 1
         self._pending: Optional[int] = None
@@ -205,14 +211,14 @@ class ForgeHeadLoss(_Trained):
         self.ignore_index = int(ignore_index)
 
     def _losses(self, X, t):
-        loss, lse = (torch.empty(X.shape[0], device=X.device) for _ in range(2))
+        loss, lse = (_f32(X.shape[0], X.device) for _ in range(2))
         ops.linear_cross_entropy(X, self.weight.data, t, loss, lse, ignore_index=self.ignore_index)
         return loss, lse
 
     def _share(self, t):
         """What each token's loss counts for in the mean."""
         counts = t != self.ignore_index
-        return counts / counts.sum().clamp_min(1)
+        return counts.float() / counts.sum().clamp_min(1)
 
     def forward(self, x: torch.Tensor, target: torch.Tensor) -> torch.Tensor:
         if x.dtype != torch.bfloat16:
