@@ -16,6 +16,7 @@ one forward.
 """
 from __future__ import annotations
 
+import functools
 from typing import Any, Optional
 
 import torch
@@ -34,6 +35,38 @@ _MOMENTS = {
 _STATE_DTYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "int8": torch.int8}
 
 
+class _NotTwice(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, anchor, what, *grads):
+        ctx.what = what
+        return tuple(g.view_as(g) for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.what}: the gradient cannot be differentiated")
+
+
+def once(what: str):
+    """For a backward pass made of the library's calls, which has no derivative of its own.  Under create_graph its
+    results would be constants, and a second derivative would leave out their terms without an error (also with
+    torch's once_differentiable, where the incoming gradient needs none): differentiating them raises one."""
+    def decorate(backward):
+        @functools.wraps(backward)
+        def wrapper(ctx, *grad_outputs):
+            with torch.no_grad():
+                grads = backward(ctx, *grad_outputs)
+            # a gradient that is passed on as it came (a residual's) keeps its own graph
+            own = [i for i, g in enumerate(grads) if g is not None and not any(g is o for o in grad_outputs)]
+            if not own or not torch.is_grad_enabled():
+                return grads
+            out = list(grads)
+            for i, g in zip(own, _NotTwice.apply(torch.zeros((), requires_grad=True), what, *(grads[i] for i in own))):
+                out[i] = g
+            return tuple(out)
+        return wrapper
+    return decorate
+
+
 class _ForgeLinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, layer, want_dx):
@@ -42,6 +75,7 @@ class _ForgeLinearFn(torch.autograd.Function):
         return torch.nn.functional.linear(x, weight)
 
     @staticmethod
+    @once("ForgeLinear")
     def backward(ctx, grad_out):
         (x,) = ctx.saved_tensors
         dY = grad_out.reshape(-1, grad_out.shape[-1]).to(torch.bfloat16).contiguous()

@@ -6,7 +6,8 @@ They put the library's operators (operators.py) behind PyTorch autograd, next to
 mechanism): the backward pass itself updates them and their optimizer state, their gradients never
 exist, and the same limits hold: one backward per forward, no weight shared with another layer of
 the same backward, one optimizer step per micro-batch.  `ForgeNorm`'s weight and bias are vectors with
-ordinary gradients, for an ordinary optimizer.
+ordinary gradients, for an ordinary optimizer.  No gradient of these modules can be differentiated again:
+it raises an error.
 
     norm1, mlp = ForgeNorm(1024), ForgeGatedMLP(1024, 4096, opt="adamw", hp=hp)
     norm2, head = ForgeNorm(1024), ForgeHeadLoss(1024, vocab, opt="adamw", hp=hp, seed=3)
@@ -20,7 +21,7 @@ from typing import Any, Optional
 import torch
 
 from . import operators as ops
-from .autograd import _MOMENTS, _STATE_DTYPES
+from .autograd import _MOMENTS, _STATE_DTYPES, once
 
 __all__ = ["ForgeNorm", "ForgeGatedMLP", "ForgeHeadLoss"]
 
@@ -47,6 +48,7 @@ class _NormFn(torch.autograd.Function):
         return y.view(x.shape)
 
     @staticmethod
+    @once("ForgeNorm")
     def backward(ctx, grad_out):
         X, weight, mean, rstd = ctx.saved_tensors
         dy = _rows(grad_out).to(X.dtype)
@@ -128,6 +130,7 @@ class _GatedFn(torch.autograd.Function):
         return Y.view(x.shape)
 
     @staticmethod
+    @once("ForgeGatedMLP")
     def backward(ctx, grad_out):
         X, G, U = ctx.saved_tensors
         b = ctx.block
@@ -186,6 +189,7 @@ class _HeadFn(torch.autograd.Function):
         return (loss * share).sum()
 
     @staticmethod
+    @once("ForgeHeadLoss")
     def backward(ctx, grad_out):
         X, t, lse, share = ctx.saved_tensors
         h = ctx.head
