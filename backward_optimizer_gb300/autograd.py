@@ -67,6 +67,35 @@ def once(what: str):
     return decorate
 
 
+class Stepped(torch.nn.Module):
+    """A module whose backward takes an optimizer step: number `step`, from 1.  The step goes with the weights and
+    moments into the state dict, under "step"; a module that has not trained yet has no such entry."""
+
+    _version = 2  # of the state dict: since 2 it holds the step
+
+    def __init__(self):
+        super().__init__()
+        self.step = 1
+        self._pending: Optional[int] = None
+
+    def _save_to_state_dict(self, destination, prefix, keep_vars):
+        super()._save_to_state_dict(destination, prefix, keep_vars)
+        if self.step != 1:
+            destination[prefix + "step"] = torch.tensor(self.step)
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs):
+        super()._load_from_state_dict(state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs)
+        key = prefix + "step"
+        if key in unexpected_keys:
+            unexpected_keys.remove(key)
+        if key in state_dict:
+            self.step = int(state_dict[key])
+        elif local_metadata.get("version", 2) >= 2:
+            self.step = 1
+        # a state dict of version 1 says nothing about the step: it stays as the caller has set it
+        self._pending = None  # a forward from before has no weights to step
+
+
 class _ForgeLinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, layer, want_dx):
@@ -85,7 +114,7 @@ class _ForgeLinearFn(torch.autograd.Function):
         return (None if dX is None else dX.reshape(x.shape)), None, None, None
 
 
-class ForgeLinear(torch.nn.Module):
+class ForgeLinear(Stepped):
     """y = x W^T with W [out_features, in_features] bf16, trained by the fused backward.
 
     opt: one of adamw, nadam, radam, lion, rmsprop, adagrad, sgd, sgd_momentum.  hp: an object or
@@ -93,7 +122,7 @@ class ForgeLinear(torch.nn.Module):
     momentum_decay, lr_decay); missing fields take the library's defaults.  state: "fp32", "bf16"
     (stochastically rounded) or "int8" (codes with one scale per 64 elements; in_features a multiple
     of 64) moments.  seed: this layer's stochastic-rounding seed, distinct per layer.  `step` is the
-    optimizer step the next backward takes; it starts at 1."""
+    optimizer step the next backward takes; it starts at 1 and is part of the state dict."""
 
     def __init__(self, in_features: int, out_features: int, opt: str = "adamw", hp: Any = None,
                  state: str = "fp32", seed: int = 0, device=None, init_std: float = 0.02):
@@ -116,8 +145,6 @@ class ForgeLinear(torch.nn.Module):
         self.register_buffer("qscales", torch.zeros(2 * out_features * in_features // 64, dtype=torch.float32, device=dev)
                              if q else None)
         self.opt, self.hp, self.seed = opt, hp, int(seed)
-        self.step = 1
-        self._pending: Optional[int] = None
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if x.dtype != torch.bfloat16:

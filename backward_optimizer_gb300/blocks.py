@@ -21,7 +21,7 @@ from typing import Any, Optional
 import torch
 
 from . import operators as ops
-from .autograd import _MOMENTS, _STATE_DTYPES, once
+from .autograd import _MOMENTS, _STATE_DTYPES, Stepped, once
 
 __all__ = ["ForgeNorm", "ForgeGatedMLP", "ForgeHeadLoss"]
 
@@ -79,7 +79,7 @@ class ForgeNorm(torch.nn.Module):
         return f"{self.weight.shape[0]}, kind={self.kind}, eps={self.eps}, bias={self.bias is not None}"
 
 
-class _Trained(torch.nn.Module):
+class _Trained(Stepped):
     """Matrices with the optimizer state that their backward pass updates."""
 
     def __init__(self, shapes: dict, opt: str, hp: Any, state: str, seed: int, device, init_std: float):
@@ -101,8 +101,6 @@ class _Trained(torch.nn.Module):
             # all-zero codes decode to zero whatever their scale
             self.register_buffer(f"{name}_q", torch.zeros(2 * w.numel() // 64, dtype=torch.float32, device=dev) if q else None)
         self.opt, self.hp, self.seed = opt, hp, int(seed)
-        self.step = 1
-        self._pending: Optional[int] = None
 
     def _layer(self, name: str, seed: int):
         return (getattr(self, name).data, getattr(self, f"{name}_m"), getattr(self, f"{name}_v"),

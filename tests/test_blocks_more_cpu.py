@@ -102,3 +102,33 @@ def test_a_second_derivative_through_forge_linear_raises(monkeypatch):
     (g,) = torch.autograd.grad(layer(x).float().sum() + (x.float() ** 2).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="ForgeLinear: the gradient cannot be differentiated"):
         g.float().square().sum().backward()
+
+
+@pytest.mark.parametrize("make", [lambda: ForgeLinear(64, 32, device="cpu"), lambda: ForgeGatedMLP(64, 128, device="cpu"),
+                                  lambda: ForgeHeadLoss(64, 100, state="int8", device="cpu")])
+def test_the_step_is_part_of_the_state(make, tmp_path):
+    def model():
+        return torch.nn.ModuleDict({"a": make(), "b": make()})
+    m = model()
+    assert not any(k.endswith("step") for k in m.state_dict())
+    m["a"].step = 7
+    m["a"]._pending = 7
+    torch.save(m.state_dict(), tmp_path / "s")
+    for state in (torch.load(tmp_path / "s"), {k: v.clone() for k, v in m.state_dict().items()}):
+        n = model()
+        n["b"].step = 3
+        n["a"]._pending = 1
+        n.load_state_dict(state)  # strict
+        assert n["a"].step == 7 and n["b"].step == 1 and type(n["a"].step) is int
+        assert n["a"]._pending is None
+    # a fresh state resets, and one saved before the step was part of it leaves the step to the caller
+    m.load_state_dict(model().state_dict())
+    assert m["a"].step == 1
+    old = model().state_dict()
+    for k in old._metadata:
+        old._metadata[k] = {"version": 1}
+    m["a"].step = 9
+    m.load_state_dict(old)
+    assert m["a"].step == 9
+    with pytest.raises(RuntimeError, match="nexpected key"):
+        m.load_state_dict({**old, "a.other": torch.zeros(1)})
