@@ -829,6 +829,16 @@ forge_status run_loss_begin(const LossBackward& l, const forge_loss_shape& s, co
                                           reinterpret_cast<uint32_t*>(ws + l.split.counts), l.split.n_counts));
 }
 
+void describe(const Plan& p, int32_t* tile_cols, int32_t* whole, int32_t* cut, int32_t* parts) {
+    *tile_cols = p.bn;
+    for (int i = 0; i < p.n; ++i) {
+        const Cut& c = p.cut[i];
+        *whole += c.split_from;
+        *cut += c.tiles_m * c.tiles_n - c.split_from;
+        *parts = std::max(*parts, c.parts);
+    }
+}
+
 }  // namespace
 
 extern "C" {
@@ -1089,6 +1099,45 @@ forge_status forge_linear_cross_entropy_step(const void* X, void* W, const int64
         FORGE_TRY(host::fused_rows(ws + l.g, p.ld, X, s.T, p.v0, p.n, W, m, v, qscales, opt_kind, hp, s.vocab, s.d_model,
                                    state, step, seed ^ (static_cast<uint64_t>(i) << 40),
                                    reinterpret_cast<const float*>(ws + l.unit), stream));
+    }
+    return FORGE_OK;
+}
+
+forge_status forge_gated_mlp_launch_shape(const forge_gated_shape* shape, int32_t launch, int32_t* tile_cols,
+                                          int32_t* whole, int32_t* cut, int32_t* parts) {
+    FORGE_TRY(check_gated(shape));
+    if (tile_cols == nullptr || whole == nullptr || cut == nullptr || parts == nullptr || launch < 0 || launch > 3)
+        return FORGE_ERR_INVALID_ARGUMENT;
+    *tile_cols = *whole = *cut = *parts = 0;
+    if (shape->T == 0) return FORGE_OK;
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    if (launch < 2) {
+        const GatedForward l = layout_gated_forward(mc, *shape);
+        if (!l.few) describe(launch == 0 ? l.up : l.down, tile_cols, whole, cut, parts);
+    } else {
+        const GatedBackward l = layout_gated_backward(mc, *shape, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                                                      nullptr, nullptr, true, true, nullptr);
+        describe(launch == 2 ? l.dh : l.grads, tile_cols, whole, cut, parts);
+    }
+    return FORGE_OK;
+}
+
+forge_status forge_linear_cross_entropy_launch_shape(const forge_loss_shape* shape, int32_t launch, int32_t* tile_cols,
+                                                     int32_t* whole, int32_t* cut, int32_t* parts) {
+    FORGE_TRY(check_loss(shape));
+    if (tile_cols == nullptr || whole == nullptr || cut == nullptr || parts == nullptr || launch < 0 || launch > 2)
+        return FORGE_ERR_INVALID_ARGUMENT;
+    *tile_cols = *whole = *cut = *parts = 0;
+    if (shape->T == 0) return FORGE_OK;
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    if (launch == 0) {
+        describe(layout_loss_forward(mc, *shape).plan, tile_cols, whole, cut, parts);
+    } else {
+        const LossBackward l = layout_loss_backward(mc, *shape, true, true);
+        const LossPiece p = loss_piece_of(mc, *shape, l, 0, nullptr, nullptr, nullptr, nullptr, true, true, nullptr);
+        describe(launch == 1 ? p.grad : p.out, tile_cols, whole, cut, parts);
     }
     return FORGE_OK;
 }

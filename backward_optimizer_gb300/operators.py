@@ -51,6 +51,8 @@ def declare(L: ctypes.CDLL) -> None:
         "forge_linear_cross_entropy": [vp] * 6 + [i64, loss, vp],
         "forge_linear_cross_entropy_backward": [vp] * 8 + [i64, loss, vp],
         "forge_linear_cross_entropy_step": [vp] * 10 + [i64, i32, ctypes.c_int, hp, loss, i64, u64, vp],
+        "forge_gated_mlp_launch_shape": [gated, i32] + [ctypes.POINTER(i32)] * 4,
+        "forge_linear_cross_entropy_launch_shape": [loss, i32] + [ctypes.POINTER(i32)] * 4,
     }.items():
         f = getattr(L, name)
         f.argtypes, f.restype = args, ctypes.c_int
@@ -326,3 +328,26 @@ def linear_cross_entropy_step(X, W, target, lse, dloss, dX=None, m=None, v=None,
         *args, dx, p(m), p(v), p(qscales), ws, n, _fg._state_of(m, v), _fg.OPT_KINDS[opt], _fg._hp_arg(hp), shape.arg,
         int(step), int(seed) & (2**64 - 1), raw)
     _fg._check(st, "forge_linear_cross_entropy_step")
+
+
+# ------------------------------------------------------------------ how the products are cut
+
+
+def _launch_shape(name: str, shape, launch: int) -> dict:
+    vals = [ctypes.c_int32() for _ in range(4)]
+    _fg._check(getattr(_fg.lib(), name)(shape.arg, launch, *[ctypes.byref(v) for v in vals]), name)
+    return dict(zip(("tile_cols", "whole", "cut", "parts"), (v.value for v in vals)))
+
+
+def gated_launch_shape(T: int, d_model: int, d_ff: int, launch: str) -> dict:
+    """Tile columns (0: the few-token kernel), whole and cut tiles and parts of a launch of the gated block: "up" (gate
+    and up projection), "down", "dh", "grads" (dX and the weights' gradients)."""
+    return _launch_shape("forge_gated_mlp_launch_shape", _shape(GatedShape, T, d_model, d_ff, 0, 0),
+                         _one_of({"up": 0, "down": 1, "dh": 2, "grads": 3}, launch, "launch"))
+
+
+def loss_launch_shape(T: int, vocab: int, d_model: int, launch: str) -> dict:
+    """The same of the head's loss: "stats" (forward), "g" and "grads" (dX and dW) of the backward pass's first piece of
+    the vocabulary."""
+    return _launch_shape("forge_linear_cross_entropy_launch_shape", _shape(LossShape, T, vocab, d_model, -100, 0),
+                         _one_of({"stats": 0, "g": 1, "grads": 2}, launch, "launch"))

@@ -436,6 +436,18 @@ FORGE_API void forge_set_wait_limit_ns(uint64_t ns);
  * CUDA context stays usable.  The outputs of that one call are unspecified.  No fault is raised. */
 FORGE_API void forge_debug_withhold_next_stage(void);
 
+/* How the products of the operators around the fused layers are cut on the current device: columns per tile (256 on
+ * CTA pairs, with 256 rows; 128 or 64 on single CTAs, with 128 rows; 0: the few-token kernel, which has no tiles),
+ * tiles that run whole, tiles cut along the reduction, and into how many parts at most; of all products of the
+ * launch together.  launch, gated block: 0 gate and up projection, 1 down projection, 2 dH, 3 dX and the weights'
+ * gradients.  launch, loss: 0 the logits' statistics, 1 g of the backward pass's first piece of the vocabulary,
+ * 2 dX and dW of that piece. */
+FORGE_API forge_status forge_gated_mlp_launch_shape(const forge_gated_shape *shape, int32_t launch, int32_t *tile_cols,
+                                                    int32_t *whole, int32_t *cut, int32_t *parts);
+FORGE_API forge_status forge_linear_cross_entropy_launch_shape(const forge_loss_shape *shape, int32_t launch,
+                                                               int32_t *tile_cols, int32_t *whole, int32_t *cut,
+                                                               int32_t *parts);
+
 /* The tile shape and persistent grid forge_fused_dw_step (and forge_dw_gemm) use for `shape` with
  * bf16 operands: rows x columns of W per tile (256 x 256 on a CTA pair, a group of the method's
  * 128 x 128 tiles, §2 Methodology; 128 x 256 or 128 x 128 on one CTA; a layer whose wider shape
