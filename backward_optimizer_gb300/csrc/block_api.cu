@@ -685,7 +685,7 @@ LossPiece loss_piece_of(const Machine& mc, const forge_loss_shape& s, const Loss
     }
     if (dw) {
         Product w = product_dw(ws + l.g, p.ld, X, s.T, p.n, s.d_model, static_cast<char*>(dW) + row);
-        w.a[0].cols = p.ld;  // g's padding is finite and ends in rows of dW that are not stored
+        w.a[0].cols = p.ld;  // g's padding (exp(-lse), which may be infinite) ends in rows of dW that are not stored
         p.pr[p.np++] = w;
     }
     for (int j = 0; j < p.np; ++j) p.pr[j].unit = reinterpret_cast<const float*>(ws + l.unit);
@@ -711,8 +711,8 @@ LossBackward layout_loss_backward(const Machine& mc, const forge_loss_shape& s, 
 
 // Whether a launch of its own finds the largest dloss and clears the counters (loss_begin_kernel), or the first
 // piece's gradient does: it can where it is not cut itself, and where a warp's look at every dloss ends before
-// the first tile does.  130 tokens over 4099 x 512: 24.6 us with the launch, 22.6 without; 1024 over 4096 x 256: 27.9
-// and 26.3; 2048: 38.8 and 39.7.
+// the first tile does.  In turn on one GPU: 130 tokens over 4099 x 512 24.6 us with the launch, 22.6 without; 1024 over
+// 4096 x 256 27.9 and 26.3; 2048 38.8 and 39.7.
 constexpr int64_t kOwnUnitRows = 1024;
 
 bool loss_begins(const LossPiece& p, const forge_loss_shape& s) { return p.grad.counts > 0 || s.T > kOwnUnitRows; }

@@ -3,7 +3,9 @@ entropy of a linear head, each with its backward pass.
 
 Like the rest of the binding this module checks and marshals arguments; the computation is the
 library's.  Results are written to the tensors passed for them.  Tensors are contiguous and on the
-current device.  Workspace comes from PyTorch's allocator, for the stream that the call runs on.
+current device.  Workspace comes from PyTorch's allocator, for the stream that the call runs on.  Calls on
+the current stream that need up to 16 MiB of it keep it from call to call, one buffer per host thread and
+stream until the thread ends, from the memory pool that was in use when it was made.
 `include/forge.h` documents every operator's formulas, types and special cases.
 """
 from __future__ import annotations

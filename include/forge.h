@@ -291,7 +291,8 @@ FORGE_API forge_status forge_linear_backward(const void *dY, const void *X, void
  * arguments the operator refuses or without a device), 256-byte aligned, free for other use once the
  * call's work on the stream is done.  Matrices are 32-byte aligned.  Sums are FP32; a value is rounded
  * to bfloat16 where it is stored as an operand of the next product, and nowhere else.  Results do not
- * depend on timing: the same call on the same inputs gives the same bits.
+ * depend on timing: the same call on the same inputs gives the same bits.  Outputs overlap no input and one
+ * another nowhere but where an operator allows it.
  */
 
 typedef enum forge_norm_kind { FORGE_NORM_LAYER = 0, FORGE_NORM_RMS = 1 } forge_norm_kind;
@@ -387,8 +388,8 @@ FORGE_API forge_status forge_linear_cross_entropy(const void *X, const void *W, 
 /* Its gradients, given dloss [T] (FP32, the gradient of each token's loss) and the forward pass's lse:
  *   g[t, v] = dloss[t] (exp(x_t . w_v - lse[t]) - [v = target[t]]), 0 where target[t] = ignore_index
  *   dX [T, d_model] = g W, dW [vocab, d_model] = g^T X                     (bfloat16)
- * g is made one piece of the vocabulary at a time, rounded to bfloat16, in the workspace; X has to be
- * finite in ignored tokens too (dW sums 0 times it).  Either of dX
+ * g is made one piece of the vocabulary at a time in the workspace, relative to the largest finite |dloss| and
+ * rounded to bfloat16; X has to be finite in ignored tokens too (dW sums 0 times it).  Either of dX
  * and dW may be null: it is not computed.  A target outside the vocabulary that is not ignore_index
  * makes the gradients NaN.  T = 0 sets dW to zero. */
 FORGE_API forge_status forge_linear_cross_entropy_backward(const void *X, const void *W, const int64_t *target,
