@@ -883,7 +883,7 @@ forge_status forge_gated_mlp(const void* X, const void* Wg, const void* Wu, cons
         r.N = static_cast<int>(s.d_ff);
         r.K = static_cast<int>(s.d_model);
         r.act = s.act;
-        r.withhold = host::take_withhold();
+        r.withhold = host::take_withhold() ? 16 : 0;
         r.status = mc.dev.status;
         r.wait_limit_ns = host::wait_limit_ns();
         FORGE_TRY(cuda_status(forge::launch_rows(r, true, mc.dev.num_sms, stream)));

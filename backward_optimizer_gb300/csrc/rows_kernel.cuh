@@ -43,7 +43,7 @@ struct RowsArgs {
     // The launch before this one on the stream does not write W, and all work before that one is done once
     // this one starts (ptx.cuh): the ring may fill before stream_wait().
     int weights_ready;
-    int withhold;  // test switch: block 0 arms its first slot but never copies into it, so a wait runs out
+    int withhold;  // test switch: bytes that each slot is armed for but never gets, so that waits run out
     int* status;
     uint64_t wait_limit_ns;
 };
@@ -85,8 +85,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) forge_rows_kernel(const RowsA
     auto issue = [&](int k, int slot) {
         const size_t at = (blockIdx.x + static_cast<size_t>(k) * stride) * kN * a.K;
         uint8_t* dst = rows_ring + static_cast<size_t>(slot) * slot_bytes;
-        mbar_arrive_expect_tx(&full[slot], slot_bytes);
-        if (a.withhold && k == 0 && blockIdx.x == 0) return;
+        mbar_arrive_expect_tx(&full[slot], slot_bytes + static_cast<uint32_t>(a.withhold));
         bulk_load(dst, a.w + at, row_bytes * kN, &full[slot]);
         if constexpr (GATED) bulk_load(dst + row_bytes * kN, a.w2 + at, row_bytes * kN, &full[slot]);
     };
@@ -105,24 +104,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1) forge_rows_kernel(const RowsA
     __syncthreads();
     if (warp == kRowsWarps) {
         if (!producer) return;
-        int slot = 0, issued = a.weights_ready ? (a.slots < mine ? a.slots : mine) : 0;
+        int slot = 0;
         uint32_t phase = a.weights_ready ? 1u : 0u;  // of the next turn through the ring
-        for (int k = issued; k < mine; ++k) {
+        for (int k = a.weights_ready ? a.slots : 0; k < mine; ++k) {
             // The slot's first turn finds it empty: the barrier's phase before its first.  Once the flag is up,
             // warps go on without their data and their arrivals say nothing: a slot whose copies have not landed
             // must not be armed again.
             if (!wait_bounded(&empty[slot], phase ^ 1u, ab) || *ab.flag) break;
             issue(k, slot);
-            ++issued;
             if (++slot == a.slots) {
                 slot = 0;
                 phase ^= 1u;
             }
         }
-        // Every copy lands before the block's memory is given up, also where the other warps have aborted and
-        // wait for none.
-        for (int i = 0; i < a.slots && i < issued; ++i)
-            drain_bounded(&full[i], static_cast<uint32_t>(((issued - 1 - i) / a.slots) & 1), a.wait_limit_ns);
         return;
     }
     uint32_t x[T][VECS][4];
@@ -229,6 +223,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) forge_rows_kernel(const RowsA
             phase ^= 1u;
         }
     }
+    // an aborted block's warps have not waited for all copies: they land before its memory is given up
+    if (tid == 0 && *ab.flag) wait_out(a.wait_limit_ns);
 }
 
 }  // namespace forge

@@ -174,6 +174,12 @@ __device__ __forceinline__ void drain_bounded(uint64_t* bar, uint32_t parity, ui
     }
 }
 
+// The same where nothing says which copies are still in flight: they land in microseconds, or not within the limit.
+__device__ __forceinline__ void wait_out(uint64_t limit_ns) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 <= limit_ns) {}
+}
+
 // ---------------------------------------------------------------- epilogues
 // Each is called by one warp for one tile.  The warp owns weight rows row0 .. row0+31 (its TMEM
 // lane quarter) and columns col0 .. col0+WIDTH-1; `taddr` is the TMEM address of (row0, col0);
