@@ -199,7 +199,7 @@ forge_status forge_layer_norm(const void* x, const void* weight, const void* bia
     NormShape n = norm_shape(s, vectors_fit(s, {x, weight, bias, y}), false);
     const int slots = ring_slots(s, n, 1);
     if (slots > 0) {
-        a.withhold = host::take_withhold() ? 16 : 0;
+        a.withhold = host::take_withhold();
         const int blocks = norm_blocks(s, n, dev.num_sms);
         const int64_t smem = n.groups * slots * s.D * (s.x_type == FORGE_TYPE_BF16 ? 2 : 4);
         return run_norm<false>(a, s, n, blocks, static_cast<size_t>(smem), slots, stream);
@@ -262,7 +262,7 @@ forge_status forge_layer_norm_backward(const void* dy, const void* x, const void
     a.status = dev.status;
     a.wait_limit_ns = host::wait_limit_ns();
     const int slots = ring_slots(s, n, add != nullptr ? 3 : 2);
-    if (slots > 0) a.withhold = host::take_withhold() ? 16 : 0;
+    if (slots > 0) a.withhold = host::take_withhold();
     // the rings, and after them the groups' columns
     const int64_t slot_bytes = s.D * (s.x_type == FORGE_TYPE_BF16 ? 2 : 4) * (add != nullptr ? 3 : 2);
     const int64_t smem = n.nv == 0 ? 0 : std::max(n.groups * slots * slot_bytes, n.groups * width * 4);

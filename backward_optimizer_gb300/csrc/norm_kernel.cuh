@@ -64,7 +64,7 @@ struct NormArgs {
     int64_t part_step;
     int* status;     // device status word
     uint64_t wait_limit_ns;
-    int withhold;    // test switch: bytes that each slot is armed for but never gets, so that waits run out
+    int withhold;    // test switch: no group's first slots are armed or filled, so that waits run out
 };
 
 // VEC elements of type TX as they lie in memory
@@ -439,13 +439,13 @@ struct NormRing {
     uint64_t* full;
     int64_t base, stride, rows;
     int slots, D, tensors;
-    uint32_t row_bytes, withhold;
+    uint32_t row_bytes;
     int slot;
     uint32_t phase;
     bool ok;  // this thread's waits so far ended with their copies landed
 
     __device__ __forceinline__ void issue(int64_t k, int at) const {
-        mbar_arrive_expect_tx(&full[at], row_bytes * tensors + withhold);
+        mbar_arrive_expect_tx(&full[at], row_bytes * tensors);
         const int64_t el = (base + k * stride) * D;
         uint8_t* dst = mem + static_cast<size_t>(at) * row_bytes * tensors;
 #pragma unroll
@@ -461,7 +461,7 @@ struct NormRing {
         return smem_addr(mem) + static_cast<uint32_t>(slot) * row_bytes * tensors;
     }
     // thread 0, where every thread of the group is known to be done with row k - 1
-    __device__ __forceinline__ void refill(int64_t k) {
+    __device__ __forceinline__ void refill(int64_t k) const {
         if (ok && k > 0 && k - 1 + slots < rows) issue(k - 1 + slots, slot == 0 ? slots - 1 : slot - 1);
     }
     __device__ __forceinline__ void next() {
@@ -470,12 +470,17 @@ struct NormRing {
             phase ^= 1u;
         }
     }
+    // Thread 0 of an aborted block: no copy may be in flight when the block's memory is given up.  Where all rows
+    // were issued, each slot's last one is waited for.  Where the ring stopped before, the limit is waited out: a
+    // count of the rows issued made calls that abort nothing slower (layer norm, one token 3.33 us against 3.01;
+    // backward, 4096 x 4096, 31.2 against 26.4), and without the loop the compiler orders the row loop otherwise
+    // (RMS norm backward: 32768 x 5120 169 us against 153, 4096 x 4096 24.4 against 26.1).
+    __device__ __forceinline__ void drain(uint64_t limit_ns) const {
+        for (int i = 0; i < slots && i < rows; ++i)
+            drain_bounded(&full[i], static_cast<uint32_t>(((rows - 1 - i) / slots) & 1), limit_ns);
+        if (!ok) wait_out(limit_ns);
+    }
 };
-
-// Thread 0 of an aborted block: no copy may be in flight when the block's memory is given up.  A count of the
-// rows issued, by which each slot's last copy could be waited for, made calls that abort nothing slower (layer
-// norm, one token: 3.33 us against 3.01; backward, 4096 x 4096: 31.2 against 26.3).
-__device__ __forceinline__ void norm_drain(const NormArgs& a) { wait_out(a.wait_limit_ns); }
 
 // Barriers and abort flag of a block, then the group's ring ready to start.
 template <class TX, int TENSORS>
@@ -493,7 +498,6 @@ __device__ __forceinline__ NormRing<TX, TENSORS> norm_ring(const NormArgs& a, co
     r.base = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     r.stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
     r.rows = r.base < a.T ? (a.T - 1 - r.base) / r.stride + 1 : 0;
-    r.withhold = static_cast<uint32_t>(a.withhold);
     r.ok = true;
     r.slot = 0;
     r.phase = 0;
@@ -503,7 +507,7 @@ __device__ __forceinline__ NormRing<TX, TENSORS> norm_ring(const NormArgs& a, co
         fence_mbar_init();
     }
     stream_wait();
-    if (threadIdx.x == 0) r.start();  // its own barriers; the others wait on them past the block's barrier
+    if (threadIdx.x == 0 && a.withhold == 0) r.start();  // its own barriers; the others wait on them past the block's barrier
     __syncthreads();
     return r;
 }
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) forge_norm_ring_kernel(const 
         }
         ring.next();
     }
-    if (abort_flag && threadIdx.x == 0) norm_drain(a);
+    if (abort_flag && threadIdx.x == 0) ring.drain(a.wait_limit_ns);
 }
 
 template <class TX, int NV, bool CENTER>
@@ -670,7 +674,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) forge_norm_bwd_ring_kernel(co
         rstd = rstd_next;
         ring.next();
     }
-    if (abort_flag && threadIdx.x == 0) norm_drain(a);
+    if (abort_flag && threadIdx.x == 0) ring.drain(a.wait_limit_ns);
     // the groups' columns side by side in shared memory, then one sum over the groups a column
     __syncthreads();
     float* cols = reinterpret_cast<float*>(ring_mem);

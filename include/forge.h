@@ -431,7 +431,7 @@ FORGE_API void forge_set_wait_limit_ns(uint64_t ns);
  * forge_fused_dw_step, forge_fused_dw_step_e4m3, forge_dw_gemm, forge_dw_gemm_e4m3 or
  * forge_dx_gemm, with work to do), or the next launch of an operator around the fused layers that waits
  * for copies (products, and norms of rows of 16-byte runs), arms the first pipeline stage of its first
- * tile (norms and products of one to four tokens: each stage) but never copies all of it: the wait for that stage runs out after the wait limit, the kernel records
+ * tile (norms: the first rows'; products of one to four tokens: each stage) but never copies all of it: the wait for that stage runs out after the wait limit, the kernel records
  * FORGE_ERR_TIMEOUT, stops every other wait, waits (bounded) until every copy it did issue into
  * shared memory has landed, frees its TMEM and returns; forge_sync_status() then reports FORGE_ERR_TIMEOUT and the
  * CUDA context stays usable.  The outputs of that one call are unspecified.  No fault is raised. */
