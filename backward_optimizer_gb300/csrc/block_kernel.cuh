@@ -32,13 +32,13 @@
 // takes two copies: its last block of 64 columns would reach past its rows.
 //
 // What bounds it, measured on one GB300.  Large products: the tensor core under the chip's power limit.  In
-// bursts below the limit, 4096 tokens: block forward 4096/14336 795 us (1.81 PFLOP/s, 0.95 of the measured
-// burst peak), block backward 1613 us (1.79), loss forward over 32768 x 4096 570 us (1.93), loss backward
-// 1766 us (1.87); run on end, at the limit, 1.82, 1.62, 1.78 and 1.68.  Products with MN-major operands
+// bursts below the limit, 4096 tokens: block forward 4096/14336 804-817 us (1.77-1.79 PFLOP/s, 0.93 of the measured
+// burst peak), block backward 1661-1676 us (1.72-1.74), loss forward over 32768 x 4096 578-586 us (1.88-1.90), loss
+// backward 1813-1835 us (1.80-1.82); run on end, at the limit, 1.62, 1.57, 1.72 and 1.64.  Products with MN-major operands
 // (dX, dW, dH) reach less there than K-major ones.  The tile with dH also shares the memory system with G,
 // U, dG, dU and H: 165 us at 2048 tokens (1.45 PFLOP/s), the same with 16 epilogue warps, with G and U
-// prefetched into L2, or loaded first to be evicted.  With one row of tiles: memory, 6.4 TB/s of weights for
-// the loss of one token over 155648 x 4096.
+// prefetched into L2, or loaded first to be evicted.  With one row of tiles: memory, 6.3 TB/s of weights for
+// the loss of one token over 131072 x 4096, 6.4 for 16 tokens over 155648 x 4096 (one token there: 3.8 to 4.8).
 //
 // Why these tiles.  A pair's 256 x 256 tile moves 32 KB into each SM's shared memory per 512 cycles of its
 // tensor core; single CTAs on 128 x 128 or 128 x 64 move more per product, fill the GPU with less and serve small

@@ -16,10 +16,12 @@
 // Either way the variance is taken about the mean in a second pass over data on the SM, not as a
 // difference of large sums.
 //
-// Measured on one GB300 (copy rate 6.78 TB/s), bf16: RMS norm forward 8192 x 5120 27.5-29.3 us (5.7-6.1 TB/s),
-// 32768 x 5120 102 us (6.5 TB/s); layer norm forward 32768 x 4096 95 us (5.6); layer norm backward
-// 4096 x 4096 26.3 us (3.8), 32768 x 4096 142 us (5.7), RMS norm backward 32768 x 5120 153 us (6.6).  A
+// Measured on one GB300 (copy rate 6.78 TB/s), bf16: RMS norm forward 8192 x 5120 29.5 us (5.7 TB/s),
+// 32768 x 5120 103 us (6.5 TB/s); layer norm forward 32768 x 4096 96 us (5.6); layer norm backward
+// 4096 x 4096 26.6 us (3.8), 32768 x 4096 140 us (5.7), RMS norm backward 32768 x 5120 153 us (6.6).  A
 // backward call has some 10 us of its own: two launches, the rings' first and last rows, the columns' join.
+// Binary32, 8192 x 4096: RMS norm 43 us forward and 65 backward (6.2 TB/s), layer norm 47 and 75 (5.7, 5.4).
+// Rows too long for scalars in registers, 2048 x 5003 bf16: layer norm 39 us forward (1.1), 111 backward (0.6).
 // The layer norm's backward arithmetic issues at 0.53 of the schedulers' rate with the 16 warps that its
 // registers leave; 32 warps of one run each took longer (32.5 us: more of a row's time in its sums).
 //

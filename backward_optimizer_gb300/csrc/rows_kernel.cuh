@@ -12,8 +12,8 @@
 // GATED: a group holds the same rows of the gate and of the up projection, and its result is
 // act(g) u (with g and u themselves where they are wanted); else y (+ add).
 //
-// Measured, both products of a gated block: 4096/14336 one token 54.2 us, 6.5 TB/s of weights (0.96 of the
-// copy rate), two 55.4; 2048/5632 one token 19 us, of which half is the two launches.
+// Measured, both products of a gated block: 4096/14336 one token 54.9 us, 6.4 TB/s of weights (0.95 of the
+// copy rate), two 56.9; 2048/5632 one token 17.6 us, of which half is the two launches.
 #pragma once
 
 #include <cstdint>
