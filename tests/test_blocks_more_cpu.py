@@ -86,6 +86,7 @@ def test_a_second_derivative_through_trained_modules_raises(on_cpu):
             g.float().square().sum().backward()
 
 
+@pytest.mark.filterwarnings("ignore:Using backward")
 def test_a_residual_keeps_its_graph(on_cpu):
     block = ForgeGatedMLP(64, 64, device="cpu")
     x, r = torch.zeros(4, 64).bfloat16(), torch.ones(4, 64).bfloat16().requires_grad_(True)
