@@ -81,7 +81,7 @@ class Stepped(torch.nn.Module):
     def _save_to_state_dict(self, destination, prefix, keep_vars):
         super()._save_to_state_dict(destination, prefix, keep_vars)
         if self.step != 1:
-            destination[prefix + "step"] = torch.tensor(self.step)
+            destination[prefix + "step"] = torch.tensor(self.step, device="cpu")
 
     def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs):
         super()._load_from_state_dict(state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs)

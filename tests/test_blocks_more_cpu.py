@@ -114,6 +114,8 @@ def test_the_step_is_part_of_the_state(make, tmp_path):
     assert not any(k.endswith("step") for k in m.state_dict())
     m["a"].step = 7
     m["a"]._pending = 7
+    with torch.device("meta"):  # whatever the default device is, the step is a number on the host
+        assert int(m.state_dict()["a.step"]) == 7
     torch.save(m.state_dict(), tmp_path / "s")
     for state in (torch.load(tmp_path / "s"), {k: v.clone() for k, v in m.state_dict().items()}):
         n = model()
