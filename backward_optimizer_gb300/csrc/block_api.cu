@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cstring>
 
+#include "block_host.h"
 #include "block_kernel.cuh"
 #include "block_launch.h"
 #include "forge.h"
@@ -21,34 +22,7 @@ using forge::BlockProblem;
 using forge::PairGroup;
 using forge::kMaxProducts;
 namespace host = forge::host;
-
-constexpr int64_t kMaxDim = 1ll << 30;
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-forge_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA; }
-
-struct Machine {
-    host::Device dev;
-    int pairs;  // CTA pairs resident at once
-};
-
-forge_status machine(Machine* m) {
-    forge_status st = host::device(&m->dev);
-    if (st != FORGE_OK) return st;
-    static std::atomic<int> pairs[64];
-    int d = 0;
-    if (cudaGetDevice(&d) != cudaSuccess) return FORGE_ERR_CUDA;
-    d &= 63;
-    int n = pairs[d].load();
-    if (n == 0) {
-        if (forge::block_pairs(m->dev.num_sms, &n) != cudaSuccess || n < 1) return FORGE_ERR_CUDA;
-        pairs[d].store(n);
-    }
-    m->pairs = n;
-    return FORGE_OK;
-}
+using namespace forge::host;
 
 // ---------------------------------------------------------------- cutting products into units
 
@@ -233,16 +207,6 @@ Plan plan_one(const Machine& mc, int64_t rows, int64_t cols, int kb, bool gated 
 
 int slices(int64_t k) { return static_cast<int>(ceil_div(k, forge::kBK)); }
 
-// Workspace: regions one after another, each 256-byte aligned.
-struct Arena {
-    int64_t used = 0;
-    int64_t take(int64_t bytes) {
-        const int64_t at = used;
-        used += round_up(bytes, 256);
-        return at;
-    }
-};
-
 // The split tiles' regions that the launches of a call share, each big enough for any of them: FP32
 // parts, and arrival counters, which are zero between launches once the call has cleared them.
 struct SplitSpace {
@@ -259,11 +223,6 @@ SplitSpace take_split(Arena& a, std::initializer_list<const Plan*> plans) {
     }
     return SplitSpace{a.take(floats * 4), a.take(counts * 4ll), counts};
 }
-
-struct Operand {
-    const void* base;
-    int64_t cols, rows, ld;  // as it lies in memory
-};
 
 // The schedule and everything of a launch that does not depend on the epilogue.  The products come
 // longest first.
@@ -315,39 +274,6 @@ forge_status fill_group(BlockGroup<NP>& g, const Plan& p, const Machine& mc, cha
     return FORGE_OK;
 }
 
-// Encoded tensor maps of recent calls, per host thread, as forge_api.cu keeps them for the weight-gradient
-// kernels: a map is plain host data determined by its key.
-struct MapKey {
-    const void* base;
-    int64_t cols, rows, ld;
-    int mn, extent;
-    bool operator==(const MapKey& o) const {
-        return base == o.base && cols == o.cols && rows == o.rows && ld == o.ld && mn == o.mn && extent == o.extent;
-    }
-};
-struct MapSlot {
-    MapKey key;
-    CUtensorMap map;
-    bool used;
-};
-constexpr int kMapSlots = 128;
-thread_local MapSlot t_maps[kMapSlots];
-
-template <class Encode>
-forge_status kept_map(CUtensorMap* map, const MapKey& key, Encode&& encode) {
-    uint64_t h = reinterpret_cast<uintptr_t>(key.base) * 0x9E3779B97F4A7C15ull;
-    h ^= static_cast<uint64_t>(key.cols) * 0xC2B2AE3D27D4EB4Full ^ static_cast<uint64_t>(key.rows) * 0x165667B19E3779F9ull;
-    h ^= static_cast<uint64_t>(key.ld * 1024 + key.extent * 2 + key.mn) * 0x85EBCA77C2B2AE63ull;
-    MapSlot& slot = t_maps[(h >> 32) % kMapSlots];
-    if (slot.used && slot.key == key) {
-        *map = slot.map;
-        return FORGE_OK;
-    }
-    const forge_status st = encode();
-    if (st == FORGE_OK) slot = MapSlot{key, *map, true};
-    return st;
-}
-
 // The map of an operand of which a CTA stages `extent` rows (K-major) or columns (MN-major) per slice, one
 // box a slice; or two boxes of 64 columns where the operand's width is no multiple of 64 (flat).
 forge_status operand_map(CUtensorMap* map, const Operand& o, bool mn, int extent) {
@@ -384,12 +310,6 @@ forge_status launch(const PairGroup<EPI>& g, const Plan& p, cudaStream_t stream)
     host::count_launch();
     return cuda_status(forge::launch_block<EPI>(&g, p.bn, std::min(p.width, g.units.n_units), stream));
 }
-
-#define FORGE_TRY(expr)                      \
-    do {                                     \
-        const forge_status st_ = (expr);     \
-        if (st_ != FORGE_OK) return st_;     \
-    } while (0)
 
 // One product of a kBlockStore launch.
 struct Product {
@@ -517,21 +437,6 @@ forge_status check_gated(const forge_gated_shape* s) {
     if (s->act != FORGE_ACT_SILU && s->act != FORGE_ACT_GELU_TANH && s->act != FORGE_ACT_RELU)
         return FORGE_ERR_INVALID_ARGUMENT;
     return FORGE_OK;
-}
-
-// Non-null and 32-byte aligned.
-forge_status check_all(std::initializer_list<const void*> ps) {
-    for (const void* p : ps)
-        if (p == nullptr) return FORGE_ERR_INVALID_ARGUMENT;
-    for (const void* p : ps)
-        if (!aligned(p, 32)) return FORGE_ERR_MISALIGNED;
-    return FORGE_OK;
-}
-
-forge_status check_workspace(const void* ws, int64_t have, int64_t need) {
-    if (need == 0) return FORGE_OK;
-    if (ws == nullptr || have < need) return FORGE_ERR_INVALID_ARGUMENT;
-    return aligned(ws, 256) ? FORGE_OK : FORGE_ERR_MISALIGNED;
 }
 
 struct GatedForward {

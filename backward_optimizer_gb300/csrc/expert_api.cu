@@ -1,0 +1,537 @@
+// expert_api.cu -- the C ABI of the products grouped by expert (include/forge.h): a linear layer and the gated
+// feed-forward block with a weight for each expert.  Argument checks, the plan made from the offsets on the
+// device, workspace layout and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "block_host.h"
+#include "expert_kernel.cuh"
+#include "expert_launch.h"
+#include "forge.h"
+#include "host.h"
+
+namespace {
+
+namespace host = forge::host;
+using namespace forge::host;
+using forge::ExpertGroup;
+using forge::ExpertProblem;
+using forge::kBlockGatedBwd;
+using forge::kBlockGatedFwd;
+using forge::kBlockStore;
+using forge::kExpertGrad;
+
+constexpr int kMaxExperts = 1024;  // the plan gives each a thread of its one block
+constexpr int kMaxRuns = 5;        // operands whose reduction is a run of rows: dG, dU, dY, X, H
+
+int slices(int64_t k) { return static_cast<int>(ceil_div(k, forge::kBK)); }
+
+// ---------------------------------------------------------------- the plan, made on the device
+
+struct RunOperand {
+    CUtensorMap map;  // of all rows
+    const char* base;
+    int64_t pitch;    // bytes from row to row
+};
+
+struct PlanArgs {
+    const int* offsets;
+    int experts, rows, tile_rows;
+    int* clean;     // [experts + 1]
+    int* n_tiles;
+    int4* tiles;
+    CUtensorMap* runs;  // [n_runs][experts]
+    int n_runs;
+    RunOperand run[kMaxRuns];
+};
+
+// Inclusive scan over the block's 1024 threads.
+template <class Op>
+__device__ __forceinline__ int block_scan(int v, int* warps, Op op) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int n = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v = op(v, n);
+    }
+    if (lane == 31) warps[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        int w = warps[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int n = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            if (lane >= o) w = op(w, n);
+        }
+        warps[lane] = w;
+    }
+    __syncthreads();
+    if (warp > 0) v = op(v, warps[warp - 1]);
+    __syncthreads();
+    return v;
+}
+
+// One block: thread e is expert e.  Offsets are brought into order and within the rows (an offset below the one
+// before it, or past the last row, ends an empty or a shorter run), so that no later launch can leave the
+// tensors whatever they hold.
+__global__ void __launch_bounds__(1024) expert_plan_kernel(const __grid_constant__ PlanArgs a) {
+    __shared__ int warps[32], first[kMaxExperts], begin[kMaxExperts], end[kMaxExperts];
+    forge::stream_wait();
+    const int e = threadIdx.x;
+    const bool mine = e < a.experts;
+    auto inside = [&](int i) { return min(max(__ldcg(a.offsets + i), 0), a.rows); };
+    const int from = block_scan(mine ? inside(e) : 0, warps, [](int x, int y) { return max(x, y); });
+    const int to = mine ? max(from, inside(e + 1)) : from;
+    if (mine) {
+        a.clean[e] = from;
+        if (e + 1 == a.experts) a.clean[a.experts] = to;
+    }
+    const int tiles = (to - from + a.tile_rows - 1) / a.tile_rows;
+    const int last = block_scan(tiles, warps, [](int x, int y) { return x + y; });
+    first[e] = last - tiles;
+    begin[e] = from;
+    end[e] = to;
+    if (e == 1023) *a.n_tiles = last;
+    __syncthreads();
+    const int total = first[1023] + (end[1023] - begin[1023] + a.tile_rows - 1) / a.tile_rows;
+    for (int i = e; i < total; i += 1024) {
+        int lo = 0, hi = a.experts - 1;  // the last expert whose first tile is not behind tile i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (first[mid] <= i) lo = mid;
+            else hi = mid - 1;
+        }
+        const int row = begin[lo] + (i - first[lo]) * a.tile_rows;
+        a.tiles[i] = make_int4(lo, row, min(row + a.tile_rows, end[lo]), 0);
+    }
+    for (int i = e; i < a.n_runs * a.experts; i += 1024) {
+        const int o = i / a.experts, x = i - o * a.experts;
+        const uint4* src = reinterpret_cast<const uint4*>(&a.run[o].map);
+        uint4* dst = reinterpret_cast<uint4*>(a.runs + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dst[j] = src[j];
+        // a run of no rows: one row that is never read (its slice lies past it)
+        const int n = end[x] - begin[x];
+        forge::tensormap_set(a.runs + i, a.run[o].base + (n > 0 ? begin[x] * a.run[o].pitch : 0), n > 0 ? n : 1);
+    }
+}
+
+// ---------------------------------------------------------------- tiles
+
+struct Tiling {
+    int bn;         // tile columns: 256 on CTA pairs, 128 or 64 on single CTAs
+    int tile_rows;  // rows of a row tile
+};
+
+// A call's rows, experts and plan in its workspace.
+struct Call {
+    Machine mc;
+    int64_t rows;
+    int experts;
+    Tiling tiling;
+    int64_t tiles;  // row tiles at most
+    int n_runs;
+    int64_t clean, n_tiles, list, runs;  // places in the workspace
+    char* ws;
+    cudaStream_t stream;
+    const int* offsets;
+};
+
+// Row tiles: 256 rows on pairs where an expert has that many to fill most of one; else 128, or 32 where
+// experts have few rows and the weights' bytes are all there is to move.
+Tiling choose_rows(int64_t rows, int64_t experts) {
+    const int64_t each = rows / std::min(rows, experts);
+    if (each > 160) return Tiling{256, 256};
+    return each > 24 ? Tiling{128, 128} : Tiling{128, 32};
+}
+
+Call make_call(const Machine& mc, int64_t rows, int64_t experts, int n_runs, Arena& a) {
+    Call c{};
+    c.mc = mc;
+    c.rows = rows;
+    c.experts = static_cast<int>(experts);
+    c.tiling = choose_rows(rows, experts);
+    c.tiles = rows / c.tiling.tile_rows + std::min(rows, experts);
+    c.n_runs = n_runs;
+    c.clean = a.take((experts + 1) * 4);
+    c.n_tiles = a.take(4);
+    c.list = a.take(c.tiles * 16);
+    c.runs = a.take(n_runs * experts * static_cast<int64_t>(sizeof(CUtensorMap)));
+    return c;
+}
+
+forge_status check_rows(int64_t rows, int64_t experts, int64_t d_in, int64_t d_out) {
+    if (rows < 0 || rows > kMaxDim || experts < 1 || experts > kMaxExperts) return FORGE_ERR_INVALID_ARGUMENT;
+    if (d_in < 8 || d_out < 8 || d_in > kMaxDim || d_out > kMaxDim || d_in % 8 != 0 || d_out % 8 != 0)
+        return FORGE_ERR_INVALID_ARGUMENT;
+    // tiles are counted in int
+    if ((rows / 32 + experts) * (std::max(d_in, d_out) / 64 + 1) > kMaxDim ||
+        3 * experts * (d_in / 128 + 1) * (d_out / 64 + 1) > kMaxDim || 3 * experts * (d_out / 128 + 1) * (d_in / 64 + 1) > kMaxDim)
+        return FORGE_ERR_INVALID_ARGUMENT;
+    return FORGE_OK;
+}
+
+// ---------------------------------------------------------------- operands
+
+// Rows by expert: A [rows, cols], K-major.
+forge_status rows_map(CUtensorMap* map, const Call& c, const void* base, int64_t cols) {
+    const int extent = c.tiling.bn == 256 ? 128 : c.tiling.tile_rows;
+    return kept_map(map, MapKey{base, cols, c.rows, cols, 0, extent}, [&] {
+        const uint64_t k = static_cast<uint64_t>(cols), r = static_cast<uint64_t>(c.rows);
+        return host::encode_map(map, base, {k, r, 1}, {2 * k, 2 * k}, {64, static_cast<uint32_t>(extent), 1});
+    });
+}
+
+// The weights [experts, rows, cols], of which a CTA stages `extent` rows (K-major) or columns (MN-major) a slice.
+forge_status weight_map(CUtensorMap* map, const void* base, int64_t experts, int64_t rows, int64_t cols, bool mn, int extent) {
+    return kept_map(map, MapKey{base, cols, rows, cols, mn, extent, experts}, [&] {
+        const uint64_t k = static_cast<uint64_t>(cols), r = static_cast<uint64_t>(rows), e = static_cast<uint64_t>(experts);
+        if (mn && cols % 64 == 0)
+            return host::encode_map(map, base, {64, r, k / 64, e}, {2 * k, 128, 2 * r * k},
+                                    {64, 64, static_cast<uint32_t>(extent / 64), 1});
+        return host::encode_map(map, base, {k, r, 1, e}, {2 * k, 2 * r * k, 2 * r * k},
+                                {64, mn ? 64u : static_cast<uint32_t>(extent), 1, 1});
+    });
+}
+
+// An operand of the weights' gradients, [rows, cols] and MN-major: the map of all rows, which the plan cuts.
+forge_status run_operand(RunOperand* o, const Call& c, const void* base, int64_t cols, int extent) {
+    o->base = static_cast<const char*>(base);
+    o->pitch = cols * 2;
+    return kept_map(&o->map, MapKey{base, cols, c.rows, cols, 1, extent}, [&] {
+        const uint64_t k = static_cast<uint64_t>(cols), r = static_cast<uint64_t>(c.rows);
+        if (cols % 64 == 0)
+            return host::encode_map(&o->map, base, {64, r, k / 64}, {2 * k, 128}, {64, 64, static_cast<uint32_t>(extent / 64)});
+        return host::encode_map(&o->map, base, {k, r, 1}, {2 * k, 2 * k}, {64, 64, 1});
+    });
+}
+
+// Result i of a staged epilogue, [experts, rows, cols] in one piece (rows by expert: experts = 1).
+template <int EPI>
+forge_status set_result(ExpertGroup<EPI>& g, const Tiling& t, int i, void* base, int64_t experts, int64_t rows, int64_t cols) {
+    g.to[i] = static_cast<uint16_t*>(base);
+    if (!forge::staged(EPI) || t.bn != 256) return FORGE_OK;
+    return kept_map(&g.outs[i], MapKey{base, cols, rows, cols, 0, 0, experts},
+                    [&] { return host::encode_result_map(&g.outs[i], base, cols, rows, experts); });
+}
+
+// ---------------------------------------------------------------- launches
+
+template <int EPI>
+void begin_group(ExpertGroup<EPI>& g, const Call& c, int64_t kb_max) {
+    std::memset(&g, 0, sizeof(g));
+    g.n = 1;
+    g.experts = c.experts;
+    g.a_rows = EPI == kExpertGrad ? 128 : c.tiling.tile_rows;
+    g.withhold_first_stage = host::take_withhold();
+    g.n_tiles = reinterpret_cast<const int*>(c.ws + c.n_tiles);
+    g.tiles = reinterpret_cast<const int4*>(c.ws + c.list);
+    g.offsets = reinterpret_cast<const int*>(c.ws + c.clean);
+    g.runs = reinterpret_cast<const CUtensorMap*>(c.ws + c.runs);
+    g.status = c.mc.dev.status;
+    g.wait_limit_ns = host::wait_limit_ns();
+    g.acc_wait_limit_ns = host::acc_wait_limit_ns(kb_max);
+}
+
+template <int EPI>
+forge_status launch(const ExpertGroup<EPI>& g, const Call& c, int bn, int64_t units) {
+    const int width = bn == 256 ? c.mc.pairs : c.mc.dev.num_sms;
+    host::count_launch();
+    return cuda_status(forge::launch_expert<EPI>(&g, bn, static_cast<int>(std::min<int64_t>(width, units)), c.stream));
+}
+
+forge_status launch_plan(const Call& c, PlanArgs& a) {
+    a.offsets = c.offsets;
+    a.experts = c.experts;
+    a.rows = static_cast<int>(c.rows);
+    a.tile_rows = c.tiling.tile_rows;
+    a.clean = reinterpret_cast<int*>(c.ws + c.clean);
+    a.n_tiles = reinterpret_cast<int*>(c.ws + c.n_tiles);
+    a.tiles = reinterpret_cast<int4*>(c.ws + c.list);
+    a.runs = reinterpret_cast<CUtensorMap*>(c.ws + c.runs);
+    return cuda_status(host::launch_early(expert_plan_kernel, dim3(1), dim3(1024), 0, c.stream, a));
+}
+
+template <int EPI>
+void set_rows(ExpertGroup<EPI>& g, const Call& c, int64_t cols, int64_t k0, int64_t k1) {
+    ExpertProblem& b = g.prob[0];
+    b.cols = static_cast<int>(cols);
+    b.ld = cols;
+    b.tiles_n = static_cast<int>(ceil_div(cols, EPI == kBlockGatedFwd ? c.tiling.bn / 2 : c.tiling.bn));
+    b.kb[0] = slices(k0);
+    b.kb[1] = slices(k1);
+    g.stream_b = c.tiling.tile_rows < 128;
+}
+
+int b_extent(const Tiling& t, bool gated) { return t.bn == 256 ? 128 : gated ? t.bn / 2 : t.bn; }
+
+// out [rows, cols] = A0 W0 (+ A1 W1): W_e [cols, k] as it is read in y = x W^T, or [k, cols] (mn)
+struct RowProduct {
+    const void* a[2];
+    const void* w[2];
+    int64_t k, cols;
+    bool mn;
+    void* out;
+};
+
+forge_status run_rows(const Call& c, const RowProduct& p) {
+    ExpertGroup<kBlockStore> g;
+    begin_group(g, c, 2 * slices(p.k));
+    set_rows(g, c, p.cols, p.k, p.a[1] != nullptr ? p.k : 0);
+    g.prob[0].b_mn = p.mn;
+    g.prob[0].b_flat = p.mn && p.cols % 64 != 0;
+    for (int i = 0; i < 2 && p.a[i] != nullptr; ++i) {
+        FORGE_TRY(rows_map(&g.maps[2 * i], c, p.a[i], p.k));
+        FORGE_TRY(weight_map(&g.maps[2 * i + 1], p.w[i], c.experts, p.mn ? p.k : p.cols, p.mn ? p.cols : p.k, p.mn,
+                             b_extent(c.tiling, false)));
+    }
+    FORGE_TRY(set_result(g, c.tiling, 0, p.out, 1, c.rows, p.cols));
+    return launch(g, c, c.tiling.bn, c.tiles * g.prob[0].tiles_n);
+}
+
+// dW of up to three products: a and b, numbers of their run operands; each dW_e [d_out, d_in]
+struct GradProduct {
+    int a, b;
+    int64_t d_out, d_in;
+    void* out;
+};
+
+Tiling grad_tiling(const Machine& mc, int64_t experts, const GradProduct* p, int n) {
+    int64_t pairs = 0;
+    for (int i = 0; i < n; ++i) pairs += experts * ceil_div(p[i].d_out, 256) * ceil_div(p[i].d_in, 256);
+    return pairs >= mc.pairs ? Tiling{256, 256} : Tiling{128, 128};
+}
+
+forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int n) {
+    ExpertGroup<kExpertGrad> g;
+    begin_group(g, c, slices(c.rows));
+    g.n = n;
+    int64_t u = 0;
+    for (int i = 0; i < n; ++i) {
+        ExpertProblem& b = g.prob[i];
+        b.rows = static_cast<int>(p[i].d_out);
+        b.cols = static_cast<int>(p[i].d_in);
+        b.ld = p[i].d_in;
+        b.tiles_m = static_cast<int>(ceil_div(p[i].d_out, t.bn == 256 ? 256 : 128));
+        b.tiles_n = static_cast<int>(ceil_div(p[i].d_in, t.bn));
+        b.unit_start = static_cast<int>(u);
+        b.a_flat = p[i].d_out % 64 != 0;
+        b.b_flat = p[i].d_in % 64 != 0;
+        b.map_a = p[i].a;
+        b.map_b = p[i].b;
+        u += static_cast<int64_t>(c.experts) * b.tiles_m * b.tiles_n;
+        FORGE_TRY(set_result(g, t, i, p[i].out, c.experts, p[i].d_out, p[i].d_in));
+    }
+    g.n_units = static_cast<int>(u);
+    return launch(g, c, t.bn, u);
+}
+
+// ---------------------------------------------------------------- a linear layer for each expert
+
+forge_status check_linear(const forge_expert_linear_shape* s) {
+    if (s == nullptr || s->reserved != 0) return FORGE_ERR_INVALID_ARGUMENT;
+    return check_rows(s->rows, s->experts, s->d_in, s->d_out);
+}
+
+forge_status check_offsets(const int32_t* offsets) {
+    if (offsets == nullptr) return FORGE_ERR_INVALID_ARGUMENT;
+    return aligned(offsets, 4) ? FORGE_OK : FORGE_ERR_MISALIGNED;
+}
+
+forge_status check_gated(const forge_expert_gated_shape* s) {
+    if (s == nullptr || s->reserved != 0) return FORGE_ERR_INVALID_ARGUMENT;
+    if (s->act != FORGE_ACT_SILU && s->act != FORGE_ACT_GELU_TANH && s->act != FORGE_ACT_RELU)
+        return FORGE_ERR_INVALID_ARGUMENT;
+    return check_rows(s->rows, s->experts, s->d_model, s->d_ff);
+}
+
+struct GatedSpace {
+    Call c;
+    int64_t dg, du, h, bytes;
+};
+
+GatedSpace layout_gated(const Machine& mc, const forge_expert_gated_shape& s, bool backward) {
+    GatedSpace l{};
+    Arena a;
+    l.c = make_call(mc, s.rows, s.experts, backward ? kMaxRuns : 0, a);
+    const int64_t bytes = s.rows * s.d_ff * 2;
+    if (backward) {
+        l.dg = a.take(bytes);
+        l.du = a.take(bytes);
+    }
+    l.h = a.take(bytes);
+    l.bytes = a.used;
+    return l;
+}
+
+int64_t linear_space(const Machine& mc, const forge_expert_linear_shape& s, Call* c) {
+    Arena a;
+    *c = make_call(mc, s.rows, s.experts, 2, a);
+    return a.used;
+}
+
+forge_status zero(std::initializer_list<void*> ps, int64_t bytes, cudaStream_t stream) {
+    for (void* p : ps)
+        if (p != nullptr && cudaMemsetAsync(p, 0, static_cast<size_t>(bytes), stream) != cudaSuccess) return FORGE_ERR_CUDA;
+    return FORGE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t forge_expert_linear_workspace(const forge_expert_linear_shape* shape) {
+    if (check_linear(shape) != FORGE_OK) return -1;
+    Machine mc;
+    if (shape->rows == 0) return 0;
+    if (machine(&mc) != FORGE_OK) return -1;
+    Call c;
+    return linear_space(mc, *shape, &c);
+}
+
+forge_status forge_expert_linear(const void* X, const void* W, const int32_t* offsets, void* Y, void* workspace,
+                                 int64_t workspace_bytes, const forge_expert_linear_shape* shape,
+                                 struct CUstream_st* stream) {
+    FORGE_TRY(check_linear(shape));
+    const forge_expert_linear_shape& s = *shape;
+    if (s.rows == 0) return FORGE_OK;
+    FORGE_TRY(check_all({X, W, Y}));
+    FORGE_TRY(check_offsets(offsets));
+    Call c;
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, &c)));
+    c.ws = static_cast<char*>(workspace);
+    c.stream = stream;
+    c.offsets = offsets;
+    PlanArgs plan{};
+    FORGE_TRY(launch_plan(c, plan));
+    return run_rows(c, RowProduct{{X, nullptr}, {W, nullptr}, s.d_in, s.d_out, false, Y});
+}
+
+forge_status forge_expert_linear_backward(const void* dY, const void* X, const void* W, const int32_t* offsets, void* dX,
+                                          void* dW, void* workspace, int64_t workspace_bytes,
+                                          const forge_expert_linear_shape* shape, struct CUstream_st* stream) {
+    FORGE_TRY(check_linear(shape));
+    const forge_expert_linear_shape& s = *shape;
+    if (dX == nullptr && dW == nullptr && s.rows > 0) return FORGE_ERR_INVALID_ARGUMENT;
+    if (!aligned(dX, 32) || !aligned(dW, 32)) return FORGE_ERR_MISALIGNED;
+    if (s.rows == 0) return zero({dW}, s.experts * s.d_out * s.d_in * 2, stream);
+    FORGE_TRY(check_all({dY, X, W}));
+    FORGE_TRY(check_offsets(offsets));
+    Call c;
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, &c)));
+    c.ws = static_cast<char*>(workspace);
+    c.stream = stream;
+    c.offsets = offsets;
+    const GradProduct p{0, 1, s.d_out, s.d_in, dW};
+    const Tiling t = grad_tiling(mc, s.experts, &p, 1);
+    PlanArgs plan{};
+    if (dW != nullptr) {
+        plan.n_runs = 2;
+        FORGE_TRY(run_operand(&plan.run[0], c, dY, s.d_out, 128));
+        FORGE_TRY(run_operand(&plan.run[1], c, X, s.d_in, b_extent(t, false)));
+    }
+    FORGE_TRY(launch_plan(c, plan));
+    if (dX != nullptr) FORGE_TRY(run_rows(c, RowProduct{{dY, nullptr}, {W, nullptr}, s.d_out, s.d_in, true, dX}));
+    return dW != nullptr ? run_grads(c, t, &p, 1) : FORGE_OK;
+}
+
+int64_t forge_expert_gated_mlp_workspace(const forge_expert_gated_shape* shape, int32_t backward) {
+    if (check_gated(shape) != FORGE_OK) return -1;
+    Machine mc;
+    if (shape->rows == 0) return 0;
+    if (machine(&mc) != FORGE_OK) return -1;
+    return layout_gated(mc, *shape, backward != 0).bytes;
+}
+
+forge_status forge_expert_gated_mlp(const void* X, const void* Wg, const void* Wu, const void* Wd, const int32_t* offsets,
+                                    void* Y, void* G, void* U, void* workspace, int64_t workspace_bytes,
+                                    const forge_expert_gated_shape* shape, struct CUstream_st* stream) {
+    FORGE_TRY(check_gated(shape));
+    const forge_expert_gated_shape& s = *shape;
+    if (s.rows == 0) return FORGE_OK;
+    FORGE_TRY(check_all({X, Wg, Wu, Wd, Y}));
+    FORGE_TRY(check_offsets(offsets));
+    if ((G == nullptr) != (U == nullptr)) return FORGE_ERR_INVALID_ARGUMENT;
+    if (!aligned(G, 32) || !aligned(U, 32)) return FORGE_ERR_MISALIGNED;
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    GatedSpace l = layout_gated(mc, s, false);
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
+    Call& c = l.c;
+    c.ws = static_cast<char*>(workspace);
+    c.stream = stream;
+    c.offsets = offsets;
+    PlanArgs plan{};
+    FORGE_TRY(launch_plan(c, plan));
+    ExpertGroup<kBlockGatedFwd> g;
+    begin_group(g, c, slices(s.d_model));
+    set_rows(g, c, s.d_ff, s.d_model, 0);
+    g.act = s.act;
+    g.keep = G != nullptr;
+    if (g.keep) {
+        FORGE_TRY(set_result(g, c.tiling, 0, G, 1, s.rows, s.d_ff));
+        FORGE_TRY(set_result(g, c.tiling, 1, U, 1, s.rows, s.d_ff));
+    }
+    FORGE_TRY(set_result(g, c.tiling, 2, c.ws + l.h, 1, s.rows, s.d_ff));
+    FORGE_TRY(rows_map(&g.maps[0], c, X, s.d_model));
+    const int extent = b_extent(c.tiling, true);
+    FORGE_TRY(weight_map(&g.maps[1], Wg, s.experts, s.d_ff, s.d_model, false, extent));
+    FORGE_TRY(weight_map(&g.maps[3], Wu, s.experts, s.d_ff, s.d_model, false, extent));
+    FORGE_TRY(launch(g, c, c.tiling.bn, c.tiles * g.prob[0].tiles_n));
+    return run_rows(c, RowProduct{{c.ws + l.h, nullptr}, {Wd, nullptr}, s.d_ff, s.d_model, false, Y});
+}
+
+forge_status forge_expert_gated_mlp_backward(const void* dY, const void* X, const void* G, const void* U, const void* Wg,
+                                             const void* Wu, const void* Wd, const int32_t* offsets, void* dX, void* dWg,
+                                             void* dWu, void* dWd, void* workspace, int64_t workspace_bytes,
+                                             const forge_expert_gated_shape* shape, struct CUstream_st* stream) {
+    FORGE_TRY(check_gated(shape));
+    const forge_expert_gated_shape& s = *shape;
+    FORGE_TRY(check_all({dWg, dWu, dWd}));
+    if (!aligned(dX, 32)) return FORGE_ERR_MISALIGNED;
+    if (s.rows == 0) return zero({dWg, dWu, dWd}, s.experts * s.d_ff * s.d_model * 2, stream);
+    FORGE_TRY(check_all({dY, X, G, U, Wg, Wu, Wd}));
+    FORGE_TRY(check_offsets(offsets));
+    Machine mc;
+    FORGE_TRY(machine(&mc));
+    GatedSpace l = layout_gated(mc, s, true);
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
+    Call& c = l.c;
+    c.ws = static_cast<char*>(workspace);
+    c.stream = stream;
+    c.offsets = offsets;
+    const GradProduct p[3] = {{0, 3, s.d_ff, s.d_model, dWg}, {1, 3, s.d_ff, s.d_model, dWu}, {2, 4, s.d_model, s.d_ff, dWd}};
+    const Tiling t = grad_tiling(mc, s.experts, p, 3);
+    PlanArgs plan{};
+    plan.n_runs = kMaxRuns;
+    FORGE_TRY(run_operand(&plan.run[0], c, c.ws + l.dg, s.d_ff, 128));
+    FORGE_TRY(run_operand(&plan.run[1], c, c.ws + l.du, s.d_ff, 128));
+    FORGE_TRY(run_operand(&plan.run[2], c, dY, s.d_model, 128));
+    FORGE_TRY(run_operand(&plan.run[3], c, X, s.d_model, b_extent(t, false)));
+    FORGE_TRY(run_operand(&plan.run[4], c, c.ws + l.h, s.d_ff, b_extent(t, false)));
+    FORGE_TRY(launch_plan(c, plan));
+    ExpertGroup<kBlockGatedBwd> g;
+    begin_group(g, c, slices(s.d_model));
+    set_rows(g, c, s.d_ff, s.d_model, 0);
+    g.act = s.act;
+    g.g_in = static_cast<const uint16_t*>(G);
+    g.u_in = static_cast<const uint16_t*>(U);
+    const int64_t outs[3] = {l.dg, l.du, l.h};
+    for (int i = 0; i < 3; ++i) FORGE_TRY(set_result(g, c.tiling, i, c.ws + outs[i], 1, s.rows, s.d_ff));
+    g.prob[0].b_flat = s.d_ff % 64 != 0;
+    FORGE_TRY(rows_map(&g.maps[0], c, dY, s.d_model));
+    FORGE_TRY(weight_map(&g.maps[1], Wd, s.experts, s.d_model, s.d_ff, true, b_extent(c.tiling, false)));
+    FORGE_TRY(launch(g, c, c.tiling.bn, c.tiles * g.prob[0].tiles_n));
+    if (dX != nullptr)
+        FORGE_TRY(run_rows(c, RowProduct{{c.ws + l.dg, c.ws + l.du}, {Wg, Wu}, s.d_ff, s.d_model, true, dX}));
+    return run_grads(c, t, p, 3);
+}
+
+}  // extern "C"

@@ -1,0 +1,426 @@
+// expert_kernel.cuh -- the persistent matrix-product kernel of products grouped by expert.
+//
+// Rows of X lie sorted by expert: expert e owns rows off_e .. off_{e+1}-1 of it and a matrix W_e of its own.  The
+// offsets are on the device (a router leaves them there), so the host knows the number of rows and of experts
+// but no expert's share.  Three kinds of product:
+//   rows by expert      Y[r] = X[r] W_e^T, dX[r] = dY[r] W_e for r of expert e: tiles of rows, each of one expert
+//   gated block         the same with the epilogues of block_kernel.cuh: G, U, H of the forward pass in one tile,
+//                       dG, dU, H of the backward pass behind dH
+//   weights' gradients  dW_e = sum over r of dY[r]^T X[r]: tiles of each dW_e, the reduction as long as e's run
+// The pipeline, tiles, roles, bounded waits and drains are those of forge_block_kernel.
+//
+// Ragged runs.  A launch in front (expert_plan_kernel) turns the offsets into a list of row tiles and, for the
+// weights' gradients, into two tensor maps per expert whose token dimension ends with the run: the copy itself
+// fills what a slice reaches past the run with zeros, for both operands, so neither values of the next expert
+// nor its infinities or NaN enter a sum.  Row products need no such map: an accumulator row depends on its own
+// row of A alone, and rows past the run are not stored.  An expert without rows takes one slice of zero fill and
+// stores a zero gradient.
+#pragma once
+
+#include "block_kernel.cuh"
+
+namespace forge {
+
+constexpr int kExpertGrad = 5;  // beside BlockEpi's kBlockStore, kBlockGatedFwd and kBlockGatedBwd, whose A are rows by expert
+
+__host__ __device__ constexpr int expert_products(int epi) { return epi == kExpertGrad ? 3 : 1; }
+
+struct ExpertProblem {
+    int cols;             // of the result (gated forward: d_ff, a tile spans BN / 2 of them)
+    int tiles_n;          // column tiles
+    int rows, tiles_m;    // kExpertGrad: rows of each expert's result, and their tiles
+    int unit_start;       // kExpertGrad: number of its first unit
+    int kb[2];            // rows by expert: 64-deep reduction slices of the two operand pairs
+    int a_flat, b_flat;   // MN-major and no multiple of 64 wide: a copy for each 64 columns
+    int b_mn;             // kBlockStore: W is read MN-major
+    int map_a, map_b;     // kExpertGrad: numbers of the operands' run maps
+    int64_t ld;           // the result's width
+};
+
+template <int EPI>
+struct ExpertGroup {
+    int n;                // products
+    int n_units;          // kExpertGrad; else tiles_n times *n_tiles
+    int experts;
+    int a_rows;           // rows of A that a stage holds, and of a tile on single CTAs (128 or 32)
+    int stream_b;         // each weight is read by one row tile or few: leave it out of the L2
+    int act, keep;
+    int withhold_first_stage;
+    const int* n_tiles;   // row tiles
+    const int4* tiles;    // each: expert, first row, one past its last row
+    const int* offsets;   // [experts + 1], as the plan left them: in order and within the rows
+    const CUtensorMap* runs;  // [map][expert]
+    const uint16_t* g_in;
+    const uint16_t* u_in;
+    int* status;
+    uint64_t wait_limit_ns, acc_wait_limit_ns;
+    uint16_t* to[3];      // results: kBlockStore's, kExpertGrad's of each product; G, U, H; dG, dU, H
+    ExpertProblem prob[expert_products(EPI)];
+    CUtensorMap maps[EPI == kExpertGrad ? 1 : 4];  // rows by expert: A, B of the first pair, A, B of the second
+    CUtensorMap outs[3];  // staged results
+};
+
+struct ExpertUnit {
+    int prob, expert, nb, row0, end;  // row0: the tile's first row of the result; end: one past its last
+    int slices;                       // kExpertGrad; rows by expert: of both operand pairs
+};
+
+template <int CG, int EPI>
+__device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int u, int n_tiles) {
+    ExpertUnit r;
+    int mb;
+    if constexpr (EPI == kExpertGrad) {
+        r.prob = 0;
+        while (r.prob + 1 < g.n && u >= g.prob[r.prob + 1].unit_start) ++r.prob;
+        const ExpertProblem& b = g.prob[r.prob];
+        const int t = u - b.unit_start, per = b.tiles_m * b.tiles_n;
+        r.expert = t / per;
+        tile_coords(t - r.expert * per, TileOrder{b.tiles_m, b.tiles_n, 8, 0}, mb, r.nb);
+        r.row0 = mb * kBM * CG;
+        r.end = b.rows;
+        const int run = __ldcg(g.offsets + r.expert + 1) - __ldcg(g.offsets + r.expert);
+        r.slices = run > 0 ? (run + kBK - 1) / kBK : 0;
+    } else {
+        const ExpertProblem& b = g.prob[0];
+        r.prob = 0;
+        tile_coords(u, TileOrder{n_tiles, b.tiles_n, 8, 0}, mb, r.nb);
+        const int4 t = __ldcg(g.tiles + mb);
+        r.expert = t.x;
+        r.row0 = t.y;
+        r.end = t.z;
+        r.slices = b.kb[0] + b.kb[1];
+    }
+    return r;
+}
+
+// A warp's results on their way to memory, as WarpOut: 32 rows x 32 columns at a time.  Staged, a warp whose 32
+// rows all belong to the tile's expert takes a tiled store; one that holds the last rows of a run writes them by
+// its lanes, since a store of the whole box would reach into the next expert's rows.
+template <bool kStaged>
+struct ExpertOut {
+    const CUtensorMap* maps;
+    uint16_t* to[3];
+    int64_t ld;
+    int rows;      // one past the last row that may be written
+    int z;         // third coordinate of the tiled store
+    bool boxed;    // the store's own bounds end the result (the weights' gradients)
+    uint32_t buf;
+    int turn;
+    template <int W>
+    __device__ __forceinline__ void put(int i, const uint32_t (&v)[W], int col, int row0) {
+        const uint32_t lane = threadIdx.x & 31u;
+        if constexpr (kStaged) {
+            static_assert(W == 16);
+            if (boxed || row0 + 32 <= rows) {
+                if (lane == 0) bulk_wait_read<1>();  // the buffer's last store has read it
+                __syncwarp();
+                const uint32_t at = buf + (static_cast<uint32_t>(turn) << 11);
+                turn ^= 1;
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j)
+                    st_shared_v4(at + lane * 64u + ((j ^ ((lane >> 1) & 3u)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2],
+                                 v[4 * j + 3]);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&maps[i], at, col, row0, z);
+                    bulk_commit();
+                }
+                return;
+            }
+        }
+        if (row0 + static_cast<int>(lane) < rows) {
+            uint16_t* p = to[i] + (static_cast<size_t>(row0) + lane) * ld + col;
+            const int left = static_cast<int>(ld) - col;
+            const bool wide = (ld & 15) == 0;
+#pragma unroll
+            for (int h = 0; h < W / 8; ++h) {
+                if (wide && left >= 16 * h + 16) {
+                    const uint32_t r[8] = {v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3],
+                                           v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]};
+                    st_v8(p + 16 * h, r);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t r[4] = {v[8 * h + 4 * q], v[8 * h + 4 * q + 1], v[8 * h + 4 * q + 2],
+                                               v[8 * h + 4 * q + 3]};
+                        if (left >= 16 * h + 8 * q + 8) st_v4(p + 16 * h + 8 * q, r);
+                    }
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void end() {
+        if constexpr (kStaged) {
+            if ((threadIdx.x & 31u) == 0) bulk_wait_read<0>();
+        }
+    }
+};
+
+template <int BN, int CG, int EPI>
+__global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
+    forge_expert_kernel(const __grid_constant__ ExpertGroup<EPI> grp) {
+    using C = BlockCfg<BN, CG, EPI>;
+    constexpr bool kGated = EPI == kBlockGatedFwd, kGrad = EPI == kExpertGrad;
+    constexpr int kColsPerTile = kGated ? BN / 2 : BN;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const int a_rows = CG == 1 ? grp.a_rows : kBM;
+    const int n_stages = CG == 1 ? C::stages(a_rows) : C::kStages;
+    const uint32_t stage_bytes = static_cast<uint32_t>(a_rows) * 128u + C::kBBytes;
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + n_stages * a_rows * 128;  // behind A: the MMA's reads past A's rows stay inside the ring
+    uint8_t* staging = smem + C::kRingBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + C::kStaging);
+    uint64_t* empty = full + C::kMaxStages;
+    uint64_t* acc_full = empty + C::kMaxStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drain = acc_empty + 2;
+    uint64_t* peer_done = drain + 1;
+    uint64_t* peer_count = peer_done + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(peer_count + 1);
+    int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = CG > 1 ? cluster_ctarank() : 0u;
+    const int pair = static_cast<int>(blockIdx.x) / CG;
+    const int pairs = static_cast<int>(gridDim.x) / CG;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < n_stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], C::kEpiWarps * CG);
+        }
+        mbar_init(drain, 1);
+        mbar_init(peer_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        if constexpr (!kGrad) {
+            tma_prefetch_desc(&grp.maps[0]);
+            tma_prefetch_desc(&grp.maps[1]);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(tmem_slot, C::kTmemCols);
+        tmem_relinquish<CG>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG > 1) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const AbortCtx ab{abort_flag, grp.status, grp.wait_limit_ns};
+    uint64_t n_issued = 0;
+    int64_t withheld = -1;
+
+    stream_wait();
+    const int n_tiles = kGrad ? 0 : __ldcg(grp.n_tiles);
+    const int n_units = kGrad ? grp.n_units : n_tiles * grp.prob[0].tiles_n;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const uint64_t keep = policy_evict_last();
+            const uint64_t pol_b = grp.stream_b ? policy_evict_first() : keep;
+            const bool leader = rank == 0;
+            const bool withhold = grp.withhold_first_stage && leader;
+            const uint32_t bars = CG == 2 ? map_to_rank(smem_addr(full), 0) : smem_addr(full);
+            const uint32_t a_bytes = static_cast<uint32_t>(a_rows) * 128u;
+            const uint32_t a_ring = smem_addr(sA), b_ring = smem_addr(sB);
+            // one slice: waits for its slot, arms it and copies into it
+            auto slice = [&](auto&& copies) {
+                if (!wait_bounded(&empty[stage], phase ^ 1u, ab)) return false;
+                if (leader) mbar_arrive_expect_tx(&full[stage], CG * stage_bytes);
+                if (withhold && n_issued == 0) {
+                    withheld = 0;  // test switch: arm this stage but never copy into it
+                } else {
+                    copies(bars + 8u * static_cast<uint32_t>(stage), a_ring + static_cast<uint32_t>(stage) * a_bytes,
+                           b_ring + static_cast<uint32_t>(stage) * C::kBBytes);
+                }
+                ++n_issued;
+                if (++stage == n_stages) { stage = 0; phase ^= 1u; }
+                return true;
+            };
+            int seen_prob = -1, seen_expert = -1;
+            for (int u = pair; ok && u < n_units; u += pairs) {
+                const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles);
+                const ExpertProblem& b = grp.prob[w.prob];
+                const int row_a = w.row0 + static_cast<int>(rank) * kBM;
+                const int col_b = kGated ? w.nb * kColsPerTile : w.nb * BN + static_cast<int>(rank) * C::kBLoad;
+                if constexpr (kGrad) {
+                    const CUtensorMap* ma = grp.runs + static_cast<size_t>(b.map_a) * grp.experts + w.expert;
+                    const CUtensorMap* mb = grp.runs + static_cast<size_t>(b.map_b) * grp.experts + w.expert;
+                    if (w.prob != seen_prob || w.expert != seen_expert) {
+                        tensormap_acquire(ma);
+                        tensormap_acquire(mb);
+                        seen_prob = w.prob;
+                        seen_expert = w.expert;
+                    }
+                    // a run of no rows: one slice past the one row that its maps have
+                    int k0 = w.slices == 0 ? kBK : 0;
+                    const bool a_flat = b.a_flat != 0, b_flat = b.b_flat != 0;
+                    const int a0 = a_flat ? row_a : 0, a2 = a_flat ? 0 : row_a / 64;
+                    const int b0 = b_flat ? col_b : 0, b2 = b_flat ? 0 : col_b / 64;
+                    for (int n = w.slices == 0 ? 1 : w.slices; ok && n > 0; --n, k0 += kBK)
+                        ok = slice([&](uint32_t bar, uint32_t a_dst, uint32_t b_dst) {
+                            tma_load_3d_cg<CG>(a_dst, ma, bar, a0, k0, a2, keep);
+                            tma_load_3d_cg<CG>(b_dst, mb, bar, b0, k0, b2, keep);
+                            if (a_flat) tma_load_3d_cg<CG>(a_dst + kBK * 128, ma, bar, a0 + 64, k0, 0, keep);
+                            if (C::kBLoad == 128 && b_flat) tma_load_3d_cg<CG>(b_dst + kBK * 128, mb, bar, b0 + 64, k0, 0, keep);
+                        });
+                } else {
+                    const bool bmn = EPI == kBlockGatedBwd || (EPI == kBlockStore && b.b_mn != 0);
+                    const bool b_flat = bmn && b.b_flat != 0;
+#pragma unroll 1
+                    for (int seg = 0; seg < (EPI == kBlockStore ? 2 : 1) && ok; ++seg) {
+                        const CUtensorMap* ma = &grp.maps[2 * seg];
+                        // gated forward: the even CTA (or the first half of the columns) holds the gate's rows, the
+                        // other the up projection's, of the same d_ff columns
+                        const CUtensorMap* mb = kGated && CG == 2 && rank == 1 ? &grp.maps[3] : ma + 1;
+                        const CUtensorMap* mu = &grp.maps[3];
+                        int k0 = 0;
+                        int b0 = bmn ? (b_flat ? col_b : 0) : 0, b1 = bmn ? 0 : col_b;
+                        const int b2 = bmn && !b_flat ? col_b / 64 : 0;
+                        const int db0 = bmn ? 0 : kBK, db1 = bmn ? kBK : 0;
+#pragma unroll 1
+                        for (int n = b.kb[seg]; ok && n > 0; --n, k0 += kBK, b0 += db0, b1 += db1)
+                            ok = slice([&](uint32_t bar, uint32_t a_dst, uint32_t b_dst) {
+                                tma_load_3d_cg<CG>(a_dst, ma, bar, k0, row_a, 0, keep);
+                                tma_load_4d_cg<CG>(b_dst, mb, bar, b0, b1, b2, w.expert, pol_b);
+                                if (kGated && CG == 1)
+                                    tma_load_4d_cg<CG>(b_dst + BN / 2 * 128, mu, bar, b0, b1, 0, w.expert, pol_b);
+                                if (!kGated && C::kBLoad == 128 && b_flat)
+                                    tma_load_4d_cg<CG>(b_dst + kBK * 128, mb, bar, b0 + 64, b1, 0, w.expert, pol_b);
+                            });
+                    }
+                }
+            }
+            if constexpr (CG == 2) {
+                if (rank == 1) {
+                    st_shared_cluster_u64(map_to_rank(smem_addr(peer_count), 0), n_issued);
+                    mbar_arrive_remote(map_to_rank(smem_addr(peer_done), 0));
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true, issued_any = false;
+            for (int u = pair; ok && u < n_units; u += pairs) {
+                const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles);
+                const bool amn = kGrad;
+                const bool bmn = kGrad || EPI == kBlockGatedBwd || (EPI == kBlockStore && grp.prob[0].b_mn != 0);
+                const uint32_t idesc = idesc_bf16_f32(kBM * CG, BN, amn, bmn);
+                const uint32_t a_step = (amn ? 2048u : 32u) >> 4, b_step = (bmn ? 2048u : 32u) >> 4;
+                const uint64_t a_desc = smem_desc_sw128(smem_addr(sA), amn ? kBK * 128u : 16u, 1024);
+                const uint64_t b_desc = smem_desc_sw128(smem_addr(sB), bmn ? kBK * 128u : 16u, 1024);
+                if (!wait_bounded(&acc_empty[acc], acc_phase ^ 1u, ab)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                const int slices = w.slices == 0 ? 1 : w.slices;
+#pragma unroll 1
+                for (int kb = 0; kb < slices; ++kb) {
+                    if (!wait_bounded(&full[stage], phase, ab)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t ad = a_desc + static_cast<uint32_t>(stage) * (static_cast<uint32_t>(a_rows) * 128u >> 4);
+                    const uint64_t bd = b_desc + static_cast<uint32_t>(stage) * (C::kBBytes >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kBK / kUmmaK; ++kk)
+                        tc_mma_bf16<CG>(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, (kb | kk) != 0 ? 1u : 0u);
+                    issued_any = true;
+                    tc_commit_mask<CG>(&empty[stage], 0x3u);
+                    if (++stage == n_stages) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                tc_commit_mask<CG>(&acc_full[acc], 0x3u);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (!ok && issued_any) {
+                tc_commit_local<CG>(drain);
+                drain_bounded(drain, 0, grp.wait_limit_ns);
+            }
+        }
+    } else {
+        const int e = warp - 2;
+        const int quarter = warp & 3;  // a warp may only touch TMEM lanes 32 (warp mod 4) .. +31
+        const int half = e >> 2;
+        const AbortCtx ab_acc{abort_flag, grp.status, grp.acc_wait_limit_ns};
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        ExpertOut<(C::kStaging > 0)> out{grp.outs, {grp.to[0], grp.to[1], grp.to[2]}, 0, 0, 0, kGrad,
+                                         smem_addr(staging) + static_cast<uint32_t>(e) * 4096u, 0};
+        for (int u = pair; u < n_units; u += pairs) {
+            const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles);
+            const ExpertProblem& p = grp.prob[w.prob];
+            const int row = w.row0 + static_cast<int>(rank) * kBM + quarter * 32 + lane;
+            BlockProblem b;
+            b.rows = w.end;
+            b.cols = p.cols;
+            b.ld = p.ld;
+            b.add = nullptr;
+            b.unit = nullptr;
+            b.sum_in = b.sum_out = 0;
+            b.act = grp.act;
+            b.keep = grp.keep;
+            b.g_in = grp.g_in;
+            b.u_in = grp.u_in;
+            out.ld = p.ld;
+            out.rows = w.end;
+            if constexpr (kGrad) {
+                const size_t each = static_cast<size_t>(p.rows) * static_cast<size_t>(p.ld);
+                out.to[0] = grp.to[w.prob] + each * static_cast<size_t>(w.expert);
+                out.maps = grp.outs + w.prob;
+                out.z = w.expert;
+            }
+            int ok = 1;
+            if (lane == 0) ok = wait_bounded(&acc_full[acc], acc_phase, ab_acc) ? 1 : 0;
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
+            tc_fence_after();
+            const AccTmem tm{tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN)};
+            if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, tm, row, w.nb, half, out);
+            else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, tm, row, w.nb, half, out);
+            else epi_store<BN>(b, tm, row, w.nb, half, out);
+            // the accumulator's reads are done: it may be overwritten
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(map_to_rank(smem_addr(&acc_empty[acc]), 0));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+        out.end();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && lane == 0 && rank == 0 && *abort_flag) {
+        uint64_t n_peer = n_issued;
+        bool counted = true;
+        if constexpr (CG == 2) {
+            counted = false;
+            const uint64_t t0 = global_timer_ns();
+            while (!counted && global_timer_ns() - t0 <= 4 * grp.wait_limit_ns) counted = mbar_try_wait_cluster(peer_done, 0);
+            if (counted) n_peer = ld_shared_volatile_u64(peer_count);
+        }
+        if (counted) drain_ring<CG>(full, n_stages, n_issued, n_peer, withheld, stage_bytes, grp.wait_limit_ns);
+        else drain_ring<1>(full, n_stages, n_issued, n_issued, withheld, stage_bytes, grp.wait_limit_ns);
+    }
+    if constexpr (CG > 1) cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc<CG>(tmem_base, C::kTmemCols);
+    }
+}
+
+}  // namespace forge

@@ -1,5 +1,5 @@
-"""The operators around the fused layers: the norm, the gated feed-forward block, and the cross
-entropy of a linear head, each with its backward pass.
+"""The operators around the fused layers: the norm, the gated feed-forward block, the cross entropy of a
+linear head, and linear layers and gated blocks with a weight for each expert, each with its backward pass.
 
 Like the rest of the binding this module checks and marshals arguments; the computation is the
 library's.  Results are written to the tensors passed for them.  Tensors are contiguous and on the
@@ -39,10 +39,21 @@ class LossShape(ctypes.Structure):
                 ("ignore_index", ctypes.c_int64), ("reserved", ctypes.c_int64)]
 
 
+class ExpertLinearShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("experts", ctypes.c_int64), ("d_in", ctypes.c_int64), ("d_out", ctypes.c_int64),
+                ("reserved", ctypes.c_int64)]
+
+
+class ExpertGatedShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("experts", ctypes.c_int64), ("d_model", ctypes.c_int64), ("d_ff", ctypes.c_int64),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 def declare(L: ctypes.CDLL) -> None:
     """Argument types of the library's functions that this module calls."""
     vp, i32, i64, u64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
     norm, gated, loss = (ctypes.POINTER(t) for t in (NormShape, GatedShape, LossShape))
+    elinear, egated = ctypes.POINTER(ExpertLinearShape), ctypes.POINTER(ExpertGatedShape)
     layer, hp = ctypes.POINTER(_fg.ForgeLayer), ctypes.POINTER(_fg.ForgeHparams)
     for name, args in {
         "forge_layer_norm": [vp] * 6 + [f32, norm, vp],
@@ -53,6 +64,10 @@ def declare(L: ctypes.CDLL) -> None:
         "forge_linear_cross_entropy": [vp] * 6 + [i64, loss, vp],
         "forge_linear_cross_entropy_backward": [vp] * 8 + [i64, loss, vp],
         "forge_linear_cross_entropy_step": [vp] * 10 + [i64, i32, ctypes.c_int, hp, loss, i64, u64, vp],
+        "forge_expert_linear": [vp] * 5 + [i64, elinear, vp],
+        "forge_expert_linear_backward": [vp] * 7 + [i64, elinear, vp],
+        "forge_expert_gated_mlp": [vp] * 9 + [i64, egated, vp],
+        "forge_expert_gated_mlp_backward": [vp] * 13 + [i64, egated, vp],
         "forge_gated_mlp_launch_shape": [gated, i32] + [ctypes.POINTER(i32)] * 4,
         "forge_linear_cross_entropy_launch_shape": [loss, i32] + [ctypes.POINTER(i32)] * 4,
     }.items():
@@ -62,6 +77,8 @@ def declare(L: ctypes.CDLL) -> None:
         "forge_layer_norm_backward_workspace": [norm],
         "forge_gated_mlp_workspace": [gated, i32],
         "forge_linear_cross_entropy_workspace": [loss, i32],
+        "forge_expert_linear_workspace": [elinear],
+        "forge_expert_gated_mlp_workspace": [egated, i32],
     }.items():
         f = getattr(L, name)
         f.argtypes, f.restype = args, i64
@@ -330,6 +347,71 @@ def linear_cross_entropy_step(X, W, target, lse, dloss, dX=None, m=None, v=None,
         *args, dx, p(m), p(v), p(qscales), ws, n, _fg._state_of(m, v), _fg.OPT_KINDS[opt], _fg._hp_arg(hp), shape.arg,
         int(step), int(seed) & (2**64 - 1), raw)
     _fg._check(st, "forge_linear_cross_entropy_step")
+
+
+# ------------------------------------------------------------------ products grouped by expert
+
+
+def _grouped(X, W, name: str):
+    """Device, rows, width, experts and the weight's other width."""
+    dev = _device(X)
+    R, D = _matrix(X, "X")
+    if W.dim() != 3:
+        raise ValueError(f"{name}: {W.dim()} dimensions, expected 3")
+    return dev, R, D, W.shape[0], W.shape[1]
+
+
+def expert_linear(X, W, offsets, Y, stream=None) -> None:
+    """Y[r] = X[r] W[e]^T for the rows r = offsets[e] .. offsets[e+1]-1 of each expert e, everything bf16: X [R, d_in]
+    sorted by expert, W [E, d_out, d_in], Y [R, d_out]; offsets int32 [E+1] on the device, never read on the host.
+    Rows of no expert are left as they were."""
+    dev, R, D, E, F = _grouped(X, W, "W")
+    shape = _shape(ExpertLinearShape, R, E, D, F, 0)
+    x, w = _take(X, _BF16, (R, D), dev, "X"), _take(W, _BF16, (E, F, D), dev, "W")
+    o, y = _take(offsets, torch.int32, (E + 1,), dev, "offsets"), _take(Y, _BF16, (R, F), dev, "Y")
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_expert_linear_workspace", dev, stream, raw)
+    _fg._check(_fg.lib().forge_expert_linear(x, w, o, y, ws, n, shape.arg, raw), "forge_expert_linear")
+
+
+def expert_linear_backward(dY, X, W, offsets, dX, dW, stream=None) -> None:
+    """dX [R, d_in] and dW [E, d_out, d_in] (bf16, either may be None) of expert_linear from dY [R, d_out].  dW of an
+    expert without rows is zero."""
+    dev, R, D, E, F = _grouped(X, W, "W")
+    shape = _shape(ExpertLinearShape, R, E, D, F, 0)
+    args = [_take(t, dt, s, dev, name) for t, dt, s, name in (
+        (dY, _BF16, (R, F), "dY"), (X, _BF16, (R, D), "X"), (W, _BF16, (E, F, D), "W"),
+        (offsets, torch.int32, (E + 1,), "offsets"), (dX, _BF16, (R, D), "dX"), (dW, _BF16, (E, F, D), "dW"))]
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_expert_linear_workspace", dev, stream, raw)
+    _fg._check(_fg.lib().forge_expert_linear_backward(*args, ws, n, shape.arg, raw), "forge_expert_linear_backward")
+
+
+def expert_gated_mlp(X, Wg, Wu, Wd, offsets, Y, G=None, U=None, act: str = "silu", stream=None) -> None:
+    """gated_mlp with each expert's weights for its rows, as expert_linear: Wg and Wu [E, F, D], Wd [E, D, F]; X and Y
+    [R, D]; G and U [R, F], both or neither, for the backward pass."""
+    dev, R, D, E, F = _grouped(X, Wg, "Wg")
+    shape = _shape(ExpertGatedShape, R, E, D, F, _one_of(ACTIVATIONS, act, "act"), 0)
+    args = [_take(t, dt, s, dev, name) for t, dt, s, name in (
+        (X, _BF16, (R, D), "X"), (Wg, _BF16, (E, F, D), "Wg"), (Wu, _BF16, (E, F, D), "Wu"), (Wd, _BF16, (E, D, F), "Wd"),
+        (offsets, torch.int32, (E + 1,), "offsets"), (Y, _BF16, (R, D), "Y"), (G, _BF16, (R, F), "G"), (U, _BF16, (R, F), "U"))]
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_expert_gated_mlp_workspace", dev, stream, raw, 0)
+    _fg._check(_fg.lib().forge_expert_gated_mlp(*args, ws, n, shape.arg, raw), "forge_expert_gated_mlp")
+
+
+def expert_gated_mlp_backward(dY, X, G, U, Wg, Wu, Wd, offsets, dX, dWg, dWu, dWd, act: str = "silu", stream=None) -> None:
+    """The gradients of expert_gated_mlp, bf16, from dY [R, D] and the forward pass's X, G and U.  dX may be None."""
+    dev, R, D, E, F = _grouped(X, Wg, "Wg")
+    shape = _shape(ExpertGatedShape, R, E, D, F, _one_of(ACTIVATIONS, act, "act"), 0)
+    args = [_take(t, dt, s, dev, name) for t, dt, s, name in (
+        (dY, _BF16, (R, D), "dY"), (X, _BF16, (R, D), "X"), (G, _BF16, (R, F), "G"), (U, _BF16, (R, F), "U"),
+        (Wg, _BF16, (E, F, D), "Wg"), (Wu, _BF16, (E, F, D), "Wu"), (Wd, _BF16, (E, D, F), "Wd"),
+        (offsets, torch.int32, (E + 1,), "offsets"), (dX, _BF16, (R, D), "dX"), (dWg, _BF16, (E, F, D), "dWg"),
+        (dWu, _BF16, (E, F, D), "dWu"), (dWd, _BF16, (E, D, F), "dWd"))]
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_expert_gated_mlp_workspace", dev, stream, raw, 1)
+    _fg._check(_fg.lib().forge_expert_gated_mlp_backward(*args, ws, n, shape.arg, raw), "forge_expert_gated_mlp_backward")
 
 
 # ------------------------------------------------------------------ how the products are cut

@@ -411,6 +411,67 @@ FORGE_API forge_status forge_linear_cross_entropy_step(const void *X, void *W, c
 /* backward: 0 for forge_linear_cross_entropy, 1 for either backward call. */
 FORGE_API int64_t forge_linear_cross_entropy_workspace(const forge_loss_shape *shape, int32_t backward);
 
+/* ------------------------------------------------------------------ products grouped by expert
+ * Rows of X lie sorted by expert: expert e owns the rows offsets[e] .. offsets[e+1]-1, any number of them, and
+ * weights of its own, which lie one expert after another.  offsets int32 [experts + 1] is in device memory and
+ * never read on the host: sizes may differ from call to call, and from replay to replay of a captured call.
+ * Offsets are in order and within 0 .. rows; one that is not is taken as the nearest one that is, so that
+ * nothing outside the tensors is read or written whatever they hold.  Rows before the first offset and from the
+ * last one on belong to no expert: results leave them as they were, and they count for no gradient, whatever
+ * they hold.  Everything else is as in the dense operators above: bfloat16, 32-byte aligned pointers, sums in
+ * FP32, widths multiples of 8. */
+
+typedef struct forge_expert_linear_shape {
+    int64_t rows;     /* of X, >= 0 */
+    int64_t experts;  /* 1 .. 1024 */
+    int64_t d_in;     /* >= 8, a multiple of 8 */
+    int64_t d_out;    /* >= 8, a multiple of 8 */
+    int64_t reserved;
+} forge_expert_linear_shape;
+
+/* Y[r] = X[r] W[e]^T for every row r of expert e: X [rows, d_in], W [experts, d_out, d_in], Y [rows, d_out].
+ * Y must not overlap X. */
+FORGE_API forge_status forge_expert_linear(const void *X, const void *W, const int32_t *offsets, void *Y,
+                                           void *workspace, int64_t workspace_bytes,
+                                           const forge_expert_linear_shape *shape, struct CUstream_st *stream);
+
+/* Its gradients: dX[r] = dY[r] W[e], dW[e] = sum over e's rows of dY[r]^T X[r] (zero for an expert without rows),
+ * bfloat16.  Either of dX and dW may be null: it is not computed.  rows = 0 sets dW to zero. */
+FORGE_API forge_status forge_expert_linear_backward(const void *dY, const void *X, const void *W, const int32_t *offsets,
+                                                    void *dX, void *dW, void *workspace, int64_t workspace_bytes,
+                                                    const forge_expert_linear_shape *shape, struct CUstream_st *stream);
+
+/* Of every expert_linear call. */
+FORGE_API int64_t forge_expert_linear_workspace(const forge_expert_linear_shape *shape);
+
+typedef struct forge_expert_gated_shape {
+    int64_t rows;     /* of X, >= 0 */
+    int64_t experts;  /* 1 .. 1024 */
+    int64_t d_model;  /* >= 8, a multiple of 8 */
+    int64_t d_ff;     /* >= 8, a multiple of 8 */
+    int32_t act;      /* forge_act */
+    int32_t reserved;
+} forge_expert_gated_shape;
+
+/* The gated feed-forward block with each expert's weights: Y [rows, d_model] = H Wd[e]^T, H = act(X Wg[e]^T) *
+ * (X Wu[e]^T); Wg and Wu [experts, d_ff, d_model], Wd [experts, d_model, d_ff].  G and U [rows, d_ff], both or
+ * neither null: what the backward pass needs.  Y must not overlap X. */
+FORGE_API forge_status forge_expert_gated_mlp(const void *X, const void *Wg, const void *Wu, const void *Wd,
+                                              const int32_t *offsets, void *Y, void *G, void *U, void *workspace,
+                                              int64_t workspace_bytes, const forge_expert_gated_shape *shape,
+                                              struct CUstream_st *stream);
+
+/* Its gradients, as forge_gated_mlp_backward's with each expert's rows and weights; an expert without rows has
+ * zero ones.  dX may be null: it is not computed.  rows = 0 sets the weights' gradients to zero. */
+FORGE_API forge_status forge_expert_gated_mlp_backward(const void *dY, const void *X, const void *G, const void *U,
+                                                       const void *Wg, const void *Wu, const void *Wd,
+                                                       const int32_t *offsets, void *dX, void *dWg, void *dWu, void *dWd,
+                                                       void *workspace, int64_t workspace_bytes,
+                                                       const forge_expert_gated_shape *shape, struct CUstream_st *stream);
+
+/* backward: 0 for forge_expert_gated_mlp, 1 for either backward call. */
+FORGE_API int64_t forge_expert_gated_mlp_workspace(const forge_expert_gated_shape *shape, int32_t backward);
+
 /* Waits for `stream`, then reads and clears the device status word of the current
  * device: FORGE_ERR_TIMEOUT if a bounded wait ran out in a kernel (on any stream of
  * this device) since the last read, FORGE_ERR_CUDA if the stream reported an error,
