@@ -86,7 +86,7 @@ __device__ __forceinline__ Philox4 philox4x32_10(uint32_t c0, uint32_t c1, uint3
 // Stochastic-rounding streams: the weight, and the first and second moments when they are stored
 // as BF16.  The stream index goes into the top two bits of the high counter word, which the
 // element index never reaches (at most 2^41 groups of 8 elements per layer).
-enum SrStream : uint32_t { kStreamW = 0, kStreamM = 1, kStreamV = 2 };
+enum SrStream : uint32_t { kStreamW = 0, kStreamM = 1, kStreamV = 2, kStreamDropout = 3 };  // the last: dropout_api.cu
 
 // 16-bit random values for the 8 elements e8*8 .. e8*8+7 of tensor `stream` at step `step`:
 // element 2k takes the low half of word k, element 2k+1 its high half.

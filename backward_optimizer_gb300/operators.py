@@ -1,5 +1,6 @@
 """The operators around the fused layers: the norm, the gated feed-forward block, the cross entropy of a
-linear head, and linear layers and gated blocks with a weight for each expert, each with its backward pass.
+linear head, linear layers and gated blocks with a weight for each expert, dropout from a counter, and the
+preference loss of pairs of sequences, each with its backward pass.
 
 Like the rest of the binding this module checks and marshals arguments; the computation is the
 library's.  Results are written to the tensors passed for them.  Tensors are contiguous and on the
@@ -19,6 +20,7 @@ import torch
 import backward_optimizer_gb300 as _fg
 
 NORM_KINDS = {"layer": 0, "rms": 1}
+PREFERENCES = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1, "relu": 2}
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 _BF16, _F32 = torch.bfloat16, torch.float32
@@ -39,6 +41,12 @@ class LossShape(ctypes.Structure):
                 ("ignore_index", ctypes.c_int64), ("reserved", ctypes.c_int64)]
 
 
+class PreferenceShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("pairs", ctypes.c_int64), ("kind", ctypes.c_int32), ("mean", ctypes.c_int32),
+                ("beta", ctypes.c_float), ("smoothing", ctypes.c_float), ("margin", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
 class ExpertLinearShape(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("experts", ctypes.c_int64), ("d_in", ctypes.c_int64), ("d_out", ctypes.c_int64),
                 ("reserved", ctypes.c_int64)]
@@ -53,7 +61,7 @@ def declare(L: ctypes.CDLL) -> None:
     """Argument types of the library's functions that this module calls."""
     vp, i32, i64, u64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
     norm, gated, loss = (ctypes.POINTER(t) for t in (NormShape, GatedShape, LossShape))
-    elinear, egated = ctypes.POINTER(ExpertLinearShape), ctypes.POINTER(ExpertGatedShape)
+    elinear, egated, pref = (ctypes.POINTER(t) for t in (ExpertLinearShape, ExpertGatedShape, PreferenceShape))
     layer, hp = ctypes.POINTER(_fg.ForgeLayer), ctypes.POINTER(_fg.ForgeHparams)
     for name, args in {
         "forge_layer_norm": [vp] * 6 + [f32, norm, vp],
@@ -68,6 +76,9 @@ def declare(L: ctypes.CDLL) -> None:
         "forge_expert_linear_backward": [vp] * 7 + [i64, elinear, vp],
         "forge_expert_gated_mlp": [vp] * 9 + [i64, egated, vp],
         "forge_expert_gated_mlp_backward": [vp] * 13 + [i64, egated, vp],
+        "forge_dropout": [vp] * 3 + [i64, i32, ctypes.c_double, u64, u64, vp, vp],
+        "forge_preference_loss": [vp] * 8 + [i64, pref, vp],
+        "forge_preference_loss_backward": [vp] * 5 + [pref, vp],
         "forge_gated_mlp_launch_shape": [gated, i32] + [ctypes.POINTER(i32)] * 4,
         "forge_linear_cross_entropy_launch_shape": [loss, i32] + [ctypes.POINTER(i32)] * 4,
     }.items():
@@ -78,6 +89,7 @@ def declare(L: ctypes.CDLL) -> None:
         "forge_gated_mlp_workspace": [gated, i32],
         "forge_linear_cross_entropy_workspace": [loss, i32],
         "forge_expert_linear_workspace": [elinear],
+        "forge_preference_loss_workspace": [pref],
         "forge_expert_gated_mlp_workspace": [egated, i32],
     }.items():
         f = getattr(L, name)
@@ -193,6 +205,12 @@ def _matrix(t, name: str) -> tuple:
     if t.dim() != 2:
         raise ValueError(f"{name}: {t.dim()} dimensions, expected 2")
     return tuple(t.shape)
+
+
+def _vector(t, name: str) -> int:
+    if t.dim() != 1:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected 1")
+    return t.shape[0]
 
 
 def _states(dev: int, W, m, v, qscales) -> None:
@@ -412,6 +430,66 @@ def expert_gated_mlp_backward(dY, X, G, U, Wg, Wu, Wd, offsets, dX, dWg, dWu, dW
     raw = _raw_stream(stream, dev)
     ws, n, _hold = _workspace(shape, "forge_expert_gated_mlp_workspace", dev, stream, raw, 1)
     _fg._check(_fg.lib().forge_expert_gated_mlp_backward(*args, ws, n, shape.arg, raw), "forge_expert_gated_mlp_backward")
+
+
+# ------------------------------------------------------------------ dropout
+
+
+def dropout(x, y, p: float, seed: int = 0, step: int = 0, residual=None, stream=None) -> None:
+    """y = dropout(x) (+ residual): each element is 0 with probability p (rounded to 2^-16), else x / (1 - p).  x,
+    residual and y bf16 or FP32, of one shape and type.  The mask is made from seed, step and the element's place and is
+    never stored.  step: a number, or an int64 tensor of one element on the device, which a captured call reads
+    at each replay."""
+    dev = _device(x)
+    dt, shape = x.dtype, tuple(x.shape)
+    at = None
+    if torch.is_tensor(step):
+        at, step = _take(step.view(-1) if step.dim() == 0 else step, torch.int64, (1,), dev, "step"), 0
+    _fg._check(_fg.lib().forge_dropout(
+        _take(x, dt, shape, dev, "x"), _take(residual, dt, shape, dev, "residual"), _take(y, dt, shape, dev, "y"), x.numel(),
+        _type(x, "x"), float(p), int(seed) & (2**64 - 1), int(step) & (2**64 - 1), at, _raw_stream(stream, dev)), "forge_dropout")
+
+
+def dropout_backward(dy, dx, p: float, seed: int = 0, step: int = 0, stream=None) -> None:
+    """dx of dropout from dy and the forward pass's p, seed and step.  (The gradient of residual is dy.)"""
+    dropout(dy, dx, p, seed=seed, step=step, stream=stream)
+
+
+# ------------------------------------------------------------------ preference loss
+
+
+def preference_loss(nll, ref, offsets, loss, reward=None, slope=None, mask=None, beta: float = 0.1, kind: str = "sigmoid",
+                    smoothing: float = 0.0, margin: float = 0.0, mean: bool = False, stream=None) -> None:
+    """loss [P] of P pairs of sequences: nll and ref [T], each token's -log probability under the model (what
+    linear_cross_entropy leaves) and under the reference (None: 0); sequence i is tokens offsets[i] .. offsets[i+1]-1
+    (int32 [2P+1] on the device), the chosen ones first, then the rejected ones; tokens where mask (bool [T]) is False do
+    not count.  score = sum of ref - nll (mean=True: the mean), z = beta (chosen - rejected) - margin; kind "sigmoid"
+    (-log sigmoid(z), with label smoothing), "hinge" (max(0, 1 - z)) or "ipo" (((z - 1/2) / beta)^2).  reward [2P] = beta
+    score; slope [2P] is what the backward pass needs.  FP32 but for offsets and mask."""
+    dev = _device(nll)
+    T, P = _vector(nll, "nll"), _vector(loss, "loss")
+    shape = _shape(PreferenceShape, T, P, _one_of(PREFERENCES, kind, "kind"), int(bool(mean)), float(beta), float(smoothing),
+                   float(margin), 0)
+    args = [_take(t, dt, s, dev, name) for t, dt, s, name in (
+        (nll, _F32, (T,), "nll"), (ref, _F32, (T,), "ref"), (mask, torch.bool, (T,), "mask"),
+        (offsets, torch.int32, (2 * P + 1,), "offsets"), (loss, _F32, (P,), "loss"), (reward, _F32, (2 * P,), "reward"),
+        (slope, _F32, (2 * P,), "slope"))]
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_preference_loss_workspace", dev, stream, raw)
+    _fg._check(_fg.lib().forge_preference_loss(*args, ws, n, shape.arg, raw), "forge_preference_loss")
+
+
+def preference_loss_backward(dloss, slope, offsets, dnll, mask=None, stream=None) -> None:
+    """dnll [T], the gradient of each token's nll (linear_cross_entropy's dloss), from dloss [P] and the forward pass's
+    slope [2P]; 0 for tokens that do not count."""
+    dev = _device(dnll)
+    T, P = _vector(dnll, "dnll"), _vector(dloss, "dloss")
+    shape = _shape(PreferenceShape, T, P, 0, 0, 1.0, 0.0, 0.0, 0)
+    args = [_take(t, dt, s, dev, name) for t, dt, s, name in (
+        (dloss, _F32, (P,), "dloss"), (slope, _F32, (2 * P,), "slope"), (mask, torch.bool, (T,), "mask"),
+        (offsets, torch.int32, (2 * P + 1,), "offsets"), (dnll, _F32, (T,), "dnll"))]
+    _fg._check(_fg.lib().forge_preference_loss_backward(*args, shape.arg, _raw_stream(stream, dev)),
+               "forge_preference_loss_backward")
 
 
 # ------------------------------------------------------------------ how the products are cut

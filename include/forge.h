@@ -472,6 +472,59 @@ FORGE_API forge_status forge_expert_gated_mlp_backward(const void *dY, const voi
 /* backward: 0 for forge_expert_gated_mlp, 1 for either backward call. */
 FORGE_API int64_t forge_expert_gated_mlp_workspace(const forge_expert_gated_shape *shape, int32_t backward);
 
+/* ------------------------------------------------------------------ dropout from a counter
+ * y[e] = x[e] s where element e is kept, 0 where it is dropped, plus residual[e] (residual may be null): x,
+ * residual and y hold n elements of forge_type `type`, any shape in one piece, at their elements' alignment (16-byte
+ * aligned ones are faster).  y may be x or residual, and must overlap neither otherwise.  Whether e is dropped
+ * depends on p, seed, step and e alone: its number is 16 bits of Philox4x32-10 keyed by seed, at the counter of the
+ * fused step's stochastic rounding in a stream of its own (the high word of e div 8 plus 3 * 2^30; e takes the low
+ * (e even) or high (e odd) half of word (e div 2) mod 4), and e is dropped where it is below q = p 2^16 rounded to
+ * the nearest whole number; s = 2^16 / (2^16 - q).  0 <= p <= 1; at p = 1 all are dropped.  A dropped element may
+ * be infinite or NaN.  step_at: where the step is read from in device memory instead, so that the replays of a captured
+ * call can differ, or null.  The same call with x = dy and no residual is the backward pass; the gradient of the
+ * residual is dy itself. */
+FORGE_API forge_status forge_dropout(const void *x, const void *residual, void *y, int64_t n, int32_t type, double p,
+                                     uint64_t seed, uint64_t step, const int64_t *step_at, struct CUstream_st *stream);
+
+/* ------------------------------------------------------------------ preference loss of pairs of sequences
+ * 2 P sequences of tokens lie one after another: sequence i owns tokens offsets[i] .. offsets[i+1]-1, offsets int32
+ * [2 P + 1] in device memory, in order and within the tokens (results are unspecified where they are not; nothing
+ * outside the tensors is read or written).  Sequences 0 .. P-1 are the chosen answers, P .. 2P-1 the rejected
+ * ones of the same pairs; any may be empty.  nll and ref FP32 [tokens]: each token's -log probability under the
+ * model and under the reference (forge_linear_cross_entropy's loss); ref null: 0.  mask [tokens], a byte each,
+ * or null: tokens with mask 0 do not count, whatever they hold.
+ *   score_i = sum of (ref - nll) over the tokens that count (mean: divided by their number; 0 where there are none),
+ *   z_p = beta (score_p - score_{P+p}) - margin,
+ *   loss_p = (1 - smoothing) log(1 + exp(-z)) + smoothing log(1 + exp(z))   (FORGE_PREF_SIGMOID),
+ *            max(0, 1 - z) (FORGE_PREF_HINGE) or ((z - 1/2) / beta)^2 (FORGE_PREF_IPO),
+ *   reward_i = beta score_i, slope_i = d loss_p / d nll of each token of sequence i that counts. */
+typedef enum forge_preference_kind { FORGE_PREF_SIGMOID = 0, FORGE_PREF_HINGE = 1, FORGE_PREF_IPO = 2 } forge_preference_kind;
+
+typedef struct forge_preference_shape {
+    int64_t tokens;   /* 0 .. 2^30 */
+    int64_t pairs;    /* P, 0 .. 2^24 */
+    int32_t kind;     /* forge_preference_kind */
+    int32_t mean;     /* scores are means over the tokens that count */
+    float beta;       /* > 0 */
+    float smoothing;  /* 0 <= smoothing < 1; 0 unless FORGE_PREF_SIGMOID */
+    float margin;
+    int32_t reserved;
+} forge_preference_shape;
+
+/* loss [P], reward [2 P] and slope [2 P], FP32; reward and slope may be null.  Sums are binary64. */
+FORGE_API forge_status forge_preference_loss(const float *nll, const float *ref, const uint8_t *mask,
+                                             const int32_t *offsets, float *loss, float *reward, float *slope,
+                                             void *workspace, int64_t workspace_bytes,
+                                             const forge_preference_shape *shape, struct CUstream_st *stream);
+FORGE_API int64_t forge_preference_loss_workspace(const forge_preference_shape *shape);
+
+/* dnll [tokens] = dloss of the token's pair times the forward pass's slope of its sequence; 0 for tokens that do not
+ * count and for tokens of no sequence.  Of the shape, tokens and pairs count.  (It is the dloss of
+ * forge_linear_cross_entropy_backward and forge_linear_cross_entropy_step.) */
+FORGE_API forge_status forge_preference_loss_backward(const float *dloss, const float *slope, const uint8_t *mask,
+                                                      const int32_t *offsets, float *dnll,
+                                                      const forge_preference_shape *shape, struct CUstream_st *stream);
+
 /* Waits for `stream`, then reads and clears the device status word of the current
  * device: FORGE_ERR_TIMEOUT if a bounded wait ran out in a kernel (on any stream of
  * this device) since the last read, FORGE_ERR_CUDA if the stream reported an error,
