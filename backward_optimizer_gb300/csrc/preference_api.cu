@@ -5,11 +5,15 @@
 //   z_p = beta (score_p - score_{P+p}) - margin, loss_p = f(z_p).
 //
 // The sums are the work.  Sequences are ragged, from none to all of the tokens, so they are not what is dealt out:
-// tokens are, `chunk` to a warp.  A warp finds the first sequence that reaches into its tokens (two steps of a
-// 32-way search) and leaves one partial sum for each sequence it meets.  Chunk c and sequence i meet at most once
-// and both grow along the tokens, so c + i numbers the meetings without a gap for two: that is the partial's
+// tokens are, `chunk` to a warp.  A warp finds the first sequence that reaches into its tokens (two or three steps
+// of a 32-way search) and leaves one partial sum for each sequence it meets.  Chunk c and sequence i meet at most
+// once and both grow along the tokens, so c + i numbers the meetings without a gap for two: that is the partial's
 // place, and it needs no counter.  A second launch adds a sequence's partials in their order, so results do not
-// depend on timing.  Sums are binary64: over long sequences the policy's and the reference's nearly cancel.
+// depend on timing; up to 4096 tokens one block does both.
+//
+// Over long sequences the policy's and the reference's sums nearly cancel, so they are kept to some 48 bits: a value
+// is a pair of binary32, each addition exact up to the pair's second part (Knuth's two-sum).  Binary64 would do the
+// same, but the chip has few units for it (262144 tokens of 256 pairs: 21.2 us with it).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,9 +30,37 @@ namespace host = forge::host;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
+// hi + lo
+struct Wide {
+    float hi, lo;
+};
+
+// a + b, and what its rounding left out
+__device__ __forceinline__ Wide two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+    return Wide{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+__device__ __forceinline__ void add(Wide& a, Wide b) {
+    const Wide s = two_sum(a.hi, b.hi);
+    a.hi = s.hi;
+    a.lo = __fadd_rn(a.lo, __fadd_rn(s.lo, b.lo));
+}
+// An infinite sum has no second part (two_sum leaves a NaN there).
+__device__ __forceinline__ Wide settled(Wide a) {
+    if (!(fabsf(a.hi) < INFINITY)) return Wide{a.hi, 0.0f};
+    const Wide s = two_sum(a.hi, a.lo);
+    return s;
+}
+// a / n
+__device__ __forceinline__ Wide divided(Wide a, int n) {
+    const float by = static_cast<float>(n), rest = static_cast<float>(n - static_cast<int>(by));
+    const float q = a.hi / by;
+    return settled(Wide{q, (__fmaf_rn(-q, by, a.hi) + a.lo - q * rest) / by});
+}
+
 struct Partial {
-    double sum;
-    int64_t count;
+    float hi, lo;
+    int count, unused;
 };
 
 struct PrefArgs {
@@ -87,15 +119,12 @@ __device__ __forceinline__ void pair_loss(const PrefArgs& a, float z, float& los
     }
 }
 
-__device__ __forceinline__ double sum_all(double v) {
+__device__ __forceinline__ void sum_all(Wide& v, int& n) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
-__device__ __forceinline__ int64_t sum_all(int64_t v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
+    for (int o = 16; o > 0; o >>= 1) {
+        add(v, Wide{__shfl_xor_sync(0xFFFFFFFFu, v.hi, o), __shfl_xor_sync(0xFFFFFFFFu, v.lo, o)});
+        n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+    }
 }
 
 // The partial sums of one chunk of tokens: a warp.
@@ -107,8 +136,8 @@ __device__ __forceinline__ void chunk_sums(const PrefArgs& a, int c) {
         end = offset_at(a, i + 1);
         const int from = max(begin, t0), to = min(end, t1);
         if (from >= to) continue;
-        double s = 0.0;
-        int64_t n = 0;
+        Wide s{0.0f, 0.0f};
+        int n = 0;
         constexpr int kAhead = 8;
         for (int t = from + lane; t < to; t += 32 * kAhead) {
             float x[kAhead], r[kAhead];
@@ -124,48 +153,52 @@ __device__ __forceinline__ void chunk_sums(const PrefArgs& a, int c) {
             for (int j = 0; j < kAhead; ++j) {
                 // a masked token's values are left out, whatever they are
                 if (counts[j]) {
-                    s += static_cast<double>(r[j]) - static_cast<double>(x[j]);
+                    add(s, two_sum(r[j], -x[j]));
                     ++n;
                 }
             }
         }
-        s = sum_all(s);
-        n = sum_all(n);
-        if (lane == 0) a.parts[c + i] = Partial{s, n};
+        sum_all(s, n);
+        if (lane == 0) a.parts[c + i] = Partial{s.hi, s.lo, n, 0};
     }
 }
 
 // One pair from its sequences' partials: a warp.
 __device__ __forceinline__ void finish_pair(const PrefArgs& a, int p) {
     const int lane = threadIdx.x & 31;
-    double score[2];
+    Wide score[2];
     float per[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = p + h * a.pairs, begin = offset_at(a, i), end = offset_at(a, i + 1);
-        double s = 0.0;
-        int64_t n = 0;
+        Wide s{0.0f, 0.0f};
+        int n = 0;
         if (begin < end) {
             const int last = (end - 1) / a.chunk;
+#pragma unroll 4
             for (int c = begin / a.chunk + lane; c <= last; c += 32) {
-                s += __ldcg(&a.parts[c + i].sum);
-                n += __ldcg(reinterpret_cast<const long long*>(&a.parts[c + i].count));
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.parts + c + i));
+                add(s, Wide{v.x, v.y});
+                n += __float_as_int(v.z);
             }
         }
-        s = sum_all(s);
-        n = sum_all(n);
-        const double count = a.mean && n > 1 ? static_cast<double>(n) : 1.0;
-        score[h] = s / count;
-        per[h] = static_cast<float>(1.0 / count);
+        sum_all(s, n);
+        const bool several = a.mean && n > 1;
+        score[h] = several ? divided(settled(s), n) : settled(s);
+        per[h] = several ? 1.0f / static_cast<float>(n) : 1.0f;
     }
     if (lane != 0) return;
-    const double beta = a.beta;
+    auto times_beta = [&](Wide v, float less) {
+        return v.lo == 0.0f ? __fmaf_rn(a.beta, v.hi, -less) : __fmaf_rn(a.beta, v.hi, __fmaf_rn(a.beta, v.lo, -less));
+    };
+    Wide d = two_sum(score[0].hi, -score[1].hi);
+    d.lo += score[0].lo - score[1].lo;
     float loss, g;
-    pair_loss(a, static_cast<float>(beta * (score[0] - score[1]) - a.margin), loss, g);
+    pair_loss(a, times_beta(settled(d), a.margin), loss, g);
     a.loss[p] = loss;
     if (a.reward != nullptr) {
-        a.reward[p] = static_cast<float>(beta * score[0]);
-        a.reward[a.pairs + p] = static_cast<float>(beta * score[1]);
+        a.reward[p] = times_beta(score[0], 0.0f);
+        a.reward[a.pairs + p] = times_beta(score[1], 0.0f);
     }
     if (a.slope != nullptr) {  // of a token's nll: it counts -1 in its score
         a.slope[p] = -g * a.beta * per[0];
@@ -175,15 +208,15 @@ __device__ __forceinline__ void finish_pair(const PrefArgs& a, int p) {
 
 // kAll: one block makes the sums and finishes the pairs itself.
 template <bool kAll>
-__global__ void __launch_bounds__(kThreads) pref_sums_kernel(const PrefArgs a) {
+__global__ void __launch_bounds__(kAll ? 1024 : kThreads) pref_sums_kernel(const PrefArgs a) {
     forge::stream_wait();
     const int warp = static_cast<int>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const int chunks = (a.tokens + a.chunk - 1) / a.chunk;
     if constexpr (kAll) {
-        for (int c = warp; c < chunks; c += kWarps) chunk_sums(a, c);
+        for (int c = warp; c < chunks; c += 32) chunk_sums(a, c);
         __threadfence_block();
         __syncthreads();
-        for (int p = warp; p < a.pairs; p += kWarps) finish_pair(a, p);
+        for (int p = warp; p < a.pairs; p += 32) finish_pair(a, p);
     } else if (warp < chunks) {
         chunk_sums(a, warp);
     }
@@ -217,14 +250,17 @@ __global__ void __launch_bounds__(kThreads) pref_grad_kernel(const PrefArgs a) {
     }
 }
 
-// Tokens of a warp: as many as a few sequences have, between 32 and 512.
-int chunk_of(int64_t tokens, int64_t pairs) {
-    int chunk = 32;
-    while (chunk < 512 && chunk < 4 * (tokens / std::max<int64_t>(2 * pairs, 1))) chunk *= 2;
-    return chunk;
-}
+constexpr int kOneBlock = 4096, kOneBlockPairs = 64;  // tokens and pairs that one block takes by itself
 
-constexpr int kOneBlock = 4096;  // tokens that one block takes by itself
+// Tokens of a warp: as many as a few sequences have, between 32 and 256 (128 where one block does it all), more only
+// where the partials of one long sequence would be too many for the warp that adds them.
+int chunk_of(int64_t tokens, int64_t pairs) {
+    const int64_t most = tokens <= kOneBlock ? 128 : 256;
+    int64_t chunk = 32;
+    while (chunk < most && chunk < 4 * (tokens / std::max<int64_t>(2 * pairs, 1))) chunk *= 2;
+    while (chunk * 8192 < tokens) chunk *= 2;
+    return static_cast<int>(chunk);
+}
 
 forge_status check(const forge_preference_shape* s) {
     if (s == nullptr || s->reserved != 0) return FORGE_ERR_INVALID_ARGUMENT;
@@ -289,8 +325,8 @@ forge_status forge_preference_loss(const float* nll, const float* ref, const uin
     a.slope = slope;
     a.parts = static_cast<Partial*>(workspace);
     const dim3 block(kThreads);
-    if (shape->tokens <= kOneBlock && shape->pairs <= 8 * kWarps)
-        return host::launch_early(pref_sums_kernel<true>, dim3(1), block, 0, stream, a) == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
+    if (shape->tokens <= kOneBlock && shape->pairs <= kOneBlockPairs)
+        return host::launch_early(pref_sums_kernel<true>, dim3(1), dim3(1024), 0, stream, a) == cudaSuccess ? FORGE_OK : FORGE_ERR_CUDA;
     if (a.tokens > 0 && host::launch_early(pref_sums_kernel<false>, dim3(blocks((a.tokens + a.chunk - 1) / a.chunk)), block, 0,
                                            stream, a) != cudaSuccess)
         return FORGE_ERR_CUDA;

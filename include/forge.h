@@ -511,7 +511,7 @@ typedef struct forge_preference_shape {
     int32_t reserved;
 } forge_preference_shape;
 
-/* loss [P], reward [2 P] and slope [2 P], FP32; reward and slope may be null.  Sums are binary64. */
+/* loss [P], reward [2 P] and slope [2 P], FP32; reward and slope may be null.  Sums keep some 48 bits. */
 FORGE_API forge_status forge_preference_loss(const float *nll, const float *ref, const uint8_t *mask,
                                              const int32_t *offsets, float *loss, float *reward, float *slope,
                                              void *workspace, int64_t workspace_bytes,

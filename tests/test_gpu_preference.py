@@ -79,7 +79,7 @@ def test_loss_and_gradient(case, kind, smoothing, margin, mean, masked):
     loss, reward, slope = (torch.full((n,), 9.0, device="cuda") for n in (P, 2 * P, 2 * P))
     fg.preference_loss(nll, ref, offsets, loss, reward, slope, mask=mask, beta=beta, kind=kind, smoothing=smoothing,
                        margin=margin, mean=mean)
-    # the sums are binary64: their own rounding is far below binary32's, into which beta, the margin, z, and each
+    # the sums keep some 48 bits: their own rounding is far below that of binary32, into which the margin, z and each
     # result are rounded.  beta here is a power of two; the margin is taken as binary32 holds it
     score, per = _scores(nll, ref, sizes, lead, mask, mean)
     m = torch.tensor(margin, dtype=torch.float32).double().item()
