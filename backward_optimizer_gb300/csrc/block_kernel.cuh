@@ -67,7 +67,8 @@ enum BlockAct : int { kActSilu = 0, kActGeluTanh = 1, kActRelu = 2 };
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Whether an epilogue's results go to memory through shared memory, on pairs (WarpOut).
-constexpr bool staged(int epi) { return epi == kBlockGatedFwd || epi == kBlockLossGrad; }
+constexpr int kExpertGrad = 5;  // expert_kernel.cuh
+constexpr bool staged(int epi) { return epi == kBlockGatedFwd || epi == kBlockLossGrad || epi == kExpertGrad; }
 
 template <int BN, int CG, int EPI>
 struct BlockCfg {

@@ -25,6 +25,7 @@ using forge::kBlockStore;
 using forge::kExpertGrad;
 
 constexpr int kMaxExperts = 1024;  // the plan gives each a thread of its one block
+constexpr int kMaxCuts = 2;        // row products of a call
 constexpr int kMaxRuns = 5;        // operands whose reduction is a run of rows: dG, dU, dY, X, H
 
 int slices(int64_t k) { return static_cast<int>(ceil_div(k, forge::kBK)); }
@@ -45,6 +46,11 @@ struct PlanArgs {
     int4* tiles;
     CUtensorMap* runs;  // [n_runs][experts]
     int n_runs;
+    int4* cuts;     // of each row product
+    int n_cuts;
+    forge::ExpertCut cut[kMaxCuts];
+    uint32_t* counts;
+    int n_counts;
     RunOperand run[kMaxRuns];
 };
 
@@ -107,6 +113,14 @@ __global__ void __launch_bounds__(1024) expert_plan_kernel(const __grid_constant
         const int row = begin[lo] + (i - first[lo]) * a.tile_rows;
         a.tiles[i] = make_int4(lo, row, min(row + a.tile_rows, end[lo]), 0);
     }
+    if (e < a.n_cuts) {
+        const forge::ExpertCut& c = a.cut[e];
+        const int all = total * c.tiles_n, rest = all % c.width;
+        const int parts = forge::expert_parts(c, rest);
+        const int from = parts > 1 ? all - rest : all;
+        a.cuts[e] = make_int4(from, parts, from + (all - from) * parts, 0);
+    }
+    for (int i = e; i < a.n_counts; i += 1024) a.counts[i] = 0u;
     for (int i = e; i < a.n_runs * a.experts; i += 1024) {
         const int o = i / a.experts, x = i - o * a.experts;
         const uint4* src = reinterpret_cast<const uint4*>(&a.run[o].map);
@@ -134,7 +148,10 @@ struct Call {
     Tiling tiling;
     int64_t tiles;  // row tiles at most
     int n_runs;
-    int64_t clean, n_tiles, list, runs;  // places in the workspace
+    int64_t clean, n_tiles, list, runs, cuts, counts, parts;  // places in the workspace
+    int n_counts;
+    forge::ExpertCut cut[kMaxCuts];  // of the call's row products, in the order of their launches
+    int n_cuts;
     char* ws;
     cudaStream_t stream;
     const int* offsets;
@@ -148,18 +165,40 @@ Tiling choose_rows(int64_t rows, int64_t experts) {
     return each > 24 ? Tiling{128, 128} : Tiling{128, 32};
 }
 
-Call make_call(const Machine& mc, int64_t rows, int64_t experts, int n_runs, Arena& a) {
+// A row product of a call: its columns, those of a tile, and its reduction.
+struct RowSize {
+    int64_t cols, k;
+    bool gated, two;  // two: two operand pairs
+};
+
+Call make_call(const Machine& mc, int64_t rows, int64_t experts, int n_runs, std::initializer_list<RowSize> products, Arena& a) {
     Call c{};
     c.mc = mc;
     c.rows = rows;
     c.experts = static_cast<int>(experts);
     c.tiling = choose_rows(rows, experts);
-    c.tiles = rows / c.tiling.tile_rows + std::min(rows, experts);
+    const Tiling& t = c.tiling;
+    c.tiles = rows / t.tile_rows + std::min(rows, experts);
     c.n_runs = n_runs;
     c.clean = a.take((experts + 1) * 4);
     c.n_tiles = a.take(4);
     c.list = a.take(c.tiles * 16);
     c.runs = a.take(n_runs * experts * static_cast<int64_t>(sizeof(CUtensorMap)));
+    c.cuts = a.take(kMaxCuts * 16);
+    const bool pair = t.bn == 256;
+    const int width = pair ? mc.pairs : mc.dev.num_sms;
+    bool cut = false;
+    for (const RowSize& p : products) {
+        const int kb = slices(p.k) * (p.two ? 2 : 1);
+        forge::ExpertCut& x = c.cut[c.n_cuts++];
+        // joins as kTiles has them (block_api.cu)
+        x = forge::ExpertCut{static_cast<int>(ceil_div(p.cols, p.gated ? t.bn / 2 : t.bn)), kb, width, pair ? 8 : t.bn == 128 ? 6 : 10,
+                             pair ? 12 : t.bn == 128 ? 5 : 2};
+        cut = cut || forge::expert_parts(x, 1) > 1;
+    }
+    c.n_counts = cut ? width * (pair ? 2 : 1) * 8 : 0;
+    c.counts = a.take(c.n_counts * 4ll);
+    c.parts = a.take(cut ? static_cast<int64_t>(width) * t.tile_rows * t.bn * 4 : 0);
     return c;
 }
 
@@ -226,6 +265,8 @@ void begin_group(ExpertGroup<EPI>& g, const Call& c, int64_t kb_max) {
     g.n = 1;
     g.experts = c.experts;
     g.a_rows = EPI == kExpertGrad ? 128 : c.tiling.tile_rows;
+    g.parts = reinterpret_cast<float*>(c.ws + c.parts);
+    g.counts = reinterpret_cast<uint32_t*>(c.ws + c.counts);
     g.withhold_first_stage = host::take_withhold();
     g.n_tiles = reinterpret_cast<const int*>(c.ws + c.n_tiles);
     g.tiles = reinterpret_cast<const int4*>(c.ws + c.list);
@@ -252,11 +293,18 @@ forge_status launch_plan(const Call& c, PlanArgs& a) {
     a.n_tiles = reinterpret_cast<int*>(c.ws + c.n_tiles);
     a.tiles = reinterpret_cast<int4*>(c.ws + c.list);
     a.runs = reinterpret_cast<CUtensorMap*>(c.ws + c.runs);
+    a.cuts = reinterpret_cast<int4*>(c.ws + c.cuts);
+    a.n_cuts = c.n_cuts;
+    for (int i = 0; i < c.n_cuts; ++i) a.cut[i] = c.cut[i];
+    a.counts = reinterpret_cast<uint32_t*>(c.ws + c.counts);
+    a.n_counts = c.n_counts;
     return cuda_status(host::launch_early(expert_plan_kernel, dim3(1), dim3(1024), 0, c.stream, a));
 }
 
+// cut: which of the call's row products this is
 template <int EPI>
-void set_rows(ExpertGroup<EPI>& g, const Call& c, int64_t cols, int64_t k0, int64_t k1) {
+void set_rows(ExpertGroup<EPI>& g, const Call& c, int cut, int64_t cols, int64_t k0, int64_t k1) {
+    g.cut = reinterpret_cast<const int4*>(c.ws + c.cuts) + cut;
     ExpertProblem& b = g.prob[0];
     b.cols = static_cast<int>(cols);
     b.ld = cols;
@@ -277,10 +325,13 @@ struct RowProduct {
     void* out;
 };
 
-forge_status run_rows(const Call& c, const RowProduct& p) {
+// Units of a row product at most.
+int64_t most_units(const Call& c, int cut) { return c.tiles * c.cut[cut].tiles_n + (c.n_counts > 0 ? c.cut[cut].width : 0); }
+
+forge_status run_rows(const Call& c, int cut, const RowProduct& p) {
     ExpertGroup<kBlockStore> g;
     begin_group(g, c, 2 * slices(p.k));
-    set_rows(g, c, p.cols, p.k, p.a[1] != nullptr ? p.k : 0);
+    set_rows(g, c, cut, p.cols, p.k, p.a[1] != nullptr ? p.k : 0);
     g.prob[0].b_mn = p.mn;
     g.prob[0].b_flat = p.mn && p.cols % 64 != 0;
     for (int i = 0; i < 2 && p.a[i] != nullptr; ++i) {
@@ -289,7 +340,7 @@ forge_status run_rows(const Call& c, const RowProduct& p) {
                              b_extent(c.tiling, false)));
     }
     FORGE_TRY(set_result(g, c.tiling, 0, p.out, 1, c.rows, p.cols));
-    return launch(g, c, c.tiling.bn, c.tiles * g.prob[0].tiles_n);
+    return launch(g, c, c.tiling.bn, most_units(c, cut));
 }
 
 // dW of up to three products: a and b, numbers of their run operands; each dW_e [d_out, d_in]
@@ -356,7 +407,8 @@ struct GatedSpace {
 GatedSpace layout_gated(const Machine& mc, const forge_expert_gated_shape& s, bool backward) {
     GatedSpace l{};
     Arena a;
-    l.c = make_call(mc, s.rows, s.experts, backward ? kMaxRuns : 0, a);
+    if (backward) l.c = make_call(mc, s.rows, s.experts, kMaxRuns, {{s.d_ff, s.d_model, false, false}, {s.d_model, s.d_ff, false, true}}, a);
+    else l.c = make_call(mc, s.rows, s.experts, 0, {{s.d_ff, s.d_model, true, false}, {s.d_model, s.d_ff, false, false}}, a);
     const int64_t bytes = s.rows * s.d_ff * 2;
     if (backward) {
         l.dg = a.take(bytes);
@@ -367,9 +419,10 @@ GatedSpace layout_gated(const Machine& mc, const forge_expert_gated_shape& s, bo
     return l;
 }
 
-int64_t linear_space(const Machine& mc, const forge_expert_linear_shape& s, Call* c) {
+int64_t linear_space(const Machine& mc, const forge_expert_linear_shape& s, bool backward, Call* c) {
     Arena a;
-    *c = make_call(mc, s.rows, s.experts, 2, a);
+    if (backward) *c = make_call(mc, s.rows, s.experts, 2, {{s.d_in, s.d_out, false, false}}, a);
+    else *c = make_call(mc, s.rows, s.experts, 0, {{s.d_out, s.d_in, false, false}}, a);
     return a.used;
 }
 
@@ -383,13 +436,13 @@ forge_status zero(std::initializer_list<void*> ps, int64_t bytes, cudaStream_t s
 
 extern "C" {
 
-int64_t forge_expert_linear_workspace(const forge_expert_linear_shape* shape) {
+int64_t forge_expert_linear_workspace(const forge_expert_linear_shape* shape, int32_t backward) {
     if (check_linear(shape) != FORGE_OK) return -1;
     Machine mc;
     if (shape->rows == 0) return 0;
     if (machine(&mc) != FORGE_OK) return -1;
     Call c;
-    return linear_space(mc, *shape, &c);
+    return linear_space(mc, *shape, backward != 0, &c);
 }
 
 forge_status forge_expert_linear(const void* X, const void* W, const int32_t* offsets, void* Y, void* workspace,
@@ -403,13 +456,13 @@ forge_status forge_expert_linear(const void* X, const void* W, const int32_t* of
     Call c;
     Machine mc;
     FORGE_TRY(machine(&mc));
-    FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, &c)));
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, false, &c)));
     c.ws = static_cast<char*>(workspace);
     c.stream = stream;
     c.offsets = offsets;
     PlanArgs plan{};
     FORGE_TRY(launch_plan(c, plan));
-    return run_rows(c, RowProduct{{X, nullptr}, {W, nullptr}, s.d_in, s.d_out, false, Y});
+    return run_rows(c, 0, RowProduct{{X, nullptr}, {W, nullptr}, s.d_in, s.d_out, false, Y});
 }
 
 forge_status forge_expert_linear_backward(const void* dY, const void* X, const void* W, const int32_t* offsets, void* dX,
@@ -425,7 +478,7 @@ forge_status forge_expert_linear_backward(const void* dY, const void* X, const v
     Call c;
     Machine mc;
     FORGE_TRY(machine(&mc));
-    FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, &c)));
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, true, &c)));
     c.ws = static_cast<char*>(workspace);
     c.stream = stream;
     c.offsets = offsets;
@@ -438,7 +491,7 @@ forge_status forge_expert_linear_backward(const void* dY, const void* X, const v
         FORGE_TRY(run_operand(&plan.run[1], c, X, s.d_in, b_extent(t, false)));
     }
     FORGE_TRY(launch_plan(c, plan));
-    if (dX != nullptr) FORGE_TRY(run_rows(c, RowProduct{{dY, nullptr}, {W, nullptr}, s.d_out, s.d_in, true, dX}));
+    if (dX != nullptr) FORGE_TRY(run_rows(c, 0, RowProduct{{dY, nullptr}, {W, nullptr}, s.d_out, s.d_in, true, dX}));
     return dW != nullptr ? run_grads(c, t, &p, 1) : FORGE_OK;
 }
 
@@ -472,7 +525,7 @@ forge_status forge_expert_gated_mlp(const void* X, const void* Wg, const void* W
     FORGE_TRY(launch_plan(c, plan));
     ExpertGroup<kBlockGatedFwd> g;
     begin_group(g, c, slices(s.d_model));
-    set_rows(g, c, s.d_ff, s.d_model, 0);
+    set_rows(g, c, 0, s.d_ff, s.d_model, 0);
     g.act = s.act;
     g.keep = G != nullptr;
     if (g.keep) {
@@ -484,8 +537,8 @@ forge_status forge_expert_gated_mlp(const void* X, const void* Wg, const void* W
     const int extent = b_extent(c.tiling, true);
     FORGE_TRY(weight_map(&g.maps[1], Wg, s.experts, s.d_ff, s.d_model, false, extent));
     FORGE_TRY(weight_map(&g.maps[3], Wu, s.experts, s.d_ff, s.d_model, false, extent));
-    FORGE_TRY(launch(g, c, c.tiling.bn, c.tiles * g.prob[0].tiles_n));
-    return run_rows(c, RowProduct{{c.ws + l.h, nullptr}, {Wd, nullptr}, s.d_ff, s.d_model, false, Y});
+    FORGE_TRY(launch(g, c, c.tiling.bn, most_units(c, 0)));
+    return run_rows(c, 1, RowProduct{{c.ws + l.h, nullptr}, {Wd, nullptr}, s.d_ff, s.d_model, false, Y});
 }
 
 forge_status forge_expert_gated_mlp_backward(const void* dY, const void* X, const void* G, const void* U, const void* Wg,
@@ -519,7 +572,7 @@ forge_status forge_expert_gated_mlp_backward(const void* dY, const void* X, cons
     FORGE_TRY(launch_plan(c, plan));
     ExpertGroup<kBlockGatedBwd> g;
     begin_group(g, c, slices(s.d_model));
-    set_rows(g, c, s.d_ff, s.d_model, 0);
+    set_rows(g, c, 0, s.d_ff, s.d_model, 0);
     g.act = s.act;
     g.g_in = static_cast<const uint16_t*>(G);
     g.u_in = static_cast<const uint16_t*>(U);
@@ -528,9 +581,9 @@ forge_status forge_expert_gated_mlp_backward(const void* dY, const void* X, cons
     g.prob[0].b_flat = s.d_ff % 64 != 0;
     FORGE_TRY(rows_map(&g.maps[0], c, dY, s.d_model));
     FORGE_TRY(weight_map(&g.maps[1], Wd, s.experts, s.d_model, s.d_ff, true, b_extent(c.tiling, false)));
-    FORGE_TRY(launch(g, c, c.tiling.bn, c.tiles * g.prob[0].tiles_n));
+    FORGE_TRY(launch(g, c, c.tiling.bn, most_units(c, 0)));
     if (dX != nullptr)
-        FORGE_TRY(run_rows(c, RowProduct{{c.ws + l.dg, c.ws + l.du}, {Wg, Wu}, s.d_ff, s.d_model, true, dX}));
+        FORGE_TRY(run_rows(c, 1, RowProduct{{c.ws + l.dg, c.ws + l.du}, {Wg, Wu}, s.d_ff, s.d_model, true, dX}));
     return run_grads(c, t, p, 3);
 }
 

@@ -15,14 +15,17 @@
 // nor its infinities or NaN enter a sum.  Row products need no such map: an accumulator row depends on its own
 // row of A alone, and rows past the run are not stored.  An expert without rows takes one slice of zero fill and
 // stores a zero gradient.
+//
+// Few row tiles.  The plan knows how many there are; where the last wave of tiles leaves SMs idle it cuts them
+// along the reduction (expert_cut), and the parts are joined as in forge_block_kernel: no CTA waits for another, the
+// last to arrive adds the parts in their order.
 #pragma once
 
 #include "block_kernel.cuh"
 
 namespace forge {
 
-constexpr int kExpertGrad = 5;  // beside BlockEpi's kBlockStore, kBlockGatedFwd and kBlockGatedBwd, whose A are rows by expert
-
+// kExpertGrad beside BlockEpi's kBlockStore, kBlockGatedFwd and kBlockGatedBwd, whose A are rows by expert
 __host__ __device__ constexpr int expert_products(int epi) { return epi == kExpertGrad ? 3 : 1; }
 
 struct ExpertProblem {
@@ -46,12 +49,15 @@ struct ExpertGroup {
     int stream_b;         // each weight is read by one row tile or few: leave it out of the L2
     int act, keep;
     int withhold_first_stage;
+    const int4* cut;      // row products: tiles before .x are whole, the others cut into .y parts; .z units
     const int* n_tiles;   // row tiles
     const int4* tiles;    // each: expert, first row, one past its last row
     const int* offsets;   // [experts + 1], as the plan left them: in order and within the rows
     const CUtensorMap* runs;  // [map][expert]
     const uint16_t* g_in;
     const uint16_t* u_in;
+    float* parts;         // of cut tiles
+    uint32_t* counts;     // their arrivals: zero before the launch and after it
     int* status;
     uint64_t wait_limit_ns, acc_wait_limit_ns;
     uint16_t* to[3];      // results: kBlockStore's, kExpertGrad's of each product; G, U, H; dG, dU, H
@@ -62,12 +68,34 @@ struct ExpertGroup {
 
 struct ExpertUnit {
     int prob, expert, nb, row0, end;  // row0: the tile's first row of the result; end: one past its last
-    int slices;                       // kExpertGrad; rows by expert: of both operand pairs
+    int k_first, k_end;               // slices (rows by expert: of both operand pairs, one after the other)
+    int split, part;                  // which cut tile, or -1
 };
 
+// How the last wave of a row product is cut: `tiles` tiles of kb slices on `width` pairs or CTAs.  A part costs its
+// slices and its share of the join, in slices (the host's figures for the tile: TileCost).  Parts fit one wave.
+struct ExpertCut {
+    int tiles_n, kb, width, join, per_part;
+};
+constexpr int kExpertMinSlices = 8, kExpertMaxParts = 16;
+
+FORGE_HD int expert_parts(const ExpertCut& c, int rest) {
+    int best = 1, time = c.kb;
+    for (int p = 2; p <= kExpertMaxParts && c.kb >= kExpertMinSlices * p && rest * p <= c.width; ++p) {
+        const int t = (c.kb + p - 1) / p + c.join + c.per_part * p;
+        if (t < time) {
+            best = p;
+            time = t;
+        }
+    }
+    return best;
+}
+
 template <int CG, int EPI>
-__device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int u, int n_tiles) {
+__device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int u, int n_tiles, int4 cut) {
     ExpertUnit r;
+    r.split = -1;
+    r.part = r.k_first = 0;
     int mb;
     if constexpr (EPI == kExpertGrad) {
         r.prob = 0;
@@ -79,16 +107,25 @@ __device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int
         r.row0 = mb * kBM * CG;
         r.end = b.rows;
         const int run = __ldcg(g.offsets + r.expert + 1) - __ldcg(g.offsets + r.expert);
-        r.slices = run > 0 ? (run + kBK - 1) / kBK : 0;
+        r.k_end = run > 0 ? (run + kBK - 1) / kBK : 0;
     } else {
         const ExpertProblem& b = g.prob[0];
         r.prob = 0;
-        tile_coords(u, TileOrder{n_tiles, b.tiles_n, 8, 0}, mb, r.nb);
-        const int4 t = __ldcg(g.tiles + mb);
-        r.expert = t.x;
-        r.row0 = t.y;
-        r.end = t.z;
-        r.slices = b.kb[0] + b.kb[1];
+        r.k_end = b.kb[0] + b.kb[1];
+        int t = u;
+        if (u >= cut.x) {
+            const int s = u - cut.x, kb = r.k_end;
+            r.split = s / cut.y;
+            r.part = s - r.split * cut.y;
+            r.k_first = static_cast<int>(static_cast<int64_t>(kb) * r.part / cut.y);
+            r.k_end = static_cast<int>(static_cast<int64_t>(kb) * (r.part + 1) / cut.y);
+            t = cut.x + r.split;
+        }
+        tile_coords(t, TileOrder{n_tiles, b.tiles_n, 8, 0}, mb, r.nb);
+        const int4 at = __ldcg(g.tiles + mb);
+        r.expert = at.x;
+        r.row0 = at.y;
+        r.end = at.z;
     }
     return r;
 }
@@ -221,7 +258,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
 
     stream_wait();
     const int n_tiles = kGrad ? 0 : __ldcg(grp.n_tiles);
-    const int n_units = kGrad ? grp.n_units : n_tiles * grp.prob[0].tiles_n;
+    const int4 cut = kGrad ? make_int4(0, 0, 0, 0) : __ldcg(grp.cut);
+    const int n_units = kGrad ? grp.n_units : cut.z;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -251,7 +289,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             };
             int seen_prob = -1, seen_expert = -1;
             for (int u = pair; ok && u < n_units; u += pairs) {
-                const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles);
+                const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles, cut);
                 const ExpertProblem& b = grp.prob[w.prob];
                 const int row_a = w.row0 + static_cast<int>(rank) * kBM;
                 const int col_b = kGated ? w.nb * kColsPerTile : w.nb * BN + static_cast<int>(rank) * C::kBLoad;
@@ -265,11 +303,11 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                         seen_expert = w.expert;
                     }
                     // a run of no rows: one slice past the one row that its maps have
-                    int k0 = w.slices == 0 ? kBK : 0;
+                    int k0 = w.k_end == 0 ? kBK : 0;
                     const bool a_flat = b.a_flat != 0, b_flat = b.b_flat != 0;
                     const int a0 = a_flat ? row_a : 0, a2 = a_flat ? 0 : row_a / 64;
                     const int b0 = b_flat ? col_b : 0, b2 = b_flat ? 0 : col_b / 64;
-                    for (int n = w.slices == 0 ? 1 : w.slices; ok && n > 0; --n, k0 += kBK)
+                    for (int n = w.k_end == 0 ? 1 : w.k_end; ok && n > 0; --n, k0 += kBK)
                         ok = slice([&](uint32_t bar, uint32_t a_dst, uint32_t b_dst) {
                             tma_load_3d_cg<CG>(a_dst, ma, bar, a0, k0, a2, keep);
                             tma_load_3d_cg<CG>(b_dst, mb, bar, b0, k0, b2, keep);
@@ -281,17 +319,21 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                     const bool b_flat = bmn && b.b_flat != 0;
 #pragma unroll 1
                     for (int seg = 0; seg < (EPI == kBlockStore ? 2 : 1) && ok; ++seg) {
+                        // the unit's slices of this operand pair
+                        const int base = seg == 0 ? 0 : b.kb[0];
+                        const int from = w.k_first > base ? w.k_first - base : 0;
+                        const int to = (w.k_end < base + b.kb[seg] ? w.k_end : base + b.kb[seg]) - base;
                         const CUtensorMap* ma = &grp.maps[2 * seg];
                         // gated forward: the even CTA (or the first half of the columns) holds the gate's rows, the
                         // other the up projection's, of the same d_ff columns
                         const CUtensorMap* mb = kGated && CG == 2 && rank == 1 ? &grp.maps[3] : ma + 1;
                         const CUtensorMap* mu = &grp.maps[3];
-                        int k0 = 0;
-                        int b0 = bmn ? (b_flat ? col_b : 0) : 0, b1 = bmn ? 0 : col_b;
+                        int k0 = from * kBK;
+                        int b0 = bmn ? (b_flat ? col_b : 0) : k0, b1 = bmn ? k0 : col_b;
                         const int b2 = bmn && !b_flat ? col_b / 64 : 0;
                         const int db0 = bmn ? 0 : kBK, db1 = bmn ? kBK : 0;
 #pragma unroll 1
-                        for (int n = b.kb[seg]; ok && n > 0; --n, k0 += kBK, b0 += db0, b1 += db1)
+                        for (int n = to - from; ok && n > 0; --n, k0 += kBK, b0 += db0, b1 += db1)
                             ok = slice([&](uint32_t bar, uint32_t a_dst, uint32_t b_dst) {
                                 tma_load_3d_cg<CG>(a_dst, ma, bar, k0, row_a, 0, keep);
                                 tma_load_4d_cg<CG>(b_dst, mb, bar, b0, b1, b2, w.expert, pol_b);
@@ -316,7 +358,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, issued_any = false;
             for (int u = pair; ok && u < n_units; u += pairs) {
-                const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles);
+                const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles, cut);
                 const bool amn = kGrad;
                 const bool bmn = kGrad || EPI == kBlockGatedBwd || (EPI == kBlockStore && grp.prob[0].b_mn != 0);
                 const uint32_t idesc = idesc_bf16_f32(kBM * CG, BN, amn, bmn);
@@ -326,7 +368,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                 if (!wait_bounded(&acc_empty[acc], acc_phase ^ 1u, ab)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-                const int slices = w.slices == 0 ? 1 : w.slices;
+                const int slices = w.k_end == w.k_first ? 1 : w.k_end - w.k_first;
 #pragma unroll 1
                 for (int kb = 0; kb < slices; ++kb) {
                     if (!wait_bounded(&full[stage], phase, ab)) { ok = false; break; }
@@ -360,7 +402,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
         ExpertOut<(C::kStaging > 0)> out{grp.outs, {grp.to[0], grp.to[1], grp.to[2]}, 0, 0, 0, kGrad,
                                          smem_addr(staging) + static_cast<uint32_t>(e) * 4096u, 0};
         for (int u = pair; u < n_units; u += pairs) {
-            const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles);
+            const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles, cut);
             const ExpertProblem& p = grp.prob[w.prob];
             const int row = w.row0 + static_cast<int>(rank) * kBM + quarter * 32 + lane;
             BlockProblem b;
@@ -388,15 +430,57 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const AccTmem tm{tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN)};
-            if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, tm, row, w.nb, half, out);
-            else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, tm, row, w.nb, half, out);
-            else epi_store<BN>(b, tm, row, w.nb, half, out);
+            auto epilogue = [&](const auto& acc_from) {
+                if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, acc_from, row, w.nb, half, out);
+                else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, acc_from, row, w.nb, half, out);
+                else epi_store<BN>(b, acc_from, row, w.nb, half, out);
+            };
+            // [cut tile][part][CTA][lane quarter][column][lane]; quarters past the tile's rows are not there
+            const size_t quarters = CG == 1 ? a_rows / 32 : 4;
+            const size_t step = static_cast<size_t>(CG) * quarters * BN * 32;
+            const size_t own = (static_cast<size_t>(rank) * quarters + quarter) * BN * 32 + lane;
+            const bool whole = kGrad || w.split < 0;
+            if (whole) epilogue(tm);
+            else if (warp_row0(row) < b.rows) {
+                float* to = grp.parts + (static_cast<size_t>(w.split) * cut.y + w.part) * step + own;
+                // the columns whose epilogue this warp runs: gate and up columns come from both halves
+                constexpr int kRuns = kGated ? 2 : 1, kRun = BN / 2 / kRuns, kStep = kRun < 32 ? kRun : 32;
+#pragma unroll 1
+                for (int r = 0; r < kRuns; ++r) {
+#pragma unroll 1
+                    for (int c = 0; c < kRun; c += kStep) {
+                        const int at = r * (BN / 2) + half * kRun + c;
+                        uint32_t g[kStep];
+                        tm.load(at, g);
+                        if (row < b.rows) {
+#pragma unroll
+                            for (int j = 0; j < kStep; ++j)
+                                __stcg(to + static_cast<size_t>(at + j) * 32, __uint_as_float(g[j]));
+                        }
+                    }
+                }
+            }
             // the accumulator's reads are done: it may be overwritten
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_relaxed(map_to_rank(smem_addr(&acc_empty[acc]), 0));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
+            if (!whole) {
+                // every lane's values are visible device-wide before the warp counts itself in; the last one to
+                // arrive sees the other parts' values
+                __threadfence();
+                __syncwarp();
+                uint32_t before = 0;
+                uint32_t* count = grp.counts + (w.split * CG + static_cast<int>(rank)) * C::kEpiWarps + e;
+                if (lane == 0) before = atomicAdd(count, 1u);
+                before = __shfl_sync(0xFFFFFFFFu, before, 0);
+                if (before + 1 == static_cast<uint32_t>(cut.y)) {
+                    __threadfence();
+                    if (lane == 0) *count = 0u;
+                    epilogue(AccParts{grp.parts + static_cast<size_t>(w.split) * cut.y * step + own, step, cut.y, row < b.rows});
+                }
+            }
         }
         out.end();
     }

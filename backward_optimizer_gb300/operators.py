@@ -88,7 +88,7 @@ def declare(L: ctypes.CDLL) -> None:
         "forge_layer_norm_backward_workspace": [norm],
         "forge_gated_mlp_workspace": [gated, i32],
         "forge_linear_cross_entropy_workspace": [loss, i32],
-        "forge_expert_linear_workspace": [elinear],
+        "forge_expert_linear_workspace": [elinear, i32],
         "forge_preference_loss_workspace": [pref],
         "forge_expert_gated_mlp_workspace": [egated, i32],
     }.items():
@@ -388,7 +388,7 @@ def expert_linear(X, W, offsets, Y, stream=None) -> None:
     x, w = _take(X, _BF16, (R, D), dev, "X"), _take(W, _BF16, (E, F, D), dev, "W")
     o, y = _take(offsets, torch.int32, (E + 1,), dev, "offsets"), _take(Y, _BF16, (R, F), dev, "Y")
     raw = _raw_stream(stream, dev)
-    ws, n, _hold = _workspace(shape, "forge_expert_linear_workspace", dev, stream, raw)
+    ws, n, _hold = _workspace(shape, "forge_expert_linear_workspace", dev, stream, raw, 0)
     _fg._check(_fg.lib().forge_expert_linear(x, w, o, y, ws, n, shape.arg, raw), "forge_expert_linear")
 
 
@@ -401,7 +401,7 @@ def expert_linear_backward(dY, X, W, offsets, dX, dW, stream=None) -> None:
         (dY, _BF16, (R, F), "dY"), (X, _BF16, (R, D), "X"), (W, _BF16, (E, F, D), "W"),
         (offsets, torch.int32, (E + 1,), "offsets"), (dX, _BF16, (R, D), "dX"), (dW, _BF16, (E, F, D), "dW"))]
     raw = _raw_stream(stream, dev)
-    ws, n, _hold = _workspace(shape, "forge_expert_linear_workspace", dev, stream, raw)
+    ws, n, _hold = _workspace(shape, "forge_expert_linear_workspace", dev, stream, raw, 1)
     _fg._check(_fg.lib().forge_expert_linear_backward(*args, ws, n, shape.arg, raw), "forge_expert_linear_backward")
 
 

@@ -441,8 +441,8 @@ FORGE_API forge_status forge_expert_linear_backward(const void *dY, const void *
                                                     void *dX, void *dW, void *workspace, int64_t workspace_bytes,
                                                     const forge_expert_linear_shape *shape, struct CUstream_st *stream);
 
-/* Of every expert_linear call. */
-FORGE_API int64_t forge_expert_linear_workspace(const forge_expert_linear_shape *shape);
+/* backward: 0 for forge_expert_linear, 1 for the backward call. */
+FORGE_API int64_t forge_expert_linear_workspace(const forge_expert_linear_shape *shape, int32_t backward);
 
 typedef struct forge_expert_gated_shape {
     int64_t rows;     /* of X, >= 0 */

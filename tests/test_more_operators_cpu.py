@@ -31,7 +31,7 @@ def _gated(**kw):
 def test_linear_shapes_refused(L, kw):
     assert L.forge_expert_linear(A, A, A, A, A, BIG, _linear(**kw), None) == 1
     assert L.forge_expert_linear_backward(A, A, A, A, A, A, A, BIG, _linear(**kw), None) == 1
-    assert L.forge_expert_linear_workspace(_linear(**kw)) == -1
+    assert L.forge_expert_linear_workspace(_linear(**kw), 0) == -1
 
 
 @pytest.mark.parametrize("kw", [dict(rows=-1), dict(experts=0), dict(experts=1025), dict(d_model=0), dict(d_model=60),
