@@ -33,9 +33,10 @@ int slices(int64_t k) { return static_cast<int>(ceil_div(k, forge::kBK)); }
 // ---------------------------------------------------------------- the plan, made on the device
 
 struct RunOperand {
-    CUtensorMap map;  // of all rows
+    CUtensorMap map;  // of 64 columns of one row: tensormap_set widens it
     const char* base;
     int64_t pitch;    // bytes from row to row
+    uint32_t dim0, dim2;
 };
 
 struct PlanArgs {
@@ -129,7 +130,8 @@ __global__ void __launch_bounds__(1024) expert_plan_kernel(const __grid_constant
         for (int j = 0; j < 8; ++j) dst[j] = src[j];
         // a run of no rows: one row that is never read (its slice lies past it)
         const int n = end[x] - begin[x];
-        forge::tensormap_set(a.runs + i, a.run[o].base + (n > 0 ? begin[x] * a.run[o].pitch : 0), n > 0 ? n : 1);
+        forge::tensormap_set(a.runs + i, a.run[o].base + (n > 0 ? begin[x] * a.run[o].pitch : 0), a.run[o].dim0, n > 0 ? n : 1,
+                             a.run[o].dim2);
     }
 }
 
@@ -236,15 +238,17 @@ forge_status weight_map(CUtensorMap* map, const void* base, int64_t experts, int
     });
 }
 
-// An operand of the weights' gradients, [rows, cols] and MN-major: the map of all rows, which the plan cuts.
-forge_status run_operand(RunOperand* o, const Call& c, const void* base, int64_t cols, int extent) {
+// An operand of the weights' gradients, [rows, cols] and MN-major: its map, which the plan makes one of each run.
+forge_status run_operand(RunOperand* o, const void* base, int64_t cols, int extent) {
+    const bool blocks = cols % 64 == 0;
     o->base = static_cast<const char*>(base);
     o->pitch = cols * 2;
-    return kept_map(&o->map, MapKey{base, cols, c.rows, cols, 1, extent}, [&] {
-        const uint64_t k = static_cast<uint64_t>(cols), r = static_cast<uint64_t>(c.rows);
-        if (cols % 64 == 0)
-            return host::encode_map(&o->map, base, {64, r, k / 64}, {2 * k, 128}, {64, 64, static_cast<uint32_t>(extent / 64)});
-        return host::encode_map(&o->map, base, {k, r, 1}, {2 * k, 2 * k}, {64, 64, 1});
+    o->dim0 = blocks ? 64 : static_cast<uint32_t>(cols);
+    o->dim2 = blocks ? static_cast<uint32_t>(cols / 64) : 1;
+    return kept_map(&o->map, MapKey{base, cols, 1, cols, 2, extent}, [&] {
+        const uint64_t pitch = static_cast<uint64_t>(cols) * 2;
+        return host::encode_map(&o->map, base, {64, 1, 1}, {pitch, blocks ? 128 : pitch},
+                                {64, 64, blocks ? static_cast<uint32_t>(extent / 64) : 1});
     });
 }
 
@@ -356,6 +360,8 @@ Tiling grad_tiling(const Machine& mc, int64_t experts, const GradProduct* p, int
     return pairs >= mc.pairs ? Tiling{256, 256} : Tiling{128, 128};
 }
 
+int grad_chunk(const Call& c) { return c.rows < 256ll * c.experts ? 4 : 1; }
+
 forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int n) {
     ExpertGroup<kExpertGrad> g;
     begin_group(g, c, slices(c.rows));
@@ -377,6 +383,7 @@ forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int
         FORGE_TRY(set_result(g, t, i, p[i].out, c.experts, p[i].d_out, p[i].d_in));
     }
     g.n_units = static_cast<int>(u);
+    g.chunk = grad_chunk(c);
     return launch(g, c, t.bn, u);
 }
 
@@ -487,8 +494,8 @@ forge_status forge_expert_linear_backward(const void* dY, const void* X, const v
     PlanArgs plan{};
     if (dW != nullptr) {
         plan.n_runs = 2;
-        FORGE_TRY(run_operand(&plan.run[0], c, dY, s.d_out, 128));
-        FORGE_TRY(run_operand(&plan.run[1], c, X, s.d_in, b_extent(t, false)));
+        FORGE_TRY(run_operand(&plan.run[0], dY, s.d_out, 128));
+        FORGE_TRY(run_operand(&plan.run[1], X, s.d_in, b_extent(t, false)));
     }
     FORGE_TRY(launch_plan(c, plan));
     if (dX != nullptr) FORGE_TRY(run_rows(c, 0, RowProduct{{dY, nullptr}, {W, nullptr}, s.d_out, s.d_in, true, dX}));
@@ -564,11 +571,11 @@ forge_status forge_expert_gated_mlp_backward(const void* dY, const void* X, cons
     const Tiling t = grad_tiling(mc, s.experts, p, 3);
     PlanArgs plan{};
     plan.n_runs = kMaxRuns;
-    FORGE_TRY(run_operand(&plan.run[0], c, c.ws + l.dg, s.d_ff, 128));
-    FORGE_TRY(run_operand(&plan.run[1], c, c.ws + l.du, s.d_ff, 128));
-    FORGE_TRY(run_operand(&plan.run[2], c, dY, s.d_model, 128));
-    FORGE_TRY(run_operand(&plan.run[3], c, X, s.d_model, b_extent(t, false)));
-    FORGE_TRY(run_operand(&plan.run[4], c, c.ws + l.h, s.d_ff, b_extent(t, false)));
+    FORGE_TRY(run_operand(&plan.run[0], c.ws + l.dg, s.d_ff, 128));
+    FORGE_TRY(run_operand(&plan.run[1], c.ws + l.du, s.d_ff, 128));
+    FORGE_TRY(run_operand(&plan.run[2], dY, s.d_model, 128));
+    FORGE_TRY(run_operand(&plan.run[3], X, s.d_model, b_extent(t, false)));
+    FORGE_TRY(run_operand(&plan.run[4], c.ws + l.h, s.d_ff, b_extent(t, false)));
     FORGE_TRY(launch_plan(c, plan));
     ExpertGroup<kBlockGatedBwd> g;
     begin_group(g, c, slices(s.d_model));

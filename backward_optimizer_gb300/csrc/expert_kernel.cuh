@@ -44,6 +44,7 @@ template <int EPI>
 struct ExpertGroup {
     int n;                // products
     int n_units;          // kExpertGrad; else tiles_n times *n_tiles
+    int chunk;            // kExpertGrad: neighbouring units that a pair or CTA takes
     int experts;
     int a_rows;           // rows of A that a stage holds, and of a tile on single CTAs (128 or 32)
     int stream_b;         // each weight is read by one row tile or few: leave it out of the L2
@@ -90,6 +91,21 @@ FORGE_HD int expert_parts(const ExpertCut& c, int rest) {
     }
     return best;
 }
+
+// The units of a pair or CTA: `chunk` neighbours at a time, dealt out in turn.
+struct ExpertWalk {
+    int u, left, chunk, jump;
+    __device__ __forceinline__ ExpertWalk(int pair, int pairs, int chunk_)
+        : u(pair * chunk_), left(chunk_), chunk(chunk_), jump(1 + (pairs - 1) * chunk_) {}
+    __device__ __forceinline__ void next() {
+        if (--left > 0) {
+            ++u;
+        } else {
+            u += jump;
+            left = chunk;
+        }
+    }
+};
 
 template <int CG, int EPI>
 __device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int u, int n_tiles, int4 cut) {
@@ -260,6 +276,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
     const int n_tiles = kGrad ? 0 : __ldcg(grp.n_tiles);
     const int4 cut = kGrad ? make_int4(0, 0, 0, 0) : __ldcg(grp.cut);
     const int n_units = kGrad ? grp.n_units : cut.z;
+    const int chunk = kGrad ? grp.chunk : 1;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -288,8 +305,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                 return true;
             };
             int seen_prob = -1, seen_expert = -1;
-            for (int u = pair; ok && u < n_units; u += pairs) {
-                const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles, cut);
+            for (ExpertWalk at(pair, pairs, chunk); ok && at.u < n_units; at.next()) {
+                const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut);
                 const ExpertProblem& b = grp.prob[w.prob];
                 const int row_a = w.row0 + static_cast<int>(rank) * kBM;
                 const int col_b = kGated ? w.nb * kColsPerTile : w.nb * BN + static_cast<int>(rank) * C::kBLoad;
@@ -357,8 +374,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, issued_any = false;
-            for (int u = pair; ok && u < n_units; u += pairs) {
-                const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles, cut);
+            for (ExpertWalk at(pair, pairs, chunk); ok && at.u < n_units; at.next()) {
+                const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut);
                 const bool amn = kGrad;
                 const bool bmn = kGrad || EPI == kBlockGatedBwd || (EPI == kBlockStore && grp.prob[0].b_mn != 0);
                 const uint32_t idesc = idesc_bf16_f32(kBM * CG, BN, amn, bmn);
@@ -401,8 +418,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
         uint32_t acc_phase = 0;
         ExpertOut<(C::kStaging > 0)> out{grp.outs, {grp.to[0], grp.to[1], grp.to[2]}, 0, 0, 0, kGrad,
                                          smem_addr(staging) + static_cast<uint32_t>(e) * 4096u, 0};
-        for (int u = pair; u < n_units; u += pairs) {
-            const ExpertUnit w = expert_unit<CG, EPI>(grp, u, n_tiles, cut);
+        for (ExpertWalk at(pair, pairs, chunk); at.u < n_units; at.next()) {
+            const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut);
             const ExpertProblem& p = grp.prob[w.prob];
             const int row = w.row0 + static_cast<int>(rank) * kBM + quarter * 32 + lane;
             BlockProblem b;

@@ -199,14 +199,20 @@ __device__ __forceinline__ void tma_load_4d_cg(uint32_t dst, const CUtensorMap* 
     }
 }
 
-// Tensor maps made on the device: a copy of an encoded one in global memory (128-byte aligned) whose base address
-// and second extent are replaced, then released by the thread that made it and acquired by each that copies with it.
-__device__ __forceinline__ void tensormap_set(CUtensorMap* map, const void* base, uint32_t extent) {
+// Tensor maps made on the device: a copy of an encoded one in global memory (128-byte aligned) whose base address and
+// extents are replaced, then released by the thread that made it and acquired by each that copies with it.  The
+// encoded one has to be of a tensor of a few bytes, widened here: a map that was encoded for a large tensor and cut
+// down copies the right values, but fetches what lies past the new extents as well (2000 boxes of 64 rows with one
+// row inside: 513 thousand L2 sectors, 137 thousand when made on the host for one row), which is a page fault where
+// the tensor ends with its page.
+__device__ __forceinline__ void tensormap_set(CUtensorMap* map, const void* base, uint32_t dim0, uint32_t dim1, uint32_t dim2) {
     const uint64_t at = reinterpret_cast<uint64_t>(map);
     asm volatile("tensormap.replace.tile.global_address.global.b1024.b64 [%0], %1;" ::"l"(at),
                  "l"(reinterpret_cast<uint64_t>(base))
                  : "memory");
-    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(at), "r"(extent) : "memory");
+    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 0, %1;" ::"l"(at), "r"(dim0) : "memory");
+    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(at), "r"(dim1) : "memory");
+    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 2, %1;" ::"l"(at), "r"(dim2) : "memory");
     asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
 }
 __device__ __forceinline__ void tensormap_acquire(const CUtensorMap* map) {

@@ -204,3 +204,27 @@ def test_no_rows():
     fg.expert_gated_mlp_backward(X, X, dY, dY, W, W, _full(3, 64, 72), off, None, *out)
     assert fg.sync_status() == 0
     assert not any(t.any() for t in out)
+
+
+@pytest.mark.parametrize("D, F", [(520, 1032), (512, 1024)])
+def test_tensors_that_end_with_their_memory(D, F):
+    """Runs shorter than a slice at the very end of an allocation of whole pages: nothing past it is read."""
+    sizes = [82, 20, 57, 0, 10, 7, 0, 36, 110, 8, 237, 0, 2, 117, 237, 13]
+    R, E = sum(sizes), len(sizes)
+    gen = torch.Generator().manual_seed(8)
+
+    def at_the_end(t):
+        whole = torch.zeros(22 << 19 << 1, dtype=torch.bfloat16, device="cuda")  # 44 MiB, a segment of its own
+        v = whole[-t.numel():].view(t.shape)
+        v.copy_(t)
+        return v
+    X, dY, U = at_the_end(_tensor(gen, R, D)), at_the_end(_tensor(gen, R, D, std=0.01)), at_the_end(_tensor(gen, R, F))
+    i = {"X": X, "dY": dY, "G": at_the_end(_tensor(gen, R, F)), "U": U, "Wg": _tensor(gen, E, F, D, std=D ** -0.5),
+         "Wu": _tensor(gen, E, F, D, std=D ** -0.5), "Wd": _tensor(gen, E, D, F, std=F ** -0.5)}
+    dX, *dW = _backward(i, _offsets(sizes), "silu")
+    assert fg.sync_status() == 0
+    for e, r in _runs(sizes):
+        if r.stop > r.start:
+            want, tol = dense._gradients(_of(i, e, r), "silu")
+            for got, c, t in zip((dX[r], *(w[e] for w in dW)), want, tol):
+                assert_close(got, c, (1 + U8) * t + U8 * c.abs(), f"expert {e}")
