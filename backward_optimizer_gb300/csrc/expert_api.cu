@@ -159,12 +159,14 @@ struct Call {
     const int* offsets;
 };
 
-// Row tiles: 256 rows on pairs where an expert has that many to fill most of one; else 128, or 32 where
-// experts have few rows and the weights' bytes are all there is to move.
+// Row tiles, by the rows that an expert has on average: 256 on pairs, 128, 64 or 32 on single CTAs, whose copies of A
+// are as many rows.  Gated forward, 2048/1408, 64 experts, us on 256 / 128 / 64 / 32 rows: 8 rows each 182 / 173 / 167 / 167;
+// 32: 199 / 187 / 186 / 225; 64: 203 / 195 / 229; 128: 218 / 239; 256: 281 / 355.  4096/14336, 8 experts: 128 rows each 539 / 566;
+// 16: 458 / 441 / 425 / 435; one row of two experts 176 / 183 / 140 / 122.
 Tiling choose_rows(int64_t rows, int64_t experts) {
     const int64_t each = rows / std::min(rows, experts);
-    if (each > 160) return Tiling{256, 256};
-    return each > 24 ? Tiling{128, 128} : Tiling{128, 32};
+    if (each > 90) return Tiling{256, 256};
+    return Tiling{128, each > 40 ? 128 : each > 4 ? 64 : 32};
 }
 
 // A row product of a call: its columns, those of a tile, and its reduction.
@@ -257,8 +259,9 @@ template <int EPI>
 forge_status set_result(ExpertGroup<EPI>& g, const Tiling& t, int i, void* base, int64_t experts, int64_t rows, int64_t cols) {
     g.to[i] = static_cast<uint16_t*>(base);
     if (!forge::staged(EPI) || t.bn != 256) return FORGE_OK;
-    return kept_map(&g.outs[i], MapKey{base, cols, rows, cols, 0, 0, experts},
-                    [&] { return host::encode_result_map(&g.outs[i], base, cols, rows, experts); });
+    const int box = EPI == kExpertGrad ? 64 : 32;
+    return kept_map(&g.outs[i], MapKey{base, cols, rows, cols, -box, 0, experts},
+                    [&] { return host::encode_result_map(&g.outs[i], base, cols, rows, experts, box); });
 }
 
 // ---------------------------------------------------------------- launches
@@ -360,7 +363,10 @@ Tiling grad_tiling(const Machine& mc, int64_t experts, const GradProduct* p, int
     return pairs >= mc.pairs ? Tiling{256, 256} : Tiling{128, 128};
 }
 
-int grad_chunk(const Call& c) { return c.rows < 256ll * c.experts ? 4 : 1; }
+// Neighbouring units of a pair or CTA.  A unit of another expert costs two fences on its maps: with short runs four units
+// of one expert at a time (2048 rows of 64 experts, gated backward 2048/1408: 405 us, one at a time 432), where each still
+// gets several such groups (1003 rows of 16 experts, 520/1032: 63.8 us so, 61.2 one at a time).
+int grad_chunk(const Call& c, int64_t units, int width) { return c.rows < 256ll * c.experts && units >= 16ll * width ? 4 : 1; }
 
 forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int n) {
     ExpertGroup<kExpertGrad> g;
@@ -383,7 +389,7 @@ forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int
         FORGE_TRY(set_result(g, t, i, p[i].out, c.experts, p[i].d_out, p[i].d_in));
     }
     g.n_units = static_cast<int>(u);
-    g.chunk = grad_chunk(c);
+    g.chunk = grad_chunk(c, u, t.bn == 256 ? c.mc.pairs : c.mc.dev.num_sms);
     return launch(g, c, t.bn, u);
 }
 

@@ -155,8 +155,7 @@ struct ExpertOut {
     uint16_t* to[3];
     int64_t ld;
     int rows;      // one past the last row that may be written
-    int z;         // third coordinate of the tiled store
-    bool boxed;    // the store's own bounds end the result (the weights' gradients)
+    int z;         // third coordinate of the tiled store: 0, or the expert of a weight's gradient
     uint32_t buf;
     int turn;
     template <int W>
@@ -164,7 +163,7 @@ struct ExpertOut {
         const uint32_t lane = threadIdx.x & 31u;
         if constexpr (kStaged) {
             static_assert(W == 16);
-            if (boxed || row0 + 32 <= rows) {
+            if (row0 + 32 <= rows) {
                 if (lane == 0) bulk_wait_read<1>();  // the buffer's last store has read it
                 __syncwarp();
                 const uint32_t at = buf + (static_cast<uint32_t>(turn) << 11);
@@ -209,6 +208,42 @@ struct ExpertOut {
         }
     }
 };
+
+// The weights' gradients on pairs leave in boxes of 32 rows x 64 columns, whole 128-byte lines: what a store's copy
+// engine takes a row of a box, not a byte, sets the pace of tiles with few slices (2048 rows of 32 experts, 1024 x 2048
+// weights, 134 MB of results: 39 us in boxes of 32 columns).
+template <int BN, class Acc>
+__device__ __forceinline__ void epi_expert_grad(const BlockProblem& b, const Acc& acc, int row, int nb, int h, const CUtensorMap* map,
+                                                int expert, uint32_t buf) {
+    const int row0 = warp_row0(row);
+    if (row0 >= b.rows) return;
+    const uint32_t lane = threadIdx.x & 31u;
+#pragma unroll 1
+    for (int c = h * (BN / 2); c < (h + 1) * (BN / 2); c += 64) {
+        const int col = nb * BN + c;
+        if (b.cols - col <= 0) break;  // the same for the whole warp
+        uint32_t o[32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t g[32];
+            acc.load(c + 32 * i, g);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[16 * i + j] = pack_bf16x2_rn(g[2 * j], g[2 * j + 1]);
+        }
+        if (lane == 0) bulk_wait_read<0>();  // the last box has left the buffer
+        __syncwarp();
+        // the 128-byte swizzle: 16-byte piece j of row r lies at piece j ^ (r mod 8)
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+            st_shared_v4(buf + lane * 128u + ((j ^ (lane & 7u)) << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(map, buf, col, row0, expert);
+            bulk_commit();
+        }
+    }
+}
 
 template <int BN, int CG, int EPI>
 __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
@@ -416,7 +451,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
         const AbortCtx ab_acc{abort_flag, grp.status, grp.acc_wait_limit_ns};
         int acc = 0;
         uint32_t acc_phase = 0;
-        ExpertOut<(C::kStaging > 0)> out{grp.outs, {grp.to[0], grp.to[1], grp.to[2]}, 0, 0, 0, kGrad,
+        ExpertOut<(C::kStaging > 0)> out{grp.outs, {grp.to[0], grp.to[1], grp.to[2]}, 0, 0, 0,
                                          smem_addr(staging) + static_cast<uint32_t>(e) * 4096u, 0};
         for (ExpertWalk at(pair, pairs, chunk); at.u < n_units; at.next()) {
             const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut);
@@ -450,6 +485,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             auto epilogue = [&](const auto& acc_from) {
                 if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, acc_from, row, w.nb, half, out);
                 else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, acc_from, row, w.nb, half, out);
+                else if constexpr (kGrad && C::kStaging > 0) epi_expert_grad<BN>(b, acc_from, row, w.nb, half, out.maps, out.z, out.buf);
                 else epi_store<BN>(b, acc_from, row, w.nb, half, out);
             };
             // [cut tile][part][CTA][lane quarter][column][lane]; quarters past the tile's rows are not there
