@@ -437,6 +437,7 @@ def debug_withhold_next_stage() -> None:
 
 from . import operators  # noqa: E402  (it uses the checks above)
 from .operators import (dropout, dropout_backward, expert_gated_mlp, expert_gated_mlp_backward,  # noqa: E402
-                        expert_linear, expert_linear_backward, gated_mlp, gated_mlp_backward, gated_mlp_backward_step,
-                        layer_norm, layer_norm_backward, linear_cross_entropy, linear_cross_entropy_backward,
-                        linear_cross_entropy_step, preference_loss, preference_loss_backward)
+                        expert_gated_mlp_backward_step, expert_linear, expert_linear_backward, expert_linear_backward_step,
+                        gated_mlp, gated_mlp_backward, gated_mlp_backward_step, layer_norm, layer_norm_backward,
+                        linear_cross_entropy, linear_cross_entropy_backward, linear_cross_entropy_step, preference_loss,
+                        preference_loss_backward)

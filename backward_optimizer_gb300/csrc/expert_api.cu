@@ -240,9 +240,11 @@ forge_status weight_map(CUtensorMap* map, const void* base, int64_t experts, int
     });
 }
 
-// An operand of the weights' gradients, [rows, cols] and MN-major: its map, which the plan makes one of each run.
+// An operand of the weights' gradients, [rows, cols] and MN-major: its map, which the plan makes one of each run.  A
+// slice of `extent` columns is one box of blocks of 64 columns, or (extent 64, and widths that are no multiple of 64) a
+// box for each 64.
 forge_status run_operand(RunOperand* o, const void* base, int64_t cols, int extent) {
-    const bool blocks = cols % 64 == 0;
+    const bool blocks = extent > 64 && cols % 64 == 0;
     o->base = static_cast<const char*>(base);
     o->pitch = cols * 2;
     o->dim0 = blocks ? 64 : static_cast<uint32_t>(cols);
@@ -365,8 +367,11 @@ Tiling grad_tiling(const Machine& mc, int64_t experts, const GradProduct* p, int
 
 // Neighbouring units of a pair or CTA.  A unit of another expert costs two fences on its maps: with short runs four units
 // of one expert at a time (2048 rows of 64 experts, gated backward 2048/1408: 405 us, one at a time 432), where each still
-// gets several such groups (1003 rows of 16 experts, 520/1032: 63.8 us so, 61.2 one at a time).
-int grad_chunk(const Call& c, int64_t units, int width) { return c.rows < 256ll * c.experts && units >= 16ll * width ? 4 : 1; }
+// gets several such groups (1003 rows of 16 experts, 520/1032: 63.8 us so, 61.2 one at a time) and an expert has too few tiles to
+// keep them on it anyway (16 rows of 8 experts, 4096/14336, 896 tiles each: 895 and 878).
+int grad_chunk(const Call& c, int64_t units, int64_t each, int width) {
+    return c.rows < 256ll * c.experts && units >= 16ll * width && each < 2ll * width ? 4 : 1;
+}
 
 forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int n) {
     ExpertGroup<kExpertGrad> g;
@@ -382,14 +387,14 @@ forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int
         b.tiles_n = static_cast<int>(ceil_div(p[i].d_in, t.bn));
         b.unit_start = static_cast<int>(u);
         b.a_flat = p[i].d_out % 64 != 0;
-        b.b_flat = p[i].d_in % 64 != 0;
+        b.b_flat = t.bn == 64 || p[i].d_in % 64 != 0;  // as run_operand
         b.map_a = p[i].a;
         b.map_b = p[i].b;
         u += static_cast<int64_t>(c.experts) * b.tiles_m * b.tiles_n;
         FORGE_TRY(set_result(g, t, i, p[i].out, c.experts, p[i].d_out, p[i].d_in));
     }
     g.n_units = static_cast<int>(u);
-    g.chunk = grad_chunk(c, u, t.bn == 256 ? c.mc.pairs : c.mc.dev.num_sms);
+    g.chunk = grad_chunk(c, u, static_cast<int64_t>(g.prob[0].tiles_m) * g.prob[0].tiles_n, t.bn == 256 ? c.mc.pairs : c.mc.dev.num_sms);
     return launch(g, c, t.bn, u);
 }
 
@@ -439,10 +444,45 @@ int64_t linear_space(const Machine& mc, const forge_expert_linear_shape& s, bool
     return a.used;
 }
 
+// dH, and with it dG, dU and H in the workspace
+forge_status run_gated_dh(const GatedSpace& l, const forge_expert_gated_shape& s, const void* dY, const void* G, const void* U,
+                          const void* Wd) {
+    const Call& c = l.c;
+    ExpertGroup<kBlockGatedBwd> g;
+    begin_group(g, c, slices(s.d_model));
+    set_rows(g, c, 0, s.d_ff, s.d_model, 0);
+    g.act = s.act;
+    g.g_in = static_cast<const uint16_t*>(G);
+    g.u_in = static_cast<const uint16_t*>(U);
+    const int64_t outs[3] = {l.dg, l.du, l.h};
+    for (int i = 0; i < 3; ++i) FORGE_TRY(set_result(g, c.tiling, i, c.ws + outs[i], 1, s.rows, s.d_ff));
+    g.prob[0].b_flat = s.d_ff % 64 != 0;
+    FORGE_TRY(rows_map(&g.maps[0], c, dY, s.d_model));
+    FORGE_TRY(weight_map(&g.maps[1], Wd, s.experts, s.d_model, s.d_ff, true, b_extent(c.tiling, false)));
+    return launch(g, c, c.tiling.bn, most_units(c, 0));
+}
+
+forge_status run_gated_dx(const GatedSpace& l, const forge_expert_gated_shape& s, const void* Wg, const void* Wu, void* dX) {
+    return run_rows(l.c, 1, RowProduct{{l.c.ws + l.dg, l.c.ws + l.du}, {Wg, Wu}, s.d_ff, s.d_model, true, dX});
+}
+
 forge_status zero(std::initializer_list<void*> ps, int64_t bytes, cudaStream_t stream) {
     for (void* p : ps)
         if (p != nullptr && cudaMemsetAsync(p, 0, static_cast<size_t>(bytes), stream) != cudaSuccess) return FORGE_ERR_CUDA;
     return FORGE_OK;
+}
+
+// The rows of all experts' weights are numbered as one matrix's.
+forge_status check_stacked(int64_t experts, int64_t d_out) {
+    return experts * d_out > kMaxDim ? FORGE_ERR_INVALID_ARGUMENT : FORGE_OK;
+}
+
+// The fused step of one layer; a and b: its run operands' numbers
+forge_status run_step(const Call& c, int a, int b, const void* dY, const void* X, int64_t rows, int64_t experts, const forge_layer& w,
+                      forge_opt_kind k, const forge_hparams* hp, int32_t state, int64_t step, cudaStream_t stream) {
+    const CUtensorMap* runs = reinterpret_cast<const CUtensorMap*>(c.ws + c.runs);
+    return host::expert_step(dY, X, reinterpret_cast<const int*>(c.ws + c.clean), runs + a * experts, runs + b * experts, rows,
+                             experts, w.W, w.m, w.v, w.qscales, k, hp, w.d_out, w.d_in, state, step, w.seed, stream);
 }
 
 }  // namespace
@@ -583,21 +623,88 @@ forge_status forge_expert_gated_mlp_backward(const void* dY, const void* X, cons
     FORGE_TRY(run_operand(&plan.run[3], X, s.d_model, b_extent(t, false)));
     FORGE_TRY(run_operand(&plan.run[4], c.ws + l.h, s.d_ff, b_extent(t, false)));
     FORGE_TRY(launch_plan(c, plan));
-    ExpertGroup<kBlockGatedBwd> g;
-    begin_group(g, c, slices(s.d_model));
-    set_rows(g, c, 0, s.d_ff, s.d_model, 0);
-    g.act = s.act;
-    g.g_in = static_cast<const uint16_t*>(G);
-    g.u_in = static_cast<const uint16_t*>(U);
-    const int64_t outs[3] = {l.dg, l.du, l.h};
-    for (int i = 0; i < 3; ++i) FORGE_TRY(set_result(g, c.tiling, i, c.ws + outs[i], 1, s.rows, s.d_ff));
-    g.prob[0].b_flat = s.d_ff % 64 != 0;
-    FORGE_TRY(rows_map(&g.maps[0], c, dY, s.d_model));
-    FORGE_TRY(weight_map(&g.maps[1], Wd, s.experts, s.d_model, s.d_ff, true, b_extent(c.tiling, false)));
-    FORGE_TRY(launch(g, c, c.tiling.bn, most_units(c, 0)));
-    if (dX != nullptr)
-        FORGE_TRY(run_rows(c, 1, RowProduct{{c.ws + l.dg, c.ws + l.du}, {Wg, Wu}, s.d_ff, s.d_model, true, dX}));
+    FORGE_TRY(run_gated_dh(l, s, dY, G, U, Wd));
+    if (dX != nullptr) FORGE_TRY(run_gated_dx(l, s, Wg, Wu, dX));
     return run_grads(c, t, p, 3);
+}
+
+forge_status forge_expert_linear_backward_step(const void* dY, const void* X, void* W, const int32_t* offsets, void* dX, void* m,
+                                               void* v, float* qscales, void* workspace, int64_t workspace_bytes, int32_t state,
+                                               forge_opt_kind opt_kind, const forge_hparams* hp,
+                                               const forge_expert_linear_shape* shape, int64_t step, uint64_t seed,
+                                               struct CUstream_st* stream) {
+    FORGE_TRY(check_linear(shape));
+    const forge_expert_linear_shape& s = *shape;
+    FORGE_TRY(check_stacked(s.experts, s.d_out));
+    FORGE_TRY(host::check_step(W, m, v, qscales, opt_kind, hp, s.d_out, s.d_in, state, step));
+    if (!aligned(dX, 32)) return FORGE_ERR_MISALIGNED;
+    Call c{};
+    if (s.rows > 0) {
+        FORGE_TRY(check_all({dY, X}));
+        FORGE_TRY(check_offsets(offsets));
+        Machine mc;
+        FORGE_TRY(machine(&mc));
+        FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, true, &c)));
+        c.ws = static_cast<char*>(workspace);
+        c.stream = stream;
+        c.offsets = offsets;
+        PlanArgs plan{};
+        plan.n_runs = 2;
+        FORGE_TRY(run_operand(&plan.run[0], dY, s.d_out, 64));
+        FORGE_TRY(run_operand(&plan.run[1], X, s.d_in, 64));
+        FORGE_TRY(launch_plan(c, plan));
+        // dX reads the weights before the fused step replaces them: same stream, this order
+        if (dX != nullptr) FORGE_TRY(run_rows(c, 0, RowProduct{{dY, nullptr}, {W, nullptr}, s.d_out, s.d_in, true, dX}));
+    }
+    return run_step(c, 0, 1, dY, X, s.rows, s.experts, forge_layer{nullptr, nullptr, W, m, v, qscales, 0, s.d_out, s.d_in, seed},
+                    opt_kind, hp, state, step, stream);
+}
+
+forge_status forge_expert_gated_mlp_backward_step(const void* dY, const void* X, const void* G, const void* U,
+                                                  const forge_layer* gate, const forge_layer* up, const forge_layer* down,
+                                                  const int32_t* offsets, void* dX, void* workspace, int64_t workspace_bytes,
+                                                  int32_t state, forge_opt_kind opt_kind, const forge_hparams* hp,
+                                                  const forge_expert_gated_shape* shape, int64_t step, struct CUstream_st* stream) {
+    FORGE_TRY(check_gated(shape));
+    const forge_expert_gated_shape& s = *shape;
+    FORGE_TRY(check_stacked(s.experts, std::max(s.d_ff, s.d_model)));
+    if (gate == nullptr || up == nullptr || down == nullptr) return FORGE_ERR_INVALID_ARGUMENT;
+    for (const forge_layer* w : {gate, up})
+        FORGE_TRY(host::check_step(w->W, w->m, w->v, w->qscales, opt_kind, hp, s.d_ff, s.d_model, state, step));
+    FORGE_TRY(host::check_step(down->W, down->m, down->v, down->qscales, opt_kind, hp, s.d_model, s.d_ff, state, step));
+    if (!aligned(dX, 32)) return FORGE_ERR_MISALIGNED;
+    forge_layer layers[3] = {*gate, *up, *down};
+    for (int i = 0; i < 3; ++i) {
+        layers[i].d_out = i < 2 ? s.d_ff : s.d_model;
+        layers[i].d_in = i < 2 ? s.d_model : s.d_ff;
+    }
+    GatedSpace l{};
+    Call& c = l.c;
+    if (s.rows > 0) {
+        FORGE_TRY(check_all({dY, X, G, U}));
+        FORGE_TRY(check_offsets(offsets));
+        Machine mc;
+        FORGE_TRY(machine(&mc));
+        l = layout_gated(mc, s, true);
+        FORGE_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
+        c.ws = static_cast<char*>(workspace);
+        c.stream = stream;
+        c.offsets = offsets;
+        PlanArgs plan{};
+        plan.n_runs = kMaxRuns;
+        FORGE_TRY(run_operand(&plan.run[0], c.ws + l.dg, s.d_ff, 64));
+        FORGE_TRY(run_operand(&plan.run[1], c.ws + l.du, s.d_ff, 64));
+        FORGE_TRY(run_operand(&plan.run[2], dY, s.d_model, 64));
+        FORGE_TRY(run_operand(&plan.run[3], X, s.d_model, 64));
+        FORGE_TRY(run_operand(&plan.run[4], c.ws + l.h, s.d_ff, 64));
+        FORGE_TRY(launch_plan(c, plan));
+        // the input gradients read the weights before the fused step replaces them: same stream, this order
+        FORGE_TRY(run_gated_dh(l, s, dY, G, U, down->W));
+        if (dX != nullptr) FORGE_TRY(run_gated_dx(l, s, gate->W, up->W, dX));
+    }
+    FORGE_TRY(run_step(c, 0, 3, c.ws + l.dg, X, s.rows, s.experts, layers[0], opt_kind, hp, state, step, stream));
+    FORGE_TRY(run_step(c, 1, 3, c.ws + l.du, X, s.rows, s.experts, layers[1], opt_kind, hp, state, step, stream));
+    return run_step(c, 2, 4, dY, c.ws + l.h, s.rows, s.experts, layers[2], opt_kind, hp, state, step, stream);
 }
 
 }  // extern "C"

@@ -345,6 +345,11 @@ TileShape pick_dx_shape(int64_t T, int64_t /*d_out*/, int64_t d_in, int num_sms)
     return pick_tiles(T, d_in, num_sms, true);
 }
 
+// A weight for each expert: CTA pairs, or single CTAs on 128 x 128.
+TileFn tile_fn_ragged(forge_opt_kind k, int state, TileShape t) {
+    return t.cg == 2 ? tile_fn_v<256, 2, forge::kOpsBF16Ragged>(k, state) : tile_fn_v<128, 1, forge::kOpsBF16Ragged>(k, state);
+}
+
 template <int OPS>
 TileFn tile_fn_ops(forge_opt_kind k, int state, int epi, TileShape t) {
     using namespace forge;
@@ -676,6 +681,41 @@ forge_status fused_rows(const void* dY, int64_t dy_ld, const void* X, int64_t T,
     const forge_shape shape{T, rows, d_in, state, 0};
     return run_tile(dY, X, nullptr, at(W, 2), at(m, state_bytes), at(v, state_bytes), ms, k, kEpiOptFP32, hp, &shape,
                     step, seed, stream, *dev, false, 1.0f, nullptr, nullptr, dy_ld, vs, unit);
+}
+
+forge_status expert_step(const void* dY, const void* X, const int* offsets, const CUtensorMap* runs_dy, const CUtensorMap* runs_x,
+                         int64_t rows, int64_t experts, void* W, void* m, void* v, float* qscales, forge_opt_kind k,
+                         const forge_hparams* hp, int64_t d_out, int64_t d_in, int32_t state, int64_t step, uint64_t seed,
+                         cudaStream_t stream) {
+    DeviceInfo* dev = nullptr;
+    forge_status st = device_info(&dev);
+    if (st != FORGE_OK) return st;
+    if (rows == 0) {  // no rows: the gradient is exactly zero
+        const forge_shape whole{0, experts * d_out, d_in, state, 0};
+        return run_opt(nullptr, W, m, v, qscales, k, hp, &whole, step, seed, stream, *dev);
+    }
+    // one layer's shape rule; experts together fill the GPU where one alone would not
+    const bool wide = (d_out % 256 == 0 || (d_out % 128 != 0 && d_out > 1024)) && (d_in % 256 == 0 || (d_in % 128 != 0 && d_in > 1024)) &&
+                      4 * experts * ceil_div(d_out, 256) * ceil_div(d_in, 256) > dev->num_sms;
+    const TileShape ts = wide ? TileShape{256, 2} : TileShape{128, 1};
+    forge::RaggedGroup g;
+    g.n = 1;
+    const forge_shape shape{rows, d_out, d_in, state, 0};
+    float* v_scales = qscales == nullptr ? nullptr : qscales + experts * d_out * d_in / 64;
+    st = prepare_layer(g.layer[0], g.maps, dY, X, nullptr, W, m, v, qscales, k, hp, &shape, step, seed, *dev, ts, false, 1.0f,
+                       nullptr, nullptr, g_withhold_next.exchange(0), 0, v_scales);
+    if (st != FORGE_OK) return st;
+    g.layer[0].num_tiles *= static_cast<int>(experts);
+    g.tile_start[0] = 0;
+    g.tile_start[1] = g.layer[0].num_tiles;
+    g.experts = static_cast<int>(experts);
+    g.offsets = offsets;
+    g.runs = runs_dy;
+    g.runs_x = runs_x;
+    TileFn fn = tile_fn_ragged(k, state, ts);
+    if (fn == nullptr) return FORGE_ERR_UNSUPPORTED;
+    g_launches.fetch_add(1);
+    return cuda_status(fn(forge::TileLaunch{&g, g.layer[0].num_tiles, dev->num_sms, stream}));
 }
 
 }  // namespace host

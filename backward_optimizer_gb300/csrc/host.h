@@ -72,5 +72,13 @@ forge_status fused_rows(const void* dY, int64_t dy_ld, const void* X, int64_t T,
                         int64_t d_in, int32_t state, int64_t step, uint64_t seed, const float* unit,
                         cudaStream_t stream);
 
+// The fused step on the weights [experts, d_out, d_in] of a layer whose rows lie sorted by expert: dY [rows, d_out], X
+// [rows, d_in]; offsets and the operands' maps of each run as the plan of expert_api.cu left them on the device (boxes
+// of 64 rows and 64 columns).  Element numbers and scales are those of one matrix of experts * d_out rows.
+forge_status expert_step(const void* dY, const void* X, const int* offsets, const CUtensorMap* runs_dy, const CUtensorMap* runs_x,
+                         int64_t rows, int64_t experts, void* W, void* m, void* v, float* qscales, forge_opt_kind k,
+                         const forge_hparams* hp, int64_t d_out, int64_t d_in, int32_t state, int64_t step, uint64_t seed,
+                         cudaStream_t stream);
+
 }  // namespace host
 }  // namespace forge

@@ -1,0 +1,3 @@
+// Kernel instantiations with a weight for each expert for one optimizer (lion).
+#include "instantiate.cuh"
+FORGE_INSTANTIATE_OPT_RAGGED(forge::kLion)

@@ -50,12 +50,12 @@ cudaError_t launch_tile(const TileLaunch& l) {
     // persistent grid: one CTA per SM (or one cluster per CL SMs), never more units than tiles.
     // Pair kernels with bf16 operands split a short last wave into half tiles (schedule.h).
     const int cap = CL == 1 ? l.num_sms : max_clusters[dev].load();
-    constexpr bool kSplitTail = CG == 2 && BN == 256 && OPS != kOpsE4M3;
+    constexpr bool kSplitTail = CG == 2 && BN == 256 && OPS != kOpsE4M3 && OPS != kOpsBF16Ragged;
     const int split_from = kSplitTail ? split_tail_from(l.num_tiles, cap) : l.num_tiles;
     const int launch_tiles = l.num_tiles + (l.num_tiles - split_from);
     const int units = launch_tiles < cap ? launch_tiles : cap;
     cfg.gridDim = dim3(units * CL, 1, 1);
-    return cudaLaunchKernelEx(&cfg, kernel, *static_cast<const TileGroup<G>*>(l.group), split_from);
+    return cudaLaunchKernelEx(&cfg, kernel, *static_cast<const TileGroupOf<G, OPS>*>(l.group), split_from);
 }
 
 // CTA count and cluster size a launch_tile<..., BN, CL> call with `num_tiles` tiles would use.
@@ -124,6 +124,16 @@ cudaError_t launch_opt(const OptArgs& a, int grid, cudaStream_t stream) {
     FORGE_INSTANTIATE_SCALED(OPT, forge::kEpiOptFP32)  \
     FORGE_INSTANTIATE_SCALED(OPT, forge::kEpiOptBF16)  \
     FORGE_INSTANTIATE_TILES_OPS(OPT, forge::kEpiOptINT8, forge::kOpsBF16Scaled)
+
+// A weight for each expert, every state format.
+#define FORGE_INSTANTIATE_RAGGED(OPT, EPI)                                                                           \
+    template cudaError_t forge::launch_tile<OPT, EPI, 128, 1, forge::kOpsBF16Ragged, 1>(const forge::TileLaunch&);  \
+    template cudaError_t forge::launch_tile<OPT, EPI, 256, 2, forge::kOpsBF16Ragged, 1>(const forge::TileLaunch&);
+
+#define FORGE_INSTANTIATE_OPT_RAGGED(OPT)              \
+    FORGE_INSTANTIATE_RAGGED(OPT, forge::kEpiOptFP32)  \
+    FORGE_INSTANTIATE_RAGGED(OPT, forge::kEpiOptBF16)  \
+    FORGE_INSTANTIATE_RAGGED(OPT, forge::kEpiOptINT8)
 
 #define FORGE_INSTANTIATE_OPT(OPT)                    \
     FORGE_INSTANTIATE_TILES(OPT, forge::kEpiOptFP32) \

@@ -31,6 +31,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "opt_math.cuh"
 #include "ptx.cuh"
@@ -51,7 +52,8 @@ enum EpiKind : int { kEpiStoreGrad = 0, kEpiOptFP32 = 1, kEpiOptINT8 = 2, kEpiDX
 // gradient divided by a number in device memory; instantiations of their own, so that the unscaled ones stay
 // as they are (a test of a pointer in their epilogue, and the pointer among their parameters, cost 1 %:
 // Llama-8B MLP with INT8 states 1.034 ms per step against 1.023).
-enum OperandKind : int { kOpsBF16 = 0, kOpsE4M3 = 1, kOpsBF16Scaled = 2 };
+// kOpsBF16Ragged: bf16, and a weight for each expert over its run of the rows (RaggedGroup).
+enum OperandKind : int { kOpsBF16 = 0, kOpsE4M3 = 1, kOpsBF16Scaled = 2, kOpsBF16Ragged = 3 };
 
 template <int OPS>
 struct OperandTraits {
@@ -135,6 +137,28 @@ struct TileGroup {
     CUtensorMap maps[2 * G];      // per layer: dY (or dY for dX), X (or W for dX)
     TileArgs layer[G];
 };
+
+// One layer with a weight for each expert, [experts, d_out, d_in], whose gradient is summed over the expert's run of
+// the rows (expert_kernel.cuh).  The experts' weights and states are rows e d_out .. of one matrix of experts * d_out
+// rows: row numbers, element numbers (the random bits' counters) and scales are that matrix's.  The reduction ends
+// with the run: its tensor maps do (one pair an expert, made on the device), so what a slice holds past it is zero.
+struct RaggedGroup : TileGroup<1> {
+    int experts;
+    const int* offsets;        // [experts + 1], in order and within the rows
+    const CUtensorMap* runs;   // [experts] of dY, then [experts] of X
+    const CUtensorMap* runs_x;
+};
+template <int G, int OPS>
+using TileGroupOf = std::conditional_t<OPS == kOpsBF16Ragged, RaggedGroup, TileGroup<G>>;
+
+// The expert of tile `tile`, which becomes the tile's number among the expert's; slices of its run, 0 for none.
+__device__ __forceinline__ int ragged_tile(const RaggedGroup& g, int& tile, int& slices) {
+    const int per = g.layer[0].order.tiles_m * g.layer[0].order.tiles_n, e = tile / per;
+    tile -= e * per;
+    const int run = __ldcg(g.offsets + e + 1) - __ldcg(g.offsets + e);
+    slices = run > 0 ? (run + kBK - 1) / kBK : 0;
+    return e;
+}
 
 // The layer owning tile `tile`, from a layer index known to be at or before it.
 template <int G>
@@ -727,11 +751,12 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, uint64_t n_own, uin
 
 template <int BN, int CL, int EPI, int OPT, int OPS, int G>
 __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
-    forge_tile_kernel(const __grid_constant__ TileGroup<G> grp, const int split_from) {
+    forge_tile_kernel(const __grid_constant__ TileGroupOf<G, OPS> grp, const int split_from) {
     static_assert(CL == 1 || CL == 2, "cluster size");
     static_assert(OPS == kOpsBF16 || EPI != kEpiDX, "the input gradient takes bf16 operands");
     using O = OperandTraits<OPS>;
-    constexpr int kScale = OPS;
+    constexpr bool kRagged = OPS == kOpsBF16Ragged;
+    constexpr int kScale = kRagged ? kOpsBF16 : OPS;
     constexpr int CG = CL;                    // CTAs per MMA (cta_group)
     using C = TileCfg<BN, CG, EPI, OPS>;
     constexpr bool kAKMajor = EPI == kEpiDX;  // A = dY with d_out (= K) along memory
@@ -770,9 +795,11 @@ __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
         mbar_init(peer_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        for (int l = 0; l < grp.n; ++l) {
-            tma_prefetch_desc(&grp.maps[2 * l]);
-            tma_prefetch_desc(&grp.maps[2 * l + 1]);
+        if constexpr (!kRagged) {
+            for (int l = 0; l < grp.n; ++l) {
+                tma_prefetch_desc(&grp.maps[2 * l]);
+                tma_prefetch_desc(&grp.maps[2 * l + 1]);
+            }
         }
     }
     if (warp == 1) {
@@ -790,7 +817,7 @@ __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
     const AbortCtx ab{abort_flag, a0.status, a0.wait_limit_ns};
     // pair kernels with bf16 operands run the tiles from split_from on as two 256 x 128 halves
     // (schedule.h, split_tail_from); the others take split_from = the tile count
-    constexpr bool kSplitTail = CG == 2 && BN == 256 && OPS != kOpsE4M3;
+    constexpr bool kSplitTail = CG == 2 && BN == 256 && OPS != kOpsE4M3 && !kRagged;
     const int layer_tiles = grp.tile_start[grp.n];
     const int num_tiles = kSplitTail ? layer_tiles + (layer_tiles - split_from) : layer_tiles;
     uint64_t n_issued = 0;   // producer: stages passed (armed and copied, but for the withheld one)
@@ -811,15 +838,25 @@ __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
                 const TileArgs& a = grp.layer[l];
                 const CUtensorMap* tmap_dy = &grp.maps[2 * l];
                 const CUtensorMap* tmap_x = &grp.maps[2 * l + 1];
-                int mb, nb;
-                tile_coords(ot - grp.tile_start[l], a.order, mb, nb);
+                int mb, nb, kblocks = a.k_blocks, k_from = 0, in_layer = ot - grp.tile_start[l];
+                if constexpr (kRagged) {
+                    const int e = ragged_tile(grp, in_layer, kblocks);
+                    tmap_dy = grp.runs + e;
+                    tmap_x = grp.runs_x + e;
+                    tensormap_acquire(tmap_dy);
+                    tensormap_acquire(tmap_x);
+                    if (kblocks == 0) {  // no rows: one slice past the one row that its maps have
+                        kblocks = 1;
+                        k_from = kBK;
+                    }
+                }
+                tile_coords(in_layer, a.order, mb, nb);
                 const int row_a = mb * kBM * CG + static_cast<int>(rank) * kBM;
                 // a half tile's 128 columns: each CTA of the pair stages 64 of them in its first box
                 // (its second box, still copied so that every stage carries the same bytes, holds
                 // the next 64 columns, which the N = 128 MMA does not read)
                 const int col_b = part < 0 ? nb * BN + static_cast<int>(rank) * C::kBLoad
                                            : nb * BN + part * (BN / 2) + static_cast<int>(rank) * (C::kBLoad / 2);
-                const int kblocks = a.k_blocks;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     if (!wait_bounded(&empty[stage], phase ^ 1u, ab)) { ok = false; break; }
                     uint32_t bar = smem_addr(&full[stage]);
@@ -848,6 +885,15 @@ __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
                                 for (int h = 0; h < 2; ++h)
                                     tma_load_2d_cg<CG>(b_dst + j * O::kBlockBytes + h * 8192, tmap_x, bar,
                                                        col_b + 128 * j, k0 + 64 * h, keep);
+                        } else if constexpr (kRagged) {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                tma_load_3d_cg<CG>(smem_addr(a_dst + j * kBK * 128), tmap_dy, bar, row_a + 64 * j, k_from + k0, 0,
+                                                   keep);
+#pragma unroll
+                            for (int j = 0; j < C::kBLoad / 64; ++j)
+                                tma_load_3d_cg<CG>(smem_addr(b_dst + j * kBK * 128), tmap_x, bar, col_b + 64 * j, k_from + k0, 0,
+                                                   keep);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
@@ -887,7 +933,12 @@ __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
                 int part = -1;
                 const int ot = kSplitTail ? tail_tile(tile, split_from, part) : tile;
                 l = layer_of(grp, ot, l);
-                const int kblocks = grp.layer[l].k_blocks;
+                int kblocks = grp.layer[l].k_blocks;
+                if constexpr (kRagged) {
+                    int in_layer = ot;
+                    ragged_tile(grp, in_layer, kblocks);
+                    if (kblocks == 0) kblocks = 1;
+                }
                 const uint32_t id = part < 0 ? idesc : idesc_half;
                 if (!wait_bounded(&acc_empty[acc], acc_phase ^ 1u, ab)) { ok = false; break; }
                 tc_fence_after();
@@ -950,7 +1001,7 @@ __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
                 }
             }
         };
-        if constexpr (EPI == kEpiOptFP32 || EPI == kEpiOptBF16) {
+        if constexpr ((EPI == kEpiOptFP32 || EPI == kEpiOptBF16) && !kRagged) {
             if (first_tile < num_tiles) {
                 int part = -1;
                 const int ot = kSplitTail ? tail_tile(first_tile, split_from, part) : first_tile;
@@ -970,11 +1021,26 @@ __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
             int part = -1;
             const int ot = kSplitTail ? tail_tile(tile, split_from, part) : tile;
             l = layer_of(grp, ot, l);
-            const TileArgs& a = grp.layer[l];
+            // an expert's tile ends with the expert's rows of the whole matrix
+            auto args = [&](int rows_end) {
+                TileArgs t = grp.layer[0];
+                t.d_out = rows_end;
+                return t;
+            };
+            int first_row = 0, in_layer = ot - grp.tile_start[l], expert = 0;
+            if constexpr (kRagged) {
+                int slices;
+                expert = ragged_tile(grp, in_layer, slices);
+                first_row = expert * grp.layer[0].d_out;
+            }
+            const std::conditional_t<kRagged, TileArgs, const TileArgs&> a = [&]() -> std::conditional_t<kRagged, TileArgs, const TileArgs&> {
+                if constexpr (kRagged) return args(first_row + grp.layer[0].d_out);
+                else return grp.layer[l];
+            }();
             // the wait for a finished accumulator spans a whole tile mainloop, which grows with T
             const AbortCtx ab_acc{abort_flag, a0.status, a.acc_wait_limit_ns};
             int mb, nb;
-            tile_coords(ot - grp.tile_start[l], a.order, mb, nb);
+            tile_coords(in_layer, a.order, mb, nb);
             int ok = 1;
             if (lane == 0) ok = wait_bounded(&acc_full[acc], acc_phase, ab_acc) ? 1 : 0;
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -982,7 +1048,7 @@ __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
             tc_fence_after();
             int off, width, krange;
             cols_of(part, off, width, krange);
-            const int row0 = mb * kBM * CG + static_cast<int>(rank) * kBM + quarter * 32;
+            const int row0 = first_row + mb * kBM * CG + static_cast<int>(rank) * kBM + quarter * 32;
             const int col0 = nb * BN + (part > 0 ? BN / 2 : 0) + off;
             const uint32_t taddr =
                 tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN + off);
@@ -992,7 +1058,15 @@ __global__ void __launch_bounds__(TileCfg<BN, CL, EPI, OPS>::kThreads, 1)
             else if constexpr (EPI == kEpiOptFP32 || EPI == kEpiOptBF16) {
                 // the next tile's first run is prefetched only within the same layer
                 int row0n = -1, col0n = 0;
-                if (tile + tile_stride < num_tiles) {
+                if constexpr (kRagged) {
+                    int next = tile + tile_stride, slices;
+                    if (next < num_tiles && ragged_tile(grp, next, slices) == expert) {
+                        int mbn, nbn;
+                        tile_coords(next, a.order, mbn, nbn);
+                        row0n = first_row + mbn * kBM * CG + static_cast<int>(rank) * kBM + quarter * 32;
+                        col0n = nbn * BN + off;
+                    }
+                } else if (tile + tile_stride < num_tiles) {
                     int pn = -1;
                     const int otn = kSplitTail ? tail_tile(tile + tile_stride, split_from, pn) : tile + tile_stride;
                     if (layer_of(grp, otn, l) == l) {

@@ -76,6 +76,8 @@ def declare(L: ctypes.CDLL) -> None:
         "forge_expert_linear_backward": [vp] * 7 + [i64, elinear, vp],
         "forge_expert_gated_mlp": [vp] * 9 + [i64, egated, vp],
         "forge_expert_gated_mlp_backward": [vp] * 13 + [i64, egated, vp],
+        "forge_expert_linear_backward_step": [vp] * 9 + [i64, i32, ctypes.c_int, hp, elinear, i64, u64, vp],
+        "forge_expert_gated_mlp_backward_step": [vp] * 4 + [layer] * 3 + [vp] * 3 + [i64, i32, ctypes.c_int, hp, egated, i64, vp],
         "forge_dropout": [vp] * 3 + [i64, i32, ctypes.c_double, u64, u64, vp, vp],
         "forge_preference_loss": [vp] * 8 + [i64, pref, vp],
         "forge_preference_loss_backward": [vp] * 5 + [pref, vp],
@@ -405,6 +407,29 @@ def expert_linear_backward(dY, X, W, offsets, dX, dW, stream=None) -> None:
     _fg._check(_fg.lib().forge_expert_linear_backward(*args, ws, n, shape.arg, raw), "forge_expert_linear_backward")
 
 
+def _stacked(dev: int, W, m, v, qscales, name: str):
+    """Addresses of the experts' weights and states [E, F, D], checked as those of one matrix [E F, D], and their format."""
+    flat = [None if t is None else t.view(-1, W.shape[2]) if t.is_contiguous() and t.shape == W.shape else t for t in (W, m, v)]
+    _states(dev, flat[0], flat[1], flat[2], qscales)
+    return [_take(W, _BF16, tuple(W.shape), dev, name)] + [_fg._ptr(t) for t in (m, v, qscales)], _fg._state_of(m, v)
+
+
+def expert_linear_backward_step(dY, X, W, offsets, dX=None, m=None, v=None, qscales=None, opt: str = "adamw", hp: Any = None,
+                                step: int = 1, seed: int = 0, stream=None) -> None:
+    """The same backward pass with the fused step in place of dW: dX (None: not computed) from the weights as they are, and
+    W, m, v [E, d_out, d_in] updated in place; qscales as fused_dw_step takes them for one matrix of E d_out rows."""
+    dev, R, D, E, F = _grouped(X, W, "W")
+    shape = _shape(ExpertLinearShape, R, E, D, F, 0)
+    dy, x = _take(dY, _BF16, (R, F), dev, "dY"), _take(X, _BF16, (R, D), dev, "X")
+    o, dx = _take(offsets, torch.int32, (E + 1,), dev, "offsets"), _take(dX, _BF16, (R, D), dev, "dX")
+    (w, *states), state = _stacked(dev, W, m, v, qscales, "W")
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_expert_linear_workspace", dev, stream, raw, 1)
+    st = _fg.lib().forge_expert_linear_backward_step(dy, x, w, o, dx, *states, ws, n, state, _fg.OPT_KINDS[opt], _fg._hp_arg(hp),
+                                                     shape.arg, int(step), int(seed) & (2**64 - 1), raw)
+    _fg._check(st, "forge_expert_linear_backward_step")
+
+
 def expert_gated_mlp(X, Wg, Wu, Wd, offsets, Y, G=None, U=None, act: str = "silu", stream=None) -> None:
     """gated_mlp with each expert's weights for its rows, as expert_linear: Wg and Wu [E, F, D], Wd [E, D, F]; X and Y
     [R, D]; G and U [R, F], both or neither, for the backward pass."""
@@ -430,6 +455,31 @@ def expert_gated_mlp_backward(dY, X, G, U, Wg, Wu, Wd, offsets, dX, dWg, dWu, dW
     raw = _raw_stream(stream, dev)
     ws, n, _hold = _workspace(shape, "forge_expert_gated_mlp_workspace", dev, stream, raw, 1)
     _fg._check(_fg.lib().forge_expert_gated_mlp_backward(*args, ws, n, shape.arg, raw), "forge_expert_gated_mlp_backward")
+
+
+def expert_gated_mlp_backward_step(dY, X, G, U, gate, up, down, offsets, dX=None, act: str = "silu", opt: str = "adamw",
+                                   hp: Any = None, step: int = 1, stream=None) -> None:
+    """gated_mlp_backward_step with each expert's weights: gate, up and down are (W, m, v, qscales, seed) with W, m, v
+    [E, F, D] ([E, D, F] for down) and qscales of one matrix of E F (E D) rows."""
+    dev, R, D, E, F = _grouped(X, gate[0], "gate's W")
+    shape = _shape(ExpertGatedShape, R, E, D, F, _one_of(ACTIVATIONS, act, "act"), 0)
+    args = [_take(t, _BF16, s, dev, name) for t, s, name in (
+        (dY, (R, D), "dY"), (X, (R, D), "X"), (G, (R, F), "G"), (U, (R, F), "U"))]
+    layers, kinds = [], set()
+    for (W, m, v, q, seed), s, name in ((gate, (E, F, D), "gate"), (up, (E, F, D), "up"), (down, (E, D, F), "down")):
+        _take(W, _BF16, s, dev, f"{name}'s W")
+        ptrs, state = _stacked(dev, W, m, v, q, f"{name}'s W")
+        kinds.add(state)
+        layers.append(_fg.ForgeLayer(None, None, *ptrs, 0, 0, 0, int(seed) & (2**64 - 1)))
+    if len(kinds) > 1:
+        raise TypeError("the three layers must use the same state format")
+    o, dx = _take(offsets, torch.int32, (E + 1,), dev, "offsets"), _take(dX, _BF16, (R, D), dev, "dX")
+    raw = _raw_stream(stream, dev)
+    ws, n, _hold = _workspace(shape, "forge_expert_gated_mlp_workspace", dev, stream, raw, 1)
+    st = _fg.lib().forge_expert_gated_mlp_backward_step(
+        *args, *(ctypes.byref(a) for a in layers), o, dx, ws, n, kinds.pop(), _fg.OPT_KINDS[opt], _fg._hp_arg(hp), shape.arg,
+        int(step), raw)
+    _fg._check(st, "forge_expert_gated_mlp_backward_step")
 
 
 # ------------------------------------------------------------------ dropout

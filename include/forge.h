@@ -441,7 +441,17 @@ FORGE_API forge_status forge_expert_linear_backward(const void *dY, const void *
                                                     void *dX, void *dW, void *workspace, int64_t workspace_bytes,
                                                     const forge_expert_linear_shape *shape, struct CUstream_st *stream);
 
-/* backward: 0 for forge_expert_linear, 1 for the backward call. */
+/* The same backward pass with the fused step in place of dW: dX from the weights as they are (null: not computed), then
+ * W, m, v updated in place.  W, m and v are [experts, d_out, d_in], an expert without rows has gradient zero (its weights
+ * and moments still take their step); qscales and the elements' numbers (the counters of the random bits) are
+ * those of one matrix of experts * d_out rows, experts * d_out at most 2^30.  The gradients of the weights never exist. */
+FORGE_API forge_status forge_expert_linear_backward_step(const void *dY, const void *X, void *W, const int32_t *offsets,
+                                                         void *dX, void *m, void *v, float *qscales, void *workspace,
+                                                         int64_t workspace_bytes, int32_t state, forge_opt_kind opt_kind,
+                                                         const forge_hparams *hp, const forge_expert_linear_shape *shape,
+                                                         int64_t step, uint64_t seed, struct CUstream_st *stream);
+
+/* backward: 0 for forge_expert_linear, 1 for either backward call. */
 FORGE_API int64_t forge_expert_linear_workspace(const forge_expert_linear_shape *shape, int32_t backward);
 
 typedef struct forge_expert_gated_shape {
@@ -468,6 +478,16 @@ FORGE_API forge_status forge_expert_gated_mlp_backward(const void *dY, const voi
                                                        const int32_t *offsets, void *dX, void *dWg, void *dWu, void *dWd,
                                                        void *workspace, int64_t workspace_bytes,
                                                        const forge_expert_gated_shape *shape, struct CUstream_st *stream);
+
+/* The same backward pass with the fused step in place of the weights' gradients, as forge_gated_mlp_backward_step and
+ * forge_expert_linear_backward_step: of each forge_layer only W, m, v, qscales and seed are read. */
+FORGE_API forge_status forge_expert_gated_mlp_backward_step(const void *dY, const void *X, const void *G, const void *U,
+                                                            const forge_layer *gate, const forge_layer *up,
+                                                            const forge_layer *down, const int32_t *offsets, void *dX,
+                                                            void *workspace, int64_t workspace_bytes, int32_t state,
+                                                            forge_opt_kind opt_kind, const forge_hparams *hp,
+                                                            const forge_expert_gated_shape *shape, int64_t step,
+                                                            struct CUstream_st *stream);
 
 /* backward: 0 for forge_expert_gated_mlp, 1 for either backward call. */
 FORGE_API int64_t forge_expert_gated_mlp_workspace(const forge_expert_gated_shape *shape, int32_t backward);
