@@ -1,4 +1,5 @@
-"""Modules around the fused layers: the norm, the gated feed-forward block, and the head with its loss.
+"""Modules around the fused layers: the norm, the gated feed-forward block (dense, or one for each expert), dropout on a
+residual branch, the head with its loss, and the preference loss behind it.
 
 They put the library's operators (operators.py) behind PyTorch autograd, next to `ForgeLinear`
 (autograd.py).  The matrices of `ForgeGatedMLP` and `ForgeHeadLoss` are trained as `ForgeLinear`'s is
@@ -13,6 +14,12 @@ it raises an error.
     norm2, head = ForgeNorm(1024), ForgeHeadLoss(1024, vocab, opt="adamw", hp=hp, seed=3)
     h = mlp(norm1(x), residual=x)
     head(norm2(h), target).backward()
+
+With experts, dropout and pairs of sequences (rows sorted by expert; head made with reduction="none"):
+
+    h = dropout(experts(norm1(x)[order], offsets)[place], residual=x)
+    loss, reward = preference(head(norm2(h), target), ref_nll, sequences)
+    loss.mean().backward()
 """
 from __future__ import annotations
 
@@ -23,7 +30,7 @@ import torch
 from . import operators as ops
 from .autograd import _MOMENTS, _STATE_DTYPES, Stepped, once
 
-__all__ = ["ForgeNorm", "ForgeGatedMLP", "ForgeHeadLoss"]
+__all__ = ["ForgeNorm", "ForgeGatedMLP", "ForgeExpertMLP", "ForgeDropout", "ForgeHeadLoss", "ForgePreferenceLoss"]
 
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
@@ -176,15 +183,115 @@ class ForgeGatedMLP(_Trained):
         return f"d_model={d}, d_ff={f}, act={self.act}, opt={self.opt}, step={self.step}"
 
 
+class _ExpertFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, offsets, block, want_dx):
+        X = x.detach().contiguous()
+        F = block.gate.shape[1]
+        Y = torch.zeros_like(X)
+        G, U = (torch.empty(X.shape[0], F, dtype=torch.bfloat16, device=X.device) for _ in range(2))
+        ops.expert_gated_mlp(X, block.gate.data, block.up.data, block.down.data, offsets, Y, G, U, act=block.act)
+        ctx.save_for_backward(X, G, U, offsets)
+        ctx.block, ctx.want_dx = block, want_dx
+        return Y
+
+    @staticmethod
+    @once("ForgeExpertMLP")
+    def backward(ctx, grad_out):
+        X, G, U, offsets = ctx.saved_tensors
+        b = ctx.block
+        b._once()
+        dX = torch.zeros_like(X) if ctx.want_dx else None
+        ops.expert_gated_mlp_backward_step(grad_out.to(torch.bfloat16).contiguous(), X, G, U, b._layer("gate", b.seed),
+                                           b._layer("up", b.seed + 1), b._layer("down", b.seed + 2), offsets, dX, act=b.act,
+                                           opt=b.opt, hp=b.hp, step=b.step)
+        b._done()
+        return dX, None, None, None
+
+
+class ForgeExpertMLP(_Trained):
+    """ForgeGatedMLP with a block for each expert: rows offsets[e] .. offsets[e+1]-1 of x [rows, d_model] go through expert e
+    (offsets int32 [experts + 1] on the device, never read on the host); rows of no expert give 0.  Every expert takes the
+    optimizer step, with a gradient of zero where it had no row.  Arguments as for ForgeGatedMLP; seed, seed + 1 and
+    seed + 2 are the three stacked matrices'."""
+
+    def __init__(self, d_model: int, d_ff: int, experts: int, act: str = "silu", opt: str = "adamw", hp: Any = None,
+                 state: str = "fp32", seed: int = 0, device=None, init_std: float = 0.02):
+        if act not in ops.ACTIVATIONS:
+            raise ValueError(f"act: {act!r}, expected one of {list(ops.ACTIVATIONS)}")
+        super().__init__({"gate": (experts, d_ff, d_model), "up": (experts, d_ff, d_model), "down": (experts, d_model, d_ff)},
+                         opt, hp, state, seed, device, init_std)
+        self.act = act
+
+    def forward(self, x: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+        if x.dtype != torch.bfloat16:
+            raise TypeError("ForgeExpertMLP takes bfloat16 inputs")
+        if x.dim() != 2:
+            raise ValueError(f"x: {x.dim()} dimensions, expected 2")
+        if not torch.is_grad_enabled():
+            Y = torch.zeros_like(x, memory_format=torch.contiguous_format)
+            ops.expert_gated_mlp(x.contiguous(), self.gate.data, self.up.data, self.down.data, offsets, Y, act=self.act)
+            return Y
+        want_dx = x.requires_grad
+        anchor = x if want_dx else x.detach().requires_grad_(True)
+        self._pending = self.step
+        return _ExpertFn.apply(anchor, offsets, self, want_dx)
+
+    def extra_repr(self) -> str:
+        e, f, d = self.gate.shape
+        return f"d_model={d}, d_ff={f}, experts={e}, act={self.act}, opt={self.opt}, step={self.step}"
+
+
+class _DropoutFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, step):
+        X = x.detach().contiguous()
+        y = torch.empty_like(X)
+        ops.dropout(X, y, p, seed=seed, step=step, residual=None if residual is None else residual.detach().contiguous())
+        ctx.p, ctx.seed, ctx.step, ctx.dtype, ctx.has_residual = p, seed, step, x.dtype, residual is not None
+        return y
+
+    @staticmethod
+    @once("ForgeDropout")
+    def backward(ctx, grad_out):
+        dx = None
+        if ctx.needs_input_grad[0]:
+            dy = grad_out.to(ctx.dtype).contiguous()
+            dx = torch.empty_like(dy)
+            ops.dropout_backward(dy, dx, ctx.p, seed=ctx.seed, step=ctx.step)
+        return dx, grad_out if ctx.has_residual else None, None, None, None
+
+
+class ForgeDropout(Stepped):
+    """dropout(x) (+ residual), bf16 or FP32, whose mask is made again in the backward pass and never stored.  In training
+    mode each forward takes a mask of its own: number `step`, from 1, which goes into the state dict; seed is distinct
+    from other dropouts'.  In evaluation mode x (+ residual)."""
+
+    def __init__(self, p: float = 0.1, seed: int = 0):
+        if not 0.0 <= p <= 1.0:
+            raise ValueError(f"p: {p}, expected a number between 0 and 1")
+        super().__init__()
+        self.p, self.seed = float(p), int(seed)
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if not self.training:
+            return x if residual is None else x + residual
+        step, self.step = self.step, self.step + 1
+        return _DropoutFn.apply(x, residual, self.p, self.seed, step)
+
+    def extra_repr(self) -> str:
+        return f"p={self.p}, seed={self.seed}, step={self.step}"
+
+
 class _HeadFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, target, head, want_dx):
         X, t = _rows(x.detach()), target.reshape(-1).contiguous()
         loss, lse = head._losses(X, t)
-        share = head._share(t)
+        share = head._share(t) if head.reduction == "mean" else None
         ctx.save_for_backward(X, t, lse, share)
         ctx.head, ctx.want_dx, ctx.shape = head, want_dx, x.shape
-        return (loss * share).sum()
+        return loss.view(target.shape) if share is None else (loss * share).sum()
 
     @staticmethod
     @once("ForgeHeadLoss")
@@ -194,7 +301,8 @@ class _HeadFn(torch.autograd.Function):
         h._once()
         dX = torch.empty_like(X) if ctx.want_dx else None
         W, m, v, q, seed = h._layer("weight", h.seed)
-        ops.linear_cross_entropy_step(X, W, t, lse, share * grad_out, dX, m, v, q, ignore_index=h.ignore_index, opt=h.opt,
+        dloss = grad_out.float().reshape(-1).contiguous() if share is None else share * grad_out
+        ops.linear_cross_entropy_step(X, W, t, lse, dloss, dX, m, v, q, ignore_index=h.ignore_index, opt=h.opt,
                                       hp=h.hp, step=h.step, seed=seed)
         h._done()
         return (None if dX is None else dX.view(ctx.shape)), None, None, None
@@ -204,13 +312,16 @@ class ForgeHeadLoss(_Trained):
     """The mean softmax cross entropy of the logits x weight^T over the tokens whose target is not
     ignore_index (0 where there are none), trained by its backward pass; the logits never exist.
 
+    reduction="none": each token's loss instead, in target's shape (0 where it is ignored).
     x [..., d_model] bf16, target [...] int64, weight [vocab, d_model].  opt, hp, state and seed as for
     ForgeLinear (int8 states need d_model to be a multiple of 64)."""
 
     def __init__(self, d_model: int, vocab: int, opt: str = "adamw", hp: Any = None, state: str = "fp32", seed: int = 0,
-                 ignore_index: int = -100, device=None, init_std: float = 0.02):
+                 ignore_index: int = -100, device=None, init_std: float = 0.02, reduction: str = "mean"):
+        if reduction not in ("mean", "none"):
+            raise ValueError(f"reduction: {reduction!r}, expected 'mean' or 'none'")
         super().__init__({"weight": (vocab, d_model)}, opt, hp, state, seed, device, init_std)
-        self.ignore_index = int(ignore_index)
+        self.ignore_index, self.reduction = int(ignore_index), reduction
 
     def _losses(self, X, t):
         loss, lse = (_f32(X.shape[0], X.device) for _ in range(2))
@@ -229,7 +340,8 @@ class ForgeHeadLoss(_Trained):
             raise ValueError(f"target: shape {tuple(target.shape)}, expected {tuple(x.shape[:-1])}")
         if not torch.is_grad_enabled():
             t = target.reshape(-1).contiguous()
-            return (self._losses(_rows(x), t)[0] * self._share(t)).sum()
+            loss = self._losses(_rows(x), t)[0]
+            return loss.view(target.shape) if self.reduction == "none" else (loss * self._share(t)).sum()
         want_dx = x.requires_grad
         anchor = x if want_dx else x.detach().requires_grad_(True)
         self._pending = self.step
@@ -238,3 +350,46 @@ class ForgeHeadLoss(_Trained):
     def extra_repr(self) -> str:
         v, d = self.weight.shape
         return f"d_model={d}, vocab={v}, opt={self.opt}, ignore_index={self.ignore_index}, step={self.step}"
+
+
+class _PreferenceFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, nll, ref, offsets, mask, module):
+        n = nll.detach().reshape(-1).contiguous()
+        P = (offsets.shape[0] - 1) // 2
+        loss, reward, slope = (_f32(k, n.device) for k in (P, 2 * P, 2 * P))
+        r, m = (None if t is None else t.detach().reshape(-1).contiguous() for t in (ref, mask))
+        ops.preference_loss(n, r, offsets, loss, reward, slope, mask=m, **module.options)
+        ctx.save_for_backward(slope, offsets, m)
+        ctx.shape = nll.shape
+        ctx.mark_non_differentiable(reward)
+        return loss, reward
+
+    @staticmethod
+    @once("ForgePreferenceLoss")
+    def backward(ctx, grad_loss, _):
+        slope, offsets, mask = ctx.saved_tensors
+        dnll = _f32(ctx.shape.numel(), slope.device)
+        ops.preference_loss_backward(grad_loss.float().contiguous(), slope, offsets, dnll, mask=mask)
+        return dnll.view(ctx.shape), None, None, None, None
+
+
+class ForgePreferenceLoss(torch.nn.Module):
+    """The loss of each of P pairs of sequences, and the reward of each of the 2 P sequences (chosen ones first; not
+    differentiable), from each token's -log probability under the model (ForgeHeadLoss with reduction="none") and under the
+    reference (None: 0).  offsets int32 [2P + 1] on the device: where the sequences lie among the tokens; mask: tokens that
+    count.  beta, kind ("sigmoid", "hinge", "ipo"), smoothing, margin and mean as for operators.preference_loss."""
+
+    def __init__(self, beta: float = 0.1, kind: str = "sigmoid", smoothing: float = 0.0, margin: float = 0.0, mean: bool = False):
+        if kind not in ops.PREFERENCES:
+            raise ValueError(f"kind: {kind!r}, expected one of {list(ops.PREFERENCES)}")
+        super().__init__()
+        self.options = dict(beta=float(beta), kind=kind, smoothing=float(smoothing), margin=float(margin), mean=bool(mean))
+
+    def forward(self, nll: torch.Tensor, ref: Optional[torch.Tensor], offsets: torch.Tensor, mask: Optional[torch.Tensor] = None):
+        if offsets.dim() != 1 or offsets.shape[0] % 2 == 0:
+            raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected (2 P + 1,)")
+        return _PreferenceFn.apply(nll, ref, offsets, mask, self)
+
+    def extra_repr(self) -> str:
+        return ", ".join(f"{k}={v}" for k, v in self.options.items())
