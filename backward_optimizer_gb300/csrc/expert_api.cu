@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(1024) expert_plan_kernel(const __grid_constant
 // ---------------------------------------------------------------- tiles
 
 struct Tiling {
-    int bn;         // tile columns: 256 on CTA pairs, 128 or 64 on single CTAs
+    int bn;         // tile columns: 256 on CTA pairs, 128 on single CTAs
     int tile_rows;  // rows of a row tile
 };
 
@@ -196,8 +196,7 @@ Call make_call(const Machine& mc, int64_t rows, int64_t experts, int n_runs, std
         const int kb = slices(p.k) * (p.two ? 2 : 1);
         forge::ExpertCut& x = c.cut[c.n_cuts++];
         // joins as kTiles has them (block_api.cu)
-        x = forge::ExpertCut{static_cast<int>(ceil_div(p.cols, p.gated ? t.bn / 2 : t.bn)), kb, width, pair ? 8 : t.bn == 128 ? 6 : 10,
-                             pair ? 12 : t.bn == 128 ? 5 : 2};
+        x = forge::ExpertCut{static_cast<int>(ceil_div(p.cols, p.gated ? t.bn / 2 : t.bn)), kb, width, pair ? 8 : 6, pair ? 12 : 5};
         cut = cut || forge::expert_parts(x, 1) > 1;
     }
     c.n_counts = cut ? width * (pair ? 2 : 1) * 8 : 0;
@@ -387,7 +386,7 @@ forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int
         b.tiles_n = static_cast<int>(ceil_div(p[i].d_in, t.bn));
         b.unit_start = static_cast<int>(u);
         b.a_flat = p[i].d_out % 64 != 0;
-        b.b_flat = t.bn == 64 || p[i].d_in % 64 != 0;  // as run_operand
+        b.b_flat = p[i].d_in % 64 != 0;
         b.map_a = p[i].a;
         b.map_b = p[i].b;
         u += static_cast<int64_t>(c.experts) * b.tiles_m * b.tiles_n;

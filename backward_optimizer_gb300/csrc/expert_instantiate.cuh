@@ -41,8 +41,7 @@ cudaError_t launch_expert_as(const void* group, int units, cudaStream_t stream) 
 
 template <int EPI>
 cudaError_t launch_expert(const void* group, int bn, int units, cudaStream_t stream) {
-    if (bn == 256) return launch_expert_as<256, 2, EPI>(group, units, stream);
-    return bn == 128 ? launch_expert_as<128, 1, EPI>(group, units, stream) : launch_expert_as<64, 1, EPI>(group, units, stream);
+    return bn == 256 ? launch_expert_as<256, 2, EPI>(group, units, stream) : launch_expert_as<128, 1, EPI>(group, units, stream);
 }
 
 }  // namespace forge

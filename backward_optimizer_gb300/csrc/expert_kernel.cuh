@@ -46,7 +46,7 @@ struct ExpertGroup {
     int n_units;          // kExpertGrad; else tiles_n times *n_tiles
     int chunk;            // kExpertGrad: neighbouring units that a pair or CTA takes
     int experts;
-    int a_rows;           // rows of A that a stage holds, and of a tile on single CTAs (128 or 32)
+    int a_rows;           // rows of A that a stage holds, and of a tile on single CTAs (128, 64 or 32)
     int stream_b;         // each weight is read by one row tile or few: leave it out of the L2
     int act, keep;
     int withhold_first_stage;
@@ -64,7 +64,7 @@ struct ExpertGroup {
     uint16_t* to[3];      // results: kBlockStore's, kExpertGrad's of each product; G, U, H; dG, dU, H
     ExpertProblem prob[expert_products(EPI)];
     CUtensorMap maps[EPI == kExpertGrad ? 1 : 4];  // rows by expert: A, B of the first pair, A, B of the second
-    CUtensorMap outs[3];  // staged results
+    CUtensorMap outs[staged(EPI) ? 3 : 1];  // staged results, on pairs
 };
 
 struct ExpertUnit {
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                             tma_load_3d_cg<CG>(a_dst, ma, bar, a0, k0, a2, keep);
                             tma_load_3d_cg<CG>(b_dst, mb, bar, b0, k0, b2, keep);
                             if (a_flat) tma_load_3d_cg<CG>(a_dst + kBK * 128, ma, bar, a0 + 64, k0, 0, keep);
-                            if (C::kBLoad == 128 && b_flat) tma_load_3d_cg<CG>(b_dst + kBK * 128, mb, bar, b0 + 64, k0, 0, keep);
+                            if (b_flat) tma_load_3d_cg<CG>(b_dst + kBK * 128, mb, bar, b0 + 64, k0, 0, keep);
                         });
                 } else {
                     const bool bmn = EPI == kBlockGatedBwd || (EPI == kBlockStore && b.b_mn != 0);
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                                 tma_load_4d_cg<CG>(b_dst, mb, bar, b0, b1, b2, w.expert, pol_b);
                                 if (kGated && CG == 1)
                                     tma_load_4d_cg<CG>(b_dst + BN / 2 * 128, mu, bar, b0, b1, 0, w.expert, pol_b);
-                                if (!kGated && C::kBLoad == 128 && b_flat)
+                                if (!kGated && b_flat)
                                     tma_load_4d_cg<CG>(b_dst + kBK * 128, mb, bar, b0 + 64, b1, 0, w.expert, pol_b);
                             });
                     }

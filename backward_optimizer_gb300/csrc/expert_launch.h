@@ -5,8 +5,8 @@
 
 namespace forge {
 
-// One launch of EPI on CTA pairs with 256 x 256 tiles (bn = 256) or single CTAs with a_rows x bn tiles (128,
-// 64); group: an ExpertGroup<EPI>; units: pairs or CTAs.
+// One launch of EPI on CTA pairs with 256 x 256 tiles (bn = 256) or single CTAs with a_rows x 128 tiles;
+// group: an ExpertGroup<EPI>; units: pairs or CTAs.
 template <int EPI> cudaError_t launch_expert(const void* group, int bn, int units, cudaStream_t stream);
 
 }  // namespace forge
