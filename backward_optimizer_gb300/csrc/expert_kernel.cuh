@@ -12,8 +12,11 @@
 // Ragged runs.  A launch in front (expert_plan_kernel) turns the offsets into a list of row tiles and, for the
 // weights' gradients, into two tensor maps per expert whose token dimension ends with the run: the copy itself
 // fills what a slice reaches past the run with zeros, for both operands, so neither values of the next expert
-// nor its infinities or NaN enter a sum.  Row products need no such map: an accumulator row depends on its own
-// row of A alone, and rows past the run are not stored.  An expert without rows takes one slice of zero fill and
+// nor its infinities or NaN enter a sum.  Row products need none for their results: an accumulator row depends on its own
+// row of A alone, and rows past the run are not stored.  On pairs they have them all the same: the large products run at
+// the chip's power limit, and zeros past the run cost less than the next expert's rows (32768 rows of 64 experts, gated
+// forward 2048/1408, passes on end: 475 us with them, 505 without).  On single CTAs the fences for them would show (2048 rows
+// there: 193 us with them, 189 without).  An expert without rows takes one slice of zero fill and
 // stores a zero gradient.
 //
 // Few row tiles.  The plan knows how many there are; where the last wave of tiles leaves SMs idle it cuts them
@@ -36,7 +39,7 @@ struct ExpertProblem {
     int kb[2];            // rows by expert: 64-deep reduction slices of the two operand pairs
     int a_flat, b_flat;   // MN-major and no multiple of 64 wide: a copy for each 64 columns
     int b_mn;             // kBlockStore: W is read MN-major
-    int map_a, map_b;     // kExpertGrad: numbers of the operands' run maps
+    int map_a, map_b;     // numbers of run maps: kExpertGrad's operands, or (pairs) the A of each operand pair
     int64_t ld;           // the result's width
 };
 
@@ -52,7 +55,7 @@ struct ExpertGroup {
     int withhold_first_stage;
     const int4* cut;      // row products: tiles before .x are whole, the others cut into .y parts; .z units
     const int* n_tiles;   // row tiles
-    const int4* tiles;    // each: expert, first row, one past its last row
+    const int4* tiles;    // each: expert, first row, one past its last row, first row of its run
     const int* offsets;   // [experts + 1], as the plan left them: in order and within the rows
     const CUtensorMap* runs;  // [map][expert]
     const uint16_t* g_in;
@@ -63,12 +66,15 @@ struct ExpertGroup {
     uint64_t wait_limit_ns, acc_wait_limit_ns;
     uint16_t* to[3];      // results: kBlockStore's, kExpertGrad's of each product; G, U, H; dG, dU, H
     ExpertProblem prob[expert_products(EPI)];
-    CUtensorMap maps[EPI == kExpertGrad ? 1 : 4];  // rows by expert: A, B of the first pair, A, B of the second
+    // rows by expert: the weights of each operand pair, or the gate's and the up projection's; then, on single CTAs, A of
+    // each pair (on pairs: run maps)
+    CUtensorMap maps[EPI == kExpertGrad ? 1 : 4];
     CUtensorMap outs[staged(EPI) ? 3 : 1];  // staged results, on pairs
 };
 
 struct ExpertUnit {
     int prob, expert, nb, row0, end;  // row0: the tile's first row of the result; end: one past its last
+    int begin;                        // rows by expert: the run's first row
     int k_first, k_end;               // slices (rows by expert: of both operand pairs, one after the other)
     int split, part;                  // which cut tile, or -1
 };
@@ -122,6 +128,7 @@ __device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int
         tile_coords(t - r.expert * per, TileOrder{b.tiles_m, b.tiles_n, 8, 0}, mb, r.nb);
         r.row0 = mb * kBM * CG;
         r.end = b.rows;
+        r.begin = 0;
         const int run = __ldcg(g.offsets + r.expert + 1) - __ldcg(g.offsets + r.expert);
         r.k_end = run > 0 ? (run + kBK - 1) / kBK : 0;
     } else {
@@ -142,6 +149,7 @@ __device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int
         r.expert = at.x;
         r.row0 = at.y;
         r.end = at.z;
+        r.begin = at.w;
     }
     return r;
 }
@@ -291,7 +299,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
         fence_mbar_init();
         if constexpr (!kGrad) {
             tma_prefetch_desc(&grp.maps[0]);
-            tma_prefetch_desc(&grp.maps[1]);
+            if constexpr (kGated) tma_prefetch_desc(&grp.maps[1]);
+            if constexpr (CG == 1) tma_prefetch_desc(&grp.maps[2]);
         }
     }
     if (warp == 1) {
@@ -369,17 +378,24 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                 } else {
                     const bool bmn = EPI == kBlockGatedBwd || (EPI == kBlockStore && b.b_mn != 0);
                     const bool b_flat = bmn && b.b_flat != 0;
+                    if (CG == 2 && w.expert != seen_expert) {
+                        tensormap_acquire(grp.runs + static_cast<size_t>(b.map_a) * grp.experts + w.expert);
+                        if (b.kb[1] > 0) tensormap_acquire(grp.runs + static_cast<size_t>(b.map_b) * grp.experts + w.expert);
+                        seen_expert = w.expert;
+                    }
+                    const int map_row = CG == 2 ? row_a - w.begin : row_a;
 #pragma unroll 1
                     for (int seg = 0; seg < (EPI == kBlockStore ? 2 : 1) && ok; ++seg) {
                         // the unit's slices of this operand pair
                         const int base = seg == 0 ? 0 : b.kb[0];
                         const int from = w.k_first > base ? w.k_first - base : 0;
                         const int to = (w.k_end < base + b.kb[seg] ? w.k_end : base + b.kb[seg]) - base;
-                        const CUtensorMap* ma = &grp.maps[2 * seg];
+                        const CUtensorMap* ma = CG == 2 ? grp.runs + static_cast<size_t>(seg == 0 ? b.map_a : b.map_b) * grp.experts + w.expert
+                                                        : &grp.maps[2 + seg];
                         // gated forward: the even CTA (or the first half of the columns) holds the gate's rows, the
                         // other the up projection's, of the same d_ff columns
-                        const CUtensorMap* mb = kGated && CG == 2 && rank == 1 ? &grp.maps[3] : ma + 1;
-                        const CUtensorMap* mu = &grp.maps[3];
+                        const CUtensorMap* mb = &grp.maps[kGated && CG == 2 && rank == 1 ? 1 : seg];
+                        const CUtensorMap* mu = &grp.maps[1];
                         int k0 = from * kBK;
                         int b0 = bmn ? (b_flat ? col_b : 0) : k0, b1 = bmn ? k0 : col_b;
                         const int b2 = bmn && !b_flat ? col_b / 64 : 0;
@@ -387,7 +403,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
 #pragma unroll 1
                         for (int n = to - from; ok && n > 0; --n, k0 += kBK, b0 += db0, b1 += db1)
                             ok = slice([&](uint32_t bar, uint32_t a_dst, uint32_t b_dst) {
-                                tma_load_3d_cg<CG>(a_dst, ma, bar, k0, row_a, 0, keep);
+                                tma_load_3d_cg<CG>(a_dst, ma, bar, k0, map_row, 0, keep);
                                 tma_load_4d_cg<CG>(b_dst, mb, bar, b0, b1, b2, w.expert, pol_b);
                                 if (kGated && CG == 1)
                                     tma_load_4d_cg<CG>(b_dst + BN / 2 * 128, mu, bar, b0, b1, 0, w.expert, pol_b);
