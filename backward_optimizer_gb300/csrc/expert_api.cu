@@ -56,7 +56,7 @@ struct PlanArgs {
     RunOperand run[kMaxRuns];
 };
 
-// Inclusive scan over the block's 1024 threads.
+// Inclusive scan over the block's threads of values that are not negative; 0 is neutral.
 template <class Op>
 __device__ __forceinline__ int block_scan(int v, int* warps, Op op) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -68,7 +68,7 @@ __device__ __forceinline__ int block_scan(int v, int* warps, Op op) {
     if (lane == 31) warps[warp] = v;
     __syncthreads();
     if (warp == 0) {
-        int w = warps[lane];
+        int w = lane < static_cast<int>(blockDim.x >> 5) ? warps[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
             const int n = __shfl_up_sync(0xFFFFFFFFu, w, o);
@@ -82,11 +82,12 @@ __device__ __forceinline__ int block_scan(int v, int* warps, Op op) {
     return v;
 }
 
-// One block: thread e is expert e.  Offsets are brought into order and within the rows (an offset below the one
+// One block: thread e is expert e, and there are as many threads as there are experts, maps or tiles to deal out (up to
+// 1024).  Offsets are brought into order and within the rows (an offset below the one
 // before it, or past the last row, ends an empty or a shorter run), so that no later launch can leave the
 // tensors whatever they hold.
 __global__ void __launch_bounds__(1024) expert_plan_kernel(const __grid_constant__ PlanArgs a) {
-    __shared__ int warps[32], first[kMaxExperts], begin[kMaxExperts], end[kMaxExperts];
+    __shared__ int warps[32], first[kMaxExperts], begin[kMaxExperts], end[kMaxExperts], total;
     forge::stream_wait();
     const int e = threadIdx.x;
     const bool mine = e < a.experts;
@@ -102,10 +103,10 @@ __global__ void __launch_bounds__(1024) expert_plan_kernel(const __grid_constant
     first[e] = last - tiles;
     begin[e] = from;
     end[e] = to;
-    if (e == 1023) *a.n_tiles = last;
+    if (e + 1 == a.experts) total = *a.n_tiles = last;
     __syncthreads();
-    const int total = first[1023] + (end[1023] - begin[1023] + a.tile_rows - 1) / a.tile_rows;
-    for (int i = e; i < total; i += 1024) {
+    const int threads = static_cast<int>(blockDim.x);
+    for (int i = e; i < total; i += threads) {
         int lo = 0, hi = a.experts - 1;  // the last expert whose first tile is not behind tile i
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
@@ -122,8 +123,8 @@ __global__ void __launch_bounds__(1024) expert_plan_kernel(const __grid_constant
         const int from = parts > 1 ? all - rest : all;
         a.cuts[e] = make_int4(from, parts, from + (all - from) * parts, 0);
     }
-    for (int i = e; i < a.n_counts; i += 1024) a.counts[i] = 0u;
-    for (int i = e; i < a.n_runs * a.experts; i += 1024) {
+    for (int i = e; i < a.n_counts; i += threads) a.counts[i] = 0u;
+    for (int i = e; i < a.n_runs * a.experts; i += threads) {
         const int o = i / a.experts, x = i - o * a.experts;
         const uint4* src = reinterpret_cast<const uint4*>(&a.run[o].map);
         uint4* dst = reinterpret_cast<uint4*>(a.runs + i);
@@ -331,7 +332,9 @@ forge_status launch_plan(const Call& c, PlanArgs& a) {
     for (int i = 0; i < c.n_cuts; ++i) a.cut[i] = c.cut[i];
     a.counts = reinterpret_cast<uint32_t*>(c.ws + c.counts);
     a.n_counts = c.n_counts;
-    return cuda_status(host::launch_early(expert_plan_kernel, dim3(1), dim3(1024), 0, c.stream, a));
+    const int64_t work = std::max({c.experts * std::max<int64_t>(a.n_runs, 1), std::min<int64_t>(c.tiles, 1024), int64_t{a.n_counts / 4}});
+    const int64_t threads = std::min<int64_t>(1024, round_up(std::max<int64_t>(work, 64), 32));
+    return cuda_status(host::launch_early(expert_plan_kernel, dim3(1), dim3(static_cast<unsigned>(threads)), 0, c.stream, a));
 }
 
 // cut: which of the call's row products this is
