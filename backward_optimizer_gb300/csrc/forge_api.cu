@@ -694,9 +694,13 @@ forge_status expert_step(const void* dY, const void* X, const int* offsets, cons
         const forge_shape whole{0, experts * d_out, d_in, state, 0};
         return run_opt(nullptr, W, m, v, qscales, k, hp, &whole, step, seed, stream, *dev);
     }
-    // one layer's shape rule; experts together fill the GPU where one alone would not
-    const bool wide = (d_out % 256 == 0 || (d_out % 128 != 0 && d_out > 1024)) && (d_in % 256 == 0 || (d_in % 128 != 0 && d_in > 1024)) &&
-                      4 * experts * ceil_div(d_out, 256) * ceil_div(d_in, 256) > dev->num_sms;
+    // CTA pairs where all experts' tiles occupy over half of them and, but for INT8 states (whose epilogue has 16 warps on a
+    // pair), their edges waste less than a fifth.  us on single CTAs / pairs, AdamW, FP32, BF16, INT8 states: 64 experts,
+    // 1408 x 2048, 512 rows: 754 / 677, 786 / 762, 1622 / 904; 16 of 1920 x 1152, 2048 rows: 168 / 161, 178 / 175, 320 / 201;
+    // 16 of 1280 x 640: 75 / 76, 73 / 83, 110 / 84; 8 of 512 x 512, 64 rows: 30 / 31, 31 / 33, 35 / 33.
+    const int64_t tiles = ceil_div(d_out, 256) * ceil_div(d_in, 256);
+    const bool wide = 4 * experts * tiles > dev->num_sms &&
+                      (state == FORGE_STATE_INT8_B64 || 5 * tiles * 65536 < 6 * d_out * d_in);
     const TileShape ts = wide ? TileShape{256, 2} : TileShape{128, 1};
     forge::RaggedGroup g;
     g.n = 1;

@@ -145,3 +145,15 @@ def test_elements_past_32_bits():
     fg.dropout(x, x, 0.5, seed=11, step=5)
     for first in (0, (1 << 31) - 64, (1 << 32) - 64, n - 128):
         assert torch.equal(x[first:first + 128] == 0, _drops(128, 0.5, 11, 5, first))
+
+
+def test_gradient_against_differences():
+    """dropout is linear: dropout(x + d) - dropout(x) is what dropout_backward makes of d."""
+    gen = torch.Generator().manual_seed(9)
+    x, d = torch.randn(5000, generator=gen).cuda(), torch.randn(5000, generator=gen).cuda()
+    y, y2, dx = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    fg.dropout(x, y, 0.3, seed=4, step=2)
+    fg.dropout(x + d, y2, 0.3, seed=4, step=2)
+    fg.dropout_backward(d, dx, 0.3, seed=4, step=2)
+    # x + d, two products by the scale (below 1.5) and their difference are rounded to binary32
+    assert_close(dx, y2.to(F64) - y.to(F64), 8 * 2.0 ** -24 * (x.abs() + d.abs()).to(F64), "dx")

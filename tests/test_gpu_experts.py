@@ -228,3 +228,51 @@ def test_tensors_that_end_with_their_memory(D, F):
             want, tol = dense._gradients(_of(i, e, r), "silu")
             for got, c, t in zip((dX[r], *(w[e] for w in dW)), want, tol):
                 assert_close(got, c, (1 + U8) * t + U8 * c.abs(), f"expert {e}")
+
+
+def test_gradients_against_differences():
+    """Along random directions, in binary64, about the kernel's own inputs: d/dh of sum(C * block(inputs + h direction))."""
+    sizes, D, F = [9, 0, 70, 33], 64, 136
+    i = _gated_inputs(sizes, 0, 0, D, F, seed=5)
+    off, names = _offsets(sizes), ("X", "Wg", "Wu", "Wd")
+    C = i["dY"]
+
+    def value(v):
+        total = 0.0
+        for e, r in _runs(sizes):
+            g, u = v["X"][r] @ v["Wg"][e].T, v["X"][r] @ v["Wu"][e].T
+            total = total + (C[r].to(F64) * ((ref.act_both(g, "silu")[0] * u) @ v["Wd"][e].T)).sum()
+        return total
+    v = {n: i[n].to(F64) for n in names}
+    # the backward pass starts from G and U as the forward pass left them
+    _, i["G"], i["U"] = _forward(i, off, "silu")
+    got = dict(zip(names, _backward(i, off, "silu")))
+    gen = torch.Generator().manual_seed(6)
+    for n in names:
+        for e, r in _runs(sizes):
+            if r.stop == r.start:
+                continue
+            at = r if n == "X" else e
+            d = torch.zeros_like(v[n])
+            d[at] = torch.randn(d[at].shape, generator=gen, dtype=F64).cuda()
+            h = 1e-4
+            diff = (value({**v, n: v[n] + h * d}) - value({**v, n: v[n] - h * d})) / (2 * h)
+            own = (got[n][at].to(F64) * d[at]).sum()
+            # a random direction takes the square root of the sum of the elements' squared errors: each at most a few
+            # half steps of bf16 (the result, and dG, dU, H, G and U before it) of its own size; seven deviations
+            tol = 7 * 4 * U8 * (got[n][at].to(F64) * d[at]).square().sum().sqrt()
+            assert abs(diff - own) < tol, (n, e, diff.item(), own.item(), tol.item())
+    lin = {n: i[n].to(F64) for n in ("X",)} | {"W": i["Wg"].to(F64)}
+    dX, dW = _full(*i["X"].shape), _full(*i["Wg"].shape)
+    dZ = i["G"]
+    fg.expert_linear_backward(dZ, i["X"], i["Wg"], off, dX, dW)
+    for n, g in (("X", dX), ("W", dW)):
+        d = torch.randn(g.shape, generator=gen, dtype=F64).cuda()
+
+        def out(x, w):
+            return sum((dZ[r].to(F64) * (x[r] @ w[e].T)).sum() for e, r in _runs(sizes))
+        args = {"X": lin["X"], "W": lin["W"]}
+        up, down = {**args, n: args[n] + 1e-3 * d}, {**args, n: args[n] - 1e-3 * d}
+        diff = (out(up["X"], up["W"]) - out(down["X"], down["W"])) / 2e-3
+        own, tol = (g.to(F64) * d).sum(), 7 * 2 * U8 * (g.to(F64) * d).square().sum().sqrt()
+        assert abs(diff - own) < tol
