@@ -67,8 +67,10 @@ enum BlockAct : int { kActSilu = 0, kActGeluTanh = 1, kActRelu = 2 };
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Whether an epilogue's results go to memory through shared memory, on pairs (WarpOut).
-constexpr int kExpertGrad = 5;  // expert_kernel.cuh
-constexpr bool staged(int epi) { return epi == kBlockGatedFwd || epi == kBlockLossGrad || epi == kExpertGrad; }
+constexpr int kExpertGrad = 5, kExpertBoth = 6;  // expert_kernel.cuh
+constexpr bool staged(int epi) {
+    return epi == kBlockGatedFwd || epi == kBlockLossGrad || epi == kExpertGrad || epi == kExpertBoth;
+}
 
 template <int BN, int CG, int EPI>
 struct BlockCfg {

@@ -22,6 +22,7 @@ using forge::ExpertProblem;
 using forge::kBlockGatedBwd;
 using forge::kBlockGatedFwd;
 using forge::kBlockStore;
+using forge::kExpertBoth;
 using forge::kExpertGrad;
 
 constexpr int kMaxExperts = 1024;  // the plan gives each a thread of its one block
@@ -171,18 +172,52 @@ Tiling choose_rows(int64_t rows, int64_t experts) {
     return Tiling{128, each > 40 ? 128 : each > 4 ? 64 : 32};
 }
 
+// dW of up to three products: a and b, numbers of their run operands; each dW_e [d_out, d_in]
+struct GradProduct {
+    int a, b;
+    int64_t d_out, d_in;
+    void* out;
+};
+
+Tiling grad_tiling(const Machine& mc, int64_t experts, const GradProduct* p, int n) {
+    int64_t pairs = 0;
+    for (int i = 0; i < n; ++i) pairs += experts * ceil_div(p[i].d_out, 256) * ceil_div(p[i].d_in, 256);
+    return pairs >= mc.pairs ? Tiling{256, 256} : Tiling{128, 128};
+}
+
+// The tiles of a linear layer's backward pass that wants dX and dW, and whether one launch makes both: dX's units first,
+// the gradients' behind them and beside its last wave.  It does with short runs, where both have the same tiles;
+// experts of over 40 rows take pairs for that.  us in two launches / in one: 2048 rows of 32 experts, 1024 x 2048 66 / 62;
+// 1003 of 16, 1032 x 520 25 / 22; 200 of 3, 512 x 256 12.6 / 8.8; with long runs 30 / 33 (4096 of 4, 1024 x 1024).  The
+// gated block's dX has long units (its two products), which are better cut in a launch of their own (1003 rows of 16
+// experts, 520/1032: 60 us, 67 in one; 300 of 4, 1024/776 41 and 48).
+struct BackwardTiles {
+    Tiling rows, grads;
+    bool together;
+};
+BackwardTiles linear_tiles(const Machine& mc, const forge_expert_linear_shape& s) {
+    const GradProduct p{0, 0, s.d_out, s.d_in, nullptr};
+    BackwardTiles t{choose_rows(s.rows, s.experts), grad_tiling(mc, s.experts, &p, 1), false};
+    if (s.rows >= 256 * s.experts) return t;
+    if (t.grads.bn == 256 && s.rows > 40 * std::min(s.rows, s.experts)) t.rows = Tiling{256, 256};
+    t.together = t.rows.bn == t.grads.bn && t.rows.tile_rows >= 128;
+    return t;
+}
+
 // A row product of a call: its columns, those of a tile, and its reduction.
 struct RowSize {
     int64_t cols, k;
     bool gated, two;  // two: two operand pairs
+    bool beside;      // in the gradients' launch, whose units fill its last wave: not cut
 };
 
-Call make_call(const Machine& mc, int64_t rows, int64_t experts, int n_runs, std::initializer_list<RowSize> products, Arena& a) {
+Call make_call(const Machine& mc, int64_t rows, int64_t experts, const Tiling& tiling, int n_runs,
+               std::initializer_list<RowSize> products, Arena& a) {
     Call c{};
     c.mc = mc;
     c.rows = rows;
     c.experts = static_cast<int>(experts);
-    c.tiling = choose_rows(rows, experts);
+    c.tiling = tiling;
     const Tiling& t = c.tiling;
     c.tiles = rows / t.tile_rows + std::min(rows, experts);
     c.n_runs = n_runs;
@@ -195,7 +230,7 @@ Call make_call(const Machine& mc, int64_t rows, int64_t experts, int n_runs, std
     const int width = pair ? mc.pairs : mc.dev.num_sms;
     bool cut = false;
     for (const RowSize& p : products) {
-        const int kb = slices(p.k) * (p.two ? 2 : 1);
+        const int kb = p.beside ? 0 : slices(p.k) * (p.two ? 2 : 1);
         forge::ExpertCut& x = c.cut[c.n_cuts++];
         // joins as kTiles has them (block_api.cu)
         x = forge::ExpertCut{static_cast<int>(ceil_div(p.cols, p.gated ? t.bn / 2 : t.bn)), kb, width, pair ? 8 : 6, pair ? 12 : 5};
@@ -286,7 +321,7 @@ template <int EPI>
 forge_status set_result(ExpertGroup<EPI>& g, const Tiling& t, int i, void* base, int64_t experts, int64_t rows, int64_t cols) {
     g.to[i] = static_cast<uint16_t*>(base);
     if (!forge::staged(EPI) || t.bn != 256) return FORGE_OK;
-    const int box = EPI == kExpertGrad ? 64 : 32;
+    const int box = forge::expert_grads(EPI) ? 64 : 32;
     return kept_map(&g.outs[i], MapKey{base, cols, rows, cols, -box, 0, experts},
                     [&] { return host::encode_result_map(&g.outs[i], base, cols, rows, experts, box); });
 }
@@ -298,7 +333,7 @@ void begin_group(ExpertGroup<EPI>& g, const Call& c, int64_t kb_max) {
     std::memset(&g, 0, sizeof(g));
     g.n = 1;
     g.experts = c.experts;
-    g.a_rows = EPI == kExpertGrad ? 128 : c.tiling.tile_rows;
+    g.a_rows = forge::expert_grads(EPI) ? 128 : c.tiling.tile_rows;  // (row products beside gradients have tiles of 128 rows, or pairs)
     g.parts = reinterpret_cast<float*>(c.ws + c.parts);
     g.counts = reinterpret_cast<uint32_t*>(c.ws + c.counts);
     g.withhold_first_stage = host::take_withhold();
@@ -365,9 +400,8 @@ struct RowProduct {
 // Units of a row product at most.
 int64_t most_units(const Call& c, int cut) { return c.tiles * c.cut[cut].tiles_n + (c.n_counts > 0 ? c.cut[cut].width : 0); }
 
-forge_status run_rows(const Call& c, int cut, const RowProduct& p) {
-    ExpertGroup<kBlockStore> g;
-    begin_group(g, c, 2 * slices(p.k));
+template <int EPI>
+forge_status fill_rows(ExpertGroup<EPI>& g, const Call& c, int cut, const RowProduct& p) {
     set_rows(g, c, cut, p.cols, p.k, p.a[1] != nullptr ? p.k : 0);
     g.prob[0].map_a = p.run[0];
     g.prob[0].map_b = p.run[1];
@@ -378,21 +412,15 @@ forge_status run_rows(const Call& c, int cut, const RowProduct& p) {
         FORGE_TRY(weight_map(&g.maps[i], p.w[i], c.experts, p.mn ? p.k : p.cols, p.mn ? p.cols : p.k, p.mn,
                              b_extent(c.tiling, false)));
     }
-    FORGE_TRY(set_result(g, c.tiling, 0, p.out, 1, c.rows, p.cols));
-    return launch(g, c, c.tiling.bn, most_units(c, cut));
+    g.to[0] = static_cast<uint16_t*>(p.out);
+    return FORGE_OK;
 }
 
-// dW of up to three products: a and b, numbers of their run operands; each dW_e [d_out, d_in]
-struct GradProduct {
-    int a, b;
-    int64_t d_out, d_in;
-    void* out;
-};
-
-Tiling grad_tiling(const Machine& mc, int64_t experts, const GradProduct* p, int n) {
-    int64_t pairs = 0;
-    for (int i = 0; i < n; ++i) pairs += experts * ceil_div(p[i].d_out, 256) * ceil_div(p[i].d_in, 256);
-    return pairs >= mc.pairs ? Tiling{256, 256} : Tiling{128, 128};
+forge_status run_rows(const Call& c, int cut, const RowProduct& p) {
+    ExpertGroup<kBlockStore> g;
+    begin_group(g, c, 2 * slices(p.k));
+    FORGE_TRY(fill_rows(g, c, cut, p));
+    return launch(g, c, c.tiling.bn, most_units(c, cut));
 }
 
 // Neighbouring units of a pair or CTA.  A unit of another expert costs two fences on its maps: with short runs four units
@@ -403,13 +431,17 @@ int grad_chunk(const Call& c, int64_t units, int64_t each, int width) {
     return c.rows < 256ll * c.experts && units >= 16ll * width && each < 2ll * width ? 4 : 1;
 }
 
-forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int n) {
-    ExpertGroup<kExpertGrad> g;
-    begin_group(g, c, slices(c.rows));
-    g.n = n;
+// EPI: kExpertGrad, or kExpertBoth with dx, the call's first row product, in front of the gradients
+template <int EPI>
+forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int n, const RowProduct* dx) {
+    ExpertGroup<EPI> g;
+    begin_group(g, c, std::max(slices(c.rows), dx != nullptr ? 2 * slices(dx->k) : 0));
+    constexpr int first = forge::expert_first_grad(EPI);
+    g.n = first + n;
+    if constexpr (EPI == kExpertBoth) FORGE_TRY(fill_rows(g, c, 0, *dx));
     int64_t u = 0;
     for (int i = 0; i < n; ++i) {
-        ExpertProblem& b = g.prob[i];
+        ExpertProblem& b = g.prob[first + i];
         b.rows = static_cast<int>(p[i].d_out);
         b.cols = static_cast<int>(p[i].d_in);
         b.ld = p[i].d_in;
@@ -421,11 +453,11 @@ forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int
         b.map_a = p[i].a;
         b.map_b = p[i].b;
         u += static_cast<int64_t>(c.experts) * b.tiles_m * b.tiles_n;
-        FORGE_TRY(set_result(g, t, i, p[i].out, c.experts, p[i].d_out, p[i].d_in));
+        FORGE_TRY(set_result(g, t, first + i, p[i].out, c.experts, p[i].d_out, p[i].d_in));
     }
     g.n_units = static_cast<int>(u);
-    g.chunk = grad_chunk(c, u, static_cast<int64_t>(g.prob[0].tiles_m) * g.prob[0].tiles_n, t.bn == 256 ? c.mc.pairs : c.mc.dev.num_sms);
-    return launch(g, c, t.bn, u);
+    g.chunk = grad_chunk(c, u, static_cast<int64_t>(g.prob[first].tiles_m) * g.prob[first].tiles_n, t.bn == 256 ? c.mc.pairs : c.mc.dev.num_sms);
+    return launch(g, c, t.bn, u + (dx != nullptr ? c.tiles * g.prob[0].tiles_n : 0));
 }
 
 // ---------------------------------------------------------------- a linear layer for each expert
@@ -455,8 +487,13 @@ struct GatedSpace {
 GatedSpace layout_gated(const Machine& mc, const forge_expert_gated_shape& s, bool backward) {
     GatedSpace l{};
     Arena a;
-    if (backward) l.c = make_call(mc, s.rows, s.experts, kMaxRuns, {{s.d_ff, s.d_model, false, false}, {s.d_model, s.d_ff, false, true}}, a);
-    else l.c = make_call(mc, s.rows, s.experts, 2, {{s.d_ff, s.d_model, true, false}, {s.d_model, s.d_ff, false, false}}, a);
+    const Tiling rows = choose_rows(s.rows, s.experts);
+    if (backward)
+        l.c = make_call(mc, s.rows, s.experts, rows, kMaxRuns,
+                        {{s.d_ff, s.d_model, false, false, false}, {s.d_model, s.d_ff, false, true, false}}, a);
+    else
+        l.c = make_call(mc, s.rows, s.experts, rows, 2, {{s.d_ff, s.d_model, true, false, false}, {s.d_model, s.d_ff, false, false, false}},
+                        a);
     const int64_t bytes = s.rows * s.d_ff * 2;
     if (backward) {
         l.dg = a.take(bytes);
@@ -467,10 +504,10 @@ GatedSpace layout_gated(const Machine& mc, const forge_expert_gated_shape& s, bo
     return l;
 }
 
-int64_t linear_space(const Machine& mc, const forge_expert_linear_shape& s, bool backward, Call* c) {
+int64_t linear_space(const Machine& mc, const forge_expert_linear_shape& s, bool backward, const Tiling& rows, bool together, Call* c) {
     Arena a;
-    if (backward) *c = make_call(mc, s.rows, s.experts, 3, {{s.d_in, s.d_out, false, false}}, a);
-    else *c = make_call(mc, s.rows, s.experts, 1, {{s.d_out, s.d_in, false, false}}, a);
+    if (backward) *c = make_call(mc, s.rows, s.experts, rows, 3, {{s.d_in, s.d_out, false, false, together}}, a);
+    else *c = make_call(mc, s.rows, s.experts, rows, 1, {{s.d_out, s.d_in, false, false, false}}, a);
     return a.used;
 }
 
@@ -505,8 +542,8 @@ forge_status run_gated_dh(const GatedSpace& l, const forge_expert_gated_shape& s
     return launch(g, c, c.tiling.bn, most_units(c, 0));
 }
 
-forge_status run_gated_dx(const GatedSpace& l, const forge_expert_gated_shape& s, const void* Wg, const void* Wu, void* dX) {
-    return run_rows(l.c, 1, RowProduct{{l.c.ws + l.dg, l.c.ws + l.du}, {6, 7}, {Wg, Wu}, s.d_ff, s.d_model, true, dX});
+RowProduct gated_dx(const GatedSpace& l, const forge_expert_gated_shape& s, const void* Wg, const void* Wu, void* dX) {
+    return RowProduct{{l.c.ws + l.dg, l.c.ws + l.du}, {6, 7}, {Wg, Wu}, s.d_ff, s.d_model, true, dX};
 }
 
 forge_status zero(std::initializer_list<void*> ps, int64_t bytes, cudaStream_t stream) {
@@ -538,7 +575,11 @@ int64_t forge_expert_linear_workspace(const forge_expert_linear_shape* shape, in
     if (shape->rows == 0) return 0;
     if (machine(&mc) != FORGE_OK) return -1;
     Call c;
-    return linear_space(mc, *shape, backward != 0, &c);
+    const Tiling alone = choose_rows(shape->rows, shape->experts);
+    const int64_t n = linear_space(mc, *shape, backward != 0, alone, false, &c);
+    if (!backward) return n;
+    const BackwardTiles t = linear_tiles(mc, *shape);
+    return std::max(n, linear_space(mc, *shape, true, t.rows, t.together, &c));
 }
 
 forge_status forge_expert_linear(const void* X, const void* W, const int32_t* offsets, void* Y, void* workspace,
@@ -552,7 +593,7 @@ forge_status forge_expert_linear(const void* X, const void* W, const int32_t* of
     Call c;
     Machine mc;
     FORGE_TRY(machine(&mc));
-    FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, false, &c)));
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, false, choose_rows(s.rows, s.experts), false, &c)));
     c.ws = static_cast<char*>(workspace);
     c.stream = stream;
     c.offsets = offsets;
@@ -575,19 +616,23 @@ forge_status forge_expert_linear_backward(const void* dY, const void* X, const v
     Call c;
     Machine mc;
     FORGE_TRY(machine(&mc));
-    FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, true, &c)));
+    const bool both = dX != nullptr && dW != nullptr;
+    const GradProduct p{0, 1, s.d_out, s.d_in, dW};
+    BackwardTiles t = linear_tiles(mc, s);
+    if (!both) t = BackwardTiles{choose_rows(s.rows, s.experts), t.grads, false};
+    FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, true, t.rows, t.together, &c)));
     c.ws = static_cast<char*>(workspace);
     c.stream = stream;
     c.offsets = offsets;
-    const GradProduct p{0, 1, s.d_out, s.d_in, dW};
-    const Tiling t = grad_tiling(mc, s.experts, &p, 1);
     PlanArgs plan{};
     FORGE_TRY(run_operand(&plan.run[0], dY, s.d_out, 128));
-    FORGE_TRY(run_operand(&plan.run[1], X, s.d_in, b_extent(t, false)));
+    FORGE_TRY(run_operand(&plan.run[1], X, s.d_in, b_extent(t.grads, false)));
     FORGE_TRY(plan_rows(plan, c, 2, {{dY, s.d_out}}));
     FORGE_TRY(launch_plan(c, plan));
-    if (dX != nullptr) FORGE_TRY(run_rows(c, 0, RowProduct{{dY, nullptr}, {2, 0}, {W, nullptr}, s.d_out, s.d_in, true, dX}));
-    return dW != nullptr ? run_grads(c, t, &p, 1) : FORGE_OK;
+    const RowProduct dx{{dY, nullptr}, {2, 0}, {W, nullptr}, s.d_out, s.d_in, true, dX};
+    if (t.together) return run_grads<kExpertBoth>(c, t.grads, &p, 1, &dx);
+    if (dX != nullptr) FORGE_TRY(run_rows(c, 0, dx));
+    return dW != nullptr ? run_grads<kExpertGrad>(c, t.grads, &p, 1, nullptr) : FORGE_OK;
 }
 
 int64_t forge_expert_gated_mlp_workspace(const forge_expert_gated_shape* shape, int32_t backward) {
@@ -662,8 +707,8 @@ forge_status forge_expert_gated_mlp_backward(const void* dY, const void* X, cons
     FORGE_TRY(gated_runs(plan, l, s, dY, X, 128, b_extent(t, false)));
     FORGE_TRY(launch_plan(c, plan));
     FORGE_TRY(run_gated_dh(l, s, dY, G, U, Wd));
-    if (dX != nullptr) FORGE_TRY(run_gated_dx(l, s, Wg, Wu, dX));
-    return run_grads(c, t, p, 3);
+    if (dX != nullptr) FORGE_TRY(run_rows(c, 1, gated_dx(l, s, Wg, Wu, dX)));
+    return run_grads<kExpertGrad>(c, t, p, 3, nullptr);
 }
 
 forge_status forge_expert_linear_backward_step(const void* dY, const void* X, void* W, const int32_t* offsets, void* dX, void* m,
@@ -682,7 +727,7 @@ forge_status forge_expert_linear_backward_step(const void* dY, const void* X, vo
         FORGE_TRY(check_offsets(offsets));
         Machine mc;
         FORGE_TRY(machine(&mc));
-        FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, true, &c)));
+        FORGE_TRY(check_workspace(workspace, workspace_bytes, linear_space(mc, s, true, choose_rows(s.rows, s.experts), false, &c)));
         c.ws = static_cast<char*>(workspace);
         c.stream = stream;
         c.offsets = offsets;
@@ -733,7 +778,7 @@ forge_status forge_expert_gated_mlp_backward_step(const void* dY, const void* X,
         FORGE_TRY(launch_plan(c, plan));
         // the input gradients read the weights before the fused step replaces them: same stream, this order
         FORGE_TRY(run_gated_dh(l, s, dY, G, U, down->W));
-        if (dX != nullptr) FORGE_TRY(run_gated_dx(l, s, gate->W, up->W, dX));
+        if (dX != nullptr) FORGE_TRY(run_rows(c, 1, gated_dx(l, s, gate->W, up->W, dX)));
     }
     FORGE_TRY(run_step(c, 0, 3, c.ws + l.dg, X, s.rows, s.experts, layers[0], opt_kind, hp, state, step, stream));
     FORGE_TRY(run_step(c, 1, 3, c.ws + l.du, X, s.rows, s.experts, layers[1], opt_kind, hp, state, step, stream));

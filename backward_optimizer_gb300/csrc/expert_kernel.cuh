@@ -28,26 +28,31 @@
 
 namespace forge {
 
-// kExpertGrad beside BlockEpi's kBlockStore, kBlockGatedFwd and kBlockGatedBwd, whose A are rows by expert
-__host__ __device__ constexpr int expert_products(int epi) { return epi == kExpertGrad ? 3 : 1; }
+// Beside BlockEpi's kBlockStore, kBlockGatedFwd and kBlockGatedBwd, whose A are rows by expert: kExpertGrad, up to three
+// weights' gradients, and kExpertBoth, the same behind a row product (dX) in one launch.  (One kernel for both cost the
+// gradients alone 3 %: 512 rows of 64 experts, gated backward 2048/1408: 383 us against 370.)
+__host__ __device__ constexpr bool expert_grads(int epi) { return epi == kExpertGrad || epi == kExpertBoth; }
+// The first gradient's place among the products, and the products.
+__host__ __device__ constexpr int expert_first_grad(int epi) { return epi == kExpertBoth ? 1 : 0; }
+__host__ __device__ constexpr int expert_products(int epi) { return expert_grads(epi) ? expert_first_grad(epi) + 3 : 1; }
 
 struct ExpertProblem {
     int cols;             // of the result (gated forward: d_ff, a tile spans BN / 2 of them)
     int tiles_n;          // column tiles
-    int rows, tiles_m;    // kExpertGrad: rows of each expert's result, and their tiles
-    int unit_start;       // kExpertGrad: number of its first unit
+    int rows, tiles_m;    // gradients: rows of each expert's result, and their tiles
+    int unit_start;       // gradients: number of its first unit among theirs
     int kb[2];            // rows by expert: 64-deep reduction slices of the two operand pairs
     int a_flat, b_flat;   // MN-major and no multiple of 64 wide: a copy for each 64 columns
-    int b_mn;             // kBlockStore: W is read MN-major
-    int map_a, map_b;     // numbers of run maps: kExpertGrad's operands, or (pairs) the A of each operand pair
+    int b_mn;             // row products: W is read MN-major
+    int map_a, map_b;     // numbers of run maps: a gradient's operands, or (pairs) the A of each operand pair
     int64_t ld;           // the result's width
 };
 
 template <int EPI>
 struct ExpertGroup {
     int n;                // products
-    int n_units;          // kExpertGrad; else tiles_n times *n_tiles
-    int chunk;            // kExpertGrad: neighbouring units that a pair or CTA takes
+    int n_units;          // of gradients
+    int chunk;            // neighbouring units of gradients that a pair or CTA takes
     int experts;
     int a_rows;           // rows of A that a stage holds, and of a tile on single CTAs (128, 64 or 32)
     int stream_b;         // each weight is read by one row tile or few: leave it out of the L2
@@ -64,12 +69,12 @@ struct ExpertGroup {
     uint32_t* counts;     // their arrivals: zero before the launch and after it
     int* status;
     uint64_t wait_limit_ns, acc_wait_limit_ns;
-    uint16_t* to[3];      // results: kBlockStore's, kExpertGrad's of each product; G, U, H; dG, dU, H
+    uint16_t* to[expert_products(EPI) > 3 ? 4 : 3];  // results: kBlockStore's; of each product; G, U, H; dG, dU, H
     ExpertProblem prob[expert_products(EPI)];
     // rows by expert: the weights of each operand pair, or the gate's and the up projection's; then, on single CTAs, A of
     // each pair (on pairs: run maps)
     CUtensorMap maps[EPI == kExpertGrad ? 1 : 4];
-    CUtensorMap outs[staged(EPI) ? 3 : 1];  // staged results, on pairs
+    CUtensorMap outs[staged(EPI) ? (EPI == kExpertBoth ? 4 : 3) : 1];  // staged results, on pairs
 };
 
 struct ExpertUnit {
@@ -98,13 +103,31 @@ FORGE_HD int expert_parts(const ExpertCut& c, int rest) {
     return best;
 }
 
-// The units of a pair or CTA: `chunk` neighbours at a time, dealt out in turn.
+// The units of a pair or CTA: tiles of the row product one by one, then gradients, `chunk` neighbours at a time, beginning
+// with the pairs that the row product's last wave left without a tile.
+template <int EPI>
 struct ExpertWalk {
-    int u, left, chunk, jump;
-    __device__ __forceinline__ ExpertWalk(int pair, int pairs, int chunk_)
-        : u(pair * chunk_), left(chunk_), chunk(chunk_), jump(1 + (pairs - 1) * chunk_) {}
+    int u, left, jump, pairs;
+    int rows, pair, chunk;
+    __device__ __forceinline__ ExpertWalk(int pair_, int pairs_, int rows_, int chunk_)
+        : u(pair_), left(1), jump(1 + (pairs_ - 1) * chunk_), pairs(pairs_), rows(rows_), pair(pair_), chunk(chunk_) {
+        if (EPI == kExpertGrad) begin_grads(pair);
+        if (EPI == kExpertBoth && u >= rows) behind_rows();
+    }
+    __device__ __forceinline__ void begin_grads(int at) {
+        u = at * chunk;
+        left = chunk;
+    }
+    __device__ __forceinline__ void behind_rows() {
+        const int rest = rows % pairs;
+        begin_grads(pair >= rest ? pair - rest : pair - rest + pairs);
+        u += rows;
+    }
     __device__ __forceinline__ void next() {
-        if (--left > 0) {
+        if (!expert_grads(EPI) || (EPI == kExpertBoth && u < rows)) {
+            u += pairs;
+            if (EPI == kExpertBoth && u >= rows) behind_rows();
+        } else if (--left > 0) {
             ++u;
         } else {
             u += jump;
@@ -114,13 +137,14 @@ struct ExpertWalk {
 };
 
 template <int CG, int EPI>
-__device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int u, int n_tiles, int4 cut) {
+__device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int u, int n_tiles, int4 cut, int row_units) {
     ExpertUnit r;
     r.split = -1;
     r.part = r.k_first = 0;
     int mb;
-    if constexpr (EPI == kExpertGrad) {
-        r.prob = 0;
+    if (expert_grads(EPI) && (EPI == kExpertGrad || u >= row_units)) {
+        u -= row_units;
+        r.prob = expert_first_grad(EPI);
         while (r.prob + 1 < g.n && u >= g.prob[r.prob + 1].unit_start) ++r.prob;
         const ExpertProblem& b = g.prob[r.prob];
         const int t = u - b.unit_start, per = b.tiles_m * b.tiles_n;
@@ -163,7 +187,6 @@ struct ExpertOut {
     uint16_t* to[3];
     int64_t ld;
     int rows;      // one past the last row that may be written
-    int z;         // third coordinate of the tiled store: 0, or the expert of a weight's gradient
     uint32_t buf;
     int turn;
     template <int W>
@@ -183,7 +206,7 @@ struct ExpertOut {
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_3d(&maps[i], at, col, row0, z);
+                    tma_store_3d(&maps[i], at, col, row0, 0);
                     bulk_commit();
                 }
                 return;
@@ -257,7 +280,7 @@ template <int BN, int CG, int EPI>
 __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
     forge_expert_kernel(const __grid_constant__ ExpertGroup<EPI> grp) {
     using C = BlockCfg<BN, CG, EPI>;
-    constexpr bool kGated = EPI == kBlockGatedFwd, kGrad = EPI == kExpertGrad;
+    constexpr bool kGated = EPI == kBlockGatedFwd, kGrads = expert_grads(EPI), kRows = EPI != kExpertGrad;
     constexpr int kColsPerTile = kGated ? BN / 2 : BN;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -297,7 +320,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
         mbar_init(peer_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        if constexpr (!kGrad) {
+        if constexpr (kRows) {
             tma_prefetch_desc(&grp.maps[0]);
             if constexpr (kGated) tma_prefetch_desc(&grp.maps[1]);
             if constexpr (CG == 1) tma_prefetch_desc(&grp.maps[2]);
@@ -317,10 +340,10 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
     int64_t withheld = -1;
 
     stream_wait();
-    const int n_tiles = kGrad ? 0 : __ldcg(grp.n_tiles);
-    const int4 cut = kGrad ? make_int4(0, 0, 0, 0) : __ldcg(grp.cut);
-    const int n_units = kGrad ? grp.n_units : cut.z;
-    const int chunk = kGrad ? grp.chunk : 1;
+    const int n_tiles = kRows ? __ldcg(grp.n_tiles) : 0;
+    const int4 cut = kRows ? __ldcg(grp.cut) : make_int4(0, 1, 0, 0);
+    const int row_units = cut.z, n_units = row_units + (kGrads ? grp.n_units : 0);
+    const int chunk = kGrads ? grp.chunk : 1;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -349,12 +372,12 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                 return true;
             };
             int seen_prob = -1, seen_expert = -1;
-            for (ExpertWalk at(pair, pairs, chunk); ok && at.u < n_units; at.next()) {
-                const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut);
+            for (ExpertWalk<EPI> at(pair, pairs, row_units, chunk); ok && at.u < n_units; at.next()) {
+                const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut, row_units);
                 const ExpertProblem& b = grp.prob[w.prob];
                 const int row_a = w.row0 + static_cast<int>(rank) * kBM;
                 const int col_b = kGated ? w.nb * kColsPerTile : w.nb * BN + static_cast<int>(rank) * C::kBLoad;
-                if constexpr (kGrad) {
+                if (kGrads && (!kRows || at.u >= row_units)) {
                     const CUtensorMap* ma = grp.runs + static_cast<size_t>(b.map_a) * grp.experts + w.expert;
                     const CUtensorMap* mb = grp.runs + static_cast<size_t>(b.map_b) * grp.experts + w.expert;
                     if (w.prob != seen_prob || w.expert != seen_expert) {
@@ -376,16 +399,17 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                             if (b_flat) tma_load_3d_cg<CG>(b_dst + kBK * 128, mb, bar, b0 + 64, k0, 0, keep);
                         });
                 } else {
-                    const bool bmn = EPI == kBlockGatedBwd || (EPI == kBlockStore && b.b_mn != 0);
+                    const bool bmn = EPI == kBlockGatedBwd || (!kGated && b.b_mn != 0);
                     const bool b_flat = bmn && b.b_flat != 0;
                     if (CG == 2 && w.expert != seen_expert) {
                         tensormap_acquire(grp.runs + static_cast<size_t>(b.map_a) * grp.experts + w.expert);
                         if (b.kb[1] > 0) tensormap_acquire(grp.runs + static_cast<size_t>(b.map_b) * grp.experts + w.expert);
+                        seen_prob = 0;
                         seen_expert = w.expert;
                     }
                     const int map_row = CG == 2 ? row_a - w.begin : row_a;
 #pragma unroll 1
-                    for (int seg = 0; seg < (EPI == kBlockStore ? 2 : 1) && ok; ++seg) {
+                    for (int seg = 0; seg < (EPI == kBlockStore || kGrads ? 2 : 1) && ok; ++seg) {
                         // the unit's slices of this operand pair
                         const int base = seg == 0 ? 0 : b.kb[0];
                         const int from = w.k_first > base ? w.k_first - base : 0;
@@ -425,10 +449,10 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, issued_any = false;
-            for (ExpertWalk at(pair, pairs, chunk); ok && at.u < n_units; at.next()) {
-                const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut);
-                const bool amn = kGrad;
-                const bool bmn = kGrad || EPI == kBlockGatedBwd || (EPI == kBlockStore && grp.prob[0].b_mn != 0);
+            for (ExpertWalk<EPI> at(pair, pairs, row_units, chunk); ok && at.u < n_units; at.next()) {
+                const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut, row_units);
+                const bool amn = kGrads && (!kRows || at.u >= row_units);
+                const bool bmn = amn || EPI == kBlockGatedBwd || (!kGated && grp.prob[0].b_mn != 0);
                 const uint32_t idesc = idesc_bf16_f32(kBM * CG, BN, amn, bmn);
                 const uint32_t a_step = (amn ? 2048u : 32u) >> 4, b_step = (bmn ? 2048u : 32u) >> 4;
                 const uint64_t a_desc = smem_desc_sw128(smem_addr(sA), amn ? kBK * 128u : 16u, 1024);
@@ -467,10 +491,10 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
         const AbortCtx ab_acc{abort_flag, grp.status, grp.acc_wait_limit_ns};
         int acc = 0;
         uint32_t acc_phase = 0;
-        ExpertOut<(C::kStaging > 0)> out{grp.outs, {grp.to[0], grp.to[1], grp.to[2]}, 0, 0, 0,
+        ExpertOut<(C::kStaging > 0 && !kGrads)> out{grp.outs, {grp.to[0], grp.to[1], grp.to[2]}, 0, 0,
                                          smem_addr(staging) + static_cast<uint32_t>(e) * 4096u, 0};
-        for (ExpertWalk at(pair, pairs, chunk); at.u < n_units; at.next()) {
-            const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut);
+        for (ExpertWalk<EPI> at(pair, pairs, row_units, chunk); at.u < n_units; at.next()) {
+            const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut, row_units);
             const ExpertProblem& p = grp.prob[w.prob];
             const int row = w.row0 + static_cast<int>(rank) * kBM + quarter * 32 + lane;
             BlockProblem b;
@@ -486,11 +510,10 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             b.u_in = grp.u_in;
             out.ld = p.ld;
             out.rows = w.end;
-            if constexpr (kGrad) {
+            const bool grad = kGrads && (!kRows || at.u >= row_units);
+            if constexpr (kGrads) {
                 const size_t each = static_cast<size_t>(p.rows) * static_cast<size_t>(p.ld);
-                out.to[0] = grp.to[w.prob] + each * static_cast<size_t>(w.expert);
-                out.maps = grp.outs + w.prob;
-                out.z = w.expert;
+                out.to[0] = grp.to[w.prob] + (grad ? each * static_cast<size_t>(w.expert) : 0);
             }
             int ok = 1;
             if (lane == 0) ok = wait_bounded(&acc_full[acc], acc_phase, ab_acc) ? 1 : 0;
@@ -501,14 +524,18 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             auto epilogue = [&](const auto& acc_from) {
                 if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, acc_from, row, w.nb, half, out);
                 else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, acc_from, row, w.nb, half, out);
-                else if constexpr (kGrad && C::kStaging > 0) epi_expert_grad<BN>(b, acc_from, row, w.nb, half, out.maps, out.z, out.buf);
-                else epi_store<BN>(b, acc_from, row, w.nb, half, out);
+                else if constexpr (kGrads && C::kStaging > 0) {
+                    if (grad) epi_expert_grad<BN>(b, acc_from, row, w.nb, half, grp.outs + w.prob, w.expert, out.buf);
+                    else epi_store<BN>(b, acc_from, row, w.nb, half, out);
+                } else {
+                    epi_store<BN>(b, acc_from, row, w.nb, half, out);
+                }
             };
             // [cut tile][part][CTA][lane quarter][column][lane]; quarters past the tile's rows are not there
             const size_t quarters = CG == 1 ? a_rows / 32 : 4;
             const size_t step = static_cast<size_t>(CG) * quarters * BN * 32;
             const size_t own = (static_cast<size_t>(rank) * quarters + quarter) * BN * 32 + lane;
-            const bool whole = kGrad || w.split < 0;
+            const bool whole = kGrads || w.split < 0;
             if (whole) epilogue(tm);
             else if (warp_row0(row) < b.rows) {
                 float* to = grp.parts + (static_cast<size_t>(w.split) * cut.y + w.part) * step + own;
@@ -550,6 +577,9 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                     epilogue(AccParts{grp.parts + static_cast<size_t>(w.split) * cut.y * step + own, step, cut.y, row < b.rows});
                 }
             }
+        }
+        if constexpr (kGrads && C::kStaging > 0) {
+            if (lane == 0) bulk_wait_read<0>();
         }
         out.end();
     }
