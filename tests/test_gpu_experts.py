@@ -7,6 +7,7 @@ import backward_optimizer_gb300 as fg
 from tests import operators_reference as ref
 from tests import test_gpu_gated as dense
 from tests.operators_reference import F64, U8, acc, assert_close
+from workloads import Hparams
 
 pytestmark = pytest.mark.gpu
 
@@ -276,3 +277,81 @@ def test_gradients_against_differences():
         diff = (out(up["X"], up["W"]) - out(down["X"], down["W"])) / 2e-3
         own, tol = (g.to(F64) * d).sum(), 7 * 2 * U8 * (g.to(F64) * d).square().sum().sqrt()
         assert abs(diff - own) < tol
+
+
+@pytest.mark.parametrize("experts, rows", [(1024, 1), (1024, 700), (1000, 5000), (1, 4097)])
+def test_many_experts_and_one(experts, rows):
+    gen = torch.Generator().manual_seed(10)
+    D, F = 64, 72
+    cuts = torch.randint(0, rows + 1, (experts - 1,), generator=gen).sort().values.tolist()
+    sizes = [b - a for a, b in zip([0] + cuts, cuts + [rows])]
+    X, dY, W = _tensor(gen, rows, D), _tensor(gen, rows, F), _tensor(gen, experts, F, D, std=D ** -0.5)
+    off = _offsets(sizes)
+    Y, dX, dW = _full(rows, F), _full(rows, D), _full(experts, F, D)
+    fg.expert_linear(X, W, off, Y)
+    fg.expert_linear_backward(dY, X, W, off, dX, dW)
+    assert fg.sync_status() == 0
+    which = torch.repeat_interleave(torch.arange(experts), torch.tensor(sizes)).cuda()
+    x, d, w = X.to(F64), dY.to(F64), W.to(F64)
+    # binary32 sums of 64 and 72 products: far inside one more half step of bf16
+    y = torch.einsum("rd,rfd->rf", x, w[which])
+    g = torch.einsum("rf,rfd->rd", d, w[which])
+    h = torch.zeros(experts, F, D, dtype=F64, device="cuda")
+    for e, r in _runs(sizes):
+        if r.stop > r.start:
+            h[e] = d[r].T @ x[r]
+    for got, c, k, name in ((Y, y, D, "Y"), (dX, g, F, "dX"), (dW, h, rows, "dW")):
+        assert_close(got, c, U8 * c.abs() + (1 + U8) * acc(c, k), name)
+
+
+def test_rows_and_weights_past_32_bits():
+    """Element numbers over 2^32 in X and dX (rows) and in W and dW (experts): the last rows and the last experts."""
+    D, F = 8192, 64
+    sizes = [260000, 0, 300000, 5, 40]
+    R, E = sum(sizes), len(sizes)
+    X = torch.zeros(R, D, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator().manual_seed(11)
+    tail = _tensor(gen, 45, D)
+    X[-45:] = tail
+    W, dY = _tensor(gen, E, F, D, std=D ** -0.5), torch.zeros(R, F, dtype=torch.bfloat16, device="cuda")
+    dY[-45:] = _tensor(gen, 45, F)
+    off = _offsets(sizes)
+    Y, dX, dW = _full(R, F), _full(R, D), _full(E, F, D)
+    fg.expert_linear(X, W, off, Y)
+    fg.expert_linear_backward(dY, X, W, off, dX, dW)
+    assert fg.sync_status() == 0
+    assert not Y[:-45].any() and not dX[:-45].any() and not dW[:3].any()
+    for e, r in ((3, slice(R - 45, R - 40)), (4, slice(R - 40, R))):
+        x, d, w = X[r].to(F64), dY[r].to(F64), W[e].to(F64)
+        for got, c, k, name in ((Y[r], x @ w.T, D, "Y"), (dX[r], d @ w, F, "dX"), (dW[e], d.T @ x, 64, "dW")):
+            assert_close(got, c, U8 * c.abs() + (1 + U8) * acc(c, k), f"{name} of expert {e}")
+    del X, dY, Y, dX
+    E, D, F = 70, 8192, 8192
+    sizes = [0] * E
+    sizes[0], sizes[68], sizes[69] = 3, 40, 90
+    R = sum(sizes)
+    W = torch.zeros(E, F, D, dtype=torch.bfloat16, device="cuda")
+    for e in (0, 68, 69):
+        W[e] = _tensor(gen, F, D, std=D ** -0.5)
+    X, dY, off = _tensor(gen, R, D), _tensor(gen, R, F, std=0.1), _offsets(sizes)
+    Y, dX, dW = _full(R, F), _full(R, D), _full(E, F, D)
+    fg.expert_linear(X, W, off, Y)
+    fg.expert_linear_backward(dY, X, W, off, dX, dW)
+    m = torch.zeros(E, F, D, dtype=torch.bfloat16, device="cuda")
+    old = W[69].clone()
+    fg.expert_linear_backward_step(dY, X, W, off, None, m, None, None, opt="sgd_momentum",
+                                   hp=Hparams(lr=1.0, momentum=0.0, weight_decay=0.0), step=1)
+    assert fg.sync_status() == 0
+    assert not dW[1:68].any() and not m[1:68].any()
+    for e, r in _runs(sizes):
+        if r.stop == r.start:
+            continue
+        x, d = X[r].to(F64), dY[r].to(F64)
+        w = (old if e == 69 else W[e]).to(F64)
+        if e == 69:
+            for got, c, k, name in ((Y[r], x @ w.T, D, "Y"), (dX[r], d @ w, F, "dX")):
+                assert_close(got, c, U8 * c.abs() + (1 + U8) * acc(c, k), f"{name} of expert {e}")
+        c = d.T @ x
+        assert_close(dW[e], c, U8 * c.abs() + (1 + U8) * acc(c, 128), f"dW of expert {e}")
+        # the moment is the gradient, rounded stochastically: a whole step
+        assert_close(m[e], c, 2 * U8 * c.abs() + (1 + 2 * U8) * acc(c, 128), f"m of expert {e}")
