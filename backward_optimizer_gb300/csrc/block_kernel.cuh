@@ -67,12 +67,9 @@ enum BlockAct : int { kActSilu = 0, kActGeluTanh = 1, kActRelu = 2 };
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Whether an epilogue's results go to memory through shared memory, on pairs (WarpOut).
-constexpr int kExpertGrad = 5, kExpertBoth = 6;  // expert_kernel.cuh
-constexpr bool staged(int epi) {
-    return epi == kBlockGatedFwd || epi == kBlockLossGrad || epi == kExpertGrad || epi == kExpertBoth;
-}
+constexpr bool staged(int epi) { return epi == kBlockGatedFwd || epi == kBlockLossGrad; }
 
-template <int BN, int CG, int EPI>
+template <int BN, int CG, int EPI, bool STAGED = CG == 2 && staged(EPI)>
 struct BlockCfg {
     static_assert((BN == 256 && CG == 2) || ((BN == 128 || BN == 64) && CG == 1), "tile shapes");
     static constexpr int kBLoad = BN / CG;  // B rows (or columns) staged by this CTA
@@ -83,7 +80,7 @@ struct BlockCfg {
     static constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, half the columns each
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
     // two 2 KiB buffers per epilogue warp, 32 rows x 32 columns of bfloat16 each, on their way to memory
-    static constexpr int kStaging = CG == 2 && staged(EPI) ? kEpiWarps * 4096 : 0;
+    static constexpr int kStaging = STAGED ? kEpiWarps * 4096 : 0;
     static constexpr int kStages = (7 * 32768 - kStaging) / kStageBytes;
     static constexpr int kRingBytes = kStages * kStageBytes;
     // where A has few rows (BlockGroup::a_rows) its slices are smaller and the ring holds more stages

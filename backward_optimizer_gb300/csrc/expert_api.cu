@@ -230,13 +230,13 @@ Call make_call(const Machine& mc, int64_t rows, int64_t experts, const Tiling& t
     const int width = pair ? mc.pairs : mc.dev.num_sms;
     bool cut = false;
     for (const RowSize& p : products) {
-        const int kb = p.beside ? 0 : slices(p.k) * (p.two ? 2 : 1);
+        const int kb = p.beside || pair ? 0 : slices(p.k) * (p.two ? 2 : 1);  // pairs' tiles are not cut
         forge::ExpertCut& x = c.cut[c.n_cuts++];
         // joins as kTiles has them (block_api.cu)
-        x = forge::ExpertCut{static_cast<int>(ceil_div(p.cols, p.gated ? t.bn / 2 : t.bn)), kb, width, pair ? 8 : 6, pair ? 12 : 5};
+        x = forge::ExpertCut{static_cast<int>(ceil_div(p.cols, p.gated ? t.bn / 2 : t.bn)), kb, width, 6, 5};
         cut = cut || forge::expert_parts(x, 1) > 1;
     }
-    c.n_counts = cut ? width * (pair ? 2 : 1) * 8 : 0;
+    c.n_counts = cut ? width * 8 : 0;
     c.counts = a.take(c.n_counts * 4ll);
     c.parts = a.take(cut ? static_cast<int64_t>(width) * t.tile_rows * t.bn * 4 : 0);
     return c;
@@ -316,14 +316,13 @@ forge_status run_operand(RunOperand* o, const void* base, int64_t cols, int exte
     });
 }
 
-// Result i of a staged epilogue, [experts, rows, cols] in one piece (rows by expert: experts = 1).
+// Gradient i, [experts, rows, cols].
 template <int EPI>
-forge_status set_result(ExpertGroup<EPI>& g, const Tiling& t, int i, void* base, int64_t experts, int64_t rows, int64_t cols) {
+forge_status set_gradient(ExpertGroup<EPI>& g, const Tiling& t, int i, void* base, int64_t experts, int64_t rows, int64_t cols) {
     g.to[i] = static_cast<uint16_t*>(base);
-    if (!forge::staged(EPI) || t.bn != 256) return FORGE_OK;
-    const int box = forge::expert_grads(EPI) ? 64 : 32;
-    return kept_map(&g.outs[i], MapKey{base, cols, rows, cols, -box, 0, experts},
-                    [&] { return host::encode_result_map(&g.outs[i], base, cols, rows, experts, box); });
+    if (t.bn != 256) return FORGE_OK;
+    return kept_map(&g.outs[i], MapKey{base, cols, rows, cols, 4, 0, experts},
+                    [&] { return host::encode_result_map(&g.outs[i], base, cols, rows, experts); });
 }
 
 // ---------------------------------------------------------------- launches
@@ -385,7 +384,8 @@ void set_rows(ExpertGroup<EPI>& g, const Call& c, int cut, int64_t cols, int64_t
     g.stream_b = c.tiling.tile_rows < 128;
 }
 
-int b_extent(const Tiling& t, bool gated) { return t.bn == 256 ? 128 : gated ? t.bn / 2 : t.bn; }
+// Of the weights, the rows or columns that a CTA stages a slice.
+constexpr int kWeightExtent = 128, kGatedExtent = 64;
 
 // out [rows, cols] = A0 W0 (+ A1 W1): W_e [cols, k] as it is read in y = x W^T, or [k, cols] (mn)
 struct RowProduct {
@@ -410,7 +410,7 @@ forge_status fill_rows(ExpertGroup<EPI>& g, const Call& c, int cut, const RowPro
     for (int i = 0; i < 2 && p.a[i] != nullptr; ++i) {
         if (c.tiling.bn != 256) FORGE_TRY(rows_map(&g.maps[2 + i], c, p.a[i], p.k));
         FORGE_TRY(weight_map(&g.maps[i], p.w[i], c.experts, p.mn ? p.k : p.cols, p.mn ? p.cols : p.k, p.mn,
-                             b_extent(c.tiling, false)));
+                             kWeightExtent));
     }
     g.to[0] = static_cast<uint16_t*>(p.out);
     return FORGE_OK;
@@ -453,7 +453,7 @@ forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int
         b.map_a = p[i].a;
         b.map_b = p[i].b;
         u += static_cast<int64_t>(c.experts) * b.tiles_m * b.tiles_n;
-        FORGE_TRY(set_result(g, t, first + i, p[i].out, c.experts, p[i].d_out, p[i].d_in));
+        FORGE_TRY(set_gradient(g, t, first + i, p[i].out, c.experts, p[i].d_out, p[i].d_in));
     }
     g.n_units = static_cast<int>(u);
     g.chunk = grad_chunk(c, u, static_cast<int64_t>(g.prob[first].tiles_m) * g.prob[first].tiles_n, t.bn == 256 ? c.mc.pairs : c.mc.dev.num_sms);
@@ -534,11 +534,11 @@ forge_status run_gated_dh(const GatedSpace& l, const forge_expert_gated_shape& s
     g.g_in = static_cast<const uint16_t*>(G);
     g.u_in = static_cast<const uint16_t*>(U);
     const int64_t outs[3] = {l.dg, l.du, l.h};
-    for (int i = 0; i < 3; ++i) FORGE_TRY(set_result(g, c.tiling, i, c.ws + outs[i], 1, s.rows, s.d_ff));
+    for (int i = 0; i < 3; ++i) g.to[i] = reinterpret_cast<uint16_t*>(c.ws + outs[i]);
     g.prob[0].b_flat = s.d_ff % 64 != 0;
     g.prob[0].map_a = 5;
     if (c.tiling.bn != 256) FORGE_TRY(rows_map(&g.maps[2], c, dY, s.d_model));
-    FORGE_TRY(weight_map(&g.maps[0], Wd, s.experts, s.d_model, s.d_ff, true, b_extent(c.tiling, false)));
+    FORGE_TRY(weight_map(&g.maps[0], Wd, s.experts, s.d_model, s.d_ff, true, kWeightExtent));
     return launch(g, c, c.tiling.bn, most_units(c, 0));
 }
 
@@ -626,7 +626,7 @@ forge_status forge_expert_linear_backward(const void* dY, const void* X, const v
     c.offsets = offsets;
     PlanArgs plan{};
     FORGE_TRY(run_operand(&plan.run[0], dY, s.d_out, 128));
-    FORGE_TRY(run_operand(&plan.run[1], X, s.d_in, b_extent(t.grads, false)));
+    FORGE_TRY(run_operand(&plan.run[1], X, s.d_in, 128));
     FORGE_TRY(plan_rows(plan, c, 2, {{dY, s.d_out}}));
     FORGE_TRY(launch_plan(c, plan));
     const RowProduct dx{{dY, nullptr}, {2, 0}, {W, nullptr}, s.d_out, s.d_in, true, dX};
@@ -670,12 +670,12 @@ forge_status forge_expert_gated_mlp(const void* X, const void* Wg, const void* W
     g.act = s.act;
     g.keep = G != nullptr;
     if (g.keep) {
-        FORGE_TRY(set_result(g, c.tiling, 0, G, 1, s.rows, s.d_ff));
-        FORGE_TRY(set_result(g, c.tiling, 1, U, 1, s.rows, s.d_ff));
+        g.to[0] = static_cast<uint16_t*>(G);
+        g.to[1] = static_cast<uint16_t*>(U);
     }
-    FORGE_TRY(set_result(g, c.tiling, 2, c.ws + l.h, 1, s.rows, s.d_ff));
+    g.to[2] = reinterpret_cast<uint16_t*>(c.ws + l.h);
     if (c.tiling.bn != 256) FORGE_TRY(rows_map(&g.maps[2], c, X, s.d_model));
-    const int extent = b_extent(c.tiling, true);
+    const int extent = kGatedExtent;
     FORGE_TRY(weight_map(&g.maps[0], Wg, s.experts, s.d_ff, s.d_model, false, extent));
     FORGE_TRY(weight_map(&g.maps[1], Wu, s.experts, s.d_ff, s.d_model, false, extent));
     FORGE_TRY(launch(g, c, c.tiling.bn, most_units(c, 0)));
@@ -704,7 +704,7 @@ forge_status forge_expert_gated_mlp_backward(const void* dY, const void* X, cons
     const GradProduct p[3] = {{0, 3, s.d_ff, s.d_model, dWg}, {1, 3, s.d_ff, s.d_model, dWu}, {2, 4, s.d_model, s.d_ff, dWd}};
     const Tiling t = grad_tiling(mc, s.experts, p, 3);
     PlanArgs plan{};
-    FORGE_TRY(gated_runs(plan, l, s, dY, X, 128, b_extent(t, false)));
+    FORGE_TRY(gated_runs(plan, l, s, dY, X, 128, 128));
     FORGE_TRY(launch_plan(c, plan));
     FORGE_TRY(run_gated_dh(l, s, dY, G, U, Wd));
     if (dX != nullptr) FORGE_TRY(run_rows(c, 1, gated_dx(l, s, Wg, Wu, dX)));

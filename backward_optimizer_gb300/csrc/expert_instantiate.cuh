@@ -10,7 +10,7 @@ namespace forge {
 
 template <int BN, int CG, int EPI>
 cudaError_t launch_expert_as(const void* group, int units, cudaStream_t stream) {
-    using C = BlockCfg<BN, CG, EPI>;
+    using C = ExpertCfg<BN, CG, EPI>;
     static std::atomic<uint64_t> configured{0};  // one bit per device ordinal
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);

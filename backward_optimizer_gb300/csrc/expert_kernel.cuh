@@ -28,6 +28,7 @@
 
 namespace forge {
 
+constexpr int kExpertGrad = 5, kExpertBoth = 6;
 // Beside BlockEpi's kBlockStore, kBlockGatedFwd and kBlockGatedBwd, whose A are rows by expert: kExpertGrad, up to three
 // weights' gradients, and kExpertBoth, the same behind a row product (dX) in one launch.  (One kernel for both cost the
 // gradients alone 3 %: 512 rows of 64 experts, gated backward 2048/1408: 383 us against 370.)
@@ -35,6 +36,10 @@ __host__ __device__ constexpr bool expert_grads(int epi) { return epi == kExpert
 // The first gradient's place among the products, and the products.
 __host__ __device__ constexpr int expert_first_grad(int epi) { return epi == kExpertBoth ? 1 : 0; }
 __host__ __device__ constexpr int expert_products(int epi) { return expert_grads(epi) ? expert_first_grad(epi) + 3 : 1; }
+
+// On pairs every epilogue works in shared memory: 4 KiB a warp.
+template <int BN, int CG, int EPI>
+using ExpertCfg = BlockCfg<BN, CG, EPI, CG == 2>;
 
 struct ExpertProblem {
     int cols;             // of the result (gated forward: d_ff, a tile spans BN / 2 of them)
@@ -44,7 +49,7 @@ struct ExpertProblem {
     int kb[2];            // rows by expert: 64-deep reduction slices of the two operand pairs
     int a_flat, b_flat;   // MN-major and no multiple of 64 wide: a copy for each 64 columns
     int b_mn;             // row products: W is read MN-major
-    int map_a, map_b;     // numbers of run maps: a gradient's operands, or (pairs) the A of each operand pair
+    int map_a, map_b;     // numbers of run maps: a gradient's operands, or (pairs) the rows of each operand pair
     int64_t ld;           // the result's width
 };
 
@@ -71,10 +76,10 @@ struct ExpertGroup {
     uint64_t wait_limit_ns, acc_wait_limit_ns;
     uint16_t* to[expert_products(EPI) > 3 ? 4 : 3];  // results: kBlockStore's; of each product; G, U, H; dG, dU, H
     ExpertProblem prob[expert_products(EPI)];
-    // rows by expert: the weights of each operand pair, or the gate's and the up projection's; then, on single CTAs, A of
-    // each pair (on pairs: run maps)
+    // rows by expert: the weights of each operand pair, or the gate's and the up projection's; then, on single CTAs, the
+    // rows of each pair (on pairs: run maps)
     CUtensorMap maps[EPI == kExpertGrad ? 1 : 4];
-    CUtensorMap outs[staged(EPI) ? (EPI == kExpertBoth ? 4 : 3) : 1];  // staged results, on pairs
+    CUtensorMap outs[expert_products(EPI)];  // gradients on pairs
 };
 
 struct ExpertUnit {
@@ -136,6 +141,9 @@ struct ExpertWalk {
     }
 };
 
+// Rows of a row product's tile on a pair, as the MMA takes them.
+__device__ __forceinline__ int expert_width(const ExpertUnit& w) { return (w.end - w.row0 + 31) / 32 * 32; }
+
 template <int CG, int EPI>
 __device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int u, int n_tiles, int4 cut, int row_units) {
     ExpertUnit r;
@@ -178,67 +186,184 @@ __device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int
     return r;
 }
 
-// A warp's results on their way to memory, as WarpOut: 32 rows x 32 columns at a time.  Staged, a warp whose 32
-// rows all belong to the tile's expert takes a tiled store; one that holds the last rows of a run writes them by
-// its lanes, since a store of the whole box would reach into the next expert's rows.
-template <bool kStaged>
-struct ExpertOut {
-    const CUtensorMap* maps;
-    uint16_t* to[3];
-    int64_t ld;
-    int rows;      // one past the last row that may be written
-    uint32_t buf;
-    int turn;
-    template <int W>
-    __device__ __forceinline__ void put(int i, const uint32_t (&v)[W], int col, int row0) {
-        const uint32_t lane = threadIdx.x & 31u;
-        if constexpr (kStaged) {
-            static_assert(W == 16);
-            if (row0 + 32 <= rows) {
-                if (lane == 0) bulk_wait_read<1>();  // the buffer's last store has read it
-                __syncwarp();
-                const uint32_t at = buf + (static_cast<uint32_t>(turn) << 11);
-                turn ^= 1;
+// ---------------------------------------------------------------- row products on pairs
+// The weights are the MMA's A (256 columns of the result, 128 a CTA) and the rows its B, whose width is any multiple
+// of 32: the last tile of a run is as wide as the run's rest, not as a whole tile.  So a warp's lanes are columns of the
+// result and the accumulator's columns its rows, 32 at a time; results (and G and U on their way in) change sides in
+// the warp's 4 KiB of shared memory, 32 rows of 64 bytes at a time, where both sides' accesses are free of conflicts.
+
+__device__ __forceinline__ void st_shared_b16(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(v)) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_b16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// A block of up to 32 rows x 32 columns of a matrix [.., ld] in memory: this warp's columns from col on.
+struct ExpertBlock {
+    uint32_t buf;      // 2 KiB of shared memory: row j's 32 columns at 64 j
+    int row, rows;     // first row, and one past the last that there is
+    int col, ld;
+    // The block's first N rows out of shared memory (every lane's writes done).
+    template <int N>
+    __device__ __forceinline__ void write(uint16_t* to) const {
+        const int lane = static_cast<int>(threadIdx.x & 31u), c = 8 * (lane & 3);
 #pragma unroll
-                for (uint32_t j = 0; j < 4; ++j)
-                    st_shared_v4(at + lane * 64u + ((j ^ ((lane >> 1) & 3u)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2],
-                                 v[4 * j + 3]);
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_3d(&maps[i], at, col, row0, 0);
-                    bulk_commit();
-                }
-                return;
-            }
-        }
-        if (row0 + static_cast<int>(lane) < rows) {
-            uint16_t* p = to[i] + (static_cast<size_t>(row0) + lane) * ld + col;
-            const int left = static_cast<int>(ld) - col;
-            const bool wide = (ld & 15) == 0;
-#pragma unroll
-            for (int h = 0; h < W / 8; ++h) {
-                if (wide && left >= 16 * h + 16) {
-                    const uint32_t r[8] = {v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3],
-                                           v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]};
-                    st_v8(p + 16 * h, r);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint32_t r[4] = {v[8 * h + 4 * q], v[8 * h + 4 * q + 1], v[8 * h + 4 * q + 2],
-                                               v[8 * h + 4 * q + 3]};
-                        if (left >= 16 * h + 8 * q + 8) st_v4(p + 16 * h + 8 * q, r);
-                    }
-                }
-            }
+        for (int k = 0; k < N / 8; ++k) {
+            const int r = (lane >> 2) + 8 * k;
+            uint32_t v[4];
+            ld_shared_v4(buf + static_cast<uint32_t>(r * 64 + 2 * c), v);
+            if (row + r < rows && col + c < ld) st_v4(to + static_cast<size_t>(row + r) * ld + col + c, v);
         }
     }
-    __device__ __forceinline__ void end() {
-        if constexpr (kStaged) {
-            if ((threadIdx.x & 31u) == 0) bulk_wait_read<0>();
+    __device__ __forceinline__ void read(const uint16_t* from, uint32_t (&v)[4][4]) const {
+        const int lane = static_cast<int>(threadIdx.x & 31u), c = 8 * (lane & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = (lane >> 2) + 8 * k;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[k][i] = 0u;
+            if (row + r < rows && col + c < ld) ld_v4(from + static_cast<size_t>(row + r) * ld + col + c, v[k]);
         }
     }
+    __device__ __forceinline__ void keep(const uint32_t (&v)[4][4]) const {
+        const int lane = static_cast<int>(threadIdx.x & 31u), c = 8 * (lane & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st_shared_v4(buf + static_cast<uint32_t>(((lane >> 2) + 8 * k) * 64 + 2 * c), v[k][0], v[k][1], v[k][2], v[k][3]);
+    }
+    // This lane's column of row j.
+    __device__ __forceinline__ uint32_t at(int j) const { return buf + static_cast<uint32_t>(64 * j + 2 * (threadIdx.x & 31)); }
+    __device__ __forceinline__ void put(int j, float v) const { st_shared_b16(at(j), pack_bf16x2_rn(__float_as_uint(v), 0u)); }
 };
+
+// rows: of the tile; blocks of 32 of them go to the two warps of a lane quarter in turn
+struct ExpertTile {
+    int row0, rows, col, cols;
+    int first, step;  // this warp's first row of the tile, and from block to block
+};
+
+template <class Acc>
+__device__ __forceinline__ void epi_rows_store(const ExpertTile& t, const Acc& acc, uint16_t* to, uint32_t buf) {
+    if (t.col >= t.cols) return;
+#pragma unroll 1
+    for (int j = t.first; j < t.rows; j += t.step) {
+        uint32_t g[32];
+        acc.load(j, g);
+        const ExpertBlock b{buf, t.row0 + j, t.row0 + t.rows, t.col, t.cols};
+        __syncwarp();  // the last block has been read
+#pragma unroll
+        for (int i = 0; i < 32; ++i) b.put(i, __uint_as_float(g[i]));
+        __syncwarp();
+        b.template write<32>(to);
+    }
+}
+
+// The activation is the same for a launch: code of its own for each leaves a branch a block instead of one an element
+// (gated forward, 4096 rows of 16 experts, 1024/2816: 94 us with it, 105 without).
+template <class F>
+__device__ __forceinline__ auto with_act(int act, F&& f) {
+    if (act == kActSilu) return f(std::integral_constant<int, kActSilu>{});
+    if (act == kActGeluTanh) return f(std::integral_constant<int, kActGeluTanh>{});
+    return f(std::integral_constant<int, kActRelu>{});
+}
+
+template <int ACT, class Acc>
+__device__ __forceinline__ void epi_rows_gated_bwd(const ExpertTile& t, const Acc& acc, const uint16_t* g_in, const uint16_t* u_in,
+                                                   uint16_t* dg, uint16_t* du, uint16_t* h, uint32_t buf) {
+    if (t.col >= t.cols) return;
+#pragma unroll 1
+    for (int j = t.first; j < t.rows; j += t.step) {
+        const ExpertBlock a{buf, t.row0 + j, t.row0 + t.rows, t.col, t.cols}, b{buf + 2048u, t.row0 + j, t.row0 + t.rows, t.col, t.cols};
+        uint32_t g[4][4], u[4][4];
+        a.read(g_in, g);
+        b.read(u_in, u);
+        uint32_t d[32], hs[16];
+        acc.load(j, d);
+        __syncwarp();  // the last block has been read
+        a.keep(g);
+        b.keep(u);
+        __syncwarp();
+        // each lane's places in the two buffers are its own from here on: dG and dU take those of G and U
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float gv = __uint_as_float(ld_shared_b16(a.at(i)) << 16), uv = __uint_as_float(ld_shared_b16(b.at(i)) << 16);
+            const float dh = __uint_as_float(d[i]);
+            float value, slope;
+            act_both(gv, ACT, value, slope);
+            a.put(i, dh * uv * slope);
+            b.put(i, dh * value);
+            const uint32_t r = pack_bf16x2_rn(__float_as_uint(value * uv), 0u);
+            hs[i / 2] = i % 2 == 0 ? r : hs[i / 2] | r << 16;
+        }
+        __syncwarp();
+        a.template write<32>(dg);
+        b.template write<32>(du);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) st_shared_b16(a.at(i), hs[i / 2] >> (16 * (i % 2)));
+        __syncwarp();
+        a.template write<32>(h);
+    }
+}
+
+// Whether two warps that meet inside a tile's epilogue both run it: the first to come to tile `no` decides for both, so that
+// neither waits for one that has given up.  The word counts the tiles that are to be run (a warp with no columns to make may be
+// some ahead of the other: it meets nobody), or says that the rest are left.  Each warp calls it once a tile until it answers 0.
+__device__ __forceinline__ int expert_agree(uint32_t* word, uint32_t no, int ok) {
+    const uint32_t run = no + 1, leave = 0xFFFFFFFFu;
+    const uint32_t before = atomicCAS(word, no, ok ? run : leave);
+    return before == no ? ok : before != leave;
+}
+
+// G and U of the same columns are in the lanes of two warps (quarters 0 and 2, 1 and 3), which trade 16 rows of each
+// block and make H of 16 rows each.  They meet on a barrier of theirs (`meeting`) when their rows are in shared memory and
+// again when they have read the other's; that both run the tile is settled before (expert_agree).
+template <int ACT, class Acc>
+__device__ __forceinline__ void epi_rows_gated_fwd(const ExpertTile& t, const Acc& acc, bool is_up, bool keep, uint16_t* own,
+                                                   uint16_t* h, uint32_t buf, uint32_t other, int meeting) {
+    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(meeting) : "memory"); };
+    const uint32_t lane = threadIdx.x & 31u, mine = buf + 2048u + 4u * lane, theirs = other + 2048u + 4u * lane;
+    const bool inside = t.col < t.cols;  // the same for both warps
+#pragma unroll 1
+    for (int j = t.first; j < t.rows; j += t.step) {
+        uint32_t v[32];
+        acc.load(j, v);
+        const ExpertBlock b{buf, t.row0 + j, t.row0 + t.rows, t.col, t.cols};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st_shared_f32(mine + 128u * i, __uint_as_float(is_up ? v[i] : v[16 + i]));
+        meet();
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = ld_shared_f32(theirs + 128u * i);
+        meet();
+        if (!inside) continue;
+        if (keep) {
+            __syncwarp();  // the last block has been read
+#pragma unroll
+            for (int i = 0; i < 32; ++i) b.put(i, __uint_as_float(v[i]));
+            __syncwarp();
+            b.template write<32>(own);
+        }
+        // H is rounded to bfloat16, the type of the next product's operand
+        const ExpertBlock c{buf, b.row + (is_up ? 16 : 0), b.rows, t.col, t.cols};
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            c.put(i, is_up ? act_value(x[i], ACT) * __uint_as_float(v[16 + i]) : act_value(__uint_as_float(v[i]), ACT) * x[i]);
+        __syncwarp();
+        c.template write<16>(h);
+    }
+}
 
 // The weights' gradients on pairs leave in boxes of 32 rows x 64 columns, whole 128-byte lines: what a store's copy
 // engine takes a row of a box, not a byte, sets the pace of tiles with few slices (2048 rows of 32 experts, 1024 x 2048
@@ -277,9 +402,9 @@ __device__ __forceinline__ void epi_expert_grad(const BlockProblem& b, const Acc
 }
 
 template <int BN, int CG, int EPI>
-__global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
+__global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
     forge_expert_kernel(const __grid_constant__ ExpertGroup<EPI> grp) {
-    using C = BlockCfg<BN, CG, EPI>;
+    using C = ExpertCfg<BN, CG, EPI>;
     constexpr bool kGated = EPI == kBlockGatedFwd, kGrads = expert_grads(EPI), kRows = EPI != kExpertGrad;
     constexpr int kColsPerTile = kGated ? BN / 2 : BN;
     extern __shared__ uint8_t smem_raw[];
@@ -298,7 +423,8 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
     uint64_t* drain = acc_empty + 2;
     uint64_t* peer_done = drain + 1;
     uint64_t* peer_count = peer_done + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(peer_count + 1);
+    uint32_t* agreed = reinterpret_cast<uint32_t*>(peer_count + 1);  // by the two warps that hold G and U of the same columns
+    uint32_t* tmem_slot = agreed + 4;
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -318,6 +444,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
         }
         mbar_init(drain, 1);
         mbar_init(peer_done, 1);
+        for (int i = 0; i < 4; ++i) agreed[i] = 0u;
         *abort_flag = 0;
         fence_mbar_init();
         if constexpr (kRows) {
@@ -398,27 +525,46 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                             if (a_flat) tma_load_3d_cg<CG>(a_dst + kBK * 128, ma, bar, a0 + 64, k0, 0, keep);
                             if (b_flat) tma_load_3d_cg<CG>(b_dst + kBK * 128, mb, bar, b0 + 64, k0, 0, keep);
                         });
+                } else if constexpr (CG == 2) {
+                    // the weights' 128 columns of the result, or 64 of the gate's rows and 64 of the up projection's
+                    const bool wmn = EPI == kBlockGatedBwd || (!kGated && b.b_mn != 0), w_flat = wmn && b.b_flat != 0;
+                    const int col = w.nb * kColsPerTile + static_cast<int>(rank) * (kColsPerTile / 2);
+                    const int map_row = w.row0 - w.begin + static_cast<int>(rank) * (expert_width(w) / 2);
+                    if (w.prob != seen_prob || w.expert != seen_expert) {
+                        tensormap_acquire(grp.runs + static_cast<size_t>(b.map_a) * grp.experts + w.expert);
+                        if (b.kb[1] > 0) tensormap_acquire(grp.runs + static_cast<size_t>(b.map_b) * grp.experts + w.expert);
+                        seen_prob = w.prob;
+                        seen_expert = w.expert;
+                    }
+#pragma unroll 1
+                    for (int seg = 0; seg < (EPI == kBlockStore || kGrads ? 2 : 1) && ok; ++seg) {
+                        const CUtensorMap* mr = grp.runs + static_cast<size_t>(seg == 0 ? b.map_a : b.map_b) * grp.experts + w.expert;
+                        const CUtensorMap* mw = &grp.maps[seg];
+                        const CUtensorMap* mu = &grp.maps[1];
+                        int k0 = 0, w0 = wmn ? (w_flat ? col : 0) : 0, w1 = wmn ? 0 : col;
+                        const int w2 = wmn && !w_flat ? col / 64 : 0, dw0 = wmn ? 0 : kBK, dw1 = wmn ? kBK : 0;
+#pragma unroll 1
+                        for (int n = b.kb[seg]; ok && n > 0; --n, k0 += kBK, w0 += dw0, w1 += dw1)
+                            ok = slice([&](uint32_t bar, uint32_t a_dst, uint32_t b_dst) {
+                                tma_load_4d_cg<CG>(a_dst, mw, bar, w0, w1, w2, w.expert, pol_b);
+                                tma_load_3d_cg<CG>(b_dst, mr, bar, k0, map_row, 0, keep);
+                                if (kGated) tma_load_4d_cg<CG>(a_dst + 64 * 128, mu, bar, w0, w1, 0, w.expert, pol_b);
+                                if (!kGated && w_flat) tma_load_4d_cg<CG>(a_dst + kBK * 128, mw, bar, w0 + 64, w1, 0, w.expert, pol_b);
+                            });
+                    }
                 } else {
                     const bool bmn = EPI == kBlockGatedBwd || (!kGated && b.b_mn != 0);
                     const bool b_flat = bmn && b.b_flat != 0;
-                    if (CG == 2 && w.expert != seen_expert) {
-                        tensormap_acquire(grp.runs + static_cast<size_t>(b.map_a) * grp.experts + w.expert);
-                        if (b.kb[1] > 0) tensormap_acquire(grp.runs + static_cast<size_t>(b.map_b) * grp.experts + w.expert);
-                        seen_prob = 0;
-                        seen_expert = w.expert;
-                    }
-                    const int map_row = CG == 2 ? row_a - w.begin : row_a;
 #pragma unroll 1
                     for (int seg = 0; seg < (EPI == kBlockStore || kGrads ? 2 : 1) && ok; ++seg) {
                         // the unit's slices of this operand pair
                         const int base = seg == 0 ? 0 : b.kb[0];
                         const int from = w.k_first > base ? w.k_first - base : 0;
                         const int to = (w.k_end < base + b.kb[seg] ? w.k_end : base + b.kb[seg]) - base;
-                        const CUtensorMap* ma = CG == 2 ? grp.runs + static_cast<size_t>(seg == 0 ? b.map_a : b.map_b) * grp.experts + w.expert
-                                                        : &grp.maps[2 + seg];
-                        // gated forward: the even CTA (or the first half of the columns) holds the gate's rows, the
-                        // other the up projection's, of the same d_ff columns
-                        const CUtensorMap* mb = &grp.maps[kGated && CG == 2 && rank == 1 ? 1 : seg];
+                        const CUtensorMap* ma = &grp.maps[2 + seg];
+                        // gated forward: the first half of the columns holds the gate's rows, the other the up
+                        // projection's, of the same d_ff columns
+                        const CUtensorMap* mb = &grp.maps[seg];
                         const CUtensorMap* mu = &grp.maps[1];
                         int k0 = from * kBK;
                         int b0 = bmn ? (b_flat ? col_b : 0) : k0, b1 = bmn ? k0 : col_b;
@@ -427,10 +573,9 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
 #pragma unroll 1
                         for (int n = to - from; ok && n > 0; --n, k0 += kBK, b0 += db0, b1 += db1)
                             ok = slice([&](uint32_t bar, uint32_t a_dst, uint32_t b_dst) {
-                                tma_load_3d_cg<CG>(a_dst, ma, bar, k0, map_row, 0, keep);
+                                tma_load_3d_cg<CG>(a_dst, ma, bar, k0, row_a, 0, keep);
                                 tma_load_4d_cg<CG>(b_dst, mb, bar, b0, b1, b2, w.expert, pol_b);
-                                if (kGated && CG == 1)
-                                    tma_load_4d_cg<CG>(b_dst + BN / 2 * 128, mu, bar, b0, b1, 0, w.expert, pol_b);
+                                if (kGated) tma_load_4d_cg<CG>(b_dst + BN / 2 * 128, mu, bar, b0, b1, 0, w.expert, pol_b);
                                 if (!kGated && b_flat)
                                     tma_load_4d_cg<CG>(b_dst + kBK * 128, mb, bar, b0 + 64, b1, 0, w.expert, pol_b);
                             });
@@ -451,9 +596,10 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             bool ok = true, issued_any = false;
             for (ExpertWalk<EPI> at(pair, pairs, row_units, chunk); ok && at.u < n_units; at.next()) {
                 const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut, row_units);
-                const bool amn = kGrads && (!kRows || at.u >= row_units);
-                const bool bmn = amn || EPI == kBlockGatedBwd || (!kGated && grp.prob[0].b_mn != 0);
-                const uint32_t idesc = idesc_bf16_f32(kBM * CG, BN, amn, bmn);
+                const bool grad = kGrads && (!kRows || at.u >= row_units), swapped = CG == 2 && !grad;
+                const bool wmn = EPI == kBlockGatedBwd || (!kGated && grp.prob[0].b_mn != 0);  // the weights' order
+                const bool amn = grad || (swapped && wmn), bmn = grad || (!swapped && wmn);
+                const uint32_t idesc = idesc_bf16_f32(kBM * CG, swapped ? expert_width(w) : BN, amn, bmn);
                 const uint32_t a_step = (amn ? 2048u : 32u) >> 4, b_step = (bmn ? 2048u : 32u) >> 4;
                 const uint64_t a_desc = smem_desc_sw128(smem_addr(sA), amn ? kBK * 128u : 16u, 1024);
                 const uint64_t b_desc = smem_desc_sw128(smem_addr(sB), bmn ? kBK * 128u : 16u, 1024);
@@ -491,8 +637,10 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
         const AbortCtx ab_acc{abort_flag, grp.status, grp.acc_wait_limit_ns};
         int acc = 0;
         uint32_t acc_phase = 0;
-        ExpertOut<(C::kStaging > 0 && !kGrads)> out{grp.outs, {grp.to[0], grp.to[1], grp.to[2]}, 0, 0,
-                                         smem_addr(staging) + static_cast<uint32_t>(e) * 4096u, 0};
+        WarpOut<false> out{nullptr, grp.to, 0, 0, 0, 0};
+        uint16_t* grad_to[1];
+        const uint32_t buf = smem_addr(staging) + static_cast<uint32_t>(e) * 4096u;
+        uint32_t tile_no = 0;
         for (ExpertWalk<EPI> at(pair, pairs, row_units, chunk); at.u < n_units; at.next()) {
             const ExpertUnit w = expert_unit<CG, EPI>(grp, at.u, n_tiles, cut, row_units);
             const ExpertProblem& p = grp.prob[w.prob];
@@ -513,10 +661,15 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             const bool grad = kGrads && (!kRows || at.u >= row_units);
             if constexpr (kGrads) {
                 const size_t each = static_cast<size_t>(p.rows) * static_cast<size_t>(p.ld);
-                out.to[0] = grp.to[w.prob] + (grad ? each * static_cast<size_t>(w.expert) : 0);
+                grad_to[0] = grp.to[w.prob] + (grad ? each * static_cast<size_t>(w.expert) : 0);
+                out.to = grad_to;
             }
             int ok = 1;
-            if (lane == 0) ok = wait_bounded(&acc_full[acc], acc_phase, ab_acc) ? 1 : 0;
+            if (lane == 0) {
+                ok = wait_bounded(&acc_full[acc], acc_phase, ab_acc) ? 1 : 0;
+                if constexpr (kGated && CG == 2) ok = expert_agree(&agreed[2 * half + (quarter & 1)], tile_no, ok);
+            }
+            ++tile_no;
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
             if (!ok) break;
             tc_fence_after();
@@ -524,20 +677,37 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
             auto epilogue = [&](const auto& acc_from) {
                 if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, acc_from, row, w.nb, half, out);
                 else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, acc_from, row, w.nb, half, out);
-                else if constexpr (kGrads && C::kStaging > 0) {
-                    if (grad) epi_expert_grad<BN>(b, acc_from, row, w.nb, half, grp.outs + w.prob, w.expert, out.buf);
-                    else epi_store<BN>(b, acc_from, row, w.nb, half, out);
-                } else {
-                    epi_store<BN>(b, acc_from, row, w.nb, half, out);
-                }
+                else epi_store<BN>(b, acc_from, row, w.nb, half, out);
             };
-            // [cut tile][part][CTA][lane quarter][column][lane]; quarters past the tile's rows are not there
-            const size_t quarters = CG == 1 ? a_rows / 32 : 4;
-            const size_t step = static_cast<size_t>(CG) * quarters * BN * 32;
-            const size_t own = (static_cast<size_t>(rank) * quarters + quarter) * BN * 32 + lane;
-            const bool whole = kGrads || w.split < 0;
-            if (whole) epilogue(tm);
-            else if (warp_row0(row) < b.rows) {
+            if constexpr (CG == 2) {
+                const int col = w.nb * kColsPerTile + static_cast<int>(rank) * (kColsPerTile / 2) + (kGated ? quarter & 1 : quarter) * 32;
+                const ExpertTile t{w.row0, w.end - w.row0, col, p.cols, half * 32, 64};
+                if constexpr (kGrads) {
+                    if (grad) epi_expert_grad<BN>(b, tm, row, w.nb, half, grp.outs + w.prob, w.expert, buf);
+                    else epi_rows_store(t, tm, grp.to[0], buf);
+                } else if constexpr (EPI == kBlockGatedFwd) {
+                    const bool is_up = quarter >= 2;
+                    const uint32_t other = smem_addr(staging) + static_cast<uint32_t>(half * 4 + quarter) * 4096u;
+                    with_act(grp.act, [&](auto a) {
+                        epi_rows_gated_fwd<decltype(a)::value>(t, tm, is_up, grp.keep != 0, grp.to[is_up ? 1 : 0], grp.to[2], buf, other,
+                                                               1 + 2 * half + (quarter & 1));
+                    });
+                } else if constexpr (EPI == kBlockGatedBwd) {
+                    with_act(grp.act, [&](auto a) {
+                        epi_rows_gated_bwd<decltype(a)::value>(t, tm, grp.g_in, grp.u_in, grp.to[0], grp.to[1], grp.to[2], buf);
+                    });
+                } else {
+                    epi_rows_store(t, tm, grp.to[0], buf);
+                }
+            }
+            // (single CTAs) [cut tile][part][lane quarter][column][lane]; quarters past the tile's rows are not there
+            const size_t step = static_cast<size_t>(a_rows / 32) * BN * 32;
+            const size_t own = static_cast<size_t>(quarter) * BN * 32 + lane;
+            const bool whole = CG == 2 || kGrads || w.split < 0;
+            if (CG == 2) {
+            } else if (whole) {
+                epilogue(tm);
+            } else if (warp_row0(row) < b.rows) {
                 float* to = grp.parts + (static_cast<size_t>(w.split) * cut.y + w.part) * step + own;
                 // the columns whose epilogue this warp runs: gate and up columns come from both halves
                 constexpr int kRuns = kGated ? 2 : 1, kRun = BN / 2 / kRuns, kStep = kRun < 32 ? kRun : 32;
@@ -568,7 +738,7 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                 __threadfence();
                 __syncwarp();
                 uint32_t before = 0;
-                uint32_t* count = grp.counts + (w.split * CG + static_cast<int>(rank)) * C::kEpiWarps + e;
+                uint32_t* count = grp.counts + w.split * C::kEpiWarps + e;
                 if (lane == 0) before = atomicAdd(count, 1u);
                 before = __shfl_sync(0xFFFFFFFFu, before, 0);
                 if (before + 1 == static_cast<uint32_t>(cut.y)) {
@@ -578,10 +748,9 @@ __global__ void __launch_bounds__(BlockCfg<BN, CG, EPI>::kThreads, 1)
                 }
             }
         }
-        if constexpr (kGrads && C::kStaging > 0) {
-            if (lane == 0) bulk_wait_read<0>();
+        if constexpr (kGrads && CG == 2) {
+            if (lane == 0) bulk_wait_read<0>();  // shared memory stays until the last stores have read it
         }
-        out.end();
     }
 
     tc_fence_before();

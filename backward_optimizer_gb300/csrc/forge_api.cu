@@ -627,12 +627,12 @@ forge_status encode_map(CUtensorMap* map, const void* base, const uint64_t (&dim
                : FORGE_ERR_CUDA;
 }
 
-forge_status encode_result_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t n, int box_cols) {
+forge_status encode_result_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t n) {
     const cuuint64_t d[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(n)};
     const cuuint64_t st[2] = {static_cast<cuuint64_t>(cols * 2), static_cast<cuuint64_t>(rows * cols * 2)};
-    const cuuint32_t bx[3] = {static_cast<cuuint32_t>(box_cols), 32, 1}, one[3] = {1, 1, 1};
+    const cuuint32_t bx[3] = {64, 32, 1}, one[3] = {1, 1, 1};
     return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, d, st, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? FORGE_OK
                : FORGE_ERR_CUDA;

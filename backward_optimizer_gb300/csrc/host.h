@@ -29,9 +29,9 @@ forge_status encode_map(CUtensorMap* map, const void* base, const uint64_t (&dim
 forge_status encode_map(CUtensorMap* map, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
                         const uint32_t (&box)[4]);
 
-// Tensor map of row-major bfloat16 results [n, rows, cols] in one piece, written in boxes of 32 rows and 32 or 64
-// columns with the swizzle of their 64 or 128 bytes.
-forge_status encode_result_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t n, int box_cols);
+// Tensor map of row-major bfloat16 results [n, rows, cols] in one piece, written in boxes of 32 rows and 64
+// columns with the 128-byte swizzle.
+forge_status encode_result_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t n);
 
 // Tensor map of a row-major bfloat16 result [rows, cols] in one piece, written in boxes of 32 x 32 with the
 // 64-byte swizzle.
