@@ -27,8 +27,7 @@ using forge::kExpertGrad;
 
 constexpr int kMaxExperts = 1024;  // the plan gives each a thread of its one block
 constexpr int kMaxCuts = 2;        // row products of a call
-constexpr int kMaxRuns = 8;        // operands that end with a run of rows: dG, dU, dY, X, H of gradients; dY, dG, dU of row
-                                   // products on pairs
+constexpr int kMaxRuns = 5;        // operands of gradients, which end with a run of rows: dG, dU, dY, X, H
 
 int slices(int64_t k) { return static_cast<int>(ceil_div(k, forge::kBK)); }
 
@@ -115,7 +114,7 @@ __global__ void __launch_bounds__(1024) expert_plan_kernel(const __grid_constant
             else hi = mid - 1;
         }
         const int row = begin[lo] + (i - first[lo]) * a.tile_rows;
-        a.tiles[i] = make_int4(lo, row, min(row + a.tile_rows, end[lo]), begin[lo]);
+        a.tiles[i] = make_int4(lo, row, min(row + a.tile_rows, end[lo]), 0);
     }
     if (e < a.n_cuts) {
         const forge::ExpertCut& c = a.cut[e];
@@ -257,35 +256,11 @@ forge_status check_rows(int64_t rows, int64_t experts, int64_t d_in, int64_t d_o
 
 // Rows by expert: A [rows, cols], K-major.
 forge_status rows_map(CUtensorMap* map, const Call& c, const void* base, int64_t cols) {
-    const int extent = c.tiling.tile_rows;
+    const int extent = std::min(c.tiling.tile_rows, 128);  // of a CTA: on pairs half of the tile
     return kept_map(map, MapKey{base, cols, c.rows, cols, 0, extent}, [&] {
         const uint64_t k = static_cast<uint64_t>(cols), r = static_cast<uint64_t>(c.rows);
         return host::encode_map(map, base, {k, r, 1}, {2 * k, 2 * k}, {64, static_cast<uint32_t>(extent), 1});
     });
-}
-
-// The same on pairs: a map that the plan makes one of each run.
-forge_status rows_operand(RunOperand* o, const void* base, int64_t cols) {
-    o->base = static_cast<const char*>(base);
-    o->pitch = cols * 2;
-    o->dim0 = static_cast<uint32_t>(cols);
-    o->dim2 = 1;
-    return kept_map(&o->map, MapKey{base, cols, 1, cols, 3, 128}, [&] {
-        const uint64_t pitch = static_cast<uint64_t>(cols) * 2;
-        return host::encode_map(&o->map, base, {64, 1, 1}, {pitch, pitch}, {64, 128, 1});
-    });
-}
-
-// A of the call's row products, as they need it: run operands behind the `first` ones (pairs), or nothing yet
-struct RowsOperand {
-    const void* base;
-    int64_t cols;
-};
-forge_status plan_rows(PlanArgs& plan, const Call& c, int first, std::initializer_list<RowsOperand> as) {
-    plan.n_runs = first;
-    if (c.tiling.bn != 256) return FORGE_OK;
-    for (const RowsOperand& a : as) FORGE_TRY(rows_operand(&plan.run[plan.n_runs++], a.base, a.cols));
-    return FORGE_OK;
 }
 
 // The weights [experts, rows, cols], of which a CTA stages `extent` rows (K-major) or columns (MN-major) a slice.
@@ -390,7 +365,6 @@ constexpr int kWeightExtent = 128, kGatedExtent = 64;
 // out [rows, cols] = A0 W0 (+ A1 W1): W_e [cols, k] as it is read in y = x W^T, or [k, cols] (mn)
 struct RowProduct {
     const void* a[2];
-    int run[2];  // their numbers as run operands
     const void* w[2];
     int64_t k, cols;
     bool mn;
@@ -403,12 +377,10 @@ int64_t most_units(const Call& c, int cut) { return c.tiles * c.cut[cut].tiles_n
 template <int EPI>
 forge_status fill_rows(ExpertGroup<EPI>& g, const Call& c, int cut, const RowProduct& p) {
     set_rows(g, c, cut, p.cols, p.k, p.a[1] != nullptr ? p.k : 0);
-    g.prob[0].map_a = p.run[0];
-    g.prob[0].map_b = p.run[1];
     g.prob[0].b_mn = p.mn;
     g.prob[0].b_flat = p.mn && p.cols % 64 != 0;
     for (int i = 0; i < 2 && p.a[i] != nullptr; ++i) {
-        if (c.tiling.bn != 256) FORGE_TRY(rows_map(&g.maps[2 + i], c, p.a[i], p.k));
+        FORGE_TRY(rows_map(&g.maps[2 + i], c, p.a[i], p.k));
         FORGE_TRY(weight_map(&g.maps[i], p.w[i], c.experts, p.mn ? p.k : p.cols, p.mn ? p.cols : p.k, p.mn,
                              kWeightExtent));
     }
@@ -492,8 +464,8 @@ GatedSpace layout_gated(const Machine& mc, const forge_expert_gated_shape& s, bo
         l.c = make_call(mc, s.rows, s.experts, rows, kMaxRuns,
                         {{s.d_ff, s.d_model, false, false, false}, {s.d_model, s.d_ff, false, true, false}}, a);
     else
-        l.c = make_call(mc, s.rows, s.experts, rows, 2, {{s.d_ff, s.d_model, true, false, false}, {s.d_model, s.d_ff, false, false, false}},
-                        a);
+        l.c = make_call(mc, s.rows, s.experts, rows, 0,
+                        {{s.d_ff, s.d_model, true, false, false}, {s.d_model, s.d_ff, false, false, false}}, a);
     const int64_t bytes = s.rows * s.d_ff * 2;
     if (backward) {
         l.dg = a.take(bytes);
@@ -506,8 +478,8 @@ GatedSpace layout_gated(const Machine& mc, const forge_expert_gated_shape& s, bo
 
 int64_t linear_space(const Machine& mc, const forge_expert_linear_shape& s, bool backward, const Tiling& rows, bool together, Call* c) {
     Arena a;
-    if (backward) *c = make_call(mc, s.rows, s.experts, rows, 3, {{s.d_in, s.d_out, false, false, together}}, a);
-    else *c = make_call(mc, s.rows, s.experts, rows, 1, {{s.d_out, s.d_in, false, false, false}}, a);
+    if (backward) *c = make_call(mc, s.rows, s.experts, rows, 2, {{s.d_in, s.d_out, false, false, together}}, a);
+    else *c = make_call(mc, s.rows, s.experts, rows, 0, {{s.d_out, s.d_in, false, false, false}}, a);
     return a.used;
 }
 
@@ -520,7 +492,8 @@ forge_status gated_runs(PlanArgs& plan, const GatedSpace& l, const forge_expert_
     FORGE_TRY(run_operand(&plan.run[2], dY, s.d_model, a));
     FORGE_TRY(run_operand(&plan.run[3], X, s.d_model, b));
     FORGE_TRY(run_operand(&plan.run[4], ws + l.h, s.d_ff, b));
-    return plan_rows(plan, l.c, 5, {{dY, s.d_model}, {ws + l.dg, s.d_ff}, {ws + l.du, s.d_ff}});
+    plan.n_runs = 5;
+    return FORGE_OK;
 }
 
 // dH, and with it dG, dU and H in the workspace
@@ -536,14 +509,13 @@ forge_status run_gated_dh(const GatedSpace& l, const forge_expert_gated_shape& s
     const int64_t outs[3] = {l.dg, l.du, l.h};
     for (int i = 0; i < 3; ++i) g.to[i] = reinterpret_cast<uint16_t*>(c.ws + outs[i]);
     g.prob[0].b_flat = s.d_ff % 64 != 0;
-    g.prob[0].map_a = 5;
-    if (c.tiling.bn != 256) FORGE_TRY(rows_map(&g.maps[2], c, dY, s.d_model));
+    FORGE_TRY(rows_map(&g.maps[2], c, dY, s.d_model));
     FORGE_TRY(weight_map(&g.maps[0], Wd, s.experts, s.d_model, s.d_ff, true, kWeightExtent));
     return launch(g, c, c.tiling.bn, most_units(c, 0));
 }
 
 RowProduct gated_dx(const GatedSpace& l, const forge_expert_gated_shape& s, const void* Wg, const void* Wu, void* dX) {
-    return RowProduct{{l.c.ws + l.dg, l.c.ws + l.du}, {6, 7}, {Wg, Wu}, s.d_ff, s.d_model, true, dX};
+    return RowProduct{{l.c.ws + l.dg, l.c.ws + l.du}, {Wg, Wu}, s.d_ff, s.d_model, true, dX};
 }
 
 forge_status zero(std::initializer_list<void*> ps, int64_t bytes, cudaStream_t stream) {
@@ -598,9 +570,8 @@ forge_status forge_expert_linear(const void* X, const void* W, const int32_t* of
     c.stream = stream;
     c.offsets = offsets;
     PlanArgs plan{};
-    FORGE_TRY(plan_rows(plan, c, 0, {{X, s.d_in}}));
     FORGE_TRY(launch_plan(c, plan));
-    return run_rows(c, 0, RowProduct{{X, nullptr}, {0, 0}, {W, nullptr}, s.d_in, s.d_out, false, Y});
+    return run_rows(c, 0, RowProduct{{X, nullptr}, {W, nullptr}, s.d_in, s.d_out, false, Y});
 }
 
 forge_status forge_expert_linear_backward(const void* dY, const void* X, const void* W, const int32_t* offsets, void* dX,
@@ -627,9 +598,9 @@ forge_status forge_expert_linear_backward(const void* dY, const void* X, const v
     PlanArgs plan{};
     FORGE_TRY(run_operand(&plan.run[0], dY, s.d_out, 128));
     FORGE_TRY(run_operand(&plan.run[1], X, s.d_in, 128));
-    FORGE_TRY(plan_rows(plan, c, 2, {{dY, s.d_out}}));
+    plan.n_runs = 2;
     FORGE_TRY(launch_plan(c, plan));
-    const RowProduct dx{{dY, nullptr}, {2, 0}, {W, nullptr}, s.d_out, s.d_in, true, dX};
+    const RowProduct dx{{dY, nullptr}, {W, nullptr}, s.d_out, s.d_in, true, dX};
     if (t.together) return run_grads<kExpertBoth>(c, t.grads, &p, 1, &dx);
     if (dX != nullptr) FORGE_TRY(run_rows(c, 0, dx));
     return dW != nullptr ? run_grads<kExpertGrad>(c, t.grads, &p, 1, nullptr) : FORGE_OK;
@@ -662,7 +633,6 @@ forge_status forge_expert_gated_mlp(const void* X, const void* Wg, const void* W
     c.stream = stream;
     c.offsets = offsets;
     PlanArgs plan{};
-    FORGE_TRY(plan_rows(plan, c, 0, {{X, s.d_model}, {c.ws + l.h, s.d_ff}}));
     FORGE_TRY(launch_plan(c, plan));
     ExpertGroup<kBlockGatedFwd> g;
     begin_group(g, c, slices(s.d_model));
@@ -674,12 +644,12 @@ forge_status forge_expert_gated_mlp(const void* X, const void* Wg, const void* W
         g.to[1] = static_cast<uint16_t*>(U);
     }
     g.to[2] = reinterpret_cast<uint16_t*>(c.ws + l.h);
-    if (c.tiling.bn != 256) FORGE_TRY(rows_map(&g.maps[2], c, X, s.d_model));
+    FORGE_TRY(rows_map(&g.maps[2], c, X, s.d_model));
     const int extent = kGatedExtent;
     FORGE_TRY(weight_map(&g.maps[0], Wg, s.experts, s.d_ff, s.d_model, false, extent));
     FORGE_TRY(weight_map(&g.maps[1], Wu, s.experts, s.d_ff, s.d_model, false, extent));
     FORGE_TRY(launch(g, c, c.tiling.bn, most_units(c, 0)));
-    return run_rows(c, 1, RowProduct{{c.ws + l.h, nullptr}, {1, 0}, {Wd, nullptr}, s.d_ff, s.d_model, false, Y});
+    return run_rows(c, 1, RowProduct{{c.ws + l.h, nullptr}, {Wd, nullptr}, s.d_ff, s.d_model, false, Y});
 }
 
 forge_status forge_expert_gated_mlp_backward(const void* dY, const void* X, const void* G, const void* U, const void* Wg,
@@ -734,10 +704,10 @@ forge_status forge_expert_linear_backward_step(const void* dY, const void* X, vo
         PlanArgs plan{};
         FORGE_TRY(run_operand(&plan.run[0], dY, s.d_out, 64));
         FORGE_TRY(run_operand(&plan.run[1], X, s.d_in, 64));
-        FORGE_TRY(plan_rows(plan, c, 2, {{dY, s.d_out}}));
+        plan.n_runs = 2;
         FORGE_TRY(launch_plan(c, plan));
         // dX reads the weights before the fused step replaces them: same stream, this order
-        if (dX != nullptr) FORGE_TRY(run_rows(c, 0, RowProduct{{dY, nullptr}, {2, 0}, {W, nullptr}, s.d_out, s.d_in, true, dX}));
+        if (dX != nullptr) FORGE_TRY(run_rows(c, 0, RowProduct{{dY, nullptr}, {W, nullptr}, s.d_out, s.d_in, true, dX}));
     }
     return run_step(c, 0, 1, dY, X, s.rows, s.experts, forge_layer{nullptr, nullptr, W, m, v, qscales, 0, s.d_out, s.d_in, seed},
                     opt_kind, hp, state, step, stream);

@@ -12,15 +12,12 @@
 // Ragged runs.  A launch in front (expert_plan_kernel) turns the offsets into a list of row tiles and, for the
 // weights' gradients, into two tensor maps per expert whose token dimension ends with the run: the copy itself
 // fills what a slice reaches past the run with zeros, for both operands, so neither values of the next expert
-// nor its infinities or NaN enter a sum.  Row products need none for their results: an accumulator row depends on its own
-// row of A alone, and rows past the run are not stored.  On pairs they have them all the same: the large products run at
-// the chip's power limit, and zeros past the run cost less than the next expert's rows (32768 rows of 64 experts, gated
-// forward 2048/1408, passes on end: 475 us with them, 505 without).  On single CTAs the fences for them would show (2048 rows
-// there: 193 us with them, 189 without).  An expert without rows takes one slice of zero fill and
+// nor its infinities or NaN enter a sum.  Row products need none: an accumulator's row depends on its own row of X alone, and rows past the
+// run are not stored.  An expert without rows takes one slice of zero fill and
 // stores a zero gradient.
 //
 // Few row tiles.  The plan knows how many there are; where the last wave of tiles leaves SMs idle it cuts them
-// along the reduction (expert_cut), and the parts are joined as in forge_block_kernel: no CTA waits for another, the
+// along the reduction (expert_parts), and the parts are joined as in forge_block_kernel: no CTA waits for another, the
 // last to arrive adds the parts in their order.
 #pragma once
 
@@ -49,7 +46,7 @@ struct ExpertProblem {
     int kb[2];            // rows by expert: 64-deep reduction slices of the two operand pairs
     int a_flat, b_flat;   // MN-major and no multiple of 64 wide: a copy for each 64 columns
     int b_mn;             // row products: W is read MN-major
-    int map_a, map_b;     // numbers of run maps: a gradient's operands, or (pairs) the rows of each operand pair
+    int map_a, map_b;     // gradients: numbers of the operands' run maps
     int64_t ld;           // the result's width
 };
 
@@ -65,7 +62,7 @@ struct ExpertGroup {
     int withhold_first_stage;
     const int4* cut;      // row products: tiles before .x are whole, the others cut into .y parts; .z units
     const int* n_tiles;   // row tiles
-    const int4* tiles;    // each: expert, first row, one past its last row, first row of its run
+    const int4* tiles;    // each: expert, first row, one past its last row
     const int* offsets;   // [experts + 1], as the plan left them: in order and within the rows
     const CUtensorMap* runs;  // [map][expert]
     const uint16_t* g_in;
@@ -76,15 +73,13 @@ struct ExpertGroup {
     uint64_t wait_limit_ns, acc_wait_limit_ns;
     uint16_t* to[expert_products(EPI) > 3 ? 4 : 3];  // results: kBlockStore's; of each product; G, U, H; dG, dU, H
     ExpertProblem prob[expert_products(EPI)];
-    // rows by expert: the weights of each operand pair, or the gate's and the up projection's; then, on single CTAs, the
-    // rows of each pair (on pairs: run maps)
+    // rows by expert: the weights of each operand pair, or the gate's and the up projection's; then the rows of each pair
     CUtensorMap maps[EPI == kExpertGrad ? 1 : 4];
     CUtensorMap outs[expert_products(EPI)];  // gradients on pairs
 };
 
 struct ExpertUnit {
     int prob, expert, nb, row0, end;  // row0: the tile's first row of the result; end: one past its last
-    int begin;                        // rows by expert: the run's first row
     int k_first, k_end;               // slices (rows by expert: of both operand pairs, one after the other)
     int split, part;                  // which cut tile, or -1
 };
@@ -160,7 +155,6 @@ __device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int
         tile_coords(t - r.expert * per, TileOrder{b.tiles_m, b.tiles_n, 8, 0}, mb, r.nb);
         r.row0 = mb * kBM * CG;
         r.end = b.rows;
-        r.begin = 0;
         const int run = __ldcg(g.offsets + r.expert + 1) - __ldcg(g.offsets + r.expert);
         r.k_end = run > 0 ? (run + kBK - 1) / kBK : 0;
     } else {
@@ -181,7 +175,6 @@ __device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int
         r.expert = at.x;
         r.row0 = at.y;
         r.end = at.z;
-        r.begin = at.w;
     }
     return r;
 }
@@ -450,7 +443,7 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
         if constexpr (kRows) {
             tma_prefetch_desc(&grp.maps[0]);
             if constexpr (kGated) tma_prefetch_desc(&grp.maps[1]);
-            if constexpr (CG == 1) tma_prefetch_desc(&grp.maps[2]);
+            tma_prefetch_desc(&grp.maps[2]);
         }
     }
     if (warp == 1) {
@@ -529,16 +522,10 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
                     // the weights' 128 columns of the result, or 64 of the gate's rows and 64 of the up projection's
                     const bool wmn = EPI == kBlockGatedBwd || (!kGated && b.b_mn != 0), w_flat = wmn && b.b_flat != 0;
                     const int col = w.nb * kColsPerTile + static_cast<int>(rank) * (kColsPerTile / 2);
-                    const int map_row = w.row0 - w.begin + static_cast<int>(rank) * (expert_width(w) / 2);
-                    if (w.prob != seen_prob || w.expert != seen_expert) {
-                        tensormap_acquire(grp.runs + static_cast<size_t>(b.map_a) * grp.experts + w.expert);
-                        if (b.kb[1] > 0) tensormap_acquire(grp.runs + static_cast<size_t>(b.map_b) * grp.experts + w.expert);
-                        seen_prob = w.prob;
-                        seen_expert = w.expert;
-                    }
+                    const int row = w.row0 + static_cast<int>(rank) * (expert_width(w) / 2);
 #pragma unroll 1
                     for (int seg = 0; seg < (EPI == kBlockStore || kGrads ? 2 : 1) && ok; ++seg) {
-                        const CUtensorMap* mr = grp.runs + static_cast<size_t>(seg == 0 ? b.map_a : b.map_b) * grp.experts + w.expert;
+                        const CUtensorMap* mr = &grp.maps[2 + seg];
                         const CUtensorMap* mw = &grp.maps[seg];
                         const CUtensorMap* mu = &grp.maps[1];
                         int k0 = 0, w0 = wmn ? (w_flat ? col : 0) : 0, w1 = wmn ? 0 : col;
@@ -547,7 +534,7 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
                         for (int n = b.kb[seg]; ok && n > 0; --n, k0 += kBK, w0 += dw0, w1 += dw1)
                             ok = slice([&](uint32_t bar, uint32_t a_dst, uint32_t b_dst) {
                                 tma_load_4d_cg<CG>(a_dst, mw, bar, w0, w1, w2, w.expert, pol_b);
-                                tma_load_3d_cg<CG>(b_dst, mr, bar, k0, map_row, 0, keep);
+                                tma_load_3d_cg<CG>(b_dst, mr, bar, k0, row, 0, keep);
                                 if (kGated) tma_load_4d_cg<CG>(a_dst + 64 * 128, mu, bar, w0, w1, 0, w.expert, pol_b);
                                 if (!kGated && w_flat) tma_load_4d_cg<CG>(a_dst + kBK * 128, mw, bar, w0 + 64, w1, 0, w.expert, pol_b);
                             });
