@@ -265,7 +265,8 @@ class _DropoutFn(torch.autograd.Function):
 class ForgeDropout(Stepped):
     """dropout(x) (+ residual), bf16 or FP32, whose mask is made again in the backward pass and never stored.  In training
     mode each forward takes a mask of its own: number `step`, from 1, which goes into the state dict; seed is distinct
-    from other dropouts'.  In evaluation mode x (+ residual)."""
+    from other dropouts'.  (A captured forward replays with its mask; operators.dropout reads the step on the device.)
+    In evaluation mode x (+ residual)."""
 
     def __init__(self, p: float = 0.1, seed: int = 0):
         if not 0.0 <= p <= 1.0:

@@ -162,9 +162,9 @@ struct Call {
 };
 
 // Row tiles, by the rows that an expert has on average: 256 on pairs, 128, 64 or 32 on single CTAs, whose copies of A
-// are as many rows.  Gated forward, 2048/1408, 64 experts, us on 256 / 128 / 64 / 32 rows: 8 rows each 182 / 173 / 167 / 167;
-// 32: 199 / 187 / 186 / 225; 64: 203 / 195 / 229; 128: 218 / 239; 256: 281 / 355.  4096/14336, 8 experts: 128 rows each 539 / 566;
-// 16: 458 / 441 / 425 / 435; one row of two experts 176 / 183 / 140 / 122.
+// are as many rows.  Gated forward, 2048/1408, 64 experts, us on 256 / 128 / 64 / 32 rows: 8 rows each 189 / 186 / 181 / 180;
+// 32: 195 / 190 / 191 / 230; 64: 200 / 199 / 230; 128: 218 / 242; 256: 278 / 360.  4096/14336, 8 experts: 128 rows each 508 / 565;
+// 16: 454 / 443 / 432 / 441; one row of two experts 174 / 169 / 132 / 120.
 Tiling choose_rows(int64_t rows, int64_t experts) {
     const int64_t each = rows / std::min(rows, experts);
     if (each > 90) return Tiling{256, 256};
@@ -186,7 +186,7 @@ Tiling grad_tiling(const Machine& mc, int64_t experts, const GradProduct* p, int
 
 // The tiles of a linear layer's backward pass that wants dX and dW, and whether one launch makes both: dX's units first,
 // the gradients' behind them and beside its last wave.  It does with short runs, where both have the same tiles;
-// experts of over 40 rows take pairs for that.  us in two launches / in one: 2048 rows of 32 experts, 1024 x 2048 66 / 62;
+// experts of over 40 rows take pairs for that.  us in two launches / in one: 2048 rows of 32 experts, 1024 x 2048 66 / 61;
 // 1003 of 16, 1032 x 520 25 / 22; 200 of 3, 512 x 256 12.6 / 8.8; with long runs 30 / 33 (4096 of 4, 1024 x 1024).  The
 // gated block's dX has long units (its two products), which are better cut in a launch of their own (1003 rows of 16
 // experts, 520/1032: 60 us, 67 in one; 300 of 4, 1024/776 41 and 48).
