@@ -59,6 +59,8 @@ CASES = [
     ([333], 0, 0, 1000, 264), ([700, 513, 0, 900], 0, 77, 640, 1288), ([255, 256, 257, 511], 3, 0, 1024, 776),
     ([0, 4000, 1, 0, 30], 0, 2, 512, 320), ([0, 0, 0], 4, 4, 64, 64),
 ]
+# on pairs, where a run's last tile is as wide as its rest: every width, at its edges
+CASES += [([32 * k + d for k in range(9) for d in (0, 1, 31)], 0, 3, 136, 328)]
 
 
 def _tensor(gen, *shape, std=1.0):
