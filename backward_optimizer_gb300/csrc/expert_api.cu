@@ -208,6 +208,10 @@ struct RowSize {
     int64_t cols, k;
     bool gated, two;  // two: two operand pairs
     bool beside;      // in the gradients' launch, whose units fill its last wave: not cut
+    // With a gated block's epilogue: not cut on pairs.  Its reduction is as long as the model is wide, and pairs gain from
+    // a cut past 64 slices only; a second copy of the epilogue for joined parts slowed small calls (2000 rows of 8 experts,
+    // 1408/2048, backward: 117.5 us with it, 115.3 without).
+    bool block;
 };
 
 Call make_call(const Machine& mc, int64_t rows, int64_t experts, const Tiling& tiling, int n_runs,
@@ -229,13 +233,14 @@ Call make_call(const Machine& mc, int64_t rows, int64_t experts, const Tiling& t
     const int width = pair ? mc.pairs : mc.dev.num_sms;
     bool cut = false;
     for (const RowSize& p : products) {
-        const int kb = p.beside || pair ? 0 : slices(p.k) * (p.two ? 2 : 1);  // pairs' tiles are not cut
+        const int kb = p.beside || (pair && p.block) ? 0 : slices(p.k) * (p.two ? 2 : 1);
         forge::ExpertCut& x = c.cut[c.n_cuts++];
-        // joins as kTiles has them (block_api.cu)
-        x = forge::ExpertCut{static_cast<int>(ceil_div(p.cols, p.gated ? t.bn / 2 : t.bn)), kb, width, 6, 5};
+        // joins as kTiles has them (block_api.cu).  Cut against whole on pairs, us: linear forward 1500 rows of 3 experts,
+        // 14336 x 256, 34 / 70; gated backward 418 of 2, 232/14152, 101 / 237; calls that are not cut within 1 %
+        x = forge::ExpertCut{static_cast<int>(ceil_div(p.cols, p.gated ? t.bn / 2 : t.bn)), kb, width, pair ? 8 : 6, pair ? 12 : 5};
         cut = cut || forge::expert_parts(x, 1) > 1;
     }
-    c.n_counts = cut ? width * 8 : 0;
+    c.n_counts = cut ? width * (pair ? 2 : 1) * 8 : 0;
     c.counts = a.take(c.n_counts * 4ll);
     c.parts = a.take(cut ? static_cast<int64_t>(width) * t.tile_rows * t.bn * 4 : 0);
     return c;
@@ -462,10 +467,10 @@ GatedSpace layout_gated(const Machine& mc, const forge_expert_gated_shape& s, bo
     const Tiling rows = choose_rows(s.rows, s.experts);
     if (backward)
         l.c = make_call(mc, s.rows, s.experts, rows, kMaxRuns,
-                        {{s.d_ff, s.d_model, false, false, false}, {s.d_model, s.d_ff, false, true, false}}, a);
+                        {{s.d_ff, s.d_model, false, false, false, true}, {s.d_model, s.d_ff, false, true, false, false}}, a);
     else
         l.c = make_call(mc, s.rows, s.experts, rows, 0,
-                        {{s.d_ff, s.d_model, true, false, false}, {s.d_model, s.d_ff, false, false, false}}, a);
+                        {{s.d_ff, s.d_model, true, false, false, true}, {s.d_model, s.d_ff, false, false, false, false}}, a);
     const int64_t bytes = s.rows * s.d_ff * 2;
     if (backward) {
         l.dg = a.take(bytes);
@@ -478,8 +483,8 @@ GatedSpace layout_gated(const Machine& mc, const forge_expert_gated_shape& s, bo
 
 int64_t linear_space(const Machine& mc, const forge_expert_linear_shape& s, bool backward, const Tiling& rows, bool together, Call* c) {
     Arena a;
-    if (backward) *c = make_call(mc, s.rows, s.experts, rows, 2, {{s.d_in, s.d_out, false, false, together}}, a);
-    else *c = make_call(mc, s.rows, s.experts, rows, 0, {{s.d_out, s.d_in, false, false, false}}, a);
+    if (backward) *c = make_call(mc, s.rows, s.experts, rows, 2, {{s.d_in, s.d_out, false, false, together, false}}, a);
+    else *c = make_call(mc, s.rows, s.experts, rows, 0, {{s.d_out, s.d_in, false, false, false, false}}, a);
     return a.used;
 }
 

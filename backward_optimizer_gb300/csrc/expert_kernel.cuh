@@ -314,6 +314,9 @@ __device__ __forceinline__ void epi_rows_gated_bwd(const ExpertTile& t, const Ac
     }
 }
 
+// Two warps' barrier.
+__device__ __forceinline__ void meet(int number) { asm volatile("bar.sync %0, 64;" ::"r"(number) : "memory"); }
+
 // Whether two warps that meet inside a tile's epilogue both run it: the first to come to tile `no` decides for both, so that
 // neither waits for one that has given up.  The word counts the tiles that are to be run (a warp with no columns to make may be
 // some ahead of the other: it meets nobody), or says that the rest are left.  Each warp calls it once a tile until it answers 0.
@@ -329,7 +332,6 @@ __device__ __forceinline__ int expert_agree(uint32_t* word, uint32_t no, int ok)
 template <int ACT, class Acc>
 __device__ __forceinline__ void epi_rows_gated_fwd(const ExpertTile& t, const Acc& acc, bool is_up, bool keep, uint16_t* own,
                                                    uint16_t* h, uint32_t buf, uint32_t other, int meeting) {
-    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(meeting) : "memory"); };
     const uint32_t lane = threadIdx.x & 31u, mine = buf + 2048u + 4u * lane, theirs = other + 2048u + 4u * lane;
     const bool inside = t.col < t.cols;  // the same for both warps
 #pragma unroll 1
@@ -339,11 +341,11 @@ __device__ __forceinline__ void epi_rows_gated_fwd(const ExpertTile& t, const Ac
         const ExpertBlock b{buf, t.row0 + j, t.row0 + t.rows, t.col, t.cols};
 #pragma unroll
         for (int i = 0; i < 16; ++i) st_shared_f32(mine + 128u * i, __uint_as_float(is_up ? v[i] : v[16 + i]));
-        meet();
+        meet(meeting);
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = ld_shared_f32(theirs + 128u * i);
-        meet();
+        meet(meeting);
         if (!inside) continue;
         if (keep) {
             __syncwarp();  // the last block has been read
@@ -404,6 +406,8 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
     forge_expert_kernel(const __grid_constant__ ExpertGroup<EPI> grp) {
     using C = ExpertCfg<BN, CG, EPI>;
     constexpr bool kGated = EPI == kBlockGatedFwd, kGrads = expert_grads(EPI), kRows = EPI != kExpertGrad;
+    constexpr bool kMeets = kGated && CG == 2;  // two warps meet in an epilogue
+    constexpr bool kCuts = !kGrads && (CG == 1 || EPI == kBlockStore);  // a last wave's tiles may be cut
     constexpr int kColsPerTile = kGated ? BN / 2 : BN;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -530,13 +534,17 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
                     const int row = w.row0 + static_cast<int>(rank) * (expert_width(w) / 2);
 #pragma unroll 1
                     for (int seg = 0; seg < (EPI == kBlockStore || kGrads ? 2 : 1) && ok; ++seg) {
+                        // the unit's slices of this operand pair
+                        const int base = seg == 0 ? 0 : b.kb[0];
+                        const int from = w.k_first > base ? w.k_first - base : 0;
+                        const int to = (w.k_end < base + b.kb[seg] ? w.k_end : base + b.kb[seg]) - base;
                         const CUtensorMap* mr = &grp.maps[2 + seg];
                         const CUtensorMap* mw = &grp.maps[seg];
                         const CUtensorMap* mu = &grp.maps[1];
-                        int k0 = 0, w0 = wmn ? (w_flat ? col : 0) : 0, w1 = wmn ? 0 : col;
+                        int k0 = from * kBK, w0 = wmn ? (w_flat ? col : 0) : k0, w1 = wmn ? k0 : col;
                         const int w2 = wmn && !w_flat ? col / 64 : 0, dw0 = wmn ? 0 : kBK, dw1 = wmn ? kBK : 0;
 #pragma unroll 1
-                        for (int n = b.kb[seg]; ok && n > 0; --n, k0 += kBK, w0 += dw0, w1 += dw1)
+                        for (int n = to - from; ok && n > 0; --n, k0 += kBK, w0 += dw0, w1 += dw1)
                             ok = slice([&](uint32_t bar, uint32_t a_dst, uint32_t b_dst) {
                                 tma_load_4d_cg<CG>(a_dst, mw, bar, w0, w1, w2, w.expert, pol_b);
                                 tma_load_3d_cg<CG>(b_dst, mr, bar, k0, row, 0, keep);
@@ -659,48 +667,57 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
             int ok = 1;
             if (lane == 0) {
                 ok = wait_bounded(&acc_full[acc], acc_phase, ab_acc) ? 1 : 0;
-                if constexpr (kGated && CG == 2) ok = expert_agree(&agreed[2 * half + (quarter & 1)], tile_no, ok);
+                if constexpr (kMeets) ok = expert_agree(&agreed[2 * half + (quarter & 1)], tile_no, ok);
             }
             ++tile_no;
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
             if (!ok) break;
             tc_fence_after();
             const AccTmem tm{tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN)};
+            const int meeting = 2 * half + (quarter & 1);  // kMeets: which two warps
+            const int col = w.nb * kColsPerTile + static_cast<int>(rank) * (kColsPerTile / 2) + (kGated ? quarter & 1 : quarter) * 32;
+            const ExpertTile t{w.row0, w.end - w.row0, col, p.cols, half * 32, 64};  // on pairs
             auto epilogue = [&](const auto& acc_from) {
-                if constexpr (EPI == kBlockGatedFwd) epi_gated_fwd<BN>(b, acc_from, row, w.nb, half, out);
-                else if constexpr (EPI == kBlockGatedBwd) epi_gated_bwd<BN>(b, acc_from, row, w.nb, half, out);
-                else epi_store<BN>(b, acc_from, row, w.nb, half, out);
-            };
-            if constexpr (CG == 2) {
-                const int col = w.nb * kColsPerTile + static_cast<int>(rank) * (kColsPerTile / 2) + (kGated ? quarter & 1 : quarter) * 32;
-                const ExpertTile t{w.row0, w.end - w.row0, col, p.cols, half * 32, 64};
-                if constexpr (kGrads) {
-                    if (grad) epi_expert_grad<BN>(b, tm, row, w.nb, half, grp.outs + w.prob, w.expert, buf);
-                    else epi_rows_store(t, tm, grp.to[0], buf);
-                } else if constexpr (EPI == kBlockGatedFwd) {
+                if constexpr (CG == 2 && EPI == kBlockGatedFwd) {
                     const bool is_up = quarter >= 2;
                     const uint32_t other = smem_addr(staging) + static_cast<uint32_t>(half * 4 + quarter) * 4096u;
                     with_act(grp.act, [&](auto a) {
-                        epi_rows_gated_fwd<decltype(a)::value>(t, tm, is_up, grp.keep != 0, grp.to[is_up ? 1 : 0], grp.to[2], buf, other,
-                                                               1 + 2 * half + (quarter & 1));
+                        epi_rows_gated_fwd<decltype(a)::value>(t, acc_from, is_up, grp.keep != 0, grp.to[is_up ? 1 : 0], grp.to[2], buf,
+                                                               other, 1 + meeting);
                     });
-                } else if constexpr (EPI == kBlockGatedBwd) {
+                } else if constexpr (CG == 2 && EPI == kBlockGatedBwd) {
                     with_act(grp.act, [&](auto a) {
-                        epi_rows_gated_bwd<decltype(a)::value>(t, tm, grp.g_in, grp.u_in, grp.to[0], grp.to[1], grp.to[2], buf);
+                        epi_rows_gated_bwd<decltype(a)::value>(t, acc_from, grp.g_in, grp.u_in, grp.to[0], grp.to[1], grp.to[2], buf);
                     });
+                } else if constexpr (CG == 2) {
+                    epi_rows_store(t, acc_from, grp.to[0], buf);
+                } else if constexpr (EPI == kBlockGatedFwd) {
+                    epi_gated_fwd<BN>(b, acc_from, row, w.nb, half, out);
+                } else if constexpr (EPI == kBlockGatedBwd) {
+                    epi_gated_bwd<BN>(b, acc_from, row, w.nb, half, out);
                 } else {
-                    epi_rows_store(t, tm, grp.to[0], buf);
+                    epi_store<BN>(b, acc_from, row, w.nb, half, out);
                 }
-            }
-            // (single CTAs) [cut tile][part][lane quarter][column][lane]; quarters past the tile's rows are not there
-            const size_t step = static_cast<size_t>(a_rows / 32) * BN * 32;
-            const size_t own = static_cast<size_t>(quarter) * BN * 32 + lane;
-            const bool whole = CG == 2 || kGrads || w.split < 0;
-            if (CG == 2) {
+            };
+            // [cut tile][part][CTA][lane quarter][column][lane]; quarters past a single CTA's tile are not there
+            const size_t step = static_cast<size_t>(CG) * (a_rows / 32) * BN * 32;
+            const size_t own = (static_cast<size_t>(rank) * (a_rows / 32) + quarter) * BN * 32 + lane;
+            const bool whole = !kCuts || w.split < 0;
+            float* const part = grp.parts + (static_cast<size_t>(w.split) * cut.y + w.part) * step + own;  // of a cut tile
+            if (CG == 2 && grad) {
+                if constexpr (CG == 2 && kGrads) epi_expert_grad<BN>(b, tm, row, w.nb, half, grp.outs + w.prob, w.expert, buf);
             } else if (whole) {
                 epilogue(tm);
+            } else if constexpr (!kCuts) {
+            } else if constexpr (CG == 2) {
+#pragma unroll 1
+                for (int j = t.first; t.col < t.cols && j < t.rows; j += t.step) {
+                    uint32_t g[32];
+                    tm.load(j, g);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) __stcg(part + static_cast<size_t>(j + i) * 32, __uint_as_float(g[i]));
+                }
             } else if (warp_row0(row) < b.rows) {
-                float* to = grp.parts + (static_cast<size_t>(w.split) * cut.y + w.part) * step + own;
                 // the columns whose epilogue this warp runs: gate and up columns come from both halves
                 constexpr int kRuns = kGated ? 2 : 1, kRun = BN / 2 / kRuns, kStep = kRun < 32 ? kRun : 32;
 #pragma unroll 1
@@ -713,7 +730,7 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
                         if (row < b.rows) {
 #pragma unroll
                             for (int j = 0; j < kStep; ++j)
-                                __stcg(to + static_cast<size_t>(at + j) * 32, __uint_as_float(g[j]));
+                                __stcg(part + static_cast<size_t>(at + j) * 32, __uint_as_float(g[j]));
                         }
                     }
                 }
@@ -724,19 +741,20 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
             if (lane == 0) mbar_arrive_relaxed(map_to_rank(smem_addr(&acc_empty[acc]), 0));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
-            if (!whole) {
+            if constexpr (kCuts) {
+                if (whole) continue;
                 // every lane's values are visible device-wide before the warp counts itself in; the last one to
                 // arrive sees the other parts' values
                 __threadfence();
                 __syncwarp();
                 uint32_t before = 0;
-                uint32_t* count = grp.counts + w.split * C::kEpiWarps + e;
+                uint32_t* count = grp.counts + (w.split * CG + static_cast<int>(rank)) * C::kEpiWarps + e;
                 if (lane == 0) before = atomicAdd(count, 1u);
                 before = __shfl_sync(0xFFFFFFFFu, before, 0);
                 if (before + 1 == static_cast<uint32_t>(cut.y)) {
                     __threadfence();
                     if (lane == 0) *count = 0u;
-                    epilogue(AccParts{grp.parts + static_cast<size_t>(w.split) * cut.y * step + own, step, cut.y, row < b.rows});
+                    epilogue(AccParts{grp.parts + static_cast<size_t>(w.split) * cut.y * step + own, step, cut.y, CG == 2 || row < b.rows});
                 }
             }
         }

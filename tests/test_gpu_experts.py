@@ -61,6 +61,8 @@ CASES = [
 ]
 # on pairs, where a run's last tile is as wide as its rest: every width, at its edges
 CASES += [([32 * k + d for k in range(9) for d in (0, 1, 31)], 0, 3, 136, 328)]
+# there, few tiles with a long reduction, which are cut
+CASES += [([150, 0, 200], 1, 2, 104, 5000)]
 
 
 def _tensor(gen, *shape, std=1.0):
