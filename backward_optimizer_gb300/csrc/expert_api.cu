@@ -153,7 +153,9 @@ struct Call {
     int64_t tiles;  // row tiles at most
     int n_runs;
     int64_t clean, n_tiles, list, runs, cuts, counts, parts;  // places in the workspace
-    int n_counts;
+    int n_counts;                    // of row products, then of gradients
+    int grad_ways, grad_counts;      // parts of each gradient tile, and where their arrivals are counted
+    int64_t grad_parts;
     forge::ExpertCut cut[kMaxCuts];  // of the call's row products, in the order of their launches
     int n_cuts;
     char* ws;
@@ -214,8 +216,28 @@ struct RowSize {
     bool block;
 };
 
+// Into how many parts each tile of gradients is cut along its run, where single CTAs have few tiles of long runs (by an
+// expert's rows on average).  Cut / whole, us: linear backward 29994 rows of 2 experts, 440 x 200, 46 / 141; 9000 of 3,
+// 256 x 256, 25 / 29; gated backward 29994 of 1, 200/440, 129 / 253; 9000 of 1, 512/512, 60 / 72.
+int grad_ways(const Machine& mc, int64_t rows, int64_t experts, const Tiling& t, int64_t units) {
+    if (t.bn == 256 || units * 2 > mc.dev.num_sms) return 1;
+    return forge::expert_parts(forge::ExpertCut{0, slices(rows / experts), mc.dev.num_sms, 6, 5}, static_cast<int>(units));
+}
+
+int64_t grad_units(const Tiling& t, int64_t experts, const GradProduct* p, int n) {
+    int64_t u = 0;
+    for (int i = 0; i < n; ++i) u += experts * ceil_div(p[i].d_out, t.bn == 256 ? 256 : 128) * ceil_div(p[i].d_in, t.bn);
+    return u;
+}
+
+// grads: the tiling and number of the gradients' tiles, if they have a launch of their own
+struct GradSize {
+    Tiling tiling;
+    int64_t units;
+};
+
 Call make_call(const Machine& mc, int64_t rows, int64_t experts, const Tiling& tiling, int n_runs,
-               std::initializer_list<RowSize> products, Arena& a) {
+               std::initializer_list<RowSize> products, const GradSize& grads, Arena& a) {
     Call c{};
     c.mc = mc;
     c.rows = rows;
@@ -241,8 +263,12 @@ Call make_call(const Machine& mc, int64_t rows, int64_t experts, const Tiling& t
         cut = cut || forge::expert_parts(x, 1) > 1;
     }
     c.n_counts = cut ? width * (pair ? 2 : 1) * 8 : 0;
+    c.grad_ways = grads.units > 0 ? grad_ways(mc, rows, experts, grads.tiling, grads.units) : 1;
+    c.grad_counts = c.n_counts;
+    if (c.grad_ways > 1) c.n_counts += static_cast<int>(grads.units) * 8;
     c.counts = a.take(c.n_counts * 4ll);
     c.parts = a.take(cut ? static_cast<int64_t>(width) * t.tile_rows * t.bn * 4 : 0);
+    c.grad_parts = a.take(c.grad_ways > 1 ? grads.units * c.grad_ways * (128 * 128 * 4) : 0);
     return c;
 }
 
@@ -432,8 +458,14 @@ forge_status run_grads(const Call& c, const Tiling& t, const GradProduct* p, int
         u += static_cast<int64_t>(c.experts) * b.tiles_m * b.tiles_n;
         FORGE_TRY(set_gradient(g, t, first + i, p[i].out, c.experts, p[i].d_out, p[i].d_in));
     }
+    g.ways = EPI == kExpertGrad ? c.grad_ways : 1;
+    if (g.ways > 1) {
+        g.parts = reinterpret_cast<float*>(c.ws + c.grad_parts);
+        g.counts = reinterpret_cast<uint32_t*>(c.ws + c.counts) + c.grad_counts;
+    }
+    u *= g.ways;
     g.n_units = static_cast<int>(u);
-    g.chunk = grad_chunk(c, u, static_cast<int64_t>(g.prob[first].tiles_m) * g.prob[first].tiles_n, t.bn == 256 ? c.mc.pairs : c.mc.dev.num_sms);
+    g.chunk = g.ways > 1 ? 1 : grad_chunk(c, u, static_cast<int64_t>(g.prob[first].tiles_m) * g.prob[first].tiles_n, t.bn == 256 ? c.mc.pairs : c.mc.dev.num_sms);
     return launch(g, c, t.bn, u + (dx != nullptr ? c.tiles * g.prob[0].tiles_n : 0));
 }
 
@@ -465,12 +497,17 @@ GatedSpace layout_gated(const Machine& mc, const forge_expert_gated_shape& s, bo
     GatedSpace l{};
     Arena a;
     const Tiling rows = choose_rows(s.rows, s.experts);
-    if (backward)
+    if (backward) {
+        const GradProduct p[3] = {{0, 0, s.d_ff, s.d_model, nullptr}, {0, 0, s.d_ff, s.d_model, nullptr}, {0, 0, s.d_model, s.d_ff, nullptr}};
+        const Tiling grads = grad_tiling(mc, s.experts, p, 3);
         l.c = make_call(mc, s.rows, s.experts, rows, kMaxRuns,
-                        {{s.d_ff, s.d_model, false, false, false, true}, {s.d_model, s.d_ff, false, true, false, false}}, a);
-    else
+                        {{s.d_ff, s.d_model, false, false, false, true}, {s.d_model, s.d_ff, false, true, false, false}},
+                        GradSize{grads, grad_units(grads, s.experts, p, 3)}, a);
+    } else {
         l.c = make_call(mc, s.rows, s.experts, rows, 0,
-                        {{s.d_ff, s.d_model, true, false, false, true}, {s.d_model, s.d_ff, false, false, false, false}}, a);
+                        {{s.d_ff, s.d_model, true, false, false, true}, {s.d_model, s.d_ff, false, false, false, false}},
+                        GradSize{}, a);
+    }
     const int64_t bytes = s.rows * s.d_ff * 2;
     if (backward) {
         l.dg = a.take(bytes);
@@ -483,8 +520,14 @@ GatedSpace layout_gated(const Machine& mc, const forge_expert_gated_shape& s, bo
 
 int64_t linear_space(const Machine& mc, const forge_expert_linear_shape& s, bool backward, const Tiling& rows, bool together, Call* c) {
     Arena a;
-    if (backward) *c = make_call(mc, s.rows, s.experts, rows, 2, {{s.d_in, s.d_out, false, false, together, false}}, a);
-    else *c = make_call(mc, s.rows, s.experts, rows, 0, {{s.d_out, s.d_in, false, false, false, false}}, a);
+    if (backward) {
+        const GradProduct p{0, 0, s.d_out, s.d_in, nullptr};
+        const Tiling grads = grad_tiling(mc, s.experts, &p, 1);
+        *c = make_call(mc, s.rows, s.experts, rows, 2, {{s.d_in, s.d_out, false, false, together, false}},
+                       GradSize{grads, together ? 0 : grad_units(grads, s.experts, &p, 1)}, a);
+    } else {
+        *c = make_call(mc, s.rows, s.experts, rows, 0, {{s.d_out, s.d_in, false, false, false, false}}, GradSize{}, a);
+    }
     return a.used;
 }
 

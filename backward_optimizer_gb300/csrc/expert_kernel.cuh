@@ -16,9 +16,10 @@
 // Row products need no such maps: a row of the result depends on its own row of X alone, and rows past the run are not
 // stored.
 //
-// Few row tiles.  The plan knows how many there are; where the last wave of tiles leaves SMs idle it cuts them
+// Few tiles.  The plan knows how many row tiles there are; where the last wave of tiles leaves SMs idle it cuts them
 // along the reduction (expert_parts), and the parts are joined as in forge_block_kernel: no CTA waits for another, the
-// last to arrive adds the parts in their order.
+// last to arrive adds the parts in their order.  Gradients of few tiles are cut along their runs by the host's rule, the
+// same number of parts for each: a run of fewer slices leaves some parts a slice of zeros.
 #pragma once
 
 #include "block_kernel.cuh"
@@ -55,6 +56,7 @@ struct ExpertGroup {
     int n;                // products
     int n_units;          // of gradients
     int chunk;            // neighbouring units of gradients that a pair or CTA takes
+    int ways;             // parts into which each of the gradients' tiles is cut along its run (single CTAs); n_units counts them
     int experts;
     int a_rows;           // rows of A that a stage holds, and of a tile on single CTAs (128, 64 or 32)
     int stream_b;         // each weight is read by one row tile or few: leave it out of the L2
@@ -147,6 +149,11 @@ __device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int
     int mb;
     if (expert_grads(EPI) && (EPI == kExpertGrad || u >= row_units)) {
         u -= row_units;
+        if (CG == 1 && EPI == kExpertGrad && g.ways > 1) {
+            r.split = u / g.ways;
+            r.part = u - r.split * g.ways;
+            u = r.split;
+        }
         r.prob = expert_first_grad(EPI);
         while (r.prob + 1 < g.n && u >= g.prob[r.prob + 1].unit_start) ++r.prob;
         const ExpertProblem& b = g.prob[r.prob];
@@ -157,6 +164,13 @@ __device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int
         r.end = b.rows;
         const int run = __ldcg(g.offsets + r.expert + 1) - __ldcg(g.offsets + r.expert);
         r.k_end = run > 0 ? (run + kBK - 1) / kBK : 0;
+        const int past = r.k_end > 0 ? r.k_end : 1;
+        if (CG == 1 && EPI == kExpertGrad && g.ways > 1) {
+            const int kb = r.k_end;
+            r.k_first = static_cast<int>(static_cast<int64_t>(kb) * r.part / g.ways);
+            r.k_end = static_cast<int>(static_cast<int64_t>(kb) * (r.part + 1) / g.ways);
+        }
+        if (r.k_end == r.k_first) r.k_first = r.k_end = past;  // one slice of zeros
     } else {
         const ExpertProblem& b = g.prob[0];
         r.prob = 0;
@@ -407,7 +421,7 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
     using C = ExpertCfg<BN, CG, EPI>;
     constexpr bool kGated = EPI == kBlockGatedFwd, kGrads = expert_grads(EPI), kRows = EPI != kExpertGrad;
     constexpr bool kMeets = kGated && CG == 2;  // two warps meet in an epilogue
-    constexpr bool kCuts = !kGrads && (CG == 1 || EPI == kBlockStore);  // a last wave's tiles may be cut
+    constexpr bool kCuts = CG == 1 ? EPI != kExpertBoth : EPI == kBlockStore;  // tiles may be cut
     constexpr int kColsPerTile = kGated ? BN / 2 : BN;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -515,12 +529,12 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
                         seen_prob = w.prob;
                         seen_expert = w.expert;
                     }
-                    // a run of no rows: one slice past the one row that its maps have
-                    int k0 = w.k_end == 0 ? kBK : 0;
+                    // a part of no slices takes one past its run (a run of no rows: past the one row that its maps have)
+                    int k0 = w.k_first * kBK;
                     const bool a_flat = b.a_flat != 0, b_flat = b.b_flat != 0;
                     const int a0 = a_flat ? row_a : 0, a2 = a_flat ? 0 : row_a / 64;
                     const int b0 = b_flat ? col_b : 0, b2 = b_flat ? 0 : col_b / 64;
-                    for (int n = w.k_end == 0 ? 1 : w.k_end; ok && n > 0; --n, k0 += kBK)
+                    for (int n = w.k_end == w.k_first ? 1 : w.k_end - w.k_first; ok && n > 0; --n, k0 += kBK)
                         ok = slice([&](uint32_t bar, uint32_t a_dst, uint32_t b_dst) {
                             tma_load_3d_cg<CG>(a_dst, ma, bar, a0, k0, a2, keep);
                             tma_load_3d_cg<CG>(b_dst, mb, bar, b0, k0, b2, keep);
@@ -703,7 +717,8 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
             const size_t step = static_cast<size_t>(CG) * (a_rows / 32) * BN * 32;
             const size_t own = (static_cast<size_t>(rank) * (a_rows / 32) + quarter) * BN * 32 + lane;
             const bool whole = !kCuts || w.split < 0;
-            float* const part = grp.parts + (static_cast<size_t>(w.split) * cut.y + w.part) * step + own;  // of a cut tile
+            const int ways = kGrads ? grp.ways : cut.y;
+            float* const part = grp.parts + (static_cast<size_t>(w.split) * ways + w.part) * step + own;  // of a cut tile
             if (CG == 2 && grad) {
                 if constexpr (CG == 2 && kGrads) epi_expert_grad<BN>(b, tm, row, w.nb, half, grp.outs + w.prob, w.expert, buf);
             } else if (whole) {
@@ -751,10 +766,10 @@ __global__ void __launch_bounds__(ExpertCfg<BN, CG, EPI>::kThreads, 1)
                 uint32_t* count = grp.counts + (w.split * CG + static_cast<int>(rank)) * C::kEpiWarps + e;
                 if (lane == 0) before = atomicAdd(count, 1u);
                 before = __shfl_sync(0xFFFFFFFFu, before, 0);
-                if (before + 1 == static_cast<uint32_t>(cut.y)) {
+                if (before + 1 == static_cast<uint32_t>(ways)) {
                     __threadfence();
                     if (lane == 0) *count = 0u;
-                    epilogue(AccParts{grp.parts + static_cast<size_t>(w.split) * cut.y * step + own, step, cut.y, CG == 2 || row < b.rows});
+                    epilogue(AccParts{grp.parts + static_cast<size_t>(w.split) * ways * step + own, step, ways, CG == 2 || row < b.rows});
                 }
             }
         }

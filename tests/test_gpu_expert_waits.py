@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 # row tiles of 32, 64, 128 and 256 rows; a last wave cut along the reduction; gradients on single CTAs and on pairs
 @pytest.mark.parametrize("sizes, D, F", [([1, 0, 1], 2048, 1024), ([9, 30, 0, 20], 512, 264), ([70, 0, 50], 256, 512),
                                          ([300, 0, 500], 1024, 1536), ([20, 0, 4, 33] * 20, 512, 512),
-                                         ([150, 0, 200], 104, 5000)])
+                                         ([150, 0, 200], 104, 5000), ([12000, 0, 70], 72, 136)])
 def test_experts(sizes, D, F):
     R, E = sum(sizes), len(sizes)
     off = torch.tensor([0] + sizes).cumsum(0).to(torch.int32).cuda()

@@ -63,6 +63,8 @@ CASES = [
 CASES += [([32 * k + d for k in range(9) for d in (0, 1, 31)], 0, 3, 136, 328)]
 # there, few tiles with a long reduction, which are cut
 CASES += [([150, 0, 200], 1, 2, 104, 5000)]
+# few tiles of gradients with long runs, which are cut; a run of fewer slices than parts
+CASES += [([12000, 0, 70], 1, 2, 72, 136)]
 
 
 def _tensor(gen, *shape, std=1.0):
