@@ -23,6 +23,7 @@ With experts, dropout and pairs of sequences (rows sorted by expert; head made w
 """
 from __future__ import annotations
 
+import collections
 from typing import Any, Optional
 
 import torch
@@ -266,19 +267,44 @@ class ForgeDropout(Stepped):
     """dropout(x) (+ residual), bf16 or FP32, whose mask is made again in the backward pass and never stored.  In training
     mode each forward takes a mask of its own: number `step`, from 1, which goes into the state dict; seed is distinct
     from other dropouts'.  (A captured forward replays with its mask; operators.dropout reads the step on the device.)
-    In evaluation mode x (+ residual)."""
+    In evaluation mode x (+ residual).
+
+    A forward that a backward pass computes again (torch.utils.checkpoint) takes its mask again.  It is known by a
+    number that each forward in training mode draws from PyTorch's CPU generator, which checkpoint sets back; an error is
+    raised where it does not (preserve_rng_state=False), where over 1024 forwards lie between, and where forwards that are
+    still to be computed again began from the same state of that generator."""
+
+    _MOST = 1024  # forwards that are known
 
     def __init__(self, p: float = 0.1, seed: int = 0):
         if not 0.0 <= p <= 1.0:
             raise ValueError(f"p: {p}, expected a number between 0 and 1")
         super().__init__()
         self.p, self.seed = float(p), int(seed)
+        # by the number drawn: the forward's step (None: it may be one of several), and whether it has been computed again
+        self._masks: collections.OrderedDict = collections.OrderedDict()
+
+    def _take_step(self) -> int:
+        """The step of a forward that begins here."""
+        drawn = int(torch.empty((), dtype=torch.int64, device="cpu").random_())
+        if torch._C._current_graph_task_id() >= 0:  # a backward pass is running on this thread
+            step, _ = self._masks.get(drawn, (None, False))
+            if step is None:
+                raise RuntimeError("ForgeDropout: a backward pass computes a forward again and its mask is not known, since "
+                                   "PyTorch's CPU generator was not set back to that forward's state alone")
+            self._masks[drawn] = step, True
+            return step
+        step, self.step = self.step, self.step + 1
+        _, through = self._masks.pop(drawn, (None, True))
+        self._masks[drawn] = step if through else None, False
+        if len(self._masks) > self._MOST:
+            self._masks.popitem(last=False)
+        return step
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
         if not self.training:
             return x if residual is None else x + residual
-        step, self.step = self.step, self.step + 1
-        return _DropoutFn.apply(x, residual, self.p, self.seed, step)
+        return _DropoutFn.apply(x, residual, self.p, self.seed, self._take_step())
 
     def extra_repr(self) -> str:
         return f"p={self.p}, seed={self.seed}, step={self.step}"
