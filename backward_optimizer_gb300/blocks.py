@@ -250,12 +250,15 @@ class _DropoutFn(torch.autograd.Function):
         y = torch.empty_like(X)
         ops.dropout(X, y, p, seed=seed, step=step, residual=None if residual is None else residual.detach().contiguous())
         ctx.p, ctx.seed, ctx.step, ctx.dtype, ctx.has_residual = p, seed, step, x.dtype, residual is not None
+        ctx.version = step._version if torch.is_tensor(step) and not step.is_inference() else None
         return y
 
     @staticmethod
     @once("ForgeDropout")
     def backward(ctx, grad_out):
         dx = None
+        if ctx.version is not None and ctx.step._version != ctx.version:
+            raise RuntimeError("ForgeDropout: step was changed between the forward and the backward pass")
         if ctx.needs_input_grad[0]:
             dy = grad_out.to(ctx.dtype).contiguous()
             dx = torch.empty_like(dy)
@@ -266,8 +269,11 @@ class _DropoutFn(torch.autograd.Function):
 class ForgeDropout(Stepped):
     """dropout(x) (+ residual), bf16 or FP32, whose mask is made again in the backward pass and never stored.  In training
     mode each forward takes a mask of its own: number `step`, from 1, which goes into the state dict; seed is distinct
-    from other dropouts'.  (A captured forward replays with its mask; operators.dropout reads the step on the device.)
-    In evaluation mode x (+ residual).
+    from other dropouts'.  In evaluation mode x (+ residual).
+
+    forward's step: the mask's number instead, and the module's own stays as it is: a number, or an int64 tensor of one
+    element on the device that holds its value until the backward pass is through.  A captured forward replays with its
+    mask, or with the one that such a tensor says at the replay.
 
     A forward that a backward pass computes again (torch.utils.checkpoint) takes its mask again.  It is known by a
     number that each forward in training mode draws from PyTorch's CPU generator, which checkpoint sets back; an error is
@@ -291,7 +297,7 @@ class ForgeDropout(Stepped):
             step, _ = self._masks.get(drawn, (None, False))
             if step is None:
                 raise RuntimeError("ForgeDropout: a backward pass computes a forward again and its mask is not known, since "
-                                   "PyTorch's CPU generator was not set back to that forward's state alone")
+                                   "PyTorch's CPU generator was not set back to that forward's state alone; pass step=")
             self._masks[drawn] = step, True
             return step
         step, self.step = self.step, self.step + 1
@@ -301,10 +307,10 @@ class ForgeDropout(Stepped):
             self._masks.popitem(last=False)
         return step
 
-    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, step=None) -> torch.Tensor:
         if not self.training:
             return x if residual is None else x + residual
-        return _DropoutFn.apply(x, residual, self.p, self.seed, self._take_step())
+        return _DropoutFn.apply(x, residual, self.p, self.seed, self._take_step() if step is None else step)
 
     def extra_repr(self) -> str:
         return f"p={self.p}, seed={self.seed}, step={self.step}"

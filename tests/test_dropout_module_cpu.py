@@ -128,3 +128,27 @@ def test_default_device_and_type_do_not_matter():
         torch.set_default_device(None)
         torch.set_default_dtype(torch.float32)
     assert torch.equal(_mask_of(y), _kept(N, 0.5, 0, 1))
+
+
+@pytest.mark.parametrize("reentrant", [True, False])
+@pytest.mark.parametrize("on_device", [False, True])
+def test_the_step_that_the_caller_gives(reentrant, on_device):
+    drop = ForgeDropout(0.5, seed=6)
+    for k in (7, 7, 9):
+        step, x = torch.tensor([k]) if on_device else k, _x()
+        state = torch.get_rng_state()
+        y = checkpoint(lambda t: drop(t, step=step).square(), x, use_reentrant=reentrant, preserve_rng_state=False)
+        y.sum().backward()
+        assert torch.equal(_mask_of(y), _kept(N, 0.5, 6, k)) and torch.equal(x.grad != 0, _mask_of(y))
+        assert torch.equal(torch.get_rng_state(), state)  # such a forward draws no number
+    assert drop.step == 1
+
+
+def test_a_step_that_changes_before_the_backward_pass_raises():
+    drop, step, x = ForgeDropout(0.5, seed=6), torch.tensor([3]), _x()
+    y = drop(x, step=step)
+    step += 1
+    with pytest.raises(RuntimeError, match="step was changed"):
+        y.sum().backward()
+    with torch.inference_mode():
+        assert torch.equal(_mask_of(drop(x, step=torch.tensor([4]))), _kept(N, 0.5, 6, 4))

@@ -66,3 +66,32 @@ def test_a_block_in_a_region(reentrant):
         results.append(got)
     assert len(results[0]) == len(results[1])
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def test_a_captured_training_step_takes_a_mask_at_each_replay():
+    """Forward and backward through the module in one graph, with the step on the device moved at its end."""
+    drop, step = ForgeDropout(0.5, seed=4), torch.tensor([1], device="cuda")
+    values, r = _rand(1, 40, 129).abs() + 0.5, _rand(2, 40, 129)
+
+    def once(x, at):
+        y = drop(x, residual=r, step=at)
+        z = (y - r).square()
+        return y.detach(), torch.autograd.grad(z.sum(), x)[0]
+
+    once(values.clone().requires_grad_(), step)
+    torch.cuda.synchronize()
+    x = values.clone().requires_grad_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y, dx = once(x, step)
+        step += 1
+    masks = []
+    for k in (1, 2, 3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert fg.sync_status() == 0 and step.item() == k + 1
+        want_y, want_dx = once(values.clone().requires_grad_(), k)
+        assert torch.equal(y, want_y) and torch.equal(dx, want_dx)
+        masks.append(dx != 0)
+    assert not torch.equal(masks[0], masks[1]) and not torch.equal(masks[1], masks[2])
+    assert drop.step == 1
