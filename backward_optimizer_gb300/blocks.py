@@ -267,7 +267,7 @@ class _DropoutFn(torch.autograd.Function):
 
 
 class ForgeDropout(Stepped):
-    """dropout(x) (+ residual), bf16 or FP32, whose mask is made again in the backward pass and never stored.  In training
+    """dropout(x) (+ residual, of its shape and type), bf16 or FP32, whose mask is made again in the backward pass and never stored.  In training
     mode each forward takes a mask of its own: number `step`, from 1, which goes into the state dict; seed is distinct
     from other dropouts'.  In evaluation mode x (+ residual).
 
@@ -308,6 +308,13 @@ class ForgeDropout(Stepped):
         return step
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, step=None) -> torch.Tensor:
+        if x.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("ForgeDropout takes bfloat16 or FP32 inputs")
+        if residual is not None:
+            if residual.dtype != x.dtype:
+                raise TypeError(f"residual: dtype {residual.dtype}, expected {x.dtype}")
+            if residual.shape != x.shape or residual.device != x.device:
+                raise ValueError(f"residual: shape {tuple(residual.shape)} on {residual.device}, expected {tuple(x.shape)} on {x.device}")
         if not self.training:
             return x if residual is None else x + residual
         return _DropoutFn.apply(x, residual, self.p, self.seed, self._take_step() if step is None else step)

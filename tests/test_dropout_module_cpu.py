@@ -152,3 +152,20 @@ def test_a_step_that_changes_before_the_backward_pass_raises():
         y.sum().backward()
     with torch.inference_mode():
         assert torch.equal(_mask_of(drop(x, step=torch.tensor([4]))), _kept(N, 0.5, 6, 4))
+
+
+@pytest.mark.parametrize("training", [True, False])
+def test_what_is_refused_in_training_and_in_evaluation(training):
+    drop, x = ForgeDropout(0.5).train(training), torch.ones(4, 8)
+    for bad, residual in ((x.half(), None), (x.double(), None), (x.half(), x.half()), (x.long(), None), (x, x.bfloat16()),
+                          (x.bfloat16(), x)):
+        with pytest.raises(TypeError):
+            drop(bad, residual=residual)
+    for residual in (x[0], x[:, :1], torch.ones(()), x.view(8, 4), torch.ones(1, 4, 8), x.to("meta")):
+        with pytest.raises(ValueError):
+            drop(x, residual=residual)
+    assert drop.step == 1 and not drop._masks  # a refused call takes no mask
+    for t in (x, x.bfloat16()):
+        assert drop(t, residual=t).dtype == t.dtype and drop(t).dtype == t.dtype
+    if not training:
+        assert drop(x) is x and torch.equal(drop(x, residual=x), x + x) and drop.step == 1
