@@ -98,6 +98,27 @@ __device__ __forceinline__ int sequence_of(const PrefArgs& a, int t) {
     return lo - 1;
 }
 
+// f(sequence, its first token, one past its last) for each sequence that has tokens among t0 .. t1-1, these tokens only,
+// by the whole warp.  Any number of empty sequences in between costs one search (one by one they would take a trip to memory
+// each, seconds for millions of them).  Offsets out of order take no more steps than those in order can: a sequence for
+// each token, and an empty one in front of it.
+template <class F>
+__device__ __forceinline__ void each_sequence(const PrefArgs& a, int t0, int t1, F&& f) {
+    int i = max(sequence_of(a, t0), 0), begin = offset_at(a, i);
+    for (int left = 2 * (t1 - t0) + 2; left > 0 && i < 2 * a.pairs && begin < t1; --left) {
+        const int end = offset_at(a, i + 1);
+        if (begin < end) {
+            const int from = max(begin, t0), to = min(end, t1);
+            if (from < to) f(i, from, to);
+            ++i;
+            begin = end;
+        } else {  // the last sequence that starts where this empty one does
+            i = max(sequence_of(a, begin), i + 1);
+            begin = offset_at(a, i);
+        }
+    }
+}
+
 // f and its slope
 __device__ __forceinline__ void pair_loss(const PrefArgs& a, float z, float& loss, float& slope) {
     if (a.kind == FORGE_PREF_SIGMOID) {
@@ -131,11 +152,7 @@ __device__ __forceinline__ void sum_all(Wide& v, int& n) {
 __device__ __forceinline__ void chunk_sums(const PrefArgs& a, int c) {
     const int lane = threadIdx.x & 31;
     const int t0 = c * a.chunk, t1 = static_cast<int>(min(static_cast<int64_t>(t0) + a.chunk, static_cast<int64_t>(a.tokens)));
-    int i = max(sequence_of(a, t0), 0);
-    for (int begin = offset_at(a, i), end; i < 2 * a.pairs && begin < t1; ++i, begin = end) {
-        end = offset_at(a, i + 1);
-        const int from = max(begin, t0), to = min(end, t1);
-        if (from >= to) continue;
+    each_sequence(a, t0, t1, [&](int i, int from, int to) {
         Wide s{0.0f, 0.0f};
         int n = 0;
         constexpr int kAhead = 8;
@@ -160,7 +177,7 @@ __device__ __forceinline__ void chunk_sums(const PrefArgs& a, int c) {
         }
         sum_all(s, n);
         if (lane == 0) a.parts[c + i] = Partial{s.hi, s.lo, n, 0};
-    }
+    });
 }
 
 // One pair from its sequences' partials: a warp.
@@ -240,14 +257,10 @@ __global__ void __launch_bounds__(kThreads) pref_grad_kernel(const PrefArgs a) {
     for (int t = t0 + lane; t < min(t1, first); t += 32) a.dnll[t] = 0.0f;
     for (int t = max(t0, max(first, end)) + lane; t < t1; t += 32) a.dnll[t] = 0.0f;
     if (a.pairs == 0) return;
-    int i = max(sequence_of(a, t0), 0);
-    for (int begin = offset_at(a, i), end; i < 2 * a.pairs && begin < t1; ++i, begin = end) {
-        end = offset_at(a, i + 1);
-        const int from = max(begin, t0), to = min(end, t1);
-        if (from >= to) continue;
+    each_sequence(a, t0, t1, [&](int i, int from, int to) {
         const float g = a.slope[i] * a.dloss[i < a.pairs ? i : i - a.pairs];
         for (int t = from + lane; t < to; t += 32) a.dnll[t] = a.mask == nullptr || a.mask[t] != 0 ? g : 0.0f;
-    }
+    });
 }
 
 constexpr int kOneBlock = 4096, kOneBlockPairs = 64;  // tokens and pairs that one block takes by itself
