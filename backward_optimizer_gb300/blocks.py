@@ -267,9 +267,9 @@ class _DropoutFn(torch.autograd.Function):
 
 
 class ForgeDropout(Stepped):
-    """dropout(x) (+ residual, of its shape and type), bf16 or FP32, whose mask is made again in the backward pass and never stored.  In training
-    mode each forward takes a mask of its own: number `step`, from 1, which goes into the state dict; seed is distinct
-    from other dropouts'.  In evaluation mode x (+ residual).
+    """dropout(x) (+ residual, of its shape and type), bf16 or FP32, whose mask is made again in the backward pass and never
+    stored.  In training mode each forward takes a mask of its own: number `step`, from 1, which goes into the state dict;
+    seed is distinct from other dropouts'.  In evaluation mode x (+ residual).
 
     forward's step: the mask's number instead, and the module's own stays as it is: a number, or an int64 tensor of one
     element on the device that holds its value until the backward pass is through.  A captured forward replays with its
@@ -289,6 +289,10 @@ class ForgeDropout(Stepped):
         self.p, self.seed = float(p), int(seed)
         # by the number drawn: the forward's step (None: it may be one of several), and whether it has been computed again
         self._masks: collections.OrderedDict = collections.OrderedDict()
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self.__dict__.setdefault("_masks", collections.OrderedDict())  # pickled before there were any
 
     def _take_step(self) -> int:
         """The step of a forward that begins here."""
@@ -355,6 +359,8 @@ class ForgeHeadLoss(_Trained):
     reduction="none": each token's loss instead, in target's shape (0 where it is ignored).
     x [..., d_model] bf16, target [...] int64, weight [vocab, d_model].  opt, hp, state and seed as for
     ForgeLinear (int8 states need d_model to be a multiple of 64)."""
+
+    reduction = "mean"  # of modules pickled before there was a choice
 
     def __init__(self, d_model: int, vocab: int, opt: str = "adamw", hp: Any = None, state: str = "fp32", seed: int = 0,
                  ignore_index: int = -100, device=None, init_std: float = 0.02, reduction: str = "mean"):

@@ -1,4 +1,7 @@
 """ForgeDropout's bookkeeping of masks, with a host function in place of the kernel (CPU only: no kernel is launched)."""
+import copy
+import pickle
+
 import pytest
 import torch
 from torch.utils.checkpoint import checkpoint
@@ -169,3 +172,29 @@ def test_what_is_refused_in_training_and_in_evaluation(training):
         assert drop(t, residual=t).dtype == t.dtype and drop(t).dtype == t.dtype
     if not training:
         assert drop(x) is x and torch.equal(drop(x, residual=x), x + x) and drop.step == 1
+
+
+def test_modules_pickled_before_they_had_these_attributes():
+    """A whole module that was pickled by an older version lacks what has been added since."""
+    drop, head = ForgeDropout(0.5), blocks.ForgeHeadLoss(64, 64, device="cpu")
+    for module, name in ((drop, "_masks"), (head, "reduction")):
+        state = {k: v for k, v in module.__dict__.items() if k != name}
+        old = type(module).__new__(type(module))
+        old.__setstate__(state)
+        assert getattr(old, name) == getattr(module, name)
+    x = _x()
+    old = ForgeDropout.__new__(ForgeDropout)
+    old.__setstate__({k: v for k, v in drop.__dict__.items() if k != "_masks"})
+    y = checkpoint(lambda t: old(t).square(), x, use_reentrant=False)
+    y.sum().backward()
+    assert torch.equal(x.grad != 0, _mask_of(y)) and not drop._masks
+
+
+def test_copies_know_their_own_forwards():
+    drop, x = ForgeDropout(0.5), _x()
+    y = checkpoint(lambda t: drop(t).square(), x, use_reentrant=False)
+    twin = pickle.loads(pickle.dumps(copy.deepcopy(drop)))
+    for _ in range(2000):
+        twin(x.detach())
+    y.sum().backward()
+    assert torch.equal(x.grad != 0, _mask_of(y)) and (drop.step, twin.step) == (2, 2002)
