@@ -10,11 +10,11 @@
 // The pipeline, tiles, roles, bounded waits and drains are those of forge_block_kernel.
 //
 // Ragged runs.  A launch in front (expert_plan_kernel) turns the offsets into a list of row tiles and, for the
-// weights' gradients, into two tensor maps per expert whose token dimension ends with the run: the copy itself
-// fills what a slice reaches past the run with zeros, for both operands, so neither values of the next expert
-// nor its infinities or NaN enter a sum.  An expert without rows takes one slice of zero fill and stores a zero gradient.
-// Row products need no such maps: a row of the result depends on its own row of X alone, and rows past the run are not
-// stored.
+// weights' gradients, into a tensor map per expert and operand (a linear layer's two, a gated block's five) whose token
+// dimension ends with the run: the copy itself fills what a slice reaches past the run with zeros, for both operands, so
+// neither values of the next expert nor its infinities or NaN enter a sum.  An expert without rows takes one slice of zero
+// fill and stores a zero gradient.  Row products need no such maps: a row of the result depends on its own row of X alone,
+// and rows past the run are not stored.
 //
 // Few tiles.  The plan knows how many row tiles there are; where the last wave of tiles leaves SMs idle it cuts them
 // along the reduction (expert_parts), and the parts are joined as in forge_block_kernel: no CTA waits for another, the
@@ -197,12 +197,12 @@ __device__ __forceinline__ ExpertUnit expert_unit(const ExpertGroup<EPI>& g, int
 // The weights are the MMA's A (256 columns of the result, 128 a CTA) and the rows its B, whose width is any multiple
 // of 32: the last tile of a run is as wide as the run's rest, not as a whole tile.  Against rows as A in tiles of 256, with
 // maps of the runs (us): gated forward 2048 rows of 8 experts, 4096/14336, 769 to 693; 8192 of 64, 2048/1408, 236 to 220;
-// linear forward 4637 of 6, 80 x 7224, 42.6 to 27.4; 32768 of 64, at the power limit, 480 to 467.  What is left is a quarter
-// of the pipe's time (4096 rows of 8, 4096 x 4096: tensor pipe 71 % active, DRAM 58 %, nothing saturated): 19 row tiles on
-// 16 columns make 4 rounds of 76 pairs and a rest, and evening the rounds out (tiles of a run equally high, experts by
-// that height) left every size where it was.  So a warp's lanes are columns of the
-// result and the accumulator's columns its rows, 32 at a time; results (and G and U on their way in) change sides in
-// the warp's 4 KiB of shared memory, 32 rows of 64 bytes at a time, where both sides' accesses are free of conflicts.
+// linear forward 4637 of 6, 80 x 7224, 42.6 to 27.4.  With long runs the tensor pipe is 65-71 % active (4096 rows of 8,
+// 4096 x 4096; 32768 of 64, 2048/1408).
+//
+// A warp's lanes are columns of the result and the accumulator's columns its rows, 32 at a time; results (and G and U on
+// their way in) change sides in the warp's 4 KiB of shared memory, 32 rows of 64 bytes at a time, where both sides' accesses
+// are free of conflicts.
 
 __device__ __forceinline__ void st_shared_b16(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(v)) : "memory");

@@ -144,9 +144,9 @@ struct TileGroup {
 // with the run: its tensor maps do (one pair an expert, made on the device), so what a slice holds past it is zero.
 struct RaggedGroup : TileGroup<1> {
     int experts;
-    const int* offsets;        // [experts + 1], in order and within the rows
-    const CUtensorMap* runs;   // [experts] of dY, then [experts] of X
-    const CUtensorMap* runs_x;
+    const int* offsets;         // [experts + 1], in order and within the rows
+    const CUtensorMap* runs;    // [experts], of dY
+    const CUtensorMap* runs_x;  // [experts], of X
 };
 template <int G, int OPS>
 using TileGroupOf = std::conditional_t<OPS == kOpsBF16Ragged, RaggedGroup, TileGroup<G>>;
