@@ -276,9 +276,9 @@ class ForgeDropout(Stepped):
     mask, or with the one that such a tensor says at the replay.
 
     A forward that a backward pass computes again (torch.utils.checkpoint) takes its mask again.  It is known by a
-    number that each forward in training mode draws from PyTorch's CPU generator, which checkpoint sets back; an error is
-    raised where it does not (preserve_rng_state=False), where over 1024 forwards lie between, and where forwards that are
-    still to be computed again began from the same state of that generator."""
+    number that both draw from PyTorch's CPU generator, which checkpoint sets back; an error is raised where it does not
+    (preserve_rng_state=False), where over 1024 forwards lie between, and where forwards that are still to be computed again
+    began from the same state of that generator.  Other forwards draw none."""
 
     _MOST = 1024  # forwards that are known
 
@@ -296,8 +296,14 @@ class ForgeDropout(Stepped):
 
     def _take_step(self) -> int:
         """The step of a forward that begins here."""
+        again = torch._C._current_graph_task_id() >= 0  # a backward pass is running on this thread
+        # a forward that is to be computed again runs without gradients, or with hooks on the tensors that it saves (drawing
+        # for every one would cost 14 us of the host's time)
+        if not again and torch.is_grad_enabled() and torch._C._autograd._top_saved_tensors_default_hooks(True) is None:
+            self.step += 1
+            return self.step - 1
         drawn = int(torch.empty((), dtype=torch.int64, device="cpu").random_())
-        if torch._C._current_graph_task_id() >= 0:  # a backward pass is running on this thread
+        if again:
             step, _ = self._masks.get(drawn, (None, False))
             if step is None:
                 raise RuntimeError("ForgeDropout: a backward pass computes a forward again and its mask is not known, since "

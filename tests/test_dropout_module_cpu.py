@@ -198,3 +198,37 @@ def test_copies_know_their_own_forwards():
         twin(x.detach())
     y.sum().backward()
     assert torch.equal(x.grad != 0, _mask_of(y)) and (drop.step, twin.step) == (2, 2002)
+
+
+def test_what_draws_from_the_generator():
+    drop, x = ForgeDropout(0.5), _x()
+    state = torch.get_rng_state()
+    drop(x).square().sum().backward()
+    assert torch.equal(torch.get_rng_state(), state) and not drop._masks and drop.step == 2
+    drop.eval()
+    with torch.no_grad():
+        drop(x)
+    assert torch.equal(torch.get_rng_state(), state) and drop.step == 2
+    drop.train()
+    for reentrant in (True, False):
+        with torch.random.fork_rng(devices=[]):
+            checkpoint(drop, x, use_reentrant=reentrant)
+            assert not torch.equal(torch.get_rng_state(), state)
+    assert drop.step == 4 and len(drop._masks) == 1  # drawn from one state: which of the two it is cannot be told
+    with pytest.raises(RuntimeError, match="mask is not known"):
+        checkpoint(lambda t: drop(t).square(), x, use_reentrant=False, preserve_rng_state=False).sum().backward()
+
+
+def test_plain_forwards_between_recomputed_ones():
+    drop, xs = ForgeDropout(0.5), [_x(i) for i in range(3)]
+    ys = []
+    for x in xs:
+        drop(x)
+        ys.append(checkpoint(lambda t: drop(drop(t)).square(), x, use_reentrant=True))
+        drop(x)
+    for x, y in zip(xs, ys):
+        kept = _mask_of(y)
+        drop(x)
+        y.sum().backward()
+        assert torch.equal(x.grad != 0, kept)
+    assert drop.step == 16
